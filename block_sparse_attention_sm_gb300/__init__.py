@@ -320,3 +320,18 @@ def lambda_of(A, B, s, L) -> float:
 def stream_status(stream=None) -> None:
     st = capi.ss_stream_status(stream)
     _check(st, "device status")
+
+
+_CACHE = ("rope_frequencies", "rope", "rope_append_paged", "chunk_paged", "chunk_paged_workspace",
+          "pages_reserve", "pages_free", "pages_fork", "pages_copy", "pages_compact")
+
+
+def __getattr__(name):
+    """The helpers around the paged cache (:mod:`.cache`), imported on first use
+    (they need torch when imported, this module only when called)."""
+    if name in _CACHE:
+        from . import cache
+
+        globals().update({n: getattr(cache, n) for n in _CACHE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

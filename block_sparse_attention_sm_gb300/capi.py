@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libssattn.so")
 
 SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_CUDA, SS_ERR_TIMEOUT, SS_ERR_WORKSPACE = range(6)
 SS_PREFILL, SS_DECODE, SS_MLA_DECODE, SS_MLA_PREFILL = 0, 1, 2, 3
+SS_ROPE_PLAIN, SS_ROPE_LINEAR, SS_ROPE_BASE, SS_ROPE_YARN, SS_ROPE_WAVELENGTH = range(5)
 
 EXPORTS = (
     "ss_attn_prefill", "ss_attn_prefill_ex", "ss_attn_mla_prefill", "ss_attn_mla_prefill_ex",
@@ -25,6 +26,10 @@ EXPORTS = (
     "ss_attn_mla_decode_workspace_size", "ss_attn_mla_decode", "ss_attn_mla_decode_ex",
     "ss_attn_mla_decode_paged",
     "ss_calibrate", "ss_fit_factor", "ss_lambda", "ss_status_string", "ss_stream_status",
+    "ss_rope", "ss_rope_append_paged", "ss_rope_frequencies",
+    "ss_attn_chunk_paged", "ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
+    "ss_pages_workspace_size", "ss_pages_reserve", "ss_pages_free", "ss_pages_fork",
+    "ss_pages_copy", "ss_pages_compact",
 )
 
 
@@ -93,11 +98,32 @@ def load() -> ctypes.CDLL:
     lib.ss_status_string.argtypes = [I]
     lib.ss_status_string.restype = ctypes.c_char_p
     lib.ss_stream_status.argtypes = [P]
+    I64, D = ctypes.c_int64, ctypes.c_double
+    lib.ss_rope.argtypes = [P, P, I, I, I, I, P, P, P, I64, P, I, I, I, I, F, P]
+    lib.ss_rope_append_paged.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, I, I, I, F,
+                                         P, P, P, I, I, P]
+    lib.ss_rope_frequencies.argtypes = [P, I, D, I, D, I, D, D, ctypes.POINTER(F)]
+    lib.ss_attn_chunk_paged.argtypes = [P, I64, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, F, I, P, P,
+                                        U, ctypes.POINTER(ss_debug_opts), P]
+    lib.ss_attn_chunk_paged_units.argtypes = [I, I, I, I, I]
+    lib.ss_attn_chunk_paged_workspace_size.argtypes = [I, I, I, I]
+    lib.ss_pages_workspace_size.argtypes = [I, I, I]
+    for name in ("ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
+                 "ss_pages_workspace_size"):
+        getattr(lib, name).restype = U
+    state = [P, I, P, I, I, P]
+    lib.ss_pages_reserve.argtypes = state + [P, P, I, P, P, U, P]
+    lib.ss_pages_free.argtypes = state + [P, I, P]
+    lib.ss_pages_fork.argtypes = [P, I, U] + state + [P, P, I, P, P, U, P]
+    lib.ss_pages_copy.argtypes = [P, I, U, I, P, P, I, P, P, U, P]
+    lib.ss_pages_compact.argtypes = [P, I, U] + state + [P, P, P, P, U, P]
     for name in ("ss_attn_prefill", "ss_attn_prefill_ex", "ss_attn_mla_prefill",
                  "ss_attn_mla_prefill_ex", "ss_attn_decode", "ss_attn_decode_ex",
                  "ss_attn_decode_noalloc", "ss_attn_decode_paged", "ss_attn_mla_decode",
                  "ss_attn_mla_decode_ex", "ss_attn_mla_decode_paged", "ss_calibrate",
-                 "ss_fit_factor", "ss_stream_status"):
+                 "ss_fit_factor", "ss_stream_status", "ss_rope", "ss_rope_append_paged",
+                 "ss_rope_frequencies", "ss_attn_chunk_paged", "ss_pages_reserve", "ss_pages_free",
+                 "ss_pages_fork", "ss_pages_copy", "ss_pages_compact"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -279,3 +305,110 @@ def ss_attn_mla_decode_paged(q, kv_pages, page_table, seq_lens, o, B, Hq, num_pa
                                            int(num_kv_splits), _ptr(skip_counts), _ptr(workspace),
                                            int(workspace_bytes), ctypes.byref(dbg),
                                            _stream(stream))
+
+
+def _strides(s):
+    """Host int64 array of strides in elements (None: contiguous)."""
+    return None if s is None else (ctypes.c_int64 * len(s))(*[int(x) for x in s])
+
+
+def _addresses(pools):
+    """Host array of the pools' device addresses."""
+    return (ctypes.c_void_p * max(1, len(pools)))(*[_ptr(p) for p in pools])
+
+
+def ss_rope(x, out, B, H, L, d, positions, inv_freq, rot_dim, x_strides=None, out_strides=None,
+            position_stride=0, rot_offset=0, interleaved=False, inverse=False, attn_factor=1.0,
+            stream=None) -> int:
+    """Rotary positions of x [B,H,L,d] (strided rows) into out."""
+    return load().ss_rope(_ptr(x), _ptr(out), B, H, L, d, _strides(x_strides), _strides(out_strides),
+                          _ptr(positions), int(position_stride), _ptr(inv_freq), int(rot_dim),
+                          int(rot_offset), int(bool(interleaved)), int(bool(inverse)),
+                          float(attn_factor), _stream(stream))
+
+
+def ss_rope_append_paged(q, q_out, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot_dim,
+                         k_pages, v_pages, page_table, num_pages, max_pages, positions=None,
+                         q_strides=None, q_out_strides=None, k_strides=None, v_strides=None,
+                         rot_offset=0, interleaved=False, attn_factor=1.0, stream=None) -> int:
+    """Rotary positions of a step's new tokens and the write of their keys and values into pages."""
+    return load().ss_rope_append_paged(
+        _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _strides(q_strides), _strides(q_out_strides),
+        _strides(k_strides), _strides(v_strides), T, B, Hq, Hkv, d, _ptr(cu_seqlens), _ptr(seq_lens),
+        _ptr(positions), _ptr(inv_freq), int(rot_dim), int(rot_offset), int(bool(interleaved)),
+        float(attn_factor), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), num_pages, max_pages,
+        _stream(stream))
+
+
+def ss_rope_frequencies(rot_dim, base=10000.0, scaling=SS_ROPE_PLAIN, factor=1.0, original_length=0,
+                        lo=0.0, hi=0.0):
+    """Returns (status, list of rot_dim / 2 frequencies, attn_factor)."""
+    n = max(1, int(rot_dim) // 2)
+    out = (ctypes.c_double * n)()
+    f = ctypes.c_float()
+    st = load().ss_rope_frequencies(out, int(rot_dim), float(base), int(scaling), float(factor),
+                                    int(original_length), float(lo), float(hi), ctypes.byref(f))
+    return st, list(out), f.value
+
+
+def ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits) -> int:
+    return int(load().ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits))
+
+
+def ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits) -> int:
+    return int(load().ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits))
+
+
+def ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,
+                        num_pages, max_pages, d, scale, causal, lambda_a, num_kv_splits,
+                        skip_counts=None, workspace=None, workspace_bytes=0, q_token_stride=0,
+                        skip_mask=None, vote_margin=None, stream=None) -> int:
+    """Attention of a step's packed new tokens over the paged cache."""
+    dbg = _dbg(skip_mask, vote_margin)
+    return load().ss_attn_chunk_paged(
+        _ptr(q), int(q_token_stride), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cu_seqlens),
+        _ptr(seq_lens), _ptr(o), T, B, Hq, Hkv, num_pages, max_pages, d, float(scale),
+        int(bool(causal)), float(lambda_a), int(num_kv_splits), _ptr(skip_counts), _ptr(workspace),
+        int(workspace_bytes), ctypes.byref(dbg), _stream(stream))
+
+
+def ss_pages_workspace_size(num_pages, num_rows, n) -> int:
+    return int(load().ss_pages_workspace_size(num_pages, num_rows, n))
+
+
+def ss_pages_reserve(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, add, n,
+                     result=None, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().ss_pages_reserve(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
+                                   _ptr(seq_lens), _ptr(rows), _ptr(add), n, _ptr(result),
+                                   _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def ss_pages_free(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, n,
+                  stream=None) -> int:
+    return load().ss_pages_free(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
+                                _ptr(seq_lens), _ptr(rows), n, _stream(stream))
+
+
+def ss_pages_fork(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
+                  src_rows, dst_rows, n, result=None, workspace=None, workspace_bytes=0,
+                  stream=None) -> int:
+    return load().ss_pages_fork(_addresses(pools), len(pools), int(page_bytes), _ptr(page_refs),
+                                num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
+                                _ptr(src_rows), _ptr(dst_rows), n, _ptr(result), _ptr(workspace),
+                                int(workspace_bytes), _stream(stream))
+
+
+def ss_pages_copy(pools, page_bytes, num_pages, src, dst, n, result=None, workspace=None,
+                  workspace_bytes=0, stream=None) -> int:
+    return load().ss_pages_copy(_addresses(pools), len(pools), int(page_bytes), num_pages, _ptr(src),
+                                _ptr(dst), n, _ptr(result), _ptr(workspace), int(workspace_bytes),
+                                _stream(stream))
+
+
+def ss_pages_compact(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
+                     out_refs=None, out_table=None, live=None, workspace=None, workspace_bytes=0,
+                     stream=None) -> int:
+    return load().ss_pages_compact(_addresses(pools), len(pools), int(page_bytes), _ptr(page_refs),
+                                   num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
+                                   _ptr(out_refs), _ptr(out_table), _ptr(live), _ptr(workspace),
+                                   int(workspace_bytes), _stream(stream))

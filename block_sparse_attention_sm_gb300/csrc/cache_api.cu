@@ -1,0 +1,386 @@
+// C-ABI entry points around the paged cache: rotary positions, the write of
+// new tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
+// Argument validation and launches; include/ssattn.h has each call's contract.
+#include <cmath>
+#include <cstring>
+
+#include "api.cuh"
+#include "chunk_paged.cuh"
+#include "pages.cuh"
+#include "rope.cuh"
+
+namespace ssattn {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool all8(const long* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] % 8 != 0) return false;
+  return true;
+}
+
+ss_status of(cudaError_t e) { return e == cudaSuccess ? SS_OK : SS_ERR_CUDA; }
+
+// The rotation's own arguments; `vec`: its entries lie in whole 16-byte words.
+ss_status turn_of(RopeTurn* t, const double* inv_freq, int rot, int off, int interleaved, float factor,
+                  int inverse, int d, bool* vec) {
+  if (rot < 0 || rot % 2 != 0 || off < 0 || rot > d || off > d - rot || !std::isfinite(factor))
+    return SS_ERR_INVALID_ARG;
+  if (rot > 0 && (inv_freq == nullptr || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0))
+    return SS_ERR_INVALID_ARG;
+  *t = RopeTurn{inv_freq, rot, off, interleaved ? 1 : 0, factor, inverse ? -1.f : 1.f};
+  *vec = d % 8 == 0 && off % 8 == 0 && rot % (interleaved ? 8 : 16) == 0;
+  return SS_OK;
+}
+
+constexpr int kMaxRopeWidth = 1 << 16;
+
+}  // namespace
+}  // namespace ssattn
+
+using namespace ssattn;
+
+extern "C" {
+
+ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const int64_t* x_strides,
+                  const int64_t* out_strides, const int32_t* positions, int64_t position_stride,
+                  const double* inv_freq, int rot_dim, int rot_offset, int interleaved, int inverse,
+                  float attn_factor, void* stream) {
+  if (B < 0 || H < 0 || L < 0 || d < 1 || rot_dim < 2 || position_stride < 0) return SS_ERR_INVALID_ARG;
+  if (d > kMaxRopeWidth) return SS_ERR_UNSUPPORTED;
+  RopeParams p{};
+  bool vec = false;
+  ss_status st = turn_of(&p.turn, inv_freq, rot_dim, rot_offset, interleaved, attn_factor, inverse, d, &vec);
+  if (st != SS_OK) return st;
+  if (B == 0 || H == 0 || L == 0) return SS_OK;
+  const int64_t dense[3] = {static_cast<int64_t>(H) * L * d, static_cast<int64_t>(L) * d, d};
+  const int64_t *xs = x_strides != nullptr ? x_strides : dense,
+                *os = out_strides != nullptr ? out_strides : dense;
+  const int size[3] = {B, H, L};
+  for (int i = 0; i < 3; ++i) {
+    p.xs[i] = xs[i];
+    p.os[i] = os[i];
+    // Rows of the output must not overlap; the input's may (a broadcast axis).
+    if (xs[i] < 0 || os[i] < 0 || (size[i] > 1 && os[i] < d)) return SS_ERR_INVALID_ARG;
+    if (x == out && size[i] > 1 && xs[i] != os[i]) return SS_ERR_INVALID_ARG;
+  }
+  if (x == nullptr || out == nullptr || positions == nullptr || !aligned2(x) || !aligned2(out) ||
+      !aligned4(positions))
+    return SS_ERR_INVALID_ARG;
+  if ((st = check_device()) != SS_OK) return st;
+  vec = vec && aligned16(x) && aligned16(out) && all8(p.xs, 3) && all8(p.os, 3);
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.pos = positions;
+  p.pos_stride = position_stride;
+  p.B = B;
+  p.H = H;
+  p.L = L;
+  p.d = d;
+  return of(launch_rope(p, vec, static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
+                               const int64_t* q_strides, const int64_t* q_out_strides,
+                               const int64_t* k_strides, const int64_t* v_strides, int T, int B, int Hq,
+                               int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* positions, const double* inv_freq, int rot_dim,
+                               int rot_offset, int interleaved, float attn_factor, void* k_pages,
+                               void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
+                               void* stream) {
+  if (T < 0 || B < 1 || Hkv < 1 || d < 1 || (q != nullptr && Hq < 1) || num_pages < 1 || max_pages < 1)
+    return SS_ERR_INVALID_ARG;
+  if (d > kMaxRopeWidth) return SS_ERR_UNSUPPORTED;
+  AppendParams p{};
+  bool vec = false;
+  ss_status st = turn_of(&p.turn, inv_freq, rot_dim, rot_offset, interleaved, attn_factor, 0, d, &vec);
+  if (st != SS_OK) return st;
+  if (k == nullptr || k_pages == nullptr || cu_seqlens == nullptr || seq_lens == nullptr ||
+      page_table == nullptr || (q != nullptr && q_out == nullptr) || (v != nullptr && v_pages == nullptr))
+    return SS_ERR_INVALID_ARG;
+  if (!aligned2(q) || !aligned2(q_out) || !aligned2(k) || !aligned2(v) || !aligned16(k_pages) ||
+      !aligned16(v_pages) || !aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(positions) ||
+      !aligned4(page_table))
+    return SS_ERR_INVALID_ARG;
+  if (static_cast<long>(max_pages) * kTile > 0x7fffffffL) return SS_ERR_INVALID_ARG;
+  const int64_t dq[2] = {static_cast<int64_t>(Hq) * d, d}, dk[2] = {static_cast<int64_t>(Hkv) * d, d};
+  for (int i = 0; i < 2; ++i) {
+    p.qs[i] = q_strides != nullptr ? q_strides[i] : dq[i];
+    p.qos[i] = q_out_strides != nullptr ? q_out_strides[i] : dq[i];
+    p.ks[i] = k_strides != nullptr ? k_strides[i] : dk[i];
+    p.vs[i] = v_strides != nullptr ? v_strides[i] : dk[i];
+    if (p.qs[i] < 0 || p.ks[i] < 0 || p.vs[i] < 0) return SS_ERR_INVALID_ARG;
+    if (q != nullptr && ((i == 0 ? T : Hq) > 1)) {
+      if (p.qos[i] < d || (q == q_out && p.qs[i] != p.qos[i])) return SS_ERR_INVALID_ARG;
+    }
+  }
+  if (T == 0) return SS_OK;
+  if ((st = check_device()) != SS_OK) return st;
+  vec = vec && aligned16(q) && aligned16(q_out) && aligned16(k) && aligned16(v) && all8(p.ks, 2) &&
+        (q == nullptr || (all8(p.qs, 2) && all8(p.qos, 2))) && (v == nullptr || all8(p.vs, 2));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.cu_seqlens = cu_seqlens;
+  p.seq_lens = seq_lens;
+  p.pos = positions;
+  p.page_table = page_table;
+  p.T = T;
+  p.B = B;
+  p.Hq = q != nullptr ? Hq : 0;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  return of(launch_rope_append(p, vec, static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_scaling scaling,
+                              double factor, int original_length, double lo, double hi,
+                              float* attn_factor_out) {
+  if (out == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+    return SS_ERR_INVALID_ARG;
+  if (scaling != SS_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return SS_ERR_INVALID_ARG;
+  const bool ramped = scaling == SS_ROPE_YARN || scaling == SS_ROPE_WAVELENGTH;
+  if (ramped && (original_length < 1 || !(lo > 0.0) || !(hi > lo) || !std::isfinite(hi)))
+    return SS_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  double b = base;
+  if (scaling == SS_ROPE_BASE) {
+    if (rot_dim < 4) return SS_ERR_INVALID_ARG;
+    b = base * std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+  }
+  double first = 0.0, last = 0.0;  // SS_ROPE_YARN: the ramp's ends, in pairs
+  if (scaling == SS_ROPE_YARN) {
+    auto pair_of = [&](double turns) {
+      return rot_dim * std::log(original_length / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    first = std::fmax(0.0, std::floor(pair_of(hi)));
+    last = std::fmin(rot_dim - 1.0, std::ceil(pair_of(lo)));
+    if (last - first < 1e-3) last = first + 1e-3;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double w = std::pow(b, -2.0 * i / rot_dim);
+    double keep = 1.0;  // share of the unscaled frequency
+    switch (scaling) {
+      case SS_ROPE_PLAIN:
+      case SS_ROPE_BASE: break;
+      case SS_ROPE_LINEAR: keep = 0.0; break;
+      case SS_ROPE_YARN: keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - first) / (last - first))); break;
+      case SS_ROPE_WAVELENGTH:
+        keep = std::fmin(1.0, std::fmax(0.0, (original_length * w / two_pi - lo) / (hi - lo)));
+        break;
+      default: return SS_ERR_INVALID_ARG;
+    }
+    out[i] = scaling == SS_ROPE_PLAIN ? w : w * keep + w / factor * (1.0 - keep);
+  }
+  if (attn_factor_out != nullptr)
+    *attn_factor_out = scaling == SS_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return SS_OK;
+}
+
+size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv, int num_kv_splits) {
+  if (T < 0 || B < 1 || Hkv < 1 || Hq < Hkv || num_kv_splits < 1) return 0;
+  const int G = Hq / Hkv;
+  if (G > kTile) return 0;
+  return 2 * static_cast<size_t>(chunk_slots(T, B, kTile / G)) * Hkv * num_kv_splits;
+}
+
+size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits) {
+  if (num_kv_splits <= 1 || T < 1 || Hq < 1 || d < 1) return 0;
+  return static_cast<size_t>(num_kv_splits) * T * Hq * (d + 2) * sizeof(float);
+}
+
+ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
+                              const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
+                              const int32_t* seq_lens, void* o, int T, int B, int Hq, int Hkv,
+                              int num_pages, int max_pages, int d, float scale, int causal,
+                              float lambda_a, int num_kv_splits, uint32_t* skip_counts, void* workspace,
+                              size_t workspace_bytes, const ss_debug_opts* dbg, void* stream) {
+  if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1 ||
+      num_kv_splits < 1 || !(scale > 0.f) || !std::isfinite(scale) || !(lambda_a >= 0.f) ||
+      !std::isfinite(lambda_a))
+    return SS_ERR_INVALID_ARG;
+  if (dbg != nullptr && (dbg->count_only || dbg->fault_inject || dbg->vote_chunk_tiles || dbg->prefill_kernel))
+    return SS_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return SS_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  if (G > kTile) return SS_ERR_UNSUPPORTED;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || page_table == nullptr ||
+      cu_seqlens == nullptr || seq_lens == nullptr || o == nullptr)
+    return SS_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * d, stride = q_token_stride != 0 ? q_token_stride : row;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+      !aligned4(page_table) || !aligned4(cu_seqlens) || !aligned4(seq_lens) || stride < row || stride % 8 != 0)
+    return SS_ERR_INVALID_ARG;
+  const long tpb = kTile / G, slots = chunk_slots(T, B, tpb);
+  if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || T > 0x7fffffff - 2 * kTile ||
+      static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL ||
+      static_cast<double>(slots) * Hkv * num_kv_splits * 2 > 0x7fffffff ||
+      static_cast<long>(T) * Hq > 8 * 0x7fffffffL || stride >= (1LL << 38))
+    return SS_ERR_INVALID_ARG;
+  const size_t need = ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits);
+  if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
+    return SS_ERR_WORKSPACE;
+  if (T == 0) return SS_OK;
+  ss_status st = check_device();
+  if (st != SS_OK) return st;
+
+  CUtensorMap tq, tk, tv;
+  const long blocks = static_cast<long>(num_pages) * Hkv;
+  if (!make_map(&tk, k_pages, d, kTile, blocks, kTile / 2) || !make_map(&tv, v_pages, d, kTile, blocks))
+    return SS_ERR_CUDA;
+  {  // q as [T][Hkv][G][d]; a box is 64 entries of a row block
+    auto fn = encode_fn();
+    if (fn == nullptr) return SS_ERR_CUDA;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G),
+                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(G) * d * 2,
+                                   static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tpb)};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return SS_ERR_CUDA;
+  }
+  ChunkParams p{};
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.tpb = static_cast<int>(tpb);
+  p.slots = static_cast<int>(slots);
+  p.S = num_kv_splits;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.causal = causal ? 1 : 0;
+  p.scale = scale;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.lambda_a = lambda_a;
+  p.cu_seqlens = cu_seqlens;
+  p.seq_lens = seq_lens;
+  p.page_table = page_table;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  if (num_kv_splits > 1) {
+    const size_t rows = static_cast<size_t>(num_kv_splits) * T * Hq;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * d);
+  }
+  p.counts = skip_counts;
+  p.mask = dbg != nullptr ? dbg->skip_mask : nullptr;
+  p.margin = dbg != nullptr ? dbg->vote_margin : nullptr;
+  p.status = status_ptr();
+  const bool vote = lambda_a > 0.f || p.mask != nullptr || p.margin != nullptr;
+  return of(launch_chunk_paged(d, vote, tq, tk, tv, p, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- pages
+
+size_t ss_pages_workspace_size(int num_pages, int num_rows, int n) {
+  if (num_pages < 0 || num_rows < 0 || n < 0) return 0;
+  return pages_workspace(num_pages, num_rows, n);
+}
+
+static ss_status check_state(const int32_t* refs, int num_pages, const int32_t* table, int num_rows,
+                             int max_pages, const int32_t* lens) {
+  if (refs == nullptr || table == nullptr || lens == nullptr || num_pages < 1 || num_rows < 1 ||
+      max_pages < 1 || static_cast<long>(max_pages) * kTile > 0x7fffffffL || !aligned16(refs) ||
+      !aligned4(table) || !aligned4(lens))
+    return SS_ERR_INVALID_ARG;
+  return SS_OK;
+}
+
+static ss_status check_pools(void* const* pools, int num_pools, size_t page_bytes) {
+  if (num_pools < 0 || (num_pools > 0 && pools == nullptr) || page_bytes == 0 || page_bytes % 16 != 0 ||
+      page_bytes > (static_cast<size_t>(1) << 40))
+    return SS_ERR_INVALID_ARG;
+  for (int i = 0; i < num_pools; ++i)
+    if (pools[i] == nullptr || !aligned16(pools[i])) return SS_ERR_INVALID_ARG;
+  return SS_OK;
+}
+
+static ss_status check_workspace(const void* ws, size_t bytes, int num_pages, int num_rows, int n) {
+  return ws == nullptr || !aligned16(ws) || bytes < pages_workspace(num_pages, num_rows, n)
+             ? SS_ERR_WORKSPACE
+             : SS_OK;
+}
+
+ss_status ss_pages_reserve(int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows,
+                           int max_pages, int32_t* seq_lens, const int32_t* rows, const int32_t* add,
+                           int n, int32_t* result, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens);
+  if (st != SS_OK) return st;
+  if (n < 0 || (n > 0 && add == nullptr) || !aligned4(rows) || !aligned4(add) || !aligned4(result) ||
+      (rows == nullptr && n > num_rows))
+    return SS_ERR_INVALID_ARG;
+  if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, n)) != SS_OK) return st;
+  if ((st = check_device()) != SS_OK) return st;
+  const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
+  return of(launch_pages_reserve(s, rows, add, n, result, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_pages_free(int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows,
+                        int max_pages, int32_t* seq_lens, const int32_t* rows, int n, void* stream) {
+  ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens);
+  if (st != SS_OK) return st;
+  if (n < 0 || (n > 0 && rows == nullptr) || !aligned4(rows)) return SS_ERR_INVALID_ARG;
+  if ((st = check_device()) != SS_OK) return st;
+  const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
+  return of(launch_pages_free(s, rows, n, static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_pages_fork(void* const* pools, int num_pools, size_t page_bytes, int32_t* page_refs,
+                        int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                        int32_t* seq_lens, const int32_t* src_rows, const int32_t* dst_rows, int n,
+                        int32_t* result, void* workspace, size_t workspace_bytes, void* stream) {
+  ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens);
+  if (st != SS_OK || (st = check_pools(pools, num_pools, page_bytes)) != SS_OK) return st;
+  if (n < 0 || (n > 0 && (src_rows == nullptr || dst_rows == nullptr)) || !aligned4(src_rows) ||
+      !aligned4(dst_rows) || !aligned4(result))
+    return SS_ERR_INVALID_ARG;
+  if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, n)) != SS_OK) return st;
+  if ((st = check_device()) != SS_OK) return st;
+  const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
+  return of(launch_pages_fork(pools, num_pools, page_bytes, s, src_rows, dst_rows, n, result, workspace,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_pages_copy(void* const* pools, int num_pools, size_t page_bytes, int num_pages,
+                        const int32_t* src, const int32_t* dst, int n, int32_t* result, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  ss_status st = check_pools(pools, num_pools, page_bytes);
+  if (st != SS_OK) return st;
+  if (num_pools < 1 || num_pages < 1 || n < 0 || (n > 0 && (src == nullptr || dst == nullptr)) ||
+      !aligned4(src) || !aligned4(dst) || !aligned4(result))
+    return SS_ERR_INVALID_ARG;
+  if ((st = check_workspace(workspace, workspace_bytes, num_pages, 0, n)) != SS_OK) return st;
+  if ((st = check_device()) != SS_OK) return st;
+  return of(launch_pages_copy(pools, num_pools, page_bytes, num_pages, src, dst, n, result, workspace,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes, int32_t* page_refs,
+                           int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                           const int32_t* seq_lens, int32_t* out_refs, int32_t* out_table, int32_t* live,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  int32_t* lens = const_cast<int32_t*>(seq_lens);
+  ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, lens);
+  if (st != SS_OK || (st = check_pools(pools, num_pools, page_bytes)) != SS_OK) return st;
+  if (out_refs == nullptr) out_refs = page_refs;
+  if (out_table == nullptr) out_table = page_table;
+  if (!aligned4(out_refs) || !aligned4(out_table) || !aligned4(live)) return SS_ERR_INVALID_ARG;
+  if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, 0)) != SS_OK) return st;
+  if ((st = check_device()) != SS_OK) return st;
+  const PageState s{page_refs, page_table, lens, num_pages, num_rows, max_pages};
+  return of(launch_pages_compact(pools, num_pools, page_bytes, s, out_refs, out_table, live, workspace,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

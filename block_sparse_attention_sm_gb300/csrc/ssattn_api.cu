@@ -8,6 +8,7 @@
 #include <mutex>
 #include <vector>
 
+#include "api.cuh"
 #include "common.cuh"
 #include "decode_rows.cuh"
 #include "mla.cuh"
@@ -23,6 +24,8 @@ cudaError_t launch_prefill_pair(int dqk, Mode mode, const CUtensorMap& tq, const
 namespace {
 
 __device__ uint32_t g_device_status = 0;
+
+}  // namespace
 
 // Device address of the status word for the current device (cached).
 uint32_t* status_ptr() {
@@ -75,7 +78,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 3-D view [BH][L][d] of a bf16 tensor, 64 x box_rows boxes, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, int d, int L, long BH, int box_rows = kTile) {
+bool make_map(CUtensorMap* m, const void* base, int d, int L, long BH, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(L),
@@ -87,6 +90,8 @@ bool make_map(CUtensorMap* m, const void* base, int d, int L, long BH, int box_r
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 

@@ -337,6 +337,221 @@ ss_status ss_attn_mla_decode_paged(const void* q, const void* kv_pages, const in
                                    void* workspace, size_t workspace_bytes,
                                    const ss_debug_opts* dbg, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Around the paged cache.  What a serving loop needs next to the attention
+ * calls above: rotary positions, the write of a step's new keys and values
+ * into pages, attention of more than one new token a sequence over pages, and
+ * the pages' bookkeeping.  The cited pages have no counterpart for these
+ * (they name serving engines); they exist for users of this library.
+ *
+ * A step's new tokens are packed: T rows, those of sequence b being
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [B + 1], non-decreasing
+ * from 0; a sequence may have none).  Rows from cu_seqlens[B] on belong to no
+ * sequence (padding): they are not computed and their outputs are left as
+ * they were.  seq_lens[b] is the sequence's number of cached keys INCLUDING
+ * its new ones, so that new token i of its n_b is key L_b - n_b + i.
+ */
+
+/*
+ * Rotary positions.  Entries [rot_offset, rot_offset + rot_dim) of a row are
+ * rot_dim / 2 pairs (a, b) -- (i, i + rot_dim / 2), or with `interleaved` the
+ * adjacent ones (2i, 2i + 1) -- and pair i of a row at position p becomes
+ *   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t),  t = p * inv_freq[i]
+ * with f = attn_factor; the row's other entries are copied.  `inverse` turns
+ * by -t (same f): the gradient with respect to x is this call on the gradient
+ * with respect to out.  Angles are exact for any int32 position (no loss at
+ * far positions); products are fp32, rounded once to bf16.
+ *   x, out: bf16 [B][H][L][d], 2-byte aligned; x_strides, out_strides: host
+ *     arrays of 3 strides in elements (batch, head, token), nullable:
+ *     contiguous; the innermost axis is contiguous.  x may have stride 0
+ *     axes.  out == x (same strides) rotates in place; otherwise x and out
+ *     must not overlap.  [T][H][d] rows are B = 1, L = T with strides
+ *     (0, d, H * d).
+ *   positions: device int32, position of (b, l) at [b * position_stride + l]
+ *     (position_stride 0: the same row of positions for every b).
+ *   inv_freq: device double [rot_dim / 2], radians per position (8-byte
+ *     aligned; ss_rope_frequencies makes the usual ones).
+ * Rows that are 16-byte aligned, with rot_offset and d multiples of 8 and
+ * rot_dim a multiple of 16 (interleaved: 8), take 16-byte accesses; any
+ * others single entries.
+ * Returns SS_OK (also for an empty x), SS_ERR_INVALID_ARG (null pointer,
+ * misalignment, odd rot_dim or one outside the row, strides that overlap
+ * output rows, attn_factor not finite), SS_ERR_UNSUPPORTED (d > 65536, or the
+ * device) or SS_ERR_CUDA.
+ */
+ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const int64_t* x_strides,
+                  const int64_t* out_strides, const int32_t* positions, int64_t position_stride,
+                  const double* inv_freq, int rot_dim, int rot_offset, int interleaved, int inverse,
+                  float attn_factor, void* stream);
+
+/*
+ * Rotary positions of a step's packed new tokens, fused with the write of
+ * their keys and values into the cache:  q_out = rotate(q); row L_b - n_b + i
+ * of sequence b's pages = rotate(k), v.
+ *   q, q_out: bf16 [T][Hq][d] (q nullable: keys and values only; q_out may be
+ *     q).  k, v: bf16 [T][Hkv][d] (v nullable: a cache of one row per token,
+ *     as the latent one with Hkv = 1, d = 576, rot_offset = 512, rot_dim =
+ *     64).  *_strides: host arrays of 2 strides in elements (token, head),
+ *     nullable: contiguous; so q, k and v may be parts of one projection.
+ *   positions: device int32 [T], nullable: the key's place L_b - n_b + i.
+ *   rot_dim = 0: no rotation (inv_freq may be NULL).
+ *   k_pages, v_pages: as in ss_attn_decode_paged ([num_pages][Hkv][128][d]).
+ * A key whose place lies outside its table row, or whose page entry is
+ * outside [0, num_pages), is not written (its q is rotated all the same).
+ * Two new tokens never share a place as long as the table names each page
+ * once.  Returns as ss_rope.
+ */
+ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
+                               const int64_t* q_strides, const int64_t* q_out_strides,
+                               const int64_t* k_strides, const int64_t* v_strides, int T, int B, int Hq,
+                               int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* positions, const double* inv_freq, int rot_dim,
+                               int rot_offset, int interleaved, float attn_factor, void* k_pages,
+                               void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
+                               void* stream);
+
+/* How ss_rope_frequencies stretches positions for contexts `factor` times the
+   original length; w_i = base^(-2i / rot_dim). */
+typedef enum {
+  SS_ROPE_PLAIN = 0,      /* w_i */
+  SS_ROPE_LINEAR = 1,     /* w_i / factor */
+  SS_ROPE_BASE = 2,       /* base * factor^(rot_dim / (rot_dim - 2)) instead of base */
+  SS_ROPE_YARN = 3,       /* pairs that make more than `hi` turns over original_length
+                             keep w_i, below `lo` turns w_i / factor, a linear ramp over
+                             the pairs between; attn_factor 0.1 ln(factor) + 1
+                             (YaRN, arXiv 2309.00071) */
+  SS_ROPE_WAVELENGTH = 4  /* the same ends, the ramp linear in the number of turns */
+} ss_rope_scaling;
+
+/*
+ * The rot_dim / 2 frequencies of rotary positions, in radians per position,
+ * into the HOST array `out` (copy it to the device for the calls above), and
+ * the factor for cosines and sines.  original_length, lo and hi (turns) are
+ * read for SS_ROPE_YARN and SS_ROPE_WAVELENGTH, factor for all but
+ * SS_ROPE_PLAIN.  Host only; SS_OK or SS_ERR_INVALID_ARG.
+ */
+ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_scaling scaling,
+                              double factor, int original_length, double lo, double hi,
+                              float* attn_factor_out);
+
+/*
+ * Attention of a step's packed new tokens over the paged cache, with the skip
+ * test: chunked prefill, drafted tokens to verify, single tokens, or a batch
+ * that mixes them; with causal = 0 cross attention to cached states (every new
+ * token of a sequence sees all its L_b keys).  Causal: new token i of sequence
+ * b sees its keys up to L_b - n_b + i; a row that sees no key gives zeros.
+ *   q: bf16 [T][Hq][d], 16-byte aligned; q_token_stride: elements between
+ *     tokens (0: Hq * d; a multiple of 8).  o: bf16 [T][Hq][d] contiguous.
+ *   k_pages, v_pages, page_table, seq_lens, lambda_a: as in
+ *     ss_attn_decode_paged (what a page holds behind its sequence's end is
+ *     not read, whatever it is; keys and values of the sequence itself must
+ *     be finite).
+ *   Voting unit: a block of 128 / G (rounded down) consecutive new tokens of
+ *     one sequence x the G = Hq / Hkv query heads of one KV head x one range
+ *     of tiles.  num_kv_splits cuts each sequence's tiles into ranges as in
+ *     ss_attn_decode_paged; each range keeps its first tile that the unit
+ *     sees.  More ranges keep more SMs busy when there are few new tokens.
+ *   skip_counts: nullable, [ss_attn_chunk_paged_units(...)]: per unit, its
+ *     skipped tiles (0 for units without tokens).  Unit of (range s, KV head
+ *     h, block k of sequence b): ((s * Hkv + h) * places + p) * 2 + k % 2 with
+ *     m = 128 / G, places = T / (2m) + B and p = cu_seqlens[b] / (2m) + b +
+ *     k / 2 (integer divisions).
+ *   workspace: at least ss_attn_chunk_paged_workspace_size(...) bytes, 16-byte
+ *     aligned (nullable when that is 0).
+ *   dbg: nullable; skip_mask / vote_margin are [units][max_pages]; its other
+ *     fields must be 0.
+ * G <= 128, d in {64, 128}.  Returns SS_OK (also for T = 0),
+ * SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
+ */
+size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv, int num_kv_splits);
+size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits);
+ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
+                              const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
+                              const int32_t* seq_lens, void* o, int T, int B, int Hq, int Hkv,
+                              int num_pages, int max_pages, int d, float scale, int causal,
+                              float lambda_a, int num_kv_splits, uint32_t* skip_counts, void* workspace,
+                              size_t workspace_bytes, const ss_debug_opts* dbg, void* stream);
+
+/*
+ * The pages' bookkeeping, all of it on the device (no host round trip; every
+ * call can be captured into a graph).  State, owned by the caller:
+ *   page_refs [num_pages] (16-byte aligned): how many sequences hold a page;
+ *     0: free.
+ *   page_table [num_rows][max_pages], seq_lens [num_rows]: each row a
+ *     sequence (length 0: unused), its keys [128j, 128j + 128) in page
+ *     page_table[row][j]; entries past its last page are unspecified.
+ * Only full pages are shared; a sequence's last page, while not full, is its
+ * own, so new keys can always be appended.  Pools: `pools` is a host array of
+ * num_pools device addresses (16-byte aligned), each num_pages pages of
+ * page_bytes (a multiple of 16) -- the key and the value pages of every layer;
+ * 64 pools a launch.  Calls on one state must be ordered by the caller (one
+ * stream, or events): they read and write it.  `workspace`: at least
+ * ss_pages_workspace_size(num_pages, num_rows, n) bytes, 16-byte aligned, for
+ * this call alone until it has run.
+ * `result` (nullable device int32): 0 done; k > 0: refused, k free pages are
+ * missing; -1: refused, an argument on the device is wrong (below).  A refused
+ * call changes nothing.
+ * All return SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED (device),
+ * SS_ERR_WORKSPACE or SS_ERR_CUDA; device memory beyond the given sizes is
+ * never touched, whatever the device arrays hold.
+ */
+size_t ss_pages_workspace_size(int num_pages, int num_rows, int n);
+
+/*
+ * Sequence rows[i] (rows NULL: row i) grows by add[i] >= 0 keys, i < n: it
+ * receives the lowest free pages, in the order of i, and seq_lens is raised.
+ * Wrong: a row outside the table or listed twice, a negative add, a length
+ * above 128 * max_pages.
+ */
+ss_status ss_pages_reserve(int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows,
+                           int max_pages, int32_t* seq_lens, const int32_t* rows, const int32_t* add,
+                           int n, int32_t* result, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * The listed sequences end: each of their pages loses a holder, their lengths
+ * become 0 and their used table entries -1.  Rows outside the table are
+ * ignored, a row listed twice is freed once.
+ */
+ss_status ss_pages_free(int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows,
+                        int max_pages, int32_t* seq_lens, const int32_t* rows, int n, void* stream);
+
+/*
+ * Unused row dst_rows[i] becomes a copy of sequence src_rows[i]: it holds the
+ * source's full pages too, and a last page that is not full is copied, in
+ * every pool, into the lowest free page (in the order of i).  A source may be
+ * listed many times.  Its table entries past the last page become -1.
+ * Wrong: a row outside the table, a destination that is listed twice, is also
+ * a source, or is in use (length not 0; free it first), a source's length
+ * outside [0, 128 * max_pages].
+ */
+ss_status ss_pages_fork(void* const* pools, int num_pools, size_t page_bytes, int32_t* page_refs,
+                        int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                        int32_t* seq_lens, const int32_t* src_rows, const int32_t* dst_rows, int n,
+                        int32_t* result, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Page src[i] is copied over page dst[i] in every pool, i < n.  Wrong: a page
+ * outside the pool, a destination that is listed twice or is also a source.
+ */
+ss_status ss_pages_copy(void* const* pools, int num_pools, size_t page_bytes, int num_pages,
+                        const int32_t* src, const int32_t* dst, int n, int32_t* result, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Moves the n_live pages in use to the front of the pools: the highest page
+ * in use at or above n_live goes into the lowest free page below it, and so
+ * on.  out_refs, out_table (nullable: in place) receive the new counts and
+ * table (entries past a sequence's last page: -1); *live (nullable device
+ * int32) n_live.  Contents of the pages that became free are unspecified.
+ * Workspace for n = 0.
+ */
+ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes, int32_t* page_refs,
+                           int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                           const int32_t* seq_lens, int32_t* out_refs, int32_t* out_table, int32_t* live,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* A calibration problem: the inputs the threshold is fitted on. */
 typedef enum { SS_PREFILL = 0, SS_DECODE = 1, SS_MLA_DECODE = 2, SS_MLA_PREFILL = 3 } ss_kind;
 typedef struct {

@@ -1,0 +1,268 @@
+"""What the calls around the paged cache refuse before any launch, and their host-side arithmetic (CPU)."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_sm_gb300 as ss
+from block_sparse_attention_sm_gb300 import capi as _capi
+
+BF, I32 = torch.bfloat16, torch.int32
+FAKE = 1 << 20  # a 16-byte-aligned non-null address; never dereferenced here
+
+
+@pytest.fixture(scope="module")
+def capi():
+    ss.build()
+    _capi.load()
+    return _capi
+
+
+# ------------------------------------------------------------------------- frequencies
+
+
+def test_frequencies(capi):
+    rot, base, orig, factor = 64, 10000.0, 4096, 8.0
+    plain = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+
+    def get(**kw):
+        w, f = ss.rope_frequencies(rot, base, original_length=orig, device="cpu", **kw)
+        assert w.dtype == torch.float64 and w.shape == (rot // 2,)
+        return w.tolist(), f
+
+    close = lambda a, b: all(math.isclose(x, y, rel_tol=1e-13) for x, y in zip(a, b))  # noqa: E731
+    w, f = get()
+    assert close(w, plain) and f == 1.0
+    w, f = get(scaling="linear", factor=factor)
+    assert close(w, [x / factor for x in plain]) and f == 1.0
+    w, f = get(scaling="base", factor=factor)
+    assert math.isclose(w[-1], plain[-1] / factor, rel_tol=1e-12) and w[0] == 1.0  # the last pair stretches by factor
+    w, f = get(scaling="yarn", factor=factor)
+    assert math.isclose(f, 0.1 * math.log(factor) + 1, rel_tol=1e-6)
+    turns = [orig * x / (2 * math.pi) for x in plain]
+    for x, y, t in zip(w, plain, turns):
+        assert y / factor * (1 - 1e-12) <= x <= y * (1 + 1e-12)
+        if t > 32 * base ** (2.0 / rot):
+            assert math.isclose(x, y, rel_tol=1e-13)
+        if t < 1 / base ** (2.0 / rot):
+            assert math.isclose(x, y / factor, rel_tol=1e-13)
+    w, f = get(scaling="wavelength", factor=factor)
+    for x, y, t in zip(w, plain, turns):
+        s = min(1.0, max(0.0, (t - 1) / 3))
+        assert math.isclose(x, y * s + y / factor * (1 - s), rel_tol=1e-13) and f == 1.0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rot_dim=0), dict(rot_dim=7), dict(base=1.0), dict(base=float("nan")), dict(scaling=_capi.SS_ROPE_LINEAR, factor=0.5),
+    dict(scaling=_capi.SS_ROPE_LINEAR, factor=float("inf")), dict(scaling=_capi.SS_ROPE_BASE, factor=2.0, rot_dim=2),
+    dict(scaling=_capi.SS_ROPE_YARN, factor=2.0, original_length=0, lo=1.0, hi=32.0),
+    dict(scaling=_capi.SS_ROPE_YARN, factor=2.0, original_length=10, lo=4.0, hi=4.0),
+    dict(scaling=_capi.SS_ROPE_WAVELENGTH, factor=2.0, original_length=10, lo=0.0, hi=4.0),
+    dict(scaling=9, factor=2.0),
+])
+def test_frequencies_refuse(capi, kw):
+    args = dict(rot_dim=64, base=10000.0)
+    args.update(kw)
+    assert capi.ss_rope_frequencies(**args)[0] == capi.SS_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------------- C entry points
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(x=None), "INVALID_ARG"), (dict(positions=None), "INVALID_ARG"), (dict(inv_freq=None), "INVALID_ARG"),
+    (dict(x=FAKE + 1), "INVALID_ARG"), (dict(inv_freq=FAKE + 4), "INVALID_ARG"),
+    (dict(rot_dim=0), "INVALID_ARG"), (dict(rot_dim=63), "INVALID_ARG"), (dict(rot_dim=130), "INVALID_ARG"),
+    (dict(rot_offset=1), "INVALID_ARG"), (dict(rot_offset=-2), "INVALID_ARG"), (dict(B=-1), "INVALID_ARG"),
+    (dict(attn_factor=float("nan")), "INVALID_ARG"), (dict(out_strides=(512, 64, 128)), "INVALID_ARG"),
+    (dict(out_strides=(0, 512, 128)), "INVALID_ARG"), (dict(x_strides=(-512, 512, 128)), "INVALID_ARG"),
+    (dict(out=FAKE, x_strides=(4096, 1024, 256)), "INVALID_ARG"),   # in place with other strides
+    (dict(d=1 << 17), "UNSUPPORTED"), (dict(position_stride=-4), "INVALID_ARG"),
+    (dict(L=0, x=None), "OK"),
+])
+def test_rope_rejects(capi, kw, expect):
+    args = dict(x=FAKE, out=2 * FAKE, B=2, H=2, L=4, d=128, positions=FAKE, inv_freq=FAKE, rot_dim=128, stream=0)
+    args.update(kw)
+    assert capi.ss_rope(**args) == getattr(capi, "SS_OK" if expect == "OK" else "SS_ERR_" + expect)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(k=None), "INVALID_ARG"), (dict(q_out=None), "INVALID_ARG"), (dict(v_pages=None), "INVALID_ARG"),
+    (dict(k_pages=FAKE + 2), "INVALID_ARG"), (dict(cu_seqlens=None), "INVALID_ARG"), (dict(seq_lens=None), "INVALID_ARG"),
+    (dict(page_table=FAKE + 2), "INVALID_ARG"), (dict(T=-1), "INVALID_ARG"), (dict(B=0), "INVALID_ARG"),
+    (dict(num_pages=0), "INVALID_ARG"), (dict(max_pages=1 << 25), "INVALID_ARG"), (dict(rot_dim=200), "INVALID_ARG"),
+    (dict(inv_freq=None), "INVALID_ARG"), (dict(q_out_strides=(1024, 0)), "INVALID_ARG"),
+    (dict(q_out=FAKE, q_strides=(4096, 128)), "INVALID_ARG"), (dict(d=1 << 17), "UNSUPPORTED"), (dict(T=0), "OK"),
+])
+def test_append_rejects(capi, kw, expect):
+    args = dict(q=FAKE, q_out=2 * FAKE, k=FAKE, v=FAKE, T=5, B=2, Hq=8, Hkv=2, d=128, cu_seqlens=FAKE, seq_lens=FAKE,
+                inv_freq=FAKE, rot_dim=128, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, num_pages=4, max_pages=4, stream=0)
+    args.update(kw)
+    assert capi.ss_rope_append_paged(**args) == getattr(capi, "SS_OK" if expect == "OK" else "SS_ERR_" + expect)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q=None), "INVALID_ARG"), (dict(q=FAKE + 8), "INVALID_ARG"), (dict(page_table=None), "INVALID_ARG"),
+    (dict(cu_seqlens=None), "INVALID_ARG"), (dict(seq_lens=None), "INVALID_ARG"), (dict(o=None), "INVALID_ARG"),
+    (dict(T=-1), "INVALID_ARG"), (dict(B=0), "INVALID_ARG"), (dict(Hq=9), "INVALID_ARG"), (dict(num_pages=0), "INVALID_ARG"),
+    (dict(max_pages=1 << 25), "INVALID_ARG"), (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
+    (dict(lambda_a=-1.0), "INVALID_ARG"), (dict(lambda_a=float("nan")), "INVALID_ARG"), (dict(num_kv_splits=0), "INVALID_ARG"),
+    (dict(q_token_stride=1020), "INVALID_ARG"), (dict(q_token_stride=512), "INVALID_ARG"), (dict(d=96), "UNSUPPORTED"),
+    (dict(Hq=258), "UNSUPPORTED"), (dict(num_kv_splits=2), "WORKSPACE"),
+    (dict(num_kv_splits=2, workspace=FAKE, workspace_bytes=2 * 5 * 8 * 130 * 4 - 1), "WORKSPACE"), (dict(T=0), "OK"),
+])
+def test_chunk_rejects(capi, kw, expect):
+    args = dict(q=FAKE, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, cu_seqlens=FAKE, seq_lens=FAKE, o=FAKE, T=5, B=2, Hq=8,
+                Hkv=2, num_pages=4, max_pages=4, d=128, scale=0.1, causal=True, lambda_a=0.0, num_kv_splits=1, stream=0)
+    args.update(kw)
+    assert capi.ss_attn_chunk_paged(**args) == getattr(capi, "SS_OK" if expect == "OK" else "SS_ERR_" + expect)
+
+
+def test_chunk_refuses_test_only_debug_fields(capi):
+    import ctypes
+
+    for field in ("count_only", "fault_inject", "vote_chunk_tiles", "prefill_kernel"):
+        dbg = capi.ss_debug_opts()
+        setattr(dbg, field, 1)
+        st = capi.load().ss_attn_chunk_paged(FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 5, 2, 8, 2, 4, 4, 128, 0.1, 1, 0.0, 1,
+                                             None, None, 0, ctypes.byref(dbg), None)
+        assert st == capi.SS_ERR_UNSUPPORTED
+
+
+def test_sizes(capi):
+    assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 1) == 0
+    assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 3) == 3 * 10 * 8 * 130 * 4
+    assert capi.ss_attn_chunk_paged_units(1000, 7, 8, 2, 3) == 2 * (1000 // 64 + 7) * 2 * 3
+    assert capi.ss_attn_chunk_paged_units(1000, 7, 6, 2, 1) == 2 * (1000 // 84 + 7) * 2
+    assert capi.ss_attn_chunk_paged_units(10, 1, 258, 2, 1) == 0
+    assert capi.ss_pages_workspace_size(100, 7, 5) >= 4 * (3 * 100 + 2 * 5)
+
+
+@pytest.mark.parametrize("m", [1, 8, 18, 42, 128])
+def test_places_of_row_blocks_never_meet(m):
+    """floor(cu[b] / 2m) + b leaves room for every sequence's pairs of blocks."""
+    import random
+
+    r = random.Random(m)
+    for _ in range(300):
+        n = [r.choice([0, 1, m, 2 * m, 2 * m + 1, r.randint(0, 9 * m)]) for _ in range(r.randint(1, 12))]
+        cu = [sum(n[:i]) for i in range(len(n) + 1)]
+        places = cu[-1] // (2 * m) + len(n)
+        start = [cu[b] // (2 * m) + b for b in range(len(n))]
+        for b, x in enumerate(n):
+            end = start[b] + -(-x // (2 * m))
+            assert end <= (start[b + 1] if b + 1 < len(n) else places)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(page_refs=None), "INVALID_ARG"), (dict(page_refs=FAKE + 4), "INVALID_ARG"), (dict(page_table=None), "INVALID_ARG"),
+    (dict(seq_lens=None), "INVALID_ARG"), (dict(num_pages=0), "INVALID_ARG"), (dict(num_rows=0), "INVALID_ARG"),
+    (dict(max_pages=1 << 25), "INVALID_ARG"), (dict(n=-1), "INVALID_ARG"),
+])
+def test_pages_reject_state(capi, kw, expect):
+    state = dict(page_refs=FAKE, num_pages=10, page_table=FAKE, num_rows=4, max_pages=4, seq_lens=FAKE, n=2)
+    state.update(kw)
+    ws = dict(workspace=FAKE, workspace_bytes=1 << 20, stream=0)
+    want = getattr(capi, "SS_ERR_" + expect)
+    assert capi.ss_pages_reserve(rows=None, add=FAKE, **state, **ws) == want
+    assert capi.ss_pages_free(rows=FAKE, **state, stream=0) == want
+    assert capi.ss_pages_fork([FAKE], 256, src_rows=FAKE, dst_rows=FAKE, **state, **ws) == want
+    if "n" not in kw:
+        state.pop("n")
+        assert capi.ss_pages_compact([FAKE], 256, **state, **ws) == want
+
+
+def test_pages_reject_pools_lists_and_workspaces(capi):
+    state = dict(page_refs=FAKE, num_pages=10, page_table=FAKE, num_rows=4, max_pages=4, seq_lens=FAKE)
+    ws = dict(workspace=FAKE, workspace_bytes=1 << 20, stream=0)
+    bad, small = capi.SS_ERR_INVALID_ARG, capi.SS_ERR_WORKSPACE
+    for pools, page_bytes in (([None], 256), ([FAKE + 8], 256), ([FAKE], 24), ([FAKE], 0)):
+        assert capi.ss_pages_fork(pools, page_bytes, src_rows=FAKE, dst_rows=FAKE, n=2, **state, **ws) == bad
+        assert capi.ss_pages_compact(pools, page_bytes, **state, **ws) == bad
+        assert capi.ss_pages_copy(pools, page_bytes, 10, FAKE, FAKE, 2, **ws) == bad
+    assert capi.ss_pages_copy([], 256, 10, FAKE, FAKE, 2, **ws) == bad
+    assert capi.ss_pages_copy([FAKE], 256, 10, None, FAKE, 2, **ws) == bad
+    assert capi.ss_pages_fork([FAKE], 256, src_rows=None, dst_rows=FAKE, n=2, **state, **ws) == bad
+    assert capi.ss_pages_reserve(rows=None, add=FAKE, n=5, **state, **ws) == bad  # more entries than rows
+    ws["workspace_bytes"] = 16
+    assert capi.ss_pages_reserve(rows=None, add=FAKE, n=2, **state, **ws) == small
+    assert capi.ss_pages_compact([FAKE], 256, **state, **ws) == small
+    assert capi.ss_pages_copy([FAKE], 256, 10, FAKE, FAKE, 2, **ws) == small
+
+
+# ----------------------------------------------------------------------------- helpers
+
+
+def _z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+FREQ = torch.ones(32, dtype=torch.float64)
+
+
+def test_rope_helper_refuses():
+    x, pos = _z(2, 3, 5, 64), _z(5, dtype=I32)
+    for kw, match in ((dict(x=x.float()), "element type"), (dict(x=_z(5, 64)), "expects x"),
+                      (dict(x=x.transpose(2, 3)), "last axis"), (dict(positions=_z(4, dtype=I32)), "expected shape"),
+                      (dict(positions=pos.long()), "element type"), (dict(inv_freq=FREQ.float()), "element type"),
+                      (dict(inv_freq=torch.ones(33, dtype=torch.float64)), "entries"), (dict(rot_offset=2), "entries"),
+                      (dict(out=_z(2, 3, 5, 32)), "expected shape"), (dict(out=_z(1, 3, 5, 64).expand(2, 3, 5, 64)), "overlap"),
+                      (dict(), "CUDA tensor")):
+        args = dict(x=x, positions=pos, inv_freq=FREQ)
+        args.update(kw)
+        with pytest.raises((ValueError, TypeError), match=match):
+            ss.rope(**args)
+    whole = _z(1, 3, 6, 64)
+    with pytest.raises(ValueError, match="overlaps its input"):
+        ss.rope(whole[:, :, 1:], pos, FREQ, out=whole[:, :, :5])
+
+
+def test_append_helper_refuses():
+    args = dict(q=_z(5, 4, 64), k=_z(5, 2, 64), v=_z(5, 2, 64), k_pages=_z(3, 2, 128, 64), v_pages=_z(3, 2, 128, 64),
+                page_table=_z(2, 4, dtype=I32), cu_seqlens=_z(3, dtype=I32), seq_lens=_z(2, dtype=I32), inv_freq=FREQ)
+    for kw, match in ((dict(q=_z(4, 4, 64)), "expects q"), (dict(v=None), "given together"), (dict(v=_z(5, 1, 64)), "v: expected"),
+                      (dict(k_pages=_z(3, 2, 64, 64)), "k_pages"), (dict(v_pages=_z(2, 2, 128, 64)), "v_pages"),
+                      (dict(page_table=_z(2, 4)), "page_table"), (dict(cu_seqlens=_z(2, dtype=I32)), "cu_seqlens"),
+                      (dict(seq_lens=_z(3, dtype=I32)), "seq_lens"), (dict(positions=_z(4, dtype=I32)), "positions"),
+                      (dict(out=_z(5, 4, 32)), "out"), (dict(q=None, out=_z(5, 4, 64)), "without q"),
+                      (dict(rot_offset=64), "entries"), (dict(), "CUDA tensor")):
+        with pytest.raises((ValueError, TypeError), match=match):
+            ss.rope_append_paged(**{**args, **kw})
+
+
+def test_chunk_helper_refuses():
+    args = dict(q=_z(5, 4, 64), k_pages=_z(3, 2, 128, 64), v_pages=_z(3, 2, 128, 64), page_table=_z(2, 4, dtype=I32),
+                cu_seqlens=_z(3, dtype=I32), seq_lens=_z(2, dtype=I32), scale=0.1)
+    units = 2 * (5 // 128 + 2) * 2
+    ss.build()
+    for kw, match in ((dict(q=_z(5, 64, 4).transpose(1, 2)), "last axis"), (dict(q=_z(5, 8, 64)[:, ::2]), "heads of a token"),
+                      (dict(k_pages=_z(3, 2, 128, 128)), "k_pages"), (dict(v_pages=_z(3, 1, 128, 64)), "v_pages"),
+                      (dict(cu_seqlens=_z(4, dtype=I32)), "cu_seqlens"), (dict(out=_z(5, 4, 128)), "out"),
+                      (dict(counts=_z(units - 1, dtype=I32)), "counts"), (dict(skip_mask=_z(units * 4 - 1, dtype=torch.uint8)), "skip_mask"),
+                      (dict(), "CUDA tensor")):
+        with pytest.raises((ValueError, TypeError), match=match):
+            ss.chunk_paged(**{**args, **kw})
+
+
+def test_pages_helpers_refuse():
+    state = dict(page_refs=_z(8, dtype=I32), page_table=_z(3, 4, dtype=I32), seq_lens=_z(3, dtype=I32))
+    pools, one = [_z(8, 16)], _z(1, dtype=I32)
+    with pytest.raises(ValueError, match="seq_lens"):
+        ss.pages_free(**{**state, "seq_lens": _z(4, dtype=I32)}, rows=one)
+    with pytest.raises(ValueError, match="rows"):
+        ss.pages_reserve(**state, add=one, rows=_z(2, dtype=I32))
+    with pytest.raises(ValueError, match="4 entries for 3 rows"):
+        ss.pages_reserve(**state, add=_z(4, dtype=I32))
+    for bad in ([_z(7, 16)], [_z(8, 16), _z(8, 32)], [_z(16, 8).t()]):
+        with pytest.raises(ValueError, match=r"pools\["):
+            ss.pages_fork(bad, **state, src_rows=one, dst_rows=one)
+    with pytest.raises(ValueError, match="dst_rows"):
+        ss.pages_fork(pools, **state, src_rows=one, dst_rows=_z(2, dtype=I32))
+    with pytest.raises(ValueError, match="no pools"):
+        ss.pages_copy([], one, one)
+    with pytest.raises(ValueError, match="out_table"):
+        ss.pages_compact(pools, **state, out_table=_z(3, 5, dtype=I32))
+    for call in (lambda: ss.pages_free(**state, rows=one), lambda: ss.pages_compact(pools, **state),
+                 lambda: ss.pages_copy(pools, one, one), lambda: ss.pages_reserve(**state, add=one)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()

@@ -1,0 +1,234 @@
+"""Rotary positions, alone and with the cache write, against 64-bit arithmetic (GPU)."""
+import decimal
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from _serving import (PAGE, assert_rounded, fill_pool, offsets, random_tables, rotate, rotate_tolerance, tiles)
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import block_sparse_attention_sm_gb300 as ss
+
+    ss.build()
+    assert torch.cuda.is_available()
+
+
+def _x(shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(BF)
+
+
+def _freq(rot, base=10000.0):
+    return torch.tensor([base ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+
+
+SHAPES = [
+    # B, H, L, d, rot, off
+    (1, 1, 1, 64, 64, 0),
+    (2, 3, 5, 128, 128, 0),
+    (1, 32, 7, 128, 64, 0),      # the first half of the head turns
+    (3, 2, 130, 64, 32, 32),     # the second
+    (1, 16, 33, 192, 64, 128),   # latent prefill rows
+    (2, 1, 129, 576, 64, 512),   # latent cache rows
+    (2, 5, 9, 80, 24, 8),        # 12 pairs: single entries
+    (1, 3, 4, 33, 10, 7),        # odd width and place
+    (1, 2, 3, 2, 2, 0),
+    (1, 70, 2, 256, 256, 0),
+]
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_rope(shape, interleaved, inverse):
+    import block_sparse_attention_sm_gb300 as ss
+
+    B, H, L, d, rot, off = shape
+    x = _x((B, H, L, d), 1)
+    pos = torch.randint(0, 1 << 20, (B, L), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    pos[0, 0] = 0
+    w, f = _freq(rot), 1.25
+    out = ss.rope(x.cuda(), pos.cuda(), w.cuda(), rot_offset=off, interleaved=interleaved, inverse=inverse,
+                  attn_factor=f)
+    want = rotate(x, pos[:, None], w, f, off, interleaved, inverse)
+    assert_rounded(out.cpu(), want, rotate_tolerance(x, w, f, off, interleaved))
+    assert torch.equal(out.cpu()[..., :off], x[..., :off])
+    assert torch.equal(out.cpu()[..., off + rot:], x[..., off + rot:])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_packed_strided_and_in_place(interleaved):
+    """[T,H,d] rows inside a wider projection; a row of positions shared by the batch; in place; empty."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    T, Hq, Hkv, d = 37, 6, 2, 128
+    w = _freq(d).cuda()
+    proj = _x((T, Hq + 2 * Hkv, d), 3)
+    pos = torch.arange(T, dtype=torch.int32) * 911
+    dev = proj.cuda()
+    q = dev[:, :Hq]
+    want = rotate(proj[:, :Hq], pos[:, None], w.cpu(), 1.0, 0, interleaved)
+    tol = rotate_tolerance(proj[:, :Hq], w.cpu(), 1.0, 0, interleaved)
+    out = ss.rope(q, pos.cuda(), w, interleaved=interleaved)
+    assert out.is_contiguous()
+    assert_rounded(out.cpu(), want, tol)
+    same = ss.rope(q, pos.cuda(), w, interleaved=interleaved, out=q)
+    assert same.data_ptr() == dev.data_ptr()
+    assert torch.equal(dev[:, :Hq].cpu(), out.cpu())
+    assert torch.equal(dev[:, Hq:].cpu(), proj[:, Hq:])  # the rows' other heads are as they were
+    # heads 8 bytes off the 16-byte grid take single entries: the same results
+    odd = torch.empty(T, Hq * d + 4, dtype=BF, device="cuda")[:, 4:].unflatten(1, (Hq, d))
+    odd.copy_(proj[:, :Hq])
+    assert torch.equal(ss.rope(odd, pos.cuda(), w, interleaved=interleaved).cpu(), out.cpu())
+    # one head broadcast over the batch
+    wide = proj[:, :1].cuda().transpose(0, 1)[None].expand(3, 1, T, d)
+    got = ss.rope(wide, pos.cuda(), w, interleaved=interleaved)
+    for b in range(3):
+        assert torch.equal(got[b, 0].cpu(), out[:, 0].cpu())
+    for empty in (torch.empty(0, 3, d), torch.empty(5, 0, d)):
+        e = empty.to(BF).cuda()
+        assert ss.rope(e, torch.zeros(e.shape[0], dtype=torch.int32, device="cuda"), w).shape == e.shape
+
+
+def test_rope_far_positions_are_exact():
+    """Angles up to position 2^31 - 1 (and negative ones) against 60-digit arithmetic."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    decimal.getcontext().prec = 60
+    two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    rot = 128
+    w = _freq(rot, 500000.0)
+    pos = [0, 1, -1, 131071, 10 ** 6 + 7, (1 << 24) + 1, (1 << 31) - 1, -(1 << 31)]
+    x = torch.zeros(len(pos), 1, rot, dtype=BF)
+    x[:, :, :rot // 2] = 1.0  # a = 1, b = 0: the outputs are cos and sin
+    out = ss.rope(x.cuda(), torch.tensor(pos, dtype=torch.int32, device="cuda"), w.cuda()).cpu().double()
+    for i, p in enumerate(pos):
+        for j in range(rot // 2):
+            t = float((decimal.Decimal(p) * decimal.Decimal(float(w[j]))) % two_pi)
+            for got, want in ((out[i, 0, j], math.cos(t)), (out[i, 0, rot // 2 + j], math.sin(t))):
+                assert abs(float(got) - want) <= abs(want) * 2.0 ** -8 + 1e-6, (p, j, float(got), want)
+
+
+def test_rope_gradient():
+    """rope(g, inverse) is the gradient: against differences of the 64-bit rotation, and <g, R x> = <R' g, x>."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    B, H, L, d, rot, off, f = 1, 2, 6, 64, 32, 16, 1.5
+    x, g = _x((B, H, L, d), 5), _x((B, H, L, d), 6)
+    pos, w = torch.arange(L, dtype=torch.int32) * 333, _freq(rot)
+    grad = ss.rope(g.cuda(), pos.cuda(), w.cuda(), rot_offset=off, inverse=True, attn_factor=f).cpu().double()
+    eps = 2.0 ** -10
+    value = lambda z: (rotate(z, pos, w, f, off, False) * g.double()).sum()  # noqa: E731
+    tol = rotate_tolerance(g, w, f, off, False)
+    for i in np.random.default_rng(0).integers(0, x.numel(), 40):
+        e = torch.zeros(x.numel(), dtype=torch.float64)
+        e[i] = eps
+        diff = float(value(x.double() + e.view_as(x)) - value(x.double() - e.view_as(x))) / (2 * eps)
+        got = float(grad.flatten()[i])  # the value is linear in x: the difference is exact to ~1e-11
+        assert abs(got - diff) <= float(tol.flatten()[i]) + (abs(diff) + 1e-6) * 2.0 ** -8 + 1e-9
+
+
+def test_rope_of_a_batch_larger_than_one_wave():
+    import block_sparse_attention_sm_gb300 as ss
+
+    x = torch.randn(2, 8, 4097, 128, device="cuda", dtype=BF)
+    pos = torch.arange(4097, dtype=torch.int32, device="cuda")
+    w = _freq(128).cuda()
+    out = ss.rope(x, pos, w)
+    for l in (0, 1, 2048, 4096):
+        want = rotate(x[:, :, l].cpu(), pos[l].cpu(), w.cpu(), 1.0, 0, False)
+        assert_rounded(out[:, :, l].cpu(), want, rotate_tolerance(x[:, :, l].cpu(), w.cpu(), 1.0, 0, False))
+
+
+APPEND = [
+    # Hq, Hkv, d, rot, off, new tokens, lengths after them
+    (4, 2, 128, 128, 0, [1, 1, 1], [1, 128, 129]),
+    (8, 1, 64, 32, 0, [5, 0, 130, 1], [5, 77, 400, 256]),
+    (3, 3, 64, 24, 8, [7, 300, 2], [200, 300, 2]),        # single entries
+    (16, 1, 576, 64, 512, [3, 1, 0, 129], [140, 64, 0, 129]),  # latent rows
+    (32, 8, 128, 128, 0, [1] * 40, list(range(1, 41))),
+    (1, 1, 576, 10, 3, [2, 9], [2, 500]),                 # 576-wide rows in single entries
+    (2, 2, 128, 0, 0, [4, 140], [130, 140]),              # no rotation
+]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("case", APPEND)
+def test_append(case, interleaved):
+    import block_sparse_attention_sm_gb300 as ss
+
+    Hq, Hkv, d, rot, off, n, L = case
+    rng = np.random.default_rng(4)
+    latent = d == 576
+    pad = 3  # rows behind the last sequence
+    T = sum(n) + pad
+    q, k, v = _x((T, Hq, d), 1), _x((T, Hkv, d), 2), _x((T, Hkv, d), 3)
+    table, pages = random_tables(L, 2, rng)
+    old_k, old_v = _x((pages, Hkv, PAGE, d), 7), _x((pages, Hkv, PAGE, d), 8)
+    w = _freq(rot) if rot else torch.empty(0, dtype=torch.float64)
+    cu = offsets(n)
+    seq = np.repeat(np.arange(len(n)), n)
+    pos = torch.tensor([L[b] - n[b] + i for b in range(len(n)) for i in range(n[b])], dtype=torch.int64)
+    kp, vp = old_k.cuda(), old_v.cuda()
+    if latent:
+        kp = kp[:, 0].contiguous()
+    out = torch.full((T, Hq, d), 9.0, dtype=BF, device="cuda")
+    # q, k and v as parts of one projection
+    proj = torch.cat([q, k, v], 1).cuda()
+    qd, kd, vd = proj.split([Hq, Hkv, Hkv], 1)
+    got = ss.rope_append_paged(qd, kd, None if latent else vd, kp, None if latent else vp, table.cuda(), cu.cuda(),
+                               torch.tensor(L, dtype=torch.int32, device="cuda"), w.cuda() if rot else None,
+                               rot_offset=off, interleaved=interleaved, attn_factor=1.5, out=out)
+    assert got is out
+    real = T - pad
+    f = 1.5
+    assert_rounded(out[:real].cpu(), rotate(q[:real], pos[:, None], w, f, off, interleaved),
+                   rotate_tolerance(q[:real], w, f, off, interleaved))
+    assert (out[real:] == 9.0).all()
+    want_k, want_v = old_k.double(), old_v.double()
+    tol = torch.zeros_like(want_k)
+    page, row = table[seq, pos.numpy() // PAGE].long(), pos % PAGE
+    want_k[page, :, row] = rotate(k[:real], pos[:, None], w, f, off, interleaved)
+    tol[page, :, row] = rotate_tolerance(k[:real], w, f, off, interleaved)
+    want_v[page, :, row] = v[:real].double()
+    kp = kp[:, None] if latent else kp
+    written = torch.zeros_like(want_k, dtype=torch.bool)
+    written[page, :, row] = True
+    assert_rounded(kp.cpu(), want_k, tol)
+    assert torch.equal(kp.cpu()[~written], old_k[~written])
+    if not latent:
+        assert torch.equal(vp.cpu().double(), want_v)
+
+
+def test_append_keys_without_a_page_and_given_positions():
+    """Places outside the table or the pool are not written; positions override the angle, not the place."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    d, pages = 64, 3
+    w = _freq(d)
+    # sequence 0: its second page does not exist; 1: shorter than its new tokens; 2: longer than the table
+    n, L = [200, 5, 2], [200, 3, 300]
+    table = torch.tensor([[0, 99], [1, -1], [2, 2]], dtype=torch.int32)
+    T = sum(n)
+    k, v = _x((T, 1, d), 1), _x((T, 1, d), 2)
+    pos = torch.randint(0, 5000, (T,), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    old = _x((pages, 1, PAGE, d), 3)
+    kp, vp = old.cuda(), old.cuda()
+    none = ss.rope_append_paged(None, k.cuda(), v.cuda(), kp, vp, table.cuda(), offsets(n).cuda(),
+                                torch.tensor(L, dtype=torch.int32, device="cuda"), w.cuda(), positions=pos.cuda())
+    assert none is None
+    want, want_v, tol = old.double(), old.clone(), torch.zeros(old.shape, dtype=torch.float64)
+    turned, t = rotate(k, pos[:, None], w, 1.0, 0, False), rotate_tolerance(k, w, 1.0, 0, False)
+    for i in range(128):  # of sequence 0, the first page
+        want[0, 0, i], tol[0, 0, i], want_v[0, 0, i] = turned[i, 0], t[i, 0], v[i, 0]
+    for i in range(2, 5):  # of sequence 1, keys 0 .. 2 (its first two tokens lie before key 0)
+        want[1, 0, i - 2], tol[1, 0, i - 2], want_v[1, 0, i - 2] = turned[200 + i, 0], t[200 + i, 0], v[200 + i, 0]
+    assert_rounded(kp.cpu(), want, tol)
+    assert torch.equal(vp.cpu(), want_v)
