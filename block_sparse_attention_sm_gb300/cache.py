@@ -30,26 +30,28 @@ def _dense(name, t, dtype, ndim=None, shape=None):
     """A contiguous tensor argument of this type, rank or shape."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: element type must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if ndim is not None and t.dim() != ndim:
+    if ndim is not None and t.ndim != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
 
 
 def _rows(name, t, ndim):
-    """A bf16 tensor argument whose rows (innermost axis) are contiguous."""
+    """Shape and strides of a bf16 tensor argument whose rows (innermost axis) are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != _BF16:
+    if t.dtype is not _BF16:
         raise ValueError(f"{name}: element type must be {_BF16}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
+    return shape, strides
 
 
 def _writable(name, t):
@@ -62,51 +64,39 @@ def _writable(name, t):
     return t
 
 
-class _Launch:
-    """Device and stream of a call: ``handle`` for the library; entered, torch
-    allocates on that stream and the device is current."""
+def _on(stream, names, *tensors):
+    """Device and stream of a call: (stream handle, context to make it in).
 
-    __slots__ = ("handle", "_stack")
+    All tensors must be on one CUDA device.  Inside the context that device is
+    current and torch allocates on that stream; where both are so already
+    there is nothing to enter."""
+    dev = None
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{names.split()[i]}: must be a CUDA tensor, got device {t.device}")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on several devices: {names.split()[i]} on {t.device}, others on cuda:{dev}")
+    if stream is None and torch._C._cuda_getDevice() == dev:  # (a tensor on a GPU: CUDA is initialised)
+        return torch._C._cuda_getCurrentRawStream(dev), _HERE
+    if isinstance(stream, int):
+        device = torch.device("cuda", dev)
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    elif stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(dev))
+    stack.enter_context(torch.cuda.stream(stream))
+    return stream.cuda_stream, stack
 
-    def __init__(self, stream, *tensors):
-        dev = None
-        for name, t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{name}: must be a CUDA tensor, got device {t.device}")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on several devices: {dev}, {name} on {t.device}")
-        contexts = []
-        if torch.cuda.current_device() != dev.index:
-            contexts.append(torch.cuda.device(dev))
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-            elif stream.device != dev:
-                raise ValueError(f"stream of {stream.device}, tensors on {dev}")
-            self.handle = stream.cuda_stream
-            contexts.append(torch.cuda.stream(stream))
-        self._stack = None
-        if contexts:
-            self._stack = contextlib.ExitStack()
-            self._contexts(contexts)
 
-    def _contexts(self, contexts):
-        for c in contexts:
-            self._stack.enter_context(c)
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self._stack is not None:
-            self._stack.close()
-        return False
+_HERE = contextlib.nullcontext()
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -137,19 +127,17 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
     [rot_offset, rot_offset + rot_dim) turn, the others are copied.
     ``inverse``: the transposed rotation; the gradient of ``rope`` with respect
     to x is ``rope(grad, ..., inverse=True)`` with the same other arguments."""
-    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
+    if not isinstance(x, torch.Tensor) or x.ndim not in (3, 4):
         raise ValueError("rope expects x [B,H,L,d] or [T,H,d]")
-    packed = x.dim() == 3
-    _rows("x", x, x.dim())
-    _dense("inv_freq", inv_freq, _F64, ndim=1)
-    d, rot = x.shape[-1], 2 * inv_freq.shape[0]
+    packed = x.ndim == 3
+    shape, xs = _rows("x", x, x.ndim)
+    _dense("inv_freq", inv_freq, _F64, 1)
     if packed:
-        L, H, _ = x.shape
-        B = 1
-        _dense("positions", positions, _I32, shape=(L,))
-        pos_stride = 0
+        L, H, d = shape
+        B, pos_stride = 1, 0
+        _dense("positions", positions, _I32, None, (L,))
     else:
-        B, H, L, _ = x.shape
+        B, H, L, d = shape
         _dense("positions", positions, _I32)
         if positions.shape == (L,):
             pos_stride = 0
@@ -157,24 +145,30 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
             pos_stride = L
         else:
             raise ValueError(f"positions: expected shape {(L,)} or {(B, L)}, got {tuple(positions.shape)}")
+    rot = 2 * inv_freq.shape[0]
     if rot < 2 or rot_offset < 0 or rot_offset + rot > d:
         raise ValueError(f"rope: entries [{rot_offset}, {rot_offset + rot}) of rows of {d}")
     if out is not None:
-        _rows("out", out, x.dim())
-        if out.shape != x.shape:
-            raise ValueError(f"out: expected shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        if out is not x:
-            _no_overlap("out", out, x)
-        _writable("out", out)
-    with _Launch(stream, ("x", x), ("positions", positions), ("inv_freq", inv_freq), ("out", out)) as handle:
-        o = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        xs, os_ = x.stride(), o.stride()
+        _output("out", out, x, shape)
+    handle, context = _on(stream, "x positions inv_freq out", x, positions, inv_freq, out)
+    with context:
+        o = out if out is not None else torch.empty(shape, dtype=_BF16, device=x.device)
+        os_ = o.stride()
         if packed:
             xs, os_ = (0, xs[1], xs[0]), (0, os_[1], os_[0])
         st = capi.ss_rope(x, o, B, H, L, d, positions, inv_freq, rot, xs[:3], os_[:3], pos_stride, rot_offset,
                           interleaved, inverse, attn_factor, handle)
     _check(st, "ss_rope")
     return o
+
+
+def _output(name, out, x, shape):
+    """``out`` for the rows of x: x itself, or memory of its own."""
+    if _rows(name, out, len(shape))[0] != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    if out is not x:
+        _no_overlap(name, out, x)
+    _writable(name, out)
 
 
 def _no_overlap(name, t, x):
@@ -187,12 +181,12 @@ def _no_overlap(name, t, x):
         raise ValueError(f"{name}: overlaps its input (only the same memory, in place, is allowed)")
 
 
-def _batch(T, page_table, cu_seqlens, seq_lens):
+def _batch(page_table, cu_seqlens, seq_lens):
     """Sequences and table width of a packed step."""
-    _dense("page_table", page_table, _I32, ndim=2)
+    _dense("page_table", page_table, _I32, 2)
     B, max_pages = page_table.shape
-    _dense("cu_seqlens", cu_seqlens, _I32, shape=(B + 1,))
-    _dense("seq_lens", seq_lens, _I32, shape=(B,))
+    _dense("cu_seqlens", cu_seqlens, _I32, None, (B + 1,))
+    _dense("seq_lens", seq_lens, _I32, None, (B,))
     return B, max_pages
 
 
@@ -210,55 +204,51 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
     ``positions`` int32 [T] says otherwise.  inv_freq None: no rotation.
     Returns the rotated q (``out``; ``out=q``: in place), rows behind the last
     sequence left as they were, or None without q."""
-    _rows("k", k, 3)
-    T, Hkv, d = k.shape
+    (T, Hkv, d), ks = _rows("k", k, 3)
+    Hq, qs, os_, vs = 0, (0, 0), (0, 0), (0, 0)
     if q is not None:
-        _rows("q", q, 3)
-        if q.shape[0] != T or q.shape[2] != d:
+        q_shape, qs = _rows("q", q, 3)
+        Hq = q_shape[1]
+        if q_shape[0] != T or q_shape[2] != d:
             raise ValueError("rope_append_paged expects q [T,Hq,d] and k [T,Hkv,d]")
-    B, max_pages = _batch(T, page_table, cu_seqlens, seq_lens)
-    latent = v is None and isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3
+    B, max_pages = _batch(page_table, cu_seqlens, seq_lens)
+    latent = v is None and isinstance(k_pages, torch.Tensor) and k_pages.ndim == 3
     if latent and Hkv != 1:
         raise ValueError("k_pages [num_pages,128,d] hold one head")
-    _dense("k_pages", k_pages, _BF16, ndim=3 if latent else 4)
-    if k_pages.shape[1:] != ((128, d) if latent else (Hkv, 128, d)):
-        raise ValueError(f"k_pages: expected [num_pages, {Hkv}, 128, {d}], got {tuple(k_pages.shape)}")
+    _dense("k_pages", k_pages, _BF16, 3 if latent else 4)
+    pool = k_pages.shape
+    if pool[1:] != ((128, d) if latent else (Hkv, 128, d)):
+        raise ValueError(f"k_pages: expected [num_pages, {Hkv}, 128, {d}], got {tuple(pool)}")
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages are given together")
     if v is not None:
-        _rows("v", v, 3)
-        if v.shape != k.shape:
-            raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
-        _dense("v_pages", v_pages, _BF16, shape=k_pages.shape)
+        v_shape, vs = _rows("v", v, 3)
+        if v_shape != (T, Hkv, d):
+            raise ValueError(f"v: expected shape {(T, Hkv, d)}, got {tuple(v_shape)}")
+        _dense("v_pages", v_pages, _BF16, None, pool)
     rot = 0
     if inv_freq is not None:
-        _dense("inv_freq", inv_freq, _F64, ndim=1)
+        _dense("inv_freq", inv_freq, _F64, 1)
         rot = 2 * inv_freq.shape[0]
         if rot_offset < 0 or rot_offset + rot > d:
             raise ValueError(f"rope: entries [{rot_offset}, {rot_offset + rot}) of rows of {d}")
     if positions is not None:
-        _dense("positions", positions, _I32, shape=(T,))
+        _dense("positions", positions, _I32, None, (T,))
     if out is not None:
         if q is None:
             raise ValueError("out without q")
-        _rows("out", out, 3)
-        if out.shape != q.shape:
-            raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
-        if out is not q:
-            _no_overlap("out", out, q)
-        _writable("out", out)
-    with _Launch(stream, ("k", k), ("q", q), ("v", v), ("k_pages", k_pages), ("v_pages", v_pages),
-                 ("page_table", page_table), ("cu_seqlens", cu_seqlens), ("seq_lens", seq_lens),
-                 ("inv_freq", inv_freq), ("positions", positions), ("out", out)) as handle:
+        _output("out", out, q, q_shape)
+    handle, context = _on(stream, "k q v k_pages v_pages page_table cu_seqlens seq_lens inv_freq positions out", k, q, v,
+                          k_pages, v_pages, page_table, cu_seqlens, seq_lens, inv_freq, positions, out)
+    with context:
         o = out
-        if q is not None and o is None:
-            o = torch.empty(q.shape, dtype=_BF16, device=q.device)
-        st = capi.ss_rope_append_paged(
-            q, o, k, v, T, B, q.shape[1] if q is not None else 0, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot,
-            k_pages, v_pages, page_table, k_pages.shape[0], max_pages, positions,
-            q.stride()[:2] if q is not None else None, o.stride()[:2] if o is not None else None,
-            k.stride()[:2], v.stride()[:2] if v is not None else None, rot_offset, interleaved, attn_factor,
-            handle)
+        if q is not None:
+            if o is None:
+                o = torch.empty(q_shape, dtype=_BF16, device=q.device)
+            os_ = o.stride()
+        st = capi.ss_rope_append_paged(q, o, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot, k_pages,
+                                       v_pages, page_table, pool[0], max_pages, positions, qs[:2], os_[:2], ks[:2],
+                                       vs[:2], rot_offset, interleaved, attn_factor, handle)
     _check(st, "ss_rope_append_paged")
     return o
 
@@ -282,33 +272,34 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
     (capi.ss_attn_chunk_paged_units entries) receives the skipped tiles per
     unit, ``skip_mask`` / ``vote_margin`` [units][max_pages] the debug outputs.
     Returns o [T,Hq,d]; rows behind the last sequence are left as they were."""
-    _rows("q", q, 3)
-    T, Hq, d = q.shape
-    if Hq > 1 and q.stride(1) != d:
+    shape, qs = _rows("q", q, 3)
+    T, Hq, d = shape
+    if Hq > 1 and qs[1] != d:
         raise ValueError("q: the heads of a token must be contiguous")
-    B, max_pages = _batch(T, page_table, cu_seqlens, seq_lens)
-    _dense("k_pages", k_pages, _BF16, ndim=4)
-    num_pages, Hkv, page, dk = k_pages.shape
+    B, max_pages = _batch(page_table, cu_seqlens, seq_lens)
+    _dense("k_pages", k_pages, _BF16, 4)
+    pool = k_pages.shape
+    num_pages, Hkv, page, dk = pool
     if page != 128 or dk != d:
-        raise ValueError(f"k_pages: expected [num_pages, Hkv, 128, {d}], got {tuple(k_pages.shape)}")
-    _dense("v_pages", v_pages, _BF16, shape=k_pages.shape)
-    units = None
-    for name, t, dtype in (("counts", counts, _I32), ("skip_mask", skip_mask, torch.uint8),
-                           ("vote_margin", vote_margin, torch.float32)):
-        if t is not None:
-            _dense(name, t, torch.uint32 if name == "counts" and t.dtype == torch.uint32 else dtype)
-            units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits) if units is None else units
-            need = units * (1 if name == "counts" else max_pages)
-            if t.numel() < need:
-                raise ValueError(f"{name}: needs at least {need} elements, has {t.numel()}")
+        raise ValueError(f"k_pages: expected [num_pages, Hkv, 128, {d}], got {tuple(pool)}")
+    _dense("v_pages", v_pages, _BF16, None, pool)
+    if counts is not None or skip_mask is not None or vote_margin is not None:
+        units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits)
+        for name, t, dtype, need in (("counts", counts, _I32, units), ("skip_mask", skip_mask, torch.uint8, units * max_pages),
+                                     ("vote_margin", vote_margin, torch.float32, units * max_pages)):
+            if t is not None:
+                _dense(name, t, torch.uint32 if dtype is _I32 and t.dtype is torch.uint32 else dtype)
+                if t.numel() < need:
+                    raise ValueError(f"{name}: needs at least {need} elements, has {t.numel()}")
     if out is not None:
-        _dense("out", out, _BF16, shape=q.shape)
+        _dense("out", out, _BF16, None, shape)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
-    with _Launch(stream, ("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                 ("cu_seqlens", cu_seqlens), ("seq_lens", seq_lens), ("out", out), ("counts", counts),
-                 ("workspace", workspace), ("skip_mask", skip_mask), ("vote_margin", vote_margin)) as handle:
-        o = out if out is not None else torch.empty(q.shape, dtype=_BF16, device=q.device)
+    handle, context = _on(stream, "q k_pages v_pages page_table cu_seqlens seq_lens out counts workspace skip_mask vote_margin",
+                          q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, out, counts, workspace, skip_mask,
+                          vote_margin)
+    with context:
+        o = out if out is not None else torch.empty(shape, dtype=_BF16, device=q.device)
         nbytes = 0
         if workspace is not None:
             nbytes = workspace.numel() * workspace.element_size()
@@ -316,50 +307,50 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
             workspace, nbytes = chunk_paged_workspace(T, Hq, d, num_kv_splits, q.device)
         st = capi.ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,
                                       num_pages, max_pages, d, scale, causal, lambda_a, num_kv_splits, counts,
-                                      workspace, nbytes, q.stride(0) if T > 1 else 0, skip_mask, vote_margin,
-                                      handle)
+                                      workspace, nbytes, qs[0] if T > 1 else 0, skip_mask, vote_margin, handle)
     _check(st, "ss_attn_chunk_paged")
     return o
 
 
 def _state(page_refs, page_table, seq_lens):
-    _dense("page_refs", page_refs, _I32, ndim=1)
-    _dense("page_table", page_table, _I32, ndim=2)
-    _dense("seq_lens", seq_lens, _I32, shape=page_table.shape[:1])
-    return page_refs.shape[0], page_table.shape[0], page_table.shape[1]
+    _dense("page_refs", page_refs, _I32, 1)
+    _dense("page_table", page_table, _I32, 2)
+    rows, max_pages = page_table.shape
+    _dense("seq_lens", seq_lens, _I32, None, (rows,))
+    return page_refs.shape[0], rows, max_pages
 
 
 def _pools(pools, num_pages):
     """Bytes of a page, the same in every pool [num_pages, ...]."""
-    page_bytes = None
+    whole = None
     for i, t in enumerate(pools):
-        if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.dim() < 2:
+        if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.ndim < 2:
             raise ValueError(f"pools[{i}]: expected a contiguous tensor [num_pages, ...]")
-        n = t.element_size() * t[0].numel() if t.shape[0] else 0
-        if t.shape[0] != num_pages or (page_bytes is not None and n != page_bytes):
-            raise ValueError(f"pools[{i}]: expected {num_pages} pages of {page_bytes or n} bytes")
-        page_bytes = n
-    return page_bytes if page_bytes is not None else 16
+        n = t.nbytes
+        if t.shape[0] != num_pages or (n != whole and whole is not None):
+            raise ValueError(f"pools[{i}]: expected {num_pages} pages of {(whole or n) // max(1, num_pages)} bytes")
+        whole = n
+    return 16 if whole is None else whole // max(1, num_pages)
 
 
 def _list(name, t, n=None):
-    _dense(name, t, _I32, ndim=1)
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name}: expected {n} entries, got {t.shape[0]}")
-    return t.shape[0]
+    _dense(name, t, _I32, 1)
+    size = t.shape[0]
+    if n is not None and size != n:
+        raise ValueError(f"{name}: expected {n} entries, got {size}")
+    return size
 
 
 def _page_scratch(num_pages, num_rows, n, workspace, result, device):
-    if workspace is None:
-        nbytes = capi.ss_pages_workspace_size(num_pages, num_rows, n)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
+    """(workspace, its bytes, result), made where they are not given."""
+    if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace: must be contiguous")
         nbytes = workspace.numel() * workspace.element_size()
-    if result is None:
-        result = torch.empty(1, dtype=_I32, device=device)
-    return workspace, nbytes, result
+        return workspace, nbytes, torch.empty(1, dtype=_I32, device=device) if result is None else result
+    nbytes = capi.ss_pages_workspace_size(num_pages, num_rows, n)
+    return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes,
+            torch.empty(1, dtype=_I32, device=device) if result is None else result)
 
 
 def pages_reserve(page_refs, page_table, seq_lens, add, *, rows=None, result=None, workspace=None, stream=None):
@@ -377,8 +368,9 @@ def pages_reserve(page_refs, page_table, seq_lens, add, *, rows=None, result=Non
         raise ValueError(f"add: {n} entries for {num_rows} rows")
     if result is not None:
         _dense("result", result, _I32, shape=(1,))
-    with _Launch(stream, ("page_refs", page_refs), ("page_table", page_table), ("seq_lens", seq_lens),
-                 ("add", add), ("rows", rows), ("result", result), ("workspace", workspace)) as handle:
+    handle, context = _on(stream, "page_refs page_table seq_lens add rows result workspace", page_refs, page_table, seq_lens,
+                          add, rows, result, workspace)
+    with context:
         ws, nbytes, result = _page_scratch(num_pages, num_rows, n, workspace, result, page_refs.device)
         st = capi.ss_pages_reserve(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, add, n,
                                    result, ws, nbytes, handle)
@@ -390,8 +382,8 @@ def pages_free(page_refs, page_table, seq_lens, rows, *, stream=None):
     """The sequences of the listed rows (int32 [n]) end; their pages lose a holder."""
     num_pages, num_rows, max_pages = _state(page_refs, page_table, seq_lens)
     n = _list("rows", rows)
-    with _Launch(stream, ("page_refs", page_refs), ("page_table", page_table), ("seq_lens", seq_lens),
-                 ("rows", rows)) as handle:
+    handle, context = _on(stream, "page_refs page_table seq_lens rows", page_refs, page_table, seq_lens, rows)
+    with context:
         st = capi.ss_pages_free(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, n, handle)
     _check(st, "ss_pages_free")
 
@@ -409,9 +401,9 @@ def pages_fork(pools, page_refs, page_table, seq_lens, src_rows, dst_rows, *, re
     _list("dst_rows", dst_rows, n)
     if result is not None:
         _dense("result", result, _I32, shape=(1,))
-    with _Launch(stream, ("page_refs", page_refs), ("page_table", page_table), ("seq_lens", seq_lens),
-                 ("src_rows", src_rows), ("dst_rows", dst_rows), ("result", result), ("workspace", workspace),
-                 *(("pools", t) for t in pools)) as handle:
+    handle, context = _on(stream, "page_refs page_table seq_lens src_rows dst_rows result workspace" + " pool" * len(pools),
+                          page_refs, page_table, seq_lens, src_rows, dst_rows, result, workspace, *pools)
+    with context:
         ws, nbytes, result = _page_scratch(num_pages, num_rows, n, workspace, result, page_refs.device)
         st = capi.ss_pages_fork(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
                                 src_rows, dst_rows, n, result, ws, nbytes, handle)
@@ -431,8 +423,8 @@ def pages_copy(pools, src, dst, *, result=None, workspace=None, stream=None):
     _list("dst", dst, n)
     if result is not None:
         _dense("result", result, _I32, shape=(1,))
-    with _Launch(stream, ("src", src), ("dst", dst), ("result", result), ("workspace", workspace),
-                 *(("pools", t) for t in pools)) as handle:
+    handle, context = _on(stream, "src dst result workspace" + " pool" * len(pools), src, dst, result, workspace, *pools)
+    with context:
         ws, nbytes, result = _page_scratch(num_pages, 0, n, workspace, result, src.device)
         st = capi.ss_pages_copy(pools, page_bytes, num_pages, src, dst, n, result, ws, nbytes, handle)
     _check(st, "ss_pages_copy")
@@ -454,9 +446,9 @@ def pages_compact(pools, page_refs, page_table, seq_lens, *, out_refs=None, out_
         _dense("out_table", out_table, _I32, shape=page_table.shape)
     if live is not None:
         _dense("live", live, _I32, shape=(1,))
-    with _Launch(stream, ("page_refs", page_refs), ("page_table", page_table), ("seq_lens", seq_lens),
-                 ("out_refs", out_refs), ("out_table", out_table), ("live", live), ("workspace", workspace),
-                 *(("pools", t) for t in pools)) as handle:
+    handle, context = _on(stream, "page_refs page_table seq_lens out_refs out_table live workspace" + " pool" * len(pools),
+                          page_refs, page_table, seq_lens, out_refs, out_table, live, workspace, *pools)
+    with context:
         ws, nbytes, live = _page_scratch(num_pages, num_rows, 0, workspace, live, page_refs.device)
         st = capi.ss_pages_compact(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages,
                                    seq_lens, out_refs, out_table, live, ws, nbytes, handle)

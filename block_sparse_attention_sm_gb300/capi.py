@@ -99,9 +99,8 @@ def load() -> ctypes.CDLL:
     lib.ss_status_string.restype = ctypes.c_char_p
     lib.ss_stream_status.argtypes = [P]
     I64, D = ctypes.c_int64, ctypes.c_double
-    lib.ss_rope.argtypes = [P, P, I, I, I, I, P, P, P, I64, P, I, I, I, I, F, P]
-    lib.ss_rope_append_paged.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, I, I, I, F,
-                                         P, P, P, I, I, P]
+    lib.ss_rope.argtypes = [P, P, I, I, I, I] + [I64] * 6 + [P, I64, P, I, I, I, I, F, P]
+    lib.ss_rope_append_paged.argtypes = [P] * 4 + [I64] * 8 + [I] * 5 + [P] * 4 + [I, I, I, F, P, P, P, I, I, P]
     lib.ss_rope_frequencies.argtypes = [P, I, D, I, D, I, D, D, ctypes.POINTER(F)]
     lib.ss_attn_chunk_paged.argtypes = [P, I64, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, F, I, P, P,
                                         U, ctypes.POINTER(ss_debug_opts), P]
@@ -307,11 +306,6 @@ def ss_attn_mla_decode_paged(q, kv_pages, page_table, seq_lens, o, B, Hq, num_pa
                                            _stream(stream))
 
 
-def _strides(s):
-    """Host int64 array of strides in elements (None: contiguous)."""
-    return None if s is None else (ctypes.c_int64 * len(s))(*[int(x) for x in s])
-
-
 def _addresses(pools):
     """Host array of the pools' device addresses."""
     return (ctypes.c_void_p * max(1, len(pools)))(*[_ptr(p) for p in pools])
@@ -320,24 +314,26 @@ def _addresses(pools):
 def ss_rope(x, out, B, H, L, d, positions, inv_freq, rot_dim, x_strides=None, out_strides=None,
             position_stride=0, rot_offset=0, interleaved=False, inverse=False, attn_factor=1.0,
             stream=None) -> int:
-    """Rotary positions of x [B,H,L,d] (strided rows) into out."""
-    return load().ss_rope(_ptr(x), _ptr(out), B, H, L, d, _strides(x_strides), _strides(out_strides),
-                          _ptr(positions), int(position_stride), _ptr(inv_freq), int(rot_dim),
-                          int(rot_offset), int(bool(interleaved)), int(bool(inverse)),
-                          float(attn_factor), _stream(stream))
+    """Rotary positions of x [B,H,L,d] into out; strides (batch, head, token), None: contiguous."""
+    dense = (H * L * d, L * d, d)
+    return (_lib or load()).ss_rope(
+        _ptr(x), _ptr(out), B, H, L, d, *(x_strides or dense), *(out_strides or dense), _ptr(positions),
+        position_stride, _ptr(inv_freq), rot_dim, rot_offset, bool(interleaved), bool(inverse), attn_factor,
+        _stream(stream))
 
 
 def ss_rope_append_paged(q, q_out, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot_dim,
                          k_pages, v_pages, page_table, num_pages, max_pages, positions=None,
                          q_strides=None, q_out_strides=None, k_strides=None, v_strides=None,
                          rot_offset=0, interleaved=False, attn_factor=1.0, stream=None) -> int:
-    """Rotary positions of a step's new tokens and the write of their keys and values into pages."""
-    return load().ss_rope_append_paged(
-        _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _strides(q_strides), _strides(q_out_strides),
-        _strides(k_strides), _strides(v_strides), T, B, Hq, Hkv, d, _ptr(cu_seqlens), _ptr(seq_lens),
-        _ptr(positions), _ptr(inv_freq), int(rot_dim), int(rot_offset), int(bool(interleaved)),
-        float(attn_factor), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), num_pages, max_pages,
-        _stream(stream))
+    """Rotary positions of a step's new tokens and the write of their keys and values into pages;
+    strides (token, head), None: contiguous."""
+    q_dense, k_dense = (Hq * d, d), (Hkv * d, d)
+    return (_lib or load()).ss_rope_append_paged(
+        _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), *(q_strides or q_dense), *(q_out_strides or q_dense),
+        *(k_strides or k_dense), *(v_strides or k_dense), T, B, Hq, Hkv, d, _ptr(cu_seqlens), _ptr(seq_lens),
+        _ptr(positions), _ptr(inv_freq), rot_dim, rot_offset, bool(interleaved), attn_factor, _ptr(k_pages),
+        _ptr(v_pages), _ptr(page_table), num_pages, max_pages, _stream(stream))
 
 
 def ss_rope_frequencies(rot_dim, base=10000.0, scaling=SS_ROPE_PLAIN, factor=1.0, original_length=0,
@@ -352,11 +348,11 @@ def ss_rope_frequencies(rot_dim, base=10000.0, scaling=SS_ROPE_PLAIN, factor=1.0
 
 
 def ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits) -> int:
-    return int(load().ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits))
+    return int((_lib or load()).ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits))
 
 
 def ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits) -> int:
-    return int(load().ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits))
+    return int((_lib or load()).ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits))
 
 
 def ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,
@@ -364,51 +360,52 @@ def ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o
                         skip_counts=None, workspace=None, workspace_bytes=0, q_token_stride=0,
                         skip_mask=None, vote_margin=None, stream=None) -> int:
     """Attention of a step's packed new tokens over the paged cache."""
-    dbg = _dbg(skip_mask, vote_margin)
-    return load().ss_attn_chunk_paged(
-        _ptr(q), int(q_token_stride), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cu_seqlens),
-        _ptr(seq_lens), _ptr(o), T, B, Hq, Hkv, num_pages, max_pages, d, float(scale),
-        int(bool(causal)), float(lambda_a), int(num_kv_splits), _ptr(skip_counts), _ptr(workspace),
-        int(workspace_bytes), ctypes.byref(dbg), _stream(stream))
+    dbg = None
+    if skip_mask is not None or vote_margin is not None:
+        dbg = ctypes.byref(_dbg(skip_mask, vote_margin))
+    return (_lib or load()).ss_attn_chunk_paged(
+        _ptr(q), q_token_stride, _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cu_seqlens),
+        _ptr(seq_lens), _ptr(o), T, B, Hq, Hkv, num_pages, max_pages, d, scale, bool(causal), lambda_a,
+        num_kv_splits, _ptr(skip_counts), _ptr(workspace), workspace_bytes, dbg, _stream(stream))
 
 
 def ss_pages_workspace_size(num_pages, num_rows, n) -> int:
-    return int(load().ss_pages_workspace_size(num_pages, num_rows, n))
+    return int((_lib or load()).ss_pages_workspace_size(num_pages, num_rows, n))
 
 
 def ss_pages_reserve(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, add, n,
                      result=None, workspace=None, workspace_bytes=0, stream=None) -> int:
-    return load().ss_pages_reserve(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
+    return (_lib or load()).ss_pages_reserve(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
                                    _ptr(seq_lens), _ptr(rows), _ptr(add), n, _ptr(result),
-                                   _ptr(workspace), int(workspace_bytes), _stream(stream))
+                                   _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def ss_pages_free(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens, rows, n,
                   stream=None) -> int:
-    return load().ss_pages_free(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
+    return (_lib or load()).ss_pages_free(_ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages,
                                 _ptr(seq_lens), _ptr(rows), n, _stream(stream))
 
 
 def ss_pages_fork(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
                   src_rows, dst_rows, n, result=None, workspace=None, workspace_bytes=0,
                   stream=None) -> int:
-    return load().ss_pages_fork(_addresses(pools), len(pools), int(page_bytes), _ptr(page_refs),
+    return (_lib or load()).ss_pages_fork(_addresses(pools), len(pools), page_bytes, _ptr(page_refs),
                                 num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
                                 _ptr(src_rows), _ptr(dst_rows), n, _ptr(result), _ptr(workspace),
-                                int(workspace_bytes), _stream(stream))
+                                workspace_bytes, _stream(stream))
 
 
 def ss_pages_copy(pools, page_bytes, num_pages, src, dst, n, result=None, workspace=None,
                   workspace_bytes=0, stream=None) -> int:
-    return load().ss_pages_copy(_addresses(pools), len(pools), int(page_bytes), num_pages, _ptr(src),
-                                _ptr(dst), n, _ptr(result), _ptr(workspace), int(workspace_bytes),
+    return (_lib or load()).ss_pages_copy(_addresses(pools), len(pools), page_bytes, num_pages, _ptr(src),
+                                _ptr(dst), n, _ptr(result), _ptr(workspace), workspace_bytes,
                                 _stream(stream))
 
 
 def ss_pages_compact(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
                      out_refs=None, out_table=None, live=None, workspace=None, workspace_bytes=0,
                      stream=None) -> int:
-    return load().ss_pages_compact(_addresses(pools), len(pools), int(page_bytes), _ptr(page_refs),
+    return (_lib or load()).ss_pages_compact(_addresses(pools), len(pools), page_bytes, _ptr(page_refs),
                                    num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
                                    _ptr(out_refs), _ptr(out_table), _ptr(live), _ptr(workspace),
-                                   int(workspace_bytes), _stream(stream))
+                                   workspace_bytes, _stream(stream))

@@ -43,10 +43,11 @@ using namespace ssattn;
 
 extern "C" {
 
-ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const int64_t* x_strides,
-                  const int64_t* out_strides, const int32_t* positions, int64_t position_stride,
-                  const double* inv_freq, int rot_dim, int rot_offset, int interleaved, int inverse,
-                  float attn_factor, void* stream) {
+ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t x_batch_stride,
+                  int64_t x_head_stride, int64_t x_token_stride, int64_t out_batch_stride,
+                  int64_t out_head_stride, int64_t out_token_stride, const int32_t* positions,
+                  int64_t position_stride, const double* inv_freq, int rot_dim, int rot_offset,
+                  int interleaved, int inverse, float attn_factor, void* stream) {
   if (B < 0 || H < 0 || L < 0 || d < 1 || rot_dim < 2 || position_stride < 0) return SS_ERR_INVALID_ARG;
   if (d > kMaxRopeWidth) return SS_ERR_UNSUPPORTED;
   RopeParams p{};
@@ -54,9 +55,8 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const in
   ss_status st = turn_of(&p.turn, inv_freq, rot_dim, rot_offset, interleaved, attn_factor, inverse, d, &vec);
   if (st != SS_OK) return st;
   if (B == 0 || H == 0 || L == 0) return SS_OK;
-  const int64_t dense[3] = {static_cast<int64_t>(H) * L * d, static_cast<int64_t>(L) * d, d};
-  const int64_t *xs = x_strides != nullptr ? x_strides : dense,
-                *os = out_strides != nullptr ? out_strides : dense;
+  const int64_t xs[3] = {x_batch_stride, x_head_stride, x_token_stride},
+                os[3] = {out_batch_stride, out_head_stride, out_token_stride};
   const int size[3] = {B, H, L};
   for (int i = 0; i < 3; ++i) {
     p.xs[i] = xs[i];
@@ -82,8 +82,9 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const in
 }
 
 ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
-                               const int64_t* q_strides, const int64_t* q_out_strides,
-                               const int64_t* k_strides, const int64_t* v_strides, int T, int B, int Hq,
+                               int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
+                               int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                               int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
                                int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
                                const int32_t* positions, const double* inv_freq, int rot_dim,
                                int rot_offset, int interleaved, float attn_factor, void* k_pages,
@@ -104,12 +105,15 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
       !aligned4(page_table))
     return SS_ERR_INVALID_ARG;
   if (static_cast<long>(max_pages) * kTile > 0x7fffffffL) return SS_ERR_INVALID_ARG;
-  const int64_t dq[2] = {static_cast<int64_t>(Hq) * d, d}, dk[2] = {static_cast<int64_t>(Hkv) * d, d};
+  const int64_t strides[4][2] = {{q_token_stride, q_head_stride},
+                                 {q_out_token_stride, q_out_head_stride},
+                                 {k_token_stride, k_head_stride},
+                                 {v_token_stride, v_head_stride}};
   for (int i = 0; i < 2; ++i) {
-    p.qs[i] = q_strides != nullptr ? q_strides[i] : dq[i];
-    p.qos[i] = q_out_strides != nullptr ? q_out_strides[i] : dq[i];
-    p.ks[i] = k_strides != nullptr ? k_strides[i] : dk[i];
-    p.vs[i] = v_strides != nullptr ? v_strides[i] : dk[i];
+    p.qs[i] = q != nullptr ? strides[0][i] : 0;
+    p.qos[i] = q != nullptr ? strides[1][i] : 0;
+    p.ks[i] = strides[2][i];
+    p.vs[i] = v != nullptr ? strides[3][i] : 0;
     if (p.qs[i] < 0 || p.ks[i] < 0 || p.vs[i] < 0) return SS_ERR_INVALID_ARG;
     if (q != nullptr && ((i == 0 ? T : Hq) > 1)) {
       if (p.qos[i] < d || (q == q_out && p.qs[i] != p.qos[i])) return SS_ERR_INVALID_ARG;

@@ -362,12 +362,11 @@ ss_status ss_attn_mla_decode_paged(const void* q, const void* kv_pages, const in
  * by -t (same f): the gradient with respect to x is this call on the gradient
  * with respect to out.  Angles are exact for any int32 position (no loss at
  * far positions); products are fp32, rounded once to bf16.
- *   x, out: bf16 [B][H][L][d], 2-byte aligned; x_strides, out_strides: host
- *     arrays of 3 strides in elements (batch, head, token), nullable:
- *     contiguous; the innermost axis is contiguous.  x may have stride 0
- *     axes.  out == x (same strides) rotates in place; otherwise x and out
- *     must not overlap.  [T][H][d] rows are B = 1, L = T with strides
- *     (0, d, H * d).
+ *   x, out: bf16 [B][H][L][d], 2-byte aligned, strides in elements (batch,
+ *     head, token; [B][H][L][d] itself: H * L * d, L * d, d); the innermost
+ *     axis is contiguous.  x may have stride 0 axes.  out == x (same strides)
+ *     rotates in place; otherwise x and out must not overlap.  [T][H][d] rows
+ *     are B = 1, L = T with strides (0, d, H * d).
  *   positions: device int32, position of (b, l) at [b * position_stride + l]
  *     (position_stride 0: the same row of positions for every b).
  *   inv_freq: device double [rot_dim / 2], radians per position (8-byte
@@ -380,10 +379,11 @@ ss_status ss_attn_mla_decode_paged(const void* q, const void* kv_pages, const in
  * output rows, attn_factor not finite), SS_ERR_UNSUPPORTED (d > 65536, or the
  * device) or SS_ERR_CUDA.
  */
-ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const int64_t* x_strides,
-                  const int64_t* out_strides, const int32_t* positions, int64_t position_stride,
-                  const double* inv_freq, int rot_dim, int rot_offset, int interleaved, int inverse,
-                  float attn_factor, void* stream);
+ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t x_batch_stride,
+                  int64_t x_head_stride, int64_t x_token_stride, int64_t out_batch_stride,
+                  int64_t out_head_stride, int64_t out_token_stride, const int32_t* positions,
+                  int64_t position_stride, const double* inv_freq, int rot_dim, int rot_offset,
+                  int interleaved, int inverse, float attn_factor, void* stream);
 
 /*
  * Rotary positions of a step's packed new tokens, fused with the write of
@@ -392,8 +392,8 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const in
  *   q, q_out: bf16 [T][Hq][d] (q nullable: keys and values only; q_out may be
  *     q).  k, v: bf16 [T][Hkv][d] (v nullable: a cache of one row per token,
  *     as the latent one with Hkv = 1, d = 576, rot_offset = 512, rot_dim =
- *     64).  *_strides: host arrays of 2 strides in elements (token, head),
- *     nullable: contiguous; so q, k and v may be parts of one projection.
+ *     64).  Strides in elements between tokens and heads: q, k and v may be
+ *     parts of one projection.
  *   positions: device int32 [T], nullable: the key's place L_b - n_b + i.
  *   rot_dim = 0: no rotation (inv_freq may be NULL).
  *   k_pages, v_pages: as in ss_attn_decode_paged ([num_pages][Hkv][128][d]).
@@ -403,8 +403,9 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, const in
  * once.  Returns as ss_rope.
  */
 ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
-                               const int64_t* q_strides, const int64_t* q_out_strides,
-                               const int64_t* k_strides, const int64_t* v_strides, int T, int B, int Hq,
+                               int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
+                               int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                               int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
                                int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
                                const int32_t* positions, const double* inv_freq, int rot_dim,
                                int rot_offset, int interleaved, float attn_factor, void* k_pages,
