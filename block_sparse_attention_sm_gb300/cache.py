@@ -284,7 +284,7 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
         raise ValueError(f"k_pages: expected [num_pages, Hkv, 128, {d}], got {tuple(pool)}")
     _dense("v_pages", v_pages, _BF16, None, pool)
     if counts is not None or skip_mask is not None or vote_margin is not None:
-        units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits)
+        units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv)
         for name, t, dtype, need in (("counts", counts, _I32, units), ("skip_mask", skip_mask, torch.uint8, units * max_pages),
                                      ("vote_margin", vote_margin, torch.float32, units * max_pages)):
             if t is not None:

@@ -104,7 +104,7 @@ def load() -> ctypes.CDLL:
     lib.ss_rope_frequencies.argtypes = [P, I, D, I, D, I, D, D, ctypes.POINTER(F)]
     lib.ss_attn_chunk_paged.argtypes = [P, I64, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, F, I, P, P,
                                         U, ctypes.POINTER(ss_debug_opts), P]
-    lib.ss_attn_chunk_paged_units.argtypes = [I, I, I, I, I]
+    lib.ss_attn_chunk_paged_units.argtypes = [I, I, I, I]
     lib.ss_attn_chunk_paged_workspace_size.argtypes = [I, I, I, I]
     lib.ss_pages_workspace_size.argtypes = [I, I, I]
     for name in ("ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
@@ -347,8 +347,8 @@ def ss_rope_frequencies(rot_dim, base=10000.0, scaling=SS_ROPE_PLAIN, factor=1.0
     return st, list(out), f.value
 
 
-def ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits) -> int:
-    return int((_lib or load()).ss_attn_chunk_paged_units(T, B, Hq, Hkv, num_kv_splits))
+def ss_attn_chunk_paged_units(T, B, Hq, Hkv) -> int:
+    return int((_lib or load()).ss_attn_chunk_paged_units(T, B, Hq, Hkv))
 
 
 def ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits) -> int:

@@ -187,11 +187,11 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
   return SS_OK;
 }
 
-size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv, int num_kv_splits) {
-  if (T < 0 || B < 1 || Hkv < 1 || Hq < Hkv || num_kv_splits < 1) return 0;
+size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv) {
+  if (T < 0 || B < 1 || Hkv < 1 || Hq < Hkv) return 0;
   const int G = Hq / Hkv;
   if (G > kTile) return 0;
-  return 2 * static_cast<size_t>(chunk_slots(T, B, kTile / G)) * Hkv * num_kv_splits;
+  return 2 * static_cast<size_t>(chunk_slots(T, B, kTile / G)) * Hkv;
 }
 
 size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits) {
@@ -261,6 +261,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   p.tpb = static_cast<int>(tpb);
   p.slots = static_cast<int>(slots);
   p.S = num_kv_splits;
+  p.parts = chunk_parts(slots * Hkv, num_kv_splits);
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.causal = causal ? 1 : 0;
@@ -271,8 +272,8 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   p.seq_lens = seq_lens;
   p.page_table = page_table;
   p.o = static_cast<__nv_bfloat16*>(o);
-  if (num_kv_splits > 1) {
-    const size_t rows = static_cast<size_t>(num_kv_splits) * T * Hq;
+  if (p.parts > 1) {
+    const size_t rows = static_cast<size_t>(p.parts) * T * Hq;
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * d);
   }

@@ -13,7 +13,8 @@ struct ChunkParams {
   int T, B, Hq, Hkv, G;    // packed new tokens, sequences, heads, Hq / Hkv
   int tpb;                 // tokens of a row block: 128 / G
   int slots;               // places for pairs of row blocks (see chunk_slots)
-  int S;                   // ranges that a sequence's tiles are cut into
+  int S;                   // ranges of the vote that a sequence's tiles are cut into
+  int parts;               // parts that the tiles are dealt to (<= S)
   int num_pages, max_pages;
   int causal;
   float scale, scale_log2, lambda_a;
@@ -21,8 +22,8 @@ struct ChunkParams {
   const int32_t* seq_lens;
   const int32_t* page_table;
   __nv_bfloat16* o;        // [T][Hq][d]
-  float* part_o;           // S > 1: [S][T * Hq][d] unnormalised outputs
-  float2* part_ml;         // S > 1: [S][T * Hq] (reference maximum in exp2 units, sum)
+  float* part_o;           // parts > 1: [parts][T * Hq][d] unnormalised outputs
+  float2* part_ml;         // parts > 1: [parts][T * Hq] (reference maximum in exp2 units, sum)
   uint32_t* counts;
   uint8_t* mask;
   float* margin;
@@ -36,6 +37,9 @@ struct ChunkParams {
 __host__ __device__ constexpr long chunk_slots(long T, long B, long tpb) {
   return T / (2 * tpb) + B;
 }
+
+// How many parts to deal the tiles of `pairs` pairs of row blocks (over all KV heads) to.
+int chunk_parts(long pairs, int S);
 
 cudaError_t launch_chunk_paged(int d, bool vote, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const ChunkParams& p, cudaStream_t st);

@@ -31,9 +31,25 @@
 // P.V accumulates in fp32.  One thread issues score MMAs, another P.V MMAs.
 // Every wait is bounded.
 //
-// Few rows and a long cache: the sequence's tiles are cut into S ranges, each
-// its own pass (its first tile is kept), and a second kernel merges the
-// partial (m, l, O) in fp32.
+// Units and clusters: a unit is (pair of row blocks, KV head, part of the
+// tiles).  Serving batches have many short units (a decoded token over a few
+// pages next to pieces of prompts), so a cluster stays resident and takes unit
+// after unit: it cancels a cluster of the grid that has not been launched yet
+// and does that one's unit (cluster launch control: the hardware hands them
+// out as clusters become free, in no memory of ours).  Barriers, TMEM and the
+// K / V rings live on: the producers load the next unit's first tiles, and the
+// score issuer starts on them, while the softmax of the last unit's tail and
+// its epilogue run.
+//   Producer warp 8 of CTA 0 asks for the next unit one unit ahead and passes
+//   its number to CTA 1; warp 8 of each CTA works out the unit's geometry
+//   (sequence, lengths, tiles) and publishes it to the CTA's other warps.
+//
+// Few rows and a long cache: the tiles are dealt to S parts whose states (m,
+// l, O) a second kernel merges in fp32.  The ranges of the vote (num_kv_splits:
+// each starts without a running maximum, so its first tile is kept) are a
+// matter of the definition, not of the launch: one unit passes through several
+// ranges in turn, restarting the vote's maximum, and only as many parts are
+// made as fill the GPU (parts_of).
 //
 // d = 64 runs with value tiles padded to 128 columns (the second SM's half of
 // a value tile is an out-of-range box): the softmax bounds that width anyway.
@@ -85,16 +101,30 @@ struct PairCfg {
   static constexpr int kKOff = kQOff + kQBytes;
   static constexpr int kVOff = kKOff + kNK * kKHalfBytes;
   static constexpr int kCtlOff = kVOff + kNV * kVHalfBytes;
-  static constexpr int kCtlBytes = 5120;
+  static constexpr int kCtlBytes = 8192;
   static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 384;
   static constexpr uint32_t kTmemCols = 512;
 };
 
+// A unit as the warps of one CTA need it.
+struct Unit {
+  int b, kvh, part;           // sequence, KV head, part of the tiles
+  int j0, j1;                 // tiles of the part, of all the sequence's
+  int n_pair, n_mine;         // of them, seen by either block / by this CTA's block
+  int tok, toks;              // this block's first new token (of the batch), its tokens
+  int lim0;                   // last key that the first of them sees (causal), or any
+  int last, last_shift;       // the sequence's last tile; zero rows in front of its keys
+  int range;                  // tiles of a range of the vote
+  float thr_raw;              // skip iff tile_max - m < thr_raw
+  int id;                     // place * 2 + CTA rank, with the KV head; -1: no more units
+};
+
 template <int NK, int NV>
 struct PairCtl {
   uint64_t q_full;             // leader: both Q blocks landed
+  uint64_t q_empty;            // each CTA: the unit's score MMAs are done, Q may be refilled
   uint64_t k_full[NK];         // leader: both K halves of a ring entry landed
   uint64_t v_full[NV];         // leader: both V halves landed
   uint64_t k_empty[NK];        // each CTA: its K slot may be refilled
@@ -105,13 +135,22 @@ struct PairCtl {
   uint64_t drain[kSoftWarps];  // each CTA, per softmax warp: the P.V MMAs issued so far are done
   uint64_t rescaled[2][kSoftWarps];  // leader: (CTA, warp) has rescaled its part of O
   uint64_t s_free[kNB];        // leader: the buffer's P.V is issued (or not needed)
-  uint64_t o_full;             // each CTA: the last P.V is done
+  uint64_t o_full;             // each CTA: the unit's last P.V is done
+  uint64_t o_free;             // leader: both CTAs' 8 warps have read the unit's O
   uint64_t mma_done[2];        // leader: teardown, per issuer
+  uint64_t unit_full[2];       // each CTA: a unit's geometry is published
+  uint64_t unit_empty[2];      // each CTA: the other 11 warps have read it
+  uint64_t next_full;          // leader: the answer to a request for a unit; CTA 1: its number
+  uint64_t next_empty;         // leader: CTA 1 has read the number
+  alignas(16) uint32_t answer[4];                     // leader: cluster launch control's
   alignas(16) uint32_t flags[kNB][kGroupWarps];       // leader: per buffer and warp of the
                                                       // tile's warpgroup, kFlagKept | kFlagRescale
   alignas(16) uint32_t peer_flags[kNB][kGroupWarps];  // leader: the same for CTA 1's warps
+  uint32_t o_note[kSoftWarps]; // leader: written by CTA 1's warps to complete bytes on o_free
+  uint32_t next_unit;          // CTA 1: the next unit's number + 1 (0: none)
   uint32_t tmem_base;
   int abort_flag;
+  Unit unit[2];
   uint32_t skipped[2];         // per warpgroup: tiles it skipped
   float red[2][kGroupWarps];   // per warpgroup and warp: largest vote statistic of a tile
   float2 hand[kTile];          // per row: (m, m_ref) after the last tile, passed between warpgroups
@@ -147,6 +186,32 @@ __device__ __forceinline__ int sequence_of_slot(const int32_t* cu, int B, int pa
   }
 }
 
+// Cluster launch control: ask the hardware for a cluster of this grid that has
+// not been launched.  The answer (16 bytes) lands in shared memory and
+// completes 16 bytes on `bar`.
+__device__ __forceinline__ void request_cluster(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// First block of the cluster that was handed over, or -1.
+__device__ __forceinline__ int requested_block(const void* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
 // DVO: the value (and output) width in memory.  DVO = 64 runs as DV = 128
 // with the second SM's half of every value tile a fully out-of-range TMA box
 // (read as zeros): O's columns 64.. stay zero and are not written.
@@ -178,60 +243,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // shared::cluster address of a barrier of the leader
   auto lead = [&](uint64_t* bar) { return map_shared(smem_u32(bar), 0u); };
 
-  // Work: two row blocks of one (sequence, KV head, range of tiles), the later
-  // (with a causal mask: the longer) pairs of a sequence first.
-  const int x = blockIdx.x >> 1;
-  const int sk = x / p.slots;  // split * Hkv + KV head
-  const int slot = p.slots - 1 - (x - sk * p.slots);
-  const int split = sk / p.Hkv, kvh = sk - split * p.Hkv;
-  const int b = sequence_of_slot(p.cu_seqlens, p.B, 2 * p.tpb, slot);
-  const int tok0 = max(0, min(p.cu_seqlens[b], p.T));  // the sequence's new tokens
-  const int n_new = max(0, min(p.cu_seqlens[b + 1], p.T) - tok0);
-  const int len = max(0, min(p.seq_lens[b], p.max_pages * kTile));
-  const int pr = slot - (tok0 / (2 * p.tpb) + b);
-  const int off = len - n_new;  // (causal) new token i sees keys up to off + i
-  const int nT_b = (len + kTile - 1) / kTile;
-  const int T_b = (nT_b + p.S - 1) / p.S;
-  const int j0 = split * T_b, j1 = min(nT_b, j0 + T_b);
-  const int last_shift = nT_b * kTile - len;  // zero rows in front of the last tile's keys
-  const float thr_raw =  // lambda_b = min(1, a / L_b)
-      (p.lambda_a > 0.f && len > 0)
-          ? logf(fminf(1.f, p.lambda_a / static_cast<float>(len))) / p.scale
-          : -INFINITY;
-  // tiles evaluated by either block of the pair (every CTA computes both)
-  int n_pair = 0, n_mine = 0, toks_mine = 0;
+  // The geometry of unit number x (a whole warp; every lane returns it).
+  // Later pairs of a sequence (with a causal mask: the longer) come first.
+  auto geometry = [&](int x) -> Unit {
+    Unit u;
+    const int sk = x / p.slots;  // part * Hkv + KV head
+    const int slot = p.slots - 1 - (x - sk * p.slots);
+    u.part = sk / p.Hkv;
+    u.kvh = sk - u.part * p.Hkv;
+    u.id = (u.kvh * p.slots + slot) * 2 + static_cast<int>(rank);
+    const int b = sequence_of_slot(p.cu_seqlens, p.B, 2 * p.tpb, slot);
+    u.b = b;
+    const int tok0 = max(0, min(__ldg(p.cu_seqlens + b), p.T));  // the sequence's new tokens
+    const int n_new = max(0, min(__ldg(p.cu_seqlens + b + 1), p.T) - tok0);
+    const int len = max(0, min(__ldg(p.seq_lens + b), p.max_pages * kTile));
+    const int pr = slot - (tok0 / (2 * p.tpb) + b);
+    const int off = len - n_new;  // (causal) new token i sees keys up to off + i
+    const int nT = (len + kTile - 1) / kTile;
+    u.last = nT - 1;
+    u.last_shift = nT * kTile - len;
+    u.range = max(1, (nT + p.S - 1) / p.S);
+    // a part: whole ranges where there is a vote, otherwise an even share
+    const int per = kVote ? (p.S + p.parts - 1) / p.parts * u.range : (nT + p.parts - 1) / p.parts;
+    u.j0 = min(nT, u.part * per);
+    u.j1 = min(nT, u.j0 + per);
+    u.thr_raw = (p.lambda_a > 0.f && len > 0)  // lambda_b = min(1, a / L_b)
+                    ? logf(fminf(1.f, p.lambda_a / static_cast<float>(len))) / p.scale
+                    : -INFINITY;
+    u.n_pair = u.n_mine = u.toks = 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int i0 = (2 * pr + t) * p.tpb;
-    const int toks = max(0, min(p.tpb, n_new - i0));
-    int n = (toks > 0) ? nT_b : 0;
-    if (p.causal && toks > 0) {
-      const int last = off + i0 + toks - 1;
-      n = last < 0 ? 0 : min(nT_b, last / kTile + 1);
-    }
-    n = max(0, min(n, j1) - j0);
-    n_pair = max(n_pair, n);
-    if (t == static_cast<int>(rank)) {
-      n_mine = n;
-      toks_mine = toks;
-    }
-  }
-  const int i0_mine = (2 * pr + static_cast<int>(rank)) * p.tpb;
-  const long unit = (static_cast<long>(sk) * p.slots + slot) * 2 + rank;
-  // Debug outputs of the tiles this unit does not evaluate.
-  if (p.mask != nullptr || p.margin != nullptr)
-    for (int j = tid; j < p.max_pages; j += kThreads)
-      if (j < j0 || j >= j0 + n_mine) {
-        if (p.mask != nullptr) p.mask[unit * p.max_pages + j] = 2;
-        if (p.margin != nullptr) p.margin[unit * p.max_pages + j] = NAN;
+    for (int t = 0; t < 2; ++t) {
+      const int i0 = (2 * pr + t) * p.tpb;
+      const int toks = (pr < 0) ? 0 : max(0, min(p.tpb, n_new - i0));
+      int n = (toks > 0) ? nT : 0;
+      if (p.causal && toks > 0) {
+        const int seen = off + i0 + toks - 1;
+        n = seen < 0 ? 0 : min(nT, seen / kTile + 1);
       }
-  if (pr < 0 || 2 * pr * p.tpb >= n_new) {  // a place that no pair took (both CTAs leave)
-    if (tid == 0 && p.counts != nullptr) p.counts[unit] = 0;
-    return;
-  }
+      n = max(0, min(n, u.j1) - u.j0);
+      u.n_pair = max(u.n_pair, n);
+      if (t == static_cast<int>(rank)) {
+        u.n_mine = n;
+        u.toks = toks;
+        u.tok = tok0 + i0;
+        u.lim0 = p.causal ? off + i0 : 0x3fffffff;
+      }
+    }
+    return u;
+  };
 
   if (tid == 0) {
     mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_empty, 1);
     for (int s = 0; s < NK; ++s) {
       mbar_init(&ctl->k_full[s], 1);
       mbar_init(&ctl->k_empty[s], 1);
@@ -245,17 +308,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // this CTA's 4 warps + the score issuer's arrival (which sets the 16
       // bytes that CTA 1's 4 warps complete)
       mbar_init(&ctl->dec[s], kGroupWarps + 1);
-
+      mbar_init(&ctl->s_free[s], 1);
     }
     for (int w = 0; w < kSoftWarps; ++w) {
       mbar_init(&ctl->drain[w], 1);
       mbar_init(&ctl->rescaled[0][w], 1);
       mbar_init(&ctl->rescaled[1][w], 1);
     }
-    for (int b = 0; b < kNB; ++b) mbar_init(&ctl->s_free[b], 1);
     mbar_init(&ctl->o_full, 1);
+    mbar_init(&ctl->o_free, kSoftWarps + 1);  // likewise, with 32 bytes from CTA 1
     mbar_init(&ctl->mma_done[0], 1);
     mbar_init(&ctl->mma_done[1], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->unit_full[s], 1);
+      mbar_init(&ctl->unit_empty[s], kThreads / 32 - 1);
+    }
+    mbar_init(&ctl->next_full, 1);
+    mbar_init(&ctl->next_empty, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -268,96 +337,168 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
 
-  // Outer coordinate of a tile in the pools: page * Hkv + KV head; a page
-  // outside the pool lies outside the map and reads zeros.
-  auto pages32 = [&](int jj) -> int {
-    const int j = j0 + jj + lane;
-    if (jj + lane >= n_pair) return 0;
-    const int page = __ldg(p.page_table + static_cast<long>(b) * p.max_pages + j);
-    return (page >= 0 && page < p.num_pages ? page : p.num_pages) * p.Hkv + kvh;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_pair(bar, parity, abort_flag, peer_abort);
+  };
+  // Waits of whole warps, and the next unit's geometry (i: units so far).
+  auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+  auto next_unit = [&](int i, Unit* u) -> bool {
+    if (!wwait(&ctl->unit_full[i & 1], (i >> 1) & 1)) return false;
+    *u = ctl->unit[i & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->unit_empty[i & 1]);
+    return u->id >= 0;
+  };
+  // Outer coordinate in the pools of tiles jj + lane of a unit: page * Hkv +
+  // KV head; a page outside the pool lies outside the map and reads zeros.
+  auto pages32 = [&](const Unit& u, int jj) -> int {
+    if (jj + lane >= u.n_pair) return 0;
+    const int page = __ldg(p.page_table + static_cast<long>(u.b) * p.max_pages + u.j0 + jj + lane);
+    return (page >= 0 && page < p.num_pages ? page : p.num_pages) * p.Hkv + u.kvh;
   };
 
+  // Counters that every role keeps alike: tc, tiles before this unit; uc, units with tiles before it.
   if (warp == kWarpK) {
-    // ------------------------------------------------------------ Q, K producer
-    if (n_pair > 0) {
+    // ------------------------------------------------------------ units, Q, K producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+    }
+    const uint32_t qbar = lead(&ctl->q_full);
+    int x = blockIdx.x >> 1;
+    uint32_t tc = 0, uc = 0;
+    for (int i = 0;; ++i) {
+      // (the geometry's slot: read by all warps two units ago)
+      if (!wwait(&ctl->unit_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
+      Unit u;
+      u.id = -1;
+      if (x >= 0) u = geometry(x);
       if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        if (leader)
-          mbar_arrive_expect_tx(&ctl->q_full, 2 * C::kChunksQ * (p.tpb * p.G * 128));
-        const uint32_t qbar = lead(&ctl->q_full);
-#pragma unroll
-        for (int c = 0; c < C::kChunksQ; ++c)
-          tma_load_4d_pair(sQ + c * (kTile * 128), &tmQ, qbar, c * 64, 0, kvh, tok0 + i0_mine);
+        ctl->unit[i & 1] = u;
+        mbar_arrive(&ctl->unit_full[i & 1]);
       }
+      __syncwarp();
+      if (x < 0) break;
+      if (leader && lane == 0) {  // ask for the next unit
+        mbar_arrive_expect_tx(&ctl->next_full, 16);
+        request_cluster(ctl->answer, &ctl->next_full);
+      }
+      bool ok = true;
+      // Q goes in once the last unit's score MMAs are done; until then the
+      // first tiles' K fill the ring.
+      const int q_at = uc == 0 ? 0 : min(u.n_pair, NK) - 1;
       int z = 0;
-      for (int jj = 0; jj < n_pair; ++jj) {
-        if ((jj & 31) == 0) z = pages32(jj);
+      for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
+        if ((jj & 31) == 0) z = pages32(u, jj);
         const int zt = __shfl_sync(0xffffffffu, z, jj & 31);
-        const int s = jj % NK;
-        const bool ok = mbar_wait_pair(&ctl->k_empty[s], ((jj / NK) & 1) ^ 1, abort_flag, peer_abort);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t s = tc % NK;
+        ok = wwait(&ctl->k_empty[s], ((tc / NK) & 1) ^ 1);
+        if (!ok) break;
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(&ctl->k_full[s], 2 * C::kKHalfBytes);
           const uint32_t kbar = lead(&ctl->k_full[s]);
-          const int y = 64 * static_cast<int>(rank) - (j0 + jj == nT_b - 1 ? last_shift : 0);
+          const int y = 64 * static_cast<int>(rank) - (u.j0 + jj == u.last ? u.last_shift : 0);
 #pragma unroll
           for (int c = 0; c < C::kChunksQ; ++c)
             tma_load_3d_pair(sK + s * C::kKHalfBytes + c * C::kKChunk, &tmK, kbar, c * 64, y, zt);
         }
+        if (jj == q_at) {
+          ok = wwait(&ctl->q_empty, (uc & 1) ^ 1);
+          if (ok && lane == 0) {
+            if (leader) mbar_arrive_expect_tx(&ctl->q_full, 2 * C::kChunksQ * (p.tpb * p.G * 128));
+#pragma unroll
+            for (int c = 0; c < C::kChunksQ; ++c)
+              tma_load_4d_pair(sQ + c * (kTile * 128), &tmQ, qbar, c * 64, 0, u.kvh, u.tok);
+          }
+        }
       }
+      if (u.n_pair > 0) ++uc;
+      // The next unit's number.  (The answer is awaited even after a failed
+      // wait: it must not land after this CTA has left.)
+      int next = -1;
+      if (leader) {
+        const bool answered = wwait(&ctl->next_full, i & 1);
+        if (answered) next = requested_block(ctl->answer);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next one lands
+        next = next >= 0 ? next >> 1 : -1;
+        if (!(ok && answered)) break;
+        if (!wwait(&ctl->next_empty, (i & 1) ^ 1)) break;
+        if (lane == 0)
+          st_async_u32(map_shared(smem_u32(&ctl->next_unit), 1u), static_cast<uint32_t>(next + 1),
+                       map_shared(smem_u32(&ctl->next_full), 1u));
+      } else {
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->next_full, 4);
+        if (!(ok && wwait(&ctl->next_full, i & 1))) break;
+        next = static_cast<int>(*reinterpret_cast<volatile uint32_t*>(&ctl->next_unit)) - 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_shared(smem_u32(&ctl->next_empty), 0u));
+      }
+      x = next;
     }
     __syncwarp();
   } else if (warp == kWarpV) {
     // ------------------------------------------------------------ V producer
-    if (n_pair > 0) {
-      if (lane == 0) tma_prefetch_desc(&tmV);
+    if (lane == 0) tma_prefetch_desc(&tmV);
+    uint32_t tc = 0;
+    Unit u;
+    bool ok = true;
+    for (int i = 0; ok && next_unit(i, &u); ++i) {
       int z = 0;
-      for (int jj = 0; jj < n_pair; ++jj) {
-        if ((jj & 31) == 0) z = pages32(jj);
+      for (int jj = 0; jj < u.n_pair; ++jj, ++tc) {
+        if ((jj & 31) == 0) z = pages32(u, jj);
         const int zt = __shfl_sync(0xffffffffu, z, jj & 31);
-        const int s = jj % NV;
-        const bool ok = mbar_wait_pair(&ctl->v_empty[s], ((jj / NV) & 1) ^ 1, abort_flag, peer_abort);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t s = tc % NV;
+        if (!(ok = wwait(&ctl->v_empty[s], ((tc / NV) & 1) ^ 1))) break;
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(&ctl->v_full[s], 2 * C::kVHalfBytes);
           tma_load_3d_pair(sV + s * C::kVHalfBytes, &tmV, lead(&ctl->v_full[s]),
-                           64 * static_cast<int>(rank), j0 + jj == nT_b - 1 ? -last_shift : 0, zt);
+                           64 * static_cast<int>(rank), u.j0 + jj == u.last ? -u.last_shift : 0, zt);
         }
       }
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ score issuer (leader)
-    if (leader && lane == 0 && n_pair > 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(256, 128, false, false);
-      const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
-      const uint32_t sKa = smem_u32(sK);
-      bool ok = mbar_wait_pair(&ctl->q_full, 0, abort_flag, peer_abort);
-      for (int t = 0; ok && t < n_pair; ++t) {
-        const int bsel = t % kNB;
-        // The buffer's previous tile has been decided by both blocks and its
-        // P.V (if any) issued: S_t is ordered after it (tcgen05 fence + barrier).
-        if (t >= kNB && !(ok = mbar_wait_pair(&ctl->s_free[bsel], ((t / kNB) - 1) & 1, abort_flag,
-                                              peer_abort)))
-          break;
-        const int s = t % NK;
-        if (!(ok = mbar_wait_pair(&ctl->k_full[s], (t / NK) & 1, abort_flag, peer_abort))) break;
-        tc_fence_after();
-        const uint64_t dk = smem_desc(sKa + s * C::kKHalfBytes, 16, 1024);
-        const uint32_t col = 128u * static_cast<uint32_t>(bsel);
+    constexpr uint32_t idS = idesc_bf16_f32(256, 128, false, false);
+    const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
+    const uint32_t sKa = smem_u32(sK);
+    uint32_t tc = 0, uc = 0;
+    Unit u;
+    bool ok = true;
+    for (int i = 0; ok && next_unit(i, &u); ++i) {
+      if (!leader || u.n_pair == 0) continue;
+      if (lane == 0) {
+        ok = wait(&ctl->q_full, uc & 1);
+        for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
+          const uint32_t bsel = tc % kNB;
+          // The buffer's previous tile has been decided by both blocks and its
+          // P.V (if any) issued: S_t is ordered after it (tcgen05 fence + barrier).
+          if (tc >= kNB && !(ok = wait(&ctl->s_free[bsel], ((tc / kNB) - 1) & 1))) break;
+          const uint32_t s = tc % NK;
+          if (!(ok = wait(&ctl->k_full[s], (tc / NK) & 1))) break;
+          tc_fence_after();
+          const uint64_t dk = smem_desc(sKa + s * C::kKHalfBytes, 16, 1024);
+          const uint32_t col = 128u * bsel;
 #pragma unroll
-        for (int kk = 0; kk < DQK / 16; ++kk) {
-          const uint32_t qoff = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-          const uint32_t koff = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
-          mma2_bf16_ss(tmem + col, dq + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < DQK / 16; ++kk) {
+            const uint32_t qoff = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+            const uint32_t koff = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
+            mma2_bf16_ss(tmem + col, dq + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
+          }
+          mma2_commit_mc(&ctl->s_full[bsel], 3);
+          mma2_commit_mc(&ctl->k_empty[s], 3);
+          // CTA 1's four warps on this tile complete 4 bytes each on dec; this
+          // arrival sets that count for the tile's phase.
+          mbar_arrive_expect_tx(&ctl->dec[bsel], 4 * kGroupWarps);
         }
-        mma2_commit_mc(&ctl->s_full[bsel], 3);
-        mma2_commit_mc(&ctl->k_empty[s], 3);
-        // CTA 1's four warps on this tile complete 4 bytes each on dec; this
-        // arrival sets that count for the tile's phase.
-        mbar_arrive_expect_tx(&ctl->dec[bsel], 4 * kGroupWarps);
+        if (ok) mma2_commit_mc(&ctl->q_empty, 3);
       }
+      ++uc;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (leader && lane == 0) {
       // Every MMA issued must have finished before TMEM is freed.
       mma2_commit_mc(&ctl->mma_done[0], 1);
       mbar_wait(&ctl->mma_done[0], 0, nullptr);
@@ -365,372 +506,412 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpPV) {
     // ------------------------------------------------------------ P.V issuer (leader)
-    if (leader && lane == 0 && n_pair > 0) {
-      constexpr uint32_t idO = idesc_bf16_f32(256, DV, false, true);
-      const uint32_t sVa = smem_u32(sV);
-      bool ok = true;
-      uint32_t o_acc = 0u;
-      uint32_t nresc = 0u;  // bit (kSoftWarps * r + warp): parity of (CTA r, warp)'s requests
-      for (int j = 0; ok && j < n_pair; ++j) {
-        const int bsel = j % kNB;
-        const uint32_t ph = (j / kNB) & 1;
-        // The tile's V halves do not depend on the decisions: wait for them
-        // first, while the softmax is still deciding.
-        const int vs = j % NV;
-        if (!mbar_wait_pair(&ctl->v_full[vs], (j / NV) & 1, abort_flag, peer_abort)) {
-          ok = false;
-          break;
-        }
-        if (!mbar_wait_pair(&ctl->dec[bsel], ph, abort_flag, peer_abort)) {
-          ok = false;
-          break;
-        }
-        // Tile j's decisions come from the warps of warpgroup j % 2.
-        const int wg0 = kGroupWarps * (j & 1);
-        uint32_t resc = 0u, any_kept = 0u;  // resc: bit (kGroupWarps * r + w)
-        {
-          // (plain loads: the barrier waits above are compiler memory barriers)
-          const uint4 f4 = *reinterpret_cast<const uint4*>(ctl->flags[bsel]);
-          const uint4 g4 = *reinterpret_cast<const uint4*>(ctl->peer_flags[bsel]);
-          const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
-          const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-          for (int w = 0; w < kGroupWarps; ++w) {
-            any_kept |= (f[w] | g[w]) & kFlagKept;
-            resc |= ((f[w] >> 1) & 1u) << w;
-            resc |= ((g[w] >> 1) & 1u) << (kGroupWarps + w);
-          }
-        }
-        if (resc) {
-          // Warps that move their reference maximum rescale O once every P.V
-          // issued so far has finished.
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int w = 0; w < kGroupWarps; ++w)
-              if (resc & (1u << (kGroupWarps * r + w)))
-                mma2_commit_mc(&ctl->drain[wg0 + w], static_cast<uint16_t>(1u << r));
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
+    constexpr uint32_t idO = idesc_bf16_f32(256, DV, false, true);
+    const uint32_t sVa = smem_u32(sV);
+    uint32_t tc = 0, uc = 0;
+    uint32_t nresc = 0u;  // bit (kSoftWarps * r + warp): parity of (CTA r, warp)'s requests
+    Unit u;
+    bool ok = true;
+    for (int i = 0; ok && next_unit(i, &u); ++i) {
+      if (!leader || u.n_pair == 0) continue;
+      if (lane == 0) {
+        // O is read by the last unit's epilogue (of CTA 1's warps: as bytes).
+        if (uc > 0) ok = wait(&ctl->o_free, (uc - 1) & 1);
+        mbar_arrive_expect_tx(&ctl->o_free, 4 * kSoftWarps);
+        uint32_t o_acc = 0u;
+        for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
+          const uint32_t bsel = tc % kNB;
+          const uint32_t ph = (tc / kNB) & 1;
+          // The tile's V halves do not depend on the decisions: wait for them
+          // first, while the softmax is still deciding.
+          const uint32_t vs = tc % NV;
+          if (!(ok = wait(&ctl->v_full[vs], (tc / NV) & 1))) break;
+          if (!(ok = wait(&ctl->dec[bsel], ph))) break;
+          // The tile's decisions come from the warps of warpgroup jj % 2.
+          const int wg0 = kGroupWarps * (jj & 1);
+          uint32_t resc = 0u, any_kept = 0u;  // resc: bit (kGroupWarps * r + w)
+          {
+            // (plain loads: the barrier waits above are compiler memory barriers)
+            const uint4 f4 = *reinterpret_cast<const uint4*>(ctl->flags[bsel]);
+            const uint4 g4 = *reinterpret_cast<const uint4*>(ctl->peer_flags[bsel]);
+            const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+            const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
             for (int w = 0; w < kGroupWarps; ++w) {
-              const uint32_t bit = 1u << (kSoftWarps * r + wg0 + w);
-              if (ok && (resc & (1u << (kGroupWarps * r + w)))) {
-                const uint32_t par = (nresc & bit) ? 1u : 0u;
-                ok = (r == 0) ? mbar_wait_pair(&ctl->rescaled[0][wg0 + w], par, abort_flag, peer_abort)
-                              : mbar_wait_pair<true>(&ctl->rescaled[1][wg0 + w], par, abort_flag,
-                                                     peer_abort);
-                nresc ^= bit;
-              }
+              any_kept |= (f[w] | g[w]) & kFlagKept;
+              resc |= ((f[w] >> 1) & 1u) << w;
+              resc |= ((g[w] >> 1) & 1u) << (kGroupWarps + w);
             }
-          if (!ok) break;
-        }
-        if (any_kept) {
-          tc_fence_after();
-          const uint64_t dv = smem_desc(sVa + vs * C::kVHalfBytes, 16384, 1024);
-          const uint32_t pcol = 128u * static_cast<uint32_t>(bsel);
+          }
+          if (resc) {
+            // Warps that move their reference maximum rescale O once every P.V
+            // issued so far has finished.
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)  // P of keys 16kk..: column 64 (kk / 4) + 8 (kk % 4)
-            mma2_bf16_ts(tmem + C::kColO, tmem + pcol + 64 * (kk >> 2) + 8 * (kk & 3),
-                         dv + ((kk * 2048) >> 4), idO, (o_acc | kk) ? 1u : 0u);
-          o_acc = 1u;
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int w = 0; w < kGroupWarps; ++w)
+                if (resc & (1u << (kGroupWarps * r + w)))
+                  mma2_commit_mc(&ctl->drain[wg0 + w], static_cast<uint16_t>(1u << r));
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int w = 0; w < kGroupWarps; ++w) {
+                const uint32_t bit = 1u << (kSoftWarps * r + wg0 + w);
+                if (ok && (resc & (1u << (kGroupWarps * r + w)))) {
+                  const uint32_t par = (nresc & bit) ? 1u : 0u;
+                  ok = (r == 0) ? wait(&ctl->rescaled[0][wg0 + w], par)
+                                : mbar_wait_pair<true>(&ctl->rescaled[1][wg0 + w], par, abort_flag,
+                                                       peer_abort);
+                  nresc ^= bit;
+                }
+              }
+            if (!ok) break;
+          }
+          if (any_kept) {
+            tc_fence_after();
+            const uint64_t dv = smem_desc(sVa + vs * C::kVHalfBytes, 16384, 1024);
+            const uint32_t pcol = 128u * bsel;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)  // P of keys 16kk..: column 64 (kk / 4) + 8 (kk % 4)
+              mma2_bf16_ts(tmem + C::kColO, tmem + pcol + 64 * (kk >> 2) + 8 * (kk & 3),
+                           dv + ((kk * 2048) >> 4), idO, (o_acc | kk) ? 1u : 0u);
+            o_acc = 1u;
+          }
+          mma2_commit_mc(&ctl->v_empty[vs], 3);
+          tc_fence_before();
+          mbar_arrive(&ctl->s_free[bsel]);
         }
-        mma2_commit_mc(&ctl->v_empty[vs], 3);
-        tc_fence_before();
-        mbar_arrive(&ctl->s_free[bsel]);
+        if (ok) mma2_commit_mc(&ctl->o_full, 3);
       }
-      if (ok) mma2_commit_mc(&ctl->o_full, 3);
+      ++uc;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (leader && lane == 0) {
       mma2_commit_mc(&ctl->mma_done[1], 1);
       mbar_wait(&ctl->mma_done[1], 0, nullptr);
     }
     __syncwarp();
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax / vote
-    // Two warpgroups take alternate tiles: warpgroup g = warp / 4 handles the
-    // tiles j with j % 2 == g, one thread per query row (warp w reads TMEM
-    // lanes 32 (w % 4) .. + 31) over all 128 score columns, loaded as two
-    // halves of 64.  A row's running state passes from one warpgroup to the
-    // other once per tile: the warpgroup on tile j - 1 writes the exact running
-    // maximum m (the vote's reference) and the reference maximum m_ref of P to
-    // shared memory and arrives on a named barrier, and the warpgroup on tile j
-    // completes that barrier before its vote (one barrier per direction, so an
-    // arrival can only complete the hand-over it is meant for).  The state chain of consecutive
-    // tiles is therefore short (a barrier, the vote, a store), and each
-    // warpgroup's loads, maxima and exponentials overlap the other's.  Each
-    // warpgroup sums its own tiles' P into l against the m_ref it last saw; a
-    // moved m_ref rescales that sum when the state arrives, and the two sums
-    // meet at the end.  After a failed wait a thread carries on to the end of
-    // the loop (every later wait gives up at once), so all threads take the
-    // same sequence of named barriers.
+    // Two warpgroups take alternate tiles of a unit: warpgroup g = warp / 4 the
+    // tiles jj with jj % 2 == g, one thread per row (warp w reads TMEM lanes
+    // 32 (w % 4) .. + 31) over all 128 score columns, loaded as two halves of
+    // 64.  A row's running state passes from one warpgroup to the other once
+    // per tile: the warpgroup on tile jj - 1 writes the running maximum m of the
+    // vote and the reference maximum m_ref of P to shared memory and arrives on
+    // a named barrier, and the warpgroup on tile jj completes that barrier
+    // before its vote (one barrier per direction, so an arrival can only
+    // complete the hand-over it is meant for).  Each warpgroup sums its own
+    // tiles' P into l against the m_ref it last saw; a moved m_ref rescales
+    // that sum when the state arrives, and the two sums meet at the end.  After
+    // a failed wait a thread carries on to the end of the unit (every later
+    // wait gives up at once), so all threads take the same sequence of named
+    // barriers; at the start of the next one the failure is agreed on and all
+    // leave together.
     const int g = warp / kGroupWarps, q4 = warp % kGroupWarps;
     const int row = q4 * 32 + lane;  // TMEM lane
     const int gtid = tid - 128 * g;  // thread index within the warpgroup
     const int tok = row / p.G, head = row - tok * p.G;  // of the block, of the group
-    const bool row_valid = tok < toks_mine;
-    int lim = len - 1;  // last key index this row may see
-    if (p.causal) lim = min(lim, off + i0_mine + tok);
-    if (!row_valid) lim = -1;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t colO = lane_base + C::kColO;
     const float sl2 = p.scale_log2;
-    const bool has_unit = toks_mine > 0;
-    float m_true = -INFINITY, m_ref = -INFINITY, l = 0.f;
-    uint32_t skipped = 0, n_drain = 0;
-    bool ok = true;
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_pair(bar, parity, abort_flag, peer_abort));
-    };
+    uint32_t n_drain = 0;
     constexpr uint32_t kBar = 2;               // named barrier of all softmax threads
     const uint32_t bar_give = 3 + g;           // hand-over from this warpgroup
     const uint32_t bar_take = 3 + (g ^ 1);     // hand-over to this warpgroup
     const uint32_t bar_vote = 5 + g;           // the 128 threads of this warpgroup
+    uint32_t tc = 0, uc = 0;
+    Unit u;
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      const bool have = next_unit(i, &u);
+      if (named_bar_or(kBar, kSoftThreads, !(ok && have))) break;
+      const bool row_valid = tok < u.toks;
+      // last key index this row may see
+      const int lim = row_valid ? min(u.last * kTile + kTile - 1 - u.last_shift, u.lim0 + tok) : -1;
+      const long unit_row = static_cast<long>(u.id) * p.max_pages;
+      float m_true = -INFINITY, m_ref = -INFINITY, l = 0.f;
+      uint32_t skipped = 0;
+      int in_range = g;  // tile jj's place in its range of the vote
+      if (kVote)
+        while (in_range >= u.range) in_range -= u.range;
 
-    // Columns 64 hf .. + 63 of the scores of tile j, masked, into sr; returns their maximum.
-    auto load_half = [&](uint32_t colS, int j, int hf, uint32_t* sr) -> float {
-      tmem_ld32p(colS + 64 * hf, sr);
-      tmem_ld32p(colS + 64 * hf + 32, sr + 32);
-      tmem_wait_ld();
-      // Column e of the half is key k0 + e; the last tile's first columns are no keys.
-      const int shift = (j == nT_b - 1) ? last_shift : 0;
-      const int first = shift - 64 * hf, vis = lim - (j * kTile - first);
-      if (first > 0 || vis < 63) {
+      // Columns 64 hf .. + 63 of the scores of tile j, masked, into sr; returns their maximum.
+      auto load_half = [&](uint32_t colS, int j, int hf, uint32_t* sr) -> float {
+        tmem_ld32p(colS + 64 * hf, sr);
+        tmem_ld32p(colS + 64 * hf + 32, sr + 32);
+        tmem_wait_ld();
+        // Column e of the half is key k0 + e; the last tile's first columns are no keys.
+        const int shift = (j == u.last) ? u.last_shift : 0;
+        const int first = shift - 64 * hf, vis = lim - (j * kTile - first);
+        if (first > 0 || vis < 63) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e < first || e > vis) sr[e] = __float_as_uint(-INFINITY);
-      }
-      float mx[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-      return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    };
-    // P = exp2(s*scale*log2e - m_ref*scale*log2e) of the 64 scores in sr, as
-    // bf16 pairs into sr[0..31]; returns their sum.
-    auto exp_half = [&](uint32_t* sr) -> float {
-      const float mb = (m_ref == -INFINITY) ? 0.f : m_ref * sl2;
-      const uint64_t sl2x2 = f32x2(sl2, sl2), nmb = f32x2(-mb, -mb);
-      uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int cc = 8 * q; cc < 8 * q + 8; ++cc) {
-          const uint64_t xp = fma_f32x2(
-              f32x2(__uint_as_float(sr[2 * cc]), __uint_as_float(sr[2 * cc + 1])), sl2x2, nmb);
-          const float p0 = ex2_approx(f32x2_lo(xp));
-          const float p1 = ex2_approx(f32x2_hi(xp));
-          ls[cc & 1] = add_f32x2(ls[cc & 1], f32x2(p0, p1));
-          sr[cc] = pack_bf16x2(p0, p1);
+          for (int e = 0; e < 64; ++e)
+            if (e < first || e > vis) sr[e] = __float_as_uint(-INFINITY);
         }
-        if (q < 3) order_after(sr + 8 * q, sr + 16 * (q + 1));
-      }
-      const uint64_t lsum = add_f32x2(ls[0], ls[1]);
-      return f32x2_lo(lsum) + f32x2_hi(lsum);
-    };
+        float mx[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      };
+      // P = exp2(s*scale*log2e - m_ref*scale*log2e) of the 64 scores in sr, as
+      // bf16 pairs into sr[0..31]; returns their sum.
+      auto exp_half = [&](uint32_t* sr) -> float {
+        const float mb = (m_ref == -INFINITY) ? 0.f : m_ref * sl2;
+        const uint64_t sl2x2 = f32x2(sl2, sl2), nmb = f32x2(-mb, -mb);
+        uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int cc = 8 * q; cc < 8 * q + 8; ++cc) {
+            const uint64_t xp = fma_f32x2(
+                f32x2(__uint_as_float(sr[2 * cc]), __uint_as_float(sr[2 * cc + 1])), sl2x2, nmb);
+            const float p0 = ex2_approx(f32x2_lo(xp));
+            const float p1 = ex2_approx(f32x2_hi(xp));
+            ls[cc & 1] = add_f32x2(ls[cc & 1], f32x2(p0, p1));
+            sr[cc] = pack_bf16x2(p0, p1);
+          }
+          if (q < 3) order_after(sr + 8 * q, sr + 16 * (q + 1));
+        }
+        const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+        return f32x2_lo(lsum) + f32x2_hi(lsum);
+      };
 
-    for (int jj = g; jj < n_pair; jj += 2) {
-      const int j = j0 + jj;  // tile of the sequence
-      const int bsel = jj % kNB;
-      const uint32_t colS = lane_base + 128u * static_cast<uint32_t>(bsel);
-      if (!wwait(&ctl->s_full[bsel], (jj / kNB) & 1)) ok = false;
-      tc_fence_after();
-      const bool mine = jj < n_mine;
-      uint32_t sr[64];
-      float tmax = -INFINITY;
-      if (mine) {
-        tmax = load_half(colS, j, 0, sr);
-        // (finish the first half's maximum before the second half's load, so
-        // that only one half of the scores is ever held in registers)
-        asm volatile("" : "+f"(tmax));
-        tmax = fmaxf(tmax, load_half(colS, j, 1, sr));  // sr keeps the second half
-      }
-      // The state after the previous tile, from the other warpgroup.
-      if (jj > 0) {
-        named_bar_sync(bar_take, kSoftThreads);
-        const float2 hs = ctl->hand[row];
-        m_true = hs.x;
-        if (hs.y != m_ref) {
-          if (m_ref != -INFINITY) l *= ex2_approx((m_ref - hs.y) * sl2);
-          m_ref = hs.y;
+      for (int jj = g; jj < u.n_pair; jj += 2) {
+        const int j = u.j0 + jj;  // tile of the sequence
+        const uint32_t t = tc + jj, bsel = t % kNB;
+        const uint32_t colS = lane_base + 128u * bsel;
+        if (!wwait(&ctl->s_full[bsel], (t / kNB) & 1)) ok = false;
+        tc_fence_after();
+        const bool mine = jj < u.n_mine;
+        uint32_t sr[64];
+        float tmax = -INFINITY;
+        if (mine) {
+          tmax = load_half(colS, j, 0, sr);
+          // (finish the first half's maximum before the second half's load, so
+          // that only one half of the scores is ever held in registers)
+          asm volatile("" : "+f"(tmax));
+          tmax = fmaxf(tmax, load_half(colS, j, 1, sr));  // sr keeps the second half
         }
-      }
-      bool kept = false, resc = false;
-      float alpha = 1.f;
-      if (mine) {
-        // Skip vote: every row of the block must pass exp(scale*(tile_max - m)) < lambda.
-        float c = -INFINITY;
-        if (tmax != -INFINITY) c = (m_true == -INFINITY) ? INFINITY : tmax - m_true;
+        // The state after the previous tile, from the other warpgroup.
+        if (jj > 0) {
+          named_bar_sync(bar_take, kSoftThreads);
+          const float2 hs = ctl->hand[row];
+          m_true = hs.x;
+          if (hs.y != m_ref) {
+            if (m_ref != -INFINITY) l *= ex2_approx((m_ref - hs.y) * sl2);
+            m_ref = hs.y;
+          }
+        }
+        bool kept = false, resc = false;
+        float alpha = 1.f;
         if constexpr (kVote) {
-          kept = !named_bar_and(bar_vote, 128, c < thr_raw);
-          if (p.margin != nullptr) {
-            float cm = c;
+          // A range of the vote starts without a running maximum.
+          if (in_range == 0) m_true = -INFINITY;
+          in_range += 2;
+          while (in_range >= u.range) in_range -= u.range;
+        }
+        if (mine) {
+          // Skip vote: every row of the block must pass exp(scale*(tile_max - m)) < lambda.
+          float c = -INFINITY;
+          if (tmax != -INFINITY) c = (m_true == -INFINITY) ? INFINITY : tmax - m_true;
+          if constexpr (kVote) {
+            kept = !named_bar_and(bar_vote, 128, c < u.thr_raw);
+            if (p.margin != nullptr) {
+              float cm = c;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
-            if (lane == 0) *reinterpret_cast<volatile float*>(&ctl->red[g][q4]) = cm;
-            named_bar_sync(bar_vote, 128);
-            if (gtid == 0 && has_unit) {
-              const volatile float* rr = ctl->red[g];
-              const float cmax = fmaxf(fmaxf(rr[0], rr[1]), fmaxf(rr[2], rr[3]));
-              p.margin[unit * p.max_pages + j] = (cmax == INFINITY) ? INFINITY : cmax * p.scale;
+              for (int o = 16; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+              if (lane == 0) *reinterpret_cast<volatile float*>(&ctl->red[g][q4]) = cm;
+              named_bar_sync(bar_vote, 128);
+              if (gtid == 0) {
+                const volatile float* rr = ctl->red[g];
+                const float cmax = fmaxf(fmaxf(rr[0], rr[1]), fmaxf(rr[2], rr[3]));
+                p.margin[unit_row + j] = (cmax == INFINITY) ? INFINITY : cmax * p.scale;
+              }
+            }
+            if (gtid == 0) {
+              skipped += kept ? 0u : 1u;
+              if (p.mask != nullptr) p.mask[unit_row + j] = kept ? 0 : 1;
+            }
+          } else {
+            kept = true;
+          }
+          m_true = fmaxf(m_true, tmax);
+          if (kept) {
+            // m_ref trails m lazily: it moves only when m has grown by more than
+            // 2^8 in exp2 units, and then the warp's rows of O are rescaled.
+            bool need = false;
+            if (m_ref == -INFINITY) {
+              m_ref = m_true;  // no key of this row counted yet: its O row and l are zero
+            } else if ((m_true - m_ref) * sl2 > kRescaleLog2) {
+              need = true;
+            }
+            resc = __any_sync(0xffffffffu, need);
+            if (resc && m_ref != -INFINITY && m_true > m_ref) {
+              alpha = ex2_approx((m_ref - m_true) * sl2);
+              l *= alpha;
+              m_ref = m_true;
             }
           }
-          if (gtid == 0 && has_unit) {
-            skipped += kept ? 0u : 1u;
-            if (p.mask != nullptr) p.mask[unit * p.max_pages + j] = kept ? 0 : 1;
-          }
-        } else {
-          kept = true;
         }
-        m_true = fmaxf(m_true, tmax);
+        if (jj + 1 < u.n_pair) {
+          ctl->hand[row] = make_float2(m_true, m_ref);
+          named_bar_arrive(bar_give, kSoftThreads);
+        }
+        // P of columns 64 hf .. as bf16 pairs over the first 32 of those score
+        // columns; the second half goes first, from the registers, then the
+        // first half is loaded again.  A skipped or unseen tile writes zeros
+        // (the pair's P.V covers both blocks; the other block may keep the tile).
         if (kept) {
-          // m_ref trails m lazily: it moves only when m has grown by more than
-          // 2^8 in exp2 units, and then the warp's rows of O are rescaled.
-          bool need = false;
-          if (m_ref == -INFINITY) {
-            m_ref = m_true;  // no key of this row counted yet: its O row and l are zero
-          } else if ((m_true - m_ref) * sl2 > kRescaleLog2) {
-            need = true;
+          float ls = exp_half(sr);
+          tmem_st32p(colS + 64, sr);
+          load_half(colS, j, 0, sr);
+          ls += exp_half(sr);
+          tmem_st32p(colS, sr);
+          l += ls;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sr[e] = 0u;
+          tmem_st32p(colS + 64, sr);
+          tmem_st32p(colS, sr);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t f = (kept ? kFlagKept : 0u) | (resc ? kFlagRescale : 0u);
+          if (leader) {
+            *reinterpret_cast<volatile uint32_t*>(&ctl->flags[bsel][q4]) = f;
+            mbar_arrive(&ctl->dec[bsel]);
+          } else {
+            st_async_u32(map_shared(smem_u32(&ctl->peer_flags[bsel][q4]), 0u), f,
+                         lead(&ctl->dec[bsel]));
           }
-          resc = __any_sync(0xffffffffu, need);
-          if (resc && m_ref != -INFINITY) {
-            alpha = ex2_approx((m_ref - m_true) * sl2);
-            l *= alpha;
-            m_ref = m_true;
+        }
+        if (resc) {
+          // The P.V issuer drains the P.V MMAs issued so far; then this warp's
+          // rows of O are rescaled before this tile's P.V.
+          if (!wwait(&ctl->drain[warp], n_drain & 1)) ok = false;
+          ++n_drain;
+          if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < DV / 32; ++cc) {
+              uint32_t orr[32];
+              tmem_ld32p(colO + cc * 32, orr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+              tmem_st32p(colO + cc * 32, orr);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(&ctl->rescaled[0][warp]);
+            else
+              mbar_arrive_cluster(lead(&ctl->rescaled[1][warp]));
           }
         }
       }
-      if (jj + 1 < n_pair) {
-        ctl->hand[row] = make_float2(m_true, m_ref);
-        named_bar_arrive(bar_give, kSoftThreads);
+      tc += u.n_pair;
+
+      // The row's denominator: both warpgroups' sums against the later m_ref
+      // (the one O is kept against).
+      ctl->fin[g][row] = make_float2(m_ref, l);
+      if (gtid == 0) ctl->skipped[g] = skipped;
+      named_bar_sync(kBar, kSoftThreads);
+      const float2 other = ctl->fin[g ^ 1][row];
+      const float m_fin = fmaxf(m_ref, other.x);
+      float l_row = 0.f;
+      if (m_fin != -INFINITY) {
+        if (m_ref != -INFINITY) l_row += l * ex2_approx((m_ref - m_fin) * sl2);
+        if (other.x != -INFINITY) l_row += other.y * ex2_approx((other.x - m_fin) * sl2);
       }
-      // P of columns 64 hf .. as bf16 pairs over the first 32 of those score
-      // columns; the second half goes first, from the registers, then the
-      // first half is loaded again.  A skipped or unseen tile writes zeros
-      // (the pair's P.V covers both blocks; the other block may keep the tile).
-      if (kept) {
-        float ls = exp_half(sr);
-        tmem_st32p(colS + 64, sr);
-        load_half(colS, j, 0, sr);
-        ls += exp_half(sr);
-        tmem_st32p(colS, sr);
-        l += ls;
+      if (u.n_pair > 0) {
+        if (!wwait(&ctl->o_full, uc & 1)) ok = false;
+        ++uc;
+        tc_fence_after();
+      }
+
+      // Epilogue: this warpgroup's half of the row's O: as O / l in bf16 (a row
+      // that saw no key writes zeros), or of a part as it is, in fp32.
+      const size_t orow = static_cast<size_t>(u.tok + tok) * p.Hq + u.kvh * p.G + head;
+      const size_t rows = static_cast<size_t>(p.T) * p.Hq;
+      const bool reads = ok && u.toks > 0 && g * (DV / 2) < DVO;
+      if (reads && row_valid && g == 0 && p.parts > 1)
+        p.part_ml[u.part * rows + orow] = make_float2(m_fin * sl2, l_row);
+      const float inv_l = (l_row > 0.f) ? 1.f / l_row : 0.f;
+      uint32_t orr[64];
+      if (reads && u.n_pair > 0) {
+        tmem_ld32p(colO + g * (DV / 2), orr);
+        tmem_ld32p(colO + g * (DV / 2) + 32, orr + 32);
+        tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sr[e] = 0u;
-        tmem_st32p(colS + 64, sr);
-        tmem_st32p(colS, sr);
+        for (int e = 0; e < 64; ++e) orr[e] = 0u;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t f = (kept ? kFlagKept : 0u) | (resc ? kFlagRescale : 0u);
-        if (leader) {
-          *reinterpret_cast<volatile uint32_t*>(&ctl->flags[bsel][q4]) = f;
-          mbar_arrive(&ctl->dec[bsel]);
-        } else {
-          st_async_u32(map_shared(smem_u32(&ctl->peer_flags[bsel][q4]), 0u), f,
-                       lead(&ctl->dec[bsel]));
-        }
-      }
-      if (resc) {
-        // The P.V issuer drains the P.V MMAs issued so far; then this warp's
-        // rows of O are rescaled before this tile's P.V.
-        if (!wwait(&ctl->drain[warp], n_drain & 1)) ok = false;
-        ++n_drain;
-        if (ok) {
-          tc_fence_after();
-#pragma unroll 1
-          for (int cc = 0; cc < DV / 32; ++cc) {
-            uint32_t orr[32];
-            tmem_ld32p(colO + cc * 32, orr);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-            tmem_st32p(colO + cc * 32, orr);
-          }
-          tmem_wait_st();
-        }
+      if (u.n_pair > 0) {  // O may be overwritten
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (leader)
-            mbar_arrive(&ctl->rescaled[0][warp]);
+            mbar_arrive(&ctl->o_free);
           else
-            mbar_arrive_cluster(lead(&ctl->rescaled[1][warp]));
+            st_async_u32(map_shared(smem_u32(&ctl->o_note[warp]), 0u), 0u, lead(&ctl->o_free));
         }
       }
-    }
-
-    // The row's denominator: both warpgroups' sums against the later m_ref
-    // (the one O is kept against).
-    ctl->fin[g][row] = make_float2(m_ref, l);
-    if (gtid == 0) ctl->skipped[g] = skipped;
-    ok = !named_bar_or(kBar, kSoftThreads, !ok);
-    const float2 other = ctl->fin[g ^ 1][row];
-    const float m_fin = fmaxf(m_ref, other.x);
-    float l_row = 0.f;
-    if (m_fin != -INFINITY) {
-      if (m_ref != -INFINITY) l_row += l * ex2_approx((m_ref - m_fin) * sl2);
-      if (other.x != -INFINITY) l_row += other.y * ex2_approx((other.x - m_fin) * sl2);
-    }
-    if (ok && n_pair > 0) {
-      ok = wwait(&ctl->o_full, 0);
-      tc_fence_after();
-    }
-    if (ok && row_valid && g == 0 && p.S > 1)
-      p.part_ml[(static_cast<size_t>(split) * p.T + tok0 + i0_mine + tok) * p.Hq + kvh * p.G + head] =
-          make_float2(m_fin * sl2, l_row);
-    if (ok && has_unit && g * (DV / 2) < DVO && (p.S == 1 || n_mine > 0)) {
-      // Epilogue: this warpgroup's half of the row's O: as O / l in bf16 (a row
-      // that saw no key writes zeros), or of a split as it is, in fp32.
-      const float inv_l = (l_row > 0.f) ? 1.f / l_row : 0.f;
-      const size_t orow =
-          static_cast<size_t>(tok0 + i0_mine + tok) * p.Hq + kvh * p.G + head;
-#pragma unroll 1
-      for (int c = 0; c < DV / 64; ++c) {
-        uint32_t orr[32];
-        if (n_pair > 0) {
-          tmem_ld32p(colO + g * (DV / 2) + c * 32, orr);
-          tmem_wait_ld();
-        } else {
+      if (reads && row_valid) {
+        if (p.parts > 1) {
+          if (l_row > 0.f) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (u.part * rows + orow) * DVO + g * (DV / 2));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) orr[e] = 0u;
-        }
-        if (p.S > 1) {
-          float4* dst = reinterpret_cast<float4*>(
-              p.part_o + (static_cast<size_t>(split) * p.T * p.Hq + orow) * DVO + g * (DV / 2) + c * 32);
-          if (row_valid) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 16; ++e)
               dst[e] = make_float4(__uint_as_float(orr[4 * e]), __uint_as_float(orr[4 * e + 1]),
                                    __uint_as_float(orr[4 * e + 2]), __uint_as_float(orr[4 * e + 3]));
           }
-          continue;
-        }
-        uint32_t w[16];
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + orow * DVO + g * (DV / 2));
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv_l,
-                             __uint_as_float(orr[2 * e + 1]) * inv_l);
-        if (row_valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + orow * DVO + g * (DV / 2) + c * 32);
+          for (int e = 0; e < 8; ++e) {
+            uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(orr[8 * e + 2 * k]) * inv_l,
+                                 __uint_as_float(orr[8 * e + 2 * k + 1]) * inv_l);
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
+      // Debug outputs: the unit's count, and the tiles that it does not see.
+      if (kVote && tid == 0 && p.counts != nullptr) {
+        const uint32_t n = ctl->skipped[0] + ctl->skipped[1];
+        if (p.parts == 1)
+          p.counts[u.id] = n;
+        else
+          atomicAdd(p.counts + u.id, n);  // (cleared before the launch)
+      }
+      if (p.mask != nullptr || p.margin != nullptr) {
+        const int end = u.part == p.parts - 1 ? p.max_pages : u.j1;
+        for (int j = u.j0 + u.n_mine + tid; j < end; j += kSoftThreads) {
+          if (p.mask != nullptr) p.mask[unit_row + j] = 2;
+          if (p.margin != nullptr) p.margin[unit_row + j] = NAN;
+        }
+      }
+      __syncwarp();
     }
-    if (tid == 0 && p.counts != nullptr)
-      p.counts[unit] = has_unit ? ctl->skipped[0] + ctl->skipped[1] : 0;
     __syncwarp();
   }
 
   // ------------------------------------------------------------ teardown
   // After an expired wait, copies may still be in flight into either CTA's
-  // shared memory (the leader's barriers count both halves): give them time
-  // to land before the pair's shared memory is released.
+  // shared memory (the leader's barriers count both halves; a requested unit's
+  // number): give them time to land before the pair's shared memory is released.
   if (*abort_flag) {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 50000ull) {
@@ -745,8 +926,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) report_timeout(p.status);
 }
 
-// Joins a row's S partial states: o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s -
-// m*) l_s, m* the largest m of the ranges that kept a key.  A warp per row; rows
+// Joins a row's partial states: o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s -
+// m*) l_s, m* the largest m of the parts that kept a key.  A warp per row; rows
 // of tokens that belong to no sequence are left as they were.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
@@ -756,7 +937,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
   const int tok = static_cast<int>(row / p.Hq);
   if (tok >= p.T || tok < p.cu_seqlens[0] || tok >= p.cu_seqlens[p.B]) return;
   float mstar = -INFINITY;
-  for (int s = 0; s < p.S; ++s) {
+  for (int s = 0; s < p.parts; ++s) {
     const float2 ml = p.part_ml[s * rows + row];
     if (ml.y > 0.f) mstar = fmaxf(mstar, ml.x);
   }
@@ -764,7 +945,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
   float acc[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s = 0; s < p.S; ++s) {
+  for (int s = 0; s < p.parts; ++s) {
     const float2 ml = p.part_ml[s * rows + row];
     if (!(ml.y > 0.f)) continue;
     const float w = ex2_approx(ml.x - mstar);
@@ -794,16 +975,29 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   auto* fn = chunk_paged_kernel<D, 128, D, MODE>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const long pairs = static_cast<long>(p.slots) * p.Hkv * p.S;
-  fn<<<dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), C::kSmemBytes, st>>>(tq, tk, tv, p);
+  // One cluster per unit; those that are not launched yet are taken over by running ones.
+  const long units = static_cast<long>(p.slots) * p.Hkv * p.parts;
+  if (p.counts != nullptr && (p.parts > 1 || MODE == Mode::kDense)) {
+    e = cudaMemsetAsync(p.counts, 0, sizeof(uint32_t) * 2 * p.slots * p.Hkv, st);
+    if (e != cudaSuccess) return e;
+  }
+  fn<<<dim3(static_cast<unsigned>(2 * units)), dim3(kThreads), C::kSmemBytes, st>>>(tq, tk, tv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.S == 1) return e;
+  if (e != cudaSuccess || p.parts == 1) return e;
   const long rows = static_cast<long>(p.T) * p.Hq;
   chunk_merge_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// Parts of the tiles: the most, up to the S ranges, that the units fill the
+// GPU's 76 cluster places with no more than twice over.
+int chunk_parts(long pairs, int S) {
+  const long places = 76;
+  const long most = 2 * places / pairs;
+  return most < 1 ? 1 : most < S ? static_cast<int>(most) : S;
+}
 
 cudaError_t launch_chunk_paged(int d, bool vote, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const ChunkParams& p, cudaStream_t st) {

@@ -448,16 +448,17 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
  *     ss_attn_decode_paged (what a page holds behind its sequence's end is
  *     not read, whatever it is; keys and values of the sequence itself must
  *     be finite).
- *   Voting unit: a block of 128 / G (rounded down) consecutive new tokens of
- *     one sequence x the G = Hq / Hkv query heads of one KV head x one range
- *     of tiles.  num_kv_splits cuts each sequence's tiles into ranges as in
- *     ss_attn_decode_paged; each range keeps its first tile that the unit
- *     sees.  More ranges keep more SMs busy when there are few new tokens.
+ *   Voting unit: a block of m = 128 / G (rounded down) consecutive new tokens
+ *     of one sequence x the G = Hq / Hkv query heads of one KV head.
+ *     num_kv_splits cuts a sequence's tiles into ranges as in
+ *     ss_attn_decode_paged: each starts without a running maximum, so the
+ *     first tile of it that the unit sees is kept.  It also bounds into how
+ *     many parts the library may deal a unit's tiles when there are few new
+ *     tokens for many SMs (lambda_a = 0: its only effect).
  *   skip_counts: nullable, [ss_attn_chunk_paged_units(...)]: per unit, its
- *     skipped tiles (0 for units without tokens).  Unit of (range s, KV head
- *     h, block k of sequence b): ((s * Hkv + h) * places + p) * 2 + k % 2 with
- *     m = 128 / G, places = T / (2m) + B and p = cu_seqlens[b] / (2m) + b +
- *     k / 2 (integer divisions).
+ *     skipped tiles (0 for units without tokens).  Unit of (KV head h, block k
+ *     of sequence b): (h * places + p) * 2 + k % 2 with places = T / (2m) + B
+ *     and p = cu_seqlens[b] / (2m) + b + k / 2 (integer divisions).
  *   workspace: at least ss_attn_chunk_paged_workspace_size(...) bytes, 16-byte
  *     aligned (nullable when that is 0).
  *   dbg: nullable; skip_mask / vote_margin are [units][max_pages]; its other
@@ -465,7 +466,7 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
  * G <= 128, d in {64, 128}.  Returns SS_OK (also for T = 0),
  * SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
  */
-size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv, int num_kv_splits);
+size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv);
 size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits);
 ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
                               const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,

@@ -132,9 +132,9 @@ def test_chunk_refuses_test_only_debug_fields(capi):
 def test_sizes(capi):
     assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 1) == 0
     assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 3) == 3 * 10 * 8 * 130 * 4
-    assert capi.ss_attn_chunk_paged_units(1000, 7, 8, 2, 3) == 2 * (1000 // 64 + 7) * 2 * 3
-    assert capi.ss_attn_chunk_paged_units(1000, 7, 6, 2, 1) == 2 * (1000 // 84 + 7) * 2
-    assert capi.ss_attn_chunk_paged_units(10, 1, 258, 2, 1) == 0
+    assert capi.ss_attn_chunk_paged_units(1000, 7, 8, 2) == 2 * (1000 // 64 + 7) * 2
+    assert capi.ss_attn_chunk_paged_units(1000, 7, 6, 2) == 2 * (1000 // 84 + 7) * 2
+    assert capi.ss_attn_chunk_paged_units(10, 1, 258, 2) == 0
     assert capi.ss_pages_workspace_size(100, 7, 5) >= 4 * (3 * 100 + 2 * 5)
 
 

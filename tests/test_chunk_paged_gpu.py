@@ -57,7 +57,7 @@ def check(Hq, Hkv, d, n, L, *, causal=True, a=0.0, splits=1, seed=0, pad=0, stri
     room[:sum(n), :Hq * d] = q.view(sum(n), -1)
     qd = room.cuda()[:, :Hq * d].unflatten(1, (Hq, d))
     scale = d ** -0.5
-    units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv, splits)
+    units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv)
     o = guarded((T, Hq, d), BF, "cuda", 7.0)
     extra, bands = {}, [o]
     if debug:
@@ -86,32 +86,29 @@ def check(Hq, Hkv, d, n, L, *, causal=True, a=0.0, splits=1, seed=0, pad=0, stri
             _, _, c = chunk_reference(q[cul[b]:cul[b + 1]], k[b], v[b], L[b], scale, causal, a, splits)
             ln_lam = math.log(min(1.0, a / L[b])) if a > 0 and L[b] > 0 else -math.inf
             nT = tiles(L[b])
-            per = -(-nT // splits) if nT else 1
             keep = torch.ones(Hkv, blocks, nT, dtype=torch.bool)
             for h in range(Hkv):
                 for blk in range(blocks):
                     place, half, places = chunk_place(cul, b, blk, G, T, B)
-                    for s in range(splits):
-                        unit = ((s * Hkv + h) * places + place) * 2 + half
-                        seen_units[unit] = True
-                        for j in range(width):
-                            mine = s * per <= j < min(nT, (s + 1) * per) and not math.isnan(float(c[h, blk, j]))
-                            if not mine:
-                                assert mask[unit, j] == 2 and math.isnan(float(margin[unit, j]))
-                                continue
-                            stat, gpu = float(c[h, blk, j]), float(margin[unit, j])
-                            evaluated += 1
-                            skip = int(mask[unit, j]) == 1
-                            assert int(mask[unit, j]) in (0, 1)
-                            if math.isfinite(stat):
-                                assert abs(gpu - stat) <= 1e-3 + 1e-5 * abs(stat)  # fp32 scores of |s| < 64
-                            else:
-                                assert gpu == stat
-                            if abs(stat - ln_lam) > 1e-2:  # (elsewhere fp32 may decide otherwise)
-                                assert skip == (stat < ln_lam)
-                            keep[h, blk, j] = not skip
-                            skipped += skip
-                        assert int(counts[unit]) == int((mask[unit] == 1).sum())
+                    unit = (h * places + place) * 2 + half
+                    seen_units[unit] = True
+                    for j in range(width):
+                        if j >= nT or math.isnan(float(c[h, blk, j])):
+                            assert mask[unit, j] == 2 and math.isnan(float(margin[unit, j]))
+                            continue
+                        stat, gpu = float(c[h, blk, j]), float(margin[unit, j])
+                        evaluated += 1
+                        skip = int(mask[unit, j]) == 1
+                        assert int(mask[unit, j]) in (0, 1)
+                        if math.isfinite(stat):
+                            assert abs(gpu - stat) <= 1e-3 + 1e-5 * abs(stat)  # fp32 scores of |s| < 64
+                        else:
+                            assert gpu == stat
+                        if abs(stat - ln_lam) > 1e-2:  # (elsewhere fp32 may decide otherwise)
+                            assert skip == (stat < ln_lam)
+                        keep[h, blk, j] = not skip
+                        skipped += skip
+                    assert int(counts[unit]) == int((mask[unit] == 1).sum())
         o_ref, weight, _ = chunk_reference(q[cul[b]:cul[b + 1]], k[b], v[b], L[b], scale, causal, a, splits, keep)
         assert_attention(got[cul[b]:cul[b + 1]], o_ref, weight, f"sequence {b}")
     if debug:
