@@ -69,6 +69,12 @@ constexpr int kSoftWarps = 8;                 // two warpgroups of 4: alternate 
 constexpr int kGroupWarps = 4;                // one thread per query row
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kThreads = kSoftThreads + 128;  // + producers and issuers
+// Register split: launched at 168 per thread (384 x 168 = 64512); the softmax
+// warpgroups raise theirs to 208, the producers' and issuers' drops to 88
+// (2 x 128 x 208 + 128 x 88 = 64512).
+constexpr int kLaunchRegs = 168;
+constexpr int kRegsUp = 200, kRegsDown = 104;
+static_assert(256 * kRegsUp + 128 * kRegsDown <= kThreads * kLaunchRegs, "register split");
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpPV = 11;
 constexpr int kNB = 3;  // score buffers
 constexpr uint32_t kFlagKept = 1u, kFlagRescale = 2u;
@@ -359,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return (page >= 0 && page < p.num_pages ? page : p.num_pages) * p.Hkv + u.kvh;
   };
 
+  if (warp >= kSoftWarps) setmaxnreg_dec<kRegsDown>();
   // Counters that every role keeps alike: tc, tiles before this unit; uc, units with tiles before it.
   if (warp == kWarpK) {
     // ------------------------------------------------------------ units, Q, K producer
@@ -608,6 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // wait gives up at once), so all threads take the same sequence of named
     // barriers; at the start of the next one the failure is agreed on and all
     // leave together.
+    setmaxnreg_inc<kRegsUp>();
     const int g = warp / kGroupWarps, q4 = warp % kGroupWarps;
     const int row = q4 * 32 + lane;  // TMEM lane
     const int gtid = tid - 128 * g;  // thread index within the warpgroup
@@ -973,6 +981,13 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
                          const ChunkParams& p, cudaStream_t st) {
   using C = PairCfg<D, 128>;
   auto* fn = chunk_paged_kernel<D, 128, D, MODE>;
+  // With fewer registers at launch the softmax warpgroups' increase could
+  // never be satisfied: refuse to launch in that case.
+  static const int launch_regs = [fn] {
+    cudaFuncAttributes attr{};
+    return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : -1;
+  }();
+  if (launch_regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   // One cluster per unit; those that are not launched yet are taken over by running ones.
