@@ -40,9 +40,11 @@
 // K / V rings live on: the producers load the next unit's first tiles, and the
 // score issuer starts on them, while the softmax of the last unit's tail and
 // its epilogue run.
-//   Producer warp 8 of CTA 0 asks for the next unit one unit ahead and passes
-//   its number to CTA 1; warp 8 of each CTA works out the unit's geometry
-//   (sequence, lengths, tiles) and publishes it to the CTA's other warps.
+//   Producer warp 8 of CTA 0 asks for the next unit when it issues the last
+//   loads of one; the answer comes to both CTAs, and warp 8 of each works out
+//   the unit's geometry (sequence, lengths, tiles) and publishes it to the
+//   CTA's other warps.  The warpgroup with a unit's last tile writes its
+//   output; the other goes on with the next unit's first tile.
 //
 // Few rows and a long cache: the tiles are dealt to S parts whose states (m,
 // l, O) a second kernel merges in fp32.  The ranges of the vote (num_kv_splits:
@@ -94,20 +96,20 @@ __device__ __forceinline__ void order_after(uint32_t* done, uint32_t* next) {
 
 template <int DQK, int DV>
 struct PairCfg {
-  static_assert(DQK % 64 == 0 && DQK >= 64 && DQK <= 192, "key width");
+  static_assert(DQK == 64 || DQK == 128, "key width");
   static_assert(DV == 128, "value width: O occupies TMEM columns 384..511");
   static constexpr int kChunksQ = DQK / 64;             // 128-byte swizzle chunks per row
   static constexpr int kQBytes = kTile * DQK * 2;        // room of this CTA's row block
   static constexpr int kKHalfBytes = 64 * DQK * 2;      // 64 keys of a tile
   static constexpr int kKChunk = 64 * 128;               // one 64-column chunk of 64 keys
   static constexpr int kVHalfBytes = kTile * 64 * 2;    // 64 value columns of a tile
-  static constexpr int kNK = (DQK <= 128) ? 6 : 4;       // K ring slots
-  static constexpr int kNV = (DQK <= 128) ? 5 : 4;       // V ring slots
-  static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQOff + kQBytes;
+  static constexpr int kNK = 4;                          // K ring slots
+  static constexpr int kNV = 5;                          // V ring slots
+  static constexpr int kQOff = 0;                        // two row blocks: this unit's, the next one's
+  static constexpr int kKOff = kQOff + 2 * kQBytes;
   static constexpr int kVOff = kKOff + kNK * kKHalfBytes;
   static constexpr int kCtlOff = kVOff + kNV * kVHalfBytes;
-  static constexpr int kCtlBytes = 8192;
+  static constexpr int kCtlBytes = 11264;
   static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 384;
@@ -129,8 +131,8 @@ struct Unit {
 
 template <int NK, int NV>
 struct PairCtl {
-  uint64_t q_full;             // leader: both Q blocks landed
-  uint64_t q_empty;            // each CTA: the unit's score MMAs are done, Q may be refilled
+  uint64_t q_full[2];          // leader: both Q blocks landed
+  uint64_t q_empty[2];         // each CTA: the unit's score MMAs are done, Q may be refilled
   uint64_t k_full[NK];         // leader: both K halves of a ring entry landed
   uint64_t v_full[NV];         // leader: both V halves landed
   uint64_t k_empty[NK];        // each CTA: its K slot may be refilled
@@ -142,25 +144,26 @@ struct PairCtl {
   uint64_t rescaled[2][kSoftWarps];  // leader: (CTA, warp) has rescaled its part of O
   uint64_t s_free[kNB];        // leader: the buffer's P.V is issued (or not needed)
   uint64_t o_full;             // each CTA: the unit's last P.V is done
-  uint64_t o_free;             // leader: both CTAs' 8 warps have read the unit's O
+  uint64_t o_free;             // leader: the unit's O has been read (4 warps of each CTA)
+  uint64_t handed[4];          // each CTA, per tile % 4: the rows' state after the tile is in `hand`
+  uint64_t summed[4];          // each CTA, per unit % 4: the other warpgroup's share is in `fin`
   uint64_t mma_done[2];        // leader: teardown, per issuer
   uint64_t unit_full[2];       // each CTA: a unit's geometry is published
   uint64_t unit_empty[2];      // each CTA: the other 11 warps have read it
-  uint64_t next_full;          // leader: the answer to a request for a unit; CTA 1: its number
-  uint64_t next_empty;         // leader: CTA 1 has read the number
-  alignas(16) uint32_t answer[4];                     // leader: cluster launch control's
+  uint64_t next_full;          // each CTA: the answer to the request for a unit
+  uint64_t next_empty;         // leader: both CTAs have read it
+  alignas(16) uint32_t answer[4];                     // cluster launch control's
   alignas(16) uint32_t flags[kNB][kGroupWarps];       // leader: per buffer and warp of the
                                                       // tile's warpgroup, kFlagKept | kFlagRescale
   alignas(16) uint32_t peer_flags[kNB][kGroupWarps];  // leader: the same for CTA 1's warps
-  uint32_t o_note[kSoftWarps]; // leader: written by CTA 1's warps to complete bytes on o_free
-  uint32_t next_unit;          // CTA 1: the next unit's number + 1 (0: none)
+  uint32_t o_note[kGroupWarps];  // leader: written by CTA 1's warps to complete bytes on o_free
   uint32_t tmem_base;
   int abort_flag;
   Unit unit[2];
-  uint32_t skipped[2];         // per warpgroup: tiles it skipped
+  uint32_t skipped[4];         // per unit % 4: tiles that the warpgroup without the last tile skipped
   float red[2][kGroupWarps];   // per warpgroup and warp: largest vote statistic of a tile
-  float2 hand[kTile];          // per row: (m, m_ref) after the last tile, passed between warpgroups
-  float2 fin[2][kTile];        // per warpgroup and row: (m_ref, l) at the end
+  float2 hand[4][kTile];       // per tile % 4 and row: (m, m_ref) after the tile
+  float2 fin[4][kTile];        // per unit % 4 and row: (m_ref, l) of the warpgroup without the last tile
 };
 
 // 4-D tiled TMA load of a row block: (d, head of the group, KV head, token).
@@ -174,30 +177,49 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// The sequence whose pairs include place `slot` (see chunk_slots): the last b
-// with floor(cu[b] / pair) + b <= slot, 32 candidates a step.  Executed by
-// whole warps.
-__device__ __forceinline__ int sequence_of_slot(const int32_t* cu, int B, int pair, int slot) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;
+// The batch's sequences as a warp sees them: a window of 32, one a lane, kept
+// from unit to unit (batches of up to 32 sequences are read once).
+struct Window {
+  int base = -32;      // sequence of lane 0
+  int start, cu0, cu1, len;  // this lane's: first place (see chunk_slots), tokens, keys
+};
+
+// The sequence whose pairs include place `slot`: the last b with floor(cu[b] /
+// pair) + b <= slot.  Moves the window to it if it is elsewhere, 32 candidates
+// a step.  Executed by whole warps.
+__device__ __forceinline__ int sequence_of_slot(Window& w, const ChunkParams& p, int slot) {
+  const int lane = threadIdx.x & 31, pair = 2 * p.tpb;
   while (true) {
-    const int stride = (n + 31) / 32;
-    const int b = lo + lane * stride;
-    const bool in = b < lo + n && __ldg(cu + b) / pair + b <= slot;
-    const int c = __popc(__ballot_sync(0xffffffffu, in));
-    const int end = lo + n;
-    if (c > 0) lo += (c - 1) * stride;
-    if (stride == 1) return lo;
-    n = min(stride, end - lo);
+    if (w.base >= 0) {
+      const int c = __popc(__ballot_sync(0xffffffffu, w.base + lane < p.B && w.start <= slot));
+      if ((c > 0 || w.base == 0) && (c < 32 || w.base + 32 >= p.B)) return w.base + max(0, c - 1);
+    }
+    int lo = 0, n = p.B;  // candidates lo .. lo + n - 1
+    while (n > 32) {
+      const int stride = (n + 31) / 32, b = lo + lane * stride;
+      const int c = __popc(__ballot_sync(0xffffffffu, b < lo + n && __ldg(p.cu_seqlens + b) / pair + b <= slot));
+      const int end = lo + n;
+      lo += max(0, c - 1) * stride;
+      n = min(stride, end - lo);
+    }
+    w.base = lo;
+    const int b = min(lo + lane, p.B - 1);
+    w.cu0 = __ldg(p.cu_seqlens + b);
+    w.cu1 = __ldg(p.cu_seqlens + b + 1);
+    w.len = __ldg(p.seq_lens + b);
+    w.start = w.cu0 / pair + b;
+    const int c = __popc(__ballot_sync(0xffffffffu, lo + lane < p.B && w.start <= slot));
+    return min(lo + max(0, c - 1), p.B - 1);
   }
 }
 
 // Cluster launch control: ask the hardware for a cluster of this grid that has
-// not been launched.  The answer (16 bytes) lands in shared memory and
-// completes 16 bytes on `bar`.
+// not been launched.  The answer (16 bytes) lands in the shared memory of both
+// CTAs and completes 16 bytes on the barrier of each.
 __device__ __forceinline__ void request_cluster(void* answer, uint64_t* bar) {
   asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all"
+      ".b128 [%0], [%1];" ::"r"(
           smem_u32(answer)),
       "r"(smem_u32(bar))
       : "memory");
@@ -251,18 +273,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // The geometry of unit number x (a whole warp; every lane returns it).
   // Later pairs of a sequence (with a causal mask: the longer) come first.
-  auto geometry = [&](int x) -> Unit {
+  auto geometry = [&](Window& w, int x) -> Unit {
     Unit u;
     const int sk = x / p.slots;  // part * Hkv + KV head
     const int slot = p.slots - 1 - (x - sk * p.slots);
     u.part = sk / p.Hkv;
     u.kvh = sk - u.part * p.Hkv;
     u.id = (u.kvh * p.slots + slot) * 2 + static_cast<int>(rank);
-    const int b = sequence_of_slot(p.cu_seqlens, p.B, 2 * p.tpb, slot);
+    const int b = sequence_of_slot(w, p, slot);
     u.b = b;
-    const int tok0 = max(0, min(__ldg(p.cu_seqlens + b), p.T));  // the sequence's new tokens
-    const int n_new = max(0, min(__ldg(p.cu_seqlens + b + 1), p.T) - tok0);
-    const int len = max(0, min(__ldg(p.seq_lens + b), p.max_pages * kTile));
+    const int cu0 = __shfl_sync(0xffffffffu, w.cu0, b - w.base), cu1 = __shfl_sync(0xffffffffu, w.cu1, b - w.base);
+    const int tok0 = max(0, min(cu0, p.T));  // the sequence's new tokens
+    const int n_new = max(0, min(cu1, p.T) - tok0);
+    const int len = max(0, min(__shfl_sync(0xffffffffu, w.len, b - w.base), p.max_pages * kTile));
     const int pr = slot - (tok0 / (2 * p.tpb) + b);
     const int off = len - n_new;  // (causal) new token i sees keys up to off + i
     const int nT = (len + kTile - 1) / kTile;
@@ -299,8 +322,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   if (tid == 0) {
-    mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 1);
     for (int s = 0; s < NK; ++s) {
       mbar_init(&ctl->k_full[s], 1);
       mbar_init(&ctl->k_empty[s], 1);
@@ -322,15 +343,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->rescaled[1][w], 1);
     }
     mbar_init(&ctl->o_full, 1);
-    mbar_init(&ctl->o_free, kSoftWarps + 1);  // likewise, with 32 bytes from CTA 1
+    mbar_init(&ctl->o_free, kGroupWarps + 1);  // likewise, with 16 bytes from CTA 1
     mbar_init(&ctl->mma_done[0], 1);
     mbar_init(&ctl->mma_done[1], 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&ctl->handed[s], kGroupWarps);
+      mbar_init(&ctl->summed[s], kGroupWarps);
+    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->unit_full[s], 1);
       mbar_init(&ctl->unit_empty[s], kThreads / 32 - 1);
     }
     mbar_init(&ctl->next_full, 1);
-    mbar_init(&ctl->next_empty, 1);
+    mbar_init(&ctl->next_empty, 2);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -373,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
     }
-    const uint32_t qbar = lead(&ctl->q_full);
+    Window w;
     int x = blockIdx.x >> 1;
     uint32_t tc = 0, uc = 0;
     for (int i = 0;; ++i) {
@@ -381,27 +408,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!wwait(&ctl->unit_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
       Unit u;
       u.id = -1;
-      if (x >= 0) u = geometry(x);
+      if (x >= 0) u = geometry(w, x);
       if (lane == 0) {
         ctl->unit[i & 1] = u;
         mbar_arrive(&ctl->unit_full[i & 1]);
       }
       __syncwarp();
       if (x < 0) break;
-      if (leader && lane == 0) {  // ask for the next unit
-        mbar_arrive_expect_tx(&ctl->next_full, 16);
-        request_cluster(ctl->answer, &ctl->next_full);
-      }
       bool ok = true;
-      // Q goes in once the last unit's score MMAs are done; until then the
-      // first tiles' K fill the ring.
-      const int q_at = uc == 0 ? 0 : min(u.n_pair, NK) - 1;
+      if (u.n_pair > 0) {
+        const uint32_t qs = uc & 1;
+        ok = wwait(&ctl->q_empty[qs], ((uc >> 1) & 1) ^ 1);
+        if (ok && lane == 0) {
+          if (leader) mbar_arrive_expect_tx(&ctl->q_full[qs], 2 * C::kChunksQ * (p.tpb * p.G * 128));
+          const uint32_t qbar = lead(&ctl->q_full[qs]);
+#pragma unroll
+          for (int c = 0; c < C::kChunksQ; ++c)
+            tma_load_4d_pair(sQ + qs * C::kQBytes + c * (kTile * 128), &tmQ, qbar, c * 64, 0, u.kvh, u.tok);
+        }
+        ++uc;
+      }
+      // The next unit is asked for when the last tiles' loads of this one go
+      // out, not before: a cluster that is far from done must not take what an
+      // idle one could.  CTA 1 has read the last answer (next_empty).
+      const int ask_at = max(0, u.n_pair - NK);
       int z = 0;
-      for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
+      for (int jj = 0; ok && jj <= u.n_pair; ++jj) {
+        if (jj == ask_at) {
+          if (leader) ok = wwait(&ctl->next_empty, (i & 1) ^ 1);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&ctl->next_full, 16);
+            if (leader) request_cluster(ctl->answer, &ctl->next_full);
+          }
+          __syncwarp();
+        }
+        if (jj == u.n_pair) break;
         if ((jj & 31) == 0) z = pages32(u, jj);
         const int zt = __shfl_sync(0xffffffffu, z, jj & 31);
         const uint32_t s = tc % NK;
-        ok = wwait(&ctl->k_empty[s], ((tc / NK) & 1) ^ 1);
+        if (ok) ok = wwait(&ctl->k_empty[s], ((tc / NK) & 1) ^ 1);
         if (!ok) break;
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(&ctl->k_full[s], 2 * C::kKHalfBytes);
@@ -411,38 +456,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < C::kChunksQ; ++c)
             tma_load_3d_pair(sK + s * C::kKHalfBytes + c * C::kKChunk, &tmK, kbar, c * 64, y, zt);
         }
-        if (jj == q_at) {
-          ok = wwait(&ctl->q_empty, (uc & 1) ^ 1);
-          if (ok && lane == 0) {
-            if (leader) mbar_arrive_expect_tx(&ctl->q_full, 2 * C::kChunksQ * (p.tpb * p.G * 128));
-#pragma unroll
-            for (int c = 0; c < C::kChunksQ; ++c)
-              tma_load_4d_pair(sQ + c * (kTile * 128), &tmQ, qbar, c * 64, 0, u.kvh, u.tok);
-          }
-        }
+        ++tc;
       }
-      if (u.n_pair > 0) ++uc;
-      // The next unit's number.  (The answer is awaited even after a failed
-      // wait: it must not land after this CTA has left.)
-      int next = -1;
-      if (leader) {
-        const bool answered = wwait(&ctl->next_full, i & 1);
-        if (answered) next = requested_block(ctl->answer);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next one lands
-        next = next >= 0 ? next >> 1 : -1;
-        if (!(ok && answered)) break;
-        if (!wwait(&ctl->next_empty, (i & 1) ^ 1)) break;
-        if (lane == 0)
-          st_async_u32(map_shared(smem_u32(&ctl->next_unit), 1u), static_cast<uint32_t>(next + 1),
-                       map_shared(smem_u32(&ctl->next_full), 1u));
-      } else {
-        if (lane == 0) mbar_arrive_expect_tx(&ctl->next_full, 4);
-        if (!(ok && wwait(&ctl->next_full, i & 1))) break;
-        next = static_cast<int>(*reinterpret_cast<volatile uint32_t*>(&ctl->next_unit)) - 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_shared(smem_u32(&ctl->next_empty), 0u));
+      if (!ok) break;
+      if (!wwait(&ctl->next_full, i & 1)) break;
+      x = requested_block(ctl->answer);
+      x = x >= 0 ? x >> 1 : -1;
+      __syncwarp();
+      if (lane == 0) {  // read before the next answer lands
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (leader)
+          mbar_arrive(&ctl->next_empty);
+        else
+          mbar_arrive_cluster(map_shared(smem_u32(&ctl->next_empty), 0u));
       }
-      x = next;
     }
     __syncwarp();
   } else if (warp == kWarpV) {
@@ -477,7 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; ok && next_unit(i, &u); ++i) {
       if (!leader || u.n_pair == 0) continue;
       if (lane == 0) {
-        ok = wait(&ctl->q_full, uc & 1);
+        ok = wait(&ctl->q_full[uc & 1], (uc >> 1) & 1);
+        const uint64_t dqu = dq + (((uc & 1) * C::kQBytes) >> 4);
         for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
           const uint32_t bsel = tc % kNB;
           // The buffer's previous tile has been decided by both blocks and its
@@ -492,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < DQK / 16; ++kk) {
             const uint32_t qoff = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
             const uint32_t koff = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
-            mma2_bf16_ss(tmem + col, dq + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
+            mma2_bf16_ss(tmem + col, dqu + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
           }
           mma2_commit_mc(&ctl->s_full[bsel], 3);
           mma2_commit_mc(&ctl->k_empty[s], 3);
@@ -500,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // arrival sets that count for the tile's phase.
           mbar_arrive_expect_tx(&ctl->dec[bsel], 4 * kGroupWarps);
         }
-        if (ok) mma2_commit_mc(&ctl->q_empty, 3);
+        if (ok) mma2_commit_mc(&ctl->q_empty[uc & 1], 3);
       }
       ++uc;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -524,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         // O is read by the last unit's epilogue (of CTA 1's warps: as bytes).
         if (uc > 0) ok = wait(&ctl->o_free, (uc - 1) & 1);
-        mbar_arrive_expect_tx(&ctl->o_free, 4 * kSoftWarps);
+        mbar_arrive_expect_tx(&ctl->o_free, 4 * kGroupWarps);
         uint32_t o_acc = 0u;
         for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
           const uint32_t bsel = tc % kNB;
@@ -534,8 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t vs = tc % NV;
           if (!(ok = wait(&ctl->v_full[vs], (tc / NV) & 1))) break;
           if (!(ok = wait(&ctl->dec[bsel], ph))) break;
-          // The tile's decisions come from the warps of warpgroup jj % 2.
-          const int wg0 = kGroupWarps * (jj & 1);
+          // The tile's decisions come from the warps of warpgroup tc % 2.
+          const int wg0 = kGroupWarps * (tc & 1);
           uint32_t resc = 0u, any_kept = 0u;  // resc: bit (kGroupWarps * r + w)
           {
             // (plain loads: the barrier waits above are compiler memory barriers)
@@ -600,21 +628,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax / vote
-    // Two warpgroups take alternate tiles of a unit: warpgroup g = warp / 4 the
-    // tiles jj with jj % 2 == g, one thread per row (warp w reads TMEM lanes
-    // 32 (w % 4) .. + 31) over all 128 score columns, loaded as two halves of
-    // 64.  A row's running state passes from one warpgroup to the other once
-    // per tile: the warpgroup on tile jj - 1 writes the running maximum m of the
-    // vote and the reference maximum m_ref of P to shared memory and arrives on
-    // a named barrier, and the warpgroup on tile jj completes that barrier
-    // before its vote (one barrier per direction, so an arrival can only
-    // complete the hand-over it is meant for).  Each warpgroup sums its own
-    // tiles' P into l against the m_ref it last saw; a moved m_ref rescales
-    // that sum when the state arrives, and the two sums meet at the end.  After
-    // a failed wait a thread carries on to the end of the unit (every later
-    // wait gives up at once), so all threads take the same sequence of named
-    // barriers; at the start of the next one the failure is agreed on and all
-    // leave together.
+    // Two warpgroups take alternate tiles: warpgroup g = warp / 4 those with an
+    // even / odd number over all units, one thread per row (warp w reads TMEM
+    // lanes 32 (w % 4) .. + 31) over all 128 score columns, loaded as two
+    // halves of 64.  Within a unit a row's running state passes from one
+    // warpgroup to the other once per tile: the warpgroup on a tile writes the
+    // running maximum m of the vote and the reference maximum m_ref of P to
+    // shared memory and its warps arrive on a barrier, which the other
+    // completes before its next vote.  Each warpgroup sums its own tiles' P
+    // into l against the m_ref it last saw; a moved m_ref rescales that sum
+    // when the state arrives.  The warpgroup with the unit's last tile adds the
+    // other's sum (`fin`) and writes the output, while the other is already at
+    // the next unit's first tile.  How far one may run ahead of the other is
+    // bounded by the three score buffers and the one O: tile t + 4 needs the
+    // buffer of t + 1, whose P.V waits for the O of t's unit to be read.  So
+    // four slots of each shared array are enough.
+    // Threads leave together per warpgroup (agreed on at the start of a unit);
+    // all waits on the other warpgroup are bounded.
     setmaxnreg_inc<kRegsUp>();
     const int g = warp / kGroupWarps, q4 = warp % kGroupWarps;
     const int row = q4 * 32 + lane;  // TMEM lane
@@ -624,23 +654,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t colO = lane_base + C::kColO;
     const float sl2 = p.scale_log2;
     uint32_t n_drain = 0;
-    constexpr uint32_t kBar = 2;               // named barrier of all softmax threads
-    const uint32_t bar_give = 3 + g;           // hand-over from this warpgroup
-    const uint32_t bar_take = 3 + (g ^ 1);     // hand-over to this warpgroup
     const uint32_t bar_vote = 5 + g;           // the 128 threads of this warpgroup
     uint32_t tc = 0, uc = 0;
     Unit u;
     bool ok = true;
     for (int i = 0;; ++i) {
       const bool have = next_unit(i, &u);
-      if (named_bar_or(kBar, kSoftThreads, !(ok && have))) break;
+      if (named_bar_or(bar_vote, 128, !(ok && have))) break;
       const bool row_valid = tok < u.toks;
-      // last key index this row may see
-      const int lim = row_valid ? min(u.last * kTile + kTile - 1 - u.last_shift, u.lim0 + tok) : -1;
+      // Last key index this row may see.  A row without a token is not masked:
+      // it takes no part in the vote, and nothing of it is kept.
+      const int lim = row_valid ? min(u.last * kTile + kTile - 1 - u.last_shift, u.lim0 + tok) : 0x3fffffff;
       const long unit_row = static_cast<long>(u.id) * p.max_pages;
       float m_true = -INFINITY, m_ref = -INFINITY, l = 0.f;
       uint32_t skipped = 0;
-      int in_range = g;  // tile jj's place in its range of the vote
+      const int jj0 = (g ^ tc) & 1;                                 // this warpgroup's first tile
+      const bool owner = ((tc + max(u.n_pair, 1) - 1) & 1) == g;    // it has the last one
+      int in_range = jj0;  // tile jj's place in its range of the vote
       if (kVote)
         while (in_range >= u.range) in_range -= u.range;
 
@@ -688,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return f32x2_lo(lsum) + f32x2_hi(lsum);
       };
 
-      for (int jj = g; jj < u.n_pair; jj += 2) {
+      for (int jj = jj0; jj < u.n_pair; jj += 2) {
         const int j = u.j0 + jj;  // tile of the sequence
         const uint32_t t = tc + jj, bsel = t % kNB;
         const uint32_t colS = lane_base + 128u * bsel;
@@ -703,11 +733,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // that only one half of the scores is ever held in registers)
           asm volatile("" : "+f"(tmax));
           tmax = fmaxf(tmax, load_half(colS, j, 1, sr));  // sr keeps the second half
+          if (!row_valid) tmax = -INFINITY;
         }
         // The state after the previous tile, from the other warpgroup.
         if (jj > 0) {
-          named_bar_sync(bar_take, kSoftThreads);
-          const float2 hs = ctl->hand[row];
+          if (!wwait(&ctl->handed[(t - 1) & 3], ((t - 1) >> 2) & 1)) ok = false;
+          const float2 hs = ctl->hand[(t - 1) & 3][row];
           m_true = hs.x;
           if (hs.y != m_ref) {
             if (m_ref != -INFINITY) l *= ex2_approx((m_ref - hs.y) * sl2);
@@ -765,10 +796,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (jj + 1 < u.n_pair) {
-          ctl->hand[row] = make_float2(m_true, m_ref);
-          named_bar_arrive(bar_give, kSoftThreads);
-        }
+        ctl->hand[t & 3][row] = make_float2(m_true, m_ref);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->handed[t & 3]);
         // P of columns 64 hf .. as bf16 pairs over the first 32 of those score
         // columns; the second half goes first, from the registers, then the
         // first half is loaded again.  A skipped or unseen tile writes zeros
@@ -829,76 +859,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc += u.n_pair;
 
-      // The row's denominator: both warpgroups' sums against the later m_ref
-      // (the one O is kept against).
-      ctl->fin[g][row] = make_float2(m_ref, l);
-      if (gtid == 0) ctl->skipped[g] = skipped;
-      named_bar_sync(kBar, kSoftThreads);
-      const float2 other = ctl->fin[g ^ 1][row];
-      const float m_fin = fmaxf(m_ref, other.x);
-      float l_row = 0.f;
-      if (m_fin != -INFINITY) {
-        if (m_ref != -INFINITY) l_row += l * ex2_approx((m_ref - m_fin) * sl2);
-        if (other.x != -INFINITY) l_row += other.y * ex2_approx((other.x - m_fin) * sl2);
+      const uint32_t fs = uc & 3;
+      if (!owner) {
+        if (u.n_pair > 0) {
+          ctl->fin[fs][row] = make_float2(m_ref, l);
+          if (gtid == 0) ctl->skipped[fs] = skipped;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->summed[fs]);
+          ++uc;
+        }
+        continue;
       }
+      // The row's denominator: both warpgroups' sums against m_ref, the one O
+      // is kept against (this warpgroup has it from the last tile).
+      float l_row = l;
       if (u.n_pair > 0) {
+        if (!wwait(&ctl->summed[fs], (uc >> 2) & 1)) ok = false;
+        const float2 other = ctl->fin[fs][row];
+        if (other.x != -INFINITY) l_row += other.y * ex2_approx((other.x - m_ref) * sl2);
         if (!wwait(&ctl->o_full, uc & 1)) ok = false;
         ++uc;
         tc_fence_after();
       }
 
-      // Epilogue: this warpgroup's half of the row's O: as O / l in bf16 (a row
-      // that saw no key writes zeros), or of a part as it is, in fp32.
+      // Epilogue: the rows' O as O / l in bf16 (a row that saw no key writes
+      // zeros), or of a part as it is, in fp32.
+      const bool writes = ok && row_valid;
       const size_t orow = static_cast<size_t>(u.tok + tok) * p.Hq + u.kvh * p.G + head;
       const size_t rows = static_cast<size_t>(p.T) * p.Hq;
-      const bool reads = ok && u.toks > 0 && g * (DV / 2) < DVO;
-      if (reads && row_valid && g == 0 && p.parts > 1)
-        p.part_ml[u.part * rows + orow] = make_float2(m_fin * sl2, l_row);
+      if (writes && p.parts > 1) p.part_ml[u.part * rows + orow] = make_float2(m_ref * sl2, l_row);
       const float inv_l = (l_row > 0.f) ? 1.f / l_row : 0.f;
-      uint32_t orr[64];
-      if (reads && u.n_pair > 0) {
-        tmem_ld32p(colO + g * (DV / 2), orr);
-        tmem_ld32p(colO + g * (DV / 2) + 32, orr + 32);
-        tmem_wait_ld();
-      } else {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) orr[e] = 0u;
-      }
-      if (u.n_pair > 0) {  // O may be overwritten
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader)
-            mbar_arrive(&ctl->o_free);
-          else
-            st_async_u32(map_shared(smem_u32(&ctl->o_note[warp]), 0u), 0u, lead(&ctl->o_free));
-        }
-      }
-      if (reads && row_valid) {
-        if (p.parts > 1) {
-          if (l_row > 0.f) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (u.part * rows + orow) * DVO + g * (DV / 2));
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              dst[e] = make_float4(__uint_as_float(orr[4 * e]), __uint_as_float(orr[4 * e + 1]),
-                                   __uint_as_float(orr[4 * e + 2]), __uint_as_float(orr[4 * e + 3]));
-          }
+      for (int c = 0; c < DVO / 64; ++c) {
+        uint32_t orr[64];
+        if (u.n_pair > 0) {
+          tmem_ld32p(colO + c * 64, orr);
+          tmem_ld32p(colO + c * 64 + 32, orr + 32);
+          tmem_wait_ld();
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + orow * DVO + g * (DV / 2));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint32_t w[4];
+          for (int e = 0; e < 64; ++e) orr[e] = 0u;
+        }
+        if (u.n_pair > 0 && c == DVO / 64 - 1) {  // O may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(&ctl->o_free);
+            else
+              st_async_u32(map_shared(smem_u32(&ctl->o_note[q4]), 0u), 0u, lead(&ctl->o_free));
+          }
+        }
+        if (writes) {
+          if (p.parts > 1) {
+            if (l_row > 0.f) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (u.part * rows + orow) * DVO + c * 64);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(orr[8 * e + 2 * k]) * inv_l,
-                                 __uint_as_float(orr[8 * e + 2 * k + 1]) * inv_l);
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 16; ++e)
+                dst[e] = make_float4(__uint_as_float(orr[4 * e]), __uint_as_float(orr[4 * e + 1]),
+                                     __uint_as_float(orr[4 * e + 2]), __uint_as_float(orr[4 * e + 3]));
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + orow * DVO + c * 64);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                v[k] = pack_bf16x2(__uint_as_float(orr[8 * e + 2 * k]) * inv_l,
+                                   __uint_as_float(orr[8 * e + 2 * k + 1]) * inv_l);
+              dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
         }
       }
       // Debug outputs: the unit's count, and the tiles that it does not see.
-      if (kVote && tid == 0 && p.counts != nullptr) {
-        const uint32_t n = ctl->skipped[0] + ctl->skipped[1];
+      if (kVote && gtid == 0 && p.counts != nullptr) {
+        const uint32_t n = skipped + (u.n_pair > 0 ? ctl->skipped[fs] : 0u);
         if (p.parts == 1)
           p.counts[u.id] = n;
         else
@@ -906,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (p.mask != nullptr || p.margin != nullptr) {
         const int end = u.part == p.parts - 1 ? p.max_pages : u.j1;
-        for (int j = u.j0 + u.n_mine + tid; j < end; j += kSoftThreads) {
+        for (int j = u.j0 + u.n_mine + gtid; j < end; j += 128) {
           if (p.mask != nullptr) p.mask[unit_row + j] = 2;
           if (p.margin != nullptr) p.margin[unit_row + j] = NAN;
         }
