@@ -39,7 +39,7 @@ __host__ __device__ constexpr long chunk_slots(long T, long B, long tpb) {
 }
 
 // How many parts to deal the tiles of `pairs` pairs of row blocks (over all KV heads) to.
-int chunk_parts(long pairs, int S);
+int chunk_parts(long pairs, int S, int max_pages);
 
 cudaError_t launch_chunk_paged(int d, bool vote, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const ChunkParams& p, cudaStream_t st);

@@ -71,14 +71,17 @@ constexpr int kSoftWarps = 8;                 // two warpgroups of 4: alternate 
 constexpr int kGroupWarps = 4;                // one thread per query row
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kThreads = kSoftThreads + 128;  // + producers and issuers
-// Register split: launched at 168 per thread (384 x 168 = 64512); the softmax
-// warpgroups raise theirs to 208, the producers' and issuers' drops to 88
-// (2 x 128 x 208 + 128 x 88 = 64512).
+// Register split: launched at 168 per thread (384 x 168 = 64512), raised for
+// the softmax warpgroups and lowered for the producers and issuers.
 constexpr int kLaunchRegs = 168;
-constexpr int kRegsUp = 200, kRegsDown = 104;
-static_assert(256 * kRegsUp + 128 * kRegsDown <= kThreads * kLaunchRegs, "register split");
+template <Mode MODE>
+constexpr int kRegsDown = (MODE == Mode::kDense) ? 104 : 88;
+template <Mode MODE>
+constexpr int kRegsUp = (kThreads * kLaunchRegs - 128 * kRegsDown<MODE>) / 256;
+static_assert(kRegsUp<Mode::kDense> == 200 && kRegsUp<Mode::kSparse> == 208, "register split");
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpPV = 11;
 constexpr int kNB = 3;  // score buffers
+constexpr int kSeqs = 512;  // sequences whose offsets and lengths are kept in shared memory
 constexpr uint32_t kFlagKept = 1u, kFlagRescale = 2u;
 
 // Scheduling fence for registers: the 8 values `done` are complete before,
@@ -109,7 +112,7 @@ struct PairCfg {
   static constexpr int kKOff = kQOff + 2 * kQBytes;
   static constexpr int kVOff = kKOff + kNK * kKHalfBytes;
   static constexpr int kCtlOff = kVOff + kNV * kVHalfBytes;
-  static constexpr int kCtlBytes = 11264;
+  static constexpr int kCtlBytes = 15360;
   static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 384;
@@ -150,9 +153,9 @@ struct PairCtl {
   uint64_t mma_done[2];        // leader: teardown, per issuer
   uint64_t unit_full[2];       // each CTA: a unit's geometry is published
   uint64_t unit_empty[2];      // each CTA: the other 11 warps have read it
-  uint64_t next_full;          // each CTA: the answer to the request for a unit
-  uint64_t next_empty;         // leader: both CTAs have read it
-  alignas(16) uint32_t answer[4];                     // cluster launch control's
+  uint64_t next_full[2];       // each CTA: the answer to the request for a unit
+  uint64_t next_empty[2];      // leader: both CTAs have read it
+  alignas(16) uint32_t answer[2][4];                  // cluster launch control's
   alignas(16) uint32_t flags[kNB][kGroupWarps];       // leader: per buffer and warp of the
                                                       // tile's warpgroup, kFlagKept | kFlagRescale
   alignas(16) uint32_t peer_flags[kNB][kGroupWarps];  // leader: the same for CTA 1's warps
@@ -164,6 +167,7 @@ struct PairCtl {
   float red[2][kGroupWarps];   // per warpgroup and warp: largest vote statistic of a tile
   float2 hand[4][kTile];       // per tile % 4 and row: (m, m_ref) after the tile
   float2 fin[4][kTile];        // per unit % 4 and row: (m_ref, l) of the warpgroup without the last tile
+  int cu[kSeqs + 1], len[kSeqs];  // the batch's offsets and lengths (B <= kSeqs)
 };
 
 // 4-D tiled TMA load of a row block: (d, head of the group, KV head, token).
@@ -177,39 +181,18 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// The batch's sequences as a warp sees them: a window of 32, one a lane, kept
-// from unit to unit (batches of up to 32 sequences are read once).
-struct Window {
-  int base = -32;      // sequence of lane 0
-  int start, cu0, cu1, len;  // this lane's: first place (see chunk_slots), tokens, keys
-};
-
 // The sequence whose pairs include place `slot`: the last b with floor(cu[b] /
-// pair) + b <= slot.  Moves the window to it if it is elsewhere, 32 candidates
-// a step.  Executed by whole warps.
-__device__ __forceinline__ int sequence_of_slot(Window& w, const ChunkParams& p, int slot) {
-  const int lane = threadIdx.x & 31, pair = 2 * p.tpb;
+// pair) + b <= slot, 32 candidates a step.  Executed by whole warps.
+__device__ __forceinline__ int sequence_of_slot(const int* cu, int B, int pair, int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
   while (true) {
-    if (w.base >= 0) {
-      const int c = __popc(__ballot_sync(0xffffffffu, w.base + lane < p.B && w.start <= slot));
-      if ((c > 0 || w.base == 0) && (c < 32 || w.base + 32 >= p.B)) return w.base + max(0, c - 1);
-    }
-    int lo = 0, n = p.B;  // candidates lo .. lo + n - 1
-    while (n > 32) {
-      const int stride = (n + 31) / 32, b = lo + lane * stride;
-      const int c = __popc(__ballot_sync(0xffffffffu, b < lo + n && __ldg(p.cu_seqlens + b) / pair + b <= slot));
-      const int end = lo + n;
-      lo += max(0, c - 1) * stride;
-      n = min(stride, end - lo);
-    }
-    w.base = lo;
-    const int b = min(lo + lane, p.B - 1);
-    w.cu0 = __ldg(p.cu_seqlens + b);
-    w.cu1 = __ldg(p.cu_seqlens + b + 1);
-    w.len = __ldg(p.seq_lens + b);
-    w.start = w.cu0 / pair + b;
-    const int c = __popc(__ballot_sync(0xffffffffu, lo + lane < p.B && w.start <= slot));
-    return min(lo + max(0, c - 1), p.B - 1);
+    const int stride = (n + 31) / 32, b = lo + lane * stride;
+    const int c = __popc(__ballot_sync(0xffffffffu, b < lo + n && cu[b] / pair + b <= slot));
+    const int end = lo + n;
+    lo += max(0, c - 1) * stride;
+    if (stride == 1) return lo;
+    n = min(stride, end - lo);
   }
 }
 
@@ -273,19 +256,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // The geometry of unit number x (a whole warp; every lane returns it).
   // Later pairs of a sequence (with a causal mask: the longer) come first.
-  auto geometry = [&](Window& w, int x) -> Unit {
+  const int* cu = p.B <= kSeqs ? ctl->cu : p.cu_seqlens;
+  const int* lens = p.B <= kSeqs ? ctl->len : p.seq_lens;
+  auto geometry = [&](int x) -> Unit {
     Unit u;
     const int sk = x / p.slots;  // part * Hkv + KV head
     const int slot = p.slots - 1 - (x - sk * p.slots);
     u.part = sk / p.Hkv;
     u.kvh = sk - u.part * p.Hkv;
     u.id = (u.kvh * p.slots + slot) * 2 + static_cast<int>(rank);
-    const int b = sequence_of_slot(w, p, slot);
+    const int b = sequence_of_slot(cu, p.B, 2 * p.tpb, slot);
     u.b = b;
-    const int cu0 = __shfl_sync(0xffffffffu, w.cu0, b - w.base), cu1 = __shfl_sync(0xffffffffu, w.cu1, b - w.base);
-    const int tok0 = max(0, min(cu0, p.T));  // the sequence's new tokens
-    const int n_new = max(0, min(cu1, p.T) - tok0);
-    const int len = max(0, min(__shfl_sync(0xffffffffu, w.len, b - w.base), p.max_pages * kTile));
+    const int tok0 = max(0, min(cu[b], p.T));  // the sequence's new tokens
+    const int n_new = max(0, min(cu[b + 1], p.T) - tok0);
+    const int len = max(0, min(lens[b], p.max_pages * kTile));
     const int pr = slot - (tok0 / (2 * p.tpb) + b);
     const int off = len - n_new;  // (causal) new token i sees keys up to off + i
     const int nT = (len + kTile - 1) / kTile;
@@ -356,8 +340,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->unit_full[s], 1);
       mbar_init(&ctl->unit_empty[s], kThreads / 32 - 1);
     }
-    mbar_init(&ctl->next_full, 1);
-    mbar_init(&ctl->next_empty, 2);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->next_full[s], 1);
+      mbar_init(&ctl->next_empty[s], 2);
+    }
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -365,6 +351,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&ctl->tmem_base, C::kTmemCols);
     tmem_relinquish_pair();
   }
+  if (p.B <= kSeqs)
+    for (int i = tid; i <= p.B; i += kThreads) {
+      ctl->cu[i] = __ldg(p.cu_seqlens + i);
+      if (i < p.B) ctl->len[i] = __ldg(p.seq_lens + i);
+    }
   tc_fence_before();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
@@ -392,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return (page >= 0 && page < p.num_pages ? page : p.num_pages) * p.Hkv + u.kvh;
   };
 
-  if (warp >= kSoftWarps) setmaxnreg_dec<kRegsDown>();
+  if (warp >= kSoftWarps) setmaxnreg_dec<kRegsDown<MODE>>();
   // Counters that every role keeps alike: tc, tiles before this unit; uc, units with tiles before it.
   if (warp == kWarpK) {
     // ------------------------------------------------------------ units, Q, K producer
@@ -400,7 +391,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
     }
-    Window w;
     int x = blockIdx.x >> 1;
     uint32_t tc = 0, uc = 0;
     for (int i = 0;; ++i) {
@@ -408,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!wwait(&ctl->unit_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
       Unit u;
       u.id = -1;
-      if (x >= 0) u = geometry(w, x);
+      if (x >= 0) u = geometry(x);
       if (lane == 0) {
         ctl->unit[i & 1] = u;
         mbar_arrive(&ctl->unit_full[i & 1]);
@@ -416,6 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (x < 0) break;
       bool ok = true;
+      int z = pages32(u, 0);
       if (u.n_pair > 0) {
         const uint32_t qs = uc & 1;
         ok = wwait(&ctl->q_empty[qs], ((uc >> 1) & 1) ^ 1);
@@ -430,20 +421,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // The next unit is asked for when the last tiles' loads of this one go
       // out, not before: a cluster that is far from done must not take what an
-      // idle one could.  CTA 1 has read the last answer (next_empty).
+      // idle one could.  Both CTAs have read the answer before the last
+      // (next_empty).
       const int ask_at = max(0, u.n_pair - NK);
-      int z = 0;
       for (int jj = 0; ok && jj <= u.n_pair; ++jj) {
         if (jj == ask_at) {
-          if (leader) ok = wwait(&ctl->next_empty, (i & 1) ^ 1);
+          if (leader) ok = wwait(&ctl->next_empty[i & 1], ((i >> 1) & 1) ^ 1);
           if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&ctl->next_full, 16);
-            if (leader) request_cluster(ctl->answer, &ctl->next_full);
+            mbar_arrive_expect_tx(&ctl->next_full[i & 1], 16);
+            if (leader) request_cluster(ctl->answer[i & 1], &ctl->next_full[i & 1]);
           }
           __syncwarp();
         }
         if (jj == u.n_pair) break;
-        if ((jj & 31) == 0) z = pages32(u, jj);
+        if ((jj & 31) == 0 && jj > 0) z = pages32(u, jj);
         const int zt = __shfl_sync(0xffffffffu, z, jj & 31);
         const uint32_t s = tc % NK;
         if (ok) ok = wwait(&ctl->k_empty[s], ((tc / NK) & 1) ^ 1);
@@ -459,16 +450,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++tc;
       }
       if (!ok) break;
-      if (!wwait(&ctl->next_full, i & 1)) break;
-      x = requested_block(ctl->answer);
+      if (!wwait(&ctl->next_full[i & 1], (i >> 1) & 1)) break;
+      x = requested_block(ctl->answer[i & 1]);
       x = x >= 0 ? x >> 1 : -1;
       __syncwarp();
       if (lane == 0) {  // read before the next answer lands
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (leader)
-          mbar_arrive(&ctl->next_empty);
+          mbar_arrive(&ctl->next_empty[i & 1]);
         else
-          mbar_arrive_cluster(map_shared(smem_u32(&ctl->next_empty), 0u));
+          mbar_arrive_cluster(map_shared(smem_u32(&ctl->next_empty[i & 1]), 0u));
       }
     }
     __syncwarp();
@@ -645,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // four slots of each shared array are enough.
     // Threads leave together per warpgroup (agreed on at the start of a unit);
     // all waits on the other warpgroup are bounded.
-    setmaxnreg_inc<kRegsUp>();
+    setmaxnreg_inc<kRegsUp<MODE>>();
     const int g = warp / kGroupWarps, q4 = warp % kGroupWarps;
     const int row = q4 * 32 + lane;  // TMEM lane
     const int gtid = tid - 128 * g;  // thread index within the warpgroup
@@ -728,11 +719,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t sr[64];
         float tmax = -INFINITY;
         if (mine) {
-          tmax = load_half(colS, j, 0, sr);
-          // (finish the first half's maximum before the second half's load, so
-          // that only one half of the scores is ever held in registers)
-          asm volatile("" : "+f"(tmax));
-          tmax = fmaxf(tmax, load_half(colS, j, 1, sr));  // sr keeps the second half
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) tmax = fmaxf(tmax, load_half(colS, j, hf, sr));  // sr keeps the second half
           if (!row_valid) tmax = -INFINITY;
         }
         // The state after the previous tile, from the other warpgroup.
@@ -804,12 +792,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // first half is loaded again.  A skipped or unseen tile writes zeros
         // (the pair's P.V covers both blocks; the other block may keep the tile).
         if (kept) {
-          float ls = exp_half(sr);
-          tmem_st32p(colS + 64, sr);
-          load_half(colS, j, 0, sr);
-          ls += exp_half(sr);
-          tmem_st32p(colS, sr);
-          l += ls;
+#pragma unroll(DQK == 64 ? 1 : 2)
+          for (int hf = 1; hf >= 0; --hf) {
+            if (hf == 0) load_half(colS, j, 0, sr);
+            l += exp_half(sr);
+            tmem_st32p(colS + 64 * hf, sr);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) sr[e] = 0u;
@@ -1043,12 +1031,16 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
 
 }  // namespace
 
-// Parts of the tiles: the most, up to the S ranges, that the units fill the
-// GPU's 76 cluster places with no more than twice over.
-int chunk_parts(long pairs, int S) {
+// Parts of the tiles.  A part's states are written and merged again (a second
+// kernel, ~6 us in all), so parts are made only where the pairs leave places
+// of the 76 clusters idle, at most as many as fit at once, and of eight tiles
+// or more.  Measured on 8 sequences x 5 new tokens x 2K keys (64 pairs, 8 KV
+// heads): 21 us as one part, 28 us as two.
+int chunk_parts(long pairs, int S, int max_pages) {
   const long places = 76;
-  const long most = 2 * places / pairs;
-  return most < 1 ? 1 : most < S ? static_cast<int>(most) : S;
+  long parts = places / pairs;
+  if (parts > max_pages / 8) parts = max_pages / 8;
+  return parts < 1 ? 1 : parts < S ? static_cast<int>(parts) : S;
 }
 
 cudaError_t launch_chunk_paged(int d, bool vote, const CUtensorMap& tq, const CUtensorMap& tk,
