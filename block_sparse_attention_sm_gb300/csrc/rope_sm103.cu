@@ -16,11 +16,11 @@
 // turns' relative) and bf16's of the result (half a step, 2^-8) are the only
 // ones.
 //
-// Bound by memory: 4 bytes per entry, read and written once.  A thread owns
-// one column of a token (8 pairs, or 4 adjacent ones: 16-byte accesses) for
-// every HS-th head, so it forms its angles once, without shared memory, and
-// has the first heads' loads in flight while it does.  HS is chosen so that
-// the launch fills the GPU when there are few tokens.
+// Bound by memory: 4 bytes per entry, read and written once.  A block takes
+// TB tokens; a thread one column of a token (8 pairs, or 4 adjacent ones:
+// 16-byte accesses) for every HS-th head, with the first heads' loads in
+// flight while the block forms the tokens' angles, each once, in shared
+// memory (a sincospif costs as much as moving a few heads' entries).
 #include "rope.cuh"
 
 #include "common.cuh"
@@ -124,11 +124,12 @@ struct Column {
       second = 0;
     }
   }
-  __device__ __forceinline__ void angles(int col, int pos, const RopeTurn& t) {
+  // This column's angles, from the block's table: entry i of column c of a
+  // token at [(token * kPairs + i) * width + c].
+  __device__ __forceinline__ void angles(const float2* table, int token, int c, int width) {
     if (turns) {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i)
-        cs[i] = turn_of(pos, __ldg(t.inv_freq + col * kPairs + i), t.factor, t.sign);
+      for (int i = 0; i < kPairs; ++i) cs[i] = table[(token * kPairs + i) * width + c];
     }
   }
   __device__ __forceinline__ void load(const __nv_bfloat16* row, Ch& a, Ch& b) const {
@@ -164,25 +165,54 @@ struct Column {
   }
 };
 
+// Forms the block's table: the angles of `width` columns from `col0` on, of
+// `tokens` tokens at the positions pos[].
+template <class C>
+__device__ __forceinline__ void fill_table(float2* table, const RopeTurn& t, const int* pos, int tokens,
+                                           int col0, int width) {
+  const int turning = min(width, max(0, C::turning(t.rot) - col0)) * C::kPairs;  // of each token
+  for (int e = threadIdx.x; e < tokens * turning; e += kThreadsRope) {
+    const int token = e / turning, pair = e - token * turning;
+    const int c = pair / C::kPairs, i = pair - c * C::kPairs;
+    table[(token * C::kPairs + i) * width + c] =
+        turn_of(pos[token], __ldg(t.inv_freq + col0 * C::kPairs + pair), t.factor, t.sign);
+  }
+}
+
+// A block: TB tokens x HS threads a column x `width` columns (of `cols`;
+// blockIdx.y steps over wider rows).
 template <bool VEC, bool ADJ>
-__global__ void __launch_bounds__(kThreadsRope) rope_kernel(const RopeParams p, int cols, int HS) {
+__global__ void __launch_bounds__(kThreadsRope)
+    rope_kernel(const RopeParams p, int cols, int width, int HS, int TB) {
   using C = Column<VEC, ADJ>;
-  const long i = static_cast<long>(blockIdx.x) * kThreadsRope + threadIdx.x;
-  const long per_token = static_cast<long>(cols) * HS;
-  const long token = i / per_token;
-  if (token >= static_cast<long>(p.B) * p.L) return;
-  const int rest = static_cast<int>(i - token * per_token);
-  const int h0 = rest / cols, col = rest - h0 * cols;
-  const long b = token / p.L, l = token - b * p.L;
+  __shared__ float2 table[kThreadsRope * C::kPairs];
+  __shared__ int pos[kThreadsRope];
+  const int tid = threadIdx.x, per_token = width * HS;
+  const long tokens = static_cast<long>(p.B) * p.L, t0 = static_cast<long>(blockIdx.x) * TB;
+  const int here = static_cast<int>(min(static_cast<long>(TB), tokens - t0));
+  const int ti = tid / per_token, rest = tid - ti * per_token;
+  const int h0 = rest / width, cw = rest - h0 * width, col = cw + blockIdx.y * width;
+  const bool mine = ti < here && col < cols;
+  const long token = t0 + ti, b = token / p.L, l = token - b * p.L;
   const __nv_bfloat16* x = p.x + b * p.xs[0] + l * p.xs[2];
   __nv_bfloat16* out = p.out + b * p.os[0] + l * p.os[2];
   C c;
   c.place(col, p.turn);
   typename C::Ch a[kAhead], bb[kAhead];
+  if (mine) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (h0 + u * HS < p.H) c.load(x + (h0 + u * HS) * p.xs[1], a[u], bb[u]);
-  c.angles(col, p.pos[b * p.pos_stride + l], p.turn);
+    for (int u = 0; u < kAhead; ++u)
+      if (h0 + u * HS < p.H) c.load(x + (h0 + u * HS) * p.xs[1], a[u], bb[u]);
+  }
+  if (tid < here) {
+    const long tt = t0 + tid, tb = tt / p.L;
+    pos[tid] = p.pos[tb * p.pos_stride + (tt - tb * p.L)];
+  }
+  __syncthreads();
+  fill_table<C>(table, p.turn, pos, here, blockIdx.y * width, width);
+  __syncthreads();
+  if (!mine) return;
+  c.angles(table, ti, cw, width);
   for (int h = h0;;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -208,15 +238,15 @@ template <bool VEC, bool ADJ>
 __global__ void __launch_bounds__(kThreadsRope)
     rope_append_kernel(const AppendParams p, int cols, int width, int HS, int TB) {
   using C = Column<VEC, ADJ>;
-  __shared__ int marks[kThreadsRope];
+  __shared__ float2 table[kThreadsRope * C::kPairs];
+  __shared__ int marks[kThreadsRope], pos[kThreadsRope], page[kThreadsRope], row[kThreadsRope];
   const int tid = threadIdx.x;
-  // `width` columns of a token side by side; blockIdx.y steps over wider rows.
   const int per_token = width * HS;
   const int t0 = blockIdx.x * TB;  // this block's tokens
   const int ti = tid / per_token;  // (threads beyond TB tokens only help to count)
   const int t = t0 + ti;
   const int rest = tid - ti * per_token;
-  const int h0 = rest / width, col = rest - h0 * width + blockIdx.y * width;
+  const int h0 = rest / width, cw = rest - h0 * width, col = cw + blockIdx.y * width;
   const bool mine = ti < TB && t < p.T && col < cols;
   const int nq = p.q != nullptr ? p.Hq : 0;
   const int heads = nq + p.Hkv * (p.v != nullptr ? 2 : 1);
@@ -245,19 +275,33 @@ __global__ void __launch_bounds__(kThreadsRope)
     if (end > t0 && end < t0 + TB) atomicAdd(&marks[end - t0], 1);
     before += __syncthreads_count(end <= t0);
   }
-  if (!mine) return;
-  int b = before;
-  for (int i = 1; i <= ti; ++i) b += marks[i];
-  if (b >= p.B || t < p.cu_seqlens[b]) return;
-  const long slot = static_cast<long>(p.seq_lens[b]) - (p.cu_seqlens[b + 1] - t);
-  const int pos = p.pos != nullptr ? p.pos[t] : static_cast<int>(slot);
-  int page = -1;
-  if (slot >= 0 && slot < static_cast<long>(p.max_pages) * kTile)
-    page = p.page_table[static_cast<long>(b) * p.max_pages + slot / kTile];
-  const bool in_cache = page >= 0 && page < p.num_pages;
-  const long page_row = (static_cast<long>(page) * p.Hkv * kTile + (slot & (kTile - 1))) * p.d;
+  // Position and place of each of them; row -1: a token of no sequence.
+  const int here = min(TB, p.T - t0);
+  if (tid < here) {
+    int b = before;
+    for (int i = 1; i <= tid; ++i) b += marks[i];
+    const int tt = t0 + tid;
+    row[tid] = -1;
+    pos[tid] = 0;
+    page[tid] = -1;
+    if (b < p.B && tt >= p.cu_seqlens[b]) {
+      const long slot = static_cast<long>(p.seq_lens[b]) - (p.cu_seqlens[b + 1] - tt);
+      pos[tid] = p.pos != nullptr ? p.pos[tt] : static_cast<int>(slot);
+      row[tid] = static_cast<int>(slot & (kTile - 1));
+      if (slot >= 0 && slot < static_cast<long>(p.max_pages) * kTile) {
+        const int pg = p.page_table[static_cast<long>(b) * p.max_pages + slot / kTile];
+        if (pg >= 0 && pg < p.num_pages) page[tid] = pg;
+      }
+    }
+  }
+  __syncthreads();
+  fill_table<C>(table, p.turn, pos, here, blockIdx.y * width, width);
+  __syncthreads();
+  if (!mine || row[ti] < 0) return;
+  const bool in_cache = page[ti] >= 0;
+  const long page_row = (static_cast<long>(page[ti]) * p.Hkv * kTile + row[ti]) * p.d;
   const long head_stride = static_cast<long>(kTile) * p.d;
-  c.angles(col, pos, p.turn);
+  c.angles(table, ti, cw, width);
   for (int h = h0;;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -285,12 +329,27 @@ __global__ void __launch_bounds__(kThreadsRope)
   }
 }
 
-// Threads that share a token's column: enough to fill the GPU (152 SMs of
-// 2048 threads) when there are few tokens, at most one per head.
-int head_split(long token_cols, int heads, int most) {
-  const long want = (152l * 2048 + token_cols - 1) / token_cols;
-  return static_cast<int>(want < 1 ? 1 : want > heads ? (heads < most ? heads : most)
-                                                      : (want < most ? want : most));
+// How a launch of `tokens` tokens x `heads` heads x `cols` columns is cut.
+// HS, the threads that share a token's column, is what fills the GPU once
+// (152 SMs of 2048 threads), at most a thread per head: a thread with many
+// heads keeps loads in flight from batch to batch, one with few pays the
+// block's two barriers and the angles for them.  Measured on 8192 tokens x 48
+// heads of 128: HS = 6, 35 us; 11, 45 us; 20, 55 us; 3, 35 us.
+struct Cut {
+  int width, passes, HS, TB;
+  unsigned blocks;
+};
+Cut cut_of(long tokens, int heads, int cols) {
+  Cut c;
+  c.passes = (cols + kThreadsRope - 1) / kThreadsRope;
+  c.width = (cols + c.passes - 1) / c.passes;
+  long hs = (152l * 2048 + tokens * cols - 1) / (tokens * cols);
+  if (hs > heads) hs = heads;
+  if (hs > kThreadsRope / c.width) hs = kThreadsRope / c.width;
+  c.HS = static_cast<int>(hs);
+  c.TB = kThreadsRope / (c.width * c.HS);
+  c.blocks = static_cast<unsigned>((tokens + c.TB - 1) / c.TB);
+  return c;
 }
 
 template <bool VEC, bool ADJ>
@@ -304,11 +363,9 @@ cudaError_t rope_impl(const RopeParams& p, cudaStream_t st) {
   const int cols = columns<VEC, ADJ>(p.turn, p.d, p.x == p.out);
   const long tokens = static_cast<long>(p.B) * p.L;
   if (tokens == 0 || p.H == 0 || cols == 0) return cudaSuccess;
-  const int HS = head_split(tokens * cols, p.H, p.H);
-  const long threads = tokens * cols * HS;
-  const long blocks = (threads + kThreadsRope - 1) / kThreadsRope;
-  if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-  rope_kernel<VEC, ADJ><<<static_cast<unsigned>(blocks), kThreadsRope, 0, st>>>(p, cols, HS);
+  if (tokens > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+  const Cut c = cut_of(tokens, p.H, cols);
+  rope_kernel<VEC, ADJ><<<dim3(c.blocks, c.passes), kThreadsRope, 0, st>>>(p, cols, c.width, c.HS, c.TB);
   return cudaGetLastError();
 }
 
@@ -317,12 +374,8 @@ cudaError_t append_impl(const AppendParams& p, cudaStream_t st) {
   const int cols = columns<VEC, ADJ>(p.turn, p.d, false);
   if (p.T == 0) return cudaSuccess;
   const int heads = (p.q != nullptr ? p.Hq : 0) + p.Hkv * (p.v != nullptr ? 2 : 1);
-  const int passes = (cols + kThreadsRope - 1) / kThreadsRope;
-  const int width = (cols + passes - 1) / passes;
-  const int HS = head_split(static_cast<long>(p.T) * cols, heads, kThreadsRope / width);
-  const int TB = kThreadsRope / (width * HS);
-  const dim3 grid((p.T + TB - 1) / TB, passes);
-  rope_append_kernel<VEC, ADJ><<<grid, kThreadsRope, 0, st>>>(p, cols, width, HS, TB);
+  const Cut c = cut_of(p.T, heads, cols);
+  rope_append_kernel<VEC, ADJ><<<dim3(c.blocks, c.passes), kThreadsRope, 0, st>>>(p, cols, c.width, c.HS, c.TB);
   return cudaGetLastError();
 }
 
