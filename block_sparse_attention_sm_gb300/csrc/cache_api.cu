@@ -224,7 +224,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   const long tpb = kTile / G, slots = chunk_slots(T, B, tpb);
   if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || T > 0x7fffffff - 2 * kTile ||
       static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL ||
-      slots > 0x3fffffffL || Hkv > 65535 ||
+      slots > 0x3fffffffL || Hkv > 65535 || 2 * slots * Hkv > 0x7fffffffL ||
       static_cast<long>(T) * Hq > 8 * 0x7fffffffL || stride >= (1LL << 38))
     return SS_ERR_INVALID_ARG;
   const size_t need = ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits);

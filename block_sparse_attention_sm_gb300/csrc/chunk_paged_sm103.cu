@@ -593,7 +593,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             if (!ok) break;
           }
-          if (any_kept) {
+          // (The first tile's P.V sets O, of zeros if no block kept it: NaN queries.)
+          if (any_kept || o_acc == 0u) {
             tc_fence_after();
             const uint64_t dv = smem_desc(sVa + vs * C::kVHalfBytes, 16384, 1024);
             const uint32_t pcol = 128u * bsel;
@@ -876,7 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const size_t orow = static_cast<size_t>(u.tok + tok) * p.Hq + u.kvh * p.G + head;
       const size_t rows = static_cast<size_t>(p.T) * p.Hq;
       if (writes && p.parts > 1) p.part_ml[u.part * rows + orow] = make_float2(m_ref * sl2, l_row);
-      const float inv_l = (l_row > 0.f) ? 1.f / l_row : 0.f;
+      const float inv_l = (l_row != 0.f) ? 1.f / l_row : 0.f;  // (NaN stays NaN)
 #pragma unroll
       for (int c = 0; c < DVO / 64; ++c) {
         uint32_t orr[64];
@@ -900,7 +901,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (writes) {
           if (p.parts > 1) {
-            if (l_row > 0.f) {
+            if (l_row != 0.f) {
               float4* dst = reinterpret_cast<float4*>(p.part_o + (u.part * rows + orow) * DVO + c * 64);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
   float mstar = -INFINITY;
   for (int s = 0; s < p.parts; ++s) {
     const float2 ml = p.part_ml[s * rows + row];
-    if (ml.y > 0.f) mstar = fmaxf(mstar, ml.x);
+    if (ml.y != 0.f) mstar = fmaxf(mstar, ml.x);
   }
   constexpr int E = D / 32;  // a lane's columns: E lane .. + E - 1
   float acc[E], l = 0.f;
@@ -980,7 +981,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int s = 0; s < p.parts; ++s) {
     const float2 ml = p.part_ml[s * rows + row];
-    if (!(ml.y > 0.f)) continue;
+    if (ml.y == 0.f) continue;
     const float w = ex2_approx(ml.x - mstar);
     l = fmaf(ml.y, w, l);
     const float* src = p.part_o + (s * rows + row) * D + E * lane;
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], w, acc[e]);
   }
-  const float inv = (l > 0.f) ? 1.f / l : 0.f;
+  const float inv = (l != 0.f) ? 1.f / l : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + E * lane);
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

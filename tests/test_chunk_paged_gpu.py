@@ -224,3 +224,77 @@ def test_chunk_bad_device_arrays_stay_in_bounds():
                    scale=0.1, out=o.t)
     want = 1.0 / (1.0 + math.exp(-0.1 * d))
     assert (o.t[0].float() - want).abs().max() <= 2.0 ** -8
+
+
+def test_chunk_repeats_bit_for_bit():
+    """Units are handed to clusters in any order; the results do not depend on it."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    n, L = [33, 1, 200, 7, 1, 90], [900, 2000, 1300, 64, 129, 700]
+    q, k, v = make(8, 4, 128, n, L, 21)
+    table, pages = random_tables(L, 1, np.random.default_rng(3))
+    args = (q.cuda(), fill_pool(k, L, table, pages).cuda(), fill_pool(v, L, table, pages).cuda(), table.cuda(),
+            offsets(n).cuda(), torch.tensor(L, dtype=torch.int32, device="cuda"))
+    for kw in (dict(num_kv_splits=1), dict(num_kv_splits=4, lambda_a=4.0)):
+        first = ss.chunk_paged(*args, scale=128 ** -0.5, **kw)
+        for _ in range(20):
+            assert torch.equal(ss.chunk_paged(*args, scale=128 ** -0.5, **kw), first)
+    one = args[0]
+    # a row alone gives what it gives among others (decode: the last token of each sequence)
+    last = torch.tensor([sum(n[:i + 1]) - 1 for i in range(len(n))], device="cuda")
+    alone = ss.chunk_paged(one[last].contiguous(), *args[1:4], offsets([1] * len(n)).cuda(), args[5], scale=128 ** -0.5)
+    among = ss.chunk_paged(*args, scale=128 ** -0.5)[last]
+    assert (alone.float() - among.float()).abs().max() <= 4 * 2.0 ** -8 * max(float(x.float().abs().max()) for x in v)
+
+
+def test_chunk_nan_query_stays_in_its_row():
+    import block_sparse_attention_sm_gb300 as ss
+
+    n, L = [20], [300]
+    q, k, v = make(4, 2, 128, n, L, 22)
+    table, pages = random_tables(L, 1, np.random.default_rng(3))
+    rest = (fill_pool(k, L, table, pages).cuda(), fill_pool(v, L, table, pages).cuda(), table.cuda(), offsets(n).cuda(),
+            torch.tensor(L, dtype=torch.int32, device="cuda"))
+    for kw in (dict(), dict(lambda_a=4.0)):
+        clean = ss.chunk_paged(q.cuda(), *rest, scale=128 ** -0.5, **kw)
+        bad = q.clone()
+        bad[7, 1] = float("nan")
+        got = ss.chunk_paged(bad.cuda(), *rest, scale=128 ** -0.5, **kw)
+        assert got[7, 1].isnan().all()
+        got[7, 1] = clean[7, 1]
+        assert torch.equal(got, clean)
+
+
+@pytest.mark.slow
+def test_chunk_and_append_beyond_32_bit_offsets():
+    """Pages more than 2^32 elements into the pool, written by the append call and read by the attention."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    Hq, Hkv, d = 8, 8, 128
+    pages = (1 << 32) // (Hkv * PAGE * d) + 40  # 8.6 GB each for keys and values
+    kp = torch.full((pages, Hkv, PAGE, d), float("nan"), dtype=BF, device="cuda")
+    vp = torch.full_like(kp, float("nan"))
+    L = [500, 129]
+    q, k, v = make(Hq, Hkv, d, L, L, 23)
+    far = [[pages - 1 - 3 * i for i in range(4)], [pages - 20 - i for i in range(4)]]
+    table = torch.tensor(far, dtype=torch.int32, device="cuda")
+    lens, cu = torch.tensor(L, dtype=torch.int32, device="cuda"), offsets(L).cuda()
+    rows = [torch.cat([x.transpose(0, 1) for x in y]).contiguous().cuda() for y in (k, v)]
+    ss.rope_append_paged(None, *rows, kp, vp, table, cu, lens)
+    o = ss.chunk_paged(q.cuda(), kp, vp, table, cu, lens, scale=d ** -0.5).cpu()
+    at = 0
+    for b, x in enumerate(L):
+        ref, weight, _ = chunk_reference(q[at:at + x], k[b], v[b], x, d ** -0.5, True, 0.0, 1)
+        assert_attention(o[at:at + x], ref, weight, f"sequence {b}")
+        at += x
+    # a fork copies such a page too
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[table.flatten().long()] = 1
+    refs[: pages - 30] = 1
+    rowsT = torch.cat([table, torch.full((1, 4), -1, dtype=torch.int32, device="cuda")]).contiguous()
+    lens3 = torch.tensor(L + [0], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0], dtype=torch.int32, device="cuda")
+    assert ss.pages_fork([kp, vp], refs, rowsT, lens3, one, one + 2).item() == 0
+    new, old = int(rowsT[2, 3]), far[0][3]
+    assert new >= pages - 30 and new != old
+    assert torch.equal(kp[new, :, :116], kp[old, :, :116]) and torch.equal(vp[new, :, :116], vp[old, :, :116])
