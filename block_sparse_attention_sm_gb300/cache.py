@@ -71,16 +71,15 @@ def _on(stream, names, *tensors):
     current and torch allocates on that stream; where both are so already
     there is nothing to enter."""
     dev = None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{names.split()[i]}: must be a CUDA tensor, got device {t.device}")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"tensors on several devices: {names.split()[i]} on {t.device}, others on cuda:{dev}")
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0 or dev is not None:
+                    name = names.split()[[t is u for u in tensors].index(True)]
+                    raise ValueError(f"{name}: must be a CUDA tensor, got device {t.device}" if d < 0 else
+                                     f"tensors on several devices: {name} on {t.device}, others on cuda:{dev}")
+                dev = d
     if stream is None and torch._C._cuda_getDevice() == dev:  # (a tensor on a GPU: CUDA is initialised)
         return torch._C._cuda_getCurrentRawStream(dev), _HERE
     if isinstance(stream, int):
@@ -152,14 +151,21 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
         _output("out", out, x, shape)
     handle, context = _on(stream, "x positions inv_freq out", x, positions, inv_freq, out)
     with context:
-        o = out if out is not None else torch.empty(shape, dtype=_BF16, device=x.device)
-        os_ = o.stride()
+        if out is None:
+            out = torch.empty(shape, dtype=_BF16, device=x.device)
         if packed:
-            xs, os_ = (0, xs[1], xs[0]), (0, os_[1], os_[0])
-        st = capi.ss_rope(x, o, B, H, L, d, positions, inv_freq, rot, xs[:3], os_[:3], pos_stride, rot_offset,
-                          interleaved, inverse, attn_factor, handle)
-    _check(st, "ss_rope")
-    return o
+            xt, xh, _ = xs
+            ot, oh, _ = out.stride()
+            xb = ob = 0
+        else:
+            xb, xh, xt, _ = xs
+            ob, oh, ot, _ = out.stride()
+        st = (capi._lib or capi.load()).ss_rope(
+            x.data_ptr(), out.data_ptr(), B, H, L, d, xb, xh, xt, ob, oh, ot, positions.data_ptr(), pos_stride,
+            inv_freq.data_ptr(), rot, rot_offset, bool(interleaved), bool(inverse), attn_factor, handle)
+    if st:
+        raise SSError(st, "ss_rope")
+    return out
 
 
 def _output(name, out, x, shape):
@@ -246,10 +252,14 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
             if o is None:
                 o = torch.empty(q_shape, dtype=_BF16, device=q.device)
             os_ = o.stride()
-        st = capi.ss_rope_append_paged(q, o, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot, k_pages,
-                                       v_pages, page_table, pool[0], max_pages, positions, qs[:2], os_[:2], ks[:2],
-                                       vs[:2], rot_offset, interleaved, attn_factor, handle)
-    _check(st, "ss_rope_append_paged")
+        st = (capi._lib or capi.load()).ss_rope_append_paged(
+            q.data_ptr() if q is not None else None, o.data_ptr() if q is not None else None, k.data_ptr(),
+            v.data_ptr() if v is not None else None, qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], T, B, Hq,
+            Hkv, d, cu_seqlens.data_ptr(), seq_lens.data_ptr(), positions.data_ptr() if positions is not None else None,
+            inv_freq.data_ptr() if rot else None, rot, rot_offset, bool(interleaved), attn_factor, k_pages.data_ptr(),
+            v_pages.data_ptr() if v is not None else None, page_table.data_ptr(), pool[0], max_pages, handle)
+    if st:
+        raise SSError(st, "ss_rope_append_paged")
     return o
 
 
@@ -322,15 +332,18 @@ def _state(page_refs, page_table, seq_lens):
 
 def _pools(pools, num_pages):
     """Bytes of a page, the same in every pool [num_pages, ...]."""
-    whole = None
+    shape = dtype = None
+    whole = 16 * num_pages
     for i, t in enumerate(pools):
-        if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.ndim < 2:
+        if not isinstance(t, torch.Tensor) or not t.is_contiguous():
             raise ValueError(f"pools[{i}]: expected a contiguous tensor [num_pages, ...]")
-        n = t.nbytes
-        if t.shape[0] != num_pages or (n != whole and whole is not None):
-            raise ValueError(f"pools[{i}]: expected {num_pages} pages of {(whole or n) // max(1, num_pages)} bytes")
-        whole = n
-    return 16 if whole is None else whole // max(1, num_pages)
+        if t.shape != shape or t.dtype is not dtype:
+            n = t.numel() * t.element_size()
+            if t.ndim < 2 or t.shape[0] != num_pages or (shape is not None and n != whole):
+                raise ValueError(f"pools[{i}]: expected {num_pages} pages of "
+                                 f"{(n if shape is None else whole) // max(1, num_pages)} bytes")
+            shape, dtype, whole = t.shape, t.dtype, n
+    return whole // max(1, num_pages)
 
 
 def _list(name, t, n=None):
@@ -348,7 +361,7 @@ def _page_scratch(num_pages, num_rows, n, workspace, result, device):
             raise ValueError("workspace: must be contiguous")
         nbytes = workspace.numel() * workspace.element_size()
         return workspace, nbytes, torch.empty(1, dtype=_I32, device=device) if result is None else result
-    nbytes = capi.ss_pages_workspace_size(num_pages, num_rows, n)
+    nbytes = (capi._lib or capi.load()).ss_pages_workspace_size(num_pages, num_rows, n)
     return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes,
             torch.empty(1, dtype=_I32, device=device) if result is None else result)
 

@@ -8,6 +8,7 @@ import of a function fails loudly -- there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -307,8 +308,8 @@ def ss_attn_mla_decode_paged(q, kv_pages, page_table, seq_lens, o, B, Hq, num_pa
 
 
 def _addresses(pools):
-    """Host array of the pools' device addresses."""
-    return (ctypes.c_void_p * max(1, len(pools)))(*[_ptr(p) for p in pools])
+    """Host array of the pools' device addresses (kept alive by the caller's reference)."""
+    return array.array("Q", [_ptr(p) or 0 for p in pools])
 
 
 def ss_rope(x, out, B, H, L, d, positions, inv_freq, rot_dim, x_strides=None, out_strides=None,
@@ -389,7 +390,7 @@ def ss_pages_free(page_refs, num_pages, page_table, num_rows, max_pages, seq_len
 def ss_pages_fork(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
                   src_rows, dst_rows, n, result=None, workspace=None, workspace_bytes=0,
                   stream=None) -> int:
-    return (_lib or load()).ss_pages_fork(_addresses(pools), len(pools), page_bytes, _ptr(page_refs),
+    return (_lib or load()).ss_pages_fork((a := _addresses(pools)).buffer_info()[0], len(a), page_bytes, _ptr(page_refs),
                                 num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
                                 _ptr(src_rows), _ptr(dst_rows), n, _ptr(result), _ptr(workspace),
                                 workspace_bytes, _stream(stream))
@@ -397,7 +398,7 @@ def ss_pages_fork(pools, page_bytes, page_refs, num_pages, page_table, num_rows,
 
 def ss_pages_copy(pools, page_bytes, num_pages, src, dst, n, result=None, workspace=None,
                   workspace_bytes=0, stream=None) -> int:
-    return (_lib or load()).ss_pages_copy(_addresses(pools), len(pools), page_bytes, num_pages, _ptr(src),
+    return (_lib or load()).ss_pages_copy((a := _addresses(pools)).buffer_info()[0], len(a), page_bytes, num_pages, _ptr(src),
                                 _ptr(dst), n, _ptr(result), _ptr(workspace), workspace_bytes,
                                 _stream(stream))
 
@@ -405,7 +406,7 @@ def ss_pages_copy(pools, page_bytes, num_pages, src, dst, n, result=None, worksp
 def ss_pages_compact(pools, page_bytes, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
                      out_refs=None, out_table=None, live=None, workspace=None, workspace_bytes=0,
                      stream=None) -> int:
-    return (_lib or load()).ss_pages_compact(_addresses(pools), len(pools), page_bytes, _ptr(page_refs),
+    return (_lib or load()).ss_pages_compact((a := _addresses(pools)).buffer_info()[0], len(a), page_bytes, _ptr(page_refs),
                                    num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
                                    _ptr(out_refs), _ptr(out_table), _ptr(live), _ptr(workspace),
                                    workspace_bytes, _stream(stream))
