@@ -152,7 +152,7 @@ struct PairCtl {
   uint64_t summed[4];          // each CTA, per unit % 4: the other warpgroup's share is in `fin`
   uint64_t mma_done[2];        // leader: teardown, per issuer
   uint64_t unit_full[2];       // each CTA: a unit's geometry is published
-  uint64_t unit_empty[2];      // each CTA: the other 11 warps have read it
+  uint64_t unit_empty[2];      // each CTA: its other warps have read it
   uint64_t next_full[2];       // each CTA: the answer to the request for a unit
   uint64_t next_empty[2];      // leader: both CTAs have read it
   alignas(16) uint32_t answer[2][4];                  // cluster launch control's
@@ -338,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->q_full[s], 1);
       mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->unit_full[s], 1);
-      mbar_init(&ctl->unit_empty[s], kThreads / 32 - 1);
+      mbar_init(&ctl->unit_empty[s], kThreads / 32 - (leader ? 1 : 3));  // (CTA 1's issuers idle)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->next_full[s], 1);
@@ -492,8 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t tc = 0, uc = 0;
     Unit u;
     bool ok = true;
-    for (int i = 0; ok && next_unit(i, &u); ++i) {
-      if (!leader || u.n_pair == 0) continue;
+    for (int i = 0; leader && ok && next_unit(i, &u); ++i) {
+      if (u.n_pair == 0) continue;
       if (lane == 0) {
         ok = wait(&ctl->q_full[uc & 1], (uc >> 1) & 1);
         const uint64_t dqu = dq + (((uc & 1) * C::kQBytes) >> 4);
@@ -538,8 +538,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t nresc = 0u;  // bit (kSoftWarps * r + warp): parity of (CTA r, warp)'s requests
     Unit u;
     bool ok = true;
-    for (int i = 0; ok && next_unit(i, &u); ++i) {
-      if (!leader || u.n_pair == 0) continue;
+    for (int i = 0; leader && ok && next_unit(i, &u); ++i) {
+      if (u.n_pair == 0) continue;
       if (lane == 0) {
         // O is read by the last unit's epilogue (of CTA 1's warps: as bytes).
         if (uc > 0) ok = wait(&ctl->o_free, (uc - 1) & 1);
