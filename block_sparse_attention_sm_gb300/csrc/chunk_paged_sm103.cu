@@ -501,9 +501,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t bsel = tc % kNB;
           // The buffer's previous tile has been decided by both blocks and its
           // P.V (if any) issued: S_t is ordered after it (tcgen05 fence + barrier).
-          if (tc >= kNB && !(ok = wait(&ctl->s_free[bsel], ((tc / kNB) - 1) & 1))) break;
           const uint32_t s = tc % NK;
           if (!(ok = wait(&ctl->k_full[s], (tc / NK) & 1))) break;
+          if (tc >= kNB && !(ok = wait(&ctl->s_free[bsel], ((tc / kNB) - 1) & 1))) break;
           tc_fence_after();
           const uint64_t dk = smem_desc(sKa + s * C::kKHalfBytes, 16, 1024);
           const uint32_t col = 128u * bsel;
@@ -604,9 +604,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            dv + ((kk * 2048) >> 4), idO, (o_acc | kk) ? 1u : 0u);
             o_acc = 1u;
           }
-          mma2_commit_mc(&ctl->v_empty[vs], 3);
           tc_fence_before();
           mbar_arrive(&ctl->s_free[bsel]);
+          mma2_commit_mc(&ctl->v_empty[vs], 3);
         }
         if (ok) mma2_commit_mc(&ctl->o_full, 3);
       }
