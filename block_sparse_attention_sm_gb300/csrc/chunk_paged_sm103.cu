@@ -97,6 +97,17 @@ __device__ __forceinline__ void order_after(uint32_t* done, uint32_t* next) {
                  "+r"(next[12]), "+r"(next[13]), "+r"(next[14]), "+r"(next[15]));
 }
 
+// A place in a ring of N slots and the parity of its current use (the
+// issuers' indices: their instructions between MMAs are time the tensor pipe
+// idles).
+template <int N>
+struct Ring {
+  uint32_t at = 0, par = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) at = 0, par ^= 1;
+  }
+};
+
 template <int DQK, int DV>
 struct PairCfg {
   static_assert(DQK == 64 || DQK == 128, "key width");
@@ -489,7 +500,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr uint32_t idS = idesc_bf16_f32(256, 128, false, false);
     const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
     const uint32_t sKa = smem_u32(sK);
-    uint32_t tc = 0, uc = 0;
+    uint32_t uc = 0;
+    Ring<NK> rk;
+    Ring<kNB> rs;
     Unit u;
     bool ok = true;
     for (int i = 0; leader && ok && next_unit(i, &u); ++i) {
@@ -497,27 +510,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         ok = wait(&ctl->q_full[uc & 1], (uc >> 1) & 1);
         const uint64_t dqu = dq + (((uc & 1) * C::kQBytes) >> 4);
-        for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
-          const uint32_t bsel = tc % kNB;
+        for (int jj = 0; ok && jj < u.n_pair; ++jj) {
+          if (!(ok = wait(&ctl->k_full[rk.at], rk.par))) break;
           // The buffer's previous tile has been decided by both blocks and its
           // P.V (if any) issued: S_t is ordered after it (tcgen05 fence + barrier).
-          const uint32_t s = tc % NK;
-          if (!(ok = wait(&ctl->k_full[s], (tc / NK) & 1))) break;
-          if (tc >= kNB && !(ok = wait(&ctl->s_free[bsel], ((tc / kNB) - 1) & 1))) break;
+          if (!(ok = wait(&ctl->s_free[rs.at], rs.par ^ 1))) break;
           tc_fence_after();
-          const uint64_t dk = smem_desc(sKa + s * C::kKHalfBytes, 16, 1024);
-          const uint32_t col = 128u * bsel;
+          const uint64_t dk = smem_desc(sKa + rk.at * C::kKHalfBytes, 16, 1024);
+          const uint32_t col = 128u * rs.at;
 #pragma unroll
           for (int kk = 0; kk < DQK / 16; ++kk) {
             const uint32_t qoff = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
             const uint32_t koff = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
             mma2_bf16_ss(tmem + col, dqu + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
           }
-          mma2_commit_mc(&ctl->s_full[bsel], 3);
-          mma2_commit_mc(&ctl->k_empty[s], 3);
+          mma2_commit_mc(&ctl->s_full[rs.at], 3);
+          mma2_commit_mc(&ctl->k_empty[rk.at], 3);
           // CTA 1's four warps on this tile complete 4 bytes each on dec; this
           // arrival sets that count for the tile's phase.
-          mbar_arrive_expect_tx(&ctl->dec[bsel], 4 * kGroupWarps);
+          mbar_arrive_expect_tx(&ctl->dec[rs.at], 4 * kGroupWarps);
+          rk.next();
+          rs.next();
         }
         if (ok) mma2_commit_mc(&ctl->q_empty[uc & 1], 3);
       }
@@ -553,23 +566,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t vs = tc % NV;
           if (!(ok = wait(&ctl->v_full[vs], (tc / NV) & 1))) break;
           if (!(ok = wait(&ctl->dec[bsel], ph))) break;
-          // The tile's decisions come from the warps of warpgroup tc % 2.
-          const int wg0 = kGroupWarps * (tc & 1);
-          uint32_t resc = 0u, any_kept = 0u;  // resc: bit (kGroupWarps * r + w)
-          {
-            // (plain loads: the barrier waits above are compiler memory barriers)
-            const uint4 f4 = *reinterpret_cast<const uint4*>(ctl->flags[bsel]);
-            const uint4 g4 = *reinterpret_cast<const uint4*>(ctl->peer_flags[bsel]);
+          // (plain loads: the barrier waits above are compiler memory barriers)
+          const uint4 f4 = *reinterpret_cast<const uint4*>(ctl->flags[bsel]);
+          const uint4 g4 = *reinterpret_cast<const uint4*>(ctl->peer_flags[bsel]);
+          const uint32_t any = f4.x | f4.y | f4.z | f4.w | g4.x | g4.y | g4.z | g4.w;
+          if (any & kFlagRescale) {
+            // The tile's decisions come from the warps of warpgroup tc % 2.
+            const int wg0 = kGroupWarps * (tc & 1);
             const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
             const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w};
+            uint32_t resc = 0u;  // bit (kGroupWarps * r + w)
 #pragma unroll
             for (int w = 0; w < kGroupWarps; ++w) {
-              any_kept |= (f[w] | g[w]) & kFlagKept;
               resc |= ((f[w] >> 1) & 1u) << w;
               resc |= ((g[w] >> 1) & 1u) << (kGroupWarps + w);
             }
-          }
-          if (resc) {
             // Warps that move their reference maximum rescale O once every P.V
             // issued so far has finished.
 #pragma unroll
@@ -594,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
           }
           // (The first tile's P.V sets O, of zeros if no block kept it: NaN queries.)
-          if (any_kept || o_acc == 0u) {
+          if ((any & kFlagKept) || o_acc == 0u) {
             tc_fence_after();
             const uint64_t dv = smem_desc(sVa + vs * C::kVHalfBytes, 16384, 1024);
             const uint32_t pcol = 128u * bsel;
