@@ -97,14 +97,16 @@ __device__ __forceinline__ void order_after(uint32_t* done, uint32_t* next) {
                  "+r"(next[12]), "+r"(next[13]), "+r"(next[14]), "+r"(next[15]));
 }
 
-// A place in a ring of N slots and the parity of its current use (the
-// issuers' indices: their instructions between MMAs are time the tensor pipe
-// idles).
-template <int N>
+// A place in a ring of N slots and the parity of its current use, STEP places
+// a time (the issuers' indices: their instructions between MMAs are time the
+// tensor pipe idles).
+template <int N, int STEP>
 struct Ring {
-  uint32_t at = 0, par = 0;
+  uint32_t at, par;
+  __device__ explicit Ring(uint32_t first, uint32_t parity = 0) : at(first), par(parity) {}
   __device__ __forceinline__ void next() {
-    if (++at == N) at = 0, par ^= 1;
+    at += STEP;
+    if (at >= N) at -= N, par ^= 1;
   }
 };
 
@@ -151,17 +153,17 @@ struct PairCtl {
   uint64_t v_full[NV];         // leader: both V halves landed
   uint64_t k_empty[NK];        // each CTA: its K slot may be refilled
   uint64_t v_empty[NV];        // each CTA: its V slot may be refilled
-  uint64_t s_full[kNB];        // each CTA: scores of the buffer's tile are in TMEM
+  uint64_t s_full[6];          // each CTA, per tile % kSlots: the tile's scores are in TMEM
   uint64_t dec[kNB];           // leader: both CTAs' 4 warps on the buffer's tile have decided
                                // it (CTA 0's by arrivals, CTA 1's as 16 bytes of stores)
   uint64_t drain[kSoftWarps];  // each CTA, per softmax warp: the P.V MMAs issued so far are done
   uint64_t rescaled[2][kSoftWarps];  // leader: (CTA, warp) has rescaled its part of O
-  uint64_t s_free[kNB];        // leader: the buffer's P.V is issued (or not needed)
+  uint64_t s_free[6];          // leader, per tile % kSlots: the tile's P.V is issued (or not needed)
   uint64_t o_full;             // each CTA: the unit's last P.V is done
   uint64_t o_free;             // leader: the unit's O has been read (4 warps of each CTA)
   uint64_t handed[4];          // each CTA, per tile % 4: the rows' state after the tile is in `hand`
   uint64_t summed[4];          // each CTA, per unit % 4: the other warpgroup's share is in `fin`
-  uint64_t mma_done[2];        // leader: teardown, per issuer
+  uint64_t mma_done[3];        // leader: teardown, per issuer
   uint64_t unit_full[2];       // each CTA: a unit's geometry is published
   uint64_t unit_empty[2];      // each CTA: its other warps have read it
   uint64_t next_full[2];       // each CTA: the answer to the request for a unit
@@ -248,6 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using Ctl = PairCtl<NK, NV>;
   static_assert(sizeof(Ctl) <= C::kCtlBytes, "control block overflow");
   constexpr bool kVote = (MODE != Mode::kDense);
+  constexpr bool kTwo = kVote;  // two score issuers, one producer
+  // Slots of a tile's barriers: with two issuers a slot belongs to one of them
+  // (and to one softmax warpgroup), so that no waiter misses a phase of it.
+  constexpr uint32_t kSlots = kTwo ? 6 : kNB;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -325,12 +331,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->v_full[s], 1);
       mbar_init(&ctl->v_empty[s], 1);
     }
-    for (int s = 0; s < kNB; ++s) {
+    for (int s = 0; s < 6; ++s) {
       mbar_init(&ctl->s_full[s], 1);
+      mbar_init(&ctl->s_free[s], 1);
+    }
+    for (int s = 0; s < kNB; ++s) {
       // this CTA's 4 warps + the score issuer's arrival (which sets the 16
       // bytes that CTA 1's 4 warps complete)
       mbar_init(&ctl->dec[s], kGroupWarps + 1);
-      mbar_init(&ctl->s_free[s], 1);
     }
     for (int w = 0; w < kSoftWarps; ++w) {
       mbar_init(&ctl->drain[w], 1);
@@ -341,15 +349,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->o_free, kGroupWarps + 1);  // likewise, with 16 bytes from CTA 1
     mbar_init(&ctl->mma_done[0], 1);
     mbar_init(&ctl->mma_done[1], 1);
+    mbar_init(&ctl->mma_done[2], 1);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl->handed[s], kGroupWarps);
       mbar_init(&ctl->summed[s], kGroupWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->q_full[s], 1);
-      mbar_init(&ctl->q_empty[s], 1);
+      mbar_init(&ctl->q_empty[s], kTwo ? 2 : 1);
       mbar_init(&ctl->unit_full[s], 1);
-      mbar_init(&ctl->unit_empty[s], kThreads / 32 - (leader ? 1 : 3));  // (CTA 1's issuers idle)
+      mbar_init(&ctl->unit_empty[s], kThreads / 32 - (leader ? 1 : kTwo ? 4 : 3));  // (CTA 1's issuers idle)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->next_full[s], 1);
@@ -395,12 +404,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= kSoftWarps) setmaxnreg_dec<kRegsDown<MODE>>();
+  // The V tile jj of a unit (outer coordinate z) into its ring entry, by a whole warp.
+  auto load_v = [&](const Unit& u, int jj, int z, uint32_t tc) -> bool {
+    const uint32_t s = tc % NV;
+    if (!wwait(&ctl->v_empty[s], ((tc / NV) & 1) ^ 1)) return false;
+    if (lane == 0) {
+      if (leader) mbar_arrive_expect_tx(&ctl->v_full[s], 2 * C::kVHalfBytes);
+      tma_load_3d_pair(sV + s * C::kVHalfBytes, &tmV, lead(&ctl->v_full[s]), 64 * static_cast<int>(rank),
+                       u.j0 + jj == u.last ? -u.last_shift : 0, z);
+    }
+    return true;
+  };
   // Counters that every role keeps alike: tc, tiles before this unit; uc, units with tiles before it.
   if (warp == kWarpK) {
     // ------------------------------------------------------------ units, Q, K producer
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
+      if (kTwo) tma_prefetch_desc(&tmV);
     }
     int x = blockIdx.x >> 1;
     uint32_t tc = 0, uc = 0;
@@ -458,6 +479,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < C::kChunksQ; ++c)
             tma_load_3d_pair(sK + s * C::kKHalfBytes + c * C::kKChunk, &tmK, kbar, c * 64, y, zt);
         }
+        if constexpr (kTwo) {
+          if (!(ok = load_v(u, jj, zt, tc))) break;
+        }
         ++tc;
       }
       if (!ok) break;
@@ -474,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kWarpV) {
+  } else if (!kTwo && warp == kWarpV) {
     // ------------------------------------------------------------ V producer
     if (lane == 0) tma_prefetch_desc(&tmV);
     uint32_t tc = 0;
@@ -482,27 +506,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; ok && next_unit(i, &u); ++i) {
       int z = 0;
-      for (int jj = 0; jj < u.n_pair; ++jj, ++tc) {
+      for (int jj = 0; ok && jj < u.n_pair; ++jj, ++tc) {
         if ((jj & 31) == 0) z = pages32(u, jj);
-        const int zt = __shfl_sync(0xffffffffu, z, jj & 31);
-        const uint32_t s = tc % NV;
-        if (!(ok = wwait(&ctl->v_empty[s], ((tc / NV) & 1) ^ 1))) break;
-        if (lane == 0) {
-          if (leader) mbar_arrive_expect_tx(&ctl->v_full[s], 2 * C::kVHalfBytes);
-          tma_load_3d_pair(sV + s * C::kVHalfBytes, &tmV, lead(&ctl->v_full[s]),
-                           64 * static_cast<int>(rank), u.j0 + jj == u.last ? -u.last_shift : 0, zt);
-        }
+        ok = load_v(u, jj, __shfl_sync(0xffffffffu, z, jj & 31), tc);
       }
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    // ------------------------------------------------------------ score issuer (leader)
+  } else if (warp == kWarpMma || warp == kWarpV) {
+    // ------------------------------------------------------------ score issuer(s) (leader)
+    // Between a tile's MMAs and the next one's, the issuer commits and waits
+    // for some 300 cycles.  In the dense path P.V fills them; with the vote,
+    // where most tiles have no P.V, two issuers take alternate tiles (0: the
+    // even ones), so that one's MMAs run while the other synchronises.
+    const uint32_t me = (kTwo && warp == kWarpV) ? 1 : 0;
+    constexpr uint32_t kStep = kTwo ? 2 : 1;
     constexpr uint32_t idS = idesc_bf16_f32(256, 128, false, false);
     const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
     const uint32_t sKa = smem_u32(sK);
-    uint32_t uc = 0;
-    Ring<NK> rk;
-    Ring<kNB> rs;
+    uint32_t tc = 0, uc = 0;
+    Ring<NK, kStep> rk{me};
+    Ring<kSlots, kStep> rt{me}, rf{(me + kNB) % kSlots, 1};  // slots of the tile; of the one three before it
+    uint32_t col = 128u * me;  // its score buffer
     Unit u;
     bool ok = true;
     for (int i = 0; leader && ok && next_unit(i, &u); ++i) {
@@ -510,37 +534,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         ok = wait(&ctl->q_full[uc & 1], (uc >> 1) & 1);
         const uint64_t dqu = dq + (((uc & 1) * C::kQBytes) >> 4);
-        for (int jj = 0; ok && jj < u.n_pair; ++jj) {
+        for (uint32_t t = tc + (kTwo ? (me ^ (tc & 1)) : 0); ok && t < tc + u.n_pair; t += kStep) {
           if (!(ok = wait(&ctl->k_full[rk.at], rk.par))) break;
-          // The buffer's previous tile has been decided by both blocks and its
-          // P.V (if any) issued: S_t is ordered after it (tcgen05 fence + barrier).
-          if (!(ok = wait(&ctl->s_free[rs.at], rs.par ^ 1))) break;
+          // The buffer's previous tile, three before, has been decided by both
+          // blocks and its P.V (if any) issued: S_t is ordered after it
+          // (tcgen05 fence + barrier).
+          if (!(ok = wait(&ctl->s_free[rf.at], rf.par))) break;
           tc_fence_after();
           const uint64_t dk = smem_desc(sKa + rk.at * C::kKHalfBytes, 16, 1024);
-          const uint32_t col = 128u * rs.at;
+          if (!kTwo) col = 128u * rt.at;
 #pragma unroll
           for (int kk = 0; kk < DQK / 16; ++kk) {
             const uint32_t qoff = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
             const uint32_t koff = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
             mma2_bf16_ss(tmem + col, dqu + qoff, dk + koff, idS, kk > 0 ? 1u : 0u);
           }
-          mma2_commit_mc(&ctl->s_full[rs.at], 3);
+          mma2_commit_mc(&ctl->s_full[rt.at], 3);
           mma2_commit_mc(&ctl->k_empty[rk.at], 3);
           // CTA 1's four warps on this tile complete 4 bytes each on dec; this
           // arrival sets that count for the tile's phase.
-          mbar_arrive_expect_tx(&ctl->dec[rs.at], 4 * kGroupWarps);
+          mbar_arrive_expect_tx(&ctl->dec[kTwo ? col >> 7 : rt.at], 4 * kGroupWarps);
           rk.next();
-          rs.next();
+          rt.next();
+          rf.next();
+          if (kTwo && (col += 256u) >= 384u) col -= 384u;
         }
         if (ok) mma2_commit_mc(&ctl->q_empty[uc & 1], 3);
       }
+      tc += u.n_pair;
       ++uc;
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (leader && lane == 0) {
       // Every MMA issued must have finished before TMEM is freed.
-      mma2_commit_mc(&ctl->mma_done[0], 1);
-      mbar_wait(&ctl->mma_done[0], 0, nullptr);
+      const int d = me ? 2 : 0;
+      mma2_commit_mc(&ctl->mma_done[d], 1);
+      mbar_wait(&ctl->mma_done[d], 0, nullptr);
     }
     __syncwarp();
   } else if (warp == kWarpPV) {
@@ -616,7 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             o_acc = 1u;
           }
           tc_fence_before();
-          mbar_arrive(&ctl->s_free[bsel]);
+          mbar_arrive(&ctl->s_free[tc % kSlots]);
           mma2_commit_mc(&ctl->v_empty[vs], 3);
         }
         if (ok) mma2_commit_mc(&ctl->o_full, 3);
@@ -725,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int j = u.j0 + jj;  // tile of the sequence
         const uint32_t t = tc + jj, bsel = t % kNB;
         const uint32_t colS = lane_base + 128u * bsel;
-        if (!wwait(&ctl->s_full[bsel], (t / kNB) & 1)) ok = false;
+        if (!wwait(&ctl->s_full[t % kSlots], (t / kSlots) & 1)) ok = false;
         tc_fence_after();
         const bool mine = jj < u.n_mine;
         uint32_t sr[64];
