@@ -26,10 +26,9 @@
 // 256); each SM stages half of each K and V tile.  TMEM per SM: three score
 // buffers and O.  Two softmax warpgroups per CTA take alternate tiles, one
 // thread per row, and hand the rows' running maximum on through shared memory;
-// P goes back to TMEM as bf16 (P <= 2^8 relative to the reference maximum, a
-// half-step of 2^-9 relative per weight; sums l are of the unrounded fp32) and
-// P.V accumulates in fp32.  One thread issues score MMAs, another P.V MMAs.
-// Every wait is bounded.
+// P goes back to TMEM as bf16 (P <= 2^8 relative to the reference maximum;
+// rounded by 2^-8 of a weight at most, the sums l are of the unrounded fp32)
+// and P.V accumulates in fp32.  Every wait is bounded.
 //
 // Units and clusters: a unit is (pair of row blocks, KV head, part of the
 // tiles).  Serving batches have many short units (a decoded token over a few
@@ -40,21 +39,38 @@
 // K / V rings live on: the producers load the next unit's first tiles, and the
 // score issuer starts on them, while the softmax of the last unit's tail and
 // its epilogue run.
-//   Producer warp 8 of CTA 0 asks for the next unit when it issues the last
-//   loads of one; the answer comes to both CTAs, and warp 8 of each works out
-//   the unit's geometry (sequence, lengths, tiles) and publishes it to the
-//   CTA's other warps.  The warpgroup with a unit's last tile writes its
-//   output; the other goes on with the next unit's first tile.
 //
-// Few rows and a long cache: the tiles are dealt to S parts whose states (m,
-// l, O) a second kernel merges in fp32.  The ranges of the vote (num_kv_splits:
+// Roles (384 threads in each CTA): warps 0-7 softmax and vote, two warpgroups;
+// warp 8 units, Q and K (it asks for the next unit when it issues the last
+// loads of one; the answer comes to both CTAs, and warp 8 of each works out the
+// unit's geometry and publishes it to the CTA's other warps); warp 9 V; warp 10
+// of CTA 0 the score MMAs; warp 11 of CTA 0 the P.V MMAs.  With the vote warp 8
+// loads V too and warp 9 of CTA 0 issues every other tile's scores.
+//
+// Few rows and a long cache: the tiles are dealt to parts whose states (m, l,
+// O) a second kernel merges in fp32.  The ranges of the vote (num_kv_splits:
 // each starts without a running maximum, so its first tile is kept) are a
 // matter of the definition, not of the launch: one unit passes through several
 // ranges in turn, restarting the vote's maximum, and only as many parts are
-// made as fill the GPU (parts_of).
+// made as there are idle clusters for (chunk_parts).
 //
 // d = 64 runs with value tiles padded to 128 columns (the second SM's half of
-// a value tile is an out-of-range box): the softmax bounds that width anyway.
+// a value tile is an out-of-range box).
+//
+// What bounds it (measured on GB300; 4 x 2048 new tokens over 32K keys, 32 / 8
+// heads of 128).  Dense: 2.85 ms, 1490 TFLOP/s, 77% of the cuBLAS rate; the
+// P.V issuer is busy throughout (8 two-SM MMAs take ~900 cycles beside the
+// other issuer's, and ~500 go to barriers and commits).  With the skip test at
+// ~88% skipped tiles: 1.98 ms; a tile's scores pass through MMA, commit, load,
+// vote and two barriers (~2900 cycles) and TMEM holds three of them.  Short
+// units: ~3 us each beside their tiles (608 units of 16 tiles: 139 us, 4.6
+// TB/s).  Instructions matter: a unit's code runs out of the instruction cache,
+// which is why the halves of a tile are rolled loops, what a sequence's units
+// share is read from shared memory, and the issuers' paths are short.  Tried
+// and slower: scores in registers with separate P buffers (two score buffers,
+// 2.67 ms with the skip test); P of skipped blocks left out by a lane mask
+// instead of zeros (the masked MMA form costs 8%); polling instead of
+// suspended waits (2.27 ms).
 #include <cuda_bf16.h>
 
 #include "chunk_paged.cuh"
