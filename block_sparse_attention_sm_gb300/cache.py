@@ -263,8 +263,9 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
     return o
 
 
-def chunk_paged_workspace(T, Hq, d, num_kv_splits, device):
-    n = capi.ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits)
+def chunk_paged_workspace(T, B, Hq, Hkv, max_pages, d, num_kv_splits, device):
+    """(workspace, its bytes) for :func:`chunk_paged` calls of these sizes."""
+    n = capi.ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
 
 
@@ -314,7 +315,7 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
         if workspace is not None:
             nbytes = workspace.numel() * workspace.element_size()
         elif num_kv_splits > 1:
-            workspace, nbytes = chunk_paged_workspace(T, Hq, d, num_kv_splits, q.device)
+            workspace, nbytes = chunk_paged_workspace(T, B, Hq, Hkv, max_pages, d, num_kv_splits, q.device)
         st = capi.ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,
                                       num_pages, max_pages, d, scale, causal, lambda_a, num_kv_splits, counts,
                                       workspace, nbytes, qs[0] if T > 1 else 0, skip_mask, vote_margin, handle)

@@ -106,7 +106,7 @@ def load() -> ctypes.CDLL:
     lib.ss_attn_chunk_paged.argtypes = [P, I64, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, F, I, P, P,
                                         U, ctypes.POINTER(ss_debug_opts), P]
     lib.ss_attn_chunk_paged_units.argtypes = [I, I, I, I]
-    lib.ss_attn_chunk_paged_workspace_size.argtypes = [I, I, I, I]
+    lib.ss_attn_chunk_paged_workspace_size.argtypes = [I] * 7
     lib.ss_pages_workspace_size.argtypes = [I, I, I]
     for name in ("ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
                  "ss_pages_workspace_size"):
@@ -352,8 +352,8 @@ def ss_attn_chunk_paged_units(T, B, Hq, Hkv) -> int:
     return int((_lib or load()).ss_attn_chunk_paged_units(T, B, Hq, Hkv))
 
 
-def ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits) -> int:
-    return int((_lib or load()).ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits))
+def ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits) -> int:
+    return int((_lib or load()).ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits))
 
 
 def ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,

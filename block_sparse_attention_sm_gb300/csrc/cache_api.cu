@@ -194,9 +194,13 @@ size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv) {
   return 2 * static_cast<size_t>(chunk_slots(T, B, kTile / G)) * Hkv;
 }
 
-size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits) {
-  if (num_kv_splits <= 1 || T < 1 || Hq < 1 || d < 1) return 0;
-  return static_cast<size_t>(num_kv_splits) * T * Hq * (d + 2) * sizeof(float);
+size_t ss_attn_chunk_paged_workspace_size(int T, int B, int Hq, int Hkv, int max_pages, int d,
+                                          int num_kv_splits) {
+  if (num_kv_splits <= 1 || T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq / Hkv > kTile || max_pages < 1 ||
+      d < 1)
+    return 0;
+  const int parts = chunk_parts(chunk_slots(T, B, kTile / (Hq / Hkv)) * Hkv, num_kv_splits, max_pages);
+  return parts == 1 ? 0 : static_cast<size_t>(parts) * T * Hq * (d + 2) * sizeof(float);
 }
 
 ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
@@ -227,7 +231,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
       slots > 0x3fffffffL || Hkv > 65535 || 2 * slots * Hkv > 0x7fffffffL ||
       static_cast<long>(T) * Hq > 8 * 0x7fffffffL || stride >= (1LL << 38))
     return SS_ERR_INVALID_ARG;
-  const size_t need = ss_attn_chunk_paged_workspace_size(T, Hq, d, num_kv_splits);
+  const size_t need = ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits);
   if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
     return SS_ERR_WORKSPACE;
   if (T == 0) return SS_OK;
@@ -303,7 +307,7 @@ static ss_status check_state(const int32_t* refs, int num_pages, const int32_t* 
 
 static ss_status check_pools(void* const* pools, int num_pools, size_t page_bytes) {
   if (num_pools < 0 || (num_pools > 0 && pools == nullptr) || page_bytes == 0 || page_bytes % 16 != 0 ||
-      page_bytes > (static_cast<size_t>(1) << 40))
+      page_bytes > (static_cast<size_t>(1) << 34))
     return SS_ERR_INVALID_ARG;
   for (int i = 0; i < num_pools; ++i)
     if (pools[i] == nullptr || !aligned16(pools[i])) return SS_ERR_INVALID_ARG;

@@ -97,6 +97,7 @@ constexpr int kRegsUp = (kThreads * kLaunchRegs - 128 * kRegsDown<MODE>) / 256;
 static_assert(kRegsUp<Mode::kDense> == 200 && kRegsUp<Mode::kSparse> == 208, "register split");
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpPV = 11;
 constexpr int kNB = 3;  // score buffers
+constexpr int kAllKeys = 0x7ffffe00;  // a row sees every key (room for + a block's tokens)
 constexpr int kSeqs = 512;  // sequences whose offsets and lengths are kept in shared memory
 constexpr uint32_t kFlagKept = 1u, kFlagRescale = 2u;
 
@@ -332,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         u.n_mine = n;
         u.toks = toks;
         u.tok = tok0 + i0;
-        u.lim0 = p.causal ? off + i0 : 0x3fffffff;
+        u.lim0 = p.causal ? off + i0 : kAllKeys;
       }
     }
     return u;
@@ -712,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool row_valid = tok < u.toks;
       // Last key index this row may see.  A row without a token is not masked:
       // it takes no part in the vote, and nothing of it is kept.
-      const int lim = row_valid ? min(u.last * kTile + kTile - 1 - u.last_shift, u.lim0 + tok) : 0x3fffffff;
+      const int lim = row_valid ? min(u.last * kTile + kTile - 1 - u.last_shift, u.lim0 + tok) : kAllKeys;
       const long unit_row = static_cast<long>(u.id) * p.max_pages;
       float m_true = -INFINITY, m_ref = -INFINITY, l = 0.f;
       uint32_t skipped = 0;

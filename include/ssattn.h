@@ -467,7 +467,8 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
  * SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
  */
 size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv);
-size_t ss_attn_chunk_paged_workspace_size(int T, int Hq, int d, int num_kv_splits);
+size_t ss_attn_chunk_paged_workspace_size(int T, int B, int Hq, int Hkv, int max_pages, int d,
+                                          int num_kv_splits);
 ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
                               const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
                               const int32_t* seq_lens, void* o, int T, int B, int Hq, int Hkv,
@@ -486,7 +487,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
  * Only full pages are shared; a sequence's last page, while not full, is its
  * own, so new keys can always be appended.  Pools: `pools` is a host array of
  * num_pools device addresses (16-byte aligned), each num_pages pages of
- * page_bytes (a multiple of 16) -- the key and the value pages of every layer;
+ * page_bytes (a multiple of 16, up to 2^34) -- the key and the value pages of every layer;
  * 64 pools a launch.  Calls on one state must be ordered by the caller (one
  * stream, or events): they read and write it.  `workspace`: at least
  * ss_pages_workspace_size(num_pages, num_rows, n) bytes, 16-byte aligned, for

@@ -110,10 +110,11 @@ def test_append_rejects(capi, kw, expect):
     (dict(q_token_stride=1020), "INVALID_ARG"), (dict(q_token_stride=512), "INVALID_ARG"), (dict(d=96), "UNSUPPORTED"),
     (dict(Hq=258), "UNSUPPORTED"), (dict(num_kv_splits=2), "WORKSPACE"),
     (dict(num_kv_splits=2, workspace=FAKE, workspace_bytes=2 * 5 * 8 * 130 * 4 - 1), "WORKSPACE"), (dict(T=0), "OK"),
+    (dict(Hkv=70000, Hq=70000), "INVALID_ARG"),
 ])
 def test_chunk_rejects(capi, kw, expect):
     args = dict(q=FAKE, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, cu_seqlens=FAKE, seq_lens=FAKE, o=FAKE, T=5, B=2, Hq=8,
-                Hkv=2, num_pages=4, max_pages=4, d=128, scale=0.1, causal=True, lambda_a=0.0, num_kv_splits=1, stream=0)
+                Hkv=2, num_pages=4, max_pages=64, d=128, scale=0.1, causal=True, lambda_a=0.0, num_kv_splits=1, stream=0)
     args.update(kw)
     assert capi.ss_attn_chunk_paged(**args) == getattr(capi, "SS_OK" if expect == "OK" else "SS_ERR_" + expect)
 
@@ -130,8 +131,13 @@ def test_chunk_refuses_test_only_debug_fields(capi):
 
 
 def test_sizes(capi):
-    assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 1) == 0
-    assert capi.ss_attn_chunk_paged_workspace_size(10, 8, 128, 3) == 3 * 10 * 8 * 130 * 4
+    ws = capi.ss_attn_chunk_paged_workspace_size
+    assert ws(10, 2, 8, 2, 64, 128, 1) == 0
+    assert ws(10, 2, 8, 2, 64, 128, 3) == 3 * 10 * 8 * 130 * 4
+    assert ws(10, 2, 8, 2, 64, 128, 1000) == 8 * 10 * 8 * 130 * 4   # 64 pages: 8 parts of 8
+    assert ws(10, 2, 8, 2, 9999, 128, 1000) == 19 * 10 * 8 * 130 * 4  # 76 clusters, 4 pairs
+    assert ws(10, 2, 8, 2, 15, 128, 1000) == 0                       # fewer than 8 pages a part
+    assert ws(8192, 4, 32, 8, 256, 128, 8) == 0                      # enough rows without parts
     assert capi.ss_attn_chunk_paged_units(1000, 7, 8, 2) == 2 * (1000 // 64 + 7) * 2
     assert capi.ss_attn_chunk_paged_units(1000, 7, 6, 2) == 2 * (1000 // 84 + 7) * 2
     assert capi.ss_attn_chunk_paged_units(10, 1, 258, 2) == 0

@@ -298,3 +298,28 @@ def test_chunk_and_append_beyond_32_bit_offsets():
     new, old = int(rowsT[2, 3]), far[0][3]
     assert new >= pages - 30 and new != old
     assert torch.equal(kp[new, :, :116], kp[old, :, :116]) and torch.equal(vp[new, :, :116], vp[old, :, :116])
+
+
+def test_chunk_counts_without_the_vote():
+    import block_sparse_attention_sm_gb300 as ss
+    from block_sparse_attention_sm_gb300 import capi
+
+    n, L = [3, 50], [300, 200]
+    q, k, v = make(4, 2, 64, n, L, 24)
+    table, pages = random_tables(L, 1, np.random.default_rng(3))
+    counts = torch.full((capi.ss_attn_chunk_paged_units(53, 2, 4, 2),), -1, dtype=torch.int32, device="cuda")
+    ss.chunk_paged(q.cuda(), fill_pool(k, L, table, pages).cuda(), fill_pool(v, L, table, pages).cuda(), table.cuda(),
+                   offsets(n).cuda(), torch.tensor(L, dtype=torch.int32, device="cuda"), scale=0.125, counts=counts)
+    assert (counts == 0).all()
+
+
+@pytest.mark.parametrize("a", [0.0, 4.0])
+def test_chunk_in_parts(a):
+    """Few new tokens over a long cache: the tiles are dealt to parts and merged."""
+    from block_sparse_attention_sm_gb300 import capi
+
+    n, L = [1, 4], [128 * 40 + 7, 128 * 33]
+    assert capi.ss_attn_chunk_paged_workspace_size(5, 2, 4, 1, 41, 128, 7) == 5 * 5 * 4 * 130 * 4  # 41 pages: 5 parts
+    check(4, 1, 128, n, L, a=a, splits=7, seed=31)
+    check(4, 1, 128, n, L, a=a, splits=7, seed=32, debug=False)
+    check(2, 2, 64, n, L, a=a, splits=3, seed=33, causal=False)
