@@ -264,7 +264,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   p.G = G;
   p.tpb = static_cast<int>(tpb);
   p.slots = static_cast<int>(slots);
-  p.S = num_kv_splits;
+  p.S = num_kv_splits < max_pages ? num_kv_splits : max_pages;  // (a range has a tile or more)
   p.parts = chunk_parts(slots * Hkv, num_kv_splits, max_pages);
   p.num_pages = num_pages;
   p.max_pages = max_pages;

@@ -311,7 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     u.last_shift = nT * kTile - len;
     u.range = max(1, (nT + p.S - 1) / p.S);
     // a part: whole ranges where there is a vote, otherwise an even share
-    const int per = kVote ? (p.S + p.parts - 1) / p.parts * u.range : (nT + p.parts - 1) / p.parts;
+    const int granule = kVote ? u.range : 1, n_granules = (nT + granule - 1) / granule;
+    const int per = (n_granules + p.parts - 1) / p.parts * granule;
     u.j0 = min(nT, u.part * per);
     u.j1 = min(nT, u.j0 + per);
     u.thr_raw = (p.lambda_a > 0.f && len > 0)  // lambda_b = min(1, a / L_b)

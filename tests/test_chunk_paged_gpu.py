@@ -323,3 +323,9 @@ def test_chunk_in_parts(a):
     check(4, 1, 128, n, L, a=a, splits=7, seed=31)
     check(4, 1, 128, n, L, a=a, splits=7, seed=32, debug=False)
     check(2, 2, 64, n, L, a=a, splits=3, seed=33, causal=False)
+
+
+@pytest.mark.parametrize("a", [0.0, 4.0])
+def test_chunk_of_more_ranges_than_tiles(a):
+    """Any count is allowed; beyond one range a tile nothing changes."""
+    check(8, 2, 64, [3], [128 * 20 + 5], a=a, splits=2 ** 31 - 1, seed=31)
