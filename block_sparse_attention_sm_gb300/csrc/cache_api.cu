@@ -2,7 +2,6 @@
 // new tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
 // Argument validation and launches; include/ssattn.h has each call's contract.
 #include <cmath>
-#include <cstring>
 
 #include "api.cuh"
 #include "chunk_paged.cuh"
@@ -35,6 +34,25 @@ ss_status turn_of(RopeTurn* t, const double* inv_freq, int rot, int off, int int
 }
 
 constexpr int kMaxRopeWidth = 1 << 16;
+// Rows and tokens are counted in 32 bits, a block's or a thread's share ahead.
+constexpr long kMaxRopeCount = 1l << 30;
+
+// Rows of d entries at these strides lie apart: each axis, from the smallest
+// stride on, steps over everything that the axes before it reach.
+bool rows_apart(const int64_t* stride, const int* size, int n, int d) {
+  __int128 reach = d;
+  bool used[3] = {false, false, false};
+  for (int k = 0; k < n; ++k) {
+    int next = -1;
+    for (int i = 0; i < n; ++i)
+      if (!used[i] && (next < 0 || stride[i] < stride[next])) next = i;
+    used[next] = true;
+    if (size[next] < 2) continue;
+    if (stride[next] < reach) return false;
+    reach += static_cast<__int128>(stride[next]) * (size[next] - 1);
+  }
+  return true;
+}
 
 }  // namespace
 }  // namespace ssattn
@@ -61,10 +79,11 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
   for (int i = 0; i < 3; ++i) {
     p.xs[i] = xs[i];
     p.os[i] = os[i];
-    // Rows of the output must not overlap; the input's may (a broadcast axis).
-    if (xs[i] < 0 || os[i] < 0 || (size[i] > 1 && os[i] < d)) return SS_ERR_INVALID_ARG;
-    if (x == out && size[i] > 1 && xs[i] != os[i]) return SS_ERR_INVALID_ARG;
+    if (xs[i] < 0 || os[i] < 0 || (x == out && size[i] > 1 && xs[i] != os[i])) return SS_ERR_INVALID_ARG;
   }
+  // Rows of the output must not overlap; the input's may (a broadcast axis).
+  if (!rows_apart(os, size, 3, d)) return SS_ERR_INVALID_ARG;
+  if (H > kMaxRopeCount || static_cast<long>(B) * L > kMaxRopeCount) return SS_ERR_UNSUPPORTED;
   if (x == nullptr || out == nullptr || positions == nullptr || !aligned2(x) || !aligned2(out) ||
       !aligned4(positions))
     return SS_ERR_INVALID_ARG;
@@ -97,6 +116,7 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
   bool vec = false;
   ss_status st = turn_of(&p.turn, inv_freq, rot_dim, rot_offset, interleaved, attn_factor, 0, d, &vec);
   if (st != SS_OK) return st;
+  if (T == 0) return SS_OK;
   if (k == nullptr || k_pages == nullptr || cu_seqlens == nullptr || seq_lens == nullptr ||
       page_table == nullptr || (q != nullptr && q_out == nullptr) || (v != nullptr && v_pages == nullptr))
     return SS_ERR_INVALID_ARG;
@@ -115,11 +135,12 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
     p.ks[i] = strides[2][i];
     p.vs[i] = v != nullptr ? strides[3][i] : 0;
     if (p.qs[i] < 0 || p.ks[i] < 0 || p.vs[i] < 0) return SS_ERR_INVALID_ARG;
-    if (q != nullptr && ((i == 0 ? T : Hq) > 1)) {
-      if (p.qos[i] < d || (q == q_out && p.qs[i] != p.qos[i])) return SS_ERR_INVALID_ARG;
-    }
+    if (q != nullptr && (p.qos[i] < 0 || (q == q_out && (i == 0 ? T : Hq) > 1 && p.qs[i] != p.qos[i])))
+      return SS_ERR_INVALID_ARG;
   }
-  if (T == 0) return SS_OK;
+  const int q_size[2] = {T, Hq};
+  if (q != nullptr && (!rows_apart(p.qos, q_size, 2, d) || q_out == k || q_out == v)) return SS_ERR_INVALID_ARG;
+  if (T > kMaxRopeCount || Hq + 2l * Hkv > kMaxRopeCount) return SS_ERR_UNSUPPORTED;
   if ((st = check_device()) != SS_OK) return st;
   vec = vec && aligned16(q) && aligned16(q_out) && aligned16(k) && aligned16(v) && all8(p.ks, 2) &&
         (q == nullptr || (all8(p.qs, 2) && all8(p.qos, 2))) && (v == nullptr || all8(p.vs, 2));
@@ -218,8 +239,8 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   if (d != 64 && d != 128) return SS_ERR_UNSUPPORTED;
   const int G = Hq / Hkv;
   if (G > kTile) return SS_ERR_UNSUPPORTED;
-  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || page_table == nullptr ||
-      cu_seqlens == nullptr || seq_lens == nullptr || o == nullptr)
+  if ((T > 0 && (q == nullptr || o == nullptr)) || k_pages == nullptr || v_pages == nullptr ||
+      page_table == nullptr || cu_seqlens == nullptr || seq_lens == nullptr)
     return SS_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(Hq) * d, stride = q_token_stride != 0 ? q_token_stride : row;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
@@ -234,9 +255,21 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   const size_t need = ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits);
   if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
     return SS_ERR_WORKSPACE;
-  if (T == 0) return SS_OK;
+  const bool outputs = skip_counts != nullptr || (dbg != nullptr && (dbg->skip_mask || dbg->vote_margin));
+  if (T == 0 && !outputs) return SS_OK;
   ss_status st = check_device();
   if (st != SS_OK) return st;
+  if (T == 0) {  // no tokens: every unit's outputs are those of one without tokens
+    const size_t units = 2 * static_cast<size_t>(slots) * Hkv, seen = units * max_pages;
+    const auto s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (skip_counts != nullptr) e = cudaMemsetAsync(skip_counts, 0, units * sizeof(uint32_t), s);
+    if (e == cudaSuccess && dbg != nullptr && dbg->skip_mask != nullptr)
+      e = cudaMemsetAsync(dbg->skip_mask, 2, seen, s);
+    if (e == cudaSuccess && dbg != nullptr && dbg->vote_margin != nullptr)
+      e = cudaMemsetAsync(dbg->vote_margin, 0xff, seen * sizeof(float), s);  // (all ones: a NaN)
+    return of(e);
+  }
 
   CUtensorMap tq, tk, tv;
   const long blocks = static_cast<long>(num_pages) * Hkv;

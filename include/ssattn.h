@@ -376,8 +376,8 @@ ss_status ss_attn_mla_decode_paged(const void* q, const void* kv_pages, const in
  * others single entries.
  * Returns SS_OK (also for an empty x), SS_ERR_INVALID_ARG (null pointer,
  * misalignment, odd rot_dim or one outside the row, strides that overlap
- * output rows, attn_factor not finite), SS_ERR_UNSUPPORTED (d > 65536, or the
- * device) or SS_ERR_CUDA.
+ * output rows, attn_factor not finite), SS_ERR_UNSUPPORTED (d > 65536, more
+ * than 2^30 heads or tokens, or the device) or SS_ERR_CUDA.
  */
 ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t x_batch_stride,
                   int64_t x_head_stride, int64_t x_token_stride, int64_t out_batch_stride,
@@ -390,10 +390,10 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
  * their keys and values into the cache:  q_out = rotate(q); row L_b - n_b + i
  * of sequence b's pages = rotate(k), v.
  *   q, q_out: bf16 [T][Hq][d] (q nullable: keys and values only; q_out may be
- *     q).  k, v: bf16 [T][Hkv][d] (v nullable: a cache of one row per token,
- *     as the latent one with Hkv = 1, d = 576, rot_offset = 512, rot_dim =
- *     64).  Strides in elements between tokens and heads: q, k and v may be
- *     parts of one projection.
+ *     q, otherwise it must not overlap an input).  k, v: bf16 [T][Hkv][d] (v
+ *     nullable: a cache of one row per token, as the latent one with Hkv = 1,
+ *     d = 576, rot_offset = 512, rot_dim = 64).  Strides in elements between
+ *     tokens and heads: q, k and v may be parts of one projection.
  *   positions: device int32 [T], nullable: the key's place L_b - n_b + i.
  *   rot_dim = 0: no rotation (inv_freq may be NULL).
  *   k_pages, v_pages: as in ss_attn_decode_paged ([num_pages][Hkv][128][d]).
@@ -443,7 +443,8 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
  * token of a sequence sees all its L_b keys).  Causal: new token i of sequence
  * b sees its keys up to L_b - n_b + i; a row that sees no key gives zeros.
  *   q: bf16 [T][Hq][d], 16-byte aligned; q_token_stride: elements between
- *     tokens (0: Hq * d; a multiple of 8).  o: bf16 [T][Hq][d] contiguous.
+ *     tokens (0: Hq * d; a multiple of 8).  o: bf16 [T][Hq][d] contiguous, not
+ *     overlapping an input.
  *   k_pages, v_pages, page_table, seq_lens, lambda_a: as in
  *     ss_attn_decode_paged (what a page holds behind its sequence's end is
  *     not read, whatever it is; keys and values of the sequence itself must

@@ -272,3 +272,36 @@ def test_pages_helpers_refuse():
                  lambda: ss.pages_copy(pools, one, one), lambda: ss.pages_reserve(**state, add=one)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=1, out_strides=(1024, 128, 128)), "INVALID_ARG"),      # heads and tokens on the same rows
+    (dict(out_strides=(1024, 256, 192)), "INVALID_ARG"),           # ... partly
+    (dict(out_strides=(1000, 128, 256)), "INVALID_ARG"),           # a batch inside the reach of 4 tokens, 1024
+    (dict(out_strides=(1 << 62, 1 << 61, 1 << 62)), "INVALID_ARG"),  # (the reach passes 64 bits)
+    (dict(H=(1 << 30) + 1), "UNSUPPORTED"), (dict(B=1 << 16, L=1 << 16), "UNSUPPORTED"),
+])
+def test_rope_rejects_overlap_and_counts(capi, kw, expect):
+    args = dict(x=FAKE, out=2 * FAKE, B=2, H=2, L=4, d=128, positions=FAKE, inv_freq=FAKE, rot_dim=128, stream=0)
+    if "out_strides" not in kw:
+        args["x_strides"] = (0, 0, 0)
+    assert capi.ss_rope(**{**args, **kw}) == getattr(capi, "SS_ERR_" + expect)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q_out_strides=(128, 128)), "INVALID_ARG"), (dict(q_out_strides=(1000, 128)), "INVALID_ARG"),
+    (dict(q_out=3 * FAKE), "INVALID_ARG"), (dict(q_out=4 * FAKE), "INVALID_ARG"), (dict(q_out_strides=(1024, -128)), "INVALID_ARG"),
+    (dict(T=(1 << 30) + 1), "UNSUPPORTED"), (dict(Hkv=1 << 30), "UNSUPPORTED"),
+    (dict(T=0, q=None, q_out=None, k=None, v=None, v_pages=None), "OK"),
+])
+def test_append_rejects_overlap_and_counts(capi, kw, expect):
+    args = dict(q=FAKE, q_out=2 * FAKE, k=3 * FAKE, v=4 * FAKE, T=5, B=2, Hq=8, Hkv=2, d=128, cu_seqlens=FAKE, seq_lens=FAKE,
+                inv_freq=FAKE, rot_dim=128, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, num_pages=4, max_pages=4, stream=0)
+    assert capi.ss_rope_append_paged(**{**args, **kw}) == getattr(capi, "SS_OK" if expect == "OK" else "SS_ERR_" + expect)
+
+
+def test_a_step_without_tokens_needs_no_rows(capi):
+    """The empty tensors of a step of no tokens have null addresses."""
+    assert capi.ss_attn_chunk_paged(q=None, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, cu_seqlens=FAKE, seq_lens=FAKE, o=None,
+                                    T=0, B=2, Hq=8, Hkv=2, num_pages=4, max_pages=64, d=128, scale=0.1, causal=True,
+                                    lambda_a=0.0, num_kv_splits=4, stream=0) == capi.SS_OK

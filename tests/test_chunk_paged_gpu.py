@@ -329,3 +329,28 @@ def test_chunk_in_parts(a):
 def test_chunk_of_more_ranges_than_tiles(a):
     """Any count is allowed; beyond one range a tile nothing changes."""
     check(8, 2, 64, [3], [128 * 20 + 5], a=a, splits=2 ** 31 - 1, seed=31)
+
+
+def test_chunk_and_append_of_no_tokens():
+    import block_sparse_attention_sm_gb300 as ss
+    from _parity import guarded
+    from block_sparse_attention_sm_gb300 import capi
+
+    L, Hq, Hkv, d = [100, 300], 4, 2, 64
+    pool = torch.ones(4, Hkv, PAGE, d, dtype=BF, device="cuda")
+    table = torch.tensor([[0, 1, 2], [1, 2, 3]], dtype=torch.int32, device="cuda")
+    cu, lens = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.tensor(L, dtype=torch.int32, device="cuda")
+    row = lambda h: torch.empty(0, h, d, dtype=BF, device="cuda")  # noqa: E731
+    freq, _ = ss.rope_frequencies(d)
+    assert ss.rope_append_paged(row(Hq), row(Hkv), row(Hkv), pool, pool.clone(), table, cu, lens, freq).shape == (0, Hq, d)
+    units = capi.ss_attn_chunk_paged_units(0, 2, Hq, Hkv)
+    bands = [guarded((units,), torch.int32, "cuda", -1), guarded((units, 3), torch.uint8, "cuda", 9),
+             guarded((units, 3), torch.float32, "cuda", 5.0)]
+    for a in (0.0, 2.0):
+        o = ss.chunk_paged(row(Hq), pool, pool, table, cu, lens, scale=0.1, lambda_a=a, num_kv_splits=2, counts=bands[0].t,
+                           skip_mask=bands[1].t, vote_margin=bands[2].t)
+        assert o.shape == (0, Hq, d)
+        assert (bands[0].t == 0).all() and (bands[1].t == 2).all() and bands[2].t.isnan().all()
+    for x in bands:
+        x.check("chunk of no tokens")
+    assert (pool == 1).all() and capi.ss_stream_status() == capi.SS_OK
