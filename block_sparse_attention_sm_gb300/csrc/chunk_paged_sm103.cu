@@ -58,10 +58,10 @@
 // a value tile is an out-of-range box).
 //
 // What bounds it (measured on GB300; 4 x 2048 new tokens over 32K keys, 32 / 8
-// heads of 128).  Dense: 2.85 ms, 1490 TFLOP/s, 77% of the cuBLAS rate; the
+// heads of 128).  Dense: 2.86 ms, 1490 TFLOP/s, 77% of the cuBLAS rate; the
 // P.V issuer is busy throughout (8 two-SM MMAs take ~900 cycles beside the
 // other issuer's, and ~500 go to barriers and commits).  With the skip test at
-// ~88% skipped tiles: 1.98 ms; a tile's scores pass through MMA, commit, load,
+// ~88% skipped tiles: 1.94 ms; a tile's scores pass through MMA, commit, load,
 // vote and two barriers (~2900 cycles) and TMEM holds three of them.  Short
 // units: ~3 us each beside their tiles (608 units of 16 tiles: 139 us, 4.6
 // TB/s).  Instructions matter: a unit's code runs out of the instruction cache,
@@ -733,9 +733,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int shift = (j == u.last) ? u.last_shift : 0;
         const int first = shift - 64 * hf, vis = lim - (j * kTile - first);
         if (first > 0 || vis < 63) {
+          // bit e: column e is seen (a bit test a column; two comparisons: 406 us
+          // for the mixed step of 48 sequences, so 399)
+          const uint64_t upto = vis >= 63 ? ~0ull : vis < 0 ? 0ull : (2ull << vis) - 1;
+          const uint64_t seen = upto & (first >= 64 ? 0ull : first > 0 ? ~0ull << first : ~0ull);
+          const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < first || e > vis) sr[e] = __float_as_uint(-INFINITY);
+          for (int e = 0; e < 32; ++e) {
+            if (!(lo & (1u << e))) sr[e] = __float_as_uint(-INFINITY);
+            if (!(hi & (1u << e))) sr[32 + e] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[4];
 #pragma unroll
@@ -778,8 +785,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t sr[64];
         float tmax = -INFINITY;
         if (mine) {
+          const bool masked = j == u.last || lim < j * kTile + kTile - 1;
+          if ((kVote || DQK == 64) && !__any_sync(0xffffffffu, masked)) {
+            // No lane of the warp masks a column: all 128 at once.  With the vote most
+            // tiles end here, at d = 64 the matrix work is short: one wait for the
+            // loads instead of two (4 x 2K on 32K with the skip test 1.98 -> 1.95 ms,
+            // mixed step 414 -> 406 us, cross attention 45 -> 43 us).  The dense path
+            // at d = 128 is bound elsewhere and loses 4% to the larger code.
+            uint32_t s0[64];
+            tmem_ld32p(colS, s0);
+            tmem_ld32p(colS + 32, s0 + 32);
+            tmem_ld32p(colS + 64, sr);
+            tmem_ld32p(colS + 96, sr + 32);
+            tmem_wait_ld();
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(s0[2 * e]), __uint_as_float(s0[2 * e + 1]));
+              mx[(e + 2) & 3] = fmax3(mx[(e + 2) & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+            }
+            tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          } else {
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) tmax = fmaxf(tmax, load_half(colS, j, hf, sr));  // sr keeps the second half
+            for (int hf = 0; hf < 2; ++hf) tmax = fmaxf(tmax, load_half(colS, j, hf, sr));  // sr keeps the second half
+          }
           if (!row_valid) tmax = -INFINITY;
         }
         // The state after the previous tile, from the other warpgroup.
