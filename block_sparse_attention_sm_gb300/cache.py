@@ -304,6 +304,8 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
                     raise ValueError(f"{name}: needs at least {need} elements, has {t.numel()}")
     if out is not None:
         _dense("out", out, _BF16, None, shape)
+        if T > 0 and out.data_ptr() == q.data_ptr():
+            raise ValueError("out: overlaps q (blocks of queries are read again by other clusters)")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     handle, context = _on(stream, "q k_pages v_pages page_table cu_seqlens seq_lens out counts workspace skip_mask vote_margin",

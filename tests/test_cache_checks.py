@@ -305,3 +305,10 @@ def test_a_step_without_tokens_needs_no_rows(capi):
     assert capi.ss_attn_chunk_paged(q=None, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, cu_seqlens=FAKE, seq_lens=FAKE, o=None,
                                     T=0, B=2, Hq=8, Hkv=2, num_pages=4, max_pages=64, d=128, scale=0.1, causal=True,
                                     lambda_a=0.0, num_kv_splits=4, stream=0) == capi.SS_OK
+
+
+def test_chunk_helper_refuses_its_queries_as_output():
+    q = _z(5, 4, 64)
+    with pytest.raises(ValueError, match="overlaps q"):
+        ss.chunk_paged(q, _z(3, 2, 128, 64), _z(3, 2, 128, 64), _z(2, 4, dtype=I32), _z(3, dtype=I32), _z(2, dtype=I32),
+                       scale=0.1, out=q)
