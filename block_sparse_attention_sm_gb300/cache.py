@@ -275,7 +275,7 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
     """Attention of a step's packed new tokens over the paged cache, with the skip test.
 
     q [T,Hq,d] bf16 CUDA (heads contiguous within a token; the tokens' stride
-    a multiple of 8), k_pages / v_pages [num_pages,Hkv,128,d], page_table int32
+    a multiple of 8, at least Hq * d: not broadcast), k_pages / v_pages [num_pages,Hkv,128,d], page_table int32
     [B,max_pages], cu_seqlens int32 [B+1], seq_lens int32 [B] (keys per
     sequence, the new ones included).  Causal: new token i of sequence b sees
     keys up to L_b - n_b + i; otherwise all L_b (cross attention).  lambda_a:
@@ -287,6 +287,8 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
     T, Hq, d = shape
     if Hq > 1 and qs[1] != d:
         raise ValueError("q: the heads of a token must be contiguous")
+    if T > 1 and qs[0] < Hq * d:  # (a stride of 0, of a broadcast row, would mean contiguous rows to the entry point)
+        raise ValueError(f"q: its tokens overlap (stride {qs[0]}, rows of {Hq * d})")
     B, max_pages = _batch(page_table, cu_seqlens, seq_lens)
     _dense("k_pages", k_pages, _BF16, 4)
     pool = k_pages.shape

@@ -312,3 +312,20 @@ def test_chunk_helper_refuses_its_queries_as_output():
     with pytest.raises(ValueError, match="overlaps q"):
         ss.chunk_paged(q, _z(3, 2, 128, 64), _z(3, 2, 128, 64), _z(2, 4, dtype=I32), _z(3, dtype=I32), _z(2, dtype=I32),
                        scale=0.1, out=q)
+
+
+@pytest.mark.parametrize("q", [
+    _z(1, 4, 64).expand(5, 4, 64),                      # one row for all tokens
+    _z(2000).as_strided((5, 4, 64), (128, 64, 1)),      # a token's last heads are the next one's first
+    _z(2000).as_strided((5, 1, 64), (8, 64, 1)),
+])
+def test_chunk_helper_refuses_queries_whose_tokens_overlap(q):
+    """A token stride of 0 means contiguous rows to the entry point, which would read behind such a tensor."""
+    with pytest.raises(ValueError, match="tokens overlap"):
+        ss.chunk_paged(q, _z(3, 1, 128, 64), _z(3, 1, 128, 64), _z(2, 4, dtype=I32), _z(3, dtype=I32), _z(2, dtype=I32), scale=0.1)
+
+
+def test_chunk_helper_takes_one_token_of_any_stride():
+    with pytest.raises(ValueError, match="CUDA tensor"):  # (the last check)
+        ss.chunk_paged(_z(2000).as_strided((1, 4, 64), (0, 64, 1)), _z(3, 1, 128, 64), _z(3, 1, 128, 64), _z(2, 4, dtype=I32),
+                       _z(3, dtype=I32), _z(2, dtype=I32), scale=0.1)
