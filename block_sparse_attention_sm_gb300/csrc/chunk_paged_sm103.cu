@@ -823,17 +823,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m_ref = hs.y;
           }
         }
-        bool kept = false, resc = false;
+        bool kept = false, resc = false, first = false;
         float alpha = 1.f;
         if constexpr (kVote) {
           // A range of the vote starts without a running maximum.
-          if (in_range == 0) m_true = -INFINITY;
+          first = in_range == 0;
+          if (first) m_true = -INFINITY;
           in_range += 2;
           while (in_range >= u.range) in_range -= u.range;
         }
         if (mine) {
           // Skip vote: every row of the block must pass exp(scale*(tile_max - m)) < lambda.
-          float c = -INFINITY;
+          // No row passes at a range's first tile.  (Some row sees a key there; but if the rows
+          // are all NaN, which the maximum drops, no other tile is kept, and they stay NaN.)
+          float c = first ? INFINITY : -INFINITY;
           if (tmax != -INFINITY) c = (m_true == -INFINITY) ? INFINITY : tmax - m_true;
           if constexpr (kVote) {
             kept = !named_bar_and(bar_vote, 128, c < u.thr_raw);
@@ -954,7 +957,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (u.n_pair > 0) {
         if (!wwait(&ctl->summed[fs], (uc >> 2) & 1)) ok = false;
         const float2 other = ctl->fin[fs][row];
-        if (other.x != -INFINITY) l_row += other.y * ex2_approx((other.x - m_ref) * sl2);
+        // (A sum of zero may stand against no maximum; that of a NaN row is NaN.)
+        if (other.y != 0.f) l_row += other.y * ex2_approx((other.x - m_ref) * sl2);
         if (!wwait(&ctl->o_full, uc & 1)) ok = false;
         ++uc;
         tc_fence_after();

@@ -354,3 +354,47 @@ def test_chunk_and_append_of_no_tokens():
     for x in bands:
         x.check("chunk of no tokens")
     assert (pool == 1).all() and capi.ss_stream_status() == capi.SS_OK
+
+
+@pytest.mark.parametrize("a", [0.0, 4.0])
+@pytest.mark.parametrize("Hq,Hkv,d,n,L,splits,spoilt", [
+    (4, 1, 128, [1, 1], [128 * 9 + 5, 700], 1, [0]),           # a decoded token: its heads are its block's only rows
+    (4, 1, 128, [2, 1], [128 * 8, 700], 1, [0, 1]),            # an even number of tiles
+    (2, 2, 64, [1, 3], [128 * 6 + 1, 700], 3, [0]),            # one head a group, ranges of the vote
+    (1, 1, 128, [130], [1500], 1, list(range(128))),           # the first block of a pair
+    (1, 1, 128, [130], [1400], 2, [128, 129]),                 # the second
+    (4, 1, 128, [1, 4], [128 * 40 + 7, 128 * 33], 7, [0]),     # dealt to parts
+    (4, 1, 128, [1, 4], [128 * 40 + 7, 128 * 33], 7, [1, 2, 3, 4]),
+])
+def test_chunk_nan_queries_that_fill_a_block(Hq, Hkv, d, n, L, splits, spoilt, a):
+    """NaN rows alone in their block give NaN, not the zeros of a row without keys, and leave the others alone."""
+    import block_sparse_attention_sm_gb300 as ss
+    from block_sparse_attention_sm_gb300 import capi
+
+    q, k, v = make(Hq, Hkv, d, n, L, 41)
+    table, pages = random_tables(L, 1, np.random.default_rng(3))
+    T, B, width = sum(n), len(n), table.shape[1]
+    args = (fill_pool(k, L, table, pages).cuda(), fill_pool(v, L, table, pages).cuda(), table.cuda(), offsets(n).cuda(),
+            torch.tensor(L, dtype=torch.int32, device="cuda"))
+    kw = dict(scale=d ** -0.5, lambda_a=a, num_kv_splits=splits)
+    clean = ss.chunk_paged(q.cuda(), *args, **kw)
+    bad = q.clone()
+    bad[spoilt] = float("nan")
+    got = ss.chunk_paged(bad.cuda(), *args, **kw)
+    assert got[spoilt].isnan().all()
+    rest = [t for t in range(T) if t not in spoilt]
+    assert torch.equal(got[rest], clean[rest])
+    # the first tile of a range is kept, whatever the rows hold
+    units = capi.ss_attn_chunk_paged_units(T, B, Hq, Hkv)
+    mask = torch.full((units, width), 9, dtype=torch.uint8, device="cuda")
+    margin = torch.zeros(units, width, device="cuda")
+    ss.chunk_paged(bad.cuda(), *args, **kw, skip_mask=mask, vote_margin=margin)
+    cu = offsets(n).tolist()
+    b = next(b for b in range(B) if cu[b] <= spoilt[0] < cu[b + 1])
+    place, half, places = chunk_place(cu, b, (spoilt[0] - cu[b]) // (PAGE // (Hq // Hkv)), Hq // Hkv, T, B)
+    per = -(-tiles(L[b]) // splits)
+    for h in range(Hkv):
+        unit = (h * places + place) * 2 + half
+        for j in range(0, tiles(L[b]), per):
+            assert int(mask[unit, j]) == 0 and float(margin[unit, j]) == math.inf
+    assert capi.ss_stream_status() == capi.SS_OK
