@@ -198,7 +198,7 @@ def _batch(page_table, cu_seqlens, seq_lens):
 
 def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_lens, inv_freq=None, *,
                       positions=None, rot_offset: int = 0, interleaved: bool = False, attn_factor: float = 1.0,
-                      out=None, stream=None):
+                      out=None, refused=None, stream=None):
     """Rotates a step's packed new tokens and writes their keys and values into the cache.
 
     q [T,Hq,d] (or None), k and v [T,Hkv,d] (v None: one row per token, as the
@@ -208,6 +208,9 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
     cu_seqlens[b] .. of the step, is key seq_lens[b] - n_b + i (seq_lens
     include the new tokens) and takes that as its position unless
     ``positions`` int32 [T] says otherwise.  inv_freq None: no rotation.
+    ``refused`` (int32 [1] on the device): what :func:`pages_reserve` returned
+    for this step; where it is not 0 the call does nothing (the lengths then do
+    not include the new tokens, which would overwrite the newest cached ones).
     Returns the rotated q (``out``; ``out=q``: in place), rows behind the last
     sequence left as they were, or None without q."""
     (T, Hkv, d), ks = _rows("k", k, 3)
@@ -244,20 +247,23 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
         if q is None:
             raise ValueError("out without q")
         _output("out", out, q, q_shape)
-    handle, context = _on(stream, "k q v k_pages v_pages page_table cu_seqlens seq_lens inv_freq positions out", k, q, v,
-                          k_pages, v_pages, page_table, cu_seqlens, seq_lens, inv_freq, positions, out)
+    if refused is not None:
+        _dense("refused", refused, _I32, None, (1,))
+    handle, context = _on(stream, "k q v k_pages v_pages page_table cu_seqlens seq_lens inv_freq positions out refused", k, q, v,
+                          k_pages, v_pages, page_table, cu_seqlens, seq_lens, inv_freq, positions, out, refused)
     with context:
         o = out
         if q is not None:
             if o is None:
                 o = torch.empty(q_shape, dtype=_BF16, device=q.device)
             os_ = o.stride()
-        st = (capi._lib or capi.load()).ss_rope_append_paged(
+        st = (capi._lib or capi.load()).ss_rope_append_paged_ex(
             q.data_ptr() if q is not None else None, o.data_ptr() if q is not None else None, k.data_ptr(),
             v.data_ptr() if v is not None else None, qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], T, B, Hq,
             Hkv, d, cu_seqlens.data_ptr(), seq_lens.data_ptr(), positions.data_ptr() if positions is not None else None,
             inv_freq.data_ptr() if rot else None, rot, rot_offset, bool(interleaved), attn_factor, k_pages.data_ptr(),
-            v_pages.data_ptr() if v is not None else None, page_table.data_ptr(), pool[0], max_pages, handle)
+            v_pages.data_ptr() if v is not None else None, page_table.data_ptr(), pool[0], max_pages,
+            refused.data_ptr() if refused is not None else None, handle)
     if st:
         raise SSError(st, "ss_rope_append_paged")
     return o
@@ -377,7 +383,8 @@ def pages_reserve(page_refs, page_table, seq_lens, add, *, rows=None, result=Non
     They receive the lowest free pages of page_refs (int32 [num_pages], holders
     of each page, 0 free), in order; seq_lens is raised.  Returns ``result``,
     an int32 [1] on the device: 0, the number of pages that are missing, or -1
-    for wrong arguments (then nothing has changed)."""
+    for wrong arguments (then nothing has changed, the lengths neither: give it
+    to :func:`rope_append_paged` as ``refused``)."""
     num_pages, num_rows, max_pages = _state(page_refs, page_table, seq_lens)
     n = _list("add", add)
     if rows is not None:

@@ -27,7 +27,7 @@ EXPORTS = (
     "ss_attn_mla_decode_workspace_size", "ss_attn_mla_decode", "ss_attn_mla_decode_ex",
     "ss_attn_mla_decode_paged",
     "ss_calibrate", "ss_fit_factor", "ss_lambda", "ss_status_string", "ss_stream_status",
-    "ss_rope", "ss_rope_append_paged", "ss_rope_frequencies",
+    "ss_rope", "ss_rope_append_paged", "ss_rope_append_paged_ex", "ss_rope_frequencies",
     "ss_attn_chunk_paged", "ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
     "ss_pages_workspace_size", "ss_pages_reserve", "ss_pages_free", "ss_pages_fork",
     "ss_pages_copy", "ss_pages_compact",
@@ -101,7 +101,9 @@ def load() -> ctypes.CDLL:
     lib.ss_stream_status.argtypes = [P]
     I64, D = ctypes.c_int64, ctypes.c_double
     lib.ss_rope.argtypes = [P, P, I, I, I, I] + [I64] * 6 + [P, I64, P, I, I, I, I, F, P]
-    lib.ss_rope_append_paged.argtypes = [P] * 4 + [I64] * 8 + [I] * 5 + [P] * 4 + [I, I, I, F, P, P, P, I, I, P]
+    append = [P] * 4 + [I64] * 8 + [I] * 5 + [P] * 4 + [I, I, I, F, P, P, P, I, I]
+    lib.ss_rope_append_paged.argtypes = append + [P]
+    lib.ss_rope_append_paged_ex.argtypes = append + [P, P]
     lib.ss_rope_frequencies.argtypes = [P, I, D, I, D, I, D, D, ctypes.POINTER(F)]
     lib.ss_attn_chunk_paged.argtypes = [P, I64, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, F, I, P, P,
                                         U, ctypes.POINTER(ss_debug_opts), P]
@@ -122,7 +124,7 @@ def load() -> ctypes.CDLL:
                  "ss_attn_decode_noalloc", "ss_attn_decode_paged", "ss_attn_mla_decode",
                  "ss_attn_mla_decode_ex", "ss_attn_mla_decode_paged", "ss_calibrate",
                  "ss_fit_factor", "ss_stream_status", "ss_rope", "ss_rope_append_paged",
-                 "ss_rope_frequencies", "ss_attn_chunk_paged", "ss_pages_reserve", "ss_pages_free",
+                 "ss_rope_append_paged_ex", "ss_rope_frequencies", "ss_attn_chunk_paged", "ss_pages_reserve", "ss_pages_free",
                  "ss_pages_fork", "ss_pages_copy", "ss_pages_compact"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -335,6 +337,19 @@ def ss_rope_append_paged(q, q_out, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens,
         *(k_strides or k_dense), *(v_strides or k_dense), T, B, Hq, Hkv, d, _ptr(cu_seqlens), _ptr(seq_lens),
         _ptr(positions), _ptr(inv_freq), rot_dim, rot_offset, bool(interleaved), attn_factor, _ptr(k_pages),
         _ptr(v_pages), _ptr(page_table), num_pages, max_pages, _stream(stream))
+
+
+def ss_rope_append_paged_ex(q, q_out, k, v, T, B, Hq, Hkv, d, cu_seqlens, seq_lens, inv_freq, rot_dim,
+                            k_pages, v_pages, page_table, num_pages, max_pages, positions=None,
+                            q_strides=None, q_out_strides=None, k_strides=None, v_strides=None,
+                            rot_offset=0, interleaved=False, attn_factor=1.0, refused=None, stream=None) -> int:
+    """ss_rope_append_paged that does nothing where the device int32 ``refused`` is not 0."""
+    q_dense, k_dense = (Hq * d, d), (Hkv * d, d)
+    return (_lib or load()).ss_rope_append_paged_ex(
+        _ptr(q), _ptr(q_out), _ptr(k), _ptr(v), *(q_strides or q_dense), *(q_out_strides or q_dense),
+        *(k_strides or k_dense), *(v_strides or k_dense), T, B, Hq, Hkv, d, _ptr(cu_seqlens), _ptr(seq_lens),
+        _ptr(positions), _ptr(inv_freq), rot_dim, rot_offset, bool(interleaved), attn_factor, _ptr(k_pages),
+        _ptr(v_pages), _ptr(page_table), num_pages, max_pages, _ptr(refused), _stream(stream))
 
 
 def ss_rope_frequencies(rot_dim, base=10000.0, scaling=SS_ROPE_PLAIN, factor=1.0, original_length=0,

@@ -100,15 +100,15 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
   return of(launch_rope(p, vec, static_cast<cudaStream_t>(stream)));
 }
 
-ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
-                               int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
-                               int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
-                               int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
-                               int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
-                               const int32_t* positions, const double* inv_freq, int rot_dim,
-                               int rot_offset, int interleaved, float attn_factor, void* k_pages,
-                               void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
-                               void* stream) {
+ss_status ss_rope_append_paged_ex(const void* q, void* q_out, const void* k, const void* v,
+                                  int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
+                                  int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                  int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
+                                  int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                  const int32_t* positions, const double* inv_freq, int rot_dim,
+                                  int rot_offset, int interleaved, float attn_factor, void* k_pages,
+                                  void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
+                                  const int32_t* refused, void* stream) {
   if (T < 0 || B < 1 || Hkv < 1 || d < 1 || (q != nullptr && Hq < 1) || num_pages < 1 || max_pages < 1)
     return SS_ERR_INVALID_ARG;
   if (d > kMaxRopeWidth) return SS_ERR_UNSUPPORTED;
@@ -122,7 +122,7 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
     return SS_ERR_INVALID_ARG;
   if (!aligned2(q) || !aligned2(q_out) || !aligned2(k) || !aligned2(v) || !aligned16(k_pages) ||
       !aligned16(v_pages) || !aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(positions) ||
-      !aligned4(page_table))
+      !aligned4(page_table) || !aligned4(refused))
     return SS_ERR_INVALID_ARG;
   if (static_cast<long>(max_pages) * kTile > 0x7fffffffL) return SS_ERR_INVALID_ARG;
   const int64_t strides[4][2] = {{q_token_stride, q_head_stride},
@@ -154,6 +154,7 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
   p.seq_lens = seq_lens;
   p.pos = positions;
   p.page_table = page_table;
+  p.refused = refused;
   p.T = T;
   p.B = B;
   p.Hq = q != nullptr ? Hq : 0;
@@ -162,6 +163,21 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   return of(launch_rope_append(p, vec, static_cast<cudaStream_t>(stream)));
+}
+
+ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
+                               int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
+                               int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                               int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
+                               int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* positions, const double* inv_freq, int rot_dim,
+                               int rot_offset, int interleaved, float attn_factor, void* k_pages,
+                               void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
+                               void* stream) {
+  return ss_rope_append_paged_ex(q, q_out, k, v, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride,
+                                 k_token_stride, k_head_stride, v_token_stride, v_head_stride, T, B, Hq, Hkv, d,
+                                 cu_seqlens, seq_lens, positions, inv_freq, rot_dim, rot_offset, interleaved,
+                                 attn_factor, k_pages, v_pages, page_table, num_pages, max_pages, nullptr, stream);
 }
 
 ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_scaling scaling,

@@ -30,6 +30,7 @@ struct AppendParams {
   __nv_bfloat16 *q_out, *k_pages, *v_pages;
   long qs[2], qos[2], ks[2], vs[2];  // (token, head)
   const int32_t *cu_seqlens, *seq_lens, *pos, *page_table;  // pos nullable
+  const int32_t* refused;  // nullable: nothing is done where it is not 0
   int T, B, Hq, Hkv, d, num_pages, max_pages;
   RopeTurn turn;
 };

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsRope)
     if (end > t0 && end < t0 + TB) atomicAdd(&marks[end - t0], 1);
     before += __syncthreads_count(end <= t0);
   }
-  // Position and place of each of them; row -1: a token of no sequence.
+  // Position and place of each of them; row -1: a token of no sequence (or a refused step's).
   const int here = min(TB, p.T - t0);
   if (tid < here) {
     int b = before;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreadsRope)
     row[tid] = -1;
     pos[tid] = 0;
     page[tid] = -1;
-    if (b < p.B && tt >= p.cu_seqlens[b]) {
+    if (b < p.B && tt >= p.cu_seqlens[b] && (p.refused == nullptr || *p.refused == 0)) {
       const long slot = static_cast<long>(p.seq_lens[b]) - (p.cu_seqlens[b + 1] - tt);
       pos[tid] = p.pos != nullptr ? p.pos[tt] : static_cast<int>(slot);
       row[tid] = static_cast<int>(slot & (kTile - 1));

@@ -400,7 +400,13 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
  * A key whose place lies outside its table row, or whose page entry is
  * outside [0, num_pages), is not written (its q is rotated all the same).
  * Two new tokens never share a place as long as the table names each page
- * once.  Returns as ss_rope.
+ * once.  The lengths must include the new tokens: after a refused
+ * ss_pages_reserve they do not, and the places L_b - n_b + i would be those of
+ * the newest cached keys, in pages that other sequences may share.  The _ex
+ * form takes that call's `result` as `refused` (nullable device int32) and does
+ * nothing at all where it is not 0, so that a step needs no host round trip
+ * between the two; what the step computes after that has no meaning and is to
+ * be dropped once the result has been read.  Returns as ss_rope.
  */
 ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const void* v,
                                int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
@@ -411,6 +417,16 @@ ss_status ss_rope_append_paged(const void* q, void* q_out, const void* k, const 
                                int rot_offset, int interleaved, float attn_factor, void* k_pages,
                                void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
                                void* stream);
+
+ss_status ss_rope_append_paged_ex(const void* q, void* q_out, const void* k, const void* v,
+                                  int64_t q_token_stride, int64_t q_head_stride, int64_t q_out_token_stride,
+                                  int64_t q_out_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                  int64_t v_token_stride, int64_t v_head_stride, int T, int B, int Hq,
+                                  int Hkv, int d, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                  const int32_t* positions, const double* inv_freq, int rot_dim,
+                                  int rot_offset, int interleaved, float attn_factor, void* k_pages,
+                                  void* v_pages, const int32_t* page_table, int num_pages, int max_pages,
+                                  const int32_t* refused, void* stream);
 
 /* How ss_rope_frequencies stretches positions for contexts `factor` times the
    original length; w_i = base^(-2i / rot_dim). */
@@ -495,7 +511,8 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
  * this call alone until it has run.
  * `result` (nullable device int32): 0 done; k > 0: refused, k free pages are
  * missing; -1: refused, an argument on the device is wrong (below).  A refused
- * call changes nothing.
+ * call changes nothing, so a step that grows its sequences must not go on as if
+ * it had (ss_rope_append_paged_ex takes the result for that).
  * All return SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED (device),
  * SS_ERR_WORKSPACE or SS_ERR_CUDA; device memory beyond the given sizes is
  * never touched, whatever the device arrays hold.

@@ -329,3 +329,19 @@ def test_chunk_helper_takes_one_token_of_any_stride():
     with pytest.raises(ValueError, match="CUDA tensor"):  # (the last check)
         ss.chunk_paged(_z(2000).as_strided((1, 4, 64), (0, 64, 1)), _z(3, 1, 128, 64), _z(3, 1, 128, 64), _z(2, 4, dtype=I32),
                        _z(3, dtype=I32), _z(2, dtype=I32), scale=0.1)
+
+
+def test_append_ex_rejects_like_append(capi):
+    args = dict(q=FAKE, q_out=2 * FAKE, k=3 * FAKE, v=4 * FAKE, T=5, B=2, Hq=8, Hkv=2, d=128, cu_seqlens=FAKE, seq_lens=FAKE,
+                inv_freq=FAKE, rot_dim=128, k_pages=FAKE, v_pages=FAKE, page_table=FAKE, num_pages=4, max_pages=4, stream=0)
+    for kw in (dict(refused=FAKE + 2), dict(k=None), dict(q_out=3 * FAKE), dict(max_pages=0)):
+        assert capi.ss_rope_append_paged_ex(**{**args, **kw}) == capi.SS_ERR_INVALID_ARG
+    assert capi.ss_rope_append_paged_ex(**{**args, "T": 0, "refused": FAKE}) == capi.SS_OK
+
+
+def test_append_helper_refuses_other_results():
+    args = dict(q=None, k=_z(5, 2, 64), v=_z(5, 2, 64), k_pages=_z(3, 2, 128, 64), v_pages=_z(3, 2, 128, 64),
+                page_table=_z(2, 4, dtype=I32), cu_seqlens=_z(3, dtype=I32), seq_lens=_z(2, dtype=I32), inv_freq=FREQ)
+    for refused, match in ((_z(1), "refused: element type"), (_z(2, dtype=I32), "refused: expected shape"), (0, "refused: expected a torch")):
+        with pytest.raises((ValueError, TypeError), match=match):
+            ss.rope_append_paged(**args, refused=refused)

@@ -213,3 +213,59 @@ def test_captured_and_replayed():
             assert (a.item(), b.item(), live.item()) == (0, 0, 3)
             assert int(refs.sum()) == 0 and int(lens.sum()) == 0
     ss.stream_status()
+
+
+def test_refused_step_leaves_the_cache_alone():
+    """A captured step whose reserve is refused writes nothing, though its places would lie in shared pages; it is
+    replayed until the pages are there."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    freq, _ = ss.rope_frequencies(D)
+    kp = torch.randn(4, HKV, PAGE, D, device="cuda").to(BF)
+    vp = torch.randn_like(kp)
+    refs, table, lens = ints([0] * 4), ints([[-1] * 4] * 3), ints([0] * 3)
+    assert ss.pages_reserve(refs, table, lens, ints([256, 0, 200])).item() == 0
+    assert ss.pages_fork([kp, vp], refs, table, lens, ints([0]), ints([1])).item() == 0  # two full pages are shared
+    assert refs.tolist() == [2, 2, 1, 1]
+    add, cu = ints([2, 1, 0]), ints([0, 2, 3, 3])
+    proj = torch.randn(3, HQ + 2 * HKV, D, device="cuda").to(BF)
+    q, k, v = proj.split([HQ, HKV, HKV], 1)
+    out = torch.full((3, HQ, D), 9.0, dtype=BF, device="cuda")
+
+    def step():
+        refused = ss.pages_reserve(refs, table, lens, add)
+        ss.rope_append_paged(q, k, v, kp, vp, table, cu, lens, freq, out=out, refused=refused)
+        return refused, ss.chunk_paged(out, kp, vp, table, cu, lens, scale=D ** -0.5)
+
+    before = [x.clone() for x in (kp, vp, refs, table, lens, out)]
+    same = lambda: all(torch.equal(a, b) for a, b in zip(before, (kp, vp, refs, table, lens, out)))  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        refused, _ = step()
+    torch.cuda.synchronize()
+    assert refused.item() == 2 and same()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        refused, o = step()
+    g.replay()
+    assert refused.item() == 2 and same()
+    add[1] = -1  # a wrong argument is a refusal too
+    g.replay()
+    assert refused.item() == -1 and same()
+    add[1] = 1
+    ss.pages_free(refs, table, lens, ints([2]))
+    g.replay()
+    assert refused.item() == 0 and lens.tolist() == [258, 257, 0] and refs.tolist() == [2, 2, 1, 1]
+    assert torch.equal(kp[:2], before[0][:2]) and torch.equal(vp[:2], before[1][:2])
+    turned = rotate(proj.cpu()[:, :HQ + HKV], torch.tensor([256, 257, 256])[:, None], freq.cpu(), 1.0, 0, False)
+    assert (out.cpu().double() - turned[:, :HQ]).abs().max() <= 2.0 ** -8 * turned.abs().max()
+    for t, (b, i) in enumerate(((0, 256), (0, 257), (1, 256))):
+        page = int(table[b, 2])
+        assert (kp[page, :, i - 256].cpu().double() - turned[t, HQ:]).abs().max() <= 2.0 ** -8 * turned.abs().max()
+        assert torch.equal(vp[page, :, i - 256], v[t])
+    for b, (t0, t1, L) in enumerate(((0, 2, 258), (2, 3, 257))):
+        rows = [x[table[b, :3].long()].transpose(0, 1).reshape(HKV, -1, D)[:, :L].cpu() for x in (kp, vp)]
+        ref, weight, _ = chunk_reference(out[t0:t1].cpu(), *rows, L, D ** -0.5, True, 0.0, 1)
+        assert_attention(o[t0:t1].cpu(), ref, weight, f"row {b}")
+    ss.stream_status()
