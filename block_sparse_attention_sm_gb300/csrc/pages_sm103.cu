@@ -128,7 +128,7 @@ __device__ __forceinline__ bool has_bit(const uint32_t* bits, int i) {
 
 // Clears both bit sets, marks `src` (nullable) in the first and `dst` in the
 // second; true if an index is out of range, `dst` has one twice, or one of
-// `dst` is also in `src`.  (allow_self: dst[i] == src[i] is a copy of nothing.)
+// `dst` is also in `src` (a page or row copied over itself too).
 __device__ bool bad_indices(uint32_t* bits, long words, const int32_t* src, const int32_t* dst, int n,
                             int limit) {
   for (long w = threadIdx.x; w < 2 * words; w += kPlan) bits[w] = 0;
@@ -290,15 +290,15 @@ __global__ void __launch_bounds__(kPlan)
   }
 }
 
-// Blocks of entry i: one for its table row (first launch only), then one per
-// (pool, chunk of a page).
+// Blocks of entry i (of those from `entry0` on): one for its table row (with
+// the first pools only), then one per (pool, chunk of a page).
 __global__ void __launch_bounds__(kCopy)
     fork_apply_kernel(const PageState s, const int32_t* src, const int32_t* dst, Plan plan,
-                      const PagePools pools, int chunks, int rows_too) {
+                      const PagePools pools, int chunks, int rows_too, int entry0) {
   if (plan.head[1] == 0) return;
-  const int per = pools.count * chunks + rows_too;
-  const int i = blockIdx.x / per;
-  int k = blockIdx.x - i * per;
+  const int per = pools.count * chunks + rows_too, at = blockIdx.x / per;
+  const int i = entry0 + at;
+  int k = blockIdx.x - at * per;
   const int to = plan.base[i];
   if (rows_too && k-- == 0) {
     const int len = s.lens[src[i]], full = len / kTile;
@@ -337,10 +337,10 @@ __global__ void __launch_bounds__(kPlan)
 
 __global__ void __launch_bounds__(kCopy)
     copy_apply_kernel(const int32_t* src, const int32_t* dst, Plan plan, const PagePools pools,
-                      int chunks) {
+                      int chunks, int entry0) {
   if (plan.head[1] == 0) return;
-  const int per = pools.count * chunks;
-  const int i = blockIdx.x / per, k = blockIdx.x - i * per;
+  const int per = pools.count * chunks, at = blockIdx.x / per;
+  const int i = entry0 + at, k = blockIdx.x - at * per;
   const int pool = k / chunks;
   copy_chunk(pools.base[pool], pools.page_bytes, src[i], dst[i], k - pool * chunks);
 }
@@ -438,6 +438,10 @@ PagePools some_pools(void* const* pools, int num_pools, int at, size_t page_byte
   return p;
 }
 
+// Entries of `per` blocks each that one launch takes (a grid has 2^31 - 1 blocks; the plan has
+// accepted all entries by then, so a longer list takes more launches).
+int entries_of_a_launch(int per) { return 0x7fffffff / per; }
+
 int chunks_of(size_t page_bytes) {
   return static_cast<int>((page_bytes + kCopyBytes - 1) / kCopyBytes);
 }
@@ -471,11 +475,13 @@ cudaError_t launch_pages_fork(void* const* pools, int num_pools, size_t page_byt
   cudaError_t e = cudaGetLastError();
   for (int at = 0; e == cudaSuccess && n > 0 && (at == 0 || at < num_pools); at += kMaxPools) {
     const PagePools some = some_pools(pools, num_pools, at, page_bytes);
-    const long blocks = static_cast<long>(n) * (static_cast<long>(some.count) * chunks + (at == 0));
-    if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    fork_apply_kernel<<<static_cast<unsigned>(blocks), kCopy, 0, st>>>(s, src, dst, plan, some,
-                                                                       chunks, at == 0);
-    e = cudaGetLastError();
+    const int per = some.count * chunks + (at == 0), most = entries_of_a_launch(per);
+    for (int i = 0, m; e == cudaSuccess && i < n; i += m) {
+      m = n - i < most ? n - i : most;
+      fork_apply_kernel<<<static_cast<unsigned>(m) * per, kCopy, 0, st>>>(s, src, dst, plan, some, chunks,
+                                                                          at == 0, i);
+      e = cudaGetLastError();
+    }
   }
   return e;
 }
@@ -489,10 +495,12 @@ cudaError_t launch_pages_copy(void* const* pools, int num_pools, size_t page_byt
   cudaError_t e = cudaGetLastError();
   for (int at = 0; e == cudaSuccess && n > 0 && at < num_pools; at += kMaxPools) {
     const PagePools some = some_pools(pools, num_pools, at, page_bytes);
-    const long blocks = static_cast<long>(n) * some.count * chunks;
-    if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    copy_apply_kernel<<<static_cast<unsigned>(blocks), kCopy, 0, st>>>(src, dst, plan, some, chunks);
-    e = cudaGetLastError();
+    const int per = some.count * chunks, most = entries_of_a_launch(per);
+    for (int i = 0, m; e == cudaSuccess && i < n; i += m) {
+      m = n - i < most ? n - i : most;
+      copy_apply_kernel<<<static_cast<unsigned>(m) * per, kCopy, 0, st>>>(src, dst, plan, some, chunks, i);
+      e = cudaGetLastError();
+    }
   }
   return e;
 }

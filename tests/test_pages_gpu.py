@@ -218,3 +218,34 @@ def test_compact_out_of_place_and_many_rows():
     dev.refs, dev.table = new_refs, new_table
     dev.same(m)
     assert new_table.tolist() == m.table
+
+
+@pytest.mark.slow
+def test_lists_of_more_blocks_than_a_launch_has():
+    """2^25 entries x 64 pools of 16-byte pages (34 GB): more than 2^31 blocks, so several launches; no result of 0
+    stands for work that was not done."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    n, pools = (1 << 25) + 3, 64
+    pages = n + 1
+    pool = torch.zeros(pools, pages, 4, dtype=torch.int32, device="cuda")
+    pool[:, 0] = torch.arange(1, 4 * pools + 1, dtype=torch.int32, device="cuda").view(pools, 4)
+    each = list(pool)
+    i = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert ss.pages_copy(each, torch.zeros_like(i), i + 1).item() == 0
+    torch.cuda.synchronize()
+    same = lambda: all(bool((p[1:] == p[:1]).all()) for p in each)  # noqa: E731
+    assert same()
+    # a fork of row 0 (5 keys in page 0) into n rows: each takes a page, in order
+    pool[:, 1:] = 0
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[0] = 1
+    table = torch.zeros(n + 1, 1, dtype=torch.int32, device="cuda")
+    table[1:] = -1
+    lens = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    lens[0] = 5
+    assert ss.pages_fork(each, refs, table, lens, torch.zeros_like(i), i + 1).item() == 0
+    torch.cuda.synchronize()
+    assert same()
+    assert bool((refs == 1).all()) and bool((lens == 5).all())
+    assert torch.equal(table[:, 0], torch.arange(n + 1, dtype=torch.int32, device="cuda"))
