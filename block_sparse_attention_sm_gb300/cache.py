@@ -187,6 +187,28 @@ def _no_overlap(name, t, x):
         raise ValueError(f"{name}: overlaps its input (only the same memory, in place, is allowed)")
 
 
+def _meet(a, b):
+    """Whether two bf16 tensors share elements.  Axis by axis from the largest stride: only those index
+    differences k matter at which what is left of both comes together.  Exact where the strides are the same
+    (parts of one tensor); where more than a few k remain it answers True."""
+    def walk(gap, x, y):  # gap: from b's first element to a's
+        ex, ey = (1 + sum(s * (n - 1) for s, n in z) for z in (x, y))
+        if gap >= ey or gap + ex <= 0:
+            return False
+        if not x and not y:
+            return True
+        s, nx, ny = max(z[0][0] for z in (x, y) if z), 1, 1
+        if x and x[0][0] == s:
+            (_, nx), x, ex = x[0], x[1:], ex - s * (x[0][1] - 1)
+        if y and y[0][0] == s:
+            (_, ny), y, ey = y[0], y[1:], ey - s * (y[0][1] - 1)
+        lo, hi = max(1 - ny, (-ex - gap) // s + 1), min(nx - 1, (ey - gap - 1) // s)
+        return hi - lo >= 4 or any(walk(gap + k * s, x, y) for k in range(lo, hi + 1))
+
+    axes = [sorted(((s, n) for s, n in zip(t.stride(), t.shape) if n > 1 and s), reverse=True) for t in (a, b)]
+    return a.numel() > 0 and b.numel() > 0 and walk((a.data_ptr() - b.data_ptr()) // 2, *axes)
+
+
 def _batch(page_table, cu_seqlens, seq_lens):
     """Sequences and table width of a packed step."""
     _dense("page_table", page_table, _I32, 2)
@@ -312,8 +334,12 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
                     raise ValueError(f"{name}: needs at least {need} elements, has {t.numel()}")
     if out is not None:
         _dense("out", out, _BF16, None, shape)
-        if T > 0 and out.data_ptr() == q.data_ptr():
-            raise ValueError("out: overlaps q (blocks of queries are read again by other clusters)")
+        start = out.data_ptr()
+        for name, t, reach in (("q", q, (T - 1) * qs[0] + Hq * d), ("k_pages", k_pages, k_pages.numel()),
+                               ("v_pages", v_pages, v_pages.numel())):
+            at = t.data_ptr()
+            if T > 0 and start < at + 2 * reach and at < start + 2 * out.numel() and _meet(out, t):
+                raise ValueError(f"out: overlaps {name} (which other clusters read while this one writes)")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     handle, context = _on(stream, "q k_pages v_pages page_table cu_seqlens seq_lens out counts workspace skip_mask vote_margin",

@@ -2,6 +2,7 @@
 // new tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
 // Argument validation and launches; include/ssattn.h has each call's contract.
 #include <cmath>
+#include <initializer_list>
 
 #include "api.cuh"
 #include "chunk_paged.cuh"
@@ -52,6 +53,57 @@ bool rows_apart(const int64_t* stride, const int* size, int n, int d) {
     reach += static_cast<__int128>(stride[next]) * (size[next] - 1);
   }
   return true;
+}
+
+// Memory of bf16 elements: up to four axes (stride, size), the contiguous one among them.
+struct Span {
+  struct Axis {
+    __int128 stride;
+    long size;
+  };
+  const void* at;
+  int n;
+  Axis axis[4];
+};
+Span span(const void* at, std::initializer_list<Span::Axis> axes) {
+  Span s{at, 0, {}};
+  for (const Span::Axis& a : axes) {
+    if (a.size < 2 || a.stride == 0) continue;
+    int i = s.n++;
+    for (; i > 0 && s.axis[i - 1].stride < a.stride; --i) s.axis[i] = s.axis[i - 1];
+    s.axis[i] = a;  // (largest stride first)
+  }
+  return s;
+}
+
+// Whether two spans, the first `gap` elements in front of which the other
+// starts, share elements.  Axis by axis from the largest stride: only those
+// index differences k matter at which what is left of both comes together.
+// Exact where the strides are the same (parts of one tensor); where more than
+// a few k remain it answers true.
+bool meet(__int128 gap, const Span::Axis* x, int nx, const Span::Axis* y, int ny) {
+  __int128 ex = 1, ey = 1;  // how far each reaches
+  for (int i = 0; i < nx; ++i) ex += x[i].stride * (x[i].size - 1);
+  for (int i = 0; i < ny; ++i) ey += y[i].stride * (y[i].size - 1);
+  if (gap >= ey || gap + ex <= 0) return false;
+  if (nx == 0 && ny == 0) return true;
+  const __int128 s = nx == 0 || (ny > 0 && y->stride > x->stride) ? y->stride : x->stride;
+  long cx = 1, cy = 1;
+  if (nx > 0 && x->stride == s) cx = x->size, ex -= s * (cx - 1), ++x, --nx;
+  if (ny > 0 && y->stride == s) cy = y->size, ey -= s * (cy - 1), ++y, --ny;
+  const auto floor_div = [](__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); };
+  __int128 lo = floor_div(-ex - gap, s) + 1, hi = floor_div(ey - gap - 1, s);
+  if (lo < 1 - cy) lo = 1 - cy;
+  if (hi > cx - 1) hi = cx - 1;
+  if (hi - lo >= 4) return true;
+  for (__int128 k = lo; k <= hi; ++k)
+    if (meet(gap + k * s, x, nx, y, ny)) return true;
+  return false;
+}
+bool meet(const Span& a, const Span& b) {
+  if (a.at == nullptr || b.at == nullptr) return false;
+  const __int128 gap = (static_cast<__int128>(reinterpret_cast<uintptr_t>(a.at)) - reinterpret_cast<uintptr_t>(b.at)) / 2;
+  return meet(gap, a.axis, a.n, b.axis, b.n);
 }
 
 }  // namespace
@@ -271,6 +323,13 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   const size_t need = ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits);
   if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
     return SS_ERR_WORKSPACE;
+  {  // the queries of a block are read again by other clusters, the pools throughout
+    const Span out = span(o, {{1, static_cast<long>(T) * row}});
+    const long pool = static_cast<long>(num_pages) * Hkv * kTile * d;
+    if (T > 0 && (meet(out, span(q, {{stride, T}, {1, row}})) || meet(out, span(k_pages, {{1, pool}})) ||
+                  meet(out, span(v_pages, {{1, pool}}))))
+      return SS_ERR_INVALID_ARG;
+  }
   const bool outputs = skip_counts != nullptr || (dbg != nullptr && (dbg->skip_mask || dbg->vote_margin));
   if (T == 0 && !outputs) return SS_OK;
   ss_status st = check_device();

@@ -345,3 +345,68 @@ def test_append_helper_refuses_other_results():
     for refused, match in ((_z(1), "refused: element type"), (_z(2, dtype=I32), "refused: expected shape"), (0, "refused: expected a torch")):
         with pytest.raises((ValueError, TypeError), match=match):
             ss.rope_append_paged(**args, refused=refused)
+
+
+# Calls with nothing to refuse but the missing GPU (their addresses are not memory).
+without_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="only without a GPU")
+
+
+@without_gpu
+def test_chunk_refuses_outputs_on_its_inputs(capi):
+    """o on q's other rows, or in a pool; rows that lie between q's are apart from them."""
+    T, Hq, Hkv, d, pages = 5, 8, 2, 128, 4
+    far, row, pool = 64 * FAKE, Hq * d, pages * Hkv * 128 * d
+    args = dict(q=far, k_pages=2 * far, v_pages=3 * far, page_table=FAKE, cu_seqlens=FAKE, seq_lens=FAKE, o=4 * far, T=T, B=2, Hq=Hq,
+                Hkv=Hkv, num_pages=pages, max_pages=64, d=d, scale=0.1, causal=True, lambda_a=0.0, num_kv_splits=1, stream=0)
+    bad, fine = capi.SS_ERR_INVALID_ARG, capi.ss_attn_chunk_paged(**args)  # (without a GPU: SS_ERR_UNSUPPORTED or SS_ERR_CUDA)
+    assert fine not in (bad, capi.SS_OK)
+    for kw, want in ((dict(o=far), bad), (dict(o=far + 2 * row), bad), (dict(o=far - 16), bad), (dict(o=far + 2 * T * row), fine),
+                     (dict(o=far - 2 * T * row), fine), (dict(o=2 * far + 2 * pool - 16), bad), (dict(o=2 * far + 2 * pool), fine),
+                     (dict(o=3 * far - 16), bad), (dict(o=far + 2 * row, T=1), fine),
+                     (dict(o=far + 2 * row, T=2, q_token_stride=3 * row), fine),     # both rows of o between q's two
+                     (dict(o=far + 2 * row + 16, T=2, q_token_stride=3 * row), bad)):
+        assert capi.ss_attn_chunk_paged(**{**args, **kw}) == want, kw
+
+
+def test_chunk_helper_refuses_outputs_on_its_inputs():
+    buf = _z(6, 4, 64)
+    pool = _z(3, 2, 128, 64)
+    args = dict(k_pages=pool, v_pages=pool.clone(), page_table=_z(2, 4, dtype=I32), cu_seqlens=_z(3, dtype=I32),
+                seq_lens=_z(2, dtype=I32), scale=0.1)
+    for q, out, match in ((buf[:-1], buf[1:], "overlaps q"), (buf[1:], buf[:-1], "overlaps q"), (buf[:5], pool.view(-1, 4, 64)[7:12], "overlaps k_pages"),
+                          (buf[:2], buf[2:4], "CUDA tensor"), (buf[:0], buf[:0], "CUDA tensor"),
+                          (buf[::3], buf[1:3], "CUDA tensor")):
+        with pytest.raises(ValueError, match=match):
+            ss.chunk_paged(q, out=out, **args)
+
+
+def test_overlap_of_strided_tensors():
+    """The test of shared elements against their sets, on random views of one buffer."""
+    import random
+
+    from block_sparse_attention_sm_gb300.cache import _meet
+
+    r, buf = random.Random(0), _z(1 << 15)
+    alike = wrong = 0
+    for _ in range(4000):
+        d, views = r.choice([1, 2, 8, 64]), []
+        h = d * r.choice([1, 1, 2, 3]) + r.choice([0, 0, 1])
+        t = h * r.randint(1, 6) + r.choice([0, 0, 5])
+        for _ in range(2):
+            shape = (r.randint(1, 5), r.randint(1, 4), d)
+            strides = r.choice([(t, h, 1), (t, h, 1), (h, t, 1), (0, h, 1)])
+            reach = sum(s * (n - 1) for s, n in zip(strides, shape)) + 1
+            views.append(buf.as_strided(shape, strides, r.randint(0, min(buf.numel() - reach, 3 * t))))
+        sets = []
+        for v in views:
+            at = torch.zeros(1, dtype=torch.long) + v.storage_offset()
+            for s, n in zip(v.stride(), v.shape):
+                at = (at[:, None] + s * torch.arange(n)).flatten()
+            sets.append(set(at.tolist()))
+        want, got = bool(sets[0] & sets[1]), _meet(*views)
+        assert got or not want                     # never calls shared elements apart
+        alike += 1
+        wrong += got and not want                  # (views of different strides may be refused)
+        if views[0].stride() == views[1].stride() and views[0].stride()[0] >= views[0].stride()[1] * 4 and views[0].stride()[1] >= d:
+            assert got == want
+    assert wrong < alike // 20
