@@ -193,6 +193,19 @@ ss_status ss_rope_append_paged_ex(const void* q, void* q_out, const void* k, con
   const int q_size[2] = {T, Hq};
   if (q != nullptr && (!rows_apart(p.qos, q_size, 2, d) || q_out == k || q_out == v)) return SS_ERR_INVALID_ARG;
   if (T > kMaxRopeCount || Hq + 2l * Hkv > kMaxRopeCount) return SS_ERR_UNSUPPORTED;
+  {  // what is written (q_out, the pools) lies apart from what is read, but for q turned in place
+    const long pool = static_cast<long>(num_pages) * Hkv * kTile * d;
+    const auto rows = [&](const void* at, const long* s, int heads) {
+      return span(at, {{s[0], T}, {s[1], heads}, {1, d}});
+    };
+    const Span in[3] = {rows(q, p.qs, Hq), rows(k, p.ks, Hkv), rows(v, p.vs, Hkv)};
+    const Span to[3] = {rows(q != nullptr ? q_out : nullptr, p.qos, Hq), span(k_pages, {{1, pool}}),
+                        span(v != nullptr ? v_pages : nullptr, {{1, pool}})};
+    for (int i = 0; i < 3; ++i)
+      for (int j = 0; j < 3; ++j)
+        if (meet(to[i], in[j]) && !(i == 0 && j == 0 && q == q_out)) return SS_ERR_INVALID_ARG;
+    if (meet(to[0], to[1]) || meet(to[0], to[2]) || meet(to[1], to[2])) return SS_ERR_INVALID_ARG;
+  }
   if ((st = check_device()) != SS_OK) return st;
   vec = vec && aligned16(q) && aligned16(q_out) && aligned16(k) && aligned16(v) && all8(p.ks, 2) &&
         (q == nullptr || (all8(p.qs, 2) && all8(p.qos, 2))) && (v == nullptr || all8(p.vs, 2));

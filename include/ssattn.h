@@ -390,7 +390,8 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
  * their keys and values into the cache:  q_out = rotate(q); row L_b - n_b + i
  * of sequence b's pages = rotate(k), v.
  *   q, q_out: bf16 [T][Hq][d] (q nullable: keys and values only; q_out may be
- *     q, otherwise it must not overlap an input).  k, v: bf16 [T][Hkv][d] (v
+ *     q, otherwise it must not overlap an input; the pools overlap neither the
+ *     inputs nor each other: refused).  k, v: bf16 [T][Hkv][d] (v
  *     nullable: a cache of one row per token, as the latent one with Hkv = 1,
  *     d = 576, rot_offset = 512, rot_dim = 64).  Strides in elements between
  *     tokens and heads: q, k and v may be parts of one projection.

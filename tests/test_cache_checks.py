@@ -410,3 +410,33 @@ def test_overlap_of_strided_tensors():
         if views[0].stride() == views[1].stride() and views[0].stride()[0] >= views[0].stride()[1] * 4 and views[0].stride()[1] >= d:
             assert got == want
     assert wrong < alike // 20
+
+
+@without_gpu
+@pytest.mark.parametrize("v", [True, False])
+def test_append_refuses_overlapping_memory(capi, v):
+    """q_out and the pools against every input and each other; parts of one projection are apart."""
+    T, Hq, Hkv, d, pages = 5, 8, 2, 128, 4
+    far, pool = 64 * FAKE, pages * Hkv * 128 * d * 2
+    wide = (Hq + 2 * Hkv) * d  # entries of a token's row: q, k and v heads
+    tok = (wide, d)
+    args = dict(q=far, q_out=2 * far, k=far + 2 * Hq * d, v=far + 2 * (Hq + Hkv) * d if v else None, T=T, B=2, Hq=Hq, Hkv=Hkv, d=d,
+                cu_seqlens=FAKE, seq_lens=FAKE, inv_freq=FAKE, rot_dim=128, k_pages=3 * far, v_pages=4 * far if v else None,
+                page_table=FAKE, num_pages=pages, max_pages=4, stream=0, q_strides=tok, k_strides=tok, v_strides=tok)
+    bad, fine = capi.SS_ERR_INVALID_ARG, capi.ss_rope_append_paged(**args)
+    assert fine not in (bad, capi.SS_OK)
+    for kw, want in ((dict(q_out=far, q_out_strides=tok), fine),                                   # in place
+                     (dict(q_out=far + 2 * d, q_out_strides=tok), bad),                            # one head on
+                     (dict(q_out=far + 2 * (Hq - 1) * d, q_out_strides=tok), bad),                 # on q, k and v
+                     (dict(q_out=far + 2 * (Hkv + Hq) * d, q_out_strides=tok), bad),               # on v, and the next token's q
+                     (dict(q_out=far + 2 * T * wide, q_out_strides=tok), fine),
+                     (dict(q_out=far + 2 * Hq * d, q_out_strides=(wide, d), Hq=Hkv), bad),           # on k
+                     (dict(q_out=far + 2 * (Hq + Hkv) * d, q_out_strides=(wide, d), Hq=Hkv), bad if v else fine),  # on v
+                     (dict(q_out=far + 2 * wide - 2), bad),
+                     (dict(q_out=3 * far + pool - 2), bad), (dict(q_out=3 * far + pool), fine),
+                     (dict(q_out=4 * far), bad if v else fine),
+                     (dict(k=3 * far + pool - 2), bad), (dict(k=3 * far - 2 * T * wide), fine),
+                     (dict(k_pages=far + 32), bad), (dict(k_pages=far - pool), fine), (dict(k_pages=far - pool + 16), bad)) + (
+                     ((dict(v=3 * far), bad), (dict(v=4 * far), bad), (dict(v_pages=3 * far), bad), (dict(v_pages=3 * far + pool), fine),
+                      (dict(v_pages=far), bad)) if v else ()):
+        assert capi.ss_rope_append_paged(**{**args, **kw}) == want, kw

@@ -232,3 +232,20 @@ def test_append_keys_without_a_page_and_given_positions():
         want[1, 0, i - 2], tol[1, 0, i - 2], want_v[1, 0, i - 2] = turned[200 + i, 0], t[200 + i, 0], v[200 + i, 0]
     assert_rounded(kp.cpu(), want, tol)
     assert torch.equal(vp.cpu(), want_v)
+
+
+def test_append_refuses_outputs_on_its_inputs():
+    import block_sparse_attention_sm_gb300 as ss
+
+    T, Hq, Hkv, d = 6, 2, 2, 64
+    proj = _x((T, Hq + 2 * Hkv, d), 1).cuda()
+    q, k, v = proj.split([Hq, Hkv, Hkv], 1)
+    pool = torch.zeros(3, Hkv, PAGE, d, dtype=BF, device="cuda")
+    table, cu = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), offsets([T]).cuda()
+    lens, w = torch.tensor([T], dtype=torch.int32, device="cuda"), _freq(d).cuda()
+    before = proj.clone()
+    for out, vp in ((k, pool.clone()), (v, pool.clone()), (pool.view(-1, Hq, d)[5:5 + T], pool.clone()), (None, pool)):
+        with pytest.raises((ss.SSError, ValueError)):
+            ss.rope_append_paged(q, k, v, pool, vp, table, cu, lens, w, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(proj, before) and not pool.any()
