@@ -178,12 +178,10 @@ def _output(name, out, x, shape):
 
 
 def _no_overlap(name, t, x):
-    """t is x's memory exactly, or apart from it."""
-    a0, b0 = t.data_ptr(), x.data_ptr()
-    if a0 == b0 and t.stride() == x.stride():
+    """t is x's memory exactly, or apart from it (rows of t may lie between rows of x)."""
+    if t.data_ptr() == x.data_ptr() and all(a == b for a, b, n in zip(t.stride(), x.stride(), t.shape) if n > 1):
         return
-    a1, b1 = (p.data_ptr() + 2 * (1 + sum((n - 1) * s for n, s in zip(p.shape, p.stride()))) for p in (t, x))
-    if t.numel() and a0 < b1 and b0 < a1 and t.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
+    if _meet(t, x):
         raise ValueError(f"{name}: overlaps its input (only the same memory, in place, is allowed)")
 
 

@@ -139,6 +139,10 @@ ss_status ss_rope(const void* x, void* out, int B, int H, int L, int d, int64_t 
   if (x == nullptr || out == nullptr || positions == nullptr || !aligned2(x) || !aligned2(out) ||
       !aligned4(positions))
     return SS_ERR_INVALID_ARG;
+  const auto rows = [&](const void* at, const long* s) {
+    return span(at, {{s[0], B}, {s[1], H}, {s[2], L}, {1, d}});
+  };
+  if (x != out && meet(rows(out, p.os), rows(x, p.xs))) return SS_ERR_INVALID_ARG;
   if ((st = check_device()) != SS_OK) return st;
   vec = vec && aligned16(x) && aligned16(out) && all8(p.xs, 3) && all8(p.os, 3);
   p.x = static_cast<const __nv_bfloat16*>(x);

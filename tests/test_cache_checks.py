@@ -440,3 +440,51 @@ def test_append_refuses_overlapping_memory(capi, v):
                      ((dict(v=3 * far), bad), (dict(v=4 * far), bad), (dict(v_pages=3 * far), bad), (dict(v_pages=3 * far + pool), fine),
                       (dict(v_pages=far), bad)) if v else ()):
         assert capi.ss_rope_append_paged(**{**args, **kw}) == want, kw
+
+
+def test_rope_helper_takes_rows_between_its_inputs():
+    """Views of one tensor without a shared element are apart; the same memory is in place whatever an axis of one is called."""
+    pos = _z(5, dtype=I32)
+    proj, whole = _z(5, 8, 64), _z(2, 3, 10, 64)
+    one = _z(1, 3, 5, 64)
+    for x, out in ((proj[:, :3], proj[:, 3:6]), (whole[:, :, 0::2], whole[:, :, 1::2]), (whole[:, :, :5], whole[:, :, 5:]),
+                   (proj[:, :3], proj[:, :3]), (one, one.as_strided(one.shape, (7, 320, 64, 1))), (_z(5, 8, 128)[..., :64], proj)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            ss.rope(x, pos, FREQ, out=out)
+    both = _z(5, 2, 128)
+    with pytest.raises(ValueError, match="CUDA tensor"):  # the rows' halves
+        ss.rope(both[..., :64], pos, FREQ, out=both[..., 64:])
+    for x, out in ((proj[:, :3], proj[:, 2:5]), (whole[:, :, :5], whole[:, :, 4:9]), (whole[:, :, 0::2], whole[:, :, :5]),
+                   (both[..., :64], both[..., 32:96])):
+        with pytest.raises(ValueError, match="overlaps its input"):
+            ss.rope(x, pos, FREQ, out=out)
+
+
+@without_gpu
+def test_rope_refuses_overlapping_memory(capi):
+    """The C entry point on the random views of one buffer that the helper is tested with."""
+    import random
+
+    from block_sparse_attention_sm_gb300.cache import _meet
+
+    args = dict(d=64, positions=FAKE, inv_freq=FAKE, rot_dim=64, stream=0)
+    fine = capi.ss_rope(FAKE, 2 * FAKE, 1, 1, 1, **args)
+    assert fine not in (capi.SS_ERR_INVALID_ARG, capi.SS_OK)
+    r, buf, met = random.Random(1), _z(1 << 16), 0
+    for _ in range(2000):
+        B, H, L = r.randint(1, 3), r.randint(1, 4), r.randint(1, 5)
+        h = 64 * r.choice([1, 1, 2, 3])
+        t = h * H * r.choice([1, 1, 2]) + r.choice([0, 64])
+        strides = r.choice([(t * L, h, t), (t * L * 2, h, t)])
+        xs = r.choice([strides, strides, (0, h, t), (t * L, 64, t)])
+        reach = lambda s: sum(a * (n - 1) for a, n in zip(s, (B, H, L))) + 64  # noqa: E731
+        x = buf.as_strided((B, H, L, 64), (*xs, 1), 2048 + r.randint(0, 3) * 64 + r.choice([0, 0, 8]))
+        o = buf.as_strided((B, H, L, 64), (*strides, 1), 2048 + r.randint(-1, 3) * r.choice([64, h, t]))
+        assert max(reach(xs), reach(strides)) < (1 << 16) - 8192  # (inside the buffer)
+        want = _meet(o, x) and not (o.data_ptr() == x.data_ptr() and all(a == b for a, b, n in zip(xs, strides, (B, H, L)) if n > 1))
+        if o.data_ptr() == x.data_ptr() and any(a != b for a, b, n in zip(xs, strides, (B, H, L)) if n > 1):
+            want = True
+        got = capi.ss_rope(x, o, B, H, L, x_strides=xs, out_strides=strides, **args)
+        assert got == (capi.SS_ERR_INVALID_ARG if want else fine), (B, H, L, xs, strides, x.storage_offset(), o.storage_offset())
+        met += want
+    assert 400 < met < 1600

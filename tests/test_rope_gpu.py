@@ -249,3 +249,19 @@ def test_append_refuses_outputs_on_its_inputs():
             ss.rope_append_paged(q, k, v, pool, vp, table, cu, lens, w, out=out)
     torch.cuda.synchronize()
     assert torch.equal(proj, before) and not pool.any()
+
+
+def test_rope_into_the_rows_between():
+    """From the first heads of a projection into the next ones, and from the even tokens into the odd ones."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    T, H, d = 9, 3, 128
+    w, pos = _freq(d).cuda(), torch.arange(T, dtype=torch.int32, device="cuda") * 77
+    proj = _x((T, 2 * H + 1, d), 5).cuda()
+    want = ss.rope(proj[:, :H].contiguous(), pos, w)
+    got = ss.rope(proj[:, :H], pos, w, out=proj[:, H:2 * H])
+    assert got.data_ptr() == proj[:, H:].data_ptr() and torch.equal(got, want)
+    x = _x((2, H, 2 * T, d), 6).cuda()
+    old, want = x.clone(), ss.rope(x[:, :, 0::2].contiguous(), pos, w)
+    ss.rope(x[:, :, 0::2], pos, w, out=x[:, :, 1::2])
+    assert torch.equal(x[:, :, 1::2], want) and torch.equal(x[:, :, 0::2], old[:, :, 0::2])
