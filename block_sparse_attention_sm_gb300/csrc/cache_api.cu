@@ -1,8 +1,11 @@
 // C-ABI entry points around the paged cache: rotary positions, the write of
 // new tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
 // Argument validation and launches; include/ssattn.h has each call's contract.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <memory>
+#include <new>
 
 #include "api.cuh"
 #include "chunk_paged.cuh"
@@ -439,6 +442,45 @@ static ss_status check_pools(void* const* pools, int num_pools, size_t page_byte
   return SS_OK;
 }
 
+namespace {
+// An array that a call is given; `written`: that it writes.
+struct Range {
+  const void* at;
+  size_t bytes;
+  bool written;
+  bool meets(const Range& r) const {
+    const auto a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(r.at);
+    return bytes > 0 && r.bytes > 0 && a < b + r.bytes && b < a + bytes;
+  }
+};
+Range reads(const int32_t* p, long n) { return {p, p != nullptr ? 4 * static_cast<size_t>(n) : 0, false}; }
+Range writes(const int32_t* p, long n) { return {p, p != nullptr ? 4 * static_cast<size_t>(n) : 0, true}; }
+
+// Nothing that a call writes may overlap anything else of it.  A pool listed
+// twice is copied twice, to the same bytes; different pools lie apart.
+ss_status check_apart(std::initializer_list<Range> arrays, void* const* pools = nullptr, int num_pools = 0,
+                      size_t pool_bytes = 0) {
+  for (const Range* a = arrays.begin(); a != arrays.end(); ++a)
+    for (const Range* b = a + 1; b != arrays.end(); ++b)
+      if ((a->written || b->written) && a->meets(*b)) return SS_ERR_INVALID_ARG;
+  for (int i = 0; i < num_pools; ++i)
+    for (const Range& a : arrays)
+      if (a.meets({pools[i], pool_bytes, true})) return SS_ERR_INVALID_ARG;
+  // Pools one behind the other, the usual order, take one pass, others are sorted.
+  const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  bool in_order = true;
+  for (int i = 1; i < num_pools; ++i) in_order = in_order && at(pools[i]) >= at(pools[i - 1]) + pool_bytes;
+  if (in_order) return SS_OK;
+  std::unique_ptr<uintptr_t[]> sorted(new (std::nothrow) uintptr_t[num_pools]);
+  if (sorted == nullptr) return SS_ERR_CUDA;
+  for (int i = 0; i < num_pools; ++i) sorted[i] = at(pools[i]);
+  std::sort(sorted.get(), sorted.get() + num_pools);
+  for (int i = 1; i < num_pools; ++i)
+    if (sorted[i] != sorted[i - 1] && sorted[i] < sorted[i - 1] + pool_bytes) return SS_ERR_INVALID_ARG;
+  return SS_OK;
+}
+}  // namespace
+
 static ss_status check_workspace(const void* ws, size_t bytes, int num_pages, int num_rows, int n) {
   return ws == nullptr || !aligned16(ws) || bytes < pages_workspace(num_pages, num_rows, n)
              ? SS_ERR_WORKSPACE
@@ -455,7 +497,11 @@ ss_status ss_pages_reserve(int32_t* page_refs, int num_pages, int32_t* page_tabl
       (rows == nullptr && n > num_rows))
     return SS_ERR_INVALID_ARG;
   if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, n)) != SS_OK) return st;
-  if ((st = check_device()) != SS_OK) return st;
+  const long entries = static_cast<long>(num_rows) * max_pages;
+  st = check_apart({writes(page_refs, num_pages), writes(page_table, entries), writes(seq_lens, num_rows),
+                    writes(result, 1), {workspace, pages_workspace(num_pages, num_rows, n), true}, reads(rows, n),
+                    reads(add, n)});
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
   return of(launch_pages_reserve(s, rows, add, n, result, workspace, static_cast<cudaStream_t>(stream)));
 }
@@ -465,7 +511,10 @@ ss_status ss_pages_free(int32_t* page_refs, int num_pages, int32_t* page_table, 
   ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens);
   if (st != SS_OK) return st;
   if (n < 0 || (n > 0 && rows == nullptr) || !aligned4(rows)) return SS_ERR_INVALID_ARG;
-  if ((st = check_device()) != SS_OK) return st;
+  const long entries = static_cast<long>(num_rows) * max_pages;
+  st = check_apart({writes(page_refs, num_pages), writes(page_table, entries), writes(seq_lens, num_rows),
+                    reads(rows, n)});
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
   return of(launch_pages_free(s, rows, n, static_cast<cudaStream_t>(stream)));
 }
@@ -480,7 +529,12 @@ ss_status ss_pages_fork(void* const* pools, int num_pools, size_t page_bytes, in
       !aligned4(dst_rows) || !aligned4(result))
     return SS_ERR_INVALID_ARG;
   if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, n)) != SS_OK) return st;
-  if ((st = check_device()) != SS_OK) return st;
+  const long entries = static_cast<long>(num_rows) * max_pages;
+  st = check_apart({writes(page_refs, num_pages), writes(page_table, entries), writes(seq_lens, num_rows),
+                    writes(result, 1), {workspace, pages_workspace(num_pages, num_rows, n), true},
+                    reads(src_rows, n), reads(dst_rows, n)},
+                   pools, num_pools, page_bytes * num_pages);
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
   return of(launch_pages_fork(pools, num_pools, page_bytes, s, src_rows, dst_rows, n, result, workspace,
                               static_cast<cudaStream_t>(stream)));
@@ -495,7 +549,10 @@ ss_status ss_pages_copy(void* const* pools, int num_pools, size_t page_bytes, in
       !aligned4(src) || !aligned4(dst) || !aligned4(result))
     return SS_ERR_INVALID_ARG;
   if ((st = check_workspace(workspace, workspace_bytes, num_pages, 0, n)) != SS_OK) return st;
-  if ((st = check_device()) != SS_OK) return st;
+  st = check_apart({writes(result, 1), {workspace, pages_workspace(num_pages, 0, n), true}, reads(src, n),
+                    reads(dst, n)},
+                   pools, num_pools, page_bytes * num_pages);
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   return of(launch_pages_copy(pools, num_pools, page_bytes, num_pages, src, dst, n, result, workspace,
                               static_cast<cudaStream_t>(stream)));
 }
@@ -511,7 +568,13 @@ ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes,
   if (out_table == nullptr) out_table = page_table;
   if (!aligned4(out_refs) || !aligned4(out_table) || !aligned4(live)) return SS_ERR_INVALID_ARG;
   if ((st = check_workspace(workspace, workspace_bytes, num_pages, num_rows, 0)) != SS_OK) return st;
-  if ((st = check_device()) != SS_OK) return st;
+  const long entries = static_cast<long>(num_rows) * max_pages;
+  st = check_apart({writes(out_refs, num_pages), writes(out_table, entries),
+                    reads(out_refs != page_refs ? page_refs : nullptr, num_pages),
+                    reads(out_table != page_table ? page_table : nullptr, entries), reads(lens, num_rows),
+                    writes(live, 1), {workspace, pages_workspace(num_pages, num_rows, 0), true}},
+                   pools, num_pools, page_bytes * num_pages);
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, lens, num_pages, num_rows, max_pages};
   return of(launch_pages_compact(pools, num_pools, page_bytes, s, out_refs, out_table, live, workspace,
                                  static_cast<cudaStream_t>(stream)));

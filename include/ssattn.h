@@ -509,7 +509,9 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
  * 64 pools a launch.  Calls on one state must be ordered by the caller (one
  * stream, or events): they read and write it.  `workspace`: at least
  * ss_pages_workspace_size(num_pages, num_rows, n) bytes, 16-byte aligned, for
- * this call alone until it has run.
+ * this call alone until it has run.  No array that a call writes may overlap
+ * another of its arrays, the pools each other neither (SS_ERR_INVALID_ARG); a
+ * pool may be listed twice, and compaction may be in place.
  * `result` (nullable device int32): 0 done; k > 0: refused, k free pages are
  * missing; -1: refused, an argument on the device is wrong (below).  A refused
  * call changes nothing, so a step that grows its sequences must not go on as if

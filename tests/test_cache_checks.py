@@ -488,3 +488,60 @@ def test_rope_refuses_overlapping_memory(capi):
         assert got == (capi.SS_ERR_INVALID_ARG if want else fine), (B, H, L, xs, strides, x.storage_offset(), o.storage_offset())
         met += want
     assert 400 < met < 1600
+
+
+@without_gpu
+def test_pages_refuse_overlapping_arrays(capi):
+    """What a call writes lies apart from everything else it is given."""
+    pages, rows, width, n, page_bytes = 40, 6, 5, 3, 256
+    at = {x: (i + 1) * 16 * FAKE for i, x in enumerate(("refs", "table", "lens", "ws", "result", "a", "b", "out_refs", "out_table"))}
+    size = dict(refs=4 * pages, table=4 * rows * width, lens=4 * rows, result=4, a=4 * n, b=4 * n, out_refs=4 * pages, out_table=4 * rows * width)
+    size["ws"] = capi.ss_pages_workspace_size(pages, rows, n)
+    pool, pool_bytes = 100 * 16 * FAKE, pages * page_bytes
+
+    def call(name, x, pools):
+        state = dict(page_refs=x["refs"], num_pages=pages, page_table=x["table"], num_rows=rows, max_pages=width, seq_lens=x["lens"])
+        ws = dict(workspace=x["ws"], workspace_bytes=size["ws"], stream=0)
+        if name == "reserve":
+            return capi.ss_pages_reserve(**state, rows=x["a"], add=x["b"], n=n, result=x["result"], **ws)
+        if name == "free":
+            return capi.ss_pages_free(**state, rows=x["a"], n=n, stream=0)
+        if name == "fork":
+            return capi.ss_pages_fork(pools, page_bytes, **state, src_rows=x["a"], dst_rows=x["b"], n=n, result=x["result"], **ws)
+        if name == "copy":
+            return capi.ss_pages_copy(pools, page_bytes, pages, x["a"], x["b"], n, result=x["result"], **ws)
+        return capi.ss_pages_compact(pools, page_bytes, **state, out_refs=x["out_refs"], out_table=x["out_table"], live=x["result"], **ws)
+
+    written = dict(reserve=("refs", "table", "lens", "result", "ws"), free=("refs", "table", "lens"),
+                   fork=("refs", "table", "lens", "result", "ws"), copy=("result", "ws"),
+                   compact=("out_refs", "out_table", "result", "ws"))
+    read = dict(reserve=("a", "b"), free=("a",), fork=("a", "b"), copy=("a", "b"), compact=("refs", "table", "lens"))
+    apart = [pool, pool + 3 * pool_bytes, pool + pool_bytes]  # (not in order)
+    bad = capi.SS_ERR_INVALID_ARG
+    for name in written:
+        fine = call(name, at, apart)
+        assert fine not in (bad, capi.SS_OK, capi.SS_ERR_WORKSPACE)
+        assert call(name, at, apart + apart[:1]) == fine  # a pool listed twice
+        size["ws"] = capi.ss_pages_workspace_size(pages, 0 if name == "copy" else rows, 0 if name == "compact" else n)
+        names = written[name] + read[name]
+        for w in written[name]:
+            for other in names:
+                if other == w or {w, other} in ({"out_refs", "refs"}, {"out_table", "table"}):
+                    continue
+                base = at[other] + (size[other] - 1) // 16 * 16  # its last word(s)
+                assert call(name, {**at, w: base}, apart) == bad, (name, w, other)
+        for r in read[name]:
+            if name in ("reserve", "fork", "copy"):
+                assert call(name, {**at, "a": at["b"]}, apart) == fine  # both are read only
+        if name == "compact":
+            assert call(name, {**at, "out_refs": at["refs"], "out_table": at["table"]}, apart) == fine
+            assert call(name, {**at, "out_refs": None, "out_table": None, "result": None}, apart) == fine
+            assert call(name, {**at, "out_refs": at["refs"] + 16}, apart) == bad
+            assert call(name, {**at, "out_table": at["table"] + 16}, apart) == bad
+        if name in ("fork", "copy", "compact"):
+            for w in names:
+                assert call(name, {**at, w: pool + pool_bytes - 16}, apart) == bad, (name, w)
+                assert call(name, {**at, w: pool + 2 * pool_bytes}, apart) == fine
+            for pools in ([pool, pool + 16], [pool + 16, pool], [pool, pool + 2 * pool_bytes, pool + pool_bytes - 16],
+                          [pool + pool_bytes, pool + pool_bytes, pool + 16]):
+                assert call(name, at, pools) == bad
