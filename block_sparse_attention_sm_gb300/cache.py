@@ -98,6 +98,11 @@ def _on(stream, names, *tensors):
 _HERE = contextlib.nullcontext()
 
 
+def _written(out):
+    """A graph that has saved ``out`` learns that a kernel has changed it (as of torch's own in-place functions)."""
+    torch.autograd.graph.increment_version(out)
+
+
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
                      original_length: int = 8192, lo: float = 1.0, hi: float | None = None, device="cuda"):
     """(inv_freq, attn_factor) for :func:`rope` and :func:`rope_append_paged`.
@@ -125,7 +130,10 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
     a contiguous last axis.  inv_freq: float64 [rot_dim / 2]; entries
     [rot_offset, rot_offset + rot_dim) turn, the others are copied.
     ``inverse``: the transposed rotation; the gradient of ``rope`` with respect
-    to x is ``rope(grad, ..., inverse=True)`` with the same other arguments."""
+    to x is ``rope(grad, ..., inverse=True)`` with the same other arguments.
+    Where gradients are recorded and x requires one, the result is part of the
+    graph and its backward pass is that call; ``out`` and frequencies that
+    require a gradient are refused there."""
     if not isinstance(x, torch.Tensor) or x.ndim not in (3, 4):
         raise ValueError("rope expects x [B,H,L,d] or [T,H,d]")
     packed = x.ndim == 3
@@ -147,7 +155,10 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
     rot = 2 * inv_freq.shape[0]
     if rot < 2 or rot_offset < 0 or rot_offset + rot > d:
         raise ValueError(f"rope: entries [{rot_offset}, {rot_offset + rot}) of rows of {d}")
-    if out is not None:
+    given = out is not None
+    if (x.requires_grad or inv_freq.requires_grad or given and out.requires_grad) and torch.is_grad_enabled():
+        return _recorded(x, positions, inv_freq, rot_offset, interleaved, inverse, attn_factor, out, stream)
+    if given:
         _output("out", out, x, shape)
     handle, context = _on(stream, "x positions inv_freq out", x, positions, inv_freq, out)
     with context:
@@ -165,7 +176,37 @@ def rope(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = Fal
             inv_freq.data_ptr(), rot, rot_offset, bool(interleaved), bool(inverse), attn_factor, handle)
     if st:
         raise SSError(st, "ss_rope")
+    if given:
+        _written(out)
     return out
+
+
+class _Rope(torch.autograd.Function):
+    """rope as a node of the graph: linear in x, its transpose is the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, options):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.options = options
+        return rope(x, positions, inv_freq, **options)
+
+    @staticmethod
+    def backward(ctx, grad):
+        options = dict(ctx.options, inverse=not ctx.options["inverse"])
+        if grad.stride(-1) != 1:  # (a broadcast gradient, as that of a sum)
+            grad = grad.contiguous()
+        return _Rope.apply(grad, *ctx.saved_tensors, options), None, None, None
+
+
+def _recorded(x, positions, inv_freq, rot_offset, interleaved, inverse, attn_factor, out, stream):
+    """rope while gradients are recorded for x; the node belongs to the call's stream."""
+    if out is not None:
+        raise ValueError("out: not where a gradient of the rotation is recorded")
+    if inv_freq.requires_grad:
+        raise ValueError("inv_freq: the rotation has no gradient with respect to its frequencies")
+    options = dict(rot_offset=rot_offset, interleaved=interleaved, inverse=inverse, attn_factor=attn_factor)
+    with _HERE if stream is None else _on(stream, "x", x)[1]:
+        return _Rope.apply(x, positions, inv_freq, options)
 
 
 def _output(name, out, x, shape):
@@ -232,7 +273,8 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
     for this step; where it is not 0 the call does nothing (the lengths then do
     not include the new tokens, which would overwrite the newest cached ones).
     Returns the rotated q (``out``; ``out=q``: in place), rows behind the last
-    sequence left as they were, or None without q."""
+    sequence left as they were, or None without q.  A serving call: it records
+    no gradients (:func:`rope` does)."""
     (T, Hkv, d), ks = _rows("k", k, 3)
     Hq, qs, os_, vs = 0, (0, 0), (0, 0), (0, 0)
     if q is not None:
@@ -286,6 +328,8 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
             refused.data_ptr() if refused is not None else None, handle)
     if st:
         raise SSError(st, "ss_rope_append_paged")
+    if out is not None:
+        _written(out)
     return o
 
 
@@ -354,6 +398,8 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
                                       num_pages, max_pages, d, scale, causal, lambda_a, num_kv_splits, counts,
                                       workspace, nbytes, qs[0] if T > 1 else 0, skip_mask, vote_margin, handle)
     _check(st, "ss_attn_chunk_paged")
+    if out is not None:
+        _written(out)
     return o
 
 

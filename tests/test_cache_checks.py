@@ -545,3 +545,18 @@ def test_pages_refuse_overlapping_arrays(capi):
             for pools in ([pool, pool + 16], [pool + 16, pool], [pool, pool + 2 * pool_bytes, pool + pool_bytes - 16],
                           [pool + pool_bytes, pool + pool_bytes, pool + 16]):
                 assert call(name, at, pools) == bad
+
+
+def test_rope_refuses_what_it_cannot_record():
+    x, pos = _z(2, 3, 5, 64).requires_grad_(True), _z(5, dtype=I32)
+    with pytest.raises(ValueError, match="out: not where a gradient"):
+        ss.rope(x, pos, FREQ, out=_z(2, 3, 5, 64))
+    with pytest.raises(ValueError, match="out: not where a gradient"):
+        ss.rope(x, pos, FREQ, out=x)
+    with pytest.raises(ValueError, match="frequencies"):
+        ss.rope(_z(2, 3, 5, 64), pos, FREQ.clone().requires_grad_(True))
+    for kw, match in ((dict(), "CUDA tensor"), (dict(positions=_z(4, dtype=I32)), "expected shape"), (dict(rot_offset=2), "entries")):
+        with pytest.raises(ValueError, match=match):  # the other checks are as they were
+            ss.rope(**{**dict(x=x, positions=pos, inv_freq=FREQ), **kw})
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+        ss.rope(x, pos, FREQ, out=x)

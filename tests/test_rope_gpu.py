@@ -265,3 +265,84 @@ def test_rope_into_the_rows_between():
     old, want = x.clone(), ss.rope(x[:, :, 0::2].contiguous(), pos, w)
     ss.rope(x[:, :, 0::2], pos, w, out=x[:, :, 1::2])
     assert torch.equal(x[:, :, 1::2], want) and torch.equal(x[:, :, 0::2], old[:, :, 0::2])
+
+
+@pytest.mark.parametrize("case", [
+    # shape, rot, off, interleaved, inverse, factor
+    ((2, 3, 7, 64), 64, 0, False, False, 1.0),
+    ((1, 2, 33, 192), 64, 128, True, False, 1.5),
+    ((9, 4, 80), 24, 8, False, True, 1.25),       # packed, single entries
+])
+def test_rope_is_recorded(case):
+    """The graph's gradients are the formula's, R' g: of a first and a second backward pass."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    shape, rot, off, inter, inv, f = case
+    L = shape[-2] if len(shape) == 4 else shape[0]
+    x, g = _x(shape, 5).cuda().requires_grad_(True), _x(shape, 6).cuda()
+    pos, w = (torch.arange(L, dtype=torch.int32) * 333).cuda(), _freq(rot).cuda()
+    kw = dict(rot_offset=off, interleaved=inter, inverse=inv, attn_factor=f)
+    at = pos.cpu()[:, None] if len(shape) == 3 else pos.cpu()
+    plain = lambda t, i: rotate(t.cpu(), at, w.cpu(), f, off, inter, i)  # noqa: E731
+    tol = lambda t: rotate_tolerance(t.cpu(), w.cpu(), f, off, inter)  # noqa: E731
+    y = ss.rope(x, pos, w, **kw)
+    assert y.requires_grad
+    with torch.no_grad():
+        same = ss.rope(x, pos, w, **kw)
+    assert torch.equal(y, same) and not same.requires_grad
+    assert_rounded(y.detach().cpu(), plain(x.detach(), inv), tol(x.detach()))
+    v = g.clone().requires_grad_(True)
+    grad, = torch.autograd.grad(y, x, v, create_graph=True)
+    assert_rounded(grad.detach().cpu(), plain(g, not inv), tol(g))
+    # <h, R' v> differentiated by v is R h
+    h = _x(shape, 7).cuda()
+    second, = torch.autograd.grad(grad, v, h)
+    assert_rounded(second.cpu(), plain(h, inv), tol(h))
+    # differences of the 64-bit rotation, in some entries
+    for i in np.random.default_rng(0).integers(0, x.numel(), 12):
+        e = torch.zeros(x.numel(), dtype=torch.float64)
+        e[i] = 2.0 ** -10
+        moved = [(plain(x.detach().double().cpu() + s * e.view(shape), inv) * g.cpu().double()).sum() for s in (1, -1)]
+        diff = float(moved[0] - moved[1]) / 2.0 ** -9
+        assert abs(float(grad.detach().flatten()[i]) - diff) <= float(tol(g).flatten()[i]) + (abs(diff) + 1e-6) * 2.0 ** -8 + 1e-9
+
+
+def test_rope_gradients_of_broadcast_and_strided_inputs():
+    """A head shared by the batch, heads of a projection, the broadcast gradient of a sum, another stream."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    T, H, d = 12, 3, 64
+    w, pos = _freq(d).cuda(), torch.arange(T, dtype=torch.int32, device="cuda") * 11
+    proj = _x((T, H + 2, d), 8).cuda().requires_grad_(True)
+    ss.rope(proj[:, :H], pos, w).sum().backward()
+    ones = torch.ones(T, H, d, dtype=BF)
+    want = rotate(ones, pos.cpu()[:, None], w.cpu(), 1.0, 0, False, True)
+    assert_rounded(proj.grad[:, :H].cpu(), want, rotate_tolerance(ones, w.cpu(), 1.0, 0, False))
+    assert not proj.grad[:, H:].any()
+    one = _x((1, 1, T, d), 9).cuda().requires_grad_(True)
+    g = _x((4, 1, T, d), 10).cuda()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    y = ss.rope(one.expand(4, 1, T, d), pos, w, stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    y.backward(g)
+    torch.cuda.synchronize()
+    parts = rotate(g.cpu(), pos.cpu(), w.cpu(), 1.0, 0, False, True)
+    # four gradients, each rounded, summed in bf16: three more roundings of sums of at most sum |part|
+    tol = (4 * 2.0 ** -8) * parts.abs().sum(0, keepdim=True) + rotate_tolerance(g.cpu(), w.cpu(), 1.0, 0, False).sum(0, keepdim=True)
+    assert ((one.grad.cpu().double() - parts.sum(0, keepdim=True)).abs() <= tol + 1e-40).all()
+
+
+def test_rope_in_place_is_seen_by_the_graph():
+    """A tensor that a graph has saved and that is rotated in place after that is an error of the backward pass."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    w, pos = _freq(64).cuda(), torch.arange(4, dtype=torch.int32, device="cuda")
+    x, scale = _x((4, 2, 64), 3).cuda(), torch.ones(64, dtype=BF, device="cuda", requires_grad=True)
+    y = (x * scale).sum()
+    ss.rope(x, pos, w, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        y.backward()
+    with torch.inference_mode():
+        z = x.clone()
+        assert ss.rope(z, pos, w, out=z) is z
