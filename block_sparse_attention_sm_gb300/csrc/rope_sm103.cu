@@ -9,8 +9,11 @@
 //
 // The angle is formed exactly: w / 2 pi, the turns per position, as a 64-bit
 // binary fraction, so that p times it modulo 2^64 is the fractional turn of
-// any 32-bit position with an error below 2^-32 turns (fp32 products lose the
-// angle of far positions: 2^-24 of 10^5 radians is 6e-3).  Integer products
+// any 32-bit position with an error below 2^-32 turns for |w| < 2 (the usual
+// frequencies are at most 1; each doubling beyond doubles the error; from 2^64
+// on no bit of the angle is left at any position, and the result is NaN, as it
+// is where w is not finite).  (fp32 products lose the
+// angle of far positions: 2^-24 of 10^5 radians is 6e-3.)  Integer products
 // only: fp64 runs at 1/64 of the fp32 rate on this GPU.  The fraction's upper
 // 32 bits become a float in half turns for sincospif; its rounding (2^-25
 // turns' relative) and bf16's of the result (half a step, 2^-8) are the only
@@ -31,10 +34,15 @@ namespace {
 constexpr int kThreadsRope = 256;
 constexpr int kAhead = 4;  // heads whose loads are in flight per thread
 
+// Binary exponent: 2^e <= |w| < 2^(e + 1); above every finite one for NaN and Inf.
+__device__ __forceinline__ int exponent_of(double w) {
+  return static_cast<int>((static_cast<uint64_t>(__double_as_longlong(w)) >> 52) & 0x7ff) - 1023;
+}
+
 // w / (2 pi) modulo 1 as a fraction of 2^64 (truncated).
 __device__ __forceinline__ uint64_t turns_per_position(double w) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(w));
-  const int e = static_cast<int>((bits >> 52) & 0x7ff) - 1023;
+  const int e = exponent_of(w);
   const uint64_t m = (bits << 11) | (1ull << 63);           // |w| = m 2^(e - 63)
   const uint64_t inv2pi = 0xA2F9836E4E441529ull;            // 2^66 / (2 pi), truncated
   const uint64_t t = __umul64hi(m, inv2pi);                 // |w| / 2 pi = t 2^(e - 65)
@@ -52,6 +60,7 @@ __device__ __forceinline__ float2 turn_of(int pos, double w, float factor, float
   const float half_turns = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f;
   float s, c;
   sincospif(half_turns, &s, &c);
+  if (exponent_of(w) >= 64) factor = NAN;  // (a select; a branch around the angle: decode append +0.2 us)
   return make_float2(factor * c, sign * factor * s);
 }
 

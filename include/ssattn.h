@@ -360,8 +360,11 @@ ss_status ss_attn_mla_decode_paged(const void* q, const void* kv_pages, const in
  *   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t),  t = p * inv_freq[i]
  * with f = attn_factor; the row's other entries are copied.  `inverse` turns
  * by -t (same f): the gradient with respect to x is this call on the gradient
- * with respect to out.  Angles are exact for any int32 position (no loss at
- * far positions); products are fp32, rounded once to bf16.
+ * with respect to out.  Angles of any int32 position are good to 2^-31 turns for
+ * frequencies below 2 in magnitude (no loss at far positions; the usual
+ * frequencies are at most 1).  At larger ones w they are off by up to
+ * |position * w| 2^-63 turns; 2^64 and more in magnitude, or not finite, gives NaN.
+ * Products are fp32, rounded once to bf16.
  *   x, out: bf16 [B][H][L][d], 2-byte aligned, strides in elements (batch,
  *     head, token; [B][H][L][d] itself: H * L * d, L * d, d); the innermost
  *     axis is contiguous.  x may have stride 0 axes.  out == x (same strides)

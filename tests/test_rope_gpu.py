@@ -346,3 +346,30 @@ def test_rope_in_place_is_seen_by_the_graph():
     with torch.inference_mode():
         z = x.clone()
         assert ss.rope(z, pos, w, out=z) is z
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_frequencies_of_any_size(interleaved):
+    """Just below 2 the angle is exact at any position; beyond, off by |p w| 2^-63 turns; NaN where there is none."""
+    import block_sparse_attention_sm_gb300 as ss
+
+    decimal.getcontext().prec = 80
+    two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    bad = [math.inf, -math.inf, math.nan, 2.0 ** 64, -1e30, 1.7e308]
+    good = [math.nextafter(2.0, 0), -1.999, 2.0, -3.75, 1000.1, 1e6, -1e12, 1e-300, 5e-324, 0.0]
+    w = torch.tensor(good + bad, dtype=torch.float64)
+    n, d = len(w), 2 * len(w)
+    pos = [0, 1, -3, 40, 131071, (1 << 31) - 1, -(1 << 31)]
+    x = torch.zeros(len(pos), 1, d + 8, dtype=BF)
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if interleaved else (slice(0, n), slice(n, d))
+    x[:, :, a] = 1.0
+    x[:, :, d:] = 3.0
+    out = ss.rope(x.cuda(), torch.tensor(pos, dtype=torch.int32, device="cuda"), w.cuda(), interleaved=interleaved).cpu().double()
+    c, s = out[:, 0, a], out[:, 0, b]
+    assert c[:, len(good):].isnan().all() and s[:, len(good):].isnan().all() and (out[:, :, d:] == 3).all()
+    for i, p in enumerate(pos):
+        for j, f in enumerate(good):
+            t = float((decimal.Decimal(p) * decimal.Decimal(f)) % two_pi)
+            off = 1e-6 + 2 * math.pi * abs(p * f) * 2.0 ** -63
+            for got, want in ((c[i, j], math.cos(t)), (s[i, j], math.sin(t))):
+                assert abs(float(got) - want) <= off + (abs(want) + off) * 2.0 ** -8, (p, f, float(got), want)
