@@ -334,8 +334,10 @@ def rope_append_paged(q, k, v, k_pages, v_pages, page_table, cu_seqlens, seq_len
 
 
 def chunk_paged_workspace(T, B, Hq, Hkv, max_pages, d, num_kv_splits, device):
-    """(workspace, its bytes) for :func:`chunk_paged` calls of these sizes."""
-    n = capi.ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits)
+    """(workspace, its bytes) that serves every :func:`chunk_paged` call of up to these sizes.
+
+    (A call alone may need less, and a smaller step more than a larger one.)"""
+    n = capi.ss_attn_chunk_paged_workspace_bound(T, Hq, Hkv, max_pages, d, num_kv_splits)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
 
 
@@ -393,7 +395,8 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
         if workspace is not None:
             nbytes = workspace.numel() * workspace.element_size()
         elif num_kv_splits > 1:
-            workspace, nbytes = chunk_paged_workspace(T, B, Hq, Hkv, max_pages, d, num_kv_splits, q.device)
+            nbytes = capi.ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
         st = capi.ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,
                                       num_pages, max_pages, d, scale, causal, lambda_a, num_kv_splits, counts,
                                       workspace, nbytes, qs[0] if T > 1 else 0, skip_mask, vote_margin, handle)

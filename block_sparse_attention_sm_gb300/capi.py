@@ -29,7 +29,7 @@ EXPORTS = (
     "ss_calibrate", "ss_fit_factor", "ss_lambda", "ss_status_string", "ss_stream_status",
     "ss_rope", "ss_rope_append_paged", "ss_rope_append_paged_ex", "ss_rope_frequencies",
     "ss_attn_chunk_paged", "ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
-    "ss_pages_workspace_size", "ss_pages_reserve", "ss_pages_free", "ss_pages_fork",
+    "ss_attn_chunk_paged_workspace_bound", "ss_pages_workspace_size", "ss_pages_reserve", "ss_pages_free", "ss_pages_fork",
     "ss_pages_copy", "ss_pages_compact",
 )
 
@@ -109,9 +109,10 @@ def load() -> ctypes.CDLL:
                                         U, ctypes.POINTER(ss_debug_opts), P]
     lib.ss_attn_chunk_paged_units.argtypes = [I, I, I, I]
     lib.ss_attn_chunk_paged_workspace_size.argtypes = [I] * 7
+    lib.ss_attn_chunk_paged_workspace_bound.argtypes = [I] * 6
     lib.ss_pages_workspace_size.argtypes = [I, I, I]
     for name in ("ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
-                 "ss_pages_workspace_size"):
+                 "ss_attn_chunk_paged_workspace_bound", "ss_pages_workspace_size"):
         getattr(lib, name).restype = U
     state = [P, I, P, I, I, P]
     lib.ss_pages_reserve.argtypes = state + [P, P, I, P, P, U, P]
@@ -369,6 +370,10 @@ def ss_attn_chunk_paged_units(T, B, Hq, Hkv) -> int:
 
 def ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits) -> int:
     return int((_lib or load()).ss_attn_chunk_paged_workspace_size(T, B, Hq, Hkv, max_pages, d, num_kv_splits))
+
+
+def ss_attn_chunk_paged_workspace_bound(T, Hq, Hkv, max_pages, d, num_kv_splits) -> int:
+    return int((_lib or load()).ss_attn_chunk_paged_workspace_bound(T, Hq, Hkv, max_pages, d, num_kv_splits))
 
 
 def ss_attn_chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, o, T, B, Hq, Hkv,

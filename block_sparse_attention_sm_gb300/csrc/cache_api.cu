@@ -312,6 +312,20 @@ size_t ss_attn_chunk_paged_workspace_size(int T, int B, int Hq, int Hkv, int max
   return parts == 1 ? 0 : static_cast<size_t>(parts) * T * Hq * (d + 2) * sizeof(float);
 }
 
+size_t ss_attn_chunk_paged_workspace_bound(int T, int Hq, int Hkv, int max_pages, int d, int num_kv_splits) {
+  if (num_kv_splits <= 1 || T < 1 || Hkv < 1 || Hq < Hkv || Hq / Hkv > kTile || max_pages < 1 || d < 1) return 0;
+  // The most parts are made for one sequence; fewer, the more places its tokens
+  // take.  Of the steps with the same places, the longest needs the most.
+  const long pair = 2 * (kTile / (Hq / Hkv));
+  size_t most = 0;
+  for (long places = 1;; ++places) {
+    const int parts = chunk_parts(places * Hkv, num_kv_splits, max_pages);
+    const long tokens = std::min<long>(T, places * pair - 1);
+    if (parts > 1) most = std::max(most, static_cast<size_t>(parts) * tokens);
+    if (parts == 1 || tokens == T) return most * Hq * (d + 2) * sizeof(float);
+  }
+}
+
 ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
                               const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
                               const int32_t* seq_lens, void* o, int T, int B, int Hq, int Hkv,

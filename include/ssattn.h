@@ -481,7 +481,10 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
  *     of sequence b): (h * places + p) * 2 + k % 2 with places = T / (2m) + B
  *     and p = cu_seqlens[b] / (2m) + b + k / 2 (integer divisions).
  *   workspace: at least ss_attn_chunk_paged_workspace_size(...) bytes, 16-byte
- *     aligned (nullable when that is 0).
+ *     aligned (nullable when that is 0).  A step of fewer tokens or sequences may
+ *     need more than a larger one (its tiles are dealt to more parts): the
+ *     _bound form gives what serves every step of up to T tokens, whatever
+ *     their sequences, and pages, for a workspace that is allocated once.
  *   dbg: nullable; skip_mask / vote_margin are [units][max_pages]; its other
  *     fields must be 0.
  * G <= 128, d in {64, 128}.  Returns SS_OK (also for T = 0),
@@ -490,6 +493,8 @@ ss_status ss_rope_frequencies(double* out, int rot_dim, double base, ss_rope_sca
 size_t ss_attn_chunk_paged_units(int T, int B, int Hq, int Hkv);
 size_t ss_attn_chunk_paged_workspace_size(int T, int B, int Hq, int Hkv, int max_pages, int d,
                                           int num_kv_splits);
+size_t ss_attn_chunk_paged_workspace_bound(int T, int Hq, int Hkv, int max_pages, int d,
+                                           int num_kv_splits);
 ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void* k_pages,
                               const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
                               const int32_t* seq_lens, void* o, int T, int B, int Hq, int Hkv,

@@ -560,3 +560,22 @@ def test_rope_refuses_what_it_cannot_record():
             ss.rope(**{**dict(x=x, positions=pos, inv_freq=FREQ), **kw})
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
         ss.rope(x, pos, FREQ, out=x)
+
+
+def test_chunk_workspace_bound(capi):
+    """What the bound promises, by trying the smaller steps; smaller steps do need more than larger ones."""
+    size, bound = capi.ss_attn_chunk_paged_workspace_size, capi.ss_attn_chunk_paged_workspace_bound
+    assert [size(T, 1, 32, 8, 256, 128, 8) for T in (2048, 256)] == [0, 0]
+    assert size(64, 1, 32, 8, 256, 128, 8) < size(63, 1, 32, 8, 256, 128, 8) <= bound(2048, 32, 8, 256, 128, 8)
+    for T, Hq, Hkv, pages, splits in ((1, 1, 1, 1, 1), (5, 4, 1, 41, 7), (700, 8, 2, 64, 3), (700, 8, 2, 64, 1), (900, 32, 8, 256, 8),
+                                      (300, 3, 1, 9999, 1000), (2000, 128, 1, 100, 2 ** 31 - 1), (9000, 1, 1, 80, 50), (50, 40, 40, 64, 4)):
+        most = max(size(t, 1, Hq, Hkv, pages, 64, splits) for t in range(1, T + 1))
+        assert bound(T, Hq, Hkv, pages, 64, splits) == most
+        for t in {1, T // 3 + 1, T}:
+            for b in (1, 2, 7, 80):
+                for p in {1, pages // 2 + 1, pages}:
+                    for s in {1, splits // 2 + 1, splits}:
+                        assert size(t, b, Hq, Hkv, p, 64, s) <= most
+    assert bound(0, 8, 2, 64, 128, 3) == 0 and bound(10, 1, 2, 64, 128, 3) == 0 and bound(10, 258, 2, 64, 128, 3) == 0
+    ws, n = ss.chunk_paged_workspace(2048, 1, 32, 8, 256, 128, 8, "cpu")
+    assert n == bound(2048, 32, 8, 256, 128, 8) and ws.numel() == n

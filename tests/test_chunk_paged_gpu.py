@@ -398,3 +398,22 @@ def test_chunk_nan_queries_that_fill_a_block(Hq, Hkv, d, n, L, splits, spoilt, a
         for j in range(0, tiles(L[b]), per):
             assert int(mask[unit, j]) == 0 and float(margin[unit, j]) == math.inf
     assert capi.ss_stream_status() == capi.SS_OK
+
+
+def test_chunk_workspace_made_once():
+    """A workspace of the largest step serves the smaller ones, which need more of it."""
+    import block_sparse_attention_sm_gb300 as ss
+    from block_sparse_attention_sm_gb300 import capi
+
+    Hq, Hkv, d, width, splits = 4, 2, 128, 64, 6
+    ws, nbytes = ss.chunk_paged_workspace(5000, 3, Hq, Hkv, width, d, splits, "cuda")
+    assert capi.ss_attn_chunk_paged_workspace_size(5000, 3, Hq, Hkv, width, d, splits) == 0 < nbytes
+    for n, L in (([1900, 60, 40], [2000, 100, 64 * PAGE]), ([1], [64 * PAGE]), ([63], [60 * PAGE + 1]), ([3, 1], [40 * PAGE, 8000])):
+        q, k, v = make(Hq, Hkv, d, n, L, 51)
+        table, pages = random_tables(L, 1, np.random.default_rng(5), width=width)
+        args = (q.cuda(), fill_pool(k, L, table, pages).cuda(), fill_pool(v, L, table, pages).cuda(), table.cuda(),
+                offsets(n).cuda(), torch.tensor(L, dtype=torch.int32, device="cuda"))
+        for a in (0.0, 4.0):
+            kw = dict(scale=d ** -0.5, lambda_a=a, num_kv_splits=splits)
+            assert torch.equal(ss.chunk_paged(*args, **kw, workspace=ws), ss.chunk_paged(*args, **kw))
+    assert capi.ss_stream_status() == capi.SS_OK
