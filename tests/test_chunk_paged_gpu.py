@@ -417,3 +417,11 @@ def test_chunk_workspace_made_once():
             kw = dict(scale=d ** -0.5, lambda_a=a, num_kv_splits=splits)
             assert torch.equal(ss.chunk_paged(*args, **kw, workspace=ws), ss.chunk_paged(*args, **kw))
     assert capi.ss_stream_status() == capi.SS_OK
+
+
+@pytest.mark.parametrize("a,splits", [(0.0, 1), (16.0, 1), (16.0, 3), (1e4, 1)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (3, 1, 64)])
+def test_chunk_votes_over_long_caches(Hq, Hkv, d, a, splits):
+    """256 tiles a unit: the rings and the softmax's state go round many times, with most tiles skipped and with none."""
+    skipped, evaluated = check(Hq, Hkv, d, [70, 1, 129], [128 * 256 + 5, 128 * 201, 128 * 255], a=a, splits=splits, seed=61)
+    assert evaluated > 1000 and (skipped > evaluated // 2 if a == 16.0 else skipped == 0 if a == 0.0 else True)
