@@ -1129,7 +1129,7 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
 // kernel, ~6 us in all), so parts are made only where the pairs leave places
 // of the 76 clusters idle, at most as many as fit at once, and of eight tiles
 // or more.  Measured on 8 sequences x 5 new tokens x 2K keys (64 pairs, 8 KV
-// heads): 21 us as one part, 28 us as two.
+// heads): 24 us as one part, 29 us as two.
 int chunk_parts(long pairs, int S, int max_pages) {
   const long places = 76;
   long parts = places / pairs;

@@ -511,7 +511,10 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
  *     sequence (length 0: unused), its keys [128j, 128j + 128) in page
  *     page_table[row][j]; entries past its last page are unspecified.
  * Only full pages are shared; a sequence's last page, while not full, is its
- * own, so new keys can always be appended.  Pools: `pools` is a host array of
+ * own, so new keys can always be appended.  Lengths grow and end by the calls
+ * below.  A caller may lower one within a last page that is not full, which
+ * gives up those keys; across a page boundary the pages behind it would be held
+ * by no row, and the new last page, as any full one, might be shared.  Pools: `pools` is a host array of
  * num_pools device addresses (16-byte aligned), each num_pages pages of
  * page_bytes (a multiple of 16, up to 2^34) -- the key and the value pages of every layer;
  * 64 pools a launch.  Calls on one state must be ordered by the caller (one
