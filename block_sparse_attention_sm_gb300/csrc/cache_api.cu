@@ -61,8 +61,7 @@ bool rows_apart(const int64_t* stride, const int* size, int n, int d) {
 // Memory of bf16 elements: up to four axes (stride, size), the contiguous one among them.
 struct Span {
   struct Axis {
-    __int128 stride;
-    long size;
+    __int128 stride, size;
   };
   const void* at;
   int n;
@@ -91,7 +90,7 @@ bool meet(__int128 gap, const Span::Axis* x, int nx, const Span::Axis* y, int ny
   if (gap >= ey || gap + ex <= 0) return false;
   if (nx == 0 && ny == 0) return true;
   const __int128 s = nx == 0 || (ny > 0 && y->stride > x->stride) ? y->stride : x->stride;
-  long cx = 1, cy = 1;
+  __int128 cx = 1, cy = 1;
   if (nx > 0 && x->stride == s) cx = x->size, ex -= s * (cx - 1), ++x, --nx;
   if (ny > 0 && y->stride == s) cy = y->size, ey -= s * (cy - 1), ++y, --ny;
   const auto floor_div = [](__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); };
@@ -201,7 +200,7 @@ ss_status ss_rope_append_paged_ex(const void* q, void* q_out, const void* k, con
   if (q != nullptr && (!rows_apart(p.qos, q_size, 2, d) || q_out == k || q_out == v)) return SS_ERR_INVALID_ARG;
   if (T > kMaxRopeCount || Hq + 2l * Hkv > kMaxRopeCount) return SS_ERR_UNSUPPORTED;
   {  // what is written (q_out, the pools) lies apart from what is read, but for q turned in place
-    const long pool = static_cast<long>(num_pages) * Hkv * kTile * d;
+    const __int128 pool = static_cast<__int128>(num_pages) * Hkv * kTile * d;
     const auto rows = [&](const void* at, const long* s, int heads) {
       return span(at, {{s[0], T}, {s[1], heads}, {1, d}});
     };
@@ -447,6 +446,11 @@ static ss_status check_state(const int32_t* refs, int num_pages, const int32_t* 
   return SS_OK;
 }
 
+// Bytes of a pool, or more than any memory where that is too many to count.
+static size_t pool_bytes_of(size_t page_bytes, int num_pages) {
+  return page_bytes > SIZE_MAX / num_pages ? SIZE_MAX : page_bytes * num_pages;
+}
+
 static ss_status check_pools(void* const* pools, int num_pools, size_t page_bytes) {
   if (num_pools < 0 || (num_pools > 0 && pools == nullptr) || page_bytes == 0 || page_bytes % 16 != 0 ||
       page_bytes > (static_cast<size_t>(1) << 34))
@@ -464,7 +468,7 @@ struct Range {
   bool written;
   bool meets(const Range& r) const {
     const auto a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(r.at);
-    return bytes > 0 && r.bytes > 0 && a < b + r.bytes && b < a + bytes;
+    return bytes > 0 && r.bytes > 0 && (a <= b ? b - a < bytes : a - b < r.bytes);
   }
 };
 Range reads(const int32_t* p, long n) { return {p, p != nullptr ? 4 * static_cast<size_t>(n) : 0, false}; }
@@ -483,14 +487,15 @@ ss_status check_apart(std::initializer_list<Range> arrays, void* const* pools = 
   // Pools one behind the other, the usual order, take one pass, others are sorted.
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   bool in_order = true;
-  for (int i = 1; i < num_pools; ++i) in_order = in_order && at(pools[i]) >= at(pools[i - 1]) + pool_bytes;
+  for (int i = 1; i < num_pools; ++i)
+    in_order = in_order && at(pools[i]) > at(pools[i - 1]) && at(pools[i]) - at(pools[i - 1]) >= pool_bytes;
   if (in_order) return SS_OK;
   std::unique_ptr<uintptr_t[]> sorted(new (std::nothrow) uintptr_t[num_pools]);
   if (sorted == nullptr) return SS_ERR_CUDA;
   for (int i = 0; i < num_pools; ++i) sorted[i] = at(pools[i]);
   std::sort(sorted.get(), sorted.get() + num_pools);
   for (int i = 1; i < num_pools; ++i)
-    if (sorted[i] != sorted[i - 1] && sorted[i] < sorted[i - 1] + pool_bytes) return SS_ERR_INVALID_ARG;
+    if (sorted[i] != sorted[i - 1] && sorted[i] - sorted[i - 1] < pool_bytes) return SS_ERR_INVALID_ARG;
   return SS_OK;
 }
 }  // namespace
@@ -547,7 +552,7 @@ ss_status ss_pages_fork(void* const* pools, int num_pools, size_t page_bytes, in
   st = check_apart({writes(page_refs, num_pages), writes(page_table, entries), writes(seq_lens, num_rows),
                     writes(result, 1), {workspace, pages_workspace(num_pages, num_rows, n), true},
                     reads(src_rows, n), reads(dst_rows, n)},
-                   pools, num_pools, page_bytes * num_pages);
+                   pools, num_pools, pool_bytes_of(page_bytes, num_pages));
   if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
   return of(launch_pages_fork(pools, num_pools, page_bytes, s, src_rows, dst_rows, n, result, workspace,
@@ -565,7 +570,7 @@ ss_status ss_pages_copy(void* const* pools, int num_pools, size_t page_bytes, in
   if ((st = check_workspace(workspace, workspace_bytes, num_pages, 0, n)) != SS_OK) return st;
   st = check_apart({writes(result, 1), {workspace, pages_workspace(num_pages, 0, n), true}, reads(src, n),
                     reads(dst, n)},
-                   pools, num_pools, page_bytes * num_pages);
+                   pools, num_pools, pool_bytes_of(page_bytes, num_pages));
   if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   return of(launch_pages_copy(pools, num_pools, page_bytes, num_pages, src, dst, n, result, workspace,
                               static_cast<cudaStream_t>(stream)));
@@ -587,7 +592,7 @@ ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes,
                     reads(out_refs != page_refs ? page_refs : nullptr, num_pages),
                     reads(out_table != page_table ? page_table : nullptr, entries), reads(lens, num_rows),
                     writes(live, 1), {workspace, pages_workspace(num_pages, num_rows, 0), true}},
-                   pools, num_pools, page_bytes * num_pages);
+                   pools, num_pools, pool_bytes_of(page_bytes, num_pages));
   if (st != SS_OK || (st = check_device()) != SS_OK) return st;
   const PageState s{page_refs, page_table, lens, num_pages, num_rows, max_pages};
   return of(launch_pages_compact(pools, num_pools, page_bytes, s, out_refs, out_table, live, workspace,

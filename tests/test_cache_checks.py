@@ -579,3 +579,19 @@ def test_chunk_workspace_bound(capi):
     assert bound(0, 8, 2, 64, 128, 3) == 0 and bound(10, 1, 2, 64, 128, 3) == 0 and bound(10, 258, 2, 64, 128, 3) == 0
     ws, n = ss.chunk_paged_workspace(2048, 1, 32, 8, 256, 128, 8, "cpu")
     assert n == bound(2048, 32, 8, 256, 128, 8) and ws.numel() == n
+
+
+@without_gpu
+def test_sizes_beyond_64_bits_are_compared(capi):
+    """Pools of more bytes than 64 bits count reach everything behind them; nothing wraps round."""
+    far = 1 << 40
+    state = dict(page_refs=far, num_pages=1 << 30, page_table=2 * far, num_rows=4, max_pages=4, seq_lens=3 * far)
+    ws = dict(workspace=4 * far, workspace_bytes=1 << 40, stream=0)
+    lists = dict(src_rows=5 * far, dst_rows=6 * far, n=2)
+    assert capi.ss_pages_fork([FAKE], 1 << 34, **state, **ws, **lists) == capi.SS_ERR_INVALID_ARG     # (2^64 bytes a pool)
+    assert capi.ss_pages_fork([7 * far], 1 << 34, **state, **ws, **lists) not in (capi.SS_OK, capi.SS_ERR_INVALID_ARG)
+    assert capi.ss_pages_fork([7 * far, 8 * far], 1 << 34, **state, **ws, **lists) == capi.SS_ERR_INVALID_ARG
+    args = dict(q=None, q_out=None, k=2 * far, v=None, T=5, B=2, Hq=8, Hkv=1 << 20, d=1 << 16, cu_seqlens=FAKE, seq_lens=FAKE, inv_freq=FAKE,
+                rot_dim=128, k_pages=far, v_pages=None, page_table=FAKE, num_pages=1 << 30, max_pages=4, stream=0)
+    assert capi.ss_rope_append_paged(**args) == capi.SS_ERR_INVALID_ARG                               # (2^74 bytes)
+    assert capi.ss_rope_append_paged(**{**args, "k": FAKE, "k_pages": 1 << 60}) not in (capi.SS_OK, capi.SS_ERR_INVALID_ARG)
