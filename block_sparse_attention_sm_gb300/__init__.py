@@ -323,7 +323,8 @@ def stream_status(stream=None) -> None:
 
 
 _CACHE = ("rope_frequencies", "rope", "rope_append_paged", "chunk_paged", "chunk_paged_workspace",
-          "pages_reserve", "pages_free", "pages_fork", "pages_copy", "pages_compact")
+          "pages_reserve", "pages_free", "pages_fork", "pages_copy", "pages_compact", "prefix_plan",
+          "decode_shared", "decode_shared_workspace", "key_weights", "pages_evict")
 
 
 def __getattr__(name):

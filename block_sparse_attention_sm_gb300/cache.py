@@ -1,5 +1,6 @@
 """Helpers around the paged key/value cache: rotary positions, the write of new
-tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
+tokens, attention of a chunk of new tokens, decode over shared pages, the record
+of attention weights and eviction by it, and the pages' bookkeeping.
 
 As the helpers of the package itself: they check the tensors, allocate outputs
 and workspaces with torch and forward to the entry points of ``libssattn``.
@@ -406,6 +407,149 @@ def chunk_paged(q, k_pages, v_pages, page_table, cu_seqlens, seq_lens, *, scale:
     return o
 
 
+def prefix_plan(page_table, seq_lens, *, out=None, stream=None):
+    """What the sequences of a batch share, for :func:`decode_shared`: an int32 tensor on the device.
+
+    page_table int32 [B,max_pages], seq_lens int32 [B] (B up to 8192).
+    Sequences share the pages that their tables name alike from the first on
+    and that are full in both (as after :func:`pages_fork`), in any grouping
+    and on several levels.  The plan holds as long as these pages stay where
+    they are: over steps that append keys, but not across a fork, free,
+    eviction or compaction, after which it is made anew."""
+    _dense("page_table", page_table, _I32, 2)
+    B, max_pages = page_table.shape
+    _dense("seq_lens", seq_lens, _I32, None, (B,))
+    words = (capi._lib or capi.load()).ss_prefix_plan_size(B) // 4
+    if words == 0:
+        raise ValueError(f"prefix_plan: {B} sequences (1 to 8192)")
+    if out is not None:
+        _dense("out", out, _I32, None, (words,))
+    handle, context = _on(stream, "page_table seq_lens out", page_table, seq_lens, out)
+    with context:
+        if out is None:
+            out = torch.empty(words, dtype=_I32, device=page_table.device)
+        st = capi.ss_prefix_plan(page_table, seq_lens, B, max_pages, out, 4 * words, handle)
+    _check(st, "ss_prefix_plan")
+    return out
+
+
+def _recorded_weights(name, t, B, Hkv, max_pages):
+    _dense(name, t, torch.float32, None, (B, Hkv, max_pages * 128))
+
+
+def _scratch(workspace, need, device):
+    """(workspace, its bytes), made where it is not given."""
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device), need
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _tokens(q):
+    """Shape and token stride of queries [T,Hq,d] whose heads are contiguous within a token."""
+    shape, qs = _rows("q", q, 3)
+    T, Hq, d = shape
+    if Hq > 1 and qs[1] != d:
+        raise ValueError("q: the heads of a token must be contiguous")
+    if T > 1 and qs[0] < Hq * d:  # (a stride of 0, of a broadcast row, would mean contiguous rows to the entry point)
+        raise ValueError(f"q: its tokens overlap (stride {qs[0]}, rows of {Hq * d})")
+    return shape, qs[0] if T > 1 else 0
+
+
+def _pages_of(k_pages, d):
+    _dense("k_pages", k_pages, _BF16, 4)
+    num_pages, Hkv, page, dk = k_pages.shape
+    if page != 128 or dk != d:
+        raise ValueError(f"k_pages: expected [num_pages, Hkv, 128, {d}], got {tuple(k_pages.shape)}")
+    return num_pages, Hkv
+
+
+def decode_shared_workspace(B, Hq, Hkv, max_pages, d, device, *, plan=True, weights=False):
+    """A workspace that serves every :func:`decode_shared` call of up to B sequences and max_pages pages each."""
+    n = capi.ss_attn_decode_shared_workspace_size(B, Hq, Hkv, max_pages, d, plan, weights)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def decode_shared(q, k_pages, v_pages, page_table, seq_lens, plan=None, *, scale: float, weights=None, out=None,
+                  workspace=None, stream=None):
+    """Attention of one new token a sequence over the paged cache, pages that sequences share read once for all.
+
+    q [B,Hq,d] bf16 CUDA (heads contiguous within a token), k_pages / v_pages
+    [num_pages,Hkv,128,d], page_table int32 [B,max_pages], seq_lens int32 [B]
+    (the new key included).  ``plan``: what :func:`prefix_plan` found; None:
+    nothing is shared.  Every key counts (no skip test).  ``weights`` float32
+    [B,Hkv,max_pages*128]: each key's softmax weight, summed over the query
+    heads of its KV head, is added to it (:func:`pages_evict` chooses by it);
+    cells behind a sequence's end are left as they are.  A sequence without keys
+    gives zeros.  Returns o [B,Hq,d].  A serving call: it records no gradients."""
+    (B, Hq, d), stride = _tokens(q)
+    _dense("page_table", page_table, _I32, 2)
+    max_pages = page_table.shape[1]
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected {B} rows, got {page_table.shape[0]}")
+    _dense("seq_lens", seq_lens, _I32, None, (B,))
+    num_pages, Hkv = _pages_of(k_pages, d)
+    _dense("v_pages", v_pages, _BF16, None, k_pages.shape)
+    lib = capi._lib or capi.load()
+    if plan is not None:
+        _dense("plan", plan, _I32, None, (lib.ss_prefix_plan_size(B) // 4,))
+    if weights is not None:
+        _recorded_weights("weights", weights, B, Hkv, max_pages)
+    if out is not None:
+        _dense("out", out, _BF16, None, q.shape)
+    handle, context = _on(stream, "q k_pages v_pages page_table seq_lens plan weights out workspace", q, k_pages, v_pages,
+                          page_table, seq_lens, plan, weights, out, workspace)
+    with context:
+        o = out if out is not None else torch.empty((B, Hq, d), dtype=_BF16, device=q.device)
+        if B == 0:
+            return o
+        ws, nbytes = _scratch(workspace, lib.ss_attn_decode_shared_workspace_size(
+            B, Hq, Hkv, max_pages, d, plan is not None, weights is not None) if workspace is None else 0, q.device)
+        st = lib.ss_attn_decode_shared(
+            q.data_ptr(), stride, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+            plan.data_ptr() if plan is not None else None, o.data_ptr(), weights.data_ptr() if weights is not None else None,
+            B, Hq, Hkv, num_pages, max_pages, d, scale, ws.data_ptr(), nbytes, handle)
+    if st:
+        raise SSError(st, "ss_attn_decode_shared")
+    if out is not None:
+        _written(out)
+    if weights is not None:
+        _written(weights)
+    return o
+
+
+def key_weights(q, k_pages, page_table, cu_seqlens, seq_lens, weights, *, scale: float, causal: bool = True,
+                workspace=None, stream=None):
+    """Adds to ``weights`` the attention weight that each cached key receives from a step's packed new tokens.
+
+    q [T,Hq,d] bf16 CUDA (heads contiguous within a token; a prompt's tokens, or
+    only its last ones), k_pages [num_pages,Hkv,128,d], page_table int32
+    [B,max_pages], cu_seqlens int32 [B+1], seq_lens int32 [B] (keys, the new
+    tokens' included), weights float32 [B,Hkv,max_pages*128]: cell k of
+    sequence b and KV head h gains the softmax weights of key k, summed over
+    the sequence's new tokens and the query heads of h.  Causal: new token i of
+    n sees keys up to L - n + i, otherwise all.  The attention's output is not
+    computed.  Returns ``weights``."""
+    (T, Hq, d), stride = _tokens(q)
+    B, max_pages = _batch(page_table, cu_seqlens, seq_lens)
+    num_pages, Hkv = _pages_of(k_pages, d)
+    _recorded_weights("weights", weights, B, Hkv, max_pages)
+    handle, context = _on(stream, "q k_pages page_table cu_seqlens seq_lens weights workspace", q, k_pages, page_table,
+                          cu_seqlens, seq_lens, weights, workspace)
+    with context:
+        lib = capi._lib or capi.load()
+        ws, nbytes = _scratch(workspace, lib.ss_attn_key_weights_workspace_size(T, B, Hq, Hkv) if workspace is None else 0,
+                              q.device)
+        st = lib.ss_attn_key_weights(
+            q.data_ptr(), stride, k_pages.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+            weights.data_ptr(), T, B, Hq, Hkv, num_pages, max_pages, d, scale, bool(causal), ws.data_ptr(), nbytes, handle)
+    if st:
+        raise SSError(st, "ss_attn_key_weights")
+    _written(weights)
+    return weights
+
+
 def _state(page_refs, page_table, seq_lens):
     _dense("page_refs", page_refs, _I32, 1)
     _dense("page_table", page_table, _I32, 2)
@@ -552,3 +696,65 @@ def pages_compact(pools, page_refs, page_table, seq_lens, *, out_refs=None, out_
                                    seq_lens, out_refs, out_table, live, ws, nbytes, handle)
     _check(st, "ss_pages_compact")
     return live
+
+
+def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=None, recent: int = 0, out_weights=None,
+                out_refs=None, out_table=None, out_lens=None, result=None, workspace=None, stream=None):
+    """Cuts sequences back to ``keep`` (int32 [n]) keys: row rows[i], or row i.
+
+    ``pools``: each layer's in turn (its key and value pages; equally many a
+    layer), contiguous [num_pages,Hkv,128,...]; ``weights``: a float32
+    [num_rows,Hkv,max_pages*128] tensor a layer, as :func:`decode_shared` and
+    :func:`key_weights` add them up.  Every KV head of every layer keeps the
+    ``recent`` newest keys and, of the older ones, those of largest weight (of
+    equal ones the first; NaN is below every number), in their order, at the
+    front of the sequence's pages.  Weights move along, the cells behind the kept
+    keys become 0.  Pages that become free lose a holder; a kept page that other
+    sequences hold too is replaced by a free one.  Sequences of ``keep`` keys or
+    fewer stay as they are.  Keys hold the positions that they were rotated at:
+    later tokens need ``positions`` of their own.  ``out_refs``, ``out_table``,
+    ``out_lens`` and ``out_weights`` (a list; listed rows only) receive the new
+    state (default: in place); pools are always changed in place.  Returns
+    ``result``, an int32 [1] on the device: 0, the number of free pages that are
+    missing, or -1 for wrong arguments (then nothing has changed)."""
+    num_pages, num_rows, max_pages = _state(page_refs, page_table, seq_lens)
+    if len(weights) == 0 or len(pools) == 0 or len(pools) % len(weights):
+        raise ValueError(f"pages_evict: {len(pools)} pools for {len(weights)} layers of weights")
+    if out_weights is not None and len(out_weights) != len(weights):
+        raise ValueError(f"out_weights: expected {len(weights)} tensors, got {len(out_weights)}")
+    page_bytes = _pools(pools, num_pages)
+    for i, t in enumerate(weights):
+        _dense(f"weights[{i}]", t, torch.float32, 3)
+    Hkv = weights[0].shape[1]
+    shape = (num_rows, Hkv, max_pages * 128)
+    for name, some in (("weights", weights), ("out_weights", out_weights or ())):
+        for i, t in enumerate(some):
+            _dense(f"{name}[{i}]", t, torch.float32, None, shape)
+    for i, t in enumerate(pools):
+        if t.shape[1:3] != ((Hkv, 128) if t.ndim > 3 or Hkv > 1 else (128, t.shape[2])):
+            raise ValueError(f"pools[{i}]: expected [num_pages, {Hkv}, 128, ...], got {tuple(t.shape)}")
+    n = _list("keep", keep)
+    if rows is not None:
+        _list("rows", rows, n)
+    elif n > num_rows:
+        raise ValueError(f"keep: {n} entries for {num_rows} rows")
+    for name, t, like in (("out_refs", out_refs, page_refs), ("out_table", out_table, page_table), ("out_lens", out_lens, seq_lens)):
+        if t is not None:
+            _dense(name, t, _I32, None, like.shape)
+    if result is not None:
+        _dense("result", result, _I32, shape=(1,))
+    given = list(pools) + list(weights) + list(out_weights or ())
+    handle, context = _on(stream, "page_refs page_table seq_lens keep rows out_refs out_table out_lens result workspace" +
+                          " pool" * len(pools) + " weights" * (len(given) - len(pools)), page_refs, page_table, seq_lens, keep,
+                          rows, out_refs, out_table, out_lens, result, workspace, *given)
+    with context:
+        ws, nbytes = _scratch(workspace, capi.ss_pages_evict_workspace_size(
+            num_pages, num_rows, max_pages, n, Hkv, len(weights), len(pools)) if workspace is None else 0, page_refs.device)
+        if result is None:
+            result = torch.empty(1, dtype=_I32, device=page_refs.device)
+        st = capi.ss_pages_evict(pools, page_bytes, weights, Hkv, page_refs, num_pages, page_table, num_rows, max_pages,
+                                 seq_lens, rows, keep, n, recent, out_weights, out_refs, out_table, out_lens, result, ws,
+                                 nbytes, handle)
+    _check(st, "ss_pages_evict")
+    _written(tuple(weights if out_weights is None else out_weights))
+    return result

@@ -30,7 +30,9 @@ EXPORTS = (
     "ss_rope", "ss_rope_append_paged", "ss_rope_append_paged_ex", "ss_rope_frequencies",
     "ss_attn_chunk_paged", "ss_attn_chunk_paged_units", "ss_attn_chunk_paged_workspace_size",
     "ss_attn_chunk_paged_workspace_bound", "ss_pages_workspace_size", "ss_pages_reserve", "ss_pages_free", "ss_pages_fork",
-    "ss_pages_copy", "ss_pages_compact",
+    "ss_pages_copy", "ss_pages_compact", "ss_pages_evict", "ss_pages_evict_workspace_size",
+    "ss_prefix_plan", "ss_prefix_plan_size", "ss_attn_decode_shared", "ss_attn_decode_shared_workspace_size",
+    "ss_attn_key_weights", "ss_attn_key_weights_workspace_size",
 )
 
 
@@ -120,13 +122,25 @@ def load() -> ctypes.CDLL:
     lib.ss_pages_fork.argtypes = [P, I, U] + state + [P, P, I, P, P, U, P]
     lib.ss_pages_copy.argtypes = [P, I, U, I, P, P, I, P, P, U, P]
     lib.ss_pages_compact.argtypes = [P, I, U] + state + [P, P, P, P, U, P]
+    lib.ss_pages_evict.argtypes = [P, I, U, P, I, I] + state + [P, P, I, I, P, P, P, P, P, P, U, P]
+    lib.ss_pages_evict_workspace_size.argtypes = [I] * 7
+    lib.ss_prefix_plan.argtypes = [P, P, I, I, P, U, P]
+    lib.ss_prefix_plan_size.argtypes = [I]
+    lib.ss_attn_decode_shared.argtypes = [P, I64] + [P] * 7 + [I] * 6 + [F, P, U, P]
+    lib.ss_attn_decode_shared_workspace_size.argtypes = [I] * 7
+    lib.ss_attn_key_weights.argtypes = [P, I64] + [P] * 5 + [I] * 7 + [F, I, P, U, P]
+    lib.ss_attn_key_weights_workspace_size.argtypes = [I] * 4
+    for name in ("ss_pages_evict_workspace_size", "ss_prefix_plan_size", "ss_attn_decode_shared_workspace_size",
+                 "ss_attn_key_weights_workspace_size"):
+        getattr(lib, name).restype = U
     for name in ("ss_attn_prefill", "ss_attn_prefill_ex", "ss_attn_mla_prefill",
                  "ss_attn_mla_prefill_ex", "ss_attn_decode", "ss_attn_decode_ex",
                  "ss_attn_decode_noalloc", "ss_attn_decode_paged", "ss_attn_mla_decode",
                  "ss_attn_mla_decode_ex", "ss_attn_mla_decode_paged", "ss_calibrate",
                  "ss_fit_factor", "ss_stream_status", "ss_rope", "ss_rope_append_paged",
                  "ss_rope_append_paged_ex", "ss_rope_frequencies", "ss_attn_chunk_paged", "ss_pages_reserve", "ss_pages_free",
-                 "ss_pages_fork", "ss_pages_copy", "ss_pages_compact"):
+                 "ss_pages_fork", "ss_pages_copy", "ss_pages_compact", "ss_pages_evict", "ss_prefix_plan",
+                 "ss_attn_decode_shared", "ss_attn_key_weights"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -430,3 +444,55 @@ def ss_pages_compact(pools, page_bytes, page_refs, num_pages, page_table, num_ro
                                    num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens),
                                    _ptr(out_refs), _ptr(out_table), _ptr(live), _ptr(workspace),
                                    workspace_bytes, _stream(stream))
+
+
+def ss_pages_evict_workspace_size(num_pages, num_rows, max_pages, n, Hkv, num_layers, num_pools) -> int:
+    return int((_lib or load()).ss_pages_evict_workspace_size(num_pages, num_rows, max_pages, n, Hkv, num_layers,
+                                                              num_pools))
+
+
+def ss_pages_evict(pools, page_bytes, weights, Hkv, page_refs, num_pages, page_table, num_rows, max_pages, seq_lens,
+                   rows, keep, n, recent=0, out_weights=None, out_refs=None, out_table=None, out_lens=None,
+                   result=None, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Cuts sequences back to their keys of largest weight and their newest ones; pools: each layer's, in turn."""
+    to = _addresses(out_weights) if out_weights is not None else None
+    return (_lib or load()).ss_pages_evict(
+        (a := _addresses(pools)).buffer_info()[0], len(a), page_bytes, (w := _addresses(weights)).buffer_info()[0],
+        len(w), Hkv, _ptr(page_refs), num_pages, _ptr(page_table), num_rows, max_pages, _ptr(seq_lens), _ptr(rows),
+        _ptr(keep), n, recent, to.buffer_info()[0] if to is not None else None, _ptr(out_refs), _ptr(out_table),
+        _ptr(out_lens), _ptr(result), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def ss_prefix_plan_size(B) -> int:
+    return int((_lib or load()).ss_prefix_plan_size(B))
+
+
+def ss_prefix_plan(page_table, seq_lens, B, max_pages, plan, plan_bytes, stream=None) -> int:
+    """What the sequences of a batch share, from their page tables."""
+    return (_lib or load()).ss_prefix_plan(_ptr(page_table), _ptr(seq_lens), B, max_pages, _ptr(plan), plan_bytes,
+                                           _stream(stream))
+
+
+def ss_attn_decode_shared_workspace_size(B, Hq, Hkv, max_pages, d, with_plan, with_weights) -> int:
+    return int((_lib or load()).ss_attn_decode_shared_workspace_size(B, Hq, Hkv, max_pages, d, bool(with_plan),
+                                                                     bool(with_weights)))
+
+
+def ss_attn_decode_shared(q, k_pages, v_pages, page_table, seq_lens, plan, o, weights, B, Hq, Hkv, num_pages,
+                          max_pages, d, scale, workspace, workspace_bytes, q_token_stride=0, stream=None) -> int:
+    """Decode of one new token a sequence, shared pages read once; weights: the keys' attention weights are added."""
+    return (_lib or load()).ss_attn_decode_shared(
+        _ptr(q), q_token_stride, _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(seq_lens), _ptr(plan), _ptr(o),
+        _ptr(weights), B, Hq, Hkv, num_pages, max_pages, d, scale, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def ss_attn_key_weights_workspace_size(T, B, Hq, Hkv) -> int:
+    return int((_lib or load()).ss_attn_key_weights_workspace_size(T, B, Hq, Hkv))
+
+
+def ss_attn_key_weights(q, k_pages, page_table, cu_seqlens, seq_lens, weights, T, B, Hq, Hkv, num_pages, max_pages,
+                        d, scale, causal, workspace, workspace_bytes, q_token_stride=0, stream=None) -> int:
+    """Adds the attention weight that each cached key receives from a step's packed new tokens."""
+    return (_lib or load()).ss_attn_key_weights(
+        _ptr(q), q_token_stride, _ptr(k_pages), _ptr(page_table), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(weights), T,
+        B, Hq, Hkv, num_pages, max_pages, d, scale, bool(causal), _ptr(workspace), workspace_bytes, _stream(stream))

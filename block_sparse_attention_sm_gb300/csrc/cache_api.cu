@@ -1,5 +1,6 @@
 // C-ABI entry points around the paged cache: rotary positions, the write of
-// new tokens, attention of a chunk of new tokens, and the pages' bookkeeping.
+// new tokens, attention of a chunk of new tokens, decode over shared pages, the
+// record of attention weights and eviction by it, and the pages' bookkeeping.
 // Argument validation and launches; include/ssattn.h has each call's contract.
 #include <algorithm>
 #include <cmath>
@@ -9,8 +10,11 @@
 
 #include "api.cuh"
 #include "chunk_paged.cuh"
+#include "evict.cuh"
+#include "key_weights.cuh"
 #include "pages.cuh"
 #include "rope.cuh"
+#include "shared_decode.cuh"
 
 namespace ssattn {
 namespace {
@@ -106,6 +110,22 @@ bool meet(const Span& a, const Span& b) {
   if (a.at == nullptr || b.at == nullptr) return false;
   const __int128 gap = (static_cast<__int128>(reinterpret_cast<uintptr_t>(a.at)) - reinterpret_cast<uintptr_t>(b.at)) / 2;
   return meet(gap, a.axis, a.n, b.axis, b.n);
+}
+
+// q as [T][Hkv][G][d], tokens `stride` elements apart; a box is 64 entries of a
+// row block (tpb tokens x the G heads of a KV head).
+bool make_query_map(CUtensorMap* m, const void* q, int T, int Hkv, int G, int d, int64_t stride, long tpb) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G),
+                              static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(G) * d * 2,
+                                 static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tpb)};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -383,20 +403,7 @@ ss_status ss_attn_chunk_paged(const void* q, int64_t q_token_stride, const void*
   const long blocks = static_cast<long>(num_pages) * Hkv;
   if (!make_map(&tk, k_pages, d, kTile, blocks, kTile / 2) || !make_map(&tv, v_pages, d, kTile, blocks))
     return SS_ERR_CUDA;
-  {  // q as [T][Hkv][G][d]; a box is 64 entries of a row block
-    auto fn = encode_fn();
-    if (fn == nullptr) return SS_ERR_CUDA;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G),
-                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(T)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(G) * d * 2,
-                                   static_cast<cuuint64_t>(stride) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tpb)};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return SS_ERR_CUDA;
-  }
+  if (!make_query_map(&tq, q, T, Hkv, G, d, stride, tpb)) return SS_ERR_CUDA;
   ChunkParams p{};
   p.T = T;
   p.B = B;
@@ -597,6 +604,253 @@ ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes,
   const PageState s{page_refs, page_table, lens, num_pages, num_rows, max_pages};
   return of(launch_pages_compact(pools, num_pools, page_bytes, s, out_refs, out_table, live, workspace,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t ss_pages_evict_workspace_size(int num_pages, int num_rows, int max_pages, int n, int Hkv, int num_layers,
+                                     int num_pools) {
+  if (num_pages < 0 || num_rows < 0 || max_pages < 1 || n < 0 || Hkv < 1 || num_layers < 1 || num_pools < num_layers ||
+      num_pools % num_layers != 0 || num_pools / num_layers > kMaxPools)
+    return 0;
+  return evict_workspace(num_pages, num_rows, max_pages, n, Hkv, num_layers, num_pools / num_layers);
+}
+
+ss_status ss_pages_evict(void* const* pools, int num_pools, size_t page_bytes, float* const* weights, int num_layers,
+                         int Hkv, int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                         int32_t* seq_lens, const int32_t* rows, const int32_t* keep, int n, int recent,
+                         float* const* out_weights, int32_t* out_refs, int32_t* out_table, int32_t* out_lens,
+                         int32_t* result, void* workspace, size_t workspace_bytes, void* stream) {
+  ss_status st = check_state(page_refs, num_pages, page_table, num_rows, max_pages, seq_lens);
+  if (st != SS_OK || (st = check_pools(pools, num_pools, page_bytes)) != SS_OK) return st;
+  if (num_layers < 1 || weights == nullptr || num_pools < num_layers || num_pools % num_layers != 0 || Hkv < 1 ||
+      page_bytes % (static_cast<size_t>(Hkv) * kTile * 16) != 0 || n < 0 || recent < 0 || (n > 0 && keep == nullptr) ||
+      (rows == nullptr && n > num_rows) || !aligned4(rows) || !aligned4(keep) || !aligned4(result))
+    return SS_ERR_INVALID_ARG;
+  if (num_pools / num_layers > kMaxPools || page_bytes / (static_cast<size_t>(Hkv) * kTile) > (1u << 20) ||
+      static_cast<__int128>(n) * Hkv * (4 * kMaxPools + 16) + num_rows > 0x3fffffff)
+    return SS_ERR_UNSUPPORTED;
+  if (out_refs == nullptr) out_refs = page_refs;
+  if (out_table == nullptr) out_table = page_table;
+  if (out_lens == nullptr) out_lens = seq_lens;
+  if (out_weights == nullptr) out_weights = weights;
+  if (!aligned16(out_refs) || !aligned4(out_table) || !aligned4(out_lens)) return SS_ERR_INVALID_ARG;
+  if (static_cast<__int128>(num_rows > n ? num_rows : n) * Hkv * max_pages > (1l << 40)) return SS_ERR_INVALID_ARG;
+  const size_t need = evict_workspace(num_pages, num_rows, max_pages, n, Hkv, num_layers, num_pools / num_layers);
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return SS_ERR_WORKSPACE;
+  const long entries = static_cast<long>(num_rows) * max_pages;
+  st = check_apart({writes(out_refs, num_pages), writes(out_table, entries), writes(out_lens, num_rows),
+                    reads(out_refs != page_refs ? page_refs : nullptr, num_pages),
+                    reads(out_table != page_table ? page_table : nullptr, entries),
+                    reads(out_lens != seq_lens ? seq_lens : nullptr, num_rows), writes(result, 1),
+                    {workspace, need, true}, reads(rows, n), reads(keep, n)},
+                   pools, num_pools, pool_bytes_of(page_bytes, num_pages));
+  if (st != SS_OK) return st;
+  // The layers' weights: apart from everything else and, as each layer chooses for itself, from one another.
+  const size_t bytes = static_cast<size_t>(num_rows) * Hkv * max_pages * kTile * 4;
+  const Range fixed[] = {writes(out_refs, num_pages), writes(out_table, entries), writes(out_lens, num_rows),
+                         writes(page_refs, num_pages), writes(page_table, entries), writes(seq_lens, num_rows),
+                         writes(result, 1), {workspace, need, true}, reads(rows, n), reads(keep, n)};
+  std::unique_ptr<uintptr_t[]> sorted(new (std::nothrow) uintptr_t[2 * static_cast<size_t>(num_layers)]);
+  if (sorted == nullptr) return SS_ERR_CUDA;
+  int count = 0;
+  for (int l = 0; l < num_layers; ++l) {
+    const float* both[2] = {weights[l], out_weights[l]};
+    for (int k = 0; k < (both[0] == both[1] ? 1 : 2); ++k) {
+      if (both[k] == nullptr || !aligned16(both[k])) return SS_ERR_INVALID_ARG;
+      const Range w{both[k], bytes, true};
+      for (const Range& r : fixed)
+        if (w.meets(r)) return SS_ERR_INVALID_ARG;
+      for (int i = 0; i < num_pools; ++i)
+        if (w.meets({pools[i], pool_bytes_of(page_bytes, num_pages), true})) return SS_ERR_INVALID_ARG;
+      sorted[count++] = reinterpret_cast<uintptr_t>(both[k]);
+    }
+  }
+  std::sort(sorted.get(), sorted.get() + count);
+  for (int i = 1; i < count; ++i)
+    if (sorted[i] - sorted[i - 1] < bytes) return SS_ERR_INVALID_ARG;
+  // (pools listed twice would be moved twice)
+  for (int i = 1; i < num_pools; ++i)
+    for (int j = 0; j < i; ++j)
+      if (pools[i] == pools[j]) return SS_ERR_INVALID_ARG;
+  if ((st = check_device()) != SS_OK) return st;
+  EvictArgs a{};
+  a.s = PageState{page_refs, page_table, seq_lens, num_pages, num_rows, max_pages};
+  a.pools = pools;
+  a.weights = weights;
+  a.out_weights = out_weights;
+  a.num_layers = num_layers;
+  a.per_layer = num_pools / num_layers;
+  a.Hkv = Hkv;
+  a.page_bytes = page_bytes;
+  a.rows = rows;
+  a.keep = keep;
+  a.n = n;
+  a.recent = recent;
+  a.out_refs = out_refs;
+  a.out_table = out_table;
+  a.out_lens = out_lens;
+  a.result = result;
+  return of(launch_pages_evict(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- shared pages, attention weights
+
+// Tiles of fp32 cells (512 bytes) that an array may have: more than any memory holds, and countable.
+constexpr long kMaxCells = 1l << 44;
+
+size_t ss_prefix_plan_size(int B) { return B < 1 || B > kPlanMaxB ? 0 : plan_words(B) * sizeof(int32_t); }
+
+ss_status ss_prefix_plan(const int32_t* page_table, const int32_t* seq_lens, int B, int max_pages, int32_t* plan,
+                         size_t plan_bytes, void* stream) {
+  if (page_table == nullptr || seq_lens == nullptr || plan == nullptr || B < 1 || max_pages < 1 ||
+      static_cast<long>(max_pages) * kTile > 0x7fffffffL || !aligned4(page_table) || !aligned4(seq_lens) ||
+      !aligned4(plan))
+    return SS_ERR_INVALID_ARG;
+  if (B > kPlanMaxB) return SS_ERR_UNSUPPORTED;
+  if (plan_bytes < ss_prefix_plan_size(B)) return SS_ERR_WORKSPACE;
+  ss_status st = check_apart({{plan, ss_prefix_plan_size(B), true}, reads(page_table, static_cast<long>(B) * max_pages),
+                              reads(seq_lens, B)});
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
+  return of(launch_prefix_plan(page_table, seq_lens, B, max_pages, plan, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ss_attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages, int d, int with_plan,
+                                            int with_weights) {
+  if (B < 1 || Hkv < 1 || Hq < Hkv || max_pages < 1 || d < 1) return 0;
+  return shared_space(B, Hq, Hkv, max_pages, d, with_plan != 0, with_weights != 0).bytes;
+}
+
+ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const void* k_pages, const void* v_pages,
+                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* plan, void* o,
+                                float* weights, int B, int Hq, int Hkv, int num_pages, int max_pages, int d,
+                                float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1 || !(scale > 0.f) ||
+      !std::isfinite(scale))
+    return SS_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hq / Hkv > kTile) return SS_ERR_UNSUPPORTED;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || page_table == nullptr || seq_lens == nullptr ||
+      o == nullptr)
+    return SS_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * d, stride = q_token_stride != 0 ? q_token_stride : row;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned16(weights) ||
+      !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(plan) || (B > 1 && stride < row) || stride % 8 != 0)
+    return SS_ERR_INVALID_ARG;
+  if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL ||
+      static_cast<long>(B) * Hq > 0x3fffffffL || stride >= (1LL << 38))
+    return SS_ERR_INVALID_ARG;
+  if (B > 65535 || Hkv > 65535 || (plan != nullptr && B > kPlanMaxB)) return SS_ERR_UNSUPPORTED;
+  if (static_cast<__int128>(B) * Hq * max_pages > kMaxCells) return SS_ERR_INVALID_ARG;
+  const SharedSpace space = shared_space(B, Hq, Hkv, max_pages, d, plan != nullptr, weights != nullptr);
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < space.bytes) return SS_ERR_WORKSPACE;
+  const size_t pool = static_cast<size_t>(num_pages) * Hkv * kTile * d * 2;
+  const long cells = weights != nullptr ? static_cast<long>(B) * Hkv * max_pages * kTile : 0;
+  ss_status st = check_apart({{o, static_cast<size_t>(B) * row * 2, true},
+                              {weights, static_cast<size_t>(cells) * 4, true},
+                              {workspace, space.bytes, true},
+                              {q, (static_cast<size_t>(B - 1) * stride + row) * 2, false},
+                              {k_pages, pool, false},
+                              {v_pages, pool, false},
+                              reads(page_table, static_cast<long>(B) * max_pages),
+                              reads(seq_lens, B),
+                              {plan, plan != nullptr ? ss_prefix_plan_size(B) : 0, false}});
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
+  CUtensorMap tk, tv;
+  const long blocks = static_cast<long>(num_pages) * Hkv;
+  if (!make_map(&tk, k_pages, d, kTile, blocks) || !make_map(&tv, v_pages, d, kTile, blocks)) return SS_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  SharedParams p{};
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.ctas = shared_ctas(B, Hq, Hkv, max_pages);
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = stride;
+  p.table = page_table;
+  p.lens = seq_lens;
+  p.plan = plan;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.part_o = reinterpret_cast<float*>(ws + space.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);
+  p.part_rows = space.part_rows;
+  p.node_at = reinterpret_cast<long long*>(ws + space.node_at);
+  p.node_rows = reinterpret_cast<long long*>(ws + space.node_rows);
+  if (weights != nullptr) {
+    p.lse = reinterpret_cast<float*>(ws + space.lse);
+    p.scores = reinterpret_cast<float*>(ws + space.scores);
+    p.weights = weights;
+  }
+  p.status = status_ptr();
+  return of(launch_shared_decode(d, tk, tv, p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ss_attn_key_weights_workspace_size(int T, int B, int Hq, int Hkv) {
+  if (T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq / Hkv > kTile) return 0;
+  return key_weights_space(T, B, Hq, Hkv).bytes;
+}
+
+ss_status ss_attn_key_weights(const void* q, int64_t q_token_stride, const void* k_pages, const int32_t* page_table,
+                              const int32_t* cu_seqlens, const int32_t* seq_lens, float* weights, int T, int B, int Hq,
+                              int Hkv, int num_pages, int max_pages, int d, float scale, int causal, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1 || !(scale > 0.f) ||
+      !std::isfinite(scale))
+    return SS_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if ((d != 64 && d != 128) || G > kTile) return SS_ERR_UNSUPPORTED;
+  if ((T > 0 && q == nullptr) || k_pages == nullptr || page_table == nullptr || cu_seqlens == nullptr ||
+      seq_lens == nullptr || weights == nullptr)
+    return SS_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * d, stride = q_token_stride != 0 ? q_token_stride : row;
+  const long tpb = kTile / G, places = key_weights_places(T, B, tpb);
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(weights) || !aligned4(page_table) || !aligned4(cu_seqlens) ||
+      !aligned4(seq_lens) || (T > 1 && stride < row) || stride % 8 != 0)
+    return SS_ERR_INVALID_ARG;
+  if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || T > 0x7fffffff - 4 * kTile ||
+      static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL || places > 0x3fffffffL || stride >= (1LL << 38))
+    return SS_ERR_INVALID_ARG;
+  if (static_cast<__int128>(B) * Hkv * max_pages > kMaxCells || static_cast<__int128>(T) * stride > (static_cast<__int128>(1) << 60))
+    return SS_ERR_INVALID_ARG;
+  if (T == 0) return SS_OK;
+  const KeyWeightsSpace space = key_weights_space(T, B, Hq, Hkv);
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < space.bytes) return SS_ERR_WORKSPACE;
+  ss_status st = check_apart({{weights, static_cast<size_t>(B) * Hkv * max_pages * kTile * 4, true},
+                              {workspace, space.bytes, true},
+                              {q, (static_cast<size_t>(T - 1) * stride + row) * 2, false},
+                              {k_pages, static_cast<size_t>(num_pages) * Hkv * kTile * d * 2, false},
+                              reads(page_table, static_cast<long>(B) * max_pages),
+                              reads(cu_seqlens, B + 1l),
+                              reads(seq_lens, B)});
+  if (st != SS_OK || (st = check_device()) != SS_OK) return st;
+  CUtensorMap tq, tk;
+  if (!make_map(&tk, k_pages, d, kTile, static_cast<long>(num_pages) * Hkv) ||
+      !make_query_map(&tq, q, T, Hkv, G, d, stride, tpb))
+    return SS_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  KeyWeightsParams p{};
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.tpb = static_cast<int>(tpb);
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.cu_seqlens = cu_seqlens;
+  p.seq_lens = seq_lens;
+  p.page_table = page_table;
+  p.weights = weights;
+  p.lse = reinterpret_cast<float*>(ws + space.lse);
+  p.places = places;
+  p.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);
+  p.part_w = reinterpret_cast<float*>(ws + space.part_w);
+  p.split = reinterpret_cast<Split*>(ws + space.split);
+  p.status = status_ptr();
+  return of(launch_key_weights(d, tq, tk, p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,491 @@
+// Eviction from the paged cache by accumulated attention weight: each listed
+// sequence is cut back to `keep` keys, every KV head of every layer choosing
+// its own (the newest `recent` of them, and of the older ones those of largest
+// weight), in the pages themselves.
+//
+// choose_kernel: one block a (sequence, layer, head).  The keep - recent
+// largest of L - recent fp32 weights by radix selection: three histograms (11,
+// 11 and 10 bits of the weight as an unsigned number in the same order) give
+// the smallest kept weight exactly, then one pass in the order of the keys
+// takes what is above it and the first of those equal to it, and writes their
+// places.  The weights are read from L2 after the first pass (4 bytes a key
+// next to the 4 d of keys and values that are moved).
+// Block 0 of the first such launch decides, as the other page calls do: it
+// checks the call, gives fresh pages to those that other sequences hold too
+// (they are read, never written), and takes note of the old and new pages.
+//
+// move_kernel: kept rows move to the front of the sequence's pages.  Row d
+// comes from src[d] >= d with src ascending, so a block that walks d upwards
+// and has read the rows of a piece [d0, d1) before it writes it can move them in
+// place: pieces behind read from src >= d1, which is not written yet.  A block
+// has (sequence, head, pool) to itself, or 64-byte columns of it where
+// there are few; it keeps kStages pieces in flight with asynchronous copies.
+// The record of weights moves along, and the tables, lengths and counts follow.
+//
+// Bound by memory: kept rows are read and written once.
+#include "evict.cuh"
+
+#include "common.cuh"
+#include "pages_plan.cuh"
+#include "ptx_sm103.cuh"
+
+namespace ssattn {
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int kChoose = 1024;  // threads of a choosing block (kPlan: block 0 plans)
+static_assert(kChoose == kPlan, "block 0 of a choosing launch plans");
+constexpr int kBins = 2048;
+constexpr int kMove = 256;
+constexpr int kPieceBytes = 16384;  // rows that a moving block reads before it writes them
+constexpr int kStages = 4;
+constexpr int kGroup = 16;     // layers of a launch
+
+struct Cut {      // what becomes of a listed sequence
+  int row, len, now;
+};
+
+// Workspace.
+struct Space {
+  int32_t* head;   // [0]: accepted
+  Cut* cut;        // [n]
+  int32_t* base;   // [n] first of a sequence's fresh pages in `list`
+  int32_t* entry;  // [num_rows] which listed sequence a row is, -1: none
+  int32_t* list;   // [num_pages] lowest free pages
+  int32_t* from;   // [n][max_pages] old pages
+  int32_t* to;     // [n][max_pages] new pages
+  uint32_t* bits;
+  int32_t* src;    // [layers of a launch][n][Hkv][max_pages * 128] kept keys
+};
+
+constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+size_t space_of(Space* s, void* ws, int num_pages, int num_rows, int max_pages, int n, int Hkv, int layers) {
+  char* base = static_cast<char*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* here = base + at;
+    at += up16(bytes);
+    return here;
+  };
+  const size_t N = n, W = max_pages;
+  Space x;
+  x.head = reinterpret_cast<int32_t*>(take(32));
+  x.cut = reinterpret_cast<Cut*>(take(N * sizeof(Cut)));
+  x.base = reinterpret_cast<int32_t*>(take(N * 4));
+  x.entry = reinterpret_cast<int32_t*>(take(static_cast<size_t>(num_rows) * 4));
+  x.list = reinterpret_cast<int32_t*>(take(static_cast<size_t>(num_pages) * 4));
+  x.from = reinterpret_cast<int32_t*>(take(N * W * 4));
+  x.to = reinterpret_cast<int32_t*>(take(N * W * 4));
+  x.bits = reinterpret_cast<uint32_t*>(take(2 * static_cast<size_t>(bit_words(num_pages, num_rows)) * 4));
+  x.src = reinterpret_cast<int32_t*>(take(static_cast<size_t>(layers) * N * Hkv * W * kTile * 4));
+  if (s != nullptr) *s = x;
+  return at;
+}
+
+int layers_of_a_launch(int num_layers, int per_layer) {
+  const int fit = kMaxPools / per_layer < kGroup ? kMaxPools / per_layer : kGroup;
+  return num_layers < fit ? num_layers : fit;
+}
+
+struct Layers {
+  const float* weights[kGroup];
+  float* out[kGroup];
+  int count;
+};
+
+struct Call {
+  PageState s;
+  const int32_t* rows;
+  const int32_t* keep;
+  int n, recent, Hkv;
+  int32_t* out_refs;
+  int32_t* out_table;
+  int32_t* out_lens;
+  int32_t* result;
+};
+
+// ---------------------------------------------------------------------- plan
+__device__ void plan_block(const Call& c, const Space& w) {
+  const PageState& s = c.s;
+  bool bad = c.rows != nullptr && bad_indices(w.bits, bit_words(s.num_pages, s.num_rows), nullptr, c.rows, c.n, s.num_rows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!bad) {
+    for (int i = threadIdx.x; i < c.n; i += kPlan) {
+      const int row = c.rows != nullptr ? c.rows[i] : i;
+      const int len = s.lens[row], keep = c.keep[i];
+      if (len < 0 || len > s.max_pages * kTile || keep < 0) bad = true;
+      w.cut[i] = Cut{row, len, min(len, keep)};
+    }
+    bad = __syncthreads_or(bad);
+  }
+  // pages that a cut sequence keeps and others hold too
+  long need = 0;
+  if (!bad) {
+    for (int i = warp; i < c.n; i += kPlan / 32) {
+      const Cut x = w.cut[i];
+      int count = 0;
+      if (x.now < x.len)
+        for (int j = lane; j < tiles_of(x.now); j += 32) {
+          const int p = s.table[static_cast<long>(x.row) * s.max_pages + j];
+          count += p >= 0 && p < s.num_pages && s.refs[p] > 1;
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+      if (lane == 0) w.base[i] = count;
+    }
+    __syncthreads();
+    for (int i0 = 0; i0 < c.n; i0 += kPlan) {
+      const int i = i0 + threadIdx.x;
+      long total;
+      const long at = block_scan(static_cast<long>(i < c.n ? w.base[i] : 0), &total);
+      if (i < c.n) w.base[i] = static_cast<int>(need + at);
+      need += total;
+    }
+  }
+  int found = 0;
+  if (!bad) found = find_free(s.refs, s.num_pages, static_cast<int>(min(need, static_cast<long>(s.num_pages))), w.list);
+  const bool accepted = !bad && found >= need;
+  if (threadIdx.x == 0) {
+    w.head[0] = accepted;
+    if (c.result != nullptr) *c.result = bad ? -1 : static_cast<int>(min(need - found, 0x7fffffffL));
+  }
+  if (!accepted) return;
+  __syncthreads();  // base, list
+  if (c.out_refs != s.refs)
+    for (int p = threadIdx.x; p < s.num_pages; p += kPlan) c.out_refs[p] = s.refs[p];
+  for (int r = threadIdx.x; r < s.num_rows; r += kPlan) w.entry[r] = -1;
+  __syncthreads();
+  // old and new pages, before any count changes
+  for (int i = warp; i < c.n; i += kPlan / 32) {
+    const Cut x = w.cut[i];
+    if (lane == 0) w.entry[x.row] = i;
+    const int old = tiles_of(x.len), now = tiles_of(x.now);
+    int32_t* from = w.from + static_cast<long>(i) * s.max_pages;
+    int32_t* to = w.to + static_cast<long>(i) * s.max_pages;
+    int at = w.base[i];
+    for (int j0 = 0; j0 < old; j0 += 32) {
+      const int j = j0 + lane;
+      const int p = j < old ? s.table[static_cast<long>(x.row) * s.max_pages + j] : -1;
+      const bool shared = x.now < x.len && j < now && p >= 0 && p < s.num_pages && s.refs[p] > 1;
+      const uint32_t m = __ballot_sync(0xffffffffu, shared);
+      if (j < old) {
+        from[j] = p;
+        to[j] = j >= now ? -1 : shared ? w.list[at + __popc(m & ((1u << lane) - 1))] : p;
+      }
+      at += __popc(m);
+    }
+  }
+  __syncthreads();
+  // pages given up lose a holder, fresh ones have one
+  for (int i = warp; i < c.n; i += kPlan / 32) {
+    const Cut x = w.cut[i];
+    for (int j = lane; j < tiles_of(x.len); j += 32) {
+      const int p = w.from[static_cast<long>(i) * s.max_pages + j], q = w.to[static_cast<long>(i) * s.max_pages + j];
+      if (p == q) continue;
+      if (p >= 0 && p < s.num_pages) atomicSub(&c.out_refs[p], 1);
+      if (q >= 0) c.out_refs[q] = 1;
+    }
+  }
+}
+
+// -------------------------------------------------------------------- choose
+// A weight as an unsigned number of the same order; NaN below everything.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kChoose)
+    choose_kernel(const Call c, const Space w, const Layers layers, int plan_too) {
+  if (plan_too && blockIdx.x == 0) {
+    plan_block(c, w);
+    return;
+  }
+  const int at = blockIdx.x - plan_too;
+  const int h = at % c.Hkv, i = at / c.Hkv % c.n, layer = at / c.Hkv / c.n;
+  const PageState& s = c.s;
+  const int row = c.rows != nullptr ? c.rows[i] : i;
+  if (row < 0 || row >= s.num_rows) return;
+  const int len = max(0, min(s.lens[row], s.max_pages * kTile)), keep = max(0, c.keep[i]);
+  if (len <= keep) return;
+  const int newest = min(keep, c.recent), rest = len - newest, best = keep - newest;
+  const long width = static_cast<long>(s.max_pages) * kTile;
+  const float* weight = layers.weights[layer] + (static_cast<long>(row) * c.Hkv + h) * width;
+  int32_t* src = w.src + ((static_cast<long>(layer) * c.n + i) * c.Hkv + h) * width;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // The value of the best-th largest of weight[0, rest), and how many of those equal to it are kept.
+  __shared__ int bins[kBins];
+  __shared__ int s_bin, s_above;
+  uint32_t value = 0;
+  int wanted = best;
+  if (best > 0 && best < rest) {
+    int low = 32;  // bits of `value` from here up are known
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int width_bits = pass < 2 ? 11 : 10;
+      const uint32_t known = pass == 0 ? 0u : 0xffffffffu << low;
+      low -= width_bits;
+      for (int b = tid; b < kBins; b += kChoose) bins[b] = 0;
+      __syncthreads();
+      for (int k0 = warp * 128; k0 < rest; k0 += kChoose * 4) {
+        const int k = k0 + lane * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < rest) v = *reinterpret_cast<const float4*>(weight + k);
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = order_of(x[e]);
+          const bool in = k + e < rest && (u & known) == value;
+          const int bin = static_cast<int>((u >> low) & ((1u << width_bits) - 1));
+          // (equal weights, as the zeros of keys that nobody looks at, are counted once a warp)
+          const uint32_t m = __ballot_sync(0xffffffffu, in);
+          if (m == 0) continue;
+          const int first = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
+          if (__ballot_sync(0xffffffffu, in && bin == first) == m) {
+            if (lane == 0) atomicAdd(&bins[first], __popc(m));
+          } else if (in) {
+            atomicAdd(&bins[bin], 1);
+          }
+        }
+      }
+      __syncthreads();
+      // from the top: thread t has bins 2047 - 2t and below it
+      const int hi = bins[kBins - 1 - 2 * tid], lo = bins[kBins - 2 - 2 * tid];
+      int total;
+      const int above = block_scan(hi + lo, &total);
+      if (above < wanted && above + hi >= wanted) {
+        s_bin = kBins - 1 - 2 * tid;
+        s_above = above;
+      } else if (above + hi < wanted && above + hi + lo >= wanted) {
+        s_bin = kBins - 2 - 2 * tid;
+        s_above = above + hi;
+      }
+      __syncthreads();
+      value |= static_cast<uint32_t>(s_bin) << low;
+      wanted -= s_above;
+    }
+  }
+  // wanted: of the weights equal to `value`; all of them if every older key is kept, none if none is.
+  const bool all = best >= rest, none = best <= 0;
+  // Each warp has a run of keys, whole words of 32; first it counts, then it writes.
+  const int words = (len + 31) / 32, each = (words + kChoose / 32 - 1) / (kChoose / 32);
+  const int w0 = min(words, warp * each), w1 = min(words, w0 + each);
+  auto kinds = [&](int word, uint32_t* above, uint32_t* equal) {
+    const int k = word * 32 + lane;
+    bool a = false, e = false;
+    if (k < rest) {
+      if (all) {
+        a = true;
+      } else if (!none) {
+        const uint32_t u = order_of(weight[k]);
+        a = u > value;
+        e = u == value;
+      }
+    } else if (k < len) {
+      a = true;  // one of the newest
+    }
+    *above = __ballot_sync(0xffffffffu, a);
+    *equal = __ballot_sync(0xffffffffu, e);
+  };
+  int n_above = 0, n_equal = 0;
+  for (int word = w0; word < w1; ++word) {
+    uint32_t a, e;
+    kinds(word, &a, &e);
+    n_above += __popc(a);
+    n_equal += __popc(e);
+  }
+  int total;
+  const int equal_before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? n_equal : 0, &total), 0);
+  const int taken = max(0, min(n_equal, wanted - equal_before));
+  int out = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? n_above + taken : 0, &total), 0);
+  int left = all || none ? 0 : taken;
+  for (int word = w0; word < w1; ++word) {
+    uint32_t a, e;
+    kinds(word, &a, &e);
+    const bool tie = (e >> lane) & 1u && __popc(e & ((1u << lane) - 1)) < left;
+    left -= min(left, __popc(e));
+    const uint32_t kept = a | __ballot_sync(0xffffffffu, tie);
+    if ((kept >> lane) & 1u) {
+      const int d = out + __popc(kept & ((1u << lane) - 1));
+      if (d < keep) src[d] = word * 32 + lane;
+    }
+    out += __popc(kept);
+  }
+}
+
+// ---------------------------------------------------------------------- move
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows of one (sequence, head, pool), columns [column, column + 16 words).
+__device__ void move_rows(const Call& c, const Space& w, unsigned char* pool, size_t page_bytes, int i, int h,
+                          const int32_t* src, int row_bytes, int column, int words, unsigned char* stage) {
+  const Cut x = w.cut[i];
+  const int32_t* from = w.from + static_cast<long>(i) * c.s.max_pages;
+  const int32_t* to = w.to + static_cast<long>(i) * c.s.max_pages;
+  const int per_pass = kMove / words;                       // rows that the block takes at once
+  const int piece = max(1, min(kTile, kPieceBytes / 16 / words)) / per_pass * per_pass;  // rows of a piece
+  const int rows = piece > 0 ? piece : per_pass;
+  const int word = threadIdx.x % words, lead = threadIdx.x / words;
+  const bool busy = lead < per_pass;
+  unsigned char* mine = pool + static_cast<size_t>(h) * kTile * row_bytes + column + word * 16;
+  const int pieces = (x.now + rows - 1) / rows;
+  auto valid = [&](int p) { return p >= 0 && p < c.s.num_pages; };
+  auto fetch = [&](int q) {
+    if (q < pieces && busy) {
+      for (int r = lead; r < rows; r += per_pass) {
+        const int d = q * rows + r;
+        if (d >= x.now) break;
+        const int k = src[d], p = from[k / kTile];
+        if (valid(p))
+          copy_async16(smem_u32(stage + (static_cast<size_t>(q % kStages) * rows + r) * words * 16 + word * 16),
+                       mine + static_cast<size_t>(p) * page_bytes + static_cast<size_t>(k % kTile) * row_bytes);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int q = 0; q < kStages - 1; ++q) fetch(q);
+#pragma unroll 1
+  for (int q = 0; q < pieces; ++q) {
+    fetch(q + kStages - 1);
+    copy_wait<kStages - 1>();
+    __syncthreads();  // the piece has been read by all
+    if (busy)
+      for (int r = lead; r < rows; r += per_pass) {
+        const int d = q * rows + r;
+        if (d >= x.now) break;
+        const int p = to[d / kTile];
+        const int k = src[d];
+        if (!valid(p) || !valid(from[k / kTile]) || (k == d && p == from[d / kTile])) continue;
+        *reinterpret_cast<uint4*>(mine + static_cast<size_t>(p) * page_bytes + static_cast<size_t>(d % kTile) * row_bytes) =
+            *reinterpret_cast<const uint4*>(stage + (static_cast<size_t>(q % kStages) * rows + r) * words * 16 + word * 16);
+      }
+    __syncthreads();  // its place is filled again in the next turn
+  }
+}
+
+// The weights of one (sequence, layer, head): as move_rows, a piece in registers.
+__device__ void move_weights(const Cut& x, const int32_t* src, const float* from, float* to, long width) {
+  const bool cut = x.now < x.len;
+  if (!cut && from == to) return;
+  constexpr int U = 8;
+  for (int d0 = 0; d0 < x.now; d0 += kMove * U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int d = d0 + u * kMove + threadIdx.x;
+      v[u] = d < x.now ? from[cut ? src[d] : d] : 0.f;
+    }
+    __syncthreads();  // all of the piece has been read
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int d = d0 + u * kMove + threadIdx.x;
+      if (d < x.now) to[d] = v[u];
+    }
+  }
+  for (long d = x.now + threadIdx.x; d < width; d += kMove) to[d] = 0.f;
+}
+
+__global__ void __launch_bounds__(kMove)
+    move_kernel(const Call c, const Space w, const Layers layers, const PagePools pools, int per_layer, int slices,
+                int state_too) {
+  extern __shared__ unsigned char stage[];
+  if (w.head[0] == 0) return;
+  const PageState& s = c.s;
+  const long width = static_cast<long>(s.max_pages) * kTile;
+  const long lists = static_cast<long>(c.n) * c.Hkv;  // of a layer
+  const long movers = lists * pools.count * slices;
+  long at = blockIdx.x;
+  if (at < movers) {
+    const int slice = static_cast<int>(at % slices);
+    at /= slices;
+    const int h = static_cast<int>(at % c.Hkv);
+    at /= c.Hkv;
+    const int i = static_cast<int>(at % c.n), pool = static_cast<int>(at / c.n);
+    const Cut x = w.cut[i];
+    if (x.now == x.len || x.now == 0) return;
+    const int row_bytes = static_cast<int>(pools.page_bytes / (static_cast<size_t>(c.Hkv) * kTile));
+    const int32_t* src = w.src + (pool / per_layer * lists + static_cast<long>(i) * c.Hkv + h) * width;
+    const int all = row_bytes / 16, each = (all + slices - 1) / slices;  // 16-byte words of a row, of a slice
+    for (int first = slice * each; first < min(all, (slice + 1) * each); first += kMove) {
+      move_rows(c, w, pools.base[pool], pools.page_bytes, i, h, src, row_bytes, first * 16,
+                min(kMove, min(all, (slice + 1) * each) - first), stage);
+      __syncthreads();
+    }
+    return;
+  }
+  at -= movers;
+  if (at < lists * layers.count) {
+    const int h = static_cast<int>(at % c.Hkv), i = static_cast<int>(at / c.Hkv % c.n), layer = static_cast<int>(at / lists);
+    const Cut x = w.cut[i];
+    const long row = (static_cast<long>(x.row) * c.Hkv + h) * width;
+    move_weights(x, w.src + at * width, layers.weights[layer] + row, layers.out[layer] + row, width);
+    return;
+  }
+  at -= lists * layers.count;
+  if (!state_too || at >= s.num_rows) return;
+  const int row = static_cast<int>(at), i = w.entry[row];
+  const int32_t* old = s.table + static_cast<long>(row) * s.max_pages;
+  int32_t* now = c.out_table + static_cast<long>(row) * s.max_pages;
+  if (i < 0) {  // not listed
+    if (now != old)
+      for (int j = threadIdx.x; j < s.max_pages; j += kMove) now[j] = old[j];
+    if (threadIdx.x == 0 && c.out_lens != s.lens) c.out_lens[row] = s.lens[row];
+    return;
+  }
+  const Cut x = w.cut[i];
+  for (int j = threadIdx.x; j < s.max_pages; j += kMove)
+    now[j] = j < tiles_of(x.now) ? w.to[static_cast<long>(i) * s.max_pages + j] : -1;
+  if (threadIdx.x == 0) c.out_lens[row] = x.now;
+}
+
+}  // namespace
+
+size_t evict_workspace(int num_pages, int num_rows, int max_pages, int n, int Hkv, int num_layers, int per_layer) {
+  return space_of(nullptr, nullptr, num_pages, num_rows, max_pages, n, Hkv, layers_of_a_launch(num_layers, per_layer));
+}
+
+cudaError_t launch_pages_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
+  const int group = layers_of_a_launch(a.num_layers, a.per_layer);
+  Space w;
+  space_of(&w, ws, a.s.num_pages, a.s.num_rows, a.s.max_pages, a.n, a.Hkv, group);
+  Call c{a.s, a.rows, a.keep, a.n, a.recent, a.Hkv, a.out_refs, a.out_table, a.out_lens, a.result};
+  const int row_words = static_cast<int>(a.page_bytes / (static_cast<size_t>(a.Hkv) * kTile) / 16);
+  cudaError_t e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kPieceBytes);
+  for (int l0 = 0; e == cudaSuccess && l0 < a.num_layers; l0 += group) {
+    Layers layers{};
+    layers.count = a.num_layers - l0 < group ? a.num_layers - l0 : group;
+    PagePools pools{};
+    pools.page_bytes = a.page_bytes;
+    pools.count = layers.count * a.per_layer;
+    for (int l = 0; l < layers.count; ++l) {
+      layers.weights[l] = a.weights[l0 + l];
+      layers.out[l] = a.out_weights[l0 + l];
+    }
+    for (int q = 0; q < pools.count; ++q) pools.base[q] = static_cast<unsigned char*>(a.pools[l0 * a.per_layer + q]);
+    const bool last = l0 + group >= a.num_layers;
+    const long lists = static_cast<long>(a.n) * a.Hkv * layers.count, movers = static_cast<long>(a.n) * a.Hkv * pools.count;
+    choose_kernel<<<static_cast<unsigned>(lists + (l0 == 0)), kChoose, 0, st>>>(c, w, layers, l0 == 0);
+    if ((e = cudaGetLastError()) != cudaSuccess) break;
+    // few movers share their rows' columns, in pieces of 64 bytes at least
+    int slices = 1;
+    while (movers * slices < 4 * kSMs && row_words % (2 * slices) == 0 && row_words / (2 * slices) >= 4) slices *= 2;
+    const long blocks = movers * slices + lists + (last ? a.s.num_rows : 0);
+    move_kernel<<<static_cast<unsigned>(blocks), kMove, kStages * kPieceBytes, st>>>(c, w, layers, pools, a.per_layer,
+                                                                                     slices, last);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace ssattn

@@ -1,0 +1,704 @@
+// How much attention weight each cached key receives from a step's packed new
+// tokens: weights[b][kvh][key] += sum over the sequence's new tokens i and the
+// G query heads h of the group of softmax_h,i[key], without the attention's
+// output (a prompt, or its last window, choosing which of its keys to keep).
+//
+// Mathematics: the weight exp2(s - lse) needs the row's denominator first, so
+// there are two passes over the scores s = q.k * scale * log2e,
+//   rows:  lse = log2 sum over keys of exp2(s)   (running maximum and sum)
+//   keys:  w[key] += sum over rows of exp2(s - lse)
+// and no other product.  The scores are computed twice because keeping them
+// would take 4 bytes a score, written and read, against 2 d operations.
+//
+// Both passes are one kernel.  Its fixed operand is two tiles of 128 rows (A of
+// the MMAs), the other streams past it in tiles of 128 (B), and every thread
+// owns a row of a fixed tile, that is a TMEM lane, and reduces along its
+// columns, so no sum crosses threads.  The rows' pass fixes query rows and
+// streams keys; the keys' pass fixes keys and streams query rows, whose lse are
+// the columns' addends.  Rows of queries: 128 / G tokens x G heads (as in the
+// chunk attention).
+//
+// Work: an item is (sequence, KV head, fixed pair); all items' steps laid end
+// to end are cut into equal shares, one a CTA.  The steps of a causal pair are
+// floors of linear functions of its number, so their sums have a closed form
+// (floor_sum) and a CTA finds its share without walking a list.  An item that
+// is cut leaves its parts' results in the workspace, and a small kernel joins
+// them in order (results do not depend on timing).
+//
+// One CTA: two streams t, each with a fixed tile, two score buffers in TMEM and
+// a reducing warpgroup.  In the rows' pass a pair whose tokens fit one block has
+// both streams take alternate tiles of keys against that block instead.
+// Warps 0-3 / 4-7 reduce, 8 loads, 9 issues MMAs, 10 works out the pieces.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "key_weights.cuh"
+#include "ptx_sm103.cuh"
+
+namespace ssattn {
+
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10;
+constexpr int kPieces = 4;
+constexpr int kPair = 2 * kTile;
+constexpr int kLaunchRegs = 168, kRegsIssue = 88, kRegsSoftmax = 208;
+static_assert(128 * kRegsIssue + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kRing = (D == 128) ? 3 : 6;  // streamed tiles
+  static constexpr int kRingOff = 4 * kTileBytes;   // behind two pairs of fixed tiles
+  static constexpr int kCtlOff = kRingOff + kRing * kTileBytes;
+  static constexpr int kCtlBytes = 2048;
+  static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's steps on (a, m)).
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long x = m;
+    m = a;
+    a = x;
+  }
+  return sum;
+}
+
+// A sequence of the step.
+struct Seq {
+  int n, len, off;   // new tokens, keys, keys in front of the first new token (may be negative)
+  int tok0;          // first new token
+  int tiles, blocks; // of keys, of query rows
+  long place;        // of its first pair of row blocks
+};
+
+__device__ __forceinline__ Seq seq_of(const KeyWeightsParams& p, int b) {
+  Seq s;
+  s.tok0 = max(0, min(p.cu_seqlens[b], p.T));
+  s.n = max(0, min(p.cu_seqlens[b + 1], p.T) - s.tok0);
+  s.len = max(0, min(p.seq_lens[b], p.max_pages * kTile));
+  s.off = s.len - s.n;
+  s.tiles = (s.len + kTile - 1) / kTile;
+  s.blocks = (s.n + p.tpb - 1) / p.tpb;
+  s.place = s.tok0 / (2 * p.tpb) + b;
+  return s;
+}
+
+__device__ __forceinline__ long long ceil_div(long long a, long long b) {  // b > 0
+  return a >= 0 ? (a + b - 1) / b : -(-a / b);
+}
+
+// Fixed pairs of a KV head, the steps of pair i, and the steps of all pairs below i.
+template <bool ROWS>
+__device__ __forceinline__ int pairs_of(const Seq& s) {
+  return ROWS ? (s.blocks + 1) / 2 : (s.tiles + 1) / 2;
+}
+template <bool ROWS>
+__device__ __forceinline__ int first_step(const KeyWeightsParams& p, const Seq& s, int i) {
+  // keys: the first block of query rows that sees a key of the pair
+  if (ROWS || !p.causal) return 0;
+  const int x = i * kPair - s.off;  // the first token that does
+  return x <= 0 ? 0 : min(s.blocks, x / p.tpb);
+}
+template <bool ROWS>
+__device__ __forceinline__ int steps_of(const KeyWeightsParams& p, const Seq& s, int i) {
+  if (!ROWS) return s.blocks - first_step<ROWS>(p, s, i);
+  if (!p.causal) return s.tiles;
+  const long long last = static_cast<long long>(s.off) + 2ll * p.tpb * (i + 1) - 1;  // key that the pair's last token sees
+  return last < 0 ? 0 : static_cast<int>(min(static_cast<long long>(s.tiles), last / kTile + 1));
+}
+template <bool ROWS>
+__device__ long long steps_below(const KeyWeightsParams& p, const Seq& s, int i) {
+  if (!p.causal) return static_cast<long long>(i) * (ROWS ? s.tiles : s.blocks);
+  if (ROWS) {
+    // clamp(floor((off + w (q + 1) - 1) / 128) + 1, 0, tiles): zero below q0, tiles from q1 on
+    const long long w = 2 * p.tpb, c = static_cast<long long>(s.off) + w - 1;
+    const long long q0 = c >= 0 ? 0 : ceil_div(-c, w);
+    long long q1 = max(q0, ceil_div(static_cast<long long>(kTile) * (s.tiles - 1) - c, w));
+    q1 = max(q1, 0ll);
+    const long long top = min(static_cast<long long>(i), q1);
+    long long sum = 0;
+    if (top > q0) sum = floor_sum(top - q0, kTile, w, c + w * q0) + (top - q0);
+    if (i > q1) sum += (i - q1) * s.tiles;
+    return sum;
+  }
+  const long long k0 = s.off < 0 ? 0 : static_cast<long long>(s.off) / kPair + 1;  // first pair with a step less
+  long long sum = static_cast<long long>(i) * s.blocks;
+  if (i > k0) sum -= floor_sum(i - k0, p.tpb, kPair, k0 * kPair - s.off);
+  return sum;
+}
+
+// Two results (m in raw scores, l) of a row become one.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float sl2) {
+  const float top = fmaxf(m, m2);
+  // (l is 0 or NaN where m is -inf)
+  l = (m == -INFINITY ? l : l * ex2_approx((m - top) * sl2)) + (m2 == -INFINITY ? l2 : l2 * ex2_approx((m2 - top) * sl2));
+  m = top;
+}
+// log2 of the denominator; a row without keys gives infinity, and so weights of 0.
+__device__ __forceinline__ float row_lse(float m, float l, float sl2) {
+  return l == 0.f ? INFINITY : m == -INFINITY ? l : fmaf(m, sl2, log2f(l));
+}
+
+// A run of steps of one item.
+struct Piece {
+  int n, u0, steps;  // steps; the first of them, all of the item's (n = 0: no more pieces)
+  int b, kvh, pair;
+  int tok0, toks;    // sequence's first token, tokens
+  int len, off;
+  int first;         // streamed tile of step 0 of the item
+  int both;          // two fixed tiles; else both streams use the first and alternate
+  long place;
+};
+
+struct Ctl {
+  uint64_t r_full[6], r_empty[6];
+  uint64_t f_full[2], f_empty[2];
+  uint64_t s_full[4], s_empty[4];  // [stream * 2 + buffer]
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  uint64_t hand_full, hand_empty;
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int r_issued, f_issued;
+  int b;              // this CTA's share begins in sequence b,
+  long long at;       // whose first step is number `at` of all
+  long long total;
+  long long scan[kThreads / 32];
+  Piece piece[kPieces];
+  float2 hand[kTile];  // rows' pass, alternate tiles: stream 1's results
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+template <int D, bool ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const KeyWeightsParams p) {
+  using C = Cfg<D>;
+  constexpr int NR = C::kRing;
+  static_assert(sizeof(Ctl) <= C::kCtlBytes, "control block overflow");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sF = smem;
+  uint8_t* sR = smem + C::kRingOff;
+  auto* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
+  volatile int* abort_flag = &ctl->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&ctl->r_full[s], 1);
+      mbar_init(&ctl->r_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->f_full[s], 1);
+      mbar_init(&ctl->f_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&ctl->s_full[s], 1);
+      mbar_init(&ctl->s_empty[s], 4);
+    }
+    for (int s = 0; s < kPieces; ++s) {
+      mbar_init(&ctl->piece_full[s], 1);
+      mbar_init(&ctl->piece_empty[s], 10);
+    }
+    mbar_init(&ctl->hand_full, 4);
+    mbar_init(&ctl->hand_empty, 4);
+    mbar_init(&ctl->mma_done, 1);
+    ctl->abort_flag = 0;
+    ctl->r_issued = ctl->f_issued = 0;
+    ctl->b = -1;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  {  // every sequence's steps, added up
+    const int each = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    auto cost = [&](int b) {
+      const Seq s = seq_of(p, b);
+      return steps_below<ROWS>(p, s, pairs_of<ROWS>(s)) * p.Hkv;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += cost(b);
+    long long at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += x;
+    }
+    if (lane == 31) ctl->scan[warp] = at;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += ctl->scan[w];
+      total += ctl->scan[w];
+    }
+    at -= mine;
+    const long long per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x;
+    if (begin >= at && begin < at + mine)
+      for (int b = b0; b < b1; ++b) {
+        const long long c = cost(b);
+        if (begin >= at && begin < at + c) {
+          ctl->b = b;
+          ctl->at = at;
+        }
+        at += c;
+      }
+    if (tid == 0) ctl->total = total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int q_rows = p.tpb * p.G;                    // rows of a block of queries
+  const uint32_t q_bytes = C::kChunks * q_rows * 128;
+
+  auto piece_at = [&](int k, Piece* out) -> bool {
+    if (!mbar_wait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) return false;
+    *out = ctl->piece[k % kPieces];
+    return true;
+  };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp == kWarpLoad) {
+      // ---------------------------------------------------------- loader
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+      }
+      int e = 0;
+      bool ok = true;
+      auto load_queries = [&](uint8_t* to, uint64_t* bar, const Piece& x, int block) {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_4d(to + c * 16384, &tmQ, bar, c * 64, 0, x.kvh, x.tok0 + block * p.tpb);
+      };
+      auto load_keys = [&](uint8_t* to, uint64_t* bar, const Piece& x, int page) {
+        const int z = page >= 0 && page < p.num_pages ? page * p.Hkv + x.kvh : p.num_pages * p.Hkv;
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) tma_load_3d(to + c * 16384, &tmK, bar, c * 64, 0, z);
+      };
+      for (int k = 0; ok; ++k) {
+        Piece x;
+        ok = __all_sync(0xffffffffu, piece_at(k, &x));
+        if (!ok || x.n == 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
+        const int32_t* pages = p.page_table + static_cast<long>(x.b) * p.max_pages;
+        const int fb = k & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->f_empty[fb], ((k >> 1) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* to = sF + fb * 2 * C::kTileBytes;
+          mbar_arrive_expect_tx(&ctl->f_full[fb], (x.both ? 2 : 1) * (ROWS ? q_bytes : C::kTileBytes));
+          for (int t = 0; t < (x.both ? 2 : 1); ++t) {
+            if (ROWS)
+              load_queries(to + t * C::kTileBytes, &ctl->f_full[fb], x, 2 * x.pair + t);
+            else
+              load_keys(to + t * C::kTileBytes, &ctl->f_full[fb], x, pages[2 * x.pair + t]);
+          }
+          *reinterpret_cast<volatile int*>(&ctl->f_issued) = k + 1;
+        }
+        int held = 0;
+        for (int i = 0; ok && i < x.n; ++i, ++e) {
+          const int u = x.first + x.u0 + i;
+          int page = 0;
+          if (ROWS) {
+            if ((i & 31) == 0) held = i + lane < x.n ? pages[u + lane] : 0;
+            page = __shfl_sync(0xffffffffu, held, i & 31);
+          }
+          const int st = e % NR;
+          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->r_empty[st], ((e / NR) & 1) ^ 1, abort_flag));
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&ctl->r_full[st], ROWS ? C::kTileBytes : q_bytes);
+            if (ROWS)
+              load_keys(sR + st * C::kTileBytes, &ctl->r_full[st], x, page);
+            else
+              load_queries(sR + st * C::kTileBytes, &ctl->r_full[st], x, u);
+            *reinterpret_cast<volatile int*>(&ctl->r_issued) = e + 1;
+          }
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t sFa = smem_u32(sF), sRa = smem_u32(sR);
+        uint32_t slot = 0, par = 0, sn[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          Piece x;
+          ok = piece_at(k, &x);
+          if (!ok || x.n == 0) break;
+          mbar_arrive(&ctl->piece_empty[k % kPieces]);
+          ok = mbar_wait(&ctl->f_full[k & 1], (k >> 1) & 1, abort_flag);
+          const uint32_t fa = sFa + (k & 1) * 2 * C::kTileBytes;
+          for (int i = 0; ok && i < x.n; ++i) {
+            ok = mbar_wait(&ctl->r_full[slot], par, abort_flag);
+            if (!ok) break;
+            const uint64_t dr = smem_desc(sRa + slot * C::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!x.both && (i & 1) != t) continue;
+              const uint32_t buf = 2 * t + (sn[t] & 1);
+              ok = ok && mbar_wait(&ctl->s_empty[buf], ((sn[t] >> 1) & 1) ^ 1, abort_flag);
+              if (!ok) break;
+              ++sn[t];
+              tc_fence_after();
+              const uint64_t df = smem_desc(fa + (x.both ? t * C::kTileBytes : 0), 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                mma_bf16_ss(tmem + 128 * buf, df + off, dr + off, idS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&ctl->s_full[buf]);
+            }
+            if (!ok) break;
+            mma_commit(&ctl->r_empty[slot]);
+            if (++slot == NR) slot = 0, par ^= 1;
+          }
+          if (ok) mma_commit(&ctl->f_empty[k & 1]);
+        }
+        mma_commit(&ctl->mma_done);
+        mbar_wait(&ctl->mma_done, 0, nullptr);
+      }
+      __syncwarp();
+    } else if (warp == kWarpPlan) {
+      // ---------------------------------------------------------- pieces
+      if (lane == 0) {
+        const long long per = (ctl->total + gridDim.x - 1) / gridDim.x;
+        long long at = per * blockIdx.x;
+        const long long end = min(at + per, ctl->total);
+        int b = ctl->b, kvh = 0, pair = 0;
+        long long u = 0;  // step of the item that comes next
+        Seq s{};
+        int pairs = 0;
+        if (b >= 0) {  // the item that the share begins in
+          s = seq_of(p, b);
+          pairs = pairs_of<ROWS>(s);
+          const long long head = steps_below<ROWS>(p, s, pairs);
+          long long in = at - ctl->at;
+          kvh = static_cast<int>(in / head);
+          in -= kvh * head;
+          int lo = 0, hi = pairs;  // the last pair with steps_below <= in
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (steps_below<ROWS>(p, s, mid) <= in) lo = mid; else hi = mid;
+          }
+          pair = lo;
+          u = in - steps_below<ROWS>(p, s, lo);
+        }
+        Split split{};
+        for (int k = 0;; ++k) {
+          Piece x{};
+          if (b >= 0 && at < end) {
+            int steps = steps_of<ROWS>(p, s, pair);
+            while (u >= steps) {  // on to the next item that has steps
+              u = 0;
+              if (++pair >= pairs) {
+                pair = 0;
+                if (++kvh == p.Hkv) {
+                  kvh = 0;
+                  do {  // (there are steps left, so a sequence is)
+                    b = min(b + 1, p.B - 1);
+                    s = seq_of(p, b);
+                    pairs = pairs_of<ROWS>(s);
+                  } while (b < p.B - 1 && (s.tiles == 0 || s.blocks == 0));
+                }
+              }
+              steps = steps_of<ROWS>(p, s, pair);
+            }
+            x.n = static_cast<int>(min(static_cast<long long>(steps - u), end - at));
+            x.u0 = static_cast<int>(u);
+            x.steps = steps;
+            x.b = b;
+            x.kvh = kvh;
+            x.pair = pair;
+            x.tok0 = s.tok0;
+            x.toks = s.n;
+            x.len = s.len;
+            x.off = s.off;
+            x.first = first_step<ROWS>(p, s, pair);
+            x.both = ROWS ? 2 * pair + 1 < s.blocks : 2 * pair + 1 < s.tiles;
+            x.place = s.place;
+            if (x.u0 == 0 && x.n < steps) split = Split{1, b, kvh, pair, steps - x.n, static_cast<int>(min(per, 0x7fffffffll))};
+            at += x.n;
+            u += x.n;
+          }
+          if (!mbar_wait(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
+          ctl->piece[k % kPieces] = x;
+          mbar_arrive(&ctl->piece_full[k % kPieces]);
+          if (x.n == 0) break;
+        }
+        p.split[blockIdx.x] = split;
+      }
+      __syncwarp();
+    }
+    if (warp == kWarpLoad && lane == 0 && *abort_flag) {
+      // let the copies in flight land before shared memory is released
+      const int n = *reinterpret_cast<volatile int*>(&ctl->r_issued);
+      const int f = *reinterpret_cast<volatile int*>(&ctl->f_issued);
+      for (int q = 0; q < NR; ++q)
+        if (n > q) mbar_wait(&ctl->r_full[q], ((n - 1 - q) / NR) & 1, nullptr);
+      for (int q = 0; q < 2; ++q)
+        if (f > q) mbar_wait(&ctl->f_full[q], ((f - 1 - q) / 2) & 1, nullptr);
+    }
+    __syncwarp();
+    tc_fence_before();
+    barrier_sync(1, kThreads);
+    if (warp == kWarpMma) {
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  } else {
+    // ---------------------------------------------------------- reduction of stream t
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int t = warp >> 2, row = tid & 127;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * t;
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = f32x2(sl2, sl2);
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    };
+    uint32_t sn = 0, hn = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Piece x;
+      ok = __all_sync(0xffffffffu, piece_at(k, &x));
+      if (!ok || x.n == 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
+      const bool alone = !x.both;
+      // (keys: a pair of one tile has the second stream take alternate blocks of rows as well)
+      const int ft = alone ? 0 : t;                       // this stream's fixed tile
+      float m = -INFINITY, m_used = -INFINITY, l = 0.f;   // rows
+      float sum[2] = {0.f, 0.f};                          // keys
+      // rows: this thread's token and the last key that it sees; keys: this thread's key
+      const int token = (2 * x.pair + ft) * p.tpb + row / p.G;
+      const bool row_live = ROWS && row < q_rows && token < x.toks;
+      const int lim = !row_live ? -1 : p.causal ? min(x.len - 1, x.off + token) : x.len - 1;
+      const int key = (2 * x.pair + ft) * kTile + row;
+      const float* lse_of = p.lse + (static_cast<long>(x.kvh) * p.places + x.place) * kPair;
+      for (int i = alone ? t : 0; i < x.n; i += alone ? 2 : 1) {
+        const uint32_t buf = sn & 1;
+        if (!wwait(&ctl->s_full[2 * t + buf], (sn >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        ++sn;
+        tc_fence_after();
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32p(lane_base + 128 * buf + 32 * c, sr + 32 * c);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->s_empty[2 * t + buf]);
+        const int u = x.first + x.u0 + i;
+        if (ROWS) {
+          const int vis = min(kTile - 1, lim - u * kTile);  // last visible column
+          if (vis < kTile - 1) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > vis) sr[e] = __float_as_uint(-INFINITY);
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+          m = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (m > m_used) {
+            if (m_used != -INFINITY) l *= ex2_approx((m_used - m) * sl2);
+            m_used = m;
+          }
+          const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
+          const uint64_t nmb = f32x2(-mb, -mb);
+          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const uint64_t xp =
+                fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
+            ls[c & 3] = add_f32x2(ls[c & 3], f32x2(ex2_approx(f32x2_lo(xp)), ex2_approx(f32x2_hi(xp))));
+          }
+          const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
+          l += f32x2_lo(s2) + f32x2_hi(s2);
+        } else {
+          // columns: rows of block u of the queries; those that see the key are [lo, hi)
+          const int i0 = u * p.tpb;
+          const int hi = min(q_rows, (x.toks - i0) * p.G);
+          const int lo = p.causal ? static_cast<int>(max(0ll, min(static_cast<long long>(kTile), (static_cast<long long>(key) - x.off - i0) * p.G))) : 0;
+          const bool some = __any_sync(0xffffffffu, hi < kTile || lo > 0);
+          const float4* lse4 = reinterpret_cast<const float4*>(lse_of + static_cast<long>(u) * kTile);
+          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float4 a = __ldg(lse4 + c);
+            const uint64_t x0 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), sl2x2,
+                                          f32x2(-a.x, -a.y));
+            const uint64_t x1 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])),
+                                          sl2x2, f32x2(-a.z, -a.w));
+            float w[4] = {ex2_approx(f32x2_lo(x0)), ex2_approx(f32x2_hi(x0)), ex2_approx(f32x2_lo(x1)),
+                          ex2_approx(f32x2_hi(x1))};
+            if (some) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (4 * c + e < lo || 4 * c + e >= hi) w[e] = 0.f;
+            }
+            ls[c & 1] = add_f32x2(ls[c & 1], f32x2(w[0], w[1]));
+            ls[2 + (c & 1)] = add_f32x2(ls[2 + (c & 1)], f32x2(w[2], w[3]));
+          }
+          const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
+          sum[0] += f32x2_lo(s2);
+          sum[1] += f32x2_hi(s2);
+        }
+      }
+      if (!ok) break;
+      // The item's result, or a part of it.
+      float total = sum[0] + sum[1];
+      if (alone) {  // the other stream's share of the same rows
+        if (t == 1) {
+          if (!(ok = wwait(&ctl->hand_empty, (hn & 1) ^ 1))) break;
+          ctl->hand[row] = ROWS ? make_float2(m_used, l) : make_float2(total, 0.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->hand_full);
+        } else {
+          if (!(ok = wwait(&ctl->hand_full, hn & 1))) break;
+          const float2 other = ctl->hand[row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->hand_empty);
+          if (ROWS)
+            join(m_used, l, other.x, other.y, sl2);
+          else
+            total += other.x;
+        }
+        ++hn;
+        if (t == 1) continue;
+      }
+      const bool whole = x.n == x.steps;
+      const long part = (2l * blockIdx.x + (x.u0 == 0 ? 1 : 0)) * kPair + ft * kTile + row;
+      if (ROWS) {
+        if (row_live) {
+          if (whole)
+            p.lse[(static_cast<long>(x.kvh) * p.places + x.place + x.pair) * kPair + ft * kTile + row] =
+                row_lse(m_used, l, sl2);
+          else
+            p.part_ml[part] = make_float2(m_used, l);
+        }
+      } else if (key < x.len) {
+        if (whole)
+          p.weights[(static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key] += total;
+        else
+          p.part_w[part] = total;
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    barrier_sync(1, kThreads);
+    if (tid == 0 && *abort_flag) report_timeout(p.status);
+  }
+}
+
+// Block c: the item that CTA c began and others went on with.
+template <bool ROWS>
+__global__ void __launch_bounds__(kPair) join_kernel(const KeyWeightsParams p) {
+  const Split x = p.split[blockIdx.x];
+  if (!x.valid) return;
+  const Seq s = seq_of(p, x.b);
+  const int t = threadIdx.x >> 7, row = threadIdx.x & 127;
+  long at = (2l * blockIdx.x + 1) * kPair + threadIdx.x;
+  if (ROWS) {
+    if (row >= p.tpb * p.G || (2 * x.pair + t) * p.tpb + row / p.G >= s.n) return;
+    float m = p.part_ml[at].x, l = p.part_ml[at].y;
+    int c = blockIdx.x + 1;
+    for (int left = x.left; left > 0 && c < p.ctas; left -= x.per, ++c) {
+      const float2 o = p.part_ml[2l * c * kPair + threadIdx.x];
+      join(m, l, o.x, o.y, p.scale_log2);
+    }
+    p.lse[(static_cast<long>(x.kvh) * p.places + s.place + x.pair) * kPair + threadIdx.x] = row_lse(m, l, p.scale_log2);
+  } else {
+    const int key = 2 * x.pair * kTile + threadIdx.x;
+    if (key >= s.len) return;
+    float sum = p.part_w[at];
+    int c = blockIdx.x + 1;
+    for (int left = x.left; left > 0 && c < p.ctas; left -= x.per, ++c) sum += p.part_w[2l * c * kPair + threadIdx.x];
+    p.weights[(static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key] += sum;
+  }
+}
+
+template <int D, bool ROWS>
+cudaError_t launch_pass(const CUtensorMap& tq, const CUtensorMap& tk, const KeyWeightsParams& p, cudaStream_t st) {
+  auto* fn = key_weights_kernel<D, ROWS>;
+  static const int launch_regs = [fn] {
+    cudaFuncAttributes attr{};
+    return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : -1;
+  }();
+  if (launch_regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  fn<<<p.ctas, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  join_kernel<ROWS><<<p.ctas, kPair, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+
+KeyWeightsSpace key_weights_space(int T, int B, int Hq, int Hkv) {
+  KeyWeightsSpace s{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += up16(n);
+    return here;
+  };
+  s.lse = take(static_cast<size_t>(Hkv) * key_weights_places(T, B, kTile / (Hq / Hkv)) * kPair * sizeof(float));
+  s.part_ml = take(2 * kSMs * kPair * sizeof(float2));
+  s.part_w = take(2 * kSMs * kPair * sizeof(float));
+  s.split = take(kSMs * sizeof(Split));
+  s.bytes = at;
+  return s;
+}
+
+cudaError_t launch_key_weights(int d, const CUtensorMap& tq, const CUtensorMap& tk, const KeyWeightsParams& p0,
+                               cudaStream_t st) {
+  KeyWeightsParams p = p0;
+  p.ctas = kSMs;
+  cudaError_t e = d == 128 ? launch_pass<128, true>(tq, tk, p, st) : launch_pass<64, true>(tq, tk, p, st);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? launch_pass<128, false>(tq, tk, p, st) : launch_pass<64, false>(tq, tk, p, st);
+}
+
+}  // namespace ssattn

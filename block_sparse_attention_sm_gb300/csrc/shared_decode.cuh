@@ -1,0 +1,61 @@
+// Declarations of the decode over shared pages, shared with the C-ABI layer.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace ssattn {
+
+// A plan of shared pages, int32 words.  The sequences in the order of their
+// tables' pages ([kPlanHead, kPlanHead + B)), then 2 B nodes of kNodeWords:
+// node i < B is what the sequence at place i has to itself, node B + i the
+// pages shared by a run of places (empty: not used).
+constexpr int kPlanHead = 8;    // words: B, max_pages, a mark
+constexpr int kPlanMark = 0x504c414e;
+constexpr int kNodeWords = 5;   // first place, places, first tile, end tile, parent node (-1: none)
+constexpr int kPlanLevels = 7;  // shared nodes above a sequence at most (bounds the partial results)
+constexpr int kPlanMaxB = 8192;
+
+__host__ __device__ constexpr size_t plan_words(long B) { return kPlanHead + B + 2 * B * kNodeWords; }
+
+cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
+                               int32_t* plan, cudaStream_t st);
+
+struct SharedParams {
+  int B, Hq, Hkv, G;
+  int num_pages, max_pages;
+  int ctas;                // CTAs of the attention kernel
+  float scale_log2;
+  const __nv_bfloat16* q;  // [B][Hq][d], rows of heads q_stride apart
+  long q_stride;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* plan;     // nullable
+  __nv_bfloat16* o;        // [B][Hq][d]
+  float* part_o;           // [part_rows][d] unnormalised partial outputs
+  float2* part_ml;         // [part_rows] (reference maximum in exp2 units, sum)
+  long part_rows;
+  long long* node_at;      // [2 B] first tile of a node among all the launch's
+  long long* node_rows;    // [2 B] its first partial row
+  float* lse;              // [B][Hq] log2 of the softmax's denominator (weights only)
+  float* scores;           // [B][Hq][max_pages][128] (weights only)
+  float* weights;          // [B][Hkv][max_pages * 128], nullable
+  uint32_t* status;
+};
+
+// Workspace: sizes and where its arrays lie.
+struct SharedSpace {
+  size_t part_o, part_ml, node_at, node_rows, lse, scores, bytes;
+  long part_rows;
+};
+SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan, bool weights);
+int shared_ctas(int B, int Hq, int Hkv, int max_pages);
+
+cudaError_t launch_shared_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const SharedParams& p, cudaStream_t st);
+
+}  // namespace ssattn

@@ -587,6 +587,112 @@ ss_status ss_pages_compact(void* const* pools, int num_pools, size_t page_bytes,
                            const int32_t* seq_lens, int32_t* out_refs, int32_t* out_table, int32_t* live,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Eviction by accumulated attention weight: sequence rows[i] (rows NULL: row
+ * i), i < n, is cut back to keep[i] >= 0 keys.  Every KV head of every layer
+ * keeps the min(recent, keep) newest keys and, of the older ones, those of
+ * largest weight (equal ones: the lowest index first; -0 is 0, NaN below every
+ * number), in their order, as its keys 0, 1, ..; their rows move to the front of
+ * the sequence's pages in every pool of the layer.  A sequence of keep[i] keys
+ * or fewer stays as it is.
+ *   pools: host array of num_pools device addresses, num_pools / num_layers
+ *     (1 .. 64) a layer, layer by layer (its key and value pages, or one pool of
+ *     latent rows), each num_pages pages [Hkv][128][row], page_bytes a multiple of
+ *     2048 Hkv; no pool twice.  They are changed in place.
+ *   weights: host array of num_layers device addresses (16-byte aligned), each
+ *     fp32 [num_rows][Hkv][max_pages * 128], as ss_attn_decode_shared and
+ *     ss_attn_key_weights add them up.  out_weights (nullable: in place): the
+ *     listed rows receive the kept keys' weights, 0 behind them (in place, a
+ *     sequence that stays as it is keeps its cells).
+ *   out_refs, out_table, out_lens (nullable: in place): the new state, of all
+ *     rows; a listed row's table entries past its last page become -1.
+ * Pages behind the kept keys lose a holder.  A kept page that other sequences
+ * hold too is not written: the lowest free page (in the order of i) takes its
+ * place.  Refused (result) where free pages are missing, or with -1 for a row
+ * outside the table or listed twice, a negative keep, a length outside
+ * [0, 128 * max_pages].  The keys keep the rotary positions that they were
+ * written with: later tokens are given positions of their own
+ * (ss_rope_append_paged's `positions`), no longer their places.  workspace: at
+ * least ss_pages_evict_workspace_size(...) bytes, 16-byte aligned.  Returns as the other page calls.
+ */
+size_t ss_pages_evict_workspace_size(int num_pages, int num_rows, int max_pages, int n, int Hkv, int num_layers,
+                                     int num_pools);
+ss_status ss_pages_evict(void* const* pools, int num_pools, size_t page_bytes, float* const* weights, int num_layers,
+                         int Hkv, int32_t* page_refs, int num_pages, int32_t* page_table, int num_rows, int max_pages,
+                         int32_t* seq_lens, const int32_t* rows, const int32_t* keep, int n, int recent,
+                         float* const* out_weights, int32_t* out_refs, int32_t* out_table, int32_t* out_lens,
+                         int32_t* result, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * What the sequences of a batch share.  Two sequences share the tiles up to
+ * which their table rows name the same pages and that are full in both (as
+ * after ss_pages_fork); the plan is the tree of these runs, on up to 7 levels
+ * (what is shared deeper is read by each sequence).
+ *   page_table: device int32 [B][max_pages]; seq_lens: device int32 [B];
+ *   plan: device int32, ss_prefix_plan_size(B) bytes (0: B not in 1 .. 8192).
+ * It holds the order of the sequences and ranges of tiles, no lengths: it is
+ * good as long as the shared pages stay in their places, over steps in which
+ * sequences grow, but not over a fork, free, eviction or compaction (shared
+ * tiles would be read for rows that no longer have them; memory beyond the given
+ * arrays is not touched whatever a plan holds).  Asynchronous; SS_OK,
+ * SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE (plan too small) or SS_ERR_CUDA.
+ */
+size_t ss_prefix_plan_size(int B);
+ss_status ss_prefix_plan(const int32_t* page_table, const int32_t* seq_lens, int B, int max_pages, int32_t* plan,
+                         size_t plan_bytes, void* stream);
+
+/*
+ * Decode over shared pages: attention of one new token a sequence over all its
+ * L_b keys (no skip test), with the pages that the plan finds shared read once
+ * for all their sequences.
+ *   q: bf16 [B][Hq][d], 16-byte aligned; q_token_stride: elements between
+ *     sequences (0: Hq * d; a multiple of 8).  o: bf16 [B][Hq][d] contiguous.
+ *   k_pages, v_pages, page_table, seq_lens: as in ss_attn_decode_paged (what a
+ *     page holds behind its sequence's end is not read; a sequence without keys
+ *     gives zeros; an entry that names no page reads zeros).
+ *   plan: what ss_prefix_plan made for this table and B; NULL, or a plan of
+ *     other sizes: every sequence reads its own pages.
+ *   weights: nullable fp32 [B][Hkv][max_pages * 128], 16-byte aligned: cell k of
+ *     (sequence, KV head) gains key k's softmax weight, summed over the group's
+ *     query heads; cells from L_b on are left as they are.
+ *   workspace: at least ss_attn_decode_shared_workspace_size(...) bytes, 16-byte
+ *     aligned (never 0; it does not shrink as B or max_pages grow: one of the
+ *     largest sizes serves all).
+ * G = Hq / Hkv <= 128, d in {64, 128}, B and Hkv <= 65535 (with a plan B <= 8192).
+ * Nothing that is written (o, weights, workspace) may overlap another argument.
+ * Partial results are joined in fp32 in a fixed order: the same from run to run.
+ * Returns SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
+ */
+size_t ss_attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages, int d, int with_plan,
+                                            int with_weights);
+ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const void* k_pages, const void* v_pages,
+                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* plan, void* o,
+                                float* weights, int B, int Hq, int Hkv, int num_pages, int max_pages, int d,
+                                float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The attention weight that each cached key receives from a step's packed new
+ * tokens, without the attention's output: cell k of (sequence b, KV head h) of
+ * `weights` gains the sum, over the sequence's n_b new tokens i and the G query
+ * heads of h, of the softmax weight of key k.  Causal: token i sees the keys up to
+ * L_b - n_b + i (a row that sees none adds nothing), otherwise all L_b.  A
+ * prompt's last tokens alone are a step of that many new tokens.
+ *   q, q_token_stride, k_pages, page_table, cu_seqlens, seq_lens: as in
+ *     ss_attn_chunk_paged (what a page holds behind its sequence's end, and rows
+ *     behind the last sequence, may be anything).
+ *   weights: fp32 [B][Hkv][max_pages * 128], 16-byte aligned, not overlapping
+ *     another argument; cells from L_b on are left as they are.
+ *   workspace: at least ss_attn_key_weights_workspace_size(...) bytes, 16-byte
+ *     aligned (more tokens or sequences never need less).
+ * G <= 128, d in {64, 128}.  Returns SS_OK (also for T = 0), SS_ERR_INVALID_ARG,
+ * SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
+ */
+size_t ss_attn_key_weights_workspace_size(int T, int B, int Hq, int Hkv);
+ss_status ss_attn_key_weights(const void* q, int64_t q_token_stride, const void* k_pages, const int32_t* page_table,
+                              const int32_t* cu_seqlens, const int32_t* seq_lens, float* weights, int T, int B, int Hq,
+                              int Hkv, int num_pages, int max_pages, int d, float scale, int causal, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* A calibration problem: the inputs the threshold is fitted on. */
 typedef enum { SS_PREFILL = 0, SS_DECODE = 1, SS_MLA_DECODE = 2, SS_MLA_PREFILL = 3 } ss_kind;
 typedef struct {
