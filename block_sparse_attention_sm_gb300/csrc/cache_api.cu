@@ -737,7 +737,8 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL ||
       static_cast<long>(B) * Hq > 0x3fffffffL || stride >= (1LL << 38))
     return SS_ERR_INVALID_ARG;
-  if (B > 65535 || Hkv > 65535 || (plan != nullptr && B > kPlanMaxB)) return SS_ERR_UNSUPPORTED;
+  if (B > (plan != nullptr ? kPlanMaxB : kSharedMaxB) || Hkv > 65535 || static_cast<long>(B) * max_pages > 0x7fffffffL)
+    return SS_ERR_UNSUPPORTED;
   if (static_cast<__int128>(B) * Hq * max_pages > kMaxCells) return SS_ERR_INVALID_ARG;
   const SharedSpace space = shared_space(B, Hq, Hkv, max_pages, d, plan != nullptr, weights != nullptr);
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < space.bytes) return SS_ERR_WORKSPACE;
@@ -756,12 +757,13 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   CUtensorMap tk, tv;
   const long blocks = static_cast<long>(num_pages) * Hkv;
   if (!make_map(&tk, k_pages, d, kTile, blocks) || !make_map(&tv, v_pages, d, kTile, blocks)) return SS_ERR_CUDA;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 127) & ~static_cast<uintptr_t>(127));
   SharedParams p{};
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
+  p.inv_g = p.G > 1 ? static_cast<uint32_t>((1ull << 32) / p.G) + 1 : 0;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.ctas = shared_ctas(B, Hq, Hkv, max_pages);
@@ -775,6 +777,8 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   p.part_o = reinterpret_cast<float*>(ws + space.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);
   p.part_rows = space.part_rows;
+  p.total = reinterpret_cast<long long*>(ws + space.total);
+  p.cum = reinterpret_cast<int*>(ws + space.cum);
   p.node_at = reinterpret_cast<long long*>(ws + space.node_at);
   p.node_rows = reinterpret_cast<long long*>(ws + space.node_rows);
   if (weights != nullptr) {

@@ -7,12 +7,12 @@
 // run of places between smaller values of c is a node of the tree: it holds the
 // tiles from the larger of the two bounding values to its own.
 //
-// Two launches.  rank_kernel: block i compares row i with every other (a warp
-// a pair, 32 pages a step; rows that differ in their first page, the usual
-// case, end there): its place is the number of smaller rows, c its longest
-// common stretch with one of them (the nearest smaller row has it).  tree_kernel:
-// one thread a place looks left and right in shared memory for the run's ends.
-// 64 rows of 256 pages that share 200: 6 us; most of it is latency.
+// Two launches.  rank_kernel: block i compares row i with every other, a warp a
+// pair, 512 pages a step (rows that differ in their first page, the usual case,
+// are sorted out before, a lane each): its place is the number of smaller rows, c
+// its longest common stretch with one of them (the nearest smaller row has it).
+// tree_kernel: a warp a place looks left and right for the run's ends, 32 places a
+// step, in shared memory.  Latency bounds both.
 #include "shared_decode.cuh"
 
 namespace ssattn {
@@ -25,17 +25,27 @@ __device__ __forceinline__ int full_pages(int len, int max_pages) {
   return min(max(len, 0) / kTile, max_pages);
 }
 
-// (tiles that rows a and b share, whether b is the smaller); a whole warp.
+// Tiles that rows a and b share, of n; *diff: how b compares with a behind them.  A whole warp.
 __device__ __forceinline__ int common_pages(const int32_t* a, const int32_t* b, int n, int* diff) {
+  constexpr int U = 16;  // words of each row that a lane has in flight
   const int lane = threadIdx.x & 31;
-  for (int j = 0; j < n; j += 32) {
-    const int x = j + lane < n ? a[j + lane] : 0, y = j + lane < n ? b[j + lane] : 0;
-    // (an entry that names no page is shared with nobody)
-    const uint32_t m = __ballot_sync(0xffffffffu, j + lane < n && (x != y || x < 0));
-    if (m != 0) {
-      const int at = __ffs(m) - 1;
-      *diff = __shfl_sync(0xffffffffu, y < x ? -1 : y > x ? 1 : 0, at);
-      return j + at;
+  for (int j0 = 0; j0 < n; j0 += 32 * U) {
+    int x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + 32 * u + lane;
+      x[u] = j < n ? a[j] : 0;
+      y[u] = j < n ? b[j] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (an entry that names no page is shared with nobody)
+      const uint32_t m = __ballot_sync(0xffffffffu, j0 + 32 * u + lane < n && (x[u] != y[u] || x[u] < 0));
+      if (m != 0) {
+        const int at = __ffs(m) - 1;
+        *diff = __shfl_sync(0xffffffffu, y[u] < x[u] ? -1 : y[u] > x[u] ? 1 : 0, at);
+        return j0 + 32 * u + at;
+      }
     }
   }
   *diff = 0;
@@ -44,42 +54,45 @@ __device__ __forceinline__ int common_pages(const int32_t* a, const int32_t* b, 
 
 __global__ void __launch_bounds__(kRank)
     rank_kernel(const int32_t* table, const int32_t* lens, int B, int max_pages, int32_t* plan) {
-  __shared__ int smaller, longest;
+  __shared__ int smaller, longest, n_open;
+  __shared__ int open[kRank], open_n[kRank];  // rows that begin as row i does, and their full pages
   const int i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) smaller = longest = 0;
-  __syncthreads();
   const int32_t* mine = table + static_cast<long>(i) * max_pages;
   const int n_mine = full_pages(lens[i], max_pages);
   const int first = n_mine > 0 ? mine[0] : -1;
   int count = 0, most = 0;
-  for (int j0 = warp * 32; j0 < B; j0 += kRank) {  // 32 rows: by their first page, a lane each
-    const int j = j0 + lane;
-    int n = 0, other = -1;
+  for (int j0 = 0; j0 < B; j0 += kRank) {
+    __syncthreads();
+    if (threadIdx.x == 0) n_open = 0;
+    __syncthreads();
+    const int j = j0 + threadIdx.x;
     if (j < B && j != i) {
-      n = min(n_mine, full_pages(lens[j], max_pages));
-      if (n > 0) other = table[static_cast<long>(j) * max_pages];
+      const int nj = full_pages(lens[j], max_pages), n = min(n_mine, nj);
+      const int other = n > 0 ? table[static_cast<long>(j) * max_pages] : -1;
+      if (n > 0 && other == first && first >= 0) {
+        const int at = atomicAdd(&n_open, 1);
+        open[at] = j;
+        open_n[at] = nj;
+      } else if (n > 0) {
+        count += other != first ? other < first : j < i;  // (both name no page: by number)
+      } else {
+        count += nj != n_mine ? nj < n_mine : j < i;
+      }
     }
-    const bool open = j < B && j != i && n > 0 && other == first && first >= 0;
-    bool less = false;
-    if (j < B && j != i && !open) {
-      const int nj = full_pages(lens[j], max_pages);
-      if (n > 0 && other != first) less = other < first;
-      else if (n > 0) less = j < i;  // (both name no page)
-      else less = nj != n_mine ? nj < n_mine : j < i;
-    }
-    count += __popc(__ballot_sync(0xffffffffu, less));
-    for (uint32_t m = __ballot_sync(0xffffffffu, open); m != 0; m &= m - 1) {
-      const int at = __ffs(m) - 1, jj = j0 + at, nn = __shfl_sync(0xffffffffu, n, at);
+    __syncthreads();
+    for (int q = warp; q < n_open; q += kRank / 32) {
+      const int jj = open[q], nj = open_n[q], n = min(n_mine, nj);
       int diff;
-      const int c = common_pages(mine, table + static_cast<long>(jj) * max_pages, nn, &diff);
-      const int nj = full_pages(lens[jj], max_pages);
-      const bool below = diff != 0 ? diff < 0 : c < nn ? jj < i : nj != n_mine ? nj < n_mine : jj < i;
+      const int c = common_pages(mine, table + static_cast<long>(jj) * max_pages, n, &diff);
+      const bool below = diff != 0 ? diff < 0 : c < n ? jj < i : nj != n_mine ? nj < n_mine : jj < i;
       if (below) {
-        ++count;
+        count += lane == 0;
         most = max(most, c);
       }
     }
   }
+  count = __reduce_add_sync(0xffffffffu, count);
   if (lane == 0) {
     atomicAdd(&smaller, count);
     atomicMax(&longest, most);
@@ -99,22 +112,37 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
   if (threadIdx.x < kPlanHead)
     plan[threadIdx.x] = threadIdx.x == 0 ? B : threadIdx.x == 1 ? max_pages : threadIdx.x == 2 ? kPlanMark : 0;
   __syncthreads();
-  // The run of places around i - 1 and i that have c[i] tiles in common: its
-  // name is the first i of it that has that value; its parent's is that of the
-  // larger of the two values that bound it.
-  auto run = [&](int i, int* lo, int* hi) {  // -> name; places [lo, hi)
+  const int lane = threadIdx.x & 31;
+  // The run of places around i - 1 and i that have c[i] > 0 tiles in common: its
+  // name is the first i of it that has that value; places [lo, hi).  A whole warp.
+  auto run = [&](int i, int* lo, int* hi) {
+    const int v = c[i];
     int name = i, l = i - 1, h = i + 1;
-    while (c[l] >= c[i]) {  // (c[0] = 0 ends it)
-      if (c[l] == c[i]) name = l;
-      --l;
+    while (true) {  // (c[0] = 0 ends it)
+      const int x = l - lane >= 0 ? c[l - lane] : -1;
+      const uint32_t stop = __ballot_sync(0xffffffffu, x < v), same = __ballot_sync(0xffffffffu, x == v);
+      const uint32_t seen = stop != 0 ? same & ((1u << (__ffs(stop) - 1)) - 1) : same;
+      if (seen != 0) name = l - (31 - __clz(seen));
+      if (stop != 0) {
+        l -= __ffs(stop) - 1;
+        break;
+      }
+      l -= 32;
     }
-    while (c[h] >= c[i]) ++h;
+    while (true) {  // (c[B] = 0)
+      const uint32_t stop = __ballot_sync(0xffffffffu, (h + lane <= B ? c[h + lane] : -1) < v);
+      if (stop != 0) {
+        h += __ffs(stop) - 1;
+        break;
+      }
+      h += 32;
+    }
     *lo = l;
     *hi = h;
     return name;
   };
-  auto bound = [&](int lo, int hi) { return c[lo] >= c[hi] ? lo : hi; };
-  auto level = [&](int i) {  // 1: no node above it
+  auto bound = [&](int lo, int hi) { return c[lo] >= c[hi] ? lo : hi; };  // the parent's value
+  auto level = [&](int i) {  // nodes from i's up
     int n = 0;
     for (; c[i] > 0; ++n) {
       int lo, hi;
@@ -123,35 +151,44 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
     }
     return n;
   };
-  auto name_of = [&](int i) {  // node of value c[i] around i, or -1
-    if (c[i] == 0) return -1;
-    int lo, hi;
-    return B + run(i, &lo, &hi);
-  };
-  for (int i = threadIdx.x; i < B; i += kTree) {
-    int first = 0, count = 0, t0 = 0, t1 = 0, parent = -1;
+  int32_t* above = nodes + 2 * B * kNodeWords;
+  for (int i = threadIdx.x >> 5; i < B; i += kTree / 32) {
+    int first = 0, count = 0, t0 = 0, t1 = 0;
     if (i > 0 && c[i] > 0) {
       int lo, hi;
       if (run(i, &lo, &hi) == i && level(i) <= kPlanLevels) {
-        const int up = bound(lo, hi);
         first = lo;
         count = hi - lo;
-        t0 = c[up];
+        t0 = c[bound(lo, hi)];
         t1 = c[i];
-        parent = name_of(up);
       }
     }
-    int32_t* n = nodes + (B + i) * kNodeWords;
-    n[0] = first, n[1] = count, n[2] = t0, n[3] = t1, n[4] = parent;
-    // The place's own tiles: those behind the deepest node above it that is kept.
-    int up = bound(i, i + 1);
-    for (int l = level(up); l > kPlanLevels; --l) {
-      int lo, hi;
-      run(up, &lo, &hi);
-      up = bound(lo, hi);
+    // The nodes above the place, from the deepest that is kept up; its own tiles are
+    // those behind that one's.
+    int up = bound(i, i + 1), own = -1;
+    for (int l = level(up), k = 0; k < kPlanLevels; ++k) {
+      while (l > kPlanLevels) {
+        int lo, hi;
+        run(up, &lo, &hi);
+        up = bound(lo, hi);
+        --l;
+      }
+      if (own < 0) own = c[up];
+      int name = -1;
+      if (c[up] > 0) {
+        int lo, hi;
+        name = B + run(up, &lo, &hi);
+        up = bound(lo, hi);
+        --l;
+      }
+      if (lane == 0) above[i * kPlanLevels + k] = name;
     }
-    n = nodes + i * kNodeWords;
-    n[0] = i, n[1] = 1, n[2] = c[up], n[3] = -1, n[4] = name_of(up);
+    if (lane == 0) {
+      int32_t* n = nodes + (B + i) * kNodeWords;
+      n[0] = first, n[1] = count, n[2] = t0, n[3] = t1;
+      n = nodes + i * kNodeWords;
+      n[0] = i, n[1] = 1, n[2] = own, n[3] = -1;
+    }
   }
 }
 

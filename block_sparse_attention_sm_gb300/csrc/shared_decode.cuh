@@ -13,20 +13,23 @@ namespace ssattn {
 // A plan of shared pages, int32 words.  The sequences in the order of their
 // tables' pages ([kPlanHead, kPlanHead + B)), then 2 B nodes of kNodeWords:
 // node i < B is what the sequence at place i has to itself, node B + i the
-// pages shared by a run of places (empty: not used).
+// pages shared by a run of places (empty: not used); then for each place the
+// kPlanLevels nodes above it, from the deepest up (-1: none).
 constexpr int kPlanHead = 8;    // words: B, max_pages, a mark
 constexpr int kPlanMark = 0x504c414e;
-constexpr int kNodeWords = 5;   // first place, places, first tile, end tile, parent node (-1: none)
+constexpr int kNodeWords = 4;   // first place, places, first tile, end tile
 constexpr int kPlanLevels = 7;  // shared nodes above a sequence at most (bounds the partial results)
 constexpr int kPlanMaxB = 8192;
+constexpr int kSharedMaxB = 32768;  // sequences of a decode without a plan (their sums fit shared memory)
 
-__host__ __device__ constexpr size_t plan_words(long B) { return kPlanHead + B + 2 * B * kNodeWords; }
+__host__ __device__ constexpr size_t plan_words(long B) { return kPlanHead + B + 2 * B * kNodeWords + B * kPlanLevels; }
 
 cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
                                int32_t* plan, cudaStream_t st);
 
 struct SharedParams {
   int B, Hq, Hkv, G;
+  uint32_t inv_g;          // floor(2^32 / G) + 1 (G > 1): r / G of a row r is the product's upper half
   int num_pages, max_pages;
   int ctas;                // CTAs of the attention kernel
   float scale_log2;
@@ -39,8 +42,10 @@ struct SharedParams {
   float* part_o;           // [part_rows][d] unnormalised partial outputs
   float2* part_ml;         // [part_rows] (reference maximum in exp2 units, sum)
   long part_rows;
-  long long* node_at;      // [2 B] first tile of a node among all the launch's
-  long long* node_rows;    // [2 B] its first partial row
+  long long* total;        // all items' cost
+  int* cum;                // [B + 1] own tiles of the places below
+  long long* node_at;      // [B] cost of the items in front of a shared node
+  long long* node_rows;    // [B] its first partial row
   float* lse;              // [B][Hq] log2 of the softmax's denominator (weights only)
   float* scores;           // [B][Hq][max_pages][128] (weights only)
   float* weights;          // [B][Hkv][max_pages * 128], nullable
@@ -49,7 +54,7 @@ struct SharedParams {
 
 // Workspace: sizes and where its arrays lie.
 struct SharedSpace {
-  size_t part_o, part_ml, node_at, node_rows, lse, scores, bytes;
+  size_t part_o, part_ml, total, cum, node_at, node_rows, lse, scores, bytes;
   long part_rows;
 };
 SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan, bool weights);

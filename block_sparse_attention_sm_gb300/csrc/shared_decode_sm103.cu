@@ -10,25 +10,32 @@
 // head, which makes of the many matrix-vector products of a decode step a
 // matrix product: 64 sequences x 4 heads are 256 rows for each key read.
 //
-// Work: an item is (node, KV head, block of up to 256 rows), as long as the
-// node has tiles.  All items' tiles laid end to end are cut into equal pieces,
-// one a CTA, so that the SMs end together whatever the lengths; a piece ends at
-// an item's end too.  Every piece writes its rows' (m, l, O) in fp32, and
-// merge_kernel joins them.  The cuts follow from the plan and the lengths, which
-// every CTA adds up for itself at its start (2 B nodes): nothing comes from the
-// host, the lengths may change from step to step under the same plan.
+// What a sequence has to itself has only G rows.  128 / G sequences are bundled:
+// their rows are the 128 rows of the MMAs, their tiles come one behind the other,
+// and each tile counts for the rows of its own sequence alone (the others' weights
+// are 0).  So the rows' state stays in place while short sequences pass: no new Q
+// and no result to write for each.
+//
+// Work: an item is (bundle, KV head) or (shared node, KV head, block of up to 256
+// rows), as long as it has tiles.  All items' tiles laid end to end are cut into
+// equal shares, one a CTA, so that the SMs end together whatever the lengths.
+// Every piece of an item writes its rows' (m, l, O) in fp32, and merge_kernel joins
+// them.  The cuts follow from the plan and the lengths, which every CTA adds up for
+// itself at its start: nothing comes from the host, the lengths may change from step
+// to step under the same plan.
 //
 // One CTA: two streams t = 0, 1, each with scores S_t, weights P_t (bf16, over
 // S_t) and output O_t in TMEM (128 columns each of S and O) and a softmax
 // warpgroup, one thread a row.  Of more than 128 rows each stream has half, and
-// both take every tile.  Of fewer both have the same rows and take alternate
-// tiles: the way of a tile from its scores to P.V is longer than the time its
-// bytes take, so two are under way at once.  Scores: S_t = Q_t K^T (SS form,
-// K-major, 128-byte swizzle); O_t += P_t V (TS form, V MN-major).
+// both take every tile.  Of fewer both have the same rows and take alternate tiles:
+// the way of a tile from its scores to P.V is longer than the time its bytes take,
+// so two are under way at once.  Scores: S_t = Q_t K^T (SS form, K-major, 128-byte swizzle); O_t += P_t V (TS
+// form, V MN-major).
 //
 // Warps 0-3 / 4-7 softmax of stream 0 / 1 (they also load their rows of Q: the
 // next piece's before they write this one's result), 8 loads K and V tiles
-// through one ring, 9 issues the MMAs, 10 works out the pieces.
+// through one ring, 9 issues the MMAs, 10 works out the pieces, in segments
+// of up to 16 tiles with a tile's page and sequence each.
 //
 // The last tile of a sequence, of r < 128 keys, is loaded from row r - 128 of
 // its page: zeros come in front, the keys follow, and what the page holds behind
@@ -52,8 +59,9 @@ constexpr float kRescaleLog2 = 8.0f;  // lazy-rescale slack, exp2 domain
 constexpr int kSMs = 152;
 constexpr int kThreads = 384;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10;
-constexpr int kRows = 256;  // rows of an item
-constexpr int kPieces = 4;  // published pieces
+constexpr int kRows = 256;      // rows of an item
+constexpr int kSegments = 4;    // published segments
+constexpr int kSegTiles = 16;
 // Register split (see the prefill kernel): the launch's pool, exactly.
 constexpr int kLaunchRegs = 168, kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
@@ -65,43 +73,58 @@ struct Cfg {
   static constexpr int kRing = (D == 128) ? 5 : 10;
   static constexpr int kRingOff = 2 * kTileBytes;  // behind the two Q tiles
   static constexpr int kCtlOff = kRingOff + kRing * kTileBytes;
-  static constexpr int kCtlBytes = 1536;
+  static constexpr int kCtlBytes = 2048;
   static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+  // The sums over the batch are made where the tiles come later: a place's tiles
+  // (4 bytes), a shared node's tiles and rows (16 bytes).
+  static_assert(4 * (kSharedMaxB + 2) <= kCtlOff && 4 * (kPlanMaxB + 2) + 16 * kPlanMaxB <= kCtlOff, "sums");
 };
+
+// Eight floats at once (32 bytes, a whole sector of a line), 32-byte aligned.
+__device__ __forceinline__ void store8(float* to, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 
 // The tiles [t0, t1) of places [first, first + count).
 struct Node {
   int first, count, t0, t1;
 };
 
-// A run of tiles of one item.
-struct Piece {
-  int n;          // tiles; 0: no more pieces
-  int t0;         // the first of them
+// A tile: where it lies in the pools, which of its sequence's it is, the zero rows in
+// front of its keys, whose rows it counts for (a place of the bundle; -1: all).
+struct Tile {
+  int z, tile;
+  short shift, place;
+};
+
+// Up to kSegTiles consecutive tiles of a piece (a run of tiles of one item).
+struct Segment {
+  short n;            // tiles; 0: no more segments
+  short odd;          // tiles of the piece in front of the segment's, modulo 2
+  short start, end;   // the piece's first / last segment
   int kvh;
-  int first;      // the node's first place
-  int row0, rows; // of the node's rows (place x head of the group)
-  int both;       // each stream has half the rows and takes every tile; else all rows, alternate tiles
-  int last, shift;  // a sequence's last tile, the zero rows in front of its keys (-1: none here)
-  int b;          // a sequence that has these tiles
-  long long out;  // its first partial row (-1: no room)
+  int first;          // the item's first place
+  int row0;           // its first row among the node's (place x head of the group)
+  short rows;         // its rows
+  short both;         // each stream has half the rows and takes every tile; else all rows, alternate tiles
+  long long out;      // its first partial row (-1: no room)
+  Tile tile[kSegTiles];
 };
 
 struct Ctl {
   uint64_t r_full[10], r_empty[10];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2];
-  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int n_issued;
-  // the start of this CTA's share: node, its first tile and row among all
-  int node;
-  long long at, rows, total;
-  long long scan[2][kThreads / 32];
-  Piece piece[kPieces];
+  long long leaf_total, total;  // cost of all bundles, of all items
+  Segment seg[kSegments];
 };
 
 __device__ __forceinline__ const int32_t* valid_plan(const SharedParams& p) {
@@ -152,26 +175,52 @@ __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
   return d;
 }
 
-// Inclusive sums over the block of two values; the totals in t0, t1.
-__device__ void block_sums(long long& a, long long& b, long long (*scan)[kThreads / 32], long long* ta) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) a += x, b += y;
-  }
-  if (lane == 31) scan[0][warp] = a, scan[1][warp] = b;
-  __syncthreads();
-  long long all = 0, pa = 0, pb = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) pa += scan[0][w], pb += scan[1][w];
-    all += scan[0][w];
-  }
-  a += pa;
-  b += pb;
-  *ta = all;
+// Cost of a tile, in the shares of the CTAs: where both streams take every tile it is
+// ~3700 cycles, else the ~2700 of its bytes (both measured).
+constexpr int kTileCost = 2, kBothCost = 3;
+__device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : kTileCost; }
+// A CTA's share of all items' cost (at least a tile, so that each CTA between an item's
+// first and last has a part of it).
+__device__ __forceinline__ long long share_of(long long total, int ctas) {
+  return max(static_cast<long long>(kBothCost), (total + ctas - 1) / ctas);
+}
+// a / b for non-negative numbers, which hardly ever need 64 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
+// Exclusive sums over the block's threads of three values, in place; the totals in t.
+__device__ void block_sums(long long (&v)[3], long long (&t)[3], long long* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int W = kThreads / 32;
+  long long mine[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    mine[k] = v[k];
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] += x;
+    }
+    if (lane == 31) scratch[k * W + warp] = v[k];
+    t[k] = 0;
+    v[k] -= mine[k];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const long long x = scratch[k * W + w];
+      if (w < warp) v[k] += x;
+      t[k] += x;
+    }
+  }
+  __syncthreads();
+}
+
+// (A launch's code comes out of L2 line by line: waits, divisions and the parts of a
+// piece appear once each, and loops that need not be unrolled are not.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -188,190 +237,212 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &ctl->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t* plan = valid_plan(p);
+  const int B = p.B, G = p.G, nb = kTile / G;  // sequences of a bundle
+  const int nodes = plan != nullptr ? B : 0;   // shared ones
 
-  if (tid == 0) {
-    for (int s = 0; s < NR; ++s) {
-      mbar_init(&ctl->r_full[s], 1);
-      mbar_init(&ctl->r_empty[s], 1);
+  if (tid < NR) {
+    mbar_init(&ctl->r_full[tid], 1);
+    mbar_init(&ctl->r_empty[tid], 1);
+  } else if (tid >= 32 && tid < 32 + kSegments) {
+    mbar_init(&ctl->seg_full[tid - 32], 1);
+    mbar_init(&ctl->seg_empty[tid - 32], 10);  // softmax warps, loader, issuer
+  } else if (tid >= 64 && tid < 66) {
+    const int t = tid - 64;
+    mbar_init(&ctl->q_full[t], 4);
+    mbar_init(&ctl->s_full[t], 1);
+    mbar_init(&ctl->p_full[t], 4);
+    mbar_init(&ctl->o_full[t], 1);
+    mbar_init(&ctl->o_free[t], 4);
+    if (t == 0) {
+      mbar_init(&ctl->mma_done, 1);
+      ctl->abort_flag = 0;
+      ctl->n_issued = 0;
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&ctl->q_full[t], 4);
-      mbar_init(&ctl->s_full[t], 1);
-      mbar_init(&ctl->p_full[t], 4);
-      mbar_init(&ctl->o_full[t], 1);
-      mbar_init(&ctl->o_free[t], 4);
-    }
-    for (int s = 0; s < kPieces; ++s) {
-      mbar_init(&ctl->piece_full[s], 1);
-      mbar_init(&ctl->piece_empty[s], 10);  // softmax warps, loader, issuer
-    }
-    mbar_init(&ctl->mma_done, 1);
-    ctl->abort_flag = 0;
-    ctl->n_issued = 0;
-    ctl->node = -1;
-    fence_mbar_init();
   }
+  fence_mbar_init();
   if (warp == kWarpMma) {
     tmem_alloc(&ctl->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  // Every node's tiles and partial rows, added up; this CTA's share begins in
-  // the node that its first tile falls into.
-  const int nodes = plan != nullptr ? 2 * p.B : p.B;
+  if (warp == kWarpLoad && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // Sums over the batch, in the shared memory that the tiles take later: the own
+  // tiles of the places below each, the cost and partial rows of the shared nodes
+  // below each.
+  int* cum = reinterpret_cast<int*>(smem);                                              // [B + 1]
+  long long* node_at = reinterpret_cast<long long*>(smem + (4 * (B + 1) + 7) / 8 * 8);  // [nodes]
+  long long* node_rows = node_at + nodes;                                               // [nodes]
   {
-    const int each = (nodes + kThreads - 1) / kThreads, n0 = min(nodes, tid * each), n1 = min(nodes, n0 + each);
-    long long tiles = 0, rows = 0;
-    for (int n = n0; n < n1; ++n) {
-      const Node x = node_of(p, plan, n);
-      const Deal d = deal_of(x, p.G);
-      tiles += static_cast<long long>(x.t1 - x.t0) * d.blocks * p.Hkv;
-      rows += static_cast<long long>(d.blocks) * p.Hkv * d.part * (x.t1 > x.t0);
-    }
-    long long at = tiles, row = rows, total;
-    __syncthreads();
-    block_sums(at, row, ctl->scan, &total);
-    at -= tiles;
-    row -= rows;
-    const long long per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x;
-    if (blockIdx.x == 0 || (begin >= at && begin < at + tiles))
+    const int each = (B + kThreads - 1) / kThreads, n0 = min(B, tid * each), n1 = min(B, n0 + each);
+    long long v[3] = {0, 0, 0}, t[3] = {0, 0, 0};
+    // twice: adding up, then (with what lies below) writing
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
       for (int n = n0; n < n1; ++n) {
         const Node x = node_of(p, plan, n);
-        const Deal d = deal_of(x, p.G);
-        const long long mine = static_cast<long long>(x.t1 - x.t0) * d.blocks * p.Hkv;
-        if (blockIdx.x == 0) {
-          p.node_at[n] = at;
-          p.node_rows[n] = row;
+        if (pass == 1) {
+          cum[n] = static_cast<int>(v[0]);
+          if (blockIdx.x == 0) p.cum[n] = static_cast<int>(v[0]);
         }
-        if (begin >= at && begin < at + mine) {
-          ctl->node = n;
-          ctl->at = at;
-          ctl->rows = row;
+        v[0] += x.t1 - x.t0;
+        if (plan != nullptr) {
+          const Node y = node_of(p, plan, B + n);
+          const Deal d = deal_of(y, G);
+          if (pass == 1) {
+            const long long at = t[0] * p.Hkv * kTileCost + v[1], row = 2ll * p.Hq * B + v[2];
+            node_at[n] = at;
+            node_rows[n] = row;
+            if (blockIdx.x == 0) {
+              p.node_at[n] = at;
+              p.node_rows[n] = row;
+            }
+          }
+          v[1] += static_cast<long long>(y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
+          v[2] += static_cast<long long>(d.blocks) * p.Hkv * d.part * (y.t1 > y.t0);
         }
-        at += mine;
-        row += static_cast<long long>(d.blocks) * p.Hkv * d.part * (x.t1 > x.t0);
       }
-    if (tid == 0) ctl->total = total;
+      if (pass == 0) block_sums(v, t, reinterpret_cast<long long*>(ctl->seg));
+    }
+    if (tid == 0) {
+      cum[B] = static_cast<int>(t[0]);
+      ctl->leaf_total = t[0] * p.Hkv * kTileCost;
+      ctl->total = ctl->leaf_total + t[1];
+      if (blockIdx.x == 0) {
+        p.cum[B] = static_cast<int>(t[0]);
+        *p.total = ctl->total;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const long long per = (ctl->total + gridDim.x - 1) / gridDim.x;
 
-  // Piece number k, when it has been published (a copy: the place is given back by the caller).
-  auto piece_at = [&](int k, Piece* out) -> bool {
-    if (!mbar_wait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) return false;
-    *out = ctl->piece[k % kPieces];
-    return true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_small(bar, parity, abort_flag); };
+  // Segment number k, when it has been published (its place is given back by `seg_done`).
+  auto seg_at = [&](int k) -> const Segment* {
+    return wait(&ctl->seg_full[k % kSegments], (k / kSegments) & 1) ? &ctl->seg[k % kSegments] : nullptr;
   };
+  auto seg_done = [&](int k) { mbar_arrive(&ctl->seg_empty[k % kSegments]); };
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsIssue>();
     if (warp == kWarpLoad) {
       // ---------------------------------------------------------- loader
+      // Order of use: K0 V0 K1 V1 .. where both streams take every tile,
+      // K0 K1 V0 K2 V1 .. where they alternate.
       if (lane == 0) {
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-      }
-      int e = 0;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        Piece x;
-        ok = __all_sync(0xffffffffu, piece_at(k, &x));
-        if (!ok || x.n == 0) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
-        // Order of use: K0 V0 K1 V1 .. where both streams take every tile,
-        // K0 K1 V0 K2 V1 .. where they alternate.
-        const int32_t* pages = p.table + static_cast<long>(x.b) * p.max_pages + x.t0;
-        int held = 0, page[2] = {0, 0};  // 32 tiles' pages, a lane each; those of the last two keys' tiles
-        int ki = 0, vi = 0;
-        while (ok && vi < x.n) {
-          const bool key = ki < x.n && (x.both ? ki == vi : ki <= vi + 1);
-          const int u = key ? ki : vi;
-          if (key) {
-            if ((u & 31) == 0) held = u + lane < x.n ? pages[u + lane] : 0;
-            page[1] = page[0];
-            page[0] = __shfl_sync(0xffffffffu, held, u & 31);
-          }
-          const int at = u == ki - (key ? 0 : 1) ? page[0] : page[1];
-          const int st = e % NR;
-          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->r_empty[st], ((e / NR) & 1) ^ 1, abort_flag));
-          if (!ok) break;
-          if (lane == 0) {
-            const int z = at >= 0 && at < p.num_pages ? at * p.Hkv + x.kvh : p.num_pages * p.Hkv;
-            const int y = x.t0 + u == x.last ? -x.shift : 0;
-            mbar_arrive_expect_tx(&ctl->r_full[st], C::kTileBytes);
+        uint32_t slot = 0, par = 1;
+        int e = 0;
+        Tile held{};  // the tile whose V comes next
+        bool ok = true;
+#pragma unroll 1
+        for (int k = 0; ok; ++k) {
+          const Segment* x = seg_at(k);
+          if (x == nullptr || x->n == 0) break;
+          const int n = x->n, both = x->both, steps = n + (!both && x->end), first = !both && x->start;
+#pragma unroll 1
+          for (int i = 0; ok && i < steps; ++i) {
+            const Tile d = i < n ? x->tile[i] : held;
+#pragma unroll 1
+            for (int v = 0; ok && v < 2; ++v) {
+              if (v == 0 ? i >= n : first && i == 0) continue;
+              const Tile y = v == 0 || both ? d : held;
+              if (!(ok = wait(&ctl->r_empty[slot], par))) break;
+              mbar_arrive_expect_tx(&ctl->r_full[slot], C::kTileBytes);
 #pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(sR + st * C::kTileBytes + c * 16384, key ? &tmK : &tmV, &ctl->r_full[st], c * 64, y, z);
-            *reinterpret_cast<volatile int*>(&ctl->n_issued) = e + 1;
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(sR + slot * C::kTileBytes + c * 16384, v == 0 ? &tmK : &tmV, &ctl->r_full[slot], c * 64,
+                            -y.shift, y.z);
+              *reinterpret_cast<volatile int*>(&ctl->n_issued) = ++e;
+              if (++slot == NR) slot = 0, par ^= 1;
+            }
+            held = d;
           }
-          ++e;
-          if (key) ++ki; else ++vi;
+          seg_done(k);
         }
       }
+      __syncwarp();
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- MMA issuer
+      // One stream's P.V of its last tile and scores of its next, then the other's:
+      // a strict order, so that one softmax runs beside the other's MMAs (with an
+      // issuer for each stream both fell into step, and a tile of two streams took
+      // 4700 cycles instead of ~3700).
       if (lane == 0) {
         constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
         const uint32_t sQa = smem_u32(sQ), sRa = smem_u32(sR);
-        uint32_t slot = 0, par = 0;            // next ring entry
-        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};  // phases
-        bool ok = true;
-        auto next_entry = [&](uint32_t* s) -> bool {
-          if (!mbar_wait(&ctl->r_full[slot], par, abort_flag)) return false;
-          *s = slot;
-          if (++slot == NR) slot = 0, par ^= 1;
-          return true;
+        uint32_t slot = 0, par = 0, ks = 0, vs = 0;
+        uint32_t qn = 0, pn = 0, on = 0;  // parities, a bit a stream
+        auto entry = [&]() -> bool {      // the ring's next entry, in `slot`
+          return wait(&ctl->r_full[slot], par);
         };
+        auto next = [&]() {
+          if (++slot == NR) slot = 0, par ^= 1;
+        };
+        int u = 0;  // tiles of the piece so far
+        bool ok = true;
+#pragma unroll 1
         for (int k = 0; ok; ++k) {
-          Piece x;
-          ok = piece_at(k, &x);
-          if (!ok || x.n == 0) break;
-          mbar_arrive(&ctl->piece_empty[k % kPieces]);
-          const bool both = x.both != 0;
-          const int steps = both ? 2 * x.n : x.n;
-          uint32_t ks = 0, vs = 0;
-          for (int i = 0; ok && i < steps + 2; ++i) {
-            const int t = i & 1;
-            if (i >= 2) {  // P.V of step i - 2
-              if ((!both || t == 0) && !(ok = next_entry(&vs))) break;
-              if (i < 4) {  // the stream's first of the piece: its O has been read
-                ok = mbar_wait(&ctl->o_free[t], (on[t] & 1) ^ 1, abort_flag);
-                ++on[t];
-                if (!ok) break;
-              }
-              ok = mbar_wait(&ctl->p_full[t], pn[t] & 1, abort_flag);
-              ++pn[t];
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t dv = smem_desc(sRa + vs * C::kTileBytes, 16384, 1024);
+          const Segment* x = seg_at(k);
+          if (x == nullptr || x->n == 0) break;
+          // P.V follows its scores by one tile (both streams) or two (alternate ones).
+          const int n = x->n, both = x->both, lag = both ? 1 : 2, steps = n + (x->end ? lag : 0);
+          if (x->start != 0) u = 0;
+          seg_done(k);
+#pragma unroll 1
+          for (int i = 0; ok && i < steps; ++i, ++u) {
+#pragma unroll 1
+            for (int t = both ? 0 : u & 1; ok && t < (both ? 2 : (u & 1) + 1); ++t) {
+              const bool lead = !both || t == 0, tail = !both || t == 1;
+              const uint32_t bit = 1u << t;
+              if (u >= lag) {  // O_t += P_t V
+                if (lead) {
+                  if (!(ok = entry())) break;
+                  vs = slot;
+                  next();
+                }
+                const bool first = u < 2 * lag;
+                if (first) {  // the piece before has been read out of O
+                  if (!(ok = wait(&ctl->o_free[t], (on & bit) ? 0 : 1))) break;
+                  on ^= bit;
+                }
+                if (!(ok = wait(&ctl->p_full[t], (pn & bit) ? 1 : 0))) break;
+                pn ^= bit;
+                tc_fence_after();
+                const uint64_t dv = smem_desc(sRa + vs * C::kTileBytes, 16384, 1024);
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_bf16_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + kk * 8, dv + ((kk * 2048) >> 4),
-                            idO, (i >= 4 || kk > 0) ? 1u : 0u);
-              if (!both || t == 1) mma_commit(&ctl->r_empty[vs]);
-              if (i >= steps) mma_commit(&ctl->o_full[t]);
-            }
-            if (i < steps) {  // scores of step i
-              if ((!both || t == 0) && !(ok = next_entry(&ks))) break;
-              if (i < 2) {
-                ok = mbar_wait(&ctl->q_full[t], qn[t] & 1, abort_flag);
-                ++qn[t];
-                if (!ok) break;
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  mma_bf16_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + kk * 8, dv + ((kk * 2048) >> 4),
+                              idO, (!first || kk > 0) ? 1u : 0u);
+                if (i >= n) mma_commit(&ctl->o_full[t]);
+                if (tail) mma_commit(&ctl->r_empty[vs]);
               }
-              tc_fence_after();
-              const uint64_t dq = smem_desc(sQa + t * C::kTileBytes, 16, 1024);
-              const uint64_t dk = smem_desc(sRa + ks * C::kTileBytes, 16, 1024);
+              if (i < n) {  // S_t = Q_t K^T
+                if (lead) {
+                  if (!(ok = entry())) break;
+                  ks = slot;
+                  next();
+                }
+                if (u < lag) {
+                  if (!(ok = wait(&ctl->q_full[t], (qn & bit) ? 1 : 0))) break;
+                  qn ^= bit;
+                }
+                tc_fence_after();
+                const uint64_t dq = smem_desc(sQa + t * C::kTileBytes, 16, 1024);
+                const uint64_t dk = smem_desc(sRa + ks * C::kTileBytes, 16, 1024);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                mma_bf16_ss(tmem + C::kColS + 128 * t, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                  mma_bf16_ss(tmem + C::kColS + 128 * t, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&ctl->s_full[t]);
+                if (tail) mma_commit(&ctl->r_empty[ks]);
               }
-              mma_commit(&ctl->s_full[t]);
-              if (!both || t == 1) mma_commit(&ctl->r_empty[ks]);
             }
           }
         }
@@ -381,58 +452,192 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kWarpPlan) {
       // ---------------------------------------------------------- pieces
-      if (lane == 0) {
-        long long at = per * blockIdx.x;
-        const long long end = min(at + per, ctl->total);
-        int n = ctl->node;
-        long long node_at = ctl->at, node_rows = ctl->rows;
-        for (int k = 0;; ++k) {
-          Piece x{};
-          if (at < end && n >= 0) {
-            Node nd = node_of(p, plan, n);
-            Deal d = deal_of(nd, p.G);
-            int T = nd.t1 - nd.t0;
-            while (n < nodes && at >= node_at + static_cast<long long>(T) * d.blocks * p.Hkv) {
-              node_at += static_cast<long long>(T) * d.blocks * p.Hkv;
-              node_rows += T > 0 ? static_cast<long long>(d.blocks) * p.Hkv * d.part : 0;
-              if (++n == nodes) break;
-              nd = node_of(p, plan, n);
-              d = deal_of(nd, p.G);
-              T = nd.t1 - nd.t0;
-            }
-            if (n < nodes) {
-              const long long in = at - node_at;
-              const int item = static_cast<int>(in / T), u = static_cast<int>(in - static_cast<long long>(item) * T);
-              x.n = static_cast<int>(min(static_cast<long long>(T - u), end - at));
-              x.t0 = nd.t0 + u;
-              x.kvh = item / d.blocks;
-              x.first = nd.first;
-              x.row0 = (item - x.kvh * d.blocks) * d.rows;
-              x.rows = min(d.rows, nd.count * p.G - x.row0);
-              x.both = d.rows > kTile;
-              x.b = place_of(plan, nd.first, p.B);
-              x.last = -1;
-              if (n < p.B) {
-                const int len = length_of(p, x.b);
-                x.last = len % kTile != 0 ? tiles_of(len) - 1 : -1;
-                x.shift = kTile - len % kTile;
-              }
-              x.out = node_rows + static_cast<long long>(item) * d.part + static_cast<long long>(blockIdx.x) * kRows;
-              if (x.out + d.part > p.part_rows) x.out = -1;
-              at += x.n;
-            }
-          }
-          if (!mbar_wait(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
-          ctl->piece[k % kPieces] = x;
-          mbar_arrive(&ctl->piece_full[k % kPieces]);  // (release: the others read it behind their wait)
-          if (x.n == 0) break;
+      // A tile belongs to the CTA whose share its cost begins in.
+      const long long leaf_total = ctl->leaf_total, total = ctl->total, per = share_of(total, gridDim.x);
+      long long at = per * blockIdx.x;
+      const long long end = min(at + per, total);
+      // Where the share begins: in a bundle ..
+      int j = 0, kvh = 0, base = 0, T = 0, skip = 0;  // bundle, head, its first place's sum, its tiles, those in front
+      int n = 0;                                      // .. or a shared node
+      long long n_at = 0, n_rows = 0;
+      if (at < end) {
+        const bool leaf = at < leaf_total;
+        int lo = 0, hi = leaf ? (B + nb - 1) / nb : nodes;
+#pragma unroll 1
+        while (hi - lo > 1) {  // the last one that begins at or below `at` (an empty one: the next begins there too)
+          const int mid = (lo + hi) / 2;
+          if ((leaf ? static_cast<long long>(cum[mid * nb]) * p.Hkv * kTileCost : node_at[mid]) <= at) lo = mid; else hi = mid;
         }
+        if (leaf) {
+          j = lo;
+          base = cum[j * nb];
+          T = cum[min(B, (j + 1) * nb)] - base;
+          const long long begin = static_cast<long long>(base) * p.Hkv * kTileCost;
+          const long long in = (at - begin + kTileCost - 1) / kTileCost;
+          at = begin + in * kTileCost;
+          kvh = min(p.Hkv - 1, static_cast<int>(quotient(in, T)));
+          skip = static_cast<int>(in - static_cast<long long>(kvh) * T);
+        } else {
+          n = lo;
+        }
+        n_at = nodes > 0 ? node_at[n] : 0;
+        n_rows = nodes > 0 ? node_rows[n] : 0;
       }
-      __syncwarp();
+      // (from here on the tiles may land over the sums)
+      // The piece that is being published, and of a bundle 32 places, a lane each.
+      Segment seg{};
+      int left = 0, done = 0;             // its tiles to come, its tiles published
+      int t_first = 0, node_b = 0;        // a node's piece: its first tile, a sequence that has them
+      bool bundle = false;
+      int w0 = 0, before = 0, window = 0; // window: first place, tiles in front of it, its tiles
+      int b = 0, t0 = 0, count = 0, len = 0, sum = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        // ---- the next piece
+#pragma unroll 1
+        while (left == 0 && at < end) {
+          done = 0;
+          if (at < leaf_total) {
+            if (skip >= T) {  // the next head's, or the next bundle that has tiles
+              skip -= T;
+              if (T == 0 || ++kvh == p.Hkv) {
+                kvh = 0;
+                if (++j * nb >= B) at = leaf_total;  // (no more)
+                T = 0;
+#pragma unroll 1
+                for (int i = j * nb + lane; i < min(B, (j + 1) * nb); i += 32) {
+                  const Node x = node_of(p, plan, i);
+                  T += x.t1 - x.t0;
+                }
+                T = __reduce_add_sync(0xffffffffu, T);
+              }
+              continue;
+            }
+            const int first = j * nb, places = min(nb, B - first), rows = places * G;
+            bundle = true;
+            seg.kvh = kvh;
+            seg.first = first;
+            seg.row0 = 0;
+            seg.rows = static_cast<short>(rows);
+            seg.both = 0;
+            seg.out = 2ll * G * p.Hkv * first + 2ll * kvh * rows + static_cast<long long>(blockIdx.x) * kRows;
+            if (seg.out + 2 * rows > p.part_rows) seg.out = -1;
+            left = static_cast<int>(min(static_cast<long long>(T - skip), (end - at + kTileCost - 1) / kTileCost));
+            at += static_cast<long long>(left) * kTileCost;
+            w0 = -32, before = window = 0;
+          } else {
+            const Node x = node_of(p, plan, B + n);
+            const Deal d = deal_of(x, G);
+            const int Tn = x.t1 - x.t0, cost = cost_of(d);
+            const long long all = static_cast<long long>(Tn) * d.blocks * p.Hkv;
+            const long long in = quotient(max(0ll, at - n_at) + cost - 1, cost);
+            if (in >= all) {
+              n_at += all * cost;
+              at = max(at, n_at);
+              n_rows += Tn > 0 ? static_cast<long long>(d.blocks) * p.Hkv * d.part : 0;
+              if (++n >= nodes) at = end;
+              continue;
+            }
+            at = n_at + in * cost;
+            if (at >= end) break;
+            const int item = static_cast<int>(quotient(in, Tn)), u = static_cast<int>(in - static_cast<long long>(item) * Tn);
+            const int head = item / d.blocks;
+            bundle = false;
+            seg.kvh = head;
+            seg.first = x.first;
+            seg.row0 = (item - head * d.blocks) * d.rows;
+            seg.rows = static_cast<short>(min(d.rows, x.count * G - seg.row0));
+            seg.both = d.rows > kTile;
+            seg.out = n_rows + static_cast<long long>(item) * d.part + static_cast<long long>(blockIdx.x) * kRows;
+            if (seg.out + d.part > p.part_rows) seg.out = -1;
+            t_first = x.t0 + u;
+            node_b = place_of(plan, x.first, B);
+            left = static_cast<int>(min(static_cast<long long>(Tn - u), quotient(end - at + cost - 1, cost)));
+            at += static_cast<long long>(left) * cost;
+          }
+        }
+        // ---- its next tiles, a lane each
+        int m = min(kSegTiles, left);
+        Tile d{0, 0, 0, -1};
+        if (m > 0) {
+          int seq = node_b;
+          d.tile = t_first + done + lane;
+          if (bundle) {
+            const int places = min(nb, B - seg.first);
+#pragma unroll 1
+            while (skip + done >= before + window && w0 + 32 < places) {  // on to the window of 32 places that has them
+              before += window;
+              w0 += 32;
+              b = t0 = count = len = 0;
+              if (w0 + lane < places) {
+                const Node x = node_of(p, plan, seg.first + w0 + lane);
+                b = place_of(plan, seg.first + w0 + lane, B);
+                len = length_of(p, b);
+                t0 = x.t0;
+                count = x.t1 - x.t0;
+              }
+              sum = count;
+#pragma unroll 1
+              for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+              }
+              window = __shfl_sync(0xffffffffu, sum, 31);
+            }
+            const int want = skip + done - before;  // of the window's
+            m = max(0, min(m, window - want));
+            if (m == 0) left = 0;  // (lengths that changed under the call)
+            // the place of tile want + lane: the first whose sum is above it
+            const int x = min(want + lane, window - 1);
+            int q = 0;
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1)
+              if (__shfl_sync(0xffffffffu, sum, q + o - 1) <= x) q += o;
+            seq = __shfl_sync(0xffffffffu, b, q);
+            d.tile = __shfl_sync(0xffffffffu, t0, q) + x -
+                     (__shfl_sync(0xffffffffu, sum, q) - __shfl_sync(0xffffffffu, count, q));
+            d.shift = static_cast<short>(max(0, (d.tile + 1) * kTile - __shfl_sync(0xffffffffu, len, q)));
+            d.place = static_cast<short>(w0 + q);
+          }
+          if (lane < m) {
+            const int page = p.table[static_cast<long>(seq) * p.max_pages + d.tile];
+            d.z = page >= 0 && page < p.num_pages ? page * p.Hkv + seg.kvh : p.num_pages * p.Hkv;
+          }
+          if (m == 0) {
+            --k;
+            continue;
+          }
+        }
+        // ---- published (without tiles: the end)
+        ok = __all_sync(0xffffffffu, wait(&ctl->seg_empty[k % kSegments], ((k / kSegments) & 1) ^ 1));
+        if (!ok) break;
+        Segment& to = ctl->seg[k % kSegments];
+        if (lane < m) to.tile[lane] = d;
+        if (lane == 0) {
+          to.n = static_cast<short>(m);
+          to.odd = static_cast<short>(done & 1);
+          to.start = done == 0;
+          to.end = m == left;
+          to.kvh = seg.kvh;
+          to.first = seg.first;
+          to.row0 = seg.row0;
+          to.rows = seg.rows;
+          to.both = seg.both;
+          to.out = seg.out;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->seg_full[k % kSegments]);
+        if (m == 0) break;
+        done += m;
+        left -= m;
+        if (left == 0 && bundle) skip += done;
+      }
     }
     if (warp == kWarpLoad && lane == 0 && *abort_flag) {
       // let the copies in flight land before shared memory is released
       const int n = *reinterpret_cast<volatile int*>(&ctl->n_issued);
+#pragma unroll 1
       for (int s = 0; s < NR; ++s)
         if (n > s) mbar_wait(&ctl->r_full[s], ((n - 1 - s) / NR) & 1, nullptr);
     }
@@ -447,180 +652,185 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------- softmax of stream t
     setmaxnreg_inc<kRegsSoftmax>();
-    const int t = warp >> 2, row = tid & 127;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int t = warp >> 2, row = tid & 127, w0 = (warp & 3) * 32;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(w0) << 16);
     const uint32_t colS = lane_base + C::kColS + 128 * t, colO = lane_base + C::kColO + 128 * t;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f32x2(sl2, sl2);
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
-    };
-    // Rows of this stream of piece x: [first, first + count) of the node's.
-    auto my_rows = [&](const Piece& x, int* first) -> int {
-      const bool both = x.both != 0;
-      const int half = (x.rows + 1) / 2;
-      *first = x.row0 + (both && t == 1 ? half : 0);
-      return !both ? x.rows : t == 0 ? half : x.rows - half;
-    };
-    auto steps_of = [&](const Piece& x) { return x.both ? x.n : (x.n + 1 - t) / 2; };
-    // Row i of the stream: 16-byte word j at j ^ (i & 7) of its 128-byte rows.
-    auto load_q = [&](const Piece& x) {
-      int first;
-      const int n = my_rows(x, &first);
-      constexpr int W = D / 8, RS = 128 / W;  // words of a row, rows a pass
-      const int j = row % W;
-      uint8_t* to = sQ + t * C::kTileBytes + (j >> 3) * 16384;
-      for (int i0 = 0; i0 < n; i0 += 8 * RS) {
-        uint4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * RS + row / W;
-          if (i < n) {
-            const int r = first + i, place = r / p.G;
-            const int b = place_of(plan, x.first + place, p.B);
-            v[u] = *reinterpret_cast<const uint4*>(
-                p.q + b * p.q_stride + static_cast<long>(x.kvh * p.G + (r - place * p.G)) * D + j * 8);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * RS + row / W;
-          if (i < n) *reinterpret_cast<uint4*>(to + i * 128 + (((j & 7) ^ (i & 7)) << 4)) = v[u];
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->q_full[t]);
-    };
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    auto place_row = [&](int r) { return p.inv_g != 0 ? static_cast<int>(__umulhi(r, p.inv_g)) : r; };  // r / G
     uint32_t ns = 0, no = 0;
-    Piece x;
-    bool ok = __all_sync(0xffffffffu, piece_at(0, &x));
-    if (ok && x.n > 0 && steps_of(x) > 0) load_q(x);
-    for (int k = 0; ok && x.n > 0; ++k) {
-      const int steps = steps_of(x);
-      const bool both = x.both != 0;
-      int first;
-      const int n_rows = my_rows(x, &first);
-      const bool mine = row < n_rows, warp_live = (warp & 3) * 32 < n_rows;
-      float* dump = nullptr;  // this row's scores in the workspace
-      if (p.scores != nullptr && mine) {
-        const int r = first + row, place = r / p.G, b = place_of(plan, x.first + place, p.B);
-        dump = p.scores + (static_cast<size_t>(b) * p.Hq + x.kvh * p.G + (r - place * p.G)) * p.max_pages * kTile;
-      }
-      float m = -INFINITY, m_used = -INFINITY, l = 0.f;
-      for (int i = 0; i < steps; ++i) {
-        if (!wwait(&ctl->s_full[t], ns & 1)) {
-          ok = false;
-          break;
-        }
-        ++ns;
-        if (warp_live) {
-          tc_fence_after();
-          const int tile = x.t0 + (both ? i : 2 * i + t);
-          uint32_t sr[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32p(colS + 32 * c, sr + 32 * c);
-          tmem_wait_ld();
-          if (dump != nullptr) {
-            float4* to = reinterpret_cast<float4*>(dump + static_cast<size_t>(tile) * kTile);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              to[c] = make_float4(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1]),
-                                  __uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3]));
-          }
-          if (tile == x.last) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e < x.shift) sr[e] = __float_as_uint(-INFINITY);
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-          m = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          float alpha = 1.f;
-          bool rescale = false;
-          if (m_used == -INFINITY) {
-            m_used = m;  // the row's first keys
-          } else if ((m - m_used) * sl2 > kRescaleLog2) {
-            alpha = ex2_approx((m_used - m) * sl2);
-            m_used = m;
-            l *= alpha;
-            rescale = true;
-          }
-          if (__any_sync(0xffffffffu, rescale) && i > 0) {
-            // (the scores' commit covers P.V of the stream's step before)
+    int k = 0;
+    bool ok = wwait(&ctl->seg_full[0], 0);
+    // What the piece before left to be written.
+    bool any = false, mine = false, warp_live = false;
+    float m_used = -INFINITY, l = 0.f;
+    long long out = -1;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t orr[32];
-              tmem_ld32p(colO + c * 32, orr);
-              tmem_wait_ld();
+    for (bool open = false; ok; open = true) {
+      const Segment* x = &ctl->seg[k % kSegments];
+      const int n_first = x->n, both = x->both, rows = x->rows, kvh = x->kvh, place0 = x->first, row0 = x->row0;
+      const int half = (rows + 1) / 2, skip = both && t == 1 ? half : 0;  // this stream's first row among the item's
+      const int n_rows = !both ? rows : t == 0 ? half : rows - half;
+      // The stream's score MMAs of the piece before are done, its Q tile is free: 16-byte
+      // word j of row i goes to word j ^ (i & 7) of its 128-byte rows.
+      if (n_first > 0 && (t == 0 || both || n_first > 1 || !x->end)) {
+        constexpr int W = D / 8, RS = 128 / W;  // words of a row, rows a pass
+        const int j = row % W;
+        uint8_t* to = sQ + t * C::kTileBytes + (j >> 3) * 16384;
+#pragma unroll 1
+        for (int i0 = row / W; i0 < n_rows; i0 += 4 * RS) {
+          uint4 v[4];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-              tmem_st32p(colO + c * 32, orr);
+          for (int u = 0; u < 4; ++u) {
+            const int r = row0 + skip + min(i0 + u * RS, n_rows - 1), place = place_row(r);
+            v[u] = *reinterpret_cast<const uint4*>(p.q + place_of(plan, place0 + place, B) * p.q_stride +
+                                                   static_cast<long>(kvh * G + (r - place * G)) * D + j * 8);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * RS;
+            if (i < n_rows) *reinterpret_cast<uint4*>(to + i * 128 + (((j & 7) ^ (i & 7)) << 4)) = v[u];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->q_full[t]);
+      }
+      if (open) {  // the piece before: its rows' results
+        if (any) {
+          if (!(ok = wwait(&ctl->o_full[t], no & 1))) break;
+          ++no;
+        }
+        if (warp_live && out >= 0) {
+          const bool some = mine && !(m_used == -INFINITY && l == 0.f);  // (a row of NaN has a sum of NaN)
+          if (any) {
+            tc_fence_after();
+            float* to = p.part_o + out * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t orr[32];
+              tmem_ld32p(colO + c, orr);
+              tmem_wait_ld();
+              if (some)
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) store8(to + c + e, orr + e);
             }
           }
-          // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of
-          // a weight); l adds up the unrounded ones.
-          const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
-          const uint64_t nmb = f32x2(-mb, -mb);
-          uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const uint64_t xp =
-                fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
-            const float p0 = ex2_approx(f32x2_lo(xp)), p1 = ex2_approx(f32x2_hi(xp));
-            ls[c & 1] = add_f32x2(ls[c & 1], f32x2(p0, p1));
-            sr[c] = pack_bf16x2(p0, p1);
-          }
-          tmem_st32p(colS, sr);
-          tmem_st32p(colS + 32, sr + 32);
-          tmem_wait_st();
-          const uint64_t lsum = add_f32x2(ls[0], ls[1]);
-          l += f32x2_lo(lsum) + f32x2_hi(lsum);
+          if (mine) p.part_ml[out] = make_float2(m_used == -INFINITY ? -INFINITY : m_used * sl2, l);
+        }
+        if (any) {
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->o_free[t]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[t]);
       }
-      if (!ok) break;
-      // The stream's score MMAs are done: its Q tile is free for the next piece.
-      Piece y;
-      ok = __all_sync(0xffffffffu, piece_at(k + 1, &y));
-      if (!ok) break;
-      if (y.n > 0 && steps_of(y) > 0) load_q(y);
-      if (steps > 0) {
-        ok = wwait(&ctl->o_full[t], no & 1);
-        ++no;
-        if (!ok) break;
-      }
-      if (warp_live && x.out >= 0) {
-        const long long at = x.out + (first - x.row0) + row + (!both && t == 1 ? x.rows : 0);
-        if (steps > 0) {
-          tc_fence_after();
-          float4* to = reinterpret_cast<float4*>(p.part_o + at * D);
+      if (n_first == 0) break;
+      mine = row < n_rows;
+      warp_live = w0 < n_rows;
+      out = x->out;
+      if (out >= 0) out += skip + row + (!both && t == 1 ? rows : 0);
+      const int my_row = row0 + skip + row, my_place = place_row(my_row);
+      float* dump = nullptr;  // this row's scores in the workspace
+      if (p.scores != nullptr && mine)
+        dump = p.scores + (static_cast<size_t>(place_of(plan, place0 + my_place, B)) * p.Hq + kvh * G +
+                           (my_row - my_place * G)) * p.max_pages * kTile;
+      float m = -INFINITY;
+      m_used = -INFINITY;
+      l = 0.f;
+      any = false;  // the stream has had a tile
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t orr[32];
-            tmem_ld32p(colO + c * 32, orr);
-            tmem_wait_ld();
-            if (mine)
+      for (bool last = false; !last;) {
+        x = &ctl->seg[k % kSegments];
+        const int n = x->n;
+        last = x->end != 0;
+#pragma unroll 1
+        for (int i = both ? 0 : (t + x->odd) & 1; i < n; i += both ? 1 : 2) {
+          if (!(ok = wwait(&ctl->s_full[t], ns & 1))) break;
+          ++ns;
+          const Tile d = x->tile[i];
+          // A bundle's tile counts for the rows of one sequence.
+          const bool counts = mine && (d.place < 0 || d.place == my_place);
+          if (warp_live) {
+            uint32_t sr[128];
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, counts)) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                to[c * 8 + e] = make_float4(__uint_as_float(orr[4 * e]), __uint_as_float(orr[4 * e + 1]),
-                                            __uint_as_float(orr[4 * e + 2]), __uint_as_float(orr[4 * e + 3]));
+              for (int c = 0; c < 4; ++c) tmem_ld32p(colS + 32 * c, sr + 32 * c);
+              tmem_wait_ld();
+              if (dump != nullptr && counts) {
+                float* to = dump + static_cast<size_t>(d.tile) * kTile;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) store8(to + 8 * c, sr + 8 * c);
+              }
+              if (d.shift > 0) {  // columns without a key
+#pragma unroll
+                for (int e = 0; e < 128; ++e)
+                  if (e < d.shift) sr[e] = __float_as_uint(-INFINITY);
+              }
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+              if (counts) m = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+              float alpha = 1.f;
+              bool rescale = false;
+              if (m_used == -INFINITY) {
+                m_used = m;  // the row's first keys
+              } else if ((m - m_used) * sl2 > kRescaleLog2) {
+                alpha = ex2_approx((m_used - m) * sl2);
+                m_used = m;
+                l *= alpha;
+                rescale = true;
+              }
+              if (__any_sync(0xffffffffu, rescale) && any) {
+                // (the scores' commit covers P.V of the stream's step before)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t orr[16];
+                  tmem_ld16p(colO + c, orr);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                  tmem_st16(colO + c, orr);
+                }
+              }
+              // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of
+              // a weight); l adds up the unrounded ones.  (Exponentials with the
+              // maximum before the tile, formed anew where that was too low, were
+              // slower: 107 instead of 88 us on 1024 rows over 32K keys.)
+              const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
+              const uint64_t nmb = f32x2(-mb, -mb);
+              uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+              for (int c = 0; c < 64; ++c) {
+                const uint64_t xp =
+                    fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
+                const float p0 = ex2_approx(f32x2_lo(xp)), p1 = ex2_approx(f32x2_hi(xp));
+                ls[c & 1] = add_f32x2(ls[c & 1], f32x2(p0, p1));
+                sr[c] = pack_bf16x2(p0, p1);
+              }
+              const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+              if (counts) l += f32x2_lo(lsum) + f32x2_hi(lsum);
+            }
+            if (d.place >= 0) {  // rows of the bundle's other sequences: their weights are 0
+#pragma unroll
+              for (int c = 0; c < 64; ++c) sr[c] = counts ? sr[c] : 0u;
+            }
+            tmem_st32p(colS, sr);
+            tmem_st32p(colS + 32, sr + 32);
+            tmem_wait_st();
+            tc_fence_before();
           }
+          any = true;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->p_full[t]);
         }
-        if (mine) p.part_ml[at] = make_float2(m_used == -INFINITY ? -INFINITY : m_used * sl2, l);
-      }
-      if (steps > 0) {
-        tc_fence_before();
+        if (!ok || !(ok = wwait(&ctl->seg_full[(k + 1) % kSegments], ((k + 1) / kSegments) & 1))) break;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->o_free[t]);
+        if (lane == 0) seg_done(k);
+        ++k;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
-      x = y;
     }
     __syncwarp();
     tc_fence_before();
@@ -629,103 +839,124 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The partial results of a row: along its place's node and those above it, the
-// pieces that their items were cut into.  One block a (place, head); a warp
-// takes every fourth result.
+// The partial results of a row: those of its own tiles and of the nodes above its
+// place, whose items were cut into pieces.  One block a (place, head): eight lanes
+// find the pieces (a level each), then a thread a piece has its weight, then a
+// thread a column adds up.
 template <int D>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p, int ctas) {
-  __shared__ float s_m[4], s_l[4];
-  __shared__ float s_o[4][D];
+  constexpr int L = 1 + kPlanLevels;
+  __shared__ long long s_row[L];              // a level's first partial row, of its first CTA
+  __shared__ int s_second[L], s_start[L + 1]; // the second stream's distance (0: one result a piece), results in front
+  __shared__ float s_w[128], s_red[2][4], s_o[128];
+  __shared__ long long s_at[128];
   const int32_t* plan = valid_plan(p);
   const int i = blockIdx.x / p.Hq, h = blockIdx.x - i * p.Hq;
   const int kvh = h / p.G, g = h - kvh * p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = place_of(plan, i, p.B);
-  const int nodes = plan != nullptr ? 2 * p.B : p.B;
-  // all tiles, as the attention kernel counted them
-  const Node end = node_of(p, plan, nodes - 1);
-  const long long total =
-      p.node_at[nodes - 1] + static_cast<long long>(end.t1 - end.t0) * deal_of(end, p.G).blocks * p.Hkv;
-  const long long per = max(1ll, (total + ctas - 1) / ctas);
-  constexpr int E = D / 32;  // entries of O a lane has
-  float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (length_of(p, b) > 0) {
-    int n = i;
-    for (int level = 0; n >= 0 && n < nodes && level <= kPlanLevels; ++level) {
-      const Node x = node_of(p, plan, n);
-      const int T = x.t1 - x.t0, r = (i - x.first) * p.G + g;
-      if (T > 0 && r >= 0 && r < x.count * p.G) {
-        const Deal d = deal_of(x, p.G);
-        const int blk = r / d.rows, rr = r - blk * d.rows;
-        const bool both = d.rows > kTile;
-        const int item = kvh * d.blocks + blk;
-        const long long a = p.node_at[n] + static_cast<long long>(item) * T;
-        const long long row = p.node_rows[n] + static_cast<long long>(item) * d.part + rr;
-        const int c0 = static_cast<int>(a / per), c1 = static_cast<int>((a + T - 1) / per);
-        const int parts = (c1 - c0 + 1) * (both ? 1 : 2);
-        for (int q0 = warp; q0 < parts; q0 += 128) {  // 32 results of this warp's at a time: a lane's each
-          const int q = q0 + 4 * lane;
-          long long at = -1;
-          float2 ml = make_float2(-INFINITY, 0.f);
-          if (q < parts) {
-            const int c = c0 + (both ? q : q >> 1);
-            at = row + static_cast<long long>(c) * kRows + (!both && (q & 1) ? d.rows : 0);
-            if (at >= p.part_rows) at = -1;
-            if (at >= 0) ml = p.part_ml[at];
-            if (ml.x == -INFINITY && ml.y == 0.f) at = -1;  // (a stream that had no tile)
-          }
-          float top = ml.x;
-#pragma unroll
-          for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-          const float now = fmaxf(m, top);
-          const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m - now);
-          const float w = at < 0 ? 0.f : ex2_approx(ml.x - now);
-          l *= keep;
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] *= keep;
-          l += w * ml.y;
-          m = now;
-          for (uint32_t some = __ballot_sync(0xffffffffu, at >= 0); some != 0; some &= some - 1) {
-            const int s = __ffs(some) - 1;
-            const float ws = __shfl_sync(0xffffffffu, w, s);
-            const float* from = p.part_o + __shfl_sync(0xffffffffu, at, s) * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 v = *reinterpret_cast<const float4*>(from);
-              o[0] += ws * v.x, o[1] += ws * v.y, o[2] += ws * v.z, o[3] += ws * v.w;
-            } else {
-              const float2 v = *reinterpret_cast<const float2*>(from);
-              o[0] += ws * v.x, o[1] += ws * v.y;
-            }
-          }
+  if (warp == 0) {
+    int parts = 0, second = 0;
+    long long row = 0, a = 0, z = 0;  // cost in front of the row's first tile, of its last
+    if (lane == 0) {
+      const int nb = kTile / p.G, j0 = i / nb * nb, places = min(nb, p.B - j0);
+      const int base = p.cum[j0], T = p.cum[j0 + places] - base, c0 = p.cum[i], n = p.cum[i + 1] - c0;
+      if (n > 0) {
+        a = (static_cast<long long>(base) * p.Hkv + static_cast<long long>(kvh) * T + (c0 - base)) * kTileCost;
+        z = a + static_cast<long long>(n - 1) * kTileCost;
+        row = 2ll * p.G * p.Hkv * j0 + 2ll * kvh * places * p.G + (i - j0) * p.G + g;
+        second = places * p.G;
+        parts = 1;
+      }
+    } else if (lane < L && plan != nullptr) {
+      const int n = plan[kPlanHead + p.B + 2l * p.B * kNodeWords + static_cast<long>(i) * kPlanLevels + lane - 1];
+      if (n >= p.B && n < 2 * p.B) {
+        const Node x = node_of(p, plan, n);
+        const int T = x.t1 - x.t0, r = (i - x.first) * p.G + g;
+        if (T > 0 && r >= 0 && r < x.count * p.G && length_of(p, b) > 0) {
+          const Deal d = deal_of(x, p.G);
+          const int blk = r / d.rows, item = kvh * d.blocks + blk, cost = cost_of(d);
+          a = p.node_at[n - p.B] + static_cast<long long>(item) * T * cost;
+          z = a + static_cast<long long>(T - 1) * cost;
+          row = p.node_rows[n - p.B] + static_cast<long long>(item) * d.part + (r - blk * d.rows);
+          second = d.rows > kTile ? 0 : d.rows;
+          parts = 1;
         }
       }
-      n = plan != nullptr ? plan[kPlanHead + p.B + static_cast<long>(n) * kNodeWords + 4] : -1;
+    }
+    if (parts > 0) {
+      const long long per = share_of(*p.total, ctas);
+      const int c0 = static_cast<int>(quotient(a, per)), c1 = static_cast<int>(quotient(z, per));
+      row += static_cast<long long>(c0) * kRows;
+      parts = min(ctas, c1 - c0 + 1) * (second > 0 ? 2 : 1);
+    }
+    int sum = parts;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane < L) {
+      s_row[lane] = row;
+      s_second[lane] = second;
+      s_start[lane] = sum - parts;
+      if (lane == L - 1) s_start[L] = sum;
     }
   }
-  // (each lane has added up its own results' sums)
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
   __syncthreads();
-  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), sum = 0.f, w[4];
+  const int all = s_start[L];
+  constexpr int R = 128 / D;  // threads a column
+  const int column = tid % D;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int q0 = 0; q0 < all; q0 += 128) {
+    const int q = q0 + tid;
+    long long at = -1;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (q < all) {
+      int v = 0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    w[q] = s_m[q] == -INFINITY ? (s_l[q] == 0.f ? 0.f : 1.f) : ex2_approx(s_m[q] - top);
-    sum += w[q] * s_l[q];
-  }
-  const size_t at = static_cast<size_t>(b) * p.Hq + h;
-  if (threadIdx.x < D) {
-    float v = 0.f;
+      for (int k = 1; k < L; ++k) v += q >= s_start[k];
+      const int x = q - s_start[v], second = s_second[v];
+      at = s_row[v] + static_cast<long long>(second > 0 ? x >> 1 : x) * kRows + (second > 0 && (x & 1) ? second : 0);
+      if (at >= p.part_rows) at = -1;
+      if (at >= 0) ml = p.part_ml[at];
+      if (ml.x == -INFINITY && ml.y == 0.f) at = -1;  // (a stream that had no tile of the row's)
+    }
+    float top = ml.x;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v += w[q] * s_o[q][threadIdx.x];
-    // (a sequence without keys: zeros; NaN stays)
-    p.o[at * D + threadIdx.x] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    if (lane == 0) s_red[0][warp] = top;
+    __syncthreads();
+    const float now = fmaxf(m, fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3])));
+    // (a row of NaN has no maximum and a sum of NaN)
+    const float w = at < 0 ? 0.f : ex2_approx(ml.x - now), keep = m == -INFINITY ? 1.f : ex2_approx(m - now);
+    float sum = at < 0 ? 0.f : w * ml.y;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (lane == 0) s_red[1][warp] = sum;
+    s_w[tid] = w;
+    s_at[tid] = at;
+    __syncthreads();
+    l = l * keep + ((s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]));
+    o *= keep;
+    m = now;
+    const int n = min(128, all - q0);
+#pragma unroll 8
+    for (int k = tid / D; k < n; k += R) {
+      const long long from = s_at[k];
+      if (from >= 0) o += s_w[k] * p.part_o[from * D + column];
+    }
+    __syncthreads();
   }
-  if (p.lse != nullptr && threadIdx.x == 0) p.lse[at] = top + log2f(sum);
+  if (R > 1) {
+    s_o[tid] = o;
+    __syncthreads();
+    o = s_o[column] + s_o[(column + D) % 128];
+  }
+  const size_t to = static_cast<size_t>(b) * p.Hq + h;
+  // (a sequence without keys: zeros; NaN stays)
+  if (tid < D) p.o[to * D + column] = __float2bfloat16(l == 0.f ? 0.f : o / l);
+  if (p.lse != nullptr && tid == 0) p.lse[to] = m + log2f(l);
 }
 
 // weights[b][kvh][key] += sum over the group's heads of exp2(s * scale * log2e - lse).
@@ -779,7 +1010,7 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Share
   return cudaGetLastError();
 }
 
-constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+constexpr size_t up128(size_t n) { return (n + 127) / 128 * 128; }
 
 }  // namespace
 
@@ -800,16 +1031,18 @@ SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
-    at += up16(n);
+    at += up128(n);
     return here;
   };
   s.part_o = take(static_cast<size_t>(s.part_rows) * d * sizeof(float));
   s.part_ml = take(static_cast<size_t>(s.part_rows) * sizeof(float2));
-  s.node_at = take(2 * static_cast<size_t>(B) * sizeof(long long));
-  s.node_rows = take(2 * static_cast<size_t>(B) * sizeof(long long));
+  s.total = take(sizeof(long long));
+  s.cum = take((static_cast<size_t>(B) + 1) * sizeof(int));
+  s.node_at = take(plan ? static_cast<size_t>(B) * sizeof(long long) : 0);
+  s.node_rows = take(plan ? static_cast<size_t>(B) * sizeof(long long) : 0);
   s.lse = weights ? take(static_cast<size_t>(B) * Hq * sizeof(float)) : 0;
   s.scores = weights ? take(static_cast<size_t>(B) * Hq * max_pages * kTile * sizeof(float)) : 0;
-  s.bytes = at;
+  s.bytes = at + 128;  // (the workspace may begin anywhere on a 16-byte boundary)
   return s;
 }
 
