@@ -737,7 +737,8 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   if (static_cast<long>(max_pages) * kTile > 0x7fffffffL || static_cast<long>(num_pages + 1L) * Hkv > 0x7fffffffL ||
       static_cast<long>(B) * Hq > 0x3fffffffL || stride >= (1LL << 38))
     return SS_ERR_INVALID_ARG;
-  if (B > (plan != nullptr ? kPlanMaxB : kSharedMaxB) || Hkv > 65535 || static_cast<long>(B) * max_pages > 0x7fffffffL)
+  if (B > (plan != nullptr ? kPlanMaxB : kSharedMaxB) || Hkv > 65535 ||
+      static_cast<__int128>(B) * max_pages * Hkv > (plan != nullptr ? kMaxPlannedTiles : kMaxSharedTiles))
     return SS_ERR_UNSUPPORTED;
   if (static_cast<__int128>(B) * Hq * max_pages > kMaxCells) return SS_ERR_INVALID_ARG;
   const SharedSpace space = shared_space(B, Hq, Hkv, max_pages, d, plan != nullptr, weights != nullptr);
@@ -777,9 +778,9 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   p.part_o = reinterpret_cast<float*>(ws + space.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);
   p.part_rows = space.part_rows;
-  p.total = reinterpret_cast<long long*>(ws + space.total);
-  p.cum = reinterpret_cast<int*>(ws + space.cum);
-  p.node_at = reinterpret_cast<long long*>(ws + space.node_at);
+  p.total = reinterpret_cast<uint32_t*>(ws + space.total);
+  p.cum = reinterpret_cast<uint32_t*>(ws + space.cum);
+  p.node_at = reinterpret_cast<uint32_t*>(ws + space.node_at);
   p.node_rows = reinterpret_cast<long long*>(ws + space.node_rows);
   if (weights != nullptr) {
     p.lse = reinterpret_cast<float*>(ws + space.lse);

@@ -42,15 +42,19 @@ struct SharedParams {
   float* part_o;           // [part_rows][d] unnormalised partial outputs
   float2* part_ml;         // [part_rows] (reference maximum in exp2 units, sum)
   long part_rows;
-  long long* total;        // all items' cost
-  int* cum;                // [B + 1] own tiles of the places below
-  long long* node_at;      // [B] cost of the items in front of a shared node
+  uint32_t* total;         // all items' cost
+  uint32_t* cum;           // [B + 1] own tiles of the places below
+  uint32_t* node_at;       // [B] cost of the items in front of a shared node
   long long* node_rows;    // [B] its first partial row
   float* lse;              // [B][Hq] log2 of the softmax's denominator (weights only)
   float* scores;           // [B][Hq][max_pages][128] (weights only)
   float* weights;          // [B][Hkv][max_pages * 128], nullable
   uint32_t* status;
 };
+
+// Tiles over all sequences and KV heads that a table may have room for: their cost (3 a tile, and as much
+// again for each level of shared nodes at most) is counted in 31 bits.
+constexpr long kMaxSharedTiles = 1l << 29, kMaxPlannedTiles = 1l << 26;
 
 // Workspace: sizes and where its arrays lie.
 struct SharedSpace {

@@ -78,8 +78,8 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
   // The sums over the batch are made where the tiles come later: a place's tiles
-  // (4 bytes), a shared node's tiles and rows (16 bytes).
-  static_assert(4 * (kSharedMaxB + 2) <= kCtlOff && 4 * (kPlanMaxB + 2) + 16 * kPlanMaxB <= kCtlOff, "sums");
+  // (4 bytes), a shared node's cost and rows (12 bytes).
+  static_assert(4 * (kSharedMaxB + 2) <= kCtlOff && 8 * (kPlanMaxB + 1) + 8 * kPlanMaxB <= kCtlOff, "sums");
 };
 
 // Eight floats at once (32 bytes, a whole sector of a line), 32-byte aligned.
@@ -123,7 +123,7 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   int n_issued;
-  long long leaf_total, total;  // cost of all bundles, of all items
+  uint32_t leaf_total, total;  // cost of all bundles, of all items
   Segment seg[kSegments];
 };
 
@@ -180,43 +180,42 @@ __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
 constexpr int kTileCost = 2, kBothCost = 3;
 __device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : kTileCost; }
 // A CTA's share of all items' cost (at least a tile, so that each CTA between an item's
-// first and last has a part of it).
-__device__ __forceinline__ long long share_of(long long total, int ctas) {
-  return max(static_cast<long long>(kBothCost), (total + ctas - 1) / ctas);
-}
-// a / b for non-negative numbers, which hardly ever need 64 bits.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+// first and last has a part of it).  Costs fit 31 bits (kMaxSharedTiles).
+__device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t ctas) {
+  return max(static_cast<uint32_t>(kBothCost), (total + ctas - 1) / ctas);
 }
 
-// Exclusive sums over the block's threads of three values, in place; the totals in t.
-__device__ void block_sums(long long (&v)[3], long long (&t)[3], long long* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int W = kThreads / 32;
-  long long mine[3];
+// What the places below a place have: own tiles, cost and partial rows of their shared nodes.
+struct Sums {
+  uint32_t tiles, cost;
+  long long rows;
+  __device__ __forceinline__ void add(const Sums& x) { tiles += x.tiles, cost += x.cost, rows += x.rows; }
+};
+// Exclusive sums over the block's first `used` threads, in place; returns the total.
+__device__ Sums block_sums(Sums& v, int used, bool nodes, Sums* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (used + 31) / 32;
+  const Sums mine = v;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    mine[k] = v[k];
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, v[k], o);
-      if (lane >= o) v[k] += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    Sums x{__shfl_up_sync(0xffffffffu, v.tiles, o), 0, 0};
+    if (nodes) {
+      x.cost = __shfl_up_sync(0xffffffffu, v.cost, o);
+      x.rows = __shfl_up_sync(0xffffffffu, v.rows, o);
     }
-    if (lane == 31) scratch[k * W + warp] = v[k];
-    t[k] = 0;
-    v[k] -= mine[k];
+    if (lane >= o) v.add(x);
+  }
+  if (lane == 31 && warp < warps) scratch[warp] = v;
+  __syncthreads();
+  v.tiles -= mine.tiles, v.cost -= mine.cost, v.rows -= mine.rows;
+  Sums all{0, 0, 0};
+#pragma unroll 1
+  for (int w = 0; w < warps; ++w) {
+    const Sums x = scratch[w];
+    if (w < warp) v.add(x);
+    all.add(x);
   }
   __syncthreads();
-#pragma unroll 1
-  for (int w = 0; w < W; ++w) {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const long long x = scratch[k * W + w];
-      if (w < warp) v[k] += x;
-      t[k] += x;
-    }
-  }
-  __syncthreads();
+  return all;
 }
 
 // (A launch's code comes out of L2 line by line: waits, divisions and the parts of a
@@ -271,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Sums over the batch, in the shared memory that the tiles take later: the own
   // tiles of the places below each, the cost and partial rows of the shared nodes
   // below each.
-  int* cum = reinterpret_cast<int*>(smem);                                              // [B + 1]
-  long long* node_at = reinterpret_cast<long long*>(smem + (4 * (B + 1) + 7) / 8 * 8);  // [nodes]
-  long long* node_rows = node_at + nodes;                                               // [nodes]
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem);                                     // [B + 1]
+  uint32_t* node_at = cum + B + 1;                                                       // [nodes]
+  long long* node_rows = reinterpret_cast<long long*>(smem + (4 * (2 * B + 1) + 7) / 8 * 8);  // [nodes]
   {
     const int each = (B + kThreads - 1) / kThreads, n0 = min(B, tid * each), n1 = min(B, n0 + each);
-    long long v[3] = {0, 0, 0}, t[3] = {0, 0, 0};
+    Sums v{0, 0, 0}, all{0, 0, 0};
     // twice: adding up, then (with what lies below) writing
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -284,15 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = n0; n < n1; ++n) {
         const Node x = node_of(p, plan, n);
         if (pass == 1) {
-          cum[n] = static_cast<int>(v[0]);
-          if (blockIdx.x == 0) p.cum[n] = static_cast<int>(v[0]);
+          cum[n] = v.tiles;
+          if (blockIdx.x == 0) p.cum[n] = v.tiles;
         }
-        v[0] += x.t1 - x.t0;
+        v.tiles += x.t1 - x.t0;
         if (plan != nullptr) {
           const Node y = node_of(p, plan, B + n);
           const Deal d = deal_of(y, G);
           if (pass == 1) {
-            const long long at = t[0] * p.Hkv * kTileCost + v[1], row = 2ll * p.Hq * B + v[2];
+            const uint32_t at = all.tiles * p.Hkv * kTileCost + v.cost;
+            const long long row = 2ll * p.Hq * B + v.rows;
             node_at[n] = at;
             node_rows[n] = row;
             if (blockIdx.x == 0) {
@@ -300,18 +300,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.node_rows[n] = row;
             }
           }
-          v[1] += static_cast<long long>(y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
-          v[2] += static_cast<long long>(d.blocks) * p.Hkv * d.part * (y.t1 > y.t0);
+          if (y.t1 > y.t0) {
+            v.cost += (y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
+            v.rows += static_cast<long long>(d.blocks) * p.Hkv * d.part;
+          }
         }
       }
-      if (pass == 0) block_sums(v, t, reinterpret_cast<long long*>(ctl->seg));
+      if (pass == 0) all = block_sums(v, (B + each - 1) / each, plan != nullptr, reinterpret_cast<Sums*>(ctl->seg));
     }
     if (tid == 0) {
-      cum[B] = static_cast<int>(t[0]);
-      ctl->leaf_total = t[0] * p.Hkv * kTileCost;
-      ctl->total = ctl->leaf_total + t[1];
+      cum[B] = all.tiles;
+      ctl->leaf_total = all.tiles * p.Hkv * kTileCost;
+      ctl->total = ctl->leaf_total + all.cost;
       if (blockIdx.x == 0) {
-        p.cum[B] = static_cast<int>(t[0]);
+        p.cum[B] = all.tiles;
         *p.total = ctl->total;
       }
     }
@@ -453,30 +455,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpPlan) {
       // ---------------------------------------------------------- pieces
       // A tile belongs to the CTA whose share its cost begins in.
-      const long long leaf_total = ctl->leaf_total, total = ctl->total, per = share_of(total, gridDim.x);
-      long long at = per * blockIdx.x;
-      const long long end = min(at + per, total);
+      const uint32_t leaf_total = ctl->leaf_total, total = ctl->total, per = share_of(total, gridDim.x);
+      uint32_t at = min(total, per * blockIdx.x);
+      const uint32_t end = min(at + per, total);
       // Where the share begins: in a bundle ..
       int j = 0, kvh = 0, base = 0, T = 0, skip = 0;  // bundle, head, its first place's sum, its tiles, those in front
       int n = 0;                                      // .. or a shared node
-      long long n_at = 0, n_rows = 0;
+      uint32_t n_at = 0;
+      long long n_rows = 0;
       if (at < end) {
         const bool leaf = at < leaf_total;
         int lo = 0, hi = leaf ? (B + nb - 1) / nb : nodes;
 #pragma unroll 1
         while (hi - lo > 1) {  // the last one that begins at or below `at` (an empty one: the next begins there too)
           const int mid = (lo + hi) / 2;
-          if ((leaf ? static_cast<long long>(cum[mid * nb]) * p.Hkv * kTileCost : node_at[mid]) <= at) lo = mid; else hi = mid;
+          if ((leaf ? cum[mid * nb] * p.Hkv * kTileCost : node_at[mid]) <= at) lo = mid; else hi = mid;
         }
         if (leaf) {
           j = lo;
           base = cum[j * nb];
           T = cum[min(B, (j + 1) * nb)] - base;
-          const long long begin = static_cast<long long>(base) * p.Hkv * kTileCost;
-          const long long in = (at - begin + kTileCost - 1) / kTileCost;
+          const uint32_t begin = base * p.Hkv * kTileCost, in = (at - begin + kTileCost - 1) / kTileCost;
           at = begin + in * kTileCost;
-          kvh = min(p.Hkv - 1, static_cast<int>(quotient(in, T)));
-          skip = static_cast<int>(in - static_cast<long long>(kvh) * T);
+          kvh = min(p.Hkv - 1, static_cast<int>(in / T));
+          skip = in - kvh * T;
         } else {
           n = lo;
         }
@@ -523,15 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             seg.both = 0;
             seg.out = 2ll * G * p.Hkv * first + 2ll * kvh * rows + static_cast<long long>(blockIdx.x) * kRows;
             if (seg.out + 2 * rows > p.part_rows) seg.out = -1;
-            left = static_cast<int>(min(static_cast<long long>(T - skip), (end - at + kTileCost - 1) / kTileCost));
-            at += static_cast<long long>(left) * kTileCost;
+            left = min(T - skip, static_cast<int>((end - at + kTileCost - 1) / kTileCost));
+            at += left * kTileCost;
             w0 = -32, before = window = 0;
           } else {
             const Node x = node_of(p, plan, B + n);
             const Deal d = deal_of(x, G);
-            const int Tn = x.t1 - x.t0, cost = cost_of(d);
-            const long long all = static_cast<long long>(Tn) * d.blocks * p.Hkv;
-            const long long in = quotient(max(0ll, at - n_at) + cost - 1, cost);
+            const uint32_t Tn = x.t1 - x.t0, cost = cost_of(d), all = Tn * d.blocks * p.Hkv;
+            const uint32_t in = ((at > n_at ? at - n_at : 0u) + cost - 1) / cost;
             if (in >= all) {
               n_at += all * cost;
               at = max(at, n_at);
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             at = n_at + in * cost;
             if (at >= end) break;
-            const int item = static_cast<int>(quotient(in, Tn)), u = static_cast<int>(in - static_cast<long long>(item) * Tn);
+            const int item = in / Tn, u = in - item * Tn;
             const int head = item / d.blocks;
             bundle = false;
             seg.kvh = head;
@@ -553,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (seg.out + d.part > p.part_rows) seg.out = -1;
             t_first = x.t0 + u;
             node_b = place_of(plan, x.first, B);
-            left = static_cast<int>(min(static_cast<long long>(Tn - u), quotient(end - at + cost - 1, cost)));
-            at += static_cast<long long>(left) * cost;
+            left = min(Tn - u, (end - at + cost - 1) / cost);
+            at += left * cost;
           }
         }
         // ---- its next tiles, a lane each
@@ -679,16 +680,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = row % W;
         uint8_t* to = sQ + t * C::kTileBytes + (j >> 3) * 16384;
 #pragma unroll 1
-        for (int i0 = row / W; i0 < n_rows; i0 += 4 * RS) {
-          uint4 v[4];
+        for (int i0 = row / W; i0 < n_rows; i0 += 8 * RS) {  // (8 rows in flight)
+          uint4 v[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < 8; ++u) {
             const int r = row0 + skip + min(i0 + u * RS, n_rows - 1), place = place_row(r);
             v[u] = *reinterpret_cast<const uint4*>(p.q + place_of(plan, place0 + place, B) * p.q_stride +
                                                    static_cast<long>(kvh * G + (r - place * G)) * D + j * 8);
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < 8; ++u) {
             const int i = i0 + u * RS;
             if (i < n_rows) *reinterpret_cast<uint4*>(to + i * 128 + (((j & 7) ^ (i & 7)) << 4)) = v[u];
           }
@@ -706,15 +707,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool some = mine && !(m_used == -INFINITY && l == 0.f);  // (a row of NaN has a sum of NaN)
           if (any) {
             tc_fence_after();
-            float* to = p.part_o + out * D;
+            // 32 columns at a time: eight lanes turn their rows' eight 16-byte words around
+            // (word j of row i to lane j), so that they write whole 128-byte lines.
+            const long long first = out - (lane & 7);
+            const uint32_t live = __ballot_sync(0xffffffffu, some) >> (lane & 24);  // of the eight lanes' rows
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-              uint32_t orr[32];
-              tmem_ld32p(colO + c, orr);
+              uint32_t o[32];
+              tmem_ld32p(colO + c, o);
               tmem_wait_ld();
-              if (some)
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) store8(to + c + e, orr + e);
+              for (int h = 1; h < 8; h <<= 1) {
+                const bool upper = (lane & h) != 0;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                  if (w & h) continue;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    uint32_t &lo = o[4 * w + e], &hi = o[4 * (w | h) + e];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, h);
+                    if (upper) lo = got; else hi = got;
+                  }
+                }
+              }
+              float* to = p.part_o + first * D + c + 4 * (lane & 7);
+#pragma unroll
+              for (int w = 0; w < 8; ++w)
+                if ((live >> w) & 1u)
+                  *reinterpret_cast<uint4*>(to + w * D) = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
             }
           }
           if (mine) p.part_ml[out] = make_float2(m_used == -INFINITY ? -INFINITY : m_used * sl2, l);
@@ -846,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p, int ctas) {
   constexpr int L = 1 + kPlanLevels;
-  __shared__ long long s_row[L];              // a level's first partial row, of its first CTA
+  __shared__ long long s_row[L];               // a level's first partial row, of its first CTA
   __shared__ int s_second[L], s_start[L + 1]; // the second stream's distance (0: one result a piece), results in front
   __shared__ float s_w[128], s_red[2][4], s_o[128];
   __shared__ long long s_at[128];
@@ -857,13 +877,14 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
   const int b = place_of(plan, i, p.B);
   if (warp == 0) {
     int parts = 0, second = 0;
-    long long row = 0, a = 0, z = 0;  // cost in front of the row's first tile, of its last
+    long long row = 0;
+    uint32_t a = 0, z = 0;  // cost in front of the row's first tile, of its last
     if (lane == 0) {
       const int nb = kTile / p.G, j0 = i / nb * nb, places = min(nb, p.B - j0);
-      const int base = p.cum[j0], T = p.cum[j0 + places] - base, c0 = p.cum[i], n = p.cum[i + 1] - c0;
+      const uint32_t base = p.cum[j0], T = p.cum[j0 + places] - base, c0 = p.cum[i], n = p.cum[i + 1] - c0;
       if (n > 0) {
-        a = (static_cast<long long>(base) * p.Hkv + static_cast<long long>(kvh) * T + (c0 - base)) * kTileCost;
-        z = a + static_cast<long long>(n - 1) * kTileCost;
+        a = (base * p.Hkv + kvh * T + (c0 - base)) * kTileCost;
+        z = a + (n - 1) * kTileCost;
         row = 2ll * p.G * p.Hkv * j0 + 2ll * kvh * places * p.G + (i - j0) * p.G + g;
         second = places * p.G;
         parts = 1;
@@ -876,8 +897,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
         if (T > 0 && r >= 0 && r < x.count * p.G && length_of(p, b) > 0) {
           const Deal d = deal_of(x, p.G);
           const int blk = r / d.rows, item = kvh * d.blocks + blk, cost = cost_of(d);
-          a = p.node_at[n - p.B] + static_cast<long long>(item) * T * cost;
-          z = a + static_cast<long long>(T - 1) * cost;
+          a = p.node_at[n - p.B] + item * T * cost;
+          z = a + (T - 1) * cost;
           row = p.node_rows[n - p.B] + static_cast<long long>(item) * d.part + (r - blk * d.rows);
           second = d.rows > kTile ? 0 : d.rows;
           parts = 1;
@@ -885,8 +906,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
       }
     }
     if (parts > 0) {
-      const long long per = share_of(*p.total, ctas);
-      const int c0 = static_cast<int>(quotient(a, per)), c1 = static_cast<int>(quotient(z, per));
+      const uint32_t per = share_of(*p.total, ctas);
+      const int c0 = a / per, c1 = z / per;
       row += static_cast<long long>(c0) * kRows;
       parts = min(ctas, c1 - c0 + 1) * (second > 0 ? 2 : 1);
     }
@@ -1036,9 +1057,9 @@ SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan
   };
   s.part_o = take(static_cast<size_t>(s.part_rows) * d * sizeof(float));
   s.part_ml = take(static_cast<size_t>(s.part_rows) * sizeof(float2));
-  s.total = take(sizeof(long long));
-  s.cum = take((static_cast<size_t>(B) + 1) * sizeof(int));
-  s.node_at = take(plan ? static_cast<size_t>(B) * sizeof(long long) : 0);
+  s.total = take(sizeof(uint32_t));
+  s.cum = take((static_cast<size_t>(B) + 1) * sizeof(uint32_t));
+  s.node_at = take(plan ? static_cast<size_t>(B) * sizeof(uint32_t) : 0);
   s.node_rows = take(plan ? static_cast<size_t>(B) * sizeof(long long) : 0);
   s.lse = weights ? take(static_cast<size_t>(B) * Hq * sizeof(float)) : 0;
   s.scores = weights ? take(static_cast<size_t>(B) * Hq * max_pages * kTile * sizeof(float)) : 0;

@@ -659,7 +659,7 @@ ss_status ss_prefix_plan(const int32_t* page_table, const int32_t* seq_lens, int
  *     aligned (never 0; it does not shrink as B or max_pages grow: one of the
  *     largest sizes serves all).
  * G = Hq / Hkv <= 128, d in {64, 128}, B <= 32768 (with a plan 8192), Hkv <= 65535,
- * B * max_pages < 2^31.
+ * B * max_pages * Hkv <= 2^29 (with a plan 2^26).
  * Nothing that is written (o, weights, workspace) may overlap another argument.
  * Partial results are joined in fp32 in a fixed order: the same from run to run.
  * Returns SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE or SS_ERR_CUDA.
