@@ -28,7 +28,7 @@
 // One CTA: two streams t, each with a fixed tile, two score buffers in TMEM and
 // a reducing warpgroup.  In the rows' pass a pair whose tokens fit one block has
 // both streams take alternate tiles of keys against that block instead.
-// Warps 0-3 / 4-7 reduce, 8 loads, 9 issues MMAs, 10 works out the pieces.
+// Warps 0-3 / 4-7 reduce, 8 loads, 9 and 11 issue the MMAs of stream 0 and 1, 10 works out the pieces.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -41,9 +41,10 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10;
-constexpr int kPieces = 4;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10, kWarpMma2 = 11;
+constexpr int kPieces = 3;
 constexpr int kPair = 2 * kTile;
+constexpr float kSlackLog2 = 40.0f;  // how far exponentials may be above 1 (exp2 domain)
 constexpr int kLaunchRegs = 168, kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
 
@@ -54,8 +55,8 @@ struct Cfg {
   static constexpr int kRing = (D == 128) ? 3 : 6;  // streamed tiles
   static constexpr int kRingOff = 4 * kTileBytes;   // behind two pairs of fixed tiles
   static constexpr int kCtlOff = kRingOff + kRing * kTileBytes;
-  static constexpr int kCtlBytes = 2048;
-  static constexpr int kSmemBytes = kCtlOff + kCtlBytes + 1024;
+  static constexpr int kCtlBytes = (D == 128) ? 3072 : 4096;
+  static constexpr int kSmemBytes = kCtlOff + kCtlBytes;  // (the base is a multiple of 1024: checked)
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -169,22 +170,24 @@ struct Piece {
   long place;
 };
 
+template <int NR>
 struct Ctl {
-  uint64_t r_full[6], r_empty[6];
+  uint64_t r_full[NR], r_empty[NR];
+  uint64_t lse_empty[3][2];        // keys' pass: stream t has used the entry's lse
   uint64_t f_full[2], f_empty[2];
   uint64_t s_full[4], s_empty[4];  // [stream * 2 + buffer]
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t hand_full, hand_empty;
-  uint64_t mma_done;
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort_flag;
   int r_issued, f_issued;
   int b;              // this CTA's share begins in sequence b,
   long long at;       // whose first step is number `at` of all
   long long total;
-  long long scan[kThreads / 32];
   Piece piece[kPieces];
-  float2 hand[kTile];  // rows' pass, alternate tiles: stream 1's results
+  alignas(16) float lse[3][kTile];  // keys' pass: the rows' lse, per ring entry % 3
+  float2 hand[kTile];   // alternate tiles: stream 1's results (before: the warps' sums over the batch)
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
@@ -202,24 +205,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const KeyWeightsParams p) {
   using C = Cfg<D>;
   constexpr int NR = C::kRing;
-  static_assert(sizeof(Ctl) <= C::kCtlBytes, "control block overflow");
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  static_assert(sizeof(Ctl<NR>) <= C::kCtlBytes, "control block overflow");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023) != 0) {  // (no static shared memory in front of it)
+    if (threadIdx.x == 0) report_timeout(p.status);
+    return;
+  }
   uint8_t* sF = smem;
   uint8_t* sR = smem + C::kRingOff;
-  auto* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
+  auto* ctl = reinterpret_cast<Ctl<NR>*>(smem + C::kCtlOff);
   volatile int* abort_flag = &ctl->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&ctl->r_full[s], 1);
-      mbar_init(&ctl->r_empty[s], 1);
+      mbar_init(&ctl->r_empty[s], 2);  // both issuers
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->f_full[s], 1);
-      mbar_init(&ctl->f_empty[s], 1);
+      mbar_init(&ctl->f_empty[s], 2);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl->s_full[s], 1);
@@ -227,11 +232,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kPieces; ++s) {
       mbar_init(&ctl->piece_full[s], 1);
-      mbar_init(&ctl->piece_empty[s], 10);
+      mbar_init(&ctl->piece_empty[s], 11);
     }
+    for (int s = 0; s < 6; ++s) mbar_init(&ctl->lse_empty[s >> 1][s & 1], 4);
     mbar_init(&ctl->hand_full, 4);
     mbar_init(&ctl->hand_empty, 4);
-    mbar_init(&ctl->mma_done, 1);
+    mbar_init(&ctl->mma_done[0], 1);
+    mbar_init(&ctl->mma_done[1], 1);
     ctl->abort_flag = 0;
     ctl->r_issued = ctl->f_issued = 0;
     ctl->b = -1;
@@ -242,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   {  // every sequence's steps, added up
+    long long* scan = reinterpret_cast<long long*>(ctl->hand);
     const int each = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     auto cost = [&](int b) {
       const Seq s = seq_of(p, b);
@@ -255,12 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long x = __shfl_up_sync(0xffffffffu, at, o);
       if (lane >= o) at += x;
     }
-    if (lane == 31) ctl->scan[warp] = at;
+    if (lane == 31) scan[warp] = at;
     __syncthreads();
     long long total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += ctl->scan[w];
-      total += ctl->scan[w];
+      if (w < warp) at += scan[w];
+      total += scan[w];
     }
     at -= mine;
     const long long per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x;
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t q_bytes = C::kChunks * q_rows * 128;
 
   auto piece_at = [&](int k, Piece* out) -> bool {
-    if (!mbar_wait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) return false;
+    if (!mbar_wait_small(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) return false;
     *out = ctl->piece[k % kPieces];
     return true;
   };
@@ -297,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmK);
       }
       int e = 0;
+      uint32_t used = 0, turn = 0;  // lse places, a bit a stream: in use, parity
       bool ok = true;
       auto load_queries = [&](uint8_t* to, uint64_t* bar, const Piece& x, int block) {
 #pragma unroll
@@ -308,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) tma_load_3d(to + c * 16384, &tmK, bar, c * 64, 0, z);
       };
+#pragma unroll 1
       for (int k = 0; ok; ++k) {
         Piece x;
         ok = __all_sync(0xffffffffu, piece_at(k, &x));
@@ -316,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
         const int32_t* pages = p.page_table + static_cast<long>(x.b) * p.max_pages;
         const int fb = k & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->f_empty[fb], ((k >> 1) & 1) ^ 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_small(&ctl->f_empty[fb], ((k >> 1) & 1) ^ 1, abort_flag));
         if (!ok) break;
         if (lane == 0) {
           uint8_t* to = sF + fb * 2 * C::kTileBytes;
@@ -329,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           *reinterpret_cast<volatile int*>(&ctl->f_issued) = k + 1;
         }
+        const float* lse_of = p.lse + (static_cast<long>(x.kvh) * p.places + x.place) * kPair;
         int held = 0;
+#pragma unroll 1
         for (int i = 0; ok && i < x.n; ++i, ++e) {
           const int u = x.first + x.u0 + i;
           int page = 0;
@@ -337,60 +349,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((i & 31) == 0) held = i + lane < x.n ? pages[u + lane] : 0;
             page = __shfl_sync(0xffffffffu, held, i & 31);
           }
-          const int st = e % NR;
-          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->r_empty[st], ((e / NR) & 1) ^ 1, abort_flag));
+          const int st = e % NR, ls = e % 3;
+          ok = __all_sync(0xffffffffu, mbar_wait_small(&ctl->r_empty[st], ((e / NR) & 1) ^ 1, abort_flag));
+          if (!ROWS) {  // the streams that used the place of the block's lse have done so
+#pragma unroll 1
+            for (int t = 0; ok && t < 2; ++t) {
+              const uint32_t bit = 1u << (2 * ls + t);
+              if (used & bit) {
+                ok = __all_sync(0xffffffffu, mbar_wait_small(&ctl->lse_empty[ls][t], (turn & bit) != 0, abort_flag));
+                turn ^= bit;
+              }
+              used &= ~bit;
+              if (x.both || (i & 1) == t) used |= bit;
+            }
+          }
           if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&ctl->r_full[st], ROWS ? C::kTileBytes : q_bytes);
-            if (ROWS)
+            mbar_arrive_expect_tx(&ctl->r_full[st], ROWS ? C::kTileBytes : q_bytes + kTile * sizeof(float));
+            if (ROWS) {
               load_keys(sR + st * C::kTileBytes, &ctl->r_full[st], x, page);
-            else
+            } else {
               load_queries(sR + st * C::kTileBytes, &ctl->r_full[st], x, u);
+              bulk_load(ctl->lse[ls], lse_of + static_cast<long>(u) * kTile, kTile * sizeof(float), &ctl->r_full[st]);
+            }
             *reinterpret_cast<volatile int*>(&ctl->r_issued) = e + 1;
           }
         }
       }
-    } else if (warp == kWarpMma) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == kWarpMma || warp == kWarpMma2) {
+      // ---------------------------------------------------------- MMAs of stream t
+      // An issuer each: one's waits and commits run beside the other's MMAs.  Both
+      // pass every streamed tile in order.
       if (lane == 0) {
+        const int t = warp == kWarpMma ? 0 : 1;
         constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const uint32_t sFa = smem_u32(sF), sRa = smem_u32(sR);
-        uint32_t slot = 0, par = 0, sn[2] = {0, 0};
+        const uint64_t df0 = smem_desc(smem_u32(sF), 16, 1024), dr0 = smem_desc(smem_u32(sR), 16, 1024);
+        uint32_t slot = 0, par = 0, sn = 0;
         bool ok = true;
+#pragma unroll 1
         for (int k = 0; ok; ++k) {
-          Piece x;
-          ok = piece_at(k, &x);
-          if (!ok || x.n == 0) break;
+          if (!mbar_wait_small(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) break;
+          const int n = ctl->piece[k % kPieces].n;
+          const bool both = ctl->piece[k % kPieces].both != 0;
+          if (n == 0) break;
           mbar_arrive(&ctl->piece_empty[k % kPieces]);
-          ok = mbar_wait(&ctl->f_full[k & 1], (k >> 1) & 1, abort_flag);
-          const uint32_t fa = sFa + (k & 1) * 2 * C::kTileBytes;
-          for (int i = 0; ok && i < x.n; ++i) {
-            ok = mbar_wait(&ctl->r_full[slot], par, abort_flag);
-            if (!ok) break;
-            const uint64_t dr = smem_desc(sRa + slot * C::kTileBytes, 16, 1024);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!x.both && (i & 1) != t) continue;
-              const uint32_t buf = 2 * t + (sn[t] & 1);
-              ok = ok && mbar_wait(&ctl->s_empty[buf], ((sn[t] >> 1) & 1) ^ 1, abort_flag);
-              if (!ok) break;
-              ++sn[t];
+          ok = mbar_wait_small(&ctl->f_full[k & 1], (k >> 1) & 1, abort_flag);
+          const uint64_t df = df0 + (((k & 1) * 2 + (both ? t : 0)) * C::kTileBytes >> 4);
+#pragma unroll 1
+          for (int i = 0; ok && i < n; ++i) {
+            if (!(ok = mbar_wait_small(&ctl->r_full[slot], par, abort_flag))) break;
+            if (both || (i & 1) == t) {
+              const uint32_t buf = sn & 1;
+              if (!(ok = mbar_wait_small(&ctl->s_empty[2 * t + buf], ((sn >> 1) & 1) ^ 1, abort_flag))) break;
+              ++sn;
               tc_fence_after();
-              const uint64_t df = smem_desc(fa + (x.both ? t * C::kTileBytes : 0), 16, 1024);
+              const uint64_t dr = dr0 + slot * (C::kTileBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                mma_bf16_ss(tmem + 128 * buf, df + off, dr + off, idS, kk > 0 ? 1u : 0u);
+                mma_bf16_ss(tmem + 256 * t + 128 * buf, df + off, dr + off, idS, kk > 0 ? 1u : 0u);
               }
-              mma_commit(&ctl->s_full[buf]);
+              mma_commit(&ctl->s_full[2 * t + buf]);
+              mma_commit(&ctl->r_empty[slot]);
+            } else {
+              mbar_arrive(&ctl->r_empty[slot]);
             }
-            if (!ok) break;
-            mma_commit(&ctl->r_empty[slot]);
             if (++slot == NR) slot = 0, par ^= 1;
           }
           if (ok) mma_commit(&ctl->f_empty[k & 1]);
         }
-        mma_commit(&ctl->mma_done);
-        mbar_wait(&ctl->mma_done, 0, nullptr);
+        mma_commit(&ctl->mma_done[t]);
+        mbar_wait(&ctl->mma_done[t], 0, nullptr);
       }
       __syncwarp();
     } else if (warp == kWarpPlan) {
@@ -455,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += x.n;
             u += x.n;
           }
-          if (!mbar_wait(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
+          if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
           ctl->piece[k % kPieces] = x;
           mbar_arrive(&ctl->piece_full[k % kPieces]);
           if (x.n == 0) break;
@@ -489,10 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f32x2(sl2, sl2);
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+      return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort_flag));
     };
     uint32_t sn = 0, hn = 0;
+    int e0 = 0;  // ring entries of the pieces before
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       Piece x;
       ok = __all_sync(0xffffffffu, piece_at(k, &x));
@@ -502,14 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool alone = !x.both;
       // (keys: a pair of one tile has the second stream take alternate blocks of rows as well)
       const int ft = alone ? 0 : t;                       // this stream's fixed tile
-      float m = -INFINITY, m_used = -INFINITY, l = 0.f;   // rows
+      float m_used = -INFINITY, l = 0.f;                  // rows
       float sum[2] = {0.f, 0.f};                          // keys
       // rows: this thread's token and the last key that it sees; keys: this thread's key
       const int token = (2 * x.pair + ft) * p.tpb + row / p.G;
       const bool row_live = ROWS && row < q_rows && token < x.toks;
       const int lim = !row_live ? -1 : p.causal ? min(x.len - 1, x.off + token) : x.len - 1;
       const int key = (2 * x.pair + ft) * kTile + row;
-      const float* lse_of = p.lse + (static_cast<long>(x.kvh) * p.places + x.place) * kPair;
+#pragma unroll 1
       for (int i = alone ? t : 0; i < x.n; i += alone ? 2 : 1) {
         const uint32_t buf = sn & 1;
         if (!wwait(&ctl->s_full[2 * t + buf], (sn >> 1) & 1)) {
@@ -528,62 +558,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int u = x.first + x.u0 + i;
         if (ROWS) {
           const int vis = min(kTile - 1, lim - u * kTile);  // last visible column
-          if (vis < kTile - 1) {
+          if (__any_sync(0xffffffffu, vis < kTile - 1)) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
               if (e > vis) sr[e] = __float_as_uint(-INFINITY);
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The reference m_used is the maximum of the row's first tile as long as no
+          // score is above it by more than 2^kSlackLog2: the maximum is formed beside
+          // the exponentials, and only a row's first tile takes a second turn.
+#pragma unroll 1
+          for (bool first = true;; first = false) {
+            const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
+            const uint64_t nmb = f32x2(-mb, -mb);
+            uint64_t ls[2] = {0ull, 0ull};
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-          m = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          if (m > m_used) {
-            if (m_used != -INFINITY) l *= ex2_approx((m_used - m) * sl2);
-            m_used = m;
+            for (int c = 0; c < 64; ++c) {
+              const float s0 = __uint_as_float(sr[2 * c]), s1 = __uint_as_float(sr[2 * c + 1]);
+              mx[c & 1] = fmax3(mx[c & 1], s0, s1);
+              const uint64_t xp = fma_f32x2(f32x2(s0, s1), sl2x2, nmb);
+              ls[c & 1] = add_f32x2(ls[c & 1], f32x2(ex2_approx(f32x2_lo(xp)), ex2_approx(f32x2_hi(xp))));
+            }
+            const float top = fmaxf(mx[0], mx[1]);
+            const bool above = first && (m_used == -INFINITY ? top > -INFINITY : (top - m_used) * sl2 > kSlackLog2);
+            if (!__any_sync(0xffffffffu, above)) {
+              const uint64_t s2 = add_f32x2(ls[0], ls[1]);
+              l += f32x2_lo(s2) + f32x2_hi(s2);
+              break;
+            }
+            if (above) {
+              if (m_used != -INFINITY) l *= ex2_approx((m_used - top) * sl2);
+              m_used = top;
+            }
           }
-          const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
-          const uint64_t nmb = f32x2(-mb, -mb);
-          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const uint64_t xp =
-                fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
-            ls[c & 3] = add_f32x2(ls[c & 3], f32x2(ex2_approx(f32x2_lo(xp)), ex2_approx(f32x2_hi(xp))));
-          }
-          const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
-          l += f32x2_lo(s2) + f32x2_hi(s2);
         } else {
           // columns: rows of block u of the queries; those that see the key are [lo, hi)
-          const int i0 = u * p.tpb;
+          const int i0 = u * p.tpb, ls_at = (e0 + i) % 3;
           const int hi = min(q_rows, (x.toks - i0) * p.G);
           const int lo = p.causal ? static_cast<int>(max(0ll, min(static_cast<long long>(kTile), (static_cast<long long>(key) - x.off - i0) * p.G))) : 0;
-          const bool some = __any_sync(0xffffffffu, hi < kTile || lo > 0);
-          const float4* lse4 = reinterpret_cast<const float4*>(lse_of + static_cast<long>(u) * kTile);
+          const float4* lse4 = reinterpret_cast<const float4*>(ctl->lse[ls_at]);
           uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+          // (a row that does not count may hold anything: its weight is dropped, not its score)
+          auto add_up = [&](auto masked) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float4 a = __ldg(lse4 + c);
-            const uint64_t x0 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), sl2x2,
-                                          f32x2(-a.x, -a.y));
-            const uint64_t x1 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])),
-                                          sl2x2, f32x2(-a.z, -a.w));
-            float w[4] = {ex2_approx(f32x2_lo(x0)), ex2_approx(f32x2_hi(x0)), ex2_approx(f32x2_lo(x1)),
-                          ex2_approx(f32x2_hi(x1))};
-            if (some) {
+            for (int c = 0; c < 32; ++c) {
+              const float4 a = lse4[c];
+              const uint64_t x0 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), sl2x2,
+                                            f32x2(-a.x, -a.y));
+              const uint64_t x1 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])),
+                                            sl2x2, f32x2(-a.z, -a.w));
+              float w[4] = {ex2_approx(f32x2_lo(x0)), ex2_approx(f32x2_hi(x0)), ex2_approx(f32x2_lo(x1)),
+                            ex2_approx(f32x2_hi(x1))};
+              if (masked()) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (4 * c + e < lo || 4 * c + e >= hi) w[e] = 0.f;
+                for (int e = 0; e < 4; ++e)
+                  if (4 * c + e < lo || 4 * c + e >= hi) w[e] = 0.f;
+              }
+              ls[c & 1] = add_f32x2(ls[c & 1], f32x2(w[0], w[1]));
+              ls[2 + (c & 1)] = add_f32x2(ls[2 + (c & 1)], f32x2(w[2], w[3]));
             }
-            ls[c & 1] = add_f32x2(ls[c & 1], f32x2(w[0], w[1]));
-            ls[2 + (c & 1)] = add_f32x2(ls[2 + (c & 1)], f32x2(w[2], w[3]));
-          }
+          };
+          if (__any_sync(0xffffffffu, hi < kTile || lo > 0))
+            add_up([] { return true; });
+          else
+            add_up([] { return false; });
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->lse_empty[ls_at][t]);
           const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
           sum[0] += f32x2_lo(s2);
           sum[1] += f32x2_hi(s2);
         }
       }
       if (!ok) break;
+      e0 += x.n;
       // The item's result, or a part of it.
       float total = sum[0] + sum[1];
       if (alone) {  // the other stream's share of the same rows
@@ -617,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (key < x.len) {
         if (whole)
-          p.weights[(static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key] += total;
+          // (one thread adds to a cell: the same as reading, adding and writing, without waiting)
+          atomicAdd(p.weights + (static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key, total);
         else
           p.part_w[part] = total;
       }

@@ -34,7 +34,7 @@
 //
 // Warps 0-3 / 4-7 softmax of stream 0 / 1 (they also load their rows of Q: the
 // next piece's before they write this one's result), 8 loads K and V tiles
-// through one ring, 9 issues the MMAs, 10 works out the pieces, in segments
+// through one ring, 9 and 11 issue the MMAs of stream 0 and 1, 10 works out the pieces, in segments
 // of up to 16 tiles with a tile's page and sequence each.
 //
 // The last tile of a sequence, of r < 128 keys, is loaded from row r - 128 of
@@ -55,10 +55,10 @@ namespace ssattn {
 
 namespace {
 
-constexpr float kRescaleLog2 = 8.0f;  // lazy-rescale slack, exp2 domain
+constexpr float kSlackLog2 = 40.0f;  // how far weights may be above 1 (exp2 domain)
 constexpr int kSMs = 152;
 constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10, kWarpMma2 = 11;
 constexpr int kRows = 256;      // rows of an item
 constexpr int kSegments = 4;    // published segments
 constexpr int kSegTiles = 16;
@@ -119,7 +119,7 @@ struct Ctl {
   uint64_t r_full[10], r_empty[10];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t seg_full[kSegments], seg_empty[kSegments];
-  uint64_t mma_done;
+  uint64_t turn[2], mma_done[2];
   uint32_t tmem_base;
   int abort_flag;
   int n_issued;
@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid < NR) {
     mbar_init(&ctl->r_full[tid], 1);
-    mbar_init(&ctl->r_empty[tid], 1);
+    mbar_init(&ctl->r_empty[tid], 2);  // both issuers
   } else if (tid >= 32 && tid < 32 + kSegments) {
     mbar_init(&ctl->seg_full[tid - 32], 1);
-    mbar_init(&ctl->seg_empty[tid - 32], 10);  // softmax warps, loader, issuer
+    mbar_init(&ctl->seg_empty[tid - 32], 11);  // softmax warps, loader, issuers
   } else if (tid >= 64 && tid < 66) {
     const int t = tid - 64;
     mbar_init(&ctl->q_full[t], 4);
@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->p_full[t], 4);
     mbar_init(&ctl->o_full[t], 1);
     mbar_init(&ctl->o_free[t], 4);
+    mbar_init(&ctl->turn[t], 1);
+    mbar_init(&ctl->mma_done[t], 1);
     if (t == 0) {
-      mbar_init(&ctl->mma_done, 1);
       ctl->abort_flag = 0;
       ctl->n_issued = 0;
     }
@@ -368,88 +369,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == kWarpMma) {
-      // ---------------------------------------------------------- MMA issuer
-      // One stream's P.V of its last tile and scores of its next, then the other's:
-      // a strict order, so that one softmax runs beside the other's MMAs (with an
-      // issuer for each stream both fell into step, and a tile of two streams took
-      // 4700 cycles instead of ~3700).
+    } else if (warp == kWarpMma || warp == kWarpMma2) {
+      // ---------------------------------------------------------- MMAs of stream t
+      // A stream's turn: P.V of its last tile and the scores of its next.  The issuers
+      // take turns (`turn`), so that one softmax runs beside the other stream's MMAs
+      // (left alone both fell into step: 4700 cycles a tile), and there are two so that
+      // one's waits and commits run beside the other's MMAs (a single issuer: 4400).
+      // Both pass every entry of the ring in order, those of the other stream too.
       if (lane == 0) {
+        const int t = warp == kWarpMma ? 0 : 1;
         constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
-        const uint32_t sQa = smem_u32(sQ), sRa = smem_u32(sR);
-        uint32_t slot = 0, par = 0, ks = 0, vs = 0;
-        uint32_t qn = 0, pn = 0, on = 0;  // parities, a bit a stream
-        auto entry = [&]() -> bool {      // the ring's next entry, in `slot`
-          return wait(&ctl->r_full[slot], par);
-        };
+        const uint64_t dq = smem_desc(smem_u32(sQ) + t * C::kTileBytes, 16, 1024);
+        const uint64_t dk0 = smem_desc(smem_u32(sR), 16, 1024), dv0 = smem_desc(smem_u32(sR), 16384, 1024);
+        const uint32_t colS = tmem + C::kColS + 128 * t, colO = tmem + C::kColO + 128 * t;
+        uint32_t slot = 0, par = 0;
+        uint32_t qn = 0, pn = 0, on = 1, tn = t ^ 1;  // parities
         auto next = [&]() {
           if (++slot == NR) slot = 0, par ^= 1;
         };
-        int u = 0;  // tiles of the piece so far
         bool ok = true;
 #pragma unroll 1
-        for (int k = 0; ok; ++k) {
+        for (int k = 0, u = 0; ok; ++k) {
           const Segment* x = seg_at(k);
           if (x == nullptr || x->n == 0) break;
           // P.V follows its scores by one tile (both streams) or two (alternate ones).
-          const int n = x->n, both = x->both, lag = both ? 1 : 2, steps = n + (x->end ? lag : 0);
+          const int n = x->n, both = x->both, lag = both ? 1 : 2, last = x->end;
           if (x->start != 0) u = 0;
+          const int end = u + n;                    // tiles up to the segment's end
+          const int steps = last ? (both ? end + 1 : (end + 3) & ~1) : end;
           seg_done(k);
 #pragma unroll 1
-          for (int i = 0; ok && i < steps; ++i, ++u) {
+          for (; ok && u < steps; ++u) {
+            const bool mine = both || (u & 1) == t, has_v = u >= lag && u < end + lag, has_k = u < end;
+            if (!mine) {
 #pragma unroll 1
-            for (int t = both ? 0 : u & 1; ok && t < (both ? 2 : (u & 1) + 1); ++t) {
-              const bool lead = !both || t == 0, tail = !both || t == 1;
-              const uint32_t bit = 1u << t;
-              if (u >= lag) {  // O_t += P_t V
-                if (lead) {
-                  if (!(ok = entry())) break;
-                  vs = slot;
-                  next();
-                }
-                const bool first = u < 2 * lag;
-                if (first) {  // the piece before has been read out of O
-                  if (!(ok = wait(&ctl->o_free[t], (on & bit) ? 0 : 1))) break;
-                  on ^= bit;
-                }
-                if (!(ok = wait(&ctl->p_full[t], (pn & bit) ? 1 : 0))) break;
-                pn ^= bit;
-                tc_fence_after();
-                const uint64_t dv = smem_desc(sRa + vs * C::kTileBytes, 16384, 1024);
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  mma_bf16_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + kk * 8, dv + ((kk * 2048) >> 4),
-                              idO, (!first || kk > 0) ? 1u : 0u);
-                if (i >= n) mma_commit(&ctl->o_full[t]);
-                if (tail) mma_commit(&ctl->r_empty[vs]);
+              for (int e = has_v + has_k; ok && e > 0; --e) {
+                ok = wait(&ctl->r_full[slot], par);
+                mbar_arrive(&ctl->r_empty[slot]);
+                next();
               }
-              if (i < n) {  // S_t = Q_t K^T
-                if (lead) {
-                  if (!(ok = entry())) break;
-                  ks = slot;
-                  next();
-                }
-                if (u < lag) {
-                  if (!(ok = wait(&ctl->q_full[t], (qn & bit) ? 1 : 0))) break;
-                  qn ^= bit;
-                }
-                tc_fence_after();
-                const uint64_t dq = smem_desc(sQa + t * C::kTileBytes, 16, 1024);
-                const uint64_t dk = smem_desc(sRa + ks * C::kTileBytes, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                  mma_bf16_ss(tmem + C::kColS + 128 * t, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(&ctl->s_full[t]);
-                if (tail) mma_commit(&ctl->r_empty[ks]);
-              }
+              continue;
             }
+            if (!(ok = wait(&ctl->turn[t], tn))) break;
+            tn ^= 1;
+            if (has_v) {  // O_t += P_t V
+              if (!(ok = wait(&ctl->r_full[slot], par))) break;
+              const bool first = u < 2 * lag;
+              if (first) {  // the piece before has been read out of O
+                if (!(ok = wait(&ctl->o_free[t], on))) break;
+                on ^= 1;
+              }
+              if (!(ok = wait(&ctl->p_full[t], pn))) break;
+              pn ^= 1;
+              tc_fence_after();
+              const uint64_t dv = dv0 + slot * (C::kTileBytes >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+              if (u >= end) mma_commit(&ctl->o_full[t]);
+              mma_commit(&ctl->r_empty[slot]);
+              next();
+            }
+            if (has_k) {  // S_t = Q_t K^T
+              if (!(ok = wait(&ctl->r_full[slot], par))) break;
+              if (u < lag) {
+                if (!(ok = wait(&ctl->q_full[t], qn))) break;
+                qn ^= 1;
+              }
+              // (S_t was read before P_t was handed over: the fence in front of P.V covers it)
+              const uint64_t dk = dk0 + slot * (C::kTileBytes >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                mma_bf16_ss(colS, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&ctl->s_full[t]);
+              mma_commit(&ctl->r_empty[slot]);
+              next();
+            }
+            mbar_arrive(&ctl->turn[t ^ 1]);
           }
         }
-        mma_commit(&ctl->mma_done);
-        mbar_wait(&ctl->mma_done, 0, nullptr);
+        mma_commit(&ctl->mma_done[t]);
+        mbar_wait(&ctl->mma_done[t], 0, nullptr);
       }
       __syncwarp();
     } else if (warp == kWarpPlan) {
@@ -755,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.scores != nullptr && mine)
         dump = p.scores + (static_cast<size_t>(place_of(plan, place0 + my_place, B)) * p.Hq + kvh * G +
                            (my_row - my_place * G)) * p.max_pages * kTile;
-      float m = -INFINITY;
       m_used = -INFINITY;
       l = 0.f;
       any = false;  // the stream has had a tile
@@ -792,18 +794,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-              if (counts) m = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              // m, the row's reference, is the maximum of its first tile as long as no
+              // score is above it by more than 2^kSlackLog2 (bf16 and fp32 have the
+              // range, and no precision is lost).
               float alpha = 1.f;
-              bool rescale = false;
-              if (m_used == -INFINITY) {
-                m_used = m;  // the row's first keys
-              } else if ((m - m_used) * sl2 > kRescaleLog2) {
-                alpha = ex2_approx((m_used - m) * sl2);
-                m_used = m;
-                l *= alpha;
-                rescale = true;
+              if (counts) {
+                if (m_used == -INFINITY) {
+                  m_used = top;
+                } else if ((top - m_used) * sl2 > kSlackLog2) {
+                  alpha = ex2_approx((m_used - top) * sl2);
+                  m_used = top;
+                  l *= alpha;
+                }
               }
-              if (__any_sync(0xffffffffu, rescale) && any) {
+              if (__any_sync(0xffffffffu, alpha != 1.f) && any) {
                 // (the scores' commit covers P.V of the stream's step before)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
@@ -815,10 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_st16(colO + c, orr);
                 }
               }
-              // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of
-              // a weight); l adds up the unrounded ones.  (Exponentials with the
-              // maximum before the tile, formed anew where that was too low, were
-              // slower: 107 instead of 88 us on 1024 rows over 32K keys.)
+              // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of a
+              // weight); l adds up the unrounded ones.  (The maximum formed beside the
+              // exponentials, with a second turn where it was too low, was slower.)
               const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
               const uint64_t nmb = f32x2(-mb, -mb);
               uint64_t ls[2] = {0ull, 0ull};
