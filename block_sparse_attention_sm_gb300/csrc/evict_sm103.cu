@@ -37,12 +37,14 @@ constexpr int kChoose = 1024;  // threads of a choosing block (kPlan: block 0 pl
 static_assert(kChoose == kPlan, "block 0 of a choosing launch plans");
 constexpr int kBins = 2048;
 constexpr int kMove = 256;
-constexpr int kPieceBytes = 16384;  // rows that a moving block reads before it writes them
+constexpr int kRounds = 2;                        // 16-byte words of a piece that a thread has
+constexpr int kPieceBytes = kRounds * kMove * 16;  // rows that a moving block reads before it writes them
 constexpr int kStages = 4;
 constexpr int kGroup = 16;     // layers of a launch
 
 struct Cut {      // what becomes of a listed sequence
   int row, len, now;
+  int fresh;      // pages that others hold too are replaced
 };
 
 // Workspace.
@@ -115,7 +117,7 @@ __device__ void plan_block(const Call& c, const Space& w) {
       const int row = c.rows != nullptr ? c.rows[i] : i;
       const int len = s.lens[row], keep = c.keep[i];
       if (len < 0 || len > s.max_pages * kTile || keep < 0) bad = true;
-      w.cut[i] = Cut{row, len, min(len, keep)};
+      w.cut[i] = Cut{row, len, min(len, keep), 0};
     }
     bad = __syncthreads_or(bad);
   }
@@ -132,7 +134,10 @@ __device__ void plan_block(const Call& c, const Space& w) {
         }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
-      if (lane == 0) w.base[i] = count;
+      if (lane == 0) {
+        w.base[i] = count;
+        w.cut[i].fresh = count;
+      }
     }
     __syncthreads();
     for (int i0 = 0; i0 < c.n; i0 += kPlan) {
@@ -197,7 +202,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kChoose)
+__global__ void __launch_bounds__(kChoose, 2)
     choose_kernel(const Call c, const Space w, const Layers layers, int plan_too) {
   if (plan_too && blockIdx.x == 0) {
     plan_block(c, w);
@@ -216,6 +221,24 @@ __global__ void __launch_bounds__(kChoose)
   int32_t* src = w.src + ((static_cast<long>(layer) * c.n + i) * c.Hkv + h) * width;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  // Each warp has a run of keys, whole words of 32 (a lane each).  Up to kHeld words
+  // of it stay in registers; longer runs are read again, kHeld words at a time, in
+  // each of the passes.
+  constexpr int kHeld = 16;
+  const int words = (len + 31) / 32, each = (words + kChoose / 32 - 1) / (kChoose / 32);
+  const int w0 = min(words, warp * each), w1 = min(words, w0 + each);
+  uint32_t u[kHeld];
+  int held = -1;  // first word that is held
+  auto hold = [&](int w) {
+    if (held == w) return;
+    held = w;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int k = (w + i) * 32 + lane;
+      u[i] = w + i < w1 && k < rest ? order_of(weight[k]) : 0u;
+    }
+  };
+
   // The value of the best-th largest of weight[0, rest), and how many of those equal to it are kept.
   __shared__ int bins[kBins];
   __shared__ int s_bin, s_above;
@@ -230,25 +253,15 @@ __global__ void __launch_bounds__(kChoose)
       low -= width_bits;
       for (int b = tid; b < kBins; b += kChoose) bins[b] = 0;
       __syncthreads();
-      for (int k0 = warp * 128; k0 < rest; k0 += kChoose * 4) {
-        const int k = k0 + lane * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < rest) v = *reinterpret_cast<const float4*>(weight + k);
-        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+      for (int w = w0; w < w1; w += kHeld) {
+        hold(w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = order_of(x[e]);
-          const bool in = k + e < rest && (u & known) == value;
-          const int bin = static_cast<int>((u >> low) & ((1u << width_bits) - 1));
-          // (equal weights, as the zeros of keys that nobody looks at, are counted once a warp)
-          const uint32_t m = __ballot_sync(0xffffffffu, in);
-          if (m == 0) continue;
-          const int first = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
-          if (__ballot_sync(0xffffffffu, in && bin == first) == m) {
-            if (lane == 0) atomicAdd(&bins[first], __popc(m));
-          } else if (in) {
-            atomicAdd(&bins[bin], 1);
-          }
+        for (int i = 0; i < kHeld; ++i) {
+          if (w + i >= w1) break;
+          const bool in = w + i < w1 && (w + i) * 32 + lane < rest && (u[i] & known) == value;
+          const int bin = static_cast<int>((u[i] >> low) & ((1u << width_bits) - 1));
+          if (in) atomicAdd(&bins[bin], 1);  // (lanes that add one to the same word are counted by the hardware)
         }
       }
       __syncthreads();
@@ -270,49 +283,42 @@ __global__ void __launch_bounds__(kChoose)
   }
   // wanted: of the weights equal to `value`; all of them if every older key is kept, none if none is.
   const bool all = best >= rest, none = best <= 0;
-  // Each warp has a run of keys, whole words of 32; first it counts, then it writes.
-  const int words = (len + 31) / 32, each = (words + kChoose / 32 - 1) / (kChoose / 32);
-  const int w0 = min(words, warp * each), w1 = min(words, w0 + each);
-  auto kinds = [&](int word, uint32_t* above, uint32_t* equal) {
-    const int k = word * 32 + lane;
-    bool a = false, e = false;
-    if (k < rest) {
-      if (all) {
-        a = true;
-      } else if (!none) {
-        const uint32_t u = order_of(weight[k]);
-        a = u > value;
-        e = u == value;
-      }
-    } else if (k < len) {
-      a = true;  // one of the newest
+  auto above = [&](int k, uint32_t x) { return k < len && (k >= rest || all || (!none && x > value)); };
+  auto equal = [&](int k, uint32_t x) { return k < rest && !all && !none && x == value; };
+  int n_above = 0, n_equal = 0;  // of the warp's keys
+#pragma unroll 1
+  for (int w = w0; w < w1; w += kHeld) {
+    hold(w);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (w + i >= w1) break;
+      const int k = (w + i) * 32 + lane;
+      n_above += __popc(__ballot_sync(0xffffffffu, w + i < w1 && above(k, u[i])));
+      n_equal += __popc(__ballot_sync(0xffffffffu, w + i < w1 && equal(k, u[i])));
     }
-    *above = __ballot_sync(0xffffffffu, a);
-    *equal = __ballot_sync(0xffffffffu, e);
-  };
-  int n_above = 0, n_equal = 0;
-  for (int word = w0; word < w1; ++word) {
-    uint32_t a, e;
-    kinds(word, &a, &e);
-    n_above += __popc(a);
-    n_equal += __popc(e);
   }
   int total;
   const int equal_before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? n_equal : 0, &total), 0);
   const int taken = max(0, min(n_equal, wanted - equal_before));
   int out = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? n_above + taken : 0, &total), 0);
   int left = all || none ? 0 : taken;
-  for (int word = w0; word < w1; ++word) {
-    uint32_t a, e;
-    kinds(word, &a, &e);
-    const bool tie = (e >> lane) & 1u && __popc(e & ((1u << lane) - 1)) < left;
-    left -= min(left, __popc(e));
-    const uint32_t kept = a | __ballot_sync(0xffffffffu, tie);
-    if ((kept >> lane) & 1u) {
-      const int d = out + __popc(kept & ((1u << lane) - 1));
-      if (d < keep) src[d] = word * 32 + lane;
+#pragma unroll 1
+  for (int w = w0; w < w1; w += kHeld) {
+    hold(w);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (w + i >= w1) break;
+      const int k = (w + i) * 32 + lane;
+      const uint32_t e = __ballot_sync(0xffffffffu, w + i < w1 && equal(k, u[i]));
+      const bool tie = ((e >> lane) & 1u) && __popc(e & ((1u << lane) - 1)) < left;
+      left -= min(left, __popc(e));
+      const uint32_t kept = __ballot_sync(0xffffffffu, tie || (w + i < w1 && above(k, u[i])));
+      if ((kept >> lane) & 1u) {
+        const int d = out + __popc(kept & ((1u << lane) - 1));
+        if (d < keep) src[d] = k;
+      }
+      out += __popc(kept);
     }
-    out += __popc(kept);
   }
 }
 
@@ -326,52 +332,78 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows of one (sequence, head, pool), columns [column, column + 16 words).
+// Rows of one (sequence, head, pool), columns [column, column + 16 words).  A piece
+// is kRounds rows a thread: what it copies in the piece after the next ones is looked
+// up before it waits for this one.
 __device__ void move_rows(const Call& c, const Space& w, unsigned char* pool, size_t page_bytes, int i, int h,
                           const int32_t* src, int row_bytes, int column, int words, unsigned char* stage) {
   const Cut x = w.cut[i];
   const int32_t* from = w.from + static_cast<long>(i) * c.s.max_pages;
   const int32_t* to = w.to + static_cast<long>(i) * c.s.max_pages;
-  const int per_pass = kMove / words;                       // rows that the block takes at once
-  const int piece = max(1, min(kTile, kPieceBytes / 16 / words)) / per_pass * per_pass;  // rows of a piece
-  const int rows = piece > 0 ? piece : per_pass;
-  const int word = threadIdx.x % words, lead = threadIdx.x / words;
-  const bool busy = lead < per_pass;
+  const int lead = threadIdx.x / words, word = threadIdx.x - lead * words;
+  const int step = kMove / words, rows = kRounds * step;  // rows that the block takes at once, of a piece
+  const bool busy = lead < step;
   unsigned char* mine = pool + static_cast<size_t>(h) * kTile * row_bytes + column + word * 16;
+  const uint32_t place = smem_u32(stage) + (lead * words + word) * 16;  // in a stage, of the first row
   const int pieces = (x.now + rows - 1) / rows;
   auto valid = [&](int p) { return p >= 0 && p < c.s.num_pages; };
+  // Pieces in front that stay where they are (src[d] - d never falls, so a piece whose
+  // last row stays does so as a whole).
+  int first = 0;
+  if (x.fresh == 0) {
+    for (int q0 = 0; q0 < pieces; q0 += kMove) {
+      const int q = q0 + threadIdx.x, d = min(x.now, (q + 1) * rows) - 1;
+      const int stay = __syncthreads_count(q < pieces && src[d] == d);
+      first += stay;
+      if (stay < kMove) break;
+    }
+  }
+  int next[kRounds];  // keys that this thread copies in the piece that is fetched next
+  auto look = [&](int q) {
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int d = q * rows + u * step + lead;
+      next[u] = busy && d < x.now ? src[d] : -1;
+    }
+  };
   auto fetch = [&](int q) {
-    if (q < pieces && busy) {
-      for (int r = lead; r < rows; r += per_pass) {
-        const int d = q * rows + r;
-        if (d >= x.now) break;
-        const int k = src[d], p = from[k / kTile];
-        if (valid(p))
-          copy_async16(smem_u32(stage + (static_cast<size_t>(q % kStages) * rows + r) * words * 16 + word * 16),
-                       mine + static_cast<size_t>(p) * page_bytes + static_cast<size_t>(k % kTile) * row_bytes);
-      }
+    int page[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) page[u] = next[u] >= 0 ? from[next[u] / kTile] : -1;
+    const uint32_t at = place + (q % kStages) * kPieceBytes;
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      if (valid(page[u]))
+        copy_async16(at + u * step * words * 16, mine + static_cast<size_t>(page[u]) * page_bytes +
+                                                     static_cast<size_t>(next[u] % kTile) * row_bytes);
+      else if (next[u] >= 0)  // (an entry that names no page reads zeros)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + u * step * words * 16), "r"(0) : "memory");
     }
     copy_commit();
+    look(q + 1);
   };
+  look(first);
 #pragma unroll 1
-  for (int q = 0; q < kStages - 1; ++q) fetch(q);
+  for (int q = first; q < first + kStages - 1; ++q) fetch(q);
 #pragma unroll 1
-  for (int q = 0; q < pieces; ++q) {
+  for (int q = first; q < pieces; ++q) {
     fetch(q + kStages - 1);
     copy_wait<kStages - 1>();
     __syncthreads();  // the piece has been read by all
-    if (busy)
-      for (int r = lead; r < rows; r += per_pass) {
-        const int d = q * rows + r;
-        if (d >= x.now) break;
-        const int p = to[d / kTile];
-        const int k = src[d];
-        if (!valid(p) || !valid(from[k / kTile]) || (k == d && p == from[d / kTile])) continue;
-        *reinterpret_cast<uint4*>(mine + static_cast<size_t>(p) * page_bytes + static_cast<size_t>(d % kTile) * row_bytes) =
-            *reinterpret_cast<const uint4*>(stage + (static_cast<size_t>(q % kStages) * rows + r) * words * 16 + word * 16);
-      }
+    const uint32_t at = place + (q % kStages) * kPieceBytes;
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int d = q * rows + u * step + lead;
+      if (!busy || d >= x.now) continue;
+      const int p = to[d / kTile];
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + u * step * words * 16));
+      if (valid(p))
+        *reinterpret_cast<uint4*>(mine + static_cast<size_t>(p) * page_bytes + static_cast<size_t>(d % kTile) * row_bytes) = v;
+    }
     __syncthreads();  // its place is filled again in the next turn
   }
+  copy_wait<0>();
 }
 
 // The weights of one (sequence, layer, head): as move_rows, a piece in registers.
