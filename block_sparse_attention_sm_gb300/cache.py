@@ -9,6 +9,7 @@ device's current stream); what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 
 import torch
@@ -419,7 +420,8 @@ def prefix_plan(page_table, seq_lens, *, out=None, stream=None):
     _dense("page_table", page_table, _I32, 2)
     B, max_pages = page_table.shape
     _dense("seq_lens", seq_lens, _I32, None, (B,))
-    words = (capi._lib or capi.load()).ss_prefix_plan_size(B) // 4
+    lib = capi._lib or capi.load()
+    words = lib.ss_prefix_plan_size(B) // 4
     if words == 0:
         raise ValueError(f"prefix_plan: {B} sequences (1 to 8192)")
     if out is not None:
@@ -428,8 +430,9 @@ def prefix_plan(page_table, seq_lens, *, out=None, stream=None):
     with context:
         if out is None:
             out = torch.empty(words, dtype=_I32, device=page_table.device)
-        st = capi.ss_prefix_plan(page_table, seq_lens, B, max_pages, out, 4 * words, handle)
-    _check(st, "ss_prefix_plan")
+        st = lib.ss_prefix_plan(page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, out.data_ptr(), 4 * words, handle)
+    if st:
+        raise SSError(st, "ss_prefix_plan")
     return out
 
 
@@ -723,15 +726,18 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
     if out_weights is not None and len(out_weights) != len(weights):
         raise ValueError(f"out_weights: expected {len(weights)} tensors, got {len(out_weights)}")
     page_bytes = _pools(pools, num_pages)
-    for i, t in enumerate(weights):
-        _dense(f"weights[{i}]", t, torch.float32, 3)
-    Hkv = weights[0].shape[1]
-    shape = (num_rows, Hkv, max_pages * 128)
-    for name, some in (("weights", weights), ("out_weights", out_weights or ())):
-        for i, t in enumerate(some):
-            _dense(f"{name}[{i}]", t, torch.float32, None, shape)
-    for i, t in enumerate(pools):
-        if t.shape[1:3] != ((Hkv, 128) if t.ndim > 3 or Hkv > 1 else (128, t.shape[2])):
+    Hkv = weights[0].shape[1] if isinstance(weights[0], torch.Tensor) and weights[0].ndim == 3 else 0
+    shape = torch.Size((num_rows, Hkv, max_pages * 128))
+    for some in (weights, out_weights) if out_weights is not None else (weights,):
+        for t in some:
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+                i = [x is t for x in some].index(True)
+                _dense(f"{'weights' if some is weights else 'out_weights'}[{i}]", t, torch.float32, 3, shape)
+    want = (Hkv, 128)
+    for t in pools:
+        at = t.shape
+        if at[1:3] != want and not (len(at) == 3 and Hkv == 1 and at[1] == 128):
+            i = [x is t for x in pools].index(True)
             raise ValueError(f"pools[{i}]: expected [num_pages, {Hkv}, 128, ...], got {tuple(t.shape)}")
     n = _list("keep", keep)
     if rows is not None:
@@ -743,18 +749,25 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
             _dense(name, t, _I32, None, like.shape)
     if result is not None:
         _dense("result", result, _I32, shape=(1,))
-    given = list(pools) + list(weights) + list(out_weights or ())
+    moved = weights if out_weights is None else out_weights
     handle, context = _on(stream, "page_refs page_table seq_lens keep rows out_refs out_table out_lens result workspace" +
-                          " pool" * len(pools) + " weights" * (len(given) - len(pools)), page_refs, page_table, seq_lens, keep,
-                          rows, out_refs, out_table, out_lens, result, workspace, *given)
+                          " pool" * len(pools) + " weights" * len(weights) + " out_weights" * len(moved), page_refs, page_table,
+                          seq_lens, keep, rows, out_refs, out_table, out_lens, result, workspace, *pools, *weights, *moved)
     with context:
-        ws, nbytes = _scratch(workspace, capi.ss_pages_evict_workspace_size(
+        lib = capi._lib or capi.load()
+        ws, nbytes = _scratch(workspace, lib.ss_pages_evict_workspace_size(
             num_pages, num_rows, max_pages, n, Hkv, len(weights), len(pools)) if workspace is None else 0, page_refs.device)
         if result is None:
             result = torch.empty(1, dtype=_I32, device=page_refs.device)
-        st = capi.ss_pages_evict(pools, page_bytes, weights, Hkv, page_refs, num_pages, page_table, num_rows, max_pages,
-                                 seq_lens, rows, keep, n, recent, out_weights, out_refs, out_table, out_lens, result, ws,
-                                 nbytes, handle)
-    _check(st, "ss_pages_evict")
-    _written(tuple(weights if out_weights is None else out_weights))
+        at, of = array.array("Q", [t.data_ptr() for t in pools]), array.array("Q", [t.data_ptr() for t in weights])
+        to = array.array("Q", [t.data_ptr() for t in moved])
+        st = lib.ss_pages_evict(
+            at.buffer_info()[0], len(at), page_bytes, of.buffer_info()[0], len(of), Hkv, page_refs.data_ptr(), num_pages,
+            page_table.data_ptr(), num_rows, max_pages, seq_lens.data_ptr(), rows.data_ptr() if rows is not None else None,
+            keep.data_ptr(), n, recent, to.buffer_info()[0], out_refs.data_ptr() if out_refs is not None else None,
+            out_table.data_ptr() if out_table is not None else None, out_lens.data_ptr() if out_lens is not None else None,
+            result.data_ptr(), ws.data_ptr(), nbytes, handle)
+    if st:
+        raise SSError(st, "ss_pages_evict")
+    _written(tuple(moved))
     return result

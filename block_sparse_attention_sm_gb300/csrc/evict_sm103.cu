@@ -26,6 +26,7 @@
 #include "evict.cuh"
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "pages_plan.cuh"
 #include "ptx_sm103.cuh"
 
@@ -204,6 +205,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 
 __global__ void __launch_bounds__(kChoose, 2)
     choose_kernel(const Call c, const Space w, const Layers layers, int plan_too) {
+  let_next_start();
   if (plan_too && blockIdx.x == 0) {
     plan_block(c, w);
     return;
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(kMove)
     move_kernel(const Call c, const Space w, const Layers layers, const PagePools pools, int per_layer, int slices,
                 int state_too) {
   extern __shared__ unsigned char stage[];
+  wait_for_previous();
   if (w.head[0] == 0) return;
   const PageState& s = c.s;
   const long width = static_cast<long>(s.max_pages) * kTile;
@@ -493,7 +496,7 @@ cudaError_t launch_pages_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   space_of(&w, ws, a.s.num_pages, a.s.num_rows, a.s.max_pages, a.n, a.Hkv, group);
   Call c{a.s, a.rows, a.keep, a.n, a.recent, a.Hkv, a.out_refs, a.out_table, a.out_lens, a.result};
   const int row_words = static_cast<int>(a.page_bytes / (static_cast<size_t>(a.Hkv) * kTile) / 16);
-  cudaError_t e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kPieceBytes);
+  cudaError_t e = cudaSuccess;
   for (int l0 = 0; e == cudaSuccess && l0 < a.num_layers; l0 += group) {
     Layers layers{};
     layers.count = a.num_layers - l0 < group ? a.num_layers - l0 : group;
@@ -513,9 +516,8 @@ cudaError_t launch_pages_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
     int slices = 1;
     while (movers * slices < 4 * kSMs && row_words % (2 * slices) == 0 && row_words / (2 * slices) >= 4) slices *= 2;
     const long blocks = movers * slices + lists + (last ? a.s.num_rows : 0);
-    move_kernel<<<static_cast<unsigned>(blocks), kMove, kStages * kPieceBytes, st>>>(c, w, layers, pools, a.per_layer,
-                                                                                     slices, last);
-    e = cudaGetLastError();
+    e = launch_behind(move_kernel, static_cast<unsigned>(blocks), kMove, kStages * kPieceBytes, st, c, w, layers, pools,
+                      a.per_layer, slices, static_cast<int>(last));
   }
   return e;
 }

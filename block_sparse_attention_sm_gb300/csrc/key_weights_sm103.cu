@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "key_weights.cuh"
 #include "ptx_sm103.cuh"
 
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) report_timeout(p.status);
     return;
   }
+  let_next_start();
   uint8_t* sF = smem;
   uint8_t* sR = smem + C::kRingOff;
   auto* ctl = reinterpret_cast<Ctl<NR>*>(smem + C::kCtlOff);
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     if (tid == 0) ctl->total = total;
   }
+  if (!ROWS) wait_for_previous();  // (the rows' lse)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -680,6 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Block c: the item that CTA c began and others went on with.
 template <bool ROWS>
 __global__ void __launch_bounds__(kPair) join_kernel(const KeyWeightsParams p) {
+  let_next_start();
+  wait_for_previous();
   const Split x = p.split[blockIdx.x];
   if (!x.valid) return;
   const Seq s = seq_of(p, x.b);
@@ -712,12 +717,16 @@ cudaError_t launch_pass(const CUtensorMap& tq, const CUtensorMap& tk, const KeyW
     return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : -1;
   }();
   if (launch_regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), Cfg<D>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  fn<<<p.ctas, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  join_kernel<ROWS><<<p.ctas, kPair, 0, st>>>(p);
-  return cudaGetLastError();
+  if (ROWS) {
+    fn<<<p.ctas, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, p);
+    e = cudaGetLastError();
+  } else {
+    e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tq, tk, p);
+  }
+  return e != cudaSuccess ? e : launch_behind(join_kernel<ROWS>, p.ctas, kPair, 0, st, p);
 }
 
 constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }

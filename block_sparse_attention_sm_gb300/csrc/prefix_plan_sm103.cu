@@ -13,6 +13,7 @@
 // its longest common stretch with one of them (the nearest smaller row has it).
 // tree_kernel: a warp a place looks left and right for the run's ends, 32 places a
 // step, in shared memory.  Latency bounds both.
+#include "launch.cuh"
 #include "shared_decode.cuh"
 
 namespace ssattn {
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kRank)
 __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32_t* plan) {
   extern __shared__ int c[];  // [B + 1] common tiles of places i - 1 and i; c[0] = c[B] = 0
   int32_t* nodes = plan + kPlanHead + B;
+  wait_for_previous();
   for (int i = threadIdx.x; i <= B; i += kTree) c[i] = i == 0 || i == B ? 0 : nodes[i * kNodeWords + 2];
   if (threadIdx.x < kPlanHead)
     plan[threadIdx.x] = threadIdx.x == 0 ? B : threadIdx.x == 1 ? max_pages : threadIdx.x == 2 ? kPlanMark : 0;
@@ -197,8 +199,8 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
 cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
                                int32_t* plan, cudaStream_t st) {
   rank_kernel<<<B, kRank, 0, st>>>(table, lens, B, max_pages, plan);
-  tree_kernel<<<1, kTree, (B + 1) * sizeof(int), st>>>(B, max_pages, plan);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_behind(tree_kernel, 1, kTree, (B + 1) * sizeof(int), st, B, max_pages, plan);
 }
 
 }  // namespace ssattn

@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "ptx_sm103.cuh"
 #include "shared_decode.cuh"
 
@@ -235,9 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
   volatile int* abort_flag = &ctl->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t* plan = valid_plan(p);
   const int B = p.B, G = p.G, nb = kTile / G;  // sequences of a bundle
-  const int nodes = plan != nullptr ? B : 0;   // shared ones
+  let_next_start();
 
   if (tid < NR) {
     mbar_init(&ctl->r_full[tid], 1);
@@ -268,6 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  wait_for_previous();
+  const int32_t* plan = valid_plan(p);
+  const int nodes = plan != nullptr ? B : 0;  // shared ones
   // Sums over the batch, in the shared memory that the tiles take later: the own
   // tiles of the places below each, the cost and partial rows of the shared nodes
   // below each.
@@ -874,6 +877,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
   __shared__ int s_second[L], s_start[L + 1]; // the second stream's distance (0: one result a piece), results in front
   __shared__ float s_w[128], s_red[2][4], s_o[128];
   __shared__ long long s_at[128];
+  let_next_start();
+  wait_for_previous();
   const int32_t* plan = valid_plan(p);
   const int i = blockIdx.x / p.Hq, h = blockIdx.x - i * p.Hq;
   const int kvh = h / p.G, g = h - kvh * p.G;
@@ -987,6 +992,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
 // weights[b][kvh][key] += sum over the group's heads of exp2(s * scale * log2e - lse).
 // A warp a tile, 4 columns a lane.
 __global__ void __launch_bounds__(256) weigh_kernel(const SharedParams p) {
+  wait_for_previous();
   const int b = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31;
   const int len = length_of(p, b), nT = tiles_of(len);
   for (int tile = blockIdx.x * 8 + (threadIdx.x >> 5); tile < nT; tile += gridDim.x * 8) {
@@ -1024,15 +1030,15 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Share
     return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : -1;
   }();
   if (launch_regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), Cfg<D>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  fn<<<p.ctas, kThreads, Cfg<D>::kSmemBytes, st>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  shared_merge_kernel<D><<<static_cast<unsigned>(p.B) * p.Hq, 128, 0, st>>>(p, p.ctas);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.weights == nullptr) return e;
+  e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  e = launch_behind(shared_merge_kernel<D>, static_cast<unsigned>(p.B) * p.Hq, 128, 0, st, p, p.ctas);
+  if (e != cudaSuccess || p.weights == nullptr) return e;
   const int blocks = (p.max_pages + 7) / 8;
-  weigh_kernel<<<dim3(blocks < 64 ? blocks : 64, p.Hkv, p.B), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_behind(weigh_kernel, dim3(blocks < 64 ? blocks : 64, p.Hkv, p.B), 256, 0, st, p);
 }
 
 constexpr size_t up128(size_t n) { return (n + 127) / 128 * 128; }
