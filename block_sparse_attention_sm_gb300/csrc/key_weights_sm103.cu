@@ -160,6 +160,17 @@ __device__ __forceinline__ float row_lse(float m, float l, float sl2) {
   return l == 0.f ? INFINITY : m == -INFINITY ? l : fmaf(m, sl2, log2f(l));
 }
 
+// What an item costs besides its steps (its fixed tiles, its results), in steps: causal
+// pairs at the short end are many (a CTA that had them ended 20% later than others).
+constexpr int kItemCost = 2;
+// Cost of all pairs below i.  Step u of pair i is at cost_below(i) + kItemCost + u, and
+// belongs to the CTA whose share that lies in.
+template <bool ROWS>
+__device__ long long cost_below(const KeyWeightsParams& p, const Seq& s, int i) {
+  if (s.tiles == 0 || s.blocks == 0) return 0;  // (no items)
+  return steps_below<ROWS>(p, s, i) + static_cast<long long>(kItemCost) * i;
+}
+
 // A run of steps of one item.
 struct Piece {
   int n, u0, steps;  // steps; the first of them, all of the item's (n = 0: no more pieces)
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int each = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     auto cost = [&](int b) {
       const Seq s = seq_of(p, b);
-      return steps_below<ROWS>(p, s, pairs_of<ROWS>(s)) * p.Hkv;
+      return cost_below<ROWS>(p, s, pairs_of<ROWS>(s)) * p.Hkv;
     };
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += cost(b);
@@ -430,61 +441,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long per = (ctl->total + gridDim.x - 1) / gridDim.x;
         long long at = per * blockIdx.x;
         const long long end = min(at + per, ctl->total);
-        int b = ctl->b, kvh = 0, pair = 0;
-        long long u = 0;  // step of the item that comes next
+        int b = at < end ? ctl->b : -1, kvh = 0, pair = 0;
+        long long begin = 0;  // cost in front of the item's first step
         Seq s{};
         int pairs = 0;
         if (b >= 0) {  // the item that the share begins in
           s = seq_of(p, b);
           pairs = pairs_of<ROWS>(s);
-          const long long head = steps_below<ROWS>(p, s, pairs);
+          const long long head = cost_below<ROWS>(p, s, pairs);
           long long in = at - ctl->at;
           kvh = static_cast<int>(in / head);
           in -= kvh * head;
-          int lo = 0, hi = pairs;  // the last pair with steps_below <= in
+          int lo = 0, hi = pairs;  // the last pair with cost_below <= in
           while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (steps_below<ROWS>(p, s, mid) <= in) lo = mid; else hi = mid;
+            if (cost_below<ROWS>(p, s, mid) <= in) lo = mid; else hi = mid;
           }
           pair = lo;
-          u = in - steps_below<ROWS>(p, s, lo);
+          begin = ctl->at + kvh * head + cost_below<ROWS>(p, s, lo) + kItemCost;
         }
         Split split{};
         for (int k = 0;; ++k) {
           Piece x{};
-          if (b >= 0 && at < end) {
-            int steps = steps_of<ROWS>(p, s, pair);
-            while (u >= steps) {  // on to the next item that has steps
-              u = 0;
-              if (++pair >= pairs) {
-                pair = 0;
-                if (++kvh == p.Hkv) {
-                  kvh = 0;
-                  do {  // (there are steps left, so a sequence is)
-                    b = min(b + 1, p.B - 1);
-                    s = seq_of(p, b);
-                    pairs = pairs_of<ROWS>(s);
-                  } while (b < p.B - 1 && (s.tiles == 0 || s.blocks == 0));
-                }
-              }
-              steps = steps_of<ROWS>(p, s, pair);
+#pragma unroll 1
+          while (b >= 0) {
+            const int steps = steps_of<ROWS>(p, s, pair);
+            if (begin >= end) break;
+            if (at < begin + steps) {
+              const int u = static_cast<int>(max(0ll, at - begin));
+              x.n = static_cast<int>(min(static_cast<long long>(steps), end - begin)) - u;
+              x.u0 = u;
+              x.steps = steps;
+              x.b = b;
+              x.kvh = kvh;
+              x.pair = pair;
+              x.tok0 = s.tok0;
+              x.toks = s.n;
+              x.len = s.len;
+              x.off = s.off;
+              x.first = first_step<ROWS>(p, s, pair);
+              x.both = ROWS ? 2 * pair + 1 < s.blocks : 2 * pair + 1 < s.tiles;
+              x.place = s.place;
+              if (u == 0 && x.n < steps) split = Split{1, b, kvh, pair, steps - x.n, static_cast<int>(min(per, 0x7fffffffll))};
             }
-            x.n = static_cast<int>(min(static_cast<long long>(steps - u), end - at));
-            x.u0 = static_cast<int>(u);
-            x.steps = steps;
-            x.b = b;
-            x.kvh = kvh;
-            x.pair = pair;
-            x.tok0 = s.tok0;
-            x.toks = s.n;
-            x.len = s.len;
-            x.off = s.off;
-            x.first = first_step<ROWS>(p, s, pair);
-            x.both = ROWS ? 2 * pair + 1 < s.blocks : 2 * pair + 1 < s.tiles;
-            x.place = s.place;
-            if (x.u0 == 0 && x.n < steps) split = Split{1, b, kvh, pair, steps - x.n, static_cast<int>(min(per, 0x7fffffffll))};
-            at += x.n;
-            u += x.n;
+            // on to the next item
+            begin += steps + kItemCost;
+            if (++pair >= pairs) {
+              pair = 0;
+              if (++kvh == p.Hkv) {
+                kvh = 0;
+                do {
+                  if (++b >= p.B) break;
+                  s = seq_of(p, b);
+                  pairs = pairs_of<ROWS>(s);
+                } while (s.tiles == 0 || s.blocks == 0);
+                if (b >= p.B) b = -1;
+              }
+            }
+            if (x.n > 0) break;
           }
           if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
           ctl->piece[k % kPieces] = x;
