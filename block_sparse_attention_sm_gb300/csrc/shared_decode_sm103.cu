@@ -12,9 +12,9 @@
 //
 // What a sequence has to itself has only G rows.  128 / G sequences are bundled:
 // their rows are the 128 rows of the MMAs, their tiles come one behind the other,
-// and each tile counts for the rows of its own sequence alone (the others' weights
-// are 0).  So the rows' state stays in place while short sequences pass: no new Q
-// and no result to write for each.
+// and each tile counts for the rows of its own sequence alone: P.V leaves the other
+// lanes of O as they are, whatever the tile's values hold.  So the rows' state stays
+// in place while short sequences pass: no new Q and no result to write for each.
 //
 // Work: an item is (bundle, KV head) or (shared node, KV head, block of up to 256
 // rows), as long as it has tiles.  All items' tiles laid end to end are cut into
@@ -392,6 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++slot == NR) slot = 0, par ^= 1;
         };
         bool ok = true;
+        // A bundle: the places of the stream's last tile and of the one whose P.V was last.
+        int place = -1, before = -1;
+        uint32_t off[4] = {0, 0, 0, 0};  // lanes that the stream's last tile does not count for
 #pragma unroll 1
         for (int k = 0, u = 0; ok; ++k) {
           const Segment* x = seg_at(k);
@@ -399,9 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // P.V follows its scores by one tile (both streams) or two (alternate ones).
           const int n = x->n, both = x->both, lag = both ? 1 : 2, last = x->end;
           if (x->start != 0) u = 0;
-          const int end = u + n;                    // tiles up to the segment's end
+          const int u0 = u, end = u + n;            // tiles up to the segment's end
           const int steps = last ? (both ? end + 1 : (end + 3) & ~1) : end;
-          seg_done(k);
+          const bool bundle = x->tile[0].place >= 0;
 #pragma unroll 1
           for (; ok && u < steps; ++u) {
             const bool mine = both || (u & 1) == t, has_v = u >= lag && u < end + lag, has_k = u < end;
@@ -423,13 +426,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&ctl->o_free[t], on))) break;
                 on ^= 1;
               }
+              const bool begins = first || place != before;
+              before = place;
               if (!(ok = wait(&ctl->p_full[t], pn))) break;
               pn ^= 1;
               tc_fence_after();
               const uint64_t dv = dv0 + slot * (C::kTileBytes >> 4);
+              if (bundle) {
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  mma_bf16_ts_lanes(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, off, (!begins || kk > 0) ? 1u : 0u);
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+              }
               if (u >= end) mma_commit(&ctl->o_full[t]);
               mma_commit(&ctl->r_empty[slot]);
               next();
@@ -452,7 +463,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               next();
             }
             mbar_arrive(&ctl->turn[t ^ 1]);
+            if (has_k && bundle) {
+              // (Behind the turn, where it costs no time.)  A bundle's tile counts for the
+              // rows of one sequence: P.V leaves the others' lanes as they are, whatever
+              // the tile's values hold, and the sequence's first tile begins its O.
+              place = x->tile[u - u0].place;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const int lo = max(0, place * G - 32 * w), hi = min(32, place * G + G - 32 * w);
+                off[w] = hi > lo ? ~((0xffffffffu >> (32 - (hi - lo))) << lo) : 0xffffffffu;
+              }
+            }
           }
+          seg_done(k);
         }
         mma_commit(&ctl->mma_done[t]);
         mbar_wait(&ctl->mma_done[t], 0, nullptr);
@@ -776,74 +799,68 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Tile d = x->tile[i];
           // A bundle's tile counts for the rows of one sequence.
           const bool counts = mine && (d.place < 0 || d.place == my_place);
-          if (warp_live) {
+          if (__any_sync(0xffffffffu, counts)) {
             uint32_t sr[128];
             tc_fence_after();
-            if (__any_sync(0xffffffffu, counts)) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld32p(colS + 32 * c, sr + 32 * c);
-              tmem_wait_ld();
-              if (dump != nullptr && counts) {
-                float* to = dump + static_cast<size_t>(d.tile) * kTile;
+            for (int c = 0; c < 4; ++c) tmem_ld32p(colS + 32 * c, sr + 32 * c);
+            tmem_wait_ld();
+            if (dump != nullptr && counts) {
+              float* to = dump + static_cast<size_t>(d.tile) * kTile;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) store8(to + 8 * c, sr + 8 * c);
+              for (int c = 0; c < 16; ++c) store8(to + 8 * c, sr + 8 * c);
+            }
+            if (d.shift > 0) {  // columns without a key
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                if (e < d.shift) sr[e] = __float_as_uint(-INFINITY);
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // m, the row's reference, is the maximum of its first tile as long as no
+            // score is above it by more than 2^kSlackLog2 (bf16 and fp32 have the
+            // range, and no precision is lost).
+            float alpha = 1.f;
+            if (counts) {
+              if (m_used == -INFINITY) {
+                m_used = top;
+              } else if ((top - m_used) * sl2 > kSlackLog2) {
+                alpha = ex2_approx((m_used - top) * sl2);
+                m_used = top;
+                l *= alpha;
               }
-              if (d.shift > 0) {  // columns without a key
-#pragma unroll
-                for (int e = 0; e < 128; ++e)
-                  if (e < d.shift) sr[e] = __float_as_uint(-INFINITY);
-              }
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              // m, the row's reference, is the maximum of its first tile as long as no
-              // score is above it by more than 2^kSlackLog2 (bf16 and fp32 have the
-              // range, and no precision is lost).
-              float alpha = 1.f;
-              if (counts) {
-                if (m_used == -INFINITY) {
-                  m_used = top;
-                } else if ((top - m_used) * sl2 > kSlackLog2) {
-                  alpha = ex2_approx((m_used - top) * sl2);
-                  m_used = top;
-                  l *= alpha;
-                }
-              }
-              if (__any_sync(0xffffffffu, alpha != 1.f) && any) {
-                // (the scores' commit covers P.V of the stream's step before)
+            }
+            if (__any_sync(0xffffffffu, alpha != 1.f) && any) {
+              // (the scores' commit covers P.V of the stream's step before)
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t orr[16];
-                  tmem_ld16p(colO + c, orr);
-                  tmem_wait_ld();
+              for (int c = 0; c < D; c += 16) {
+                uint32_t orr[16];
+                tmem_ld16p(colO + c, orr);
+                tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                  tmem_st16(colO + c, orr);
-                }
+                for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                tmem_st16(colO + c, orr);
               }
-              // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of a
-              // weight); l adds up the unrounded ones.  (The maximum formed beside the
-              // exponentials, with a second turn where it was too low, was slower.)
-              const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
-              const uint64_t nmb = f32x2(-mb, -mb);
-              uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                const uint64_t xp =
-                    fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
-                const float p0 = ex2_approx(f32x2_lo(xp)), p1 = ex2_approx(f32x2_hi(xp));
-                ls[c & 1] = add_f32x2(ls[c & 1], f32x2(p0, p1));
-                sr[c] = pack_bf16x2(p0, p1);
-              }
-              const uint64_t lsum = add_f32x2(ls[0], ls[1]);
-              if (counts) l += f32x2_lo(lsum) + f32x2_hi(lsum);
             }
-            if (d.place >= 0) {  // rows of the bundle's other sequences: their weights are 0
+            // P = exp2(s * scale * log2e - m), rounded to bf16 for P.V (2^-8 of a
+            // weight); l adds up the unrounded ones.  (The maximum formed beside the
+            // exponentials, with a second turn where it was too low, was slower.)
+            const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
+            const uint64_t nmb = f32x2(-mb, -mb);
+            uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-              for (int c = 0; c < 64; ++c) sr[c] = counts ? sr[c] : 0u;
+            for (int c = 0; c < 64; ++c) {
+              const uint64_t xp =
+                  fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sl2x2, nmb);
+              const float p0 = ex2_approx(f32x2_lo(xp)), p1 = ex2_approx(f32x2_hi(xp));
+              ls[c & 1] = add_f32x2(ls[c & 1], f32x2(p0, p1));
+              sr[c] = pack_bf16x2(p0, p1);
             }
+            const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+            if (counts) l += f32x2_lo(lsum) + f32x2_hi(lsum);
             tmem_st32p(colS, sr);
             tmem_st32p(colS + 32, sr + 32);
             tmem_wait_st();

@@ -113,3 +113,128 @@ def test_against_the_model(ss, case, kind, out):
     lens, keep, recent, layers, Hkv, row, shared = CASES[case]
     rng = np.random.default_rng(case)
     check(ss, make(rng, lens, layers, Hkv, row, shared=shared, kind=kind), keep, recent, out=out)
+
+
+def test_listed_rows(ss):
+    rng = np.random.default_rng(20)
+    for out in (False, True):
+        state = make(rng, [300, 500, 129, 700, 64], 2, 2, 64, shared=1)
+        check(ss, state, [100, 650, 129], 16, rows=[3, 0, 2], out=out)
+        check(ss, state, [], 16, rows=[], out=out)
+
+
+@pytest.mark.parametrize("out", [False, True])
+def test_refused_without_free_pages(ss, out):
+    """Shared pages must be replaced and there are too few free ones: nothing changes."""
+    rng = np.random.default_rng(21)
+    state = make(rng, [700, 650, 900], 1, 2, 64, shared=4, spare=3)
+    before = [x.clone() for x in state[0] + state[1]]
+    pools, weights, refs, table, lens = state
+    for p in [p for p, n in enumerate(refs) if n == 0][3:]:  # (somebody else's)
+        refs[p] = 1
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    gp, gw, gr, gt, gl = [p.cuda() for p in pools], [w.cuda() for w in weights], ints(refs), ints(table), ints(lens)
+    r = ss.pages_evict(gp, gw, gr, gt, gl, ints([200, 200, 200]), recent=10)
+    assert int(r) == 3  # two pages a sequence, three free
+    assert gr.tolist() == refs and gt.tolist() == table and gl.tolist() == lens
+    assert all(same(a, b) for a, b in zip(gp + gw, before))
+    check(ss, state, [128, 200, 700], 10, out=out)  # one, two and none
+
+
+@pytest.mark.parametrize("what", ["row", "twice", "keep", "length", "long"])
+def test_wrong_arguments_change_nothing(ss, what):
+    rng = np.random.default_rng(22)
+    pools, weights, refs, table, lens = make(rng, [300, 500, 129], 1, 2, 64)
+    rows, keep = [0, 1, 2], [100, 100, 100]
+    if what == "row":
+        rows[1] = 3
+    elif what == "twice":
+        rows[1] = 2
+    elif what == "keep":
+        keep[2] = -1
+    elif what == "length":
+        lens[1] = -5
+    else:
+        lens[1] = len(table[0]) * PAGE + 1
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    gp, gw, gr, gt, gl = [p.cuda() for p in pools], [w.cuda() for w in weights], ints(refs), ints(table), ints(lens)
+    r = ss.pages_evict(gp, gw, gr, gt, gl, ints(keep), rows=ints(rows))
+    assert int(r) == -1
+    assert gr.tolist() == refs and gt.tolist() == table and gl.tolist() == lens
+    assert all(same(a, b) for a, b in zip(gp + gw, pools + weights))
+    ss.stream_status()
+
+
+def test_many_layers_and_pools(ss):
+    """More layers than a launch takes; one pool a layer (latent rows), three, and wide rows."""
+    rng = np.random.default_rng(23)
+    check(ss, make(rng, [200, 300], 19, 1, 8, shared=1), [100, 257], 5)
+    check(ss, make(rng, [200, 300], 25, 2, 8, per=3), [100, 257], 5, out=True)
+    check(ss, make(rng, [300, 200], 2, 1, 576, per=1), [130, 7], 0)
+    check(ss, make(rng, [260], 1, 1, 3080, per=1), [200], 1)
+    check(ss, make(rng, [260, 140], 1, 2, 36, dtype=torch.float32), [200, 100], 1)
+
+
+def test_latent_pools_without_a_head_axis(ss):
+    rng = np.random.default_rng(24)
+    pools, weights, refs, table, lens = make(rng, [300, 290], 1, 1, 64, per=1)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    flat = pools[0][:, 0].contiguous().cuda()
+    gr, gt, gl, gw = ints(refs), ints(table), ints(lens), weights[0].cuda()
+    assert int(ss.pages_evict([flat], [gw], gr, gt, gl, ints([100, 20]), recent=3)) == 0
+    evict(pools, weights, refs, table, lens, [100, 20], 3)
+    assert same(flat, pools[0][:, 0])
+
+
+@pytest.mark.parametrize("kind", ["skewed", "ties", "odd"])
+def test_long_sequences(ss, kind):
+    """More keys than a choosing block holds in registers."""
+    rng = np.random.default_rng(25)
+    pools, weights, refs, table, lens = make(rng, [40000, 17000], 1, 1, 8, kind=kind, per=1)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    gp, gw, gr, gt, gl = [p.cuda() for p in pools], [w.cuda() for w in weights], ints(refs), ints(table), ints(lens)
+    keep, recent = [5000, 16999], 100
+    assert int(ss.pages_evict(gp, gw, gr, gt, gl, ints(keep), recent=recent)) == 0
+    from _shared import choose
+    for r, k in enumerate(keep):
+        src = choose(weights[0][r, 0, :lens[r]].double(), k, recent)
+        assert same(gw[0][r, 0, :k], weights[0][r, 0, src]) and (gw[0][r, 0, k:] == 0).all()
+        t = torch.tensor(table[r])
+        old = pools[0][t[src // PAGE], 0, src % PAGE]
+        assert same(gp[0][gt[r, :tiles(k)].long()].cpu()[:, 0].flatten(0, 1)[:k].contiguous(), old.contiguous())
+
+
+def test_streams_and_graphs(ss):
+    rng = np.random.default_rng(26)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    states = [make(rng, [700, 400 + i], 2, 2, 64, shared=1) for i in range(2)]
+    cuda = [([p.cuda() for p in s[0]], [w.cuda() for w in s[1]], ints(s[2]), ints(s[3]), ints(s[4])) for s in states]
+    out = [dict(out_weights=[torch.zeros_like(w) for w in c[1]], out_refs=torch.zeros_like(c[2]), out_table=torch.zeros_like(c[3]),
+                out_lens=torch.zeros_like(c[4])) for c in cuda]
+    keep = ints([300, 200])
+    saved = [[p.clone() for p in c[0]] for c in cuda]
+    graphs = []
+    for c, o in zip(cuda, out):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            ss.pages_evict(*c, keep, recent=8, **o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ss.pages_evict(*c, keep, recent=8, **o)
+        graphs.append(g)
+    for turn in range(2):
+        for c, s in zip(cuda, saved):
+            for p, x in zip(c[0], s):
+                p.copy_(x)
+        keep.copy_(torch.tensor([300 - 50 * turn, 200 + 9 * turn]))
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        for s, c, o in zip(states, cuda, out):
+            pools, weights = [p.clone() for p in s[0]], [w.clone() for w in s[1]]
+            want, refs, table, lens = evict(pools, weights, s[2], s[3], s[4], keep.tolist(), 8)
+            assert want == 0 and o["out_refs"].tolist() == refs and o["out_table"].tolist() == table
+            assert all(same(a, b) for a, b in zip(c[0], pools)) and all(same(a, b) for a, b in zip(o["out_weights"], weights))

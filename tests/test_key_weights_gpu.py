@@ -87,3 +87,103 @@ SIZES = [  # new tokens, keys, Hq, Hkv, d
 def test_against_64_bits(ss, n, L, Hq, Hkv, d, causal):
     rng = np.random.default_rng(sum(n) + sum(L))
     check(ss, *make(rng, n, L, Hq, Hkv, d, pad=3, extra=2), causal=causal)
+
+
+def test_the_same_from_run_to_run_streams_and_graphs(ss):
+    rng = np.random.default_rng(1)
+    batches = [make(rng, [40, 200 + i, 1], [3000, 700, 129], 8, 2, 128) for i in range(2)]
+
+    def run(x, stream=None, w=None):
+        q, kp, table, cu, lens = x
+        w = torch.zeros(3, 2, table.shape[1] * PAGE, device="cuda") if w is None else w
+        return ss.key_weights(q, kp, table, cu, lens, w, scale=0.1, stream=stream)
+
+    want = [run(x) for x in batches]
+    assert all(torch.equal(run(x), y) for x, y in zip(batches, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    room = [[torch.zeros_like(y) for _ in range(8)] for y in want]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i in range(2):
+            run(batches[i], streams[i] if k % 2 else streams[i].cuda_stream, room[i][k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, want[i]) for i in range(2) for w in room[i])
+    graphs, outs = [], []
+    for x in batches:
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            run(x)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(x))
+        graphs.append(g)
+    for turn in range(2):
+        for x in batches:
+            x[0].copy_(torch.randn(x[0].shape, device="cuda"))
+            x[4][0] -= 100 * turn
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for x, w in zip(batches, outs):
+            assert torch.equal(w, run(x))
+    assert ss.stream_status() is None
+
+
+def test_single_tokens_as_in_the_decode(ss):
+    """One token a sequence: the weights that the decode records."""
+    rng = np.random.default_rng(2)
+    q, kp, table, cu, lens = make(rng, [1] * 7, [1, 128, 300, 999, 5, 640, 2000], 8, 2, 128)
+    W = table.shape[1] * PAGE
+    a, b = torch.zeros(7, 2, W, device="cuda"), torch.zeros(7, 2, W, device="cuda")
+    ss.key_weights(q, kp, table, cu, lens, a, scale=0.1)
+    ss.decode_shared(q, kp, torch.nan_to_num(kp), table, lens, None, scale=0.1, weights=b)
+    # both are off by the same tolerances as against 64 bits: below 2^-15 here (scores of at most 12)
+    assert ((a - b).abs() <= 2.0 ** -14 * b + 1e-12).all()
+
+
+def test_more_tokens_than_a_share_and_many_sequences(ss):
+    rng = np.random.default_rng(3)
+    n = [int(x) for x in rng.integers(0, 6, 300)]
+    L = [int(x) + y for x, y in zip(rng.integers(0, 400, 300), n)]
+    check(ss, *make(rng, n, L, 4, 2, 64, pad=5))
+    check(ss, *make(rng, [64], [60000], 4, 1, 128))
+
+
+def test_one_sequence_cannot_reach_another(ss):
+    """Infinities and NaN in one sequence's keys or queries change nothing for the others, bit for bit."""
+    rng = np.random.default_rng(4)
+    q, kp, table, cu, lens = make(rng, [30, 9, 70], [500, 300, 70], 6, 2, 64)
+    run = lambda q, kp: ss.key_weights(q, kp, table, cu, lens, torch.zeros(3, 2, table.shape[1] * PAGE, device="cuda"), scale=0.1)  # noqa: E731
+    clean = run(q, kp)
+    for b in range(3):
+        for bad in (math.nan, math.inf):
+            q2, k2 = q.clone(), kp.clone()
+            q2[int(cu[b]) + 3, 1] = bad
+            k2[int(table[b, 0]), :, 5] = bad
+            got = run(q2, k2)
+            others = [i for i in range(3) if i != b]
+            assert torch.equal(got[others], clean[others])
+
+
+def test_workspace_of_larger_sizes(ss):
+    from block_sparse_attention_sm_gb300 import capi
+
+    rng = np.random.default_rng(5)
+    x = make(rng, [20, 3], [400, 100], 8, 2, 128)
+    ws = torch.full((capi.ss_attn_key_weights_workspace_size(500, 64, 8, 2),), 255, dtype=torch.uint8, device="cuda")
+    check(ss, *x, workspace=ws)
+    with pytest.raises(ss.SSError, match="workspace"):
+        check(ss, *x, workspace=ws[:4096])
+
+
+def test_pages_beyond_32_bits(ss):
+    Hkv, d, pages = 8, 128, 17000
+    kp = torch.empty((pages, Hkv, PAGE, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[pages - 1, 3, pages - 2], [5, pages - 3, 0]], dtype=torch.int32, device="cuda")
+    kp[table.long().unique()] = torch.randn(6, Hkv, PAGE, d, device="cuda").to(torch.bfloat16)
+    q = torch.randn(50, 16, d, device="cuda").to(torch.bfloat16)
+    check(ss, q, kp, table, offsets([10, 40]).cuda(), torch.tensor([300, 384], dtype=torch.int32, device="cuda"))
