@@ -15,6 +15,7 @@ struct KeyWeightsParams {
   int num_pages, max_pages;
   int causal;
   int ctas;
+  int whole;               // items are not cut
   float scale_log2;
   const int32_t* cu_seqlens;
   const int32_t* seq_lens;

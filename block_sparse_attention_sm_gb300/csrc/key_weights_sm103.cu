@@ -163,6 +163,9 @@ __device__ __forceinline__ float row_lse(float m, float l, float sl2) {
 // What an item costs besides its steps (its fixed tiles, its results), in steps: causal
 // pairs at the short end are many (a CTA that had them ended 20% later than others).
 constexpr int kItemCost = 2;
+// Items of few steps are not cut (each belongs to the CTA whose share it begins in): that
+// spares the launch that joins the parts, 3 us of ~25 on small steps.
+constexpr int kWholeSteps = 16;
 // Cost of all pairs below i.  Step u of pair i is at cost_below(i) + kItemCost + u, and
 // belongs to the CTA whose share that lies in.
 template <bool ROWS>
@@ -466,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           while (b >= 0) {
             const int steps = steps_of<ROWS>(p, s, pair);
-            if (begin >= end) break;
-            if (at < begin + steps) {
-              const int u = static_cast<int>(max(0ll, at - begin));
-              x.n = static_cast<int>(min(static_cast<long long>(steps), end - begin)) - u;
+            if (begin - (p.whole ? kItemCost : 0) >= end) break;
+            if (p.whole ? at <= begin - kItemCost && steps > 0 : at < begin + steps) {
+              const int u = p.whole ? 0 : static_cast<int>(max(0ll, at - begin));
+              x.n = p.whole ? steps : static_cast<int>(min(static_cast<long long>(steps), end - begin)) - u;
               x.u0 = u;
               x.steps = steps;
               x.b = b;
@@ -740,7 +743,7 @@ cudaError_t launch_pass(const CUtensorMap& tq, const CUtensorMap& tk, const KeyW
   } else {
     e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tq, tk, p);
   }
-  return e != cudaSuccess ? e : launch_behind(join_kernel<ROWS>, p.ctas, kPair, 0, st, p);
+  return e != cudaSuccess || p.whole ? e : launch_behind(join_kernel<ROWS>, p.ctas, kPair, 0, st, p);
 }
 
 constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -767,8 +770,10 @@ cudaError_t launch_key_weights(int d, const CUtensorMap& tq, const CUtensorMap& 
                                cudaStream_t st) {
   KeyWeightsParams p = p0;
   p.ctas = kSMs;
+  p.whole = p.max_pages <= kWholeSteps;  // (tiles of keys that a pair of row blocks sees)
   cudaError_t e = d == 128 ? launch_pass<128, true>(tq, tk, p, st) : launch_pass<64, true>(tq, tk, p, st);
   if (e != cudaSuccess) return e;
+  p.whole = (p.T + p.tpb - 1) / p.tpb <= kWholeSteps;  // (row blocks that see a pair of tiles)
   return d == 128 ? launch_pass<128, false>(tq, tk, p, st) : launch_pass<64, false>(tq, tk, p, st);
 }
 

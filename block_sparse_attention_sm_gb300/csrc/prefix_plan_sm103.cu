@@ -19,7 +19,7 @@
 namespace ssattn {
 namespace {
 
-constexpr int kRank = 512;
+constexpr int kRank = 1024;
 constexpr int kTree = 1024;
 
 __device__ __forceinline__ int full_pages(int len, int max_pages) {

@@ -162,16 +162,16 @@ __device__ __forceinline__ Node node_of(const SharedParams& p, const int32_t* pl
   return x;
 }
 
-// How a node's rows are dealt to items, and an item's rows in the partial results.
+// How a node's rows are dealt to items (whole places), and an item's rows in the partial results.
 struct Deal {
   int blocks, rows;   // items a KV head, rows of an item (the last may have fewer)
   int part;           // partial rows of a piece: two results each where the streams take alternate tiles
 };
 __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
-  const int all = x.count * G;
+  const int most = kRows / G;
   Deal d;
-  d.blocks = max(1, (all + kRows - 1) / kRows);
-  d.rows = (all + d.blocks - 1) / d.blocks;
+  d.blocks = max(1, (x.count + most - 1) / most);
+  d.rows = (x.count + d.blocks - 1) / d.blocks * G;
   d.part = d.rows <= kTile ? 2 * d.rows : d.rows;
   return d;
 }
@@ -736,34 +736,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool some = mine && !(m_used == -INFINITY && l == 0.f);  // (a row of NaN has a sum of NaN)
           if (any) {
             tc_fence_after();
-            // 32 columns at a time: eight lanes turn their rows' eight 16-byte words around
-            // (word j of row i to lane j), so that they write whole 128-byte lines.
-            const long long first = out - (lane & 7);
-            const uint32_t live = __ballot_sync(0xffffffffu, some) >> (lane & 24);  // of the eight lanes' rows
+            const uint32_t all = __ballot_sync(0xffffffffu, some);
+            if (__popc(all) <= 8) {  // few rows: as they lie, 32 bytes a lane at a time
+              float* to = p.part_o + out * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32p(colO + c, o);
-              tmem_wait_ld();
+              for (int c = 0; c < D && all != 0; c += 32) {
+                uint32_t o[32];
+                tmem_ld32p(colO + c, o);
+                tmem_wait_ld();
+                if (some)
 #pragma unroll
-              for (int h = 1; h < 8; h <<= 1) {
-                const bool upper = (lane & h) != 0;
+                  for (int e = 0; e < 32; e += 8) store8(to + c + e, o + e);
+              }
+            } else {
+              // 32 columns at a time: eight lanes turn their rows' eight 16-byte words around
+              // (word j of row i to lane j), so that they write whole 128-byte lines.
+              const long long first = out - (lane & 7);
+              const uint32_t live = all >> (lane & 24);  // of the eight lanes' rows
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32p(colO + c, o);
+                tmem_wait_ld();
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                  if (w & h) continue;
+                for (int h = 1; h < 8; h <<= 1) {
+                  const bool upper = (lane & h) != 0;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    uint32_t &lo = o[4 * w + e], &hi = o[4 * (w | h) + e];
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, h);
-                    if (upper) lo = got; else hi = got;
+                  for (int w = 0; w < 8; ++w) {
+                    if (w & h) continue;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      uint32_t &lo = o[4 * w + e], &hi = o[4 * (w | h) + e];
+                      const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, h);
+                      if (upper) lo = got; else hi = got;
+                    }
                   }
                 }
-              }
-              float* to = p.part_o + first * D + c + 4 * (lane & 7);
+                float* to = p.part_o + first * D + c + 4 * (lane & 7);
 #pragma unroll
-              for (int w = 0; w < 8; ++w)
-                if ((live >> w) & 1u)
-                  *reinterpret_cast<uint4*>(to + w * D) = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                for (int w = 0; w < 8; ++w)
+                  if ((live >> w) & 1u)
+                    *reinterpret_cast<uint4*>(to + w * D) = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+              }
             }
           }
           if (mine) p.part_ml[out] = make_float2(m_used == -INFINITY ? -INFINITY : m_used * sl2, l);
@@ -885,20 +899,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The partial results of a row: those of its own tiles and of the nodes above its
 // place, whose items were cut into pieces.  One block a (place, head): eight lanes
-// find the pieces (a level each), then a thread a piece has its weight, then a
-// thread a column adds up.
-template <int D>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p, int ctas) {
-  constexpr int L = 1 + kPlanLevels;
+// find the pieces (a level each), a thread a piece has its weight, and a warp takes
+// every fourth or eighth piece, columns a lane; the warps' sums are added in order.
+// 256 threads as long as all blocks are resident (28 heads x 24 places: 7.0 us, with
+// 128 threads 8.5), 128 beyond (32 heads x 64 places: 9.9 us, with 256 threads 15.7).
+template <int D, int kMerge>
+__global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p, int ctas) {
+  constexpr int L = 1 + kPlanLevels, E = D / 32, W = kMerge / 32;
   __shared__ long long s_row[L];               // a level's first partial row, of its first CTA
-  __shared__ int s_second[L], s_start[L + 1]; // the second stream's distance (0: one result a piece), results in front
-  __shared__ float s_w[128], s_red[2][4], s_o[128];
-  __shared__ long long s_at[128];
+  __shared__ int s_second[L], s_start[L + 1];  // the second stream's distance (0: one result a piece), results in front
+  __shared__ float s_red[2][W], s_w[kMerge], s_o[W][D];
+  __shared__ long long s_at[kMerge];
   let_next_start();
   wait_for_previous();
   const int32_t* plan = valid_plan(p);
-  const int i = blockIdx.x / p.Hq, h = blockIdx.x - i * p.Hq;
-  const int kvh = h / p.G, g = h - kvh * p.G;
+  const int G = p.G, i = blockIdx.x / p.Hq, h = blockIdx.x - i * p.Hq, kvh = h / G, g = h - kvh * G;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = place_of(plan, i, p.B);
   if (warp == 0) {
@@ -906,26 +921,26 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
     long long row = 0;
     uint32_t a = 0, z = 0;  // cost in front of the row's first tile, of its last
     if (lane == 0) {
-      const int nb = kTile / p.G, j0 = i / nb * nb, places = min(nb, p.B - j0);
+      const int nb = kTile / G, j0 = i / nb * nb, places = min(nb, p.B - j0);
       const uint32_t base = p.cum[j0], T = p.cum[j0 + places] - base, c0 = p.cum[i], n = p.cum[i + 1] - c0;
       if (n > 0) {
         a = (base * p.Hkv + kvh * T + (c0 - base)) * kTileCost;
         z = a + (n - 1) * kTileCost;
-        row = 2ll * p.G * p.Hkv * j0 + 2ll * kvh * places * p.G + (i - j0) * p.G + g;
-        second = places * p.G;
+        row = 2ll * G * p.Hkv * j0 + (2ll * kvh * places + (i - j0)) * G + g;
+        second = places * G;
         parts = 1;
       }
     } else if (lane < L && plan != nullptr) {
       const int n = plan[kPlanHead + p.B + 2l * p.B * kNodeWords + static_cast<long>(i) * kPlanLevels + lane - 1];
       if (n >= p.B && n < 2 * p.B) {
         const Node x = node_of(p, plan, n);
-        const int T = x.t1 - x.t0, r = (i - x.first) * p.G + g;
-        if (T > 0 && r >= 0 && r < x.count * p.G && length_of(p, b) > 0) {
-          const Deal d = deal_of(x, p.G);
-          const int blk = r / d.rows, item = kvh * d.blocks + blk, cost = cost_of(d);
+        const int T = x.t1 - x.t0, place = i - x.first;
+        if (T > 0 && place >= 0 && place < x.count && length_of(p, b) > 0) {
+          const Deal d = deal_of(x, G);
+          const int blk = place * G / d.rows, item = kvh * d.blocks + blk, cost = cost_of(d);
           a = p.node_at[n - p.B] + item * T * cost;
           z = a + (T - 1) * cost;
-          row = p.node_rows[n - p.B] + static_cast<long long>(item) * d.part + (r - blk * d.rows);
+          row = p.node_rows[n - p.B] + static_cast<long long>(item) * d.part + (place * G + g - blk * d.rows);
           second = d.rows > kTile ? 0 : d.rows;
           parts = 1;
         }
@@ -935,7 +950,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
       const uint32_t per = share_of(*p.total, ctas);
       const int c0 = a / per, c1 = z / per;
       row += static_cast<long long>(c0) * kRows;
-      parts = min(ctas, c1 - c0 + 1) * (second > 0 ? 2 : 1);
+      parts = max(0, min(ctas, c1 - c0 + 1)) * (second > 0 ? 2 : 1);
     }
     int sum = parts;
 #pragma unroll
@@ -952,10 +967,11 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
   }
   __syncthreads();
   const int all = s_start[L];
-  constexpr int R = 128 / D;  // threads a column
-  const int column = tid % D;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int q0 = 0; q0 < all; q0 += 128) {
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int q0 = 0; q0 < all; q0 += kMerge) {
     const int q = q0 + tid;
     long long at = -1;
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -974,7 +990,9 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
     if (lane == 0) s_red[0][warp] = top;
     __syncthreads();
-    const float now = fmaxf(m, fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3])));
+    float now = m;
+#pragma unroll
+    for (int k = 0; k < W; ++k) now = fmaxf(now, s_red[0][k]);
     // (a row of NaN has no maximum and a sum of NaN)
     const float w = at < 0 ? 0.f : ex2_approx(ml.x - now), keep = m == -INFINITY ? 1.f : ex2_approx(m - now);
     float sum = at < 0 ? 0.f : w * ml.y;
@@ -984,25 +1002,41 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p,
     s_w[tid] = w;
     s_at[tid] = at;
     __syncthreads();
-    l = l * keep + ((s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]));
-    o *= keep;
+    l *= keep;
+#pragma unroll
+    for (int k = 0; k < W; ++k) l += s_red[1][k];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
     m = now;
-    const int n = min(128, all - q0);
-#pragma unroll 8
-    for (int k = tid / D; k < n; k += R) {
+    const int n = min(kMerge, all - q0);
+#pragma unroll 4
+    for (int k = warp; k < n; k += W) {
       const long long from = s_at[k];
-      if (from >= 0) o += s_w[k] * p.part_o[from * D + column];
+      if (from >= 0) {
+        const float ws = s_w[k];
+        const float* in = p.part_o + from * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(in);
+          o[0] += ws * v.x, o[1] += ws * v.y, o[2] += ws * v.z, o[3] += ws * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(in);
+          o[0] += ws * v.x, o[1] += ws * v.y;
+        }
+      }
     }
     __syncthreads();
   }
-  if (R > 1) {
-    s_o[tid] = o;
-    __syncthreads();
-    o = s_o[column] + s_o[(column + D) % 128];
-  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  __syncthreads();
   const size_t to = static_cast<size_t>(b) * p.Hq + h;
-  // (a sequence without keys: zeros; NaN stays)
-  if (tid < D) p.o[to * D + column] = __float2bfloat16(l == 0.f ? 0.f : o / l);
+  if (tid < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) v += s_o[k][tid];
+    // (a sequence without keys: zeros; NaN stays)
+    p.o[to * D + tid] = __float2bfloat16(l == 0.f ? 0.f : v / l);
+  }
   if (p.lse != nullptr && tid == 0) p.lse[to] = m + log2f(l);
 }
 
@@ -1052,7 +1086,9 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Share
   if (e != cudaSuccess) return e;
   e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tk, tv, p);
   if (e != cudaSuccess) return e;
-  e = launch_behind(shared_merge_kernel<D>, static_cast<unsigned>(p.B) * p.Hq, 128, 0, st, p, p.ctas);
+  const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
+  e = rows <= 8 * kSMs ? launch_behind(shared_merge_kernel<D, 256>, rows, 256, 0, st, p, p.ctas)
+                       : launch_behind(shared_merge_kernel<D, 128>, rows, 128, 0, st, p, p.ctas);
   if (e != cudaSuccess || p.weights == nullptr) return e;
   const int blocks = (p.max_pages + 7) / 8;
   return launch_behind(weigh_kernel, dim3(blocks < 64 ? blocks : 64, p.Hkv, p.B), 256, 0, st, p);
