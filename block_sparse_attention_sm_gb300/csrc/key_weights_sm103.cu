@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int kRing = (D == 128) ? 3 : 6;  // streamed tiles
   static constexpr int kRingOff = 4 * kTileBytes;   // behind two pairs of fixed tiles
   static constexpr int kCtlOff = kRingOff + kRing * kTileBytes;
-  static constexpr int kCtlBytes = (D == 128) ? 3072 : 4096;
+  static constexpr int kCtlBytes = (D == 128) ? 3 * 1024 : 4 * 1024;
   static constexpr int kSmemBytes = kCtlOff + kCtlBytes;  // (the base is a multiple of 1024: checked)
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };

@@ -177,8 +177,9 @@ __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
 }
 
 // Cost of a tile, in the shares of the CTAs: where both streams take every tile it is
-// ~3700 cycles, else the ~2700 of its bytes (both measured).
-constexpr int kTileCost = 2, kBothCost = 3;
+// about twice that of its bytes alone (2:3, 4:7, 1:2, 5:11 and 1:1 give 337, 331, 317, 320 and 379 us at
+// four layers of 64 sequences on a prefix of 32K keys).
+constexpr int kTileCost = 1, kBothCost = 2;
 __device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : kTileCost; }
 // A CTA's share of all items' cost (at least a tile, so that each CTA between an item's
 // first and last has a part of it).  Costs fit 31 bits (kMaxSharedTiles).
