@@ -26,9 +26,18 @@
 // them in order (results do not depend on timing).
 //
 // One CTA: two streams t, each with a fixed tile, two score buffers in TMEM and
-// a reducing warpgroup.  In the rows' pass a pair whose tokens fit one block has
-// both streams take alternate tiles of keys against that block instead.
-// Warps 0-3 / 4-7 reduce, 8 loads, 9 and 11 issue the MMAs of stream 0 and 1, 10 works out the pieces.
+// two reducing warpgroups, one for each half of the columns (four in all hide one
+// another's waits: two prompts of 8K 825 us, two of whole rows 842 us).  A pair of one
+// block of rows, or of one tile of keys, has both streams take alternate streamed tiles
+// against that one instead.  Warps 0-15 reduce (stream 0, 1, 0, 1; the second pair the
+// second half), 16 loads, 17 and 19 issue the MMAs of stream 0 and 1, 18 works out the pieces.
+//
+// Bound: per step of two tiles the MMAs take ~1230 cycles (their operands come from shared
+// memory; alone 265 us for the rows of two prompts of 8K) and the exponentials 1024.  The
+// kernel is at ~1800: the two do not overlap fully, each tile's wait and load of the scores
+// (~300 cycles each) lies between them.  Measured and not taken: loads a chunk of 32
+// columns ahead of the reduction (20% more time), 512 fixed rows an item, which halves what
+// is streamed (25% more: the streamed tiles are not the bound).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -41,13 +50,14 @@ namespace ssattn {
 namespace {
 
 constexpr int kSMs = 152;
-constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10, kWarpMma2 = 11;
+constexpr int kThreads = 640;
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpPlan = 18, kWarpMma2 = 19;
+constexpr int kHalf = kTile / 2;  // columns of a reducing warpgroup
 constexpr int kPieces = 3;
 constexpr int kPair = 2 * kTile;
 constexpr float kSlackLog2 = 40.0f;  // how far exponentials may be above 1 (exp2 domain)
-constexpr int kLaunchRegs = 168, kRegsIssue = 88, kRegsSoftmax = 208;
-static_assert(128 * kRegsIssue + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
+constexpr int kLaunchRegs = 96, kRegsIssue = 64, kRegsReduce = 104;
+static_assert(128 * kRegsIssue + 512 * kRegsReduce == kThreads * kLaunchRegs, "register split");
 
 template <int D>
 struct Cfg {
@@ -192,7 +202,8 @@ struct Ctl {
   uint64_t f_full[2], f_empty[2];
   uint64_t s_full[4], s_empty[4];  // [stream * 2 + buffer]
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  uint64_t hand_full, hand_empty;
+  uint64_t hand_full[2], hand_empty[2];  // a stream's second half of the columns to its first
+  uint64_t cross_full;                   // alternate tiles: stream 1 to stream 0
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -201,8 +212,17 @@ struct Ctl {
   long long at;       // whose first step is number `at` of all
   long long total;
   Piece piece[kPieces];
-  alignas(16) float lse[3][kTile];  // keys' pass: the rows' lse, per ring entry % 3
-  float2 hand[kTile];   // alternate tiles: stream 1's results (before: the warps' sums over the batch)
+  union {
+    struct {
+      alignas(16) float lse[3][kTile];  // the rows' lse, per ring entry % 3
+      float sum[2][kTile];              // a stream's results on their way
+    } keys;
+    float2 rows[2][kTile];
+    struct {
+      float used[3 * kTile];            // (left to the copies of the lse)
+      long long scan[kThreads / 32];    // the warps' sums over the batch
+    } start;
+  } hand;
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
@@ -244,15 +264,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl->s_full[s], 1);
-      mbar_init(&ctl->s_empty[s], 4);
+      mbar_init(&ctl->s_empty[s], 8);
     }
     for (int s = 0; s < kPieces; ++s) {
       mbar_init(&ctl->piece_full[s], 1);
-      mbar_init(&ctl->piece_empty[s], 11);
+      mbar_init(&ctl->piece_empty[s], 19);
     }
-    for (int s = 0; s < 6; ++s) mbar_init(&ctl->lse_empty[s >> 1][s & 1], 4);
-    mbar_init(&ctl->hand_full, 4);
-    mbar_init(&ctl->hand_empty, 4);
+    for (int s = 0; s < 6; ++s) mbar_init(&ctl->lse_empty[s >> 1][s & 1], 8);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->hand_full[s], 4);
+      mbar_init(&ctl->hand_empty[s], 4);
+    }
+    mbar_init(&ctl->cross_full, 4);
     mbar_init(&ctl->mma_done[0], 1);
     mbar_init(&ctl->mma_done[1], 1);
     ctl->abort_flag = 0;
@@ -265,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   {  // every sequence's steps, added up
-    long long* scan = reinterpret_cast<long long*>(ctl->hand);
+    long long* scan = ctl->hand.start.scan;
     const int each = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     auto cost = [&](int b) {
       const Seq s = seq_of(p, b);
@@ -313,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     setmaxnreg_dec<kRegsIssue>();
     if (warp == kWarpLoad) {
       // ---------------------------------------------------------- loader
@@ -386,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_keys(sR + st * C::kTileBytes, &ctl->r_full[st], x, page);
             } else {
               load_queries(sR + st * C::kTileBytes, &ctl->r_full[st], x, u);
-              bulk_load(ctl->lse[ls], lse_of + static_cast<long>(u) * kTile, kTile * sizeof(float), &ctl->r_full[st]);
+              bulk_load(ctl->hand.keys.lse[ls], lse_of + static_cast<long>(u) * kTile, kTile * sizeof(float), &ctl->r_full[st]);
             }
             *reinterpret_cast<volatile int*>(&ctl->r_issued) = e + 1;
           }
@@ -396,30 +419,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMAs of stream t
       // An issuer each: one's waits and commits run beside the other's MMAs.  Both
       // pass every streamed tile in order.
-      if (lane == 0) {
-        const int t = warp == kWarpMma ? 0 : 1;
-        constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const uint64_t df0 = smem_desc(smem_u32(sF), 16, 1024), dr0 = smem_desc(smem_u32(sR), 16, 1024);
-        uint32_t slot = 0, par = 0, sn = 0;
-        bool ok = true;
+      const int t = __shfl_sync(0xffffffffu, warp == kWarpMma ? 0 : 1, 0);
+      constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+      const uint64_t df0 = smem_desc(smem_u32(sF), 16, 1024), dr0 = smem_desc(smem_u32(sR), 16, 1024);
+      uint32_t slot = 0, par = 0, sn = 0;
+      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort_flag));
+      };
+      bool ok = true;
 #pragma unroll 1
-        for (int k = 0; ok; ++k) {
-          if (!mbar_wait_small(&ctl->piece_full[k % kPieces], (k / kPieces) & 1, abort_flag)) break;
-          const int n = ctl->piece[k % kPieces].n;
-          const bool both = ctl->piece[k % kPieces].both != 0;
-          if (n == 0) break;
-          mbar_arrive(&ctl->piece_empty[k % kPieces]);
-          ok = mbar_wait_small(&ctl->f_full[k & 1], (k >> 1) & 1, abort_flag);
-          const uint64_t df = df0 + (((k & 1) * 2 + (both ? t : 0)) * C::kTileBytes >> 4);
+      for (int k = 0; ok; ++k) {
+        if (!wwait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1)) break;
+        const int n = __shfl_sync(0xffffffffu, ctl->piece[k % kPieces].n, 0);
+        const bool both = __shfl_sync(0xffffffffu, ctl->piece[k % kPieces].both, 0) != 0;
+        if (n == 0) break;
+        if (elect_one()) mbar_arrive(&ctl->piece_empty[k % kPieces]);
+        __syncwarp();
+        ok = wwait(&ctl->f_full[k & 1], (k >> 1) & 1);
+        const uint64_t df = df0 + (((k & 1) * 2 + (both ? t : 0)) * C::kTileBytes >> 4);
 #pragma unroll 1
-          for (int i = 0; ok && i < n; ++i) {
-            if (!(ok = mbar_wait_small(&ctl->r_full[slot], par, abort_flag))) break;
-            if (both || (i & 1) == t) {
-              const uint32_t buf = sn & 1;
-              if (!(ok = mbar_wait_small(&ctl->s_empty[2 * t + buf], ((sn >> 1) & 1) ^ 1, abort_flag))) break;
-              ++sn;
-              tc_fence_after();
-              const uint64_t dr = dr0 + slot * (C::kTileBytes >> 4);
+        for (int i = 0; ok && i < n; ++i) {
+          if (!(ok = wwait(&ctl->r_full[slot], par))) break;
+          if (both || (i & 1) == t) {
+            const uint32_t buf = sn & 1;
+            if (!(ok = wwait(&ctl->s_empty[2 * t + buf], ((sn >> 1) & 1) ^ 1))) break;
+            ++sn;
+            tc_fence_after();
+            const uint64_t dr = dr0 + slot * (C::kTileBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
@@ -427,13 +454,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               mma_commit(&ctl->s_full[2 * t + buf]);
               mma_commit(&ctl->r_empty[slot]);
-            } else {
-              mbar_arrive(&ctl->r_empty[slot]);
             }
-            if (++slot == NR) slot = 0, par ^= 1;
+            __syncwarp();
+          } else {
+            if (elect_one()) mbar_arrive(&ctl->r_empty[slot]);
+            __syncwarp();
           }
-          if (ok) mma_commit(&ctl->f_empty[k & 1]);
+          if (++slot == NR) slot = 0, par ^= 1;
         }
+        if (ok && elect_one()) mma_commit(&ctl->f_empty[k & 1]);
+        __syncwarp();
+      }
+      if (elect_one()) {
         mma_commit(&ctl->mma_done[t]);
         mbar_wait(&ctl->mma_done[t], 0, nullptr);
       }
@@ -530,25 +562,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_dealloc(tmem, 512);
     }
   } else {
-    // ---------------------------------------------------------- reduction of stream t
-    setmaxnreg_inc<kRegsSoftmax>();
-    const int t = warp >> 2, row = tid & 127;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * t;
+    // ---------------------------------------------------------- reduction of stream t, half h of its columns
+    setmaxnreg_inc<kRegsReduce>();
+    const int t = (warp >> 2) & 1, h = warp >> 3, row = tid & 127;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * t + kHalf * h;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f32x2(sl2, sl2);
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort_flag));
     };
-    uint32_t sn = 0, hn = 0;
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    uint32_t sn = 0, hn = 0, cn = 0;
     int e0 = 0;  // ring entries of the pieces before
     bool ok = true;
 #pragma unroll 1
-    for (int k = 0; ok; ++k) {
-      Piece x;
-      ok = __all_sync(0xffffffffu, piece_at(k, &x));
-      if (!ok || x.n == 0) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->piece_empty[k % kPieces]);
+    for (int k = 0; ok; ++k, ++hn) {
+      ok = wwait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1);
+      const Piece& x = ctl->piece[k % kPieces];
+      const int n = x.n;
+      if (!ok || n == 0) break;
       const bool alone = !x.both;
       // (keys: a pair of one tile has the second stream take alternate blocks of rows as well)
       const int ft = alone ? 0 : t;                       // this stream's fixed tile
@@ -559,8 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_live = ROWS && row < q_rows && token < x.toks;
       const int lim = !row_live ? -1 : p.causal ? min(x.len - 1, x.off + token) : x.len - 1;
       const int key = (2 * x.pair + ft) * kTile + row;
+      const int u0 = x.first + x.u0, toks = x.toks, ahead = key - x.off;  // keys: the first token that sees the key
 #pragma unroll 1
-      for (int i = alone ? t : 0; i < x.n; i += alone ? 2 : 1) {
+      for (int i = alone ? t : 0; i < n; i += alone ? 2 : 1) {
         const uint32_t buf = sn & 1;
         if (!wwait(&ctl->s_full[2 * t + buf], (sn >> 1) & 1)) {
           ok = false;
@@ -568,19 +604,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++sn;
         tc_fence_after();
-        uint32_t sr[128];
+        uint32_t sr[kHalf];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32p(lane_base + 128 * buf + 32 * c, sr + 32 * c);
+        for (int c = 0; c < 2; ++c) tmem_ld32p(lane_base + 128 * buf + 32 * c, sr + 32 * c);
         tmem_wait_ld();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->s_empty[2 * t + buf]);
-        const int u = x.first + x.u0 + i;
+        arrive(&ctl->s_empty[2 * t + buf]);
+        const int u = u0 + i;
         if (ROWS) {
-          const int vis = min(kTile - 1, lim - u * kTile);  // last visible column
-          if (__any_sync(0xffffffffu, vis < kTile - 1)) {
+          const int vis = min(kHalf - 1, lim - u * kTile - kHalf * h);  // last visible column
+          if (__any_sync(0xffffffffu, vis < kHalf - 1)) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
+            for (int e = 0; e < kHalf; ++e)
               if (e > vis) sr[e] = __float_as_uint(-INFINITY);
           }
           // The reference m_used is the maximum of the row's first tile as long as no
@@ -593,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t ls[2] = {0ull, 0ull};
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
+            for (int c = 0; c < kHalf / 2; ++c) {
               const float s0 = __uint_as_float(sr[2 * c]), s1 = __uint_as_float(sr[2 * c + 1]);
               mx[c & 1] = fmax3(mx[c & 1], s0, s1);
               const uint64_t xp = fma_f32x2(f32x2(s0, s1), sl2x2, nmb);
@@ -614,14 +649,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // columns: rows of block u of the queries; those that see the key are [lo, hi)
           const int i0 = u * p.tpb, ls_at = (e0 + i) % 3;
-          const int hi = min(q_rows, (x.toks - i0) * p.G);
-          const int lo = p.causal ? static_cast<int>(max(0ll, min(static_cast<long long>(kTile), (static_cast<long long>(key) - x.off - i0) * p.G))) : 0;
-          const float4* lse4 = reinterpret_cast<const float4*>(ctl->lse[ls_at]);
+          const int hi = min(q_rows, (toks - i0) * p.G) - kHalf * h;
+          const int lo = (p.causal ? static_cast<int>(max(0ll, min(static_cast<long long>(kTile), (static_cast<long long>(ahead) - i0) * p.G))) : 0) - kHalf * h;
+          const float4* lse4 = reinterpret_cast<const float4*>(ctl->hand.keys.lse[ls_at] + kHalf * h);
           uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
           // (a row that does not count may hold anything: its weight is dropped, not its score)
           auto add_up = [&](auto masked) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < kHalf / 4; ++c) {
               const float4 a = lse4[c];
               const uint64_t x0 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), sl2x2,
                                             f32x2(-a.x, -a.y));
@@ -638,57 +673,73 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls[2 + (c & 1)] = add_f32x2(ls[2 + (c & 1)], f32x2(w[2], w[3]));
             }
           };
-          if (__any_sync(0xffffffffu, hi < kTile || lo > 0))
+          if (__any_sync(0xffffffffu, hi < kHalf || lo > 0))
             add_up([] { return true; });
           else
             add_up([] { return false; });
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->lse_empty[ls_at][t]);
+          arrive(&ctl->lse_empty[ls_at][t]);
           const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
           sum[0] += f32x2_lo(s2);
           sum[1] += f32x2_hi(s2);
         }
       }
       if (!ok) break;
-      e0 += x.n;
-      // The item's result, or a part of it.
+      e0 += n;
+      // The item's result, or a part of it: the second half's to the first, where the
+      // streams alternate stream 1's to stream 0 (through the same place).
       float total = sum[0] + sum[1];
-      if (alone) {  // the other stream's share of the same rows
-        if (t == 1) {
-          if (!(ok = wwait(&ctl->hand_empty, (hn & 1) ^ 1))) break;
-          ctl->hand[row] = ROWS ? make_float2(m_used, l) : make_float2(total, 0.f);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->hand_full);
+      auto put = [&] {
+        if (ROWS) ctl->hand.rows[t][row] = make_float2(m_used, l);
+        else ctl->hand.keys.sum[t][row] = total;
+      };
+      auto add = [&](int from) {
+        if (ROWS) {
+          const float2 other = ctl->hand.rows[from][row];
+          join(m_used, l, other.x, other.y, sl2);
         } else {
-          if (!(ok = wwait(&ctl->hand_full, hn & 1))) break;
-          const float2 other = ctl->hand[row];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->hand_empty);
-          if (ROWS)
-            join(m_used, l, other.x, other.y, sl2);
-          else
-            total += other.x;
+          total += ctl->hand.keys.sum[from][row];
         }
-        ++hn;
-        if (t == 1) continue;
-      }
-      const bool whole = x.n == x.steps;
-      const long part = (2l * blockIdx.x + (x.u0 == 0 ? 1 : 0)) * kPair + ft * kTile + row;
-      if (ROWS) {
-        if (row_live) {
-          if (whole)
-            p.lse[(static_cast<long>(x.kvh) * p.places + x.place + x.pair) * kPair + ft * kTile + row] =
-                row_lse(m_used, l, sl2);
-          else
-            p.part_ml[part] = make_float2(m_used, l);
+      };
+      if (h == 1) {
+        if (!(ok = wwait(&ctl->hand_empty[t], (hn & 1) ^ 1))) break;
+        put();
+        arrive(&ctl->hand_full[t]);
+      } else {
+        if (!(ok = wwait(&ctl->hand_full[t], hn & 1))) break;
+        add(t);
+        if (alone && t == 1) {
+          put();
+          arrive(&ctl->cross_full);
+        } else {
+          arrive(&ctl->hand_empty[t]);
         }
-      } else if (key < x.len) {
-        if (whole)
-          // (one thread adds to a cell: the same as reading, adding and writing, without waiting)
-          atomicAdd(p.weights + (static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key, total);
-        else
-          p.part_w[part] = total;
+        if (alone && t == 0) {
+          if (!(ok = wwait(&ctl->cross_full, cn & 1))) break;
+          ++cn;
+          add(1);
+          arrive(&ctl->hand_empty[1]);
+        }
+        if (!(alone && t == 1)) {
+          const bool whole = n == x.steps;
+          const long part = (2l * blockIdx.x + (x.u0 == 0 ? 1 : 0)) * kPair + ft * kTile + row;
+          if (ROWS) {
+            if (row_live) {
+              if (whole)
+                p.lse[(static_cast<long>(x.kvh) * p.places + x.place + x.pair) * kPair + ft * kTile + row] =
+                    row_lse(m_used, l, sl2);
+              else
+                p.part_ml[part] = make_float2(m_used, l);
+            }
+          } else if (key < x.len) {
+            if (whole)
+              // (one thread adds to a cell: the same as reading, adding and writing, without waiting)
+              atomicAdd(p.weights + (static_cast<long>(x.b) * p.Hkv + x.kvh) * p.max_pages * kTile + key, total);
+            else
+              p.part_w[part] = total;
+          }
+        }
       }
+      arrive(&ctl->piece_empty[k % kPieces]);
     }
     __syncwarp();
     tc_fence_before();
