@@ -497,7 +497,8 @@ cudaError_t launch_pages_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   Call c{a.s, a.rows, a.keep, a.n, a.recent, a.Hkv, a.out_refs, a.out_table, a.out_lens, a.result};
   const int row_words = static_cast<int>(a.page_bytes / (static_cast<size_t>(a.Hkv) * kTile) / 16);
   cudaError_t e = cudaSuccess;
-  for (int l0 = 0; e == cudaSuccess && l0 < a.num_layers; l0 += group) {
+  // (with no sequence listed there is nothing but the state: one pair of launches)
+  for (int l0 = a.n > 0 ? 0 : (a.num_layers - 1) / group * group; e == cudaSuccess && l0 < a.num_layers; l0 += group) {
     Layers layers{};
     layers.count = a.num_layers - l0 < group ? a.num_layers - l0 : group;
     PagePools pools{};
@@ -510,7 +511,8 @@ cudaError_t launch_pages_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
     for (int q = 0; q < pools.count; ++q) pools.base[q] = static_cast<unsigned char*>(a.pools[l0 * a.per_layer + q]);
     const bool last = l0 + group >= a.num_layers;
     const long lists = static_cast<long>(a.n) * a.Hkv * layers.count, movers = static_cast<long>(a.n) * a.Hkv * pools.count;
-    choose_kernel<<<static_cast<unsigned>(lists + (l0 == 0)), kChoose, 0, st>>>(c, w, layers, l0 == 0);
+    const int plan_too = l0 == 0 || a.n == 0;
+    choose_kernel<<<static_cast<unsigned>(lists + plan_too), kChoose, 0, st>>>(c, w, layers, plan_too);
     if ((e = cudaGetLastError()) != cudaSuccess) break;
     // few movers share their rows' columns, in pieces of 64 bytes at least
     int slices = 1;

@@ -238,3 +238,12 @@ def test_streams_and_graphs(ss):
             want, refs, table, lens = evict(pools, weights, s[2], s[3], s[4], keep.tolist(), 8)
             assert want == 0 and o["out_refs"].tolist() == refs and o["out_table"].tolist() == table
             assert all(same(a, b) for a, b in zip(c[0], pools)) and all(same(a, b) for a, b in zip(o["out_weights"], weights))
+
+
+@pytest.mark.parametrize("layers", [1, 16, 17, 40])
+@pytest.mark.parametrize("out", [False, True])
+def test_nothing_listed(ss, layers, out):
+    """No sequence listed, layers of one launch and of several: the state is passed on as it is."""
+    rng = np.random.default_rng(25)
+    for rows in (None, []):
+        check(ss, make(rng, [200, 300], layers, 1, 8, shared=1), [], 3, rows=rows, out=out)
