@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import contextlib
+import functools
 
 import torch
 
@@ -421,7 +422,7 @@ def prefix_plan(page_table, seq_lens, *, out=None, stream=None):
     B, max_pages = page_table.shape
     _dense("seq_lens", seq_lens, _I32, None, (B,))
     lib = capi._lib or capi.load()
-    words = lib.ss_prefix_plan_size(B) // 4
+    words = _need("ss_prefix_plan_size", B) // 4
     if words == 0:
         raise ValueError(f"prefix_plan: {B} sequences (1 to 8192)")
     if out is not None:
@@ -440,9 +441,16 @@ def _recorded_weights(name, t, B, Hkv, max_pages):
     _dense(name, t, torch.float32, None, (B, Hkv, max_pages * 128))
 
 
-def _scratch(workspace, need, device):
+@functools.lru_cache(maxsize=4096)
+def _need(call, *sizes):
+    """Bytes that a call's workspace takes: a function of its sizes alone, and a call of its own to ask for."""
+    return getattr(capi._lib or capi.load(), call)(*sizes)
+
+
+def _scratch(workspace, device, call, *sizes):
     """(workspace, its bytes), made where it is not given."""
     if workspace is None:
+        need = _need(call, *sizes)
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device), need
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
@@ -496,7 +504,7 @@ def decode_shared(q, k_pages, v_pages, page_table, seq_lens, plan=None, *, scale
     _dense("v_pages", v_pages, _BF16, None, k_pages.shape)
     lib = capi._lib or capi.load()
     if plan is not None:
-        _dense("plan", plan, _I32, None, (lib.ss_prefix_plan_size(B) // 4,))
+        _dense("plan", plan, _I32, None, (_need("ss_prefix_plan_size", B) // 4,))
     if weights is not None:
         _recorded_weights("weights", weights, B, Hkv, max_pages)
     if out is not None:
@@ -507,8 +515,8 @@ def decode_shared(q, k_pages, v_pages, page_table, seq_lens, plan=None, *, scale
         o = out if out is not None else torch.empty((B, Hq, d), dtype=_BF16, device=q.device)
         if B == 0:
             return o
-        ws, nbytes = _scratch(workspace, lib.ss_attn_decode_shared_workspace_size(
-            B, Hq, Hkv, max_pages, d, plan is not None, weights is not None) if workspace is None else 0, q.device)
+        ws, nbytes = _scratch(workspace, q.device, "ss_attn_decode_shared_workspace_size", B, Hq, Hkv, max_pages, d,
+                              plan is not None, weights is not None)
         st = lib.ss_attn_decode_shared(
             q.data_ptr(), stride, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
             plan.data_ptr() if plan is not None else None, o.data_ptr(), weights.data_ptr() if weights is not None else None,
@@ -542,8 +550,7 @@ def key_weights(q, k_pages, page_table, cu_seqlens, seq_lens, weights, *, scale:
                           cu_seqlens, seq_lens, weights, workspace)
     with context:
         lib = capi._lib or capi.load()
-        ws, nbytes = _scratch(workspace, lib.ss_attn_key_weights_workspace_size(T, B, Hq, Hkv) if workspace is None else 0,
-                              q.device)
+        ws, nbytes = _scratch(workspace, q.device, "ss_attn_key_weights_workspace_size", T, B, Hq, Hkv)
         st = lib.ss_attn_key_weights(
             q.data_ptr(), stride, k_pages.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
             weights.data_ptr(), T, B, Hq, Hkv, num_pages, max_pages, d, scale, bool(causal), ws.data_ptr(), nbytes, handle)
@@ -755,8 +762,8 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
                           seq_lens, keep, rows, out_refs, out_table, out_lens, result, workspace, *pools, *weights, *moved)
     with context:
         lib = capi._lib or capi.load()
-        ws, nbytes = _scratch(workspace, lib.ss_pages_evict_workspace_size(
-            num_pages, num_rows, max_pages, n, Hkv, len(weights), len(pools)) if workspace is None else 0, page_refs.device)
+        ws, nbytes = _scratch(workspace, page_refs.device, "ss_pages_evict_workspace_size", num_pages, num_rows, max_pages, n,
+                              Hkv, len(weights), len(pools))
         if result is None:
             result = torch.empty(1, dtype=_I32, device=page_refs.device)
         at, of = array.array("Q", [t.data_ptr() for t in pools]), array.array("Q", [t.data_ptr() for t in weights])
