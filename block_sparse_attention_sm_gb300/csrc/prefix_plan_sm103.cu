@@ -12,7 +12,8 @@
 // are sorted out before, a lane each): its place is the number of smaller rows, c
 // its longest common stretch with one of them (the nearest smaller row has it).
 // tree_kernel: a warp a place looks left and right for the run's ends, 32 places a
-// step, in shared memory.  Latency bounds both.
+// step, in shared memory; then a thread a place goes up the tree.  Latency bounds both
+// (48 places: 6.2 us and 3.2 us).
 #include "launch.cuh"
 #include "shared_decode.cuh"
 
@@ -21,6 +22,8 @@ namespace {
 
 constexpr int kRank = 1024;
 constexpr int kTree = 1024;
+constexpr int kPlace = sizeof(int) + 2 * sizeof(uint16_t);  // shared memory of a place
+static_assert(kPlanMaxB < 65536, "places in 16 bits");
 
 __device__ __forceinline__ int full_pages(int len, int max_pages) {
   return min(max(len, 0) / kTile, max_pages);
@@ -108,6 +111,8 @@ __global__ void __launch_bounds__(kRank)
 
 __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32_t* plan) {
   extern __shared__ int c[];  // [B + 1] common tiles of places i - 1 and i; c[0] = c[B] = 0
+  auto* up = reinterpret_cast<uint16_t*>(c + B + 1);  // [B + 1] an i of the parent's run
+  uint16_t* name = up + B + 1;                        // [B + 1] the run's name
   int32_t* nodes = plan + kPlanHead + B;
   wait_for_previous();
   for (int i = threadIdx.x; i <= B; i += kTree) c[i] = i == 0 || i == B ? 0 : nodes[i * kNodeWords + 2];
@@ -115,81 +120,64 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
     plan[threadIdx.x] = threadIdx.x == 0 ? B : threadIdx.x == 1 ? max_pages : threadIdx.x == 2 ? kPlanMark : 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  // The run of places around i - 1 and i that have c[i] > 0 tiles in common: its
-  // name is the first i of it that has that value; places [lo, hi).  A whole warp.
-  auto run = [&](int i, int* lo, int* hi) {
-    const int v = c[i];
-    int name = i, l = i - 1, h = i + 1;
-    while (true) {  // (c[0] = 0 ends it)
-      const int x = l - lane >= 0 ? c[l - lane] : -1;
-      const uint32_t stop = __ballot_sync(0xffffffffu, x < v), same = __ballot_sync(0xffffffffu, x == v);
-      const uint32_t seen = stop != 0 ? same & ((1u << (__ffs(stop) - 1)) - 1) : same;
-      if (seen != 0) name = l - (31 - __clz(seen));
-      if (stop != 0) {
-        l -= __ffs(stop) - 1;
-        break;
-      }
-      l -= 32;
-    }
-    while (true) {  // (c[B] = 0)
-      const uint32_t stop = __ballot_sync(0xffffffffu, (h + lane <= B ? c[h + lane] : -1) < v);
-      if (stop != 0) {
-        h += __ffs(stop) - 1;
-        break;
-      }
-      h += 32;
-    }
-    *lo = l;
-    *hi = h;
-    return name;
-  };
   auto bound = [&](int lo, int hi) { return c[lo] >= c[hi] ? lo : hi; };  // the parent's value
+  // The runs, a warp each: the places around i - 1 and i that have c[i] > 0 tiles in
+  // common, [lo, hi).  A run's name is the first i of it that has that value.
+  for (int i = threadIdx.x >> 5; i < B; i += kTree / 32) {
+    int32_t* n = nodes + (B + i) * kNodeWords;
+    const int v = c[i];
+    int first = 0, count = 0, t0 = 0, t1 = 0;
+    if (v > 0) {
+      int at = i, l = i - 1, h = i + 1;
+      while (true) {  // (c[0] = 0 ends it)
+        const int x = l - lane >= 0 ? c[l - lane] : -1;
+        const uint32_t stop = __ballot_sync(0xffffffffu, x < v), same = __ballot_sync(0xffffffffu, x == v);
+        const uint32_t seen = stop != 0 ? same & ((1u << (__ffs(stop) - 1)) - 1) : same;
+        if (seen != 0) at = l - (31 - __clz(seen));
+        if (stop != 0) {
+          l -= __ffs(stop) - 1;
+          break;
+        }
+        l -= 32;
+      }
+      while (true) {  // (c[B] = 0)
+        const uint32_t stop = __ballot_sync(0xffffffffu, (h + lane <= B ? c[h + lane] : -1) < v);
+        if (stop != 0) {
+          h += __ffs(stop) - 1;
+          break;
+        }
+        h += 32;
+      }
+      if (at == i) first = l, count = h - l, t0 = c[bound(l, h)], t1 = v;
+      if (lane == 0) {
+        name[i] = static_cast<uint16_t>(at);
+        up[i] = static_cast<uint16_t>(bound(l, h));
+      }
+    }
+    if (lane == 0) n[0] = first, n[1] = count, n[2] = t0, n[3] = t1;
+  }
+  __syncthreads();
+  // The nodes above each place, a thread each.
   auto level = [&](int i) {  // nodes from i's up
     int n = 0;
-    for (; c[i] > 0; ++n) {
-      int lo, hi;
-      run(i, &lo, &hi);
-      i = bound(lo, hi);
-    }
+    for (; c[i] > 0; i = up[i]) ++n;
     return n;
   };
   int32_t* above = nodes + 2 * B * kNodeWords;
-  for (int i = threadIdx.x >> 5; i < B; i += kTree / 32) {
-    int first = 0, count = 0, t0 = 0, t1 = 0;
-    if (i > 0 && c[i] > 0) {
-      int lo, hi;
-      if (run(i, &lo, &hi) == i && level(i) <= kPlanLevels) {
-        first = lo;
-        count = hi - lo;
-        t0 = c[bound(lo, hi)];
-        t1 = c[i];
-      }
-    }
-    // The nodes above the place, from the deepest that is kept up; its own tiles are
-    // those behind that one's.
-    int up = bound(i, i + 1), own = -1;
-    for (int l = level(up), k = 0; k < kPlanLevels; ++k) {
-      while (l > kPlanLevels) {
-        int lo, hi;
-        run(up, &lo, &hi);
-        up = bound(lo, hi);
-        --l;
-      }
-      if (own < 0) own = c[up];
-      int name = -1;
-      if (c[up] > 0) {
-        int lo, hi;
-        name = B + run(up, &lo, &hi);
-        up = bound(lo, hi);
-        --l;
-      }
-      if (lane == 0) above[i * kPlanLevels + k] = name;
-    }
-    if (lane == 0) {
+  for (int i = threadIdx.x; i < B; i += kTree) {
+    if (level(i) > kPlanLevels) {  // (not kept)
       int32_t* n = nodes + (B + i) * kNodeWords;
-      n[0] = first, n[1] = count, n[2] = t0, n[3] = t1;
-      n = nodes + i * kNodeWords;
-      n[0] = i, n[1] = 1, n[2] = own, n[3] = -1;
+      n[0] = n[1] = n[2] = n[3] = 0;
+    }
+    // From the deepest node that is kept up; the place's own tiles are those behind that one's.
+    int at = bound(i, i + 1);
+    for (int l = level(at); l > kPlanLevels; --l) at = up[at];
+    int32_t* n = nodes + i * kNodeWords;
+    n[0] = i, n[1] = 1, n[2] = c[at], n[3] = -1;
+    for (int k = 0; k < kPlanLevels; ++k) {
+      const bool some = c[at] > 0;
+      above[i * kPlanLevels + k] = some ? B + name[at] : -1;
+      if (some) at = up[at];
     }
   }
 }
@@ -199,8 +187,10 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
 cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
                                int32_t* plan, cudaStream_t st) {
   rank_kernel<<<B, kRank, 0, st>>>(table, lens, B, max_pages, plan);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_behind(tree_kernel, 1, kTree, (B + 1) * sizeof(int), st, B, max_pages, plan);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(tree_kernel), (kPlanMaxB + 1) * kPlace, done);
+  return e != cudaSuccess ? e : launch_behind(tree_kernel, 1, kTree, (B + 1) * kPlace, st, B, max_pages, plan);
 }
 
 }  // namespace ssattn
