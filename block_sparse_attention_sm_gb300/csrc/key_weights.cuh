@@ -21,7 +21,7 @@ struct KeyWeightsParams {
   const int32_t* seq_lens;
   const int32_t* page_table;
   float* weights;          // [B][Hkv][max_pages * 128]
-  float* lse;              // [Hkv][places][2][128] log2 of the rows' denominators, by place of their pair of blocks
+  float* lse;              // [Hkv][places][2][128] -log2 of the rows' denominators, by place of their pair of blocks
   long places;
   float2* part_ml;         // [ctas][2][256] results of split items: rows' (m, l)
   float* part_w;           // [ctas][2][256] keys' sums

@@ -165,9 +165,9 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, flo
   l = (m == -INFINITY ? l : l * ex2_approx((m - top) * sl2)) + (m2 == -INFINITY ? l2 : l2 * ex2_approx((m2 - top) * sl2));
   m = top;
 }
-// log2 of the denominator; a row without keys gives infinity, and so weights of 0.
-__device__ __forceinline__ float row_lse(float m, float l, float sl2) {
-  return l == 0.f ? INFINITY : m == -INFINITY ? l : fmaf(m, sl2, log2f(l));
+// -log2 of the denominator, the addend of the keys' pass; a row without keys gives -infinity, and so weights of 0.
+__device__ __forceinline__ float row_addend(float m, float l, float sl2) {
+  return l == 0.f ? -INFINITY : m == -INFINITY ? l : -fmaf(m, sl2, log2f(l));
 }
 
 // What an item costs besides its steps (its fixed tiles, its results), in steps: causal
@@ -659,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kHalf / 4; ++c) {
               const float4 a = lse4[c];
               const uint64_t x0 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), sl2x2,
-                                            f32x2(-a.x, -a.y));
+                                            f32x2(a.x, a.y));
               const uint64_t x1 = fma_f32x2(f32x2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])),
-                                            sl2x2, f32x2(-a.z, -a.w));
+                                            sl2x2, f32x2(a.z, a.w));
               float w[4] = {ex2_approx(f32x2_lo(x0)), ex2_approx(f32x2_hi(x0)), ex2_approx(f32x2_lo(x1)),
                             ex2_approx(f32x2_hi(x1))};
               if (masked()) {
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row_live) {
               if (whole)
                 p.lse[(static_cast<long>(x.kvh) * p.places + x.place + x.pair) * kPair + ft * kTile + row] =
-                    row_lse(m_used, l, sl2);
+                    row_addend(m_used, l, sl2);
               else
                 p.part_ml[part] = make_float2(m_used, l);
             }
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kPair) join_kernel(const KeyWeightsParams p) {
       const float2 o = p.part_ml[2l * c * kPair + threadIdx.x];
       join(m, l, o.x, o.y, p.scale_log2);
     }
-    p.lse[(static_cast<long>(x.kvh) * p.places + s.place + x.pair) * kPair + threadIdx.x] = row_lse(m, l, p.scale_log2);
+    p.lse[(static_cast<long>(x.kvh) * p.places + s.place + x.pair) * kPair + threadIdx.x] = row_addend(m, l, p.scale_log2);
   } else {
     const int key = 2 * x.pair * kTile + threadIdx.x;
     if (key >= s.len) return;
