@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * t + kHalf * h;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f32x2(sl2, sl2);
+    const float slack = kSlackLog2 / sl2;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort_flag));
     };
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool alone = !x.both;
       // (keys: a pair of one tile has the second stream take alternate blocks of rows as well)
       const int ft = alone ? 0 : t;                       // this stream's fixed tile
-      float m_used = -INFINITY, l = 0.f;                  // rows
+      float m_used = -INFINITY, limit = -INFINITY, base = 0.f, l = 0.f;  // rows
       float sum[2] = {0.f, 0.f};                          // keys
       // rows: this thread's token and the last key that it sees; keys: this thread's key
       const int token = (2 * x.pair + ft) * p.tpb + row / p.G;
@@ -595,6 +596,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = !row_live ? -1 : p.causal ? min(x.len - 1, x.off + token) : x.len - 1;
       const int key = (2 * x.pair + ft) * kTile + row;
       const int u0 = x.first + x.u0, toks = x.toks, ahead = key - x.off;  // keys: the first token that sees the key
+      // Streamed tiles [whole_from, whole_to) count as a whole for all of the warp.
+      int whole_from = 0, whole_to;
+      if (ROWS) {
+        whole_to = static_cast<int>(max(0ll, __reduce_min_sync(0xffffffffu, lim) + 1ll - kHalf * h + kHalf) / kTile);
+      } else {
+        whole_to = q_rows < kTile ? 0 : toks / p.tpb;
+        if (p.causal) {  // from the first block whose token of column kHalf h sees the warp's last key
+          const long long last = static_cast<long long>(key | 31) - x.off - kHalf * h / p.G;
+          whole_from = last <= 0 ? 0 : static_cast<int>((last + p.tpb - 1) / p.tpb);
+        }
+      }
 #pragma unroll 1
       for (int i = alone ? t : 0; i < n; i += alone ? 2 : 1) {
         const uint32_t buf = sn & 1;
@@ -612,49 +624,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(&ctl->s_empty[2 * t + buf]);
         const int u = u0 + i;
         if (ROWS) {
-          const int vis = min(kHalf - 1, lim - u * kTile - kHalf * h);  // last visible column
-          if (__any_sync(0xffffffffu, vis < kHalf - 1)) {
+          if (u >= whole_to) {
+            const int vis = lim - u * kTile - kHalf * h;  // last visible column
 #pragma unroll
             for (int e = 0; e < kHalf; ++e)
               if (e > vis) sr[e] = __float_as_uint(-INFINITY);
           }
           // The reference m_used is the maximum of the row's first tile as long as no
-          // score is above it by more than 2^kSlackLog2: the maximum is formed beside
+          // score is above it by more than 2^kSlackLog2 (`limit`): the maximum is formed beside
           // the exponentials, and only a row's first tile takes a second turn.
 #pragma unroll 1
-          for (bool first = true;; first = false) {
-            const float mb = (m_used == -INFINITY) ? 0.f : m_used * sl2;
-            const uint64_t nmb = f32x2(-mb, -mb);
+          while (true) {
             uint64_t ls[2] = {0ull, 0ull};
             float mx[2] = {-INFINITY, -INFINITY};
+            const uint64_t base2 = f32x2(base, base);
 #pragma unroll
             for (int c = 0; c < kHalf / 2; ++c) {
               const float s0 = __uint_as_float(sr[2 * c]), s1 = __uint_as_float(sr[2 * c + 1]);
               mx[c & 1] = fmax3(mx[c & 1], s0, s1);
-              const uint64_t xp = fma_f32x2(f32x2(s0, s1), sl2x2, nmb);
+              const uint64_t xp = fma_f32x2(f32x2(s0, s1), sl2x2, base2);
               ls[c & 1] = add_f32x2(ls[c & 1], f32x2(ex2_approx(f32x2_lo(xp)), ex2_approx(f32x2_hi(xp))));
             }
             const float top = fmaxf(mx[0], mx[1]);
-            const bool above = first && (m_used == -INFINITY ? top > -INFINITY : (top - m_used) * sl2 > kSlackLog2);
-            if (!__any_sync(0xffffffffu, above)) {
+            if (!__any_sync(0xffffffffu, top > limit)) {
               const uint64_t s2 = add_f32x2(ls[0], ls[1]);
               l += f32x2_lo(s2) + f32x2_hi(s2);
               break;
             }
-            if (above) {
+            if (top > limit) {  // (then it is not above the new one)
               if (m_used != -INFINITY) l *= ex2_approx((m_used - top) * sl2);
               m_used = top;
+              limit = top + slack;
+              base = -top * sl2;
             }
           }
         } else {
-          // columns: rows of block u of the queries; those that see the key are [lo, hi)
-          const int i0 = u * p.tpb, ls_at = (e0 + i) % 3;
-          const int hi = min(q_rows, (toks - i0) * p.G) - kHalf * h;
-          const int lo = (p.causal ? static_cast<int>(max(0ll, min(static_cast<long long>(kTile), (static_cast<long long>(ahead) - i0) * p.G))) : 0) - kHalf * h;
+          // columns: rows of block u of the queries; those that count and see the key are [lo, hi)
+          const int ls_at = (e0 + i) % 3;
           const float4* lse4 = reinterpret_cast<const float4*>(ctl->hand.keys.lse[ls_at] + kHalf * h);
           uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
           // (a row that does not count may hold anything: its weight is dropped, not its score)
-          auto add_up = [&](auto masked) {
+          auto add_up = [&](auto masked, int lo, int hi) {
 #pragma unroll
             for (int c = 0; c < kHalf / 4; ++c) {
               const float4 a = lse4[c];
@@ -673,10 +683,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls[2 + (c & 1)] = add_f32x2(ls[2 + (c & 1)], f32x2(w[2], w[3]));
             }
           };
-          if (__any_sync(0xffffffffu, hi < kHalf || lo > 0))
-            add_up([] { return true; });
-          else
-            add_up([] { return false; });
+          if (u >= whole_from && u < whole_to) {
+            add_up([] { return false; }, 0, kHalf);
+          } else {
+            const int i0 = u * p.tpb;
+            const long long unseen = p.causal ? (static_cast<long long>(ahead) - i0) * p.G : 0;
+            add_up([] { return true; }, static_cast<int>(max(0ll, min(static_cast<long long>(kTile), unseen))) - kHalf * h,
+                   min(q_rows, (toks - i0) * p.G) - kHalf * h);
+          }
           arrive(&ctl->lse_empty[ls_at][t]);
           const uint64_t s2 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
           sum[0] += f32x2_lo(s2);
