@@ -26,18 +26,20 @@
 // them in order (results do not depend on timing).
 //
 // One CTA: two streams t, each with a fixed tile, two score buffers in TMEM and
-// two reducing warpgroups, one for each half of the columns (four in all hide one
-// another's waits: two prompts of 8K 825 us, two of whole rows 842 us).  A pair of one
-// block of rows, or of one tile of keys, has both streams take alternate streamed tiles
-// against that one instead.  Warps 0-15 reduce (stream 0, 1, 0, 1; the second pair the
-// second half), 16 loads, 17 and 19 issue the MMAs of stream 0 and 1, 18 works out the pieces.
+// two reducing warpgroups, one for each half of the columns (with one for all columns
+// the two passes of a prompt of 8K take 3% longer).  A pair of one block of rows, or of
+// one tile of keys, has both streams take alternate streamed tiles against that one
+// instead.  Warps 0-15 reduce (stream 0, 1, 0, 1; the second pair the second half), 16
+// loads, 17 and 19 issue the MMAs of stream 0 and 1, 18 works out the pieces.
 //
-// Bound: per step of two tiles the MMAs take ~1230 cycles (their operands come from shared
-// memory; alone 265 us for the rows of two prompts of 8K) and the exponentials 1024.  The
-// kernel is at ~1800: the two do not overlap fully, each tile's wait and load of the scores
-// (~300 cycles each) lies between them.  Measured and not taken: loads a chunk of 32
-// columns ahead of the reduction (20% more time), 512 fixed rows an item, which halves what
-// is streamed (25% more: the streamed tiles are not the bound).
+// Bound: a step of two tiles is ~1240 cycles of MMAs (measured without any reduction: their
+// operands come from shared memory) and 1024 of exponentials; it takes ~1800 in the rows'
+// pass, ~1950 in the keys' (two prompts of 8K, 32 / 8 heads of 128: 390 and 440 us, 1.6 times
+// the operations at the cuBLAS rate), for the reducing warps of an SM wait, load and compute in
+// step with one another.  A window of 32 tokens on long prompts is bound by its keys, read
+// twice (64 us a pass for 344 MB).  Measured and not taken: issuers in turns (rows +4%, keys -4%),
+// the loads of 32 columns ahead of the reduction (+20%), 512 fixed rows an item, which halves what
+// is streamed (+25%), the rows' tiles in reverse for what L2 still holds (-1%).
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -41,6 +41,11 @@
 // its page: zeros come in front, the keys follow, and what the page holds behind
 // the sequence's end is never read.
 //
+// Bound: 64 sequences (32 / 8 heads of 128) on a shared prefix of 32K keys with 100-900 of
+// their own take 64 us, 271 MB read, 61% of the copy rate: a tile that both streams take
+// costs ~3700 cycles (the softmax of 2 x 128 rows between two MMAs), one of a bundle ~2700
+// for the ~1300 of its bytes.  64 sequences of 32K each, nothing shared: 1.32 ms, 92%.
+
 // With weights the raw scores also go to the workspace (4 G bytes a key and KV
 // head, beside 4 d of K and V), and when the merge has the row's denominator,
 // weigh_kernel adds up exp2(s - lse) over the group's heads.  Each sum is made
@@ -902,8 +907,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // place, whose items were cut into pieces.  One block a (place, head): eight lanes
 // find the pieces (a level each), a thread a piece has its weight, and a warp takes
 // every fourth or eighth piece, columns a lane; the warps' sums are added in order.
-// 256 threads as long as all blocks are resident (28 heads x 24 places: 7.0 us, with
-// 128 threads 8.5), 128 beyond (32 heads x 64 places: 9.9 us, with 256 threads 15.7).
+// 256 threads as long as all blocks are resident (28 heads x 24 places: 6.8 us, with
+// 128 threads 8.5), 128 beyond (32 heads x 64 places: 11 us, with 256 threads 15.7): a
+// chain of dependent loads bounds it.
 template <int D, int kMerge>
 __global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p, int ctas) {
   constexpr int L = 1 + kPlanLevels, E = D / 32, W = kMerge / 32;
