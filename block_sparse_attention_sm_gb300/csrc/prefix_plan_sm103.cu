@@ -13,8 +13,10 @@
 // its longest common stretch with one of them (the nearest smaller row has it).
 // tree_kernel: a warp a place looks left and right for the run's ends, 32 places a
 // step, in shared memory; then a thread a place goes up the tree.  Latency bounds both
-// (48 places: 6.2 us and 3.2 us).
+// (48 places: 6.2 us and 3.2 us).  A batch of up to 8 has both in one launch, the blocks of
+// a cluster (8 places: 5.1 us against 4.3, but 3 us less of the host, which bounds such calls).
 #include "launch.cuh"
+#include "ptx_pair_sm103.cuh"
 #include "shared_decode.cuh"
 
 namespace ssattn {
@@ -22,6 +24,8 @@ namespace {
 
 constexpr int kRank = 1024;
 constexpr int kTree = 1024;
+constexpr int kCluster = 8;  // blocks of a cluster
+static_assert(kRank == kTree, "one block does both");
 constexpr int kPlace = sizeof(int) + 2 * sizeof(uint16_t);  // shared memory of a place
 static_assert(kPlanMaxB < 65536, "places in 16 bits");
 
@@ -56,11 +60,11 @@ __device__ __forceinline__ int common_pages(const int32_t* a, const int32_t* b, 
   return n;
 }
 
-__global__ void __launch_bounds__(kRank)
-    rank_kernel(const int32_t* table, const int32_t* lens, int B, int max_pages, int32_t* plan) {
+// Row i: its place, and its longest common stretch with a smaller row.
+__device__ __forceinline__ void rank_row(const int32_t* table, const int32_t* lens, int i, int B, int max_pages, int32_t* plan) {
   __shared__ int smaller, longest, n_open;
   __shared__ int open[kRank], open_n[kRank];  // rows that begin as row i does, and their full pages
-  const int i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) smaller = longest = 0;
   const int32_t* mine = table + static_cast<long>(i) * max_pages;
   const int n_mine = full_pages(lens[i], max_pages);
@@ -109,13 +113,13 @@ __global__ void __launch_bounds__(kRank)
   }
 }
 
-__global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32_t* plan) {
-  extern __shared__ int c[];  // [B + 1] common tiles of places i - 1 and i; c[0] = c[B] = 0
+// The tree from the ranks, by one block; `c`: kPlace bytes a place and one more.
+__device__ __forceinline__ void build_tree(int B, int max_pages, int32_t* plan, int* c) {
+  // c [B + 1]: common tiles of places i - 1 and i; c[0] = c[B] = 0
   auto* up = reinterpret_cast<uint16_t*>(c + B + 1);  // [B + 1] an i of the parent's run
   uint16_t* name = up + B + 1;                        // [B + 1] the run's name
   int32_t* nodes = plan + kPlanHead + B;
-  wait_for_previous();
-  for (int i = threadIdx.x; i <= B; i += kTree) c[i] = i == 0 || i == B ? 0 : nodes[i * kNodeWords + 2];
+  for (int i = threadIdx.x; i <= B; i += kTree) c[i] = i == 0 || i == B ? 0 : __ldcg(&nodes[i * kNodeWords + 2]);
   if (threadIdx.x < kPlanHead)
     plan[threadIdx.x] = threadIdx.x == 0 ? B : threadIdx.x == 1 ? max_pages : threadIdx.x == 2 ? kPlanMark : 0;
   __syncthreads();
@@ -182,10 +186,37 @@ __global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32
   }
 }
 
+__global__ void __launch_bounds__(kRank)
+    rank_kernel(const int32_t* table, const int32_t* lens, int B, int max_pages, int32_t* plan) {
+  rank_row(table, lens, blockIdx.x, B, max_pages, plan);
+}
+
+__global__ void __launch_bounds__(kTree) tree_kernel(int B, int max_pages, int32_t* plan) {
+  extern __shared__ int c[];
+  let_next_start();
+  wait_for_previous();
+  build_tree(B, max_pages, plan, c);
+}
+
+// Both for a batch that a cluster holds.
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kRank)
+    small_plan_kernel(const int32_t* table, const int32_t* lens, int B, int max_pages, int32_t* plan) {
+  __shared__ int c[((kCluster + 1) * kPlace + 3) / 4];
+  let_next_start();
+  if (blockIdx.x < B) rank_row(table, lens, blockIdx.x, B, max_pages, plan);
+  __syncwarp();
+  cluster_sync_all();  // (what the blocks have written to the plan as well)
+  if (blockIdx.x == 0) build_tree(B, max_pages, plan, c);
+}
+
 }  // namespace
 
 cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
                                int32_t* plan, cudaStream_t st) {
+  if (B <= kCluster) {
+    small_plan_kernel<<<kCluster, kRank, 0, st>>>(table, lens, B, max_pages, plan);
+    return cudaGetLastError();
+  }
   rank_kernel<<<B, kRank, 0, st>>>(table, lens, B, max_pages, plan);
   static std::atomic<uint64_t> done{0};
   cudaError_t e = cudaGetLastError();
