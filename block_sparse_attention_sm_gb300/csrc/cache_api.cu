@@ -841,6 +841,7 @@ ss_status ss_attn_key_weights(const void* q, int64_t q_token_stride, const void*
   p.Hkv = Hkv;
   p.G = G;
   p.tpb = static_cast<int>(tpb);
+  p.tpb_inverse = ~0ull / tpb + 1;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.causal = causal ? 1 : 0;

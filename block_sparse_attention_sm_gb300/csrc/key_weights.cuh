@@ -12,6 +12,7 @@ namespace ssattn {
 struct KeyWeightsParams {
   int T, B, Hq, Hkv, G;
   int tpb;                 // tokens of a row block: 128 / G
+  uint64_t tpb_inverse;    // ceil(2^64 / tpb), where that is below 2^64
   int num_pages, max_pages;
   int causal;
   int ctas;

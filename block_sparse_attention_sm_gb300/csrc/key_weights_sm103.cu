@@ -73,27 +73,39 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's steps on (a, m)).
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// Every CTA works its share out for itself before it loads anything, with cold code: so
+// 32-bit divisions where the numbers fit, and those by the tokens of a block as products.
+__device__ __forceinline__ long long quotient(long long a, long long b) {  // a >= 0, b > 0
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+// floor(n / tpb), n >= 0 (`tpb_inverse` = ceil(2^64 / tpb): exact for n < 2^57).
+__device__ __forceinline__ long long blocks_in(const KeyWeightsParams& p, long long n) {
+  return p.tpb == 1 ? n : static_cast<long long>(__umul64hi(n, p.tpb_inverse));
+}
+
+// sum over i < n of floor((a i + b) / m), a and b below m (Euclid's steps on (a, m)).
+template <typename U>
+__device__ __forceinline__ long long floor_sum_of(U n, U m, U a, U b) {
   long long sum = 0;
-  while (n > 0) {
-    if (a >= m) {
-      sum += (n - 1) * n / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const long long y = a * n + b;
-    if (y < m) break;
+#pragma unroll 1
+  while (true) {
+    const U y = a * n + b;
+    if (y < m) return sum;
     n = y / m;
-    b = y % m;
-    const long long x = m;
+    b = y - n * m;
+    U x = m;  // (a, m) = (m, a)
     m = a;
     a = x;
+    x = a / m;
+    a -= x * m;
+    sum += (static_cast<long long>(n) - 1) * static_cast<long long>(n) / 2 * static_cast<long long>(x);
+    x = b / m;
+    b -= x * m;
+    sum += static_cast<long long>(n) * static_cast<long long>(x);
   }
-  return sum;
+}
+__device__ __forceinline__ long long floor_sum(long long n, int m, int a, int b) {  // a, b < m <= 256
+  return n < (1 << 23) ? floor_sum_of<uint32_t>(static_cast<uint32_t>(n), m, a, b) : floor_sum_of<uint64_t>(n, m, a, b);
 }
 
 // A sequence of the step.
@@ -111,13 +123,9 @@ __device__ __forceinline__ Seq seq_of(const KeyWeightsParams& p, int b) {
   s.len = max(0, min(p.seq_lens[b], p.max_pages * kTile));
   s.off = s.len - s.n;
   s.tiles = (s.len + kTile - 1) / kTile;
-  s.blocks = (s.n + p.tpb - 1) / p.tpb;
-  s.place = s.tok0 / (2 * p.tpb) + b;
+  s.blocks = static_cast<int>(blocks_in(p, s.n + p.tpb - 1ll));
+  s.place = blocks_in(p, s.tok0) / 2 + b;
   return s;
-}
-
-__device__ __forceinline__ long long ceil_div(long long a, long long b) {  // b > 0
-  return a >= 0 ? (a + b - 1) / b : -(-a / b);
 }
 
 // Fixed pairs of a KV head, the steps of pair i, and the steps of all pairs below i.
@@ -130,7 +138,7 @@ __device__ __forceinline__ int first_step(const KeyWeightsParams& p, const Seq& 
   // keys: the first block of query rows that sees a key of the pair
   if (ROWS || !p.causal) return 0;
   const int x = i * kPair - s.off;  // the first token that does
-  return x <= 0 ? 0 : min(s.blocks, x / p.tpb);
+  return x <= 0 ? 0 : min(s.blocks, static_cast<int>(blocks_in(p, x)));
 }
 template <bool ROWS>
 __device__ __forceinline__ int steps_of(const KeyWeightsParams& p, const Seq& s, int i) {
@@ -144,19 +152,27 @@ __device__ long long steps_below(const KeyWeightsParams& p, const Seq& s, int i)
   if (!p.causal) return static_cast<long long>(i) * (ROWS ? s.tiles : s.blocks);
   if (ROWS) {
     // clamp(floor((off + w (q + 1) - 1) / 128) + 1, 0, tiles): zero below q0, tiles from q1 on
-    const long long w = 2 * p.tpb, c = static_cast<long long>(s.off) + w - 1;
-    const long long q0 = c >= 0 ? 0 : ceil_div(-c, w);
-    long long q1 = max(q0, ceil_div(static_cast<long long>(kTile) * (s.tiles - 1) - c, w));
-    q1 = max(q1, 0ll);
-    const long long top = min(static_cast<long long>(i), q1);
+    const int w = 2 * p.tpb;
+    const long long c = static_cast<long long>(s.off) + w - 1;
+    auto pairs_to = [&](long long x) { return x <= 0 ? 0ll : blocks_in(p, x + w - 1) / 2; };  // ceil(x / w)
+    const long long q0 = pairs_to(-c), q1 = max(q0, pairs_to(static_cast<long long>(kTile) * (s.tiles - 1) - c));
+    const long long n = min(static_cast<long long>(i), q1) - q0;
     long long sum = 0;
-    if (top > q0) sum = floor_sum(top - q0, kTile, w, c + w * q0) + (top - q0);
+    if (n > 0) {
+      const long long b = c + w * q0;
+      sum = n + n * (b / kTile) + (n - 1) * n / 2 * (w / kTile) + floor_sum(n, kTile, w % kTile, static_cast<int>(b % kTile));
+    }
     if (i > q1) sum += (i - q1) * s.tiles;
     return sum;
   }
-  const long long k0 = s.off < 0 ? 0 : static_cast<long long>(s.off) / kPair + 1;  // first pair with a step less
+  const long long k0 = s.off < 0 ? 0 : s.off / kPair + 1ll;  // first pair with a step less
+  const long long n = i - k0;
   long long sum = static_cast<long long>(i) * s.blocks;
-  if (i > k0) sum -= floor_sum(i - k0, p.tpb, kPair, k0 * kPair - s.off);
+  if (n > 0) {
+    const int b = static_cast<int>(k0 * kPair - s.off);  // 1 .. 256, or as far as the first tokens lie behind all keys
+    const int qa = static_cast<int>(blocks_in(p, kPair)), qb = static_cast<int>(blocks_in(p, b));
+    sum -= n * qb + (n - 1) * n / 2 * qa + floor_sum(n, p.tpb, kPair - qa * p.tpb, b - qb * p.tpb);
+  }
   return sum;
 }
 
@@ -186,6 +202,21 @@ __device__ long long cost_below(const KeyWeightsParams& p, const Seq& s, int i) 
   return steps_below<ROWS>(p, s, i) + static_cast<long long>(kItemCost) * i;
 }
 
+// The last of the pairs with cost_below <= in: a warp looks at 32 places at a time.
+template <bool ROWS>
+__device__ __forceinline__ int last_pair(const KeyWeightsParams& p, const Seq& s, int pairs, long long in) {
+  int lo = 0;  // (cost_below(0) = 0 <= in)
+#pragma unroll 1
+  for (int n = pairs; n > 1;) {  // of [lo, lo + n)
+    const int step = (n + 31) / 32, x = static_cast<int>(threadIdx.x & 31) * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, x < n && cost_below<ROWS>(p, s, lo + x) <= in);
+    const int at = (31 - __clz(below)) * step;  // (place 0 always is)
+    lo += at;
+    n = min(step, n - at);
+  }
+  return lo;
+}
+
 // A run of steps of one item.
 struct Piece {
   int n, u0, steps;  // steps; the first of them, all of the item's (n = 0: no more pieces)
@@ -211,7 +242,7 @@ struct Ctl {
   int abort_flag;
   int r_issued, f_issued;
   int b;              // this CTA's share begins in sequence b,
-  long long at;       // whose first step is number `at` of all
+  long long at, head; // with `at` of the cost in front of it and `head` a KV head
   long long total;
   Piece piece[kPieces];
   union {
@@ -223,6 +254,8 @@ struct Ctl {
     struct {
       float used[3 * kTile];            // (left to the copies of the lse)
       long long scan[kThreads / 32];    // the warps' sums over the batch
+      float room[kTile - kThreads / 16];
+      Seq seq;                          // the sequence that this CTA's share begins in
     } start;
   } hand;
 };
@@ -292,11 +325,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   {  // every sequence's steps, added up
     long long* scan = ctl->hand.start.scan;
     const int each = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    Seq s{};
+    long long head = 0;
     auto cost = [&](int b) {
-      const Seq s = seq_of(p, b);
-      return cost_below<ROWS>(p, s, pairs_of<ROWS>(s)) * p.Hkv;
+      s = seq_of(p, b);
+      head = cost_below<ROWS>(p, s, pairs_of<ROWS>(s));
+      return head * p.Hkv;
     };
     long long mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += cost(b);
     long long at = mine;
 #pragma unroll
@@ -312,16 +349,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += scan[w];
     }
     at -= mine;
-    const long long per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x;
-    if (begin >= at && begin < at + mine)
-      for (int b = b0; b < b1; ++b) {
-        const long long c = cost(b);
-        if (begin >= at && begin < at + c) {
-          ctl->b = b;
-          ctl->at = at;
+    const long long begin = quotient(total + gridDim.x - 1, gridDim.x) * blockIdx.x;
+    if (begin >= at && begin < at + mine) {
+      int b = b0;
+      if (each > 1) {  // (else it is the one that has just been looked at)
+        long long c = cost(b);
+#pragma unroll 1
+        while (begin >= at + c) {
+          at += c;
+          c = cost(++b);
         }
-        at += c;
       }
+      ctl->b = b;
+      ctl->at = at;
+      ctl->head = head;
+      ctl->hand.start.seq = s;
+    }
     if (tid == 0) ctl->total = total;
   }
   if (!ROWS) wait_for_previous();  // (the rows' lse)
@@ -474,29 +517,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kWarpPlan) {
       // ---------------------------------------------------------- pieces
+      const long long per = quotient(ctl->total + gridDim.x - 1, gridDim.x);
+      const long long at = per * blockIdx.x, end = min(at + per, ctl->total);
+      int b = at < end ? ctl->b : -1, kvh = 0, pair = 0;
+      long long begin = 0;  // cost in front of the item's first step
+      Seq s{};
+      int pairs = 0;
+      if (b >= 0) {  // the item that the share begins in
+        s = ctl->hand.start.seq;
+        pairs = pairs_of<ROWS>(s);
+        long long in = at - ctl->at;
+        kvh = static_cast<int>(quotient(in, ctl->head));
+        in -= kvh * ctl->head;
+        pair = last_pair<ROWS>(p, s, pairs, in);
+        begin = at - in + cost_below<ROWS>(p, s, pair) + kItemCost;
+      }
       if (lane == 0) {
-        const long long per = (ctl->total + gridDim.x - 1) / gridDim.x;
-        long long at = per * blockIdx.x;
-        const long long end = min(at + per, ctl->total);
-        int b = at < end ? ctl->b : -1, kvh = 0, pair = 0;
-        long long begin = 0;  // cost in front of the item's first step
-        Seq s{};
-        int pairs = 0;
-        if (b >= 0) {  // the item that the share begins in
-          s = seq_of(p, b);
-          pairs = pairs_of<ROWS>(s);
-          const long long head = cost_below<ROWS>(p, s, pairs);
-          long long in = at - ctl->at;
-          kvh = static_cast<int>(in / head);
-          in -= kvh * head;
-          int lo = 0, hi = pairs;  // the last pair with cost_below <= in
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (cost_below<ROWS>(p, s, mid) <= in) lo = mid; else hi = mid;
-          }
-          pair = lo;
-          begin = ctl->at + kvh * head + cost_below<ROWS>(p, s, lo) + kItemCost;
-        }
         Split split{};
         for (int k = 0;; ++k) {
           Piece x{};
