@@ -367,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) ctl->total = total;
   }
-  if (!ROWS) wait_for_previous();  // (the rows' lse)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -391,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int e = 0;
       uint32_t used = 0, turn = 0;  // lse places, a bit a stream: in use, parity
-      bool ok = true;
+      bool ok = true, waited = ROWS;
       auto load_queries = [&](uint8_t* to, uint64_t* bar, const Piece& x, int block) {
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
@@ -454,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_keys(sR + st * C::kTileBytes, &ctl->r_full[st], x, page);
             } else {
               load_queries(sR + st * C::kTileBytes, &ctl->r_full[st], x, u);
+              if (!waited) wait_for_previous();  // (the rows' lse)
+              waited = true;
               bulk_load(ctl->hand.keys.lse[ls], lse_of + static_cast<long>(u) * kTile, kTile * sizeof(float), &ctl->r_full[st]);
             }
             *reinterpret_cast<volatile int*>(&ctl->r_issued) = e + 1;
@@ -578,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ctl->piece_full[k % kPieces]);
           if (x.n == 0) break;
         }
+        if (!ROWS) wait_for_previous();  // (which reads its own; and no CTA ends before that kernel)
         p.split[blockIdx.x] = split;
       }
       __syncwarp();
