@@ -778,10 +778,7 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
   p.part_o = reinterpret_cast<float*>(ws + space.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);
   p.part_rows = space.part_rows;
-  p.total = reinterpret_cast<uint32_t*>(ws + space.total);
-  p.cum = reinterpret_cast<uint32_t*>(ws + space.cum);
-  p.node_at = reinterpret_cast<uint32_t*>(ws + space.node_at);
-  p.node_rows = reinterpret_cast<long long*>(ws + space.node_rows);
+  p.parts = reinterpret_cast<Parts*>(ws + space.parts);
   if (weights != nullptr) {
     p.lse = reinterpret_cast<float*>(ws + space.lse);
     p.scores = reinterpret_cast<float*>(ws + space.scores);

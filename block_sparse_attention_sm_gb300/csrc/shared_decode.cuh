@@ -27,6 +27,13 @@ __host__ __device__ constexpr size_t plan_words(long B) { return kPlanHead + B +
 cudaError_t launch_prefix_plan(const int32_t* table, const int32_t* lens, int B, int max_pages,
                                int32_t* plan, cudaStream_t st);
 
+// The results of one level (its own tiles, or a node above) of a (place, KV head): those of head g in rows row + g,
+// row + g + second, and the same a CTA's rows on, and so on; `count` of them (second = 0: one a CTA).
+struct Parts {
+  long long row;
+  int second, count;
+};
+
 struct SharedParams {
   int B, Hq, Hkv, G;
   uint32_t inv_g;          // floor(2^32 / G) + 1 (G > 1): r / G of a row r is the product's upper half
@@ -42,23 +49,20 @@ struct SharedParams {
   float* part_o;           // [part_rows][d] unnormalised partial outputs
   float2* part_ml;         // [part_rows] (reference maximum in exp2 units, sum)
   long part_rows;
-  uint32_t* total;         // all items' cost
-  uint32_t* cum;           // [B + 1] own tiles of the places below
-  uint32_t* node_at;       // [B] cost of the items in front of a shared node
-  long long* node_rows;    // [B] its first partial row
+  Parts* parts;            // [B][Hkv][1 + kPlanLevels], without a plan [B][Hkv]
   float* lse;              // [B][Hq] log2 of the softmax's denominator (weights only)
   float* scores;           // [B][Hq][max_pages][128] (weights only)
   float* weights;          // [B][Hkv][max_pages * 128], nullable
   uint32_t* status;
 };
 
-// Tiles over all sequences and KV heads that a table may have room for: their cost (3 a tile, and as much
+// Tiles over all sequences and KV heads that a table may have room for: their cost (2 a tile at most, and as much
 // again for each level of shared nodes at most) is counted in 31 bits.
 constexpr long kMaxSharedTiles = 1l << 29, kMaxPlannedTiles = 1l << 26;
 
 // Workspace: sizes and where its arrays lie.
 struct SharedSpace {
-  size_t part_o, part_ml, total, cum, node_at, node_rows, lse, scores, bytes;
+  size_t part_o, part_ml, parts, lse, scores, bytes;
   long part_rows;
 };
 SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan, bool weights);

@@ -68,6 +68,7 @@ constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpPlan = 10, kWarpMma2 = 11;
 constexpr int kRows = 256;      // rows of an item
 constexpr int kSegments = 4;    // published segments
 constexpr int kSegTiles = 16;
+constexpr int kOpeners = 256 + 32;  // softmax warps and planner
 // Register split (see the prefill kernel): the launch's pool, exactly.
 constexpr int kLaunchRegs = 168, kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax == kThreads * kLaunchRegs, "register split");
@@ -173,10 +174,12 @@ struct Deal {
   int part;           // partial rows of a piece: two results each where the streams take alternate tiles
 };
 __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
-  const int most = kRows / G;
-  Deal d;
-  d.blocks = max(1, (x.count + most - 1) / most);
-  d.rows = (x.count + d.blocks - 1) / d.blocks * G;
+  Deal d{1, x.count * G, 0};
+  if (d.rows > kRows) {
+    const int most = kRows / G;
+    d.blocks = (x.count + most - 1) / most;
+    d.rows = (x.count + d.blocks - 1) / d.blocks * G;
+  }
   d.part = d.rows <= kTile ? 2 * d.rows : d.rows;
   return d;
 }
@@ -286,34 +289,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int each = (B + kThreads - 1) / kThreads, n0 = min(B, tid * each), n1 = min(B, n0 + each);
     Sums v{0, 0, 0}, all{0, 0, 0};
+    Node x{}, y{};
+    Deal d{};
     // twice: adding up, then (with what lies below) writing
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
       for (int n = n0; n < n1; ++n) {
-        const Node x = node_of(p, plan, n);
+        if (pass == 0 || each > 1) {
+          x = node_of(p, plan, n);
+          if (plan != nullptr) {
+            y = node_of(p, plan, B + n);
+            d = deal_of(y, G);
+          }
+        }
         if (pass == 1) {
           cum[n] = v.tiles;
-          if (blockIdx.x == 0) p.cum[n] = v.tiles;
+          if (plan != nullptr) {
+            node_at[n] = all.tiles * p.Hkv * kTileCost + v.cost;
+            node_rows[n] = 2ll * p.Hq * B + v.rows;
+          }
         }
         v.tiles += x.t1 - x.t0;
-        if (plan != nullptr) {
-          const Node y = node_of(p, plan, B + n);
-          const Deal d = deal_of(y, G);
-          if (pass == 1) {
-            const uint32_t at = all.tiles * p.Hkv * kTileCost + v.cost;
-            const long long row = 2ll * p.Hq * B + v.rows;
-            node_at[n] = at;
-            node_rows[n] = row;
-            if (blockIdx.x == 0) {
-              p.node_at[n] = at;
-              p.node_rows[n] = row;
-            }
-          }
-          if (y.t1 > y.t0) {
-            v.cost += (y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
-            v.rows += static_cast<long long>(d.blocks) * p.Hkv * d.part;
-          }
+        if (y.t1 > y.t0) {
+          v.cost += (y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
+          v.rows += static_cast<long long>(d.blocks) * p.Hkv * d.part;
         }
       }
       if (pass == 0) all = block_sums(v, (B + each - 1) / each, plan != nullptr, reinterpret_cast<Sums*>(ctl->seg));
@@ -322,10 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       cum[B] = all.tiles;
       ctl->leaf_total = all.tiles * p.Hkv * kTileCost;
       ctl->total = ctl->leaf_total + all.cost;
-      if (blockIdx.x == 0) {
-        p.cum[B] = all.tiles;
-        *p.total = ctl->total;
-      }
     }
   }
   tc_fence_before();
@@ -520,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_at = nodes > 0 ? node_at[n] : 0;
         n_rows = nodes > 0 ? node_rows[n] : 0;
       }
-      // (from here on the tiles may land over the sums)
       // The piece that is being published, and of a bundle 32 places, a lane each.
       Segment seg{};
       int left = 0, done = 0;             // its tiles to come, its tiles published
@@ -528,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bundle = false;
       int w0 = 0, before = 0, window = 0; // window: first place, tiles in front of it, its tiles
       int b = 0, t0 = 0, count = 0, len = 0, sum = 0;
-      bool ok = true;
+      bool ok = true, opened = false;
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         // ---- the next piece
@@ -646,6 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- published (without tiles: the end)
+        if (!opened) barrier_sync(2, kOpeners);  // from here on the tiles may land over the sums
+        opened = true;
         ok = __all_sync(0xffffffffu, wait(&ctl->seg_empty[k % kSegments], ((k / kSegments) & 1) ^ 1));
         if (!ok) break;
         Segment& to = ctl->seg[k % kSegments];
@@ -695,6 +692,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2x2 = f32x2(sl2, sl2);
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
     auto place_row = [&](int r) { return p.inv_g != 0 ? static_cast<int>(__umulhi(r, p.inv_g)) : r; };  // r / G
+    {  // Where the merge finds the results of a (place, KV head): this CTA's part of the list, while there is nothing else to do.
+      const int levels = plan != nullptr ? 1 + kPlanLevels : 1, all = B * p.Hkv * levels;
+      const uint32_t per = share_of(ctl->total, gridDim.x);
+#pragma unroll 1
+      for (int e = blockIdx.x * 256 + tid; e < all; e += gridDim.x * 256) {
+        const int level = e & (levels - 1), r = plan != nullptr ? e / (1 + kPlanLevels) : e, i = r / p.Hkv, kvh = r - i * p.Hkv;
+        Parts x{0, 0, 0};
+        uint32_t a = 0, z = 0;  // cost in front of the row's first tile, of its last
+        if (level == 0) {
+          const int j0 = i / nb * nb, places = min(nb, B - j0);
+          const uint32_t base = cum[j0], T = cum[j0 + places] - base, c0 = cum[i], n = cum[i + 1] - c0;
+          if (n > 0) {
+            a = (base * p.Hkv + kvh * T + (c0 - base)) * kTileCost;
+            z = a + (n - 1) * kTileCost;
+            x.row = 2ll * G * p.Hkv * j0 + (2ll * kvh * places + (i - j0)) * G;
+            x.second = places * G;
+            x.count = 1;
+          }
+        } else {
+          const int n = plan[kPlanHead + B + 2l * B * kNodeWords + static_cast<long>(i) * kPlanLevels + level - 1];
+          if (n >= B && n < 2 * B) {
+            const Node y = node_of(p, plan, n);
+            const int T = y.t1 - y.t0, place = i - y.first;
+            if (T > 0 && place >= 0 && place < y.count) {
+              const Deal d = deal_of(y, G);
+              const int blk = d.blocks > 1 ? place * G / d.rows : 0, item = kvh * d.blocks + blk, cost = cost_of(d);
+              a = node_at[n - B] + item * T * cost;
+              z = a + (T - 1) * cost;
+              x.row = node_rows[n - B] + static_cast<long long>(item) * d.part + (place * G - blk * d.rows);
+              x.second = d.rows > kTile ? 0 : d.rows;
+              x.count = 1;
+            }
+          }
+        }
+        if (x.count > 0) {
+          const int c0 = a / per, c1 = z / per;
+          x.row += static_cast<long long>(c0) * kRows;
+          x.count = max(0, min(p.ctas, c1 - c0 + 1)) * (x.second > 0 ? 2 : 1);
+        }
+        p.parts[e] = x;
+      }
+      barrier_sync(2, kOpeners);
+    }
     uint32_t ns = 0, no = 0;
     int k = 0;
     bool ok = wwait(&ctl->seg_full[0], 0);
@@ -904,14 +944,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The partial results of a row: those of its own tiles and of the nodes above its
-// place, whose items were cut into pieces.  One block a (place, head): eight lanes
-// find the pieces (a level each), a thread a piece has its weight, and a warp takes
+// place, whose items were cut into pieces.  One block a (place, head): the attention
+// kernel has listed where they lie (a level a lane), a thread a piece has its weight, and a warp takes
 // every fourth or eighth piece, columns a lane; the warps' sums are added in order.
 // 256 threads as long as all blocks are resident (28 heads x 24 places: 6.8 us, with
 // 128 threads 8.5), 128 beyond (32 heads x 64 places: 11 us, with 256 threads 15.7): a
 // chain of dependent loads bounds it.
 template <int D, int kMerge>
-__global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p, int ctas) {
+__global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p) {
   constexpr int L = 1 + kPlanLevels, E = D / 32, W = kMerge / 32;
   __shared__ long long s_row[L];               // a level's first partial row, of its first CTA
   __shared__ int s_second[L], s_start[L + 1];  // the second stream's distance (0: one result a piece), results in front
@@ -924,51 +964,20 @@ __global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = place_of(plan, i, p.B);
   if (warp == 0) {
-    int parts = 0, second = 0;
-    long long row = 0;
-    uint32_t a = 0, z = 0;  // cost in front of the row's first tile, of its last
-    if (lane == 0) {
-      const int nb = kTile / G, j0 = i / nb * nb, places = min(nb, p.B - j0);
-      const uint32_t base = p.cum[j0], T = p.cum[j0 + places] - base, c0 = p.cum[i], n = p.cum[i + 1] - c0;
-      if (n > 0) {
-        a = (base * p.Hkv + kvh * T + (c0 - base)) * kTileCost;
-        z = a + (n - 1) * kTileCost;
-        row = 2ll * G * p.Hkv * j0 + (2ll * kvh * places + (i - j0)) * G + g;
-        second = places * G;
-        parts = 1;
-      }
-    } else if (lane < L && plan != nullptr) {
-      const int n = plan[kPlanHead + p.B + 2l * p.B * kNodeWords + static_cast<long>(i) * kPlanLevels + lane - 1];
-      if (n >= p.B && n < 2 * p.B) {
-        const Node x = node_of(p, plan, n);
-        const int T = x.t1 - x.t0, place = i - x.first;
-        if (T > 0 && place >= 0 && place < x.count && length_of(p, b) > 0) {
-          const Deal d = deal_of(x, G);
-          const int blk = place * G / d.rows, item = kvh * d.blocks + blk, cost = cost_of(d);
-          a = p.node_at[n - p.B] + item * T * cost;
-          z = a + (T - 1) * cost;
-          row = p.node_rows[n - p.B] + static_cast<long long>(item) * d.part + (place * G + g - blk * d.rows);
-          second = d.rows > kTile ? 0 : d.rows;
-          parts = 1;
-        }
-      }
-    }
-    if (parts > 0) {
-      const uint32_t per = share_of(*p.total, ctas);
-      const int c0 = a / per, c1 = z / per;
-      row += static_cast<long long>(c0) * kRows;
-      parts = max(0, min(ctas, c1 - c0 + 1)) * (second > 0 ? 2 : 1);
-    }
-    int sum = parts;
+    const int levels = plan != nullptr ? L : 1;
+    Parts x{0, 0, 0};
+    if (lane < levels) x = p.parts[(static_cast<long>(i) * p.Hkv + kvh) * levels + lane];
+    if (length_of(p, b) == 0) x.count = 0;
+    int sum = x.count;
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
     if (lane < L) {
-      s_row[lane] = row;
-      s_second[lane] = second;
-      s_start[lane] = sum - parts;
+      s_row[lane] = x.row + g;
+      s_second[lane] = x.second;
+      s_start[lane] = sum - x.count;
       if (lane == L - 1) s_start[L] = sum;
     }
   }
@@ -1094,8 +1103,8 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Share
   e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tk, tv, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
-  e = rows <= 8 * kSMs ? launch_behind(shared_merge_kernel<D, 256>, rows, 256, 0, st, p, p.ctas)
-                       : launch_behind(shared_merge_kernel<D, 128>, rows, 128, 0, st, p, p.ctas);
+  e = rows <= 8 * kSMs ? launch_behind(shared_merge_kernel<D, 256>, rows, 256, 0, st, p)
+                       : launch_behind(shared_merge_kernel<D, 128>, rows, 128, 0, st, p);
   if (e != cudaSuccess || p.weights == nullptr) return e;
   const int blocks = (p.max_pages + 7) / 8;
   return launch_behind(weigh_kernel, dim3(blocks < 64 ? blocks : 64, p.Hkv, p.B), 256, 0, st, p);
@@ -1127,10 +1136,7 @@ SharedSpace shared_space(int B, int Hq, int Hkv, int max_pages, int d, bool plan
   };
   s.part_o = take(static_cast<size_t>(s.part_rows) * d * sizeof(float));
   s.part_ml = take(static_cast<size_t>(s.part_rows) * sizeof(float2));
-  s.total = take(sizeof(uint32_t));
-  s.cum = take((static_cast<size_t>(B) + 1) * sizeof(uint32_t));
-  s.node_at = take(plan ? static_cast<size_t>(B) * sizeof(uint32_t) : 0);
-  s.node_rows = take(plan ? static_cast<size_t>(B) * sizeof(long long) : 0);
+  s.parts = take(static_cast<size_t>(levels) * B * Hkv * sizeof(Parts));
   s.lse = weights ? take(static_cast<size_t>(B) * Hq * sizeof(float)) : 0;
   s.scores = weights ? take(static_cast<size_t>(B) * Hq * max_pages * kTile * sizeof(float)) : 0;
   s.bytes = at + 128;  // (the workspace may begin anywhere on a 16-byte boundary)
