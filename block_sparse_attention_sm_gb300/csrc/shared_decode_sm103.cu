@@ -42,9 +42,10 @@
 // the sequence's end is never read.
 //
 // Bound: 64 sequences (32 / 8 heads of 128) on a shared prefix of 32K keys with 100-900 of
-// their own take 64 us, 271 MB read, 61% of the copy rate: a tile that both streams take
-// costs ~3700 cycles (the softmax of 2 x 128 rows between two MMAs), one of a bundle ~2700
-// for the ~1300 of its bytes.  64 sequences of 32K each, nothing shared: 1.32 ms, 92%.
+// their own take 60 us, 271 MB read, 66% of the copy rate: a tile that both streams take
+// is ~4300 cycles (the softmax of 2 x 128 rows between two MMAs), one of a bundle ~2500
+// for the ~1300 of its bytes.  64 sequences of 32K each, nothing shared: 1.32 ms, 92%.  Small
+// batches are a chain: ~4 us until the first tile is asked for, 2 until its scores, 1.2 a tile.
 
 // With weights the raw scores also go to the workspace (4 G bytes a key and KV
 // head, beside 4 d of K and V), and when the merge has the row's denominator,
@@ -184,13 +185,15 @@ __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
   return d;
 }
 
-// Cost of a tile, in the shares of the CTAs: where both streams take every tile it is
-// about twice that of its bytes alone (2:3, 4:7, 1:2, 5:11 and 1:1 give 337, 331, 317, 320 and 379 us at
-// four layers of 64 sequences on a prefix of 32K keys).
-constexpr int kTileCost = 1, kBothCost = 2;
-__device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : kTileCost; }
+// Costs, in the shares of the CTAs: 1 for a tile of a bundle; where both streams take
+// every tile it is about twice that (2:3, 4:7, 1:2, 5:11 and 1:1 give 337, 331, 317, 320 and 379 us at
+// four layers of 64 sequences on a prefix of 32K keys).  An item costs kItemCost in front of
+// its first tile: a CTA that goes on to another one ends ~2 us later than the others
+// (0, 1, 2, 3, 4, 8: 299, 287, 291, 279, 279, 284 us there, and 3 of 24 us with 8 sequences of 2K).
+constexpr int kBothCost = 2, kItemCost = 3;
+__device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : 1; }
 // A CTA's share of all items' cost (at least a tile, so that each CTA between an item's
-// first and last has a part of it).  Costs fit 31 bits (kMaxSharedTiles).
+// first and last has a part of it).  Costs fit 32 bits (kMaxSharedTiles).
 __device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t ctas) {
   return max(static_cast<uint32_t>(kBothCost), (total + ctas - 1) / ctas);
 }
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Sums v{0, 0, 0}, all{0, 0, 0};
     Node x{}, y{};
     Deal d{};
+    auto leaf_cost = [&](uint32_t tiles) { return (tiles + kItemCost * ((B + nb - 1) / nb)) * p.Hkv; };
     // twice: adding up, then (with what lies below) writing
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -306,13 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pass == 1) {
           cum[n] = v.tiles;
           if (plan != nullptr) {
-            node_at[n] = all.tiles * p.Hkv * kTileCost + v.cost;
+            node_at[n] = leaf_cost(all.tiles) + v.cost;
             node_rows[n] = 2ll * p.Hq * B + v.rows;
           }
         }
         v.tiles += x.t1 - x.t0;
         if (y.t1 > y.t0) {
-          v.cost += (y.t1 - y.t0) * d.blocks * p.Hkv * cost_of(d);
+          v.cost += ((y.t1 - y.t0) * cost_of(d) + kItemCost) * d.blocks * p.Hkv;
           v.rows += static_cast<long long>(d.blocks) * p.Hkv * d.part;
         }
       }
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) {
       cum[B] = all.tiles;
-      ctl->leaf_total = all.tiles * p.Hkv * kTileCost;
+      ctl->leaf_total = leaf_cost(all.tiles);
       ctl->total = ctl->leaf_total + all.cost;
     }
   }
@@ -494,22 +498,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;                                      // .. or a shared node
       uint32_t n_at = 0;
       long long n_rows = 0;
+      auto tile_at = [&] {  // cost in front of tile `skip` of the item
+        return static_cast<uint32_t>(base + kItemCost * j) * p.Hkv + static_cast<uint32_t>(kvh) * (T + kItemCost) + kItemCost + skip;
+      };
       if (at < end) {
         const bool leaf = at < leaf_total;
         int lo = 0, hi = leaf ? (B + nb - 1) / nb : nodes;
 #pragma unroll 1
         while (hi - lo > 1) {  // the last one that begins at or below `at` (an empty one: the next begins there too)
           const int mid = (lo + hi) / 2;
-          if ((leaf ? cum[mid * nb] * p.Hkv * kTileCost : node_at[mid]) <= at) lo = mid; else hi = mid;
+          if ((leaf ? (cum[mid * nb] + kItemCost * mid) * p.Hkv : node_at[mid]) <= at) lo = mid; else hi = mid;
         }
         if (leaf) {
           j = lo;
           base = cum[j * nb];
           T = cum[min(B, (j + 1) * nb)] - base;
-          const uint32_t begin = base * p.Hkv * kTileCost, in = (at - begin + kTileCost - 1) / kTileCost;
-          at = begin + in * kTileCost;
-          kvh = min(p.Hkv - 1, static_cast<int>(in / T));
-          skip = in - kvh * T;
+          const uint32_t in = at - static_cast<uint32_t>(base + kItemCost * j) * p.Hkv;
+          kvh = in / (T + kItemCost);
+          skip = max(0, static_cast<int>(in - static_cast<uint32_t>(kvh) * (T + kItemCost)) - kItemCost);
+          at = tile_at();
         } else {
           n = lo;
         }
@@ -532,10 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           done = 0;
           if (at < leaf_total) {
             if (skip >= T) {  // the next head's, or the next bundle that has tiles
-              skip -= T;
               if (T == 0 || ++kvh == p.Hkv) {
                 kvh = 0;
-                if (++j * nb >= B) at = leaf_total;  // (no more)
+                base += T;
+                if (++j * nb >= B) {  // (no more)
+                  at = leaf_total;
+                  continue;
+                }
                 T = 0;
 #pragma unroll 1
                 for (int i = j * nb + lane; i < min(B, (j + 1) * nb); i += 32) {
@@ -544,6 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 T = __reduce_add_sync(0xffffffffu, T);
               }
+              skip = 0;
+              at = tile_at();
               continue;
             }
             const int first = j * nb, places = min(nb, B - first), rows = places * G;
@@ -555,24 +567,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             seg.both = 0;
             seg.out = 2ll * G * p.Hkv * first + 2ll * kvh * rows + static_cast<long long>(blockIdx.x) * kRows;
             if (seg.out + 2 * rows > p.part_rows) seg.out = -1;
-            left = min(T - skip, static_cast<int>((end - at + kTileCost - 1) / kTileCost));
-            at += left * kTileCost;
+            left = min(T - skip, static_cast<int>(end - at));
+            at += left;
             w0 = -32, before = window = 0;
           } else {
             const Node x = node_of(p, plan, B + n);
             const Deal d = deal_of(x, G);
-            const uint32_t Tn = x.t1 - x.t0, cost = cost_of(d), all = Tn * d.blocks * p.Hkv;
-            const uint32_t in = ((at > n_at ? at - n_at : 0u) + cost - 1) / cost;
-            if (in >= all) {
-              n_at += all * cost;
+            const uint32_t Tn = x.t1 - x.t0, cost = cost_of(d), each = Tn * cost + kItemCost;
+            const uint32_t items = Tn > 0 ? d.blocks * p.Hkv : 0, in = at > n_at ? at - n_at : 0;
+            uint32_t item = in / each, u = 0;
+            if (in > item * each + kItemCost) u = (in - item * each - kItemCost + cost - 1) / cost;
+            if (u >= Tn) u = 0, ++item;  // (the share begins in the item's last tile)
+            if (item >= items) {
+              n_at += items * each;
               at = max(at, n_at);
-              n_rows += Tn > 0 ? static_cast<long long>(d.blocks) * p.Hkv * d.part : 0;
+              n_rows += static_cast<long long>(items) * d.part;
               if (++n >= nodes) at = end;
               continue;
             }
-            at = n_at + in * cost;
+            at = n_at + item * each + kItemCost + u * cost;
             if (at >= end) break;
-            const int item = in / Tn, u = in - item * Tn;
             const int head = item / d.blocks;
             bundle = false;
             seg.kvh = head;
@@ -701,11 +715,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         Parts x{0, 0, 0};
         uint32_t a = 0, z = 0;  // cost in front of the row's first tile, of its last
         if (level == 0) {
-          const int j0 = i / nb * nb, places = min(nb, B - j0);
+          const int j = i / nb, j0 = j * nb, places = min(nb, B - j0);
           const uint32_t base = cum[j0], T = cum[j0 + places] - base, c0 = cum[i], n = cum[i + 1] - c0;
           if (n > 0) {
-            a = (base * p.Hkv + kvh * T + (c0 - base)) * kTileCost;
-            z = a + (n - 1) * kTileCost;
+            a = (base + kItemCost * j) * p.Hkv + kvh * (T + kItemCost) + kItemCost + (c0 - base);
+            z = a + n - 1;
             x.row = 2ll * G * p.Hkv * j0 + (2ll * kvh * places + (i - j0)) * G;
             x.second = places * G;
             x.count = 1;
@@ -718,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (T > 0 && place >= 0 && place < y.count) {
               const Deal d = deal_of(y, G);
               const int blk = d.blocks > 1 ? place * G / d.rows : 0, item = kvh * d.blocks + blk, cost = cost_of(d);
-              a = node_at[n - B] + item * T * cost;
+              a = node_at[n - B] + item * (T * cost + kItemCost) + kItemCost;
               z = a + (T - 1) * cost;
               x.row = node_rows[n - B] + static_cast<long long>(item) * d.part + (place * G - blk * d.rows);
               x.second = d.rows > kTile ? 0 : d.rows;
@@ -947,9 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // place, whose items were cut into pieces.  One block a (place, head): the attention
 // kernel has listed where they lie (a level a lane), a thread a piece has its weight, and a warp takes
 // every fourth or eighth piece, columns a lane; the warps' sums are added in order.
-// 256 threads as long as all blocks are resident (28 heads x 24 places: 6.8 us, with
-// 128 threads 8.5), 128 beyond (32 heads x 64 places: 11 us, with 256 threads 15.7): a
-// chain of dependent loads bounds it.
+// 256 threads as long as all blocks are resident (28 heads x 24 places: 5 us, with
+// 128 threads 6.5), 128 beyond (32 heads x 64 places: 6 us, with 256 threads 11): a chain
+// of dependent loads bounds it.
 template <int D, int kMerge>
 __global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p) {
   constexpr int L = 1 + kPlanLevels, E = D / 32, W = kMerge / 32;
