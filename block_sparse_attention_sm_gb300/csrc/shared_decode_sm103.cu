@@ -423,21 +423,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               continue;
             }
-            if (!(ok = wait(&ctl->turn[t], tn))) break;
-            tn ^= 1;
-            if (has_v) {  // O_t += P_t V
+            // Everything that the turn needs is waited for in front of it.
+            const bool first = u < 2 * lag, begins = first || place != before;
+            const uint32_t slot_v = slot, slot_k = !has_v ? slot : slot + 1 == NR ? 0 : slot + 1;
+            if (has_v) {
               if (!(ok = wait(&ctl->r_full[slot], par))) break;
-              const bool first = u < 2 * lag;
+              next();
               if (first) {  // the piece before has been read out of O
                 if (!(ok = wait(&ctl->o_free[t], on))) break;
                 on ^= 1;
               }
-              const bool begins = first || place != before;
               before = place;
               if (!(ok = wait(&ctl->p_full[t], pn))) break;
               pn ^= 1;
-              tc_fence_after();
-              const uint64_t dv = dv0 + slot * (C::kTileBytes >> 4);
+            }
+            if (has_k) {
+              if (!(ok = wait(&ctl->r_full[slot], par))) break;
+              next();
+              if (u < lag) {
+                if (!(ok = wait(&ctl->q_full[t], qn))) break;
+                qn ^= 1;
+              }
+            }
+            if (!(ok = wait(&ctl->turn[t], tn))) break;
+            tn ^= 1;
+            tc_fence_after();
+            if (has_v) {  // O_t += P_t V
+              const uint64_t dv = dv0 + slot_v * (C::kTileBytes >> 4);
               if (bundle) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
@@ -448,27 +460,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
               }
               if (u >= end) mma_commit(&ctl->o_full[t]);
-              mma_commit(&ctl->r_empty[slot]);
-              next();
+              mma_commit(&ctl->r_empty[slot_v]);
             }
             if (has_k) {  // S_t = Q_t K^T
-              if (!(ok = wait(&ctl->r_full[slot], par))) break;
-              if (u < lag) {
-                if (!(ok = wait(&ctl->q_full[t], qn))) break;
-                qn ^= 1;
-              }
               // (S_t was read before P_t was handed over: the fence in front of P.V covers it)
-              const uint64_t dk = dk0 + slot * (C::kTileBytes >> 4);
+              const uint64_t dk = dk0 + slot_k * (C::kTileBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                 mma_bf16_ss(colS, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
               }
               mma_commit(&ctl->s_full[t]);
-              mma_commit(&ctl->r_empty[slot]);
-              next();
             }
             mbar_arrive(&ctl->turn[t ^ 1]);
+            if (has_k) mma_commit(&ctl->r_empty[slot_k]);
             if (has_k && bundle) {
               // (Behind the turn, where it costs no time.)  A bundle's tile counts for the
               // rows of one sequence: P.V leaves the others' lanes as they are, whatever
