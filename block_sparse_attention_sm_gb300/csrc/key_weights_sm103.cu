@@ -34,8 +34,8 @@
 //
 // Bound: a step of two tiles is ~1240 cycles of MMAs (measured without any reduction: their
 // operands come from shared memory) and 1024 of exponentials; it takes ~1800 in the rows'
-// pass, ~1950 in the keys' (two prompts of 8K, 32 / 8 heads of 128: 390 and 440 us, 1.6 times
-// the operations at the cuBLAS rate), for the reducing warps of an SM wait, load and compute in
+// pass, ~1950 in the keys' (two prompts of 8K, 32 / 8 heads of 128: 801 us together, 3.1 times
+// one pass's operations at the cuBLAS rate), for the reducing warps of an SM wait, load and compute in
 // step with one another.  A window of 32 tokens on long prompts is bound by its keys, read
 // twice (64 us a pass for 344 MB).  Measured and not taken: issuers in turns (rows +4%, keys -4%),
 // the loads of 32 columns ahead of the reduction (+20%), 512 fixed rows an item, which halves what
