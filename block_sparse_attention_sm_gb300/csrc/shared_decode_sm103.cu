@@ -46,7 +46,7 @@
 // is 2.2 us (the issuers' turns; the softmax waits half of the time), one of a bundle
 // 1.2 us.  64 sequences of 32K each, nothing shared: 1.30 ms, 94%.  Small batches are a
 // chain: ~4 us until the first tile is asked for, 2 until its scores, 1.2 a tile.
-
+//
 // With weights the raw scores also go to the workspace (4 G bytes a key and KV
 // head, beside 4 d of K and V), and when the merge has the row's denominator,
 // weigh_kernel adds up exp2(s - lse) over the group's heads.  Each sum is made
