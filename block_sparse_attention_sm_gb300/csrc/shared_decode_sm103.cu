@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (left alone both fell into step: 4700 cycles a tile), and there are two so that
       // one's waits and commits run beside the other's MMAs (a single issuer: 4400).
       // Both pass every entry of the ring in order, those of the other stream too.
-      if (lane == 0) {
-        const int t = warp == kWarpMma ? 0 : 1;
+      {  // (a whole warp, one lane of which issues: what the MMAs are given stays uniform)
+        const int t = __shfl_sync(0xffffffffu, warp == kWarpMma ? 0 : 1, 0);
+        auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
         constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
         const uint64_t dq = smem_desc(smem_u32(sQ) + t * C::kTileBytes, 16, 1024);
@@ -403,8 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t off[4] = {0, 0, 0, 0};  // lanes that the stream's last tile does not count for
 #pragma unroll 1
         for (int k = 0, u = 0; ok; ++k) {
-          const Segment* x = seg_at(k);
-          if (x == nullptr || x->n == 0) break;
+          if (!wwait(&ctl->seg_full[k % kSegments], (k / kSegments) & 1)) break;
+          const Segment* x = &ctl->seg[k % kSegments];
+          if (x->n == 0) break;
           // P.V follows its scores by one tile (both streams) or two (alternate ones).
           const int n = x->n, both = x->both, lag = both ? 1 : 2, last = x->end;
           if (x->start != 0) u = 0;
@@ -417,8 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mine) {
 #pragma unroll 1
               for (int e = has_v + has_k; ok && e > 0; --e) {
-                ok = wait(&ctl->r_full[slot], par);
-                mbar_arrive(&ctl->r_empty[slot]);
+                ok = wwait(&ctl->r_full[slot], par);
+                if (elect_one()) mbar_arrive(&ctl->r_empty[slot]);
+                __syncwarp();
                 next();
               }
               continue;
@@ -427,53 +430,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool first = u < 2 * lag, begins = first || place != before;
             const uint32_t slot_v = slot, slot_k = !has_v ? slot : slot + 1 == NR ? 0 : slot + 1;
             if (has_v) {
-              if (!(ok = wait(&ctl->r_full[slot], par))) break;
+              if (!(ok = wwait(&ctl->r_full[slot], par))) break;
               next();
               if (first) {  // the piece before has been read out of O
-                if (!(ok = wait(&ctl->o_free[t], on))) break;
+                if (!(ok = wwait(&ctl->o_free[t], on))) break;
                 on ^= 1;
               }
               before = place;
-              if (!(ok = wait(&ctl->p_full[t], pn))) break;
+              if (!(ok = wwait(&ctl->p_full[t], pn))) break;
               pn ^= 1;
             }
             if (has_k) {
-              if (!(ok = wait(&ctl->r_full[slot], par))) break;
+              if (!(ok = wwait(&ctl->r_full[slot], par))) break;
               next();
               if (u < lag) {
-                if (!(ok = wait(&ctl->q_full[t], qn))) break;
+                if (!(ok = wwait(&ctl->q_full[t], qn))) break;
                 qn ^= 1;
               }
             }
-            if (!(ok = wait(&ctl->turn[t], tn))) break;
+            if (!(ok = wwait(&ctl->turn[t], tn))) break;
             tn ^= 1;
             tc_fence_after();
             if (has_v) {  // O_t += P_t V
               const uint64_t dv = dv0 + slot_v * (C::kTileBytes >> 4);
-              if (bundle) {
+              if (elect_one()) {
+                if (bundle) {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  mma_bf16_ts_lanes(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, off, (!begins || kk > 0) ? 1u : 0u);
-              } else {
+                  for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_bf16_ts_lanes(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, off, (!begins || kk > 0) ? 1u : 0u);
+                } else {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+                  for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_bf16_ts(colO, colS + kk * 8, dv + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+                }
+                if (u >= end) mma_commit(&ctl->o_full[t]);
+                mma_commit(&ctl->r_empty[slot_v]);
               }
-              if (u >= end) mma_commit(&ctl->o_full[t]);
-              mma_commit(&ctl->r_empty[slot_v]);
+              __syncwarp();
             }
             if (has_k) {  // S_t = Q_t K^T
               // (S_t was read before P_t was handed over: the fence in front of P.V covers it)
               const uint64_t dk = dk0 + slot_k * (C::kTileBytes >> 4);
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                mma_bf16_ss(colS, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                  mma_bf16_ss(colS, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&ctl->s_full[t]);
               }
-              mma_commit(&ctl->s_full[t]);
+              __syncwarp();
             }
-            mbar_arrive(&ctl->turn[t ^ 1]);
-            if (has_k) mma_commit(&ctl->r_empty[slot_k]);
+            if (elect_one()) {
+              mbar_arrive(&ctl->turn[t ^ 1]);
+              if (has_k) mma_commit(&ctl->r_empty[slot_k]);
+            }
+            __syncwarp();
             if (has_k && bundle) {
               // (Behind the turn, where it costs no time.)  A bundle's tile counts for the
               // rows of one sequence: P.V leaves the others' lanes as they are, whatever
@@ -486,10 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          seg_done(k);
+          __syncwarp();
+          if (elect_one()) seg_done(k);
+          __syncwarp();
         }
-        mma_commit(&ctl->mma_done[t]);
-        mbar_wait(&ctl->mma_done[t], 0, nullptr);
+        if (elect_one()) {
+          mma_commit(&ctl->mma_done[t]);
+          mbar_wait(&ctl->mma_done[t], 0, nullptr);
+        }
       }
       __syncwarp();
     } else if (warp == kWarpPlan) {
