@@ -95,6 +95,24 @@ def test_against_64_bits(ss, B, groups, root, doc, own, Hq, Hkv, d, planned):
     check(ss, q, kp, vp, table, lens, plan, weights=False)
 
 
+@pytest.mark.parametrize("B", [2, 8, 9, 16])
+def test_plans_of_small_batches(ss, B):
+    """The sequences' places and the nodes above them, by one launch or two, and what they share with them."""
+    rng = np.random.default_rng(B)
+    lens, table, pages = tree_batch(rng, B, 2, 400, 300, [int(x) for x in rng.integers(1, 300, B)])
+    q, kp, vp, table, lens = make(rng, lens, table, pages, 8, 2, 64)
+    plans = [ss.prefix_plan(table, lens) for _ in range(3)]
+    assert sorted(plans[0][8:8 + B].tolist()) == list(range(B))
+    assert all(torch.equal(p, plans[0]) for p in plans)
+    check(ss, q, kp, vp, table, lens, plans[0])
+    order = torch.from_numpy(rng.permutation(B)).cuda()
+    o, _ = check(ss, q, kp, vp, table, lens, plans[0], weights=False)
+    swapped = table[order].contiguous()
+    p, _ = check(ss, q[order].contiguous(), kp, vp, swapped, lens[order].contiguous(), ss.prefix_plan(swapped, lens[order].contiguous()),
+                 weights=False)
+    assert p.shape == o.shape
+
+
 def batch(rng, B=12, groups=3, root=300, doc=200, own=300, Hq=8, Hkv=2, d=128):
     lens, table, pages = tree_batch(rng, B, groups, root, doc, [int(x) for x in rng.integers(1, own + 1, B)])
     return make(rng, lens, table, pages, Hq, Hkv, d)

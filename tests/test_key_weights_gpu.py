@@ -153,6 +153,28 @@ def test_more_tokens_than_a_share_and_many_sequences(ss):
     check(ss, *make(rng, [64], [60000], 4, 1, 128))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_sequences_than_threads(ss, causal):
+    rng = np.random.default_rng(5)
+    n = [int(x) for x in rng.integers(0, 4, 1500)]
+    n[700] = 90
+    L = [int(x) * (int(y) > 0) + k for x, y, k in zip(rng.integers(0, 150, 1500), rng.integers(0, 5, 1500), n)]
+    check(ss, *make(rng, n, L, 6, 3, 64, pad=2), causal=causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,L,Hq,Hkv,d", [
+    ([7], [50000], 2, 1, 128),  # one block of rows, cut: alternate tiles of keys
+    ([900, 3], [100, 7], 4, 2, 64),  # one tile of keys, cut: alternate blocks of rows
+    ([1000], [128], 128, 1, 128),  # a token a block
+    ([2100, 40], [2100, 2400], 5, 5, 64),
+    ([600], [9000], 35, 7, 128),
+])
+def test_items_that_are_cut(ss, n, L, Hq, Hkv, d, causal):
+    rng = np.random.default_rng(sum(n) + sum(L) + Hq)
+    check(ss, *make(rng, n, L, Hq, Hkv, d, pad=1), causal=causal)
+
+
 def test_one_sequence_cannot_reach_another(ss):
     """Infinities and NaN in one sequence's keys or queries change nothing for the others, bit for bit."""
     rng = np.random.default_rng(4)
