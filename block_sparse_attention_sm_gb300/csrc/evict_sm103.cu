@@ -263,9 +263,9 @@ __global__ void __launch_bounds__(kChoose, 2)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
           if (w + i >= w1) break;
-          const bool in = w + i < w1 && (w + i) * 32 + lane < rest && (u[i] & known) == value;
+          // (what lies behind the older keys counts as 0, below which nothing is: the counts above a bin are right)
           const int bin = static_cast<int>((u[i] >> low) & ((1u << width_bits) - 1));
-          if (in) atomicAdd(&bins[bin], 1);  // (lanes that add one to the same word are counted by the hardware)
+          if ((u[i] & known) == value) atomicAdd(&bins[bin], 1);  // (lanes that add one to the same word are counted by the hardware)
         }
       }
       __syncthreads();

@@ -56,7 +56,7 @@ struct SharedParams {
   uint32_t* status;
 };
 
-// Tiles over all sequences and KV heads that a table may have room for: their cost (2 a tile and 3 an item at
+// Tiles over all sequences and KV heads that a table may have room for: their cost (3 a tile and 3 an item at
 // most, and as much again for each level of shared nodes at most) is counted in 32 bits.
 constexpr long kMaxSharedTiles = 1l << 29, kMaxPlannedTiles = 1l << 26;
 

@@ -132,6 +132,7 @@ struct Ctl {
   int abort_flag;
   int n_issued;
   uint32_t leaf_total, total;  // cost of all bundles, of all items
+  uint32_t least;                // a share's least cost
   Segment seg[kSegments];
 };
 
@@ -190,12 +191,15 @@ __device__ __forceinline__ Deal deal_of(const Node& x, int G) {
 // four layers of 64 sequences on a prefix of 32K keys).  An item costs kItemCost in front of
 // its first tile: a CTA that goes on to another one ends ~2 us later than the others
 // (0, 1, 2, 3, 4, 8: 299, 287, 291, 279, 279, 284 us there, and 3 of 24 us with 8 sequences of 2K).
-constexpr int kBothCost = 2, kItemCost = 3;
-__device__ __forceinline__ int cost_of(const Deal& d) { return d.rows > kTile ? kBothCost : 1; }
-// A CTA's share of all items' cost (at least a tile, so that each CTA between an item's
-// first and last has a part of it).  Costs fit 32 bits (kMaxSharedTiles).
-__device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t ctas) {
-  return max(static_cast<uint32_t>(kBothCost), (total + ctas - 1) / ctas);
+constexpr int kItemCost = 3;
+// (With weights each of the rows writes its scores: three times; 64 sequences on 8K keys 2, 3, 4: 95, 88, 86 us,
+// 24 on 8K 43, 41, 46.)
+__device__ __forceinline__ int both_cost(const SharedParams& p) { return p.scores != nullptr ? 3 : 2; }
+__device__ __forceinline__ int cost_of(const SharedParams& p, const Deal& d) { return d.rows > kTile ? both_cost(p) : 1; }
+// A CTA's share of all items' cost: at least a tile of any kind (`least`), so that each CTA
+// between an item's first and last has a part of it.  Costs fit 32 bits (kMaxSharedTiles).
+__device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t ctas, uint32_t least) {
+  return max(least, (total + ctas - 1) / ctas);
 }
 
 // What the places below a place have: own tiles, cost and partial rows of their shared nodes.
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Sums v{0, 0, 0}, all{0, 0, 0};
     Node x{}, y{};
     Deal d{};
+    bool wide = false;  // a node of more than 128 rows
     auto leaf_cost = [&](uint32_t tiles) { return (tiles + kItemCost * ((B + nb - 1) / nb)) * p.Hkv; };
     // twice: adding up, then (with what lies below) writing
 #pragma unroll 1
@@ -316,13 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         v.tiles += x.t1 - x.t0;
         if (y.t1 > y.t0) {
-          v.cost += ((y.t1 - y.t0) * cost_of(d) + kItemCost) * d.blocks * p.Hkv;
+          wide |= d.rows > kTile;
+          v.cost += ((y.t1 - y.t0) * cost_of(p, d) + kItemCost) * d.blocks * p.Hkv;
           v.rows += static_cast<long long>(d.blocks) * p.Hkv * d.part;
         }
       }
       if (pass == 0) all = block_sums(v, (B + each - 1) / each, plan != nullptr, reinterpret_cast<Sums*>(ctl->seg));
     }
+    wide = __syncthreads_or(wide);
     if (tid == 0) {
+      ctl->least = wide ? both_cost(p) : 2;  // (two tiles of a bundle: a stream each)
       cum[B] = all.tiles;
       ctl->leaf_total = leaf_cost(all.tiles);
       ctl->total = ctl->leaf_total + all.cost;
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpPlan) {
       // ---------------------------------------------------------- pieces
       // A tile belongs to the CTA whose share its cost begins in.
-      const uint32_t leaf_total = ctl->leaf_total, total = ctl->total, per = share_of(total, gridDim.x);
+      const uint32_t leaf_total = ctl->leaf_total, total = ctl->total, per = share_of(total, gridDim.x, ctl->least);
       uint32_t at = min(total, per * blockIdx.x);
       const uint32_t end = min(at + per, total);
       // Where the share begins: in a bundle ..
@@ -594,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             const Node x = node_of(p, plan, B + n);
             const Deal d = deal_of(x, G);
-            const uint32_t Tn = x.t1 - x.t0, cost = cost_of(d), each = Tn * cost + kItemCost;
+            const uint32_t Tn = x.t1 - x.t0, cost = cost_of(p, d), each = Tn * cost + kItemCost;
             const uint32_t items = Tn > 0 ? d.blocks * p.Hkv : 0, in = at > n_at ? at - n_at : 0;
             uint32_t item = in / each, u = 0;
             if (in > item * each + kItemCost) u = (in - item * each - kItemCost + cost - 1) / cost;
@@ -729,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto place_row = [&](int r) { return p.inv_g != 0 ? static_cast<int>(__umulhi(r, p.inv_g)) : r; };  // r / G
     {  // Where the merge finds the results of a (place, KV head): this CTA's part of the list, while there is nothing else to do.
       const int levels = plan != nullptr ? 1 + kPlanLevels : 1, all = B * p.Hkv * levels;
-      const uint32_t per = share_of(ctl->total, gridDim.x);
+      const uint32_t per = share_of(ctl->total, gridDim.x, ctl->least);
 #pragma unroll 1
       for (int e = blockIdx.x * 256 + tid; e < all; e += gridDim.x * 256) {
         const int level = e & (levels - 1), r = plan != nullptr ? e / (1 + kPlanLevels) : e, i = r / p.Hkv, kvh = r - i * p.Hkv;
@@ -752,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int T = y.t1 - y.t0, place = i - y.first;
             if (T > 0 && place >= 0 && place < y.count) {
               const Deal d = deal_of(y, G);
-              const int blk = d.blocks > 1 ? place * G / d.rows : 0, item = kvh * d.blocks + blk, cost = cost_of(d);
+              const int blk = d.blocks > 1 ? place * G / d.rows : 0, item = kvh * d.blocks + blk, cost = cost_of(p, d);
               a = node_at[n - B] + item * (T * cost + kItemCost) + kItemCost;
               z = a + (T - 1) * cost;
               x.row = node_rows[n - B] + static_cast<long long>(item) * d.part + (place * G - blk * d.rows);
