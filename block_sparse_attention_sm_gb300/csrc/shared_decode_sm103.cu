@@ -434,19 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               continue;
             }
-            // Everything that the turn needs is waited for in front of it.
+            // The tiles are waited for in front of the turn, the weights last: they come latest.
             const bool first = u < 2 * lag, begins = first || place != before;
             const uint32_t slot_v = slot, slot_k = !has_v ? slot : slot + 1 == NR ? 0 : slot + 1;
             if (has_v) {
               if (!(ok = wwait(&ctl->r_full[slot], par))) break;
               next();
-              if (first) {  // the piece before has been read out of O
-                if (!(ok = wwait(&ctl->o_free[t], on))) break;
-                on ^= 1;
-              }
               before = place;
-              if (!(ok = wwait(&ctl->p_full[t], pn))) break;
-              pn ^= 1;
             }
             if (has_k) {
               if (!(ok = wwait(&ctl->r_full[slot], par))) break;
@@ -458,6 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!(ok = wwait(&ctl->turn[t], tn))) break;
             tn ^= 1;
+            if (has_v) {
+              if (first) {  // the piece before has been read out of O
+                if (!(ok = wwait(&ctl->o_free[t], on))) break;
+                on ^= 1;
+              }
+              if (!(ok = wwait(&ctl->p_full[t], pn))) break;
+              pn ^= 1;
+            }
             tc_fence_after();
             if (has_v) {  // O_t += P_t V
               const uint64_t dv = dv0 + slot_v * (C::kTileBytes >> 4);
