@@ -42,10 +42,11 @@
 // the sequence's end is never read.
 //
 // Bound: 64 sequences (32 / 8 heads of 128) on a shared prefix of 32K keys with 100-900 of
-// their own take 60 us, 271 MB read, 66% of the copy rate: a tile that both streams take
-// is 2.2 us (the issuers' turns; the softmax waits half of the time), one of a bundle
-// 1.2 us.  64 sequences of 32K each, nothing shared: 1.30 ms, 94%.  Small batches are a
-// chain: ~4 us until the first tile is asked for, 2 until its scores, 1.2 a tile.
+// their own take 60 us, 271 MB read: 7 us until the first scores, then the pages at 80% of
+// the copy rate (a tile that both streams take: ~3600 cycles, of which scores and P.V issue
+// for 1100 a stream and the softmax takes 1450; one of a bundle waits for its bytes).  64
+// sequences of 32K each, nothing shared: 1.29 ms, 95%.  Small batches are a chain: ~4 us
+// until the first tile is asked for, 2 until its scores, 1.2 a tile.
 //
 // With weights the raw scores also go to the workspace (4 G bytes a key and KV
 // head, beside 4 d of K and V), and when the merge has the row's denominator,
