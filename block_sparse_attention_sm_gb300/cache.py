@@ -70,16 +70,16 @@ def _writable(name, t):
 def _on(stream, names, *tensors):
     """Device and stream of a call: (stream handle, context to make it in).
 
-    All tensors must be on one CUDA device.  Inside the context that device is
-    current and torch allocates on that stream; where both are so already
-    there is nothing to enter."""
+    All tensors must be on one CUDA device (``names``: theirs, or a function
+    that gives them).  Inside the context that device is current and torch
+    allocates on that stream; where both are so already there is nothing to enter."""
     dev = None
     for t in tensors:
         if t is not None:
             d = t.get_device()
             if d != dev:
                 if d < 0 or dev is not None:
-                    name = names.split()[[t is u for u in tensors].index(True)]
+                    name = (names if isinstance(names, str) else names()).split()[[t is u for u in tensors].index(True)]
                     raise ValueError(f"{name}: must be a CUDA tensor, got device {t.device}" if d < 0 else
                                      f"tensors on several devices: {name} on {t.device}, others on cuda:{dev}")
                 dev = d
@@ -734,7 +734,7 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
         raise ValueError(f"out_weights: expected {len(weights)} tensors, got {len(out_weights)}")
     page_bytes = _pools(pools, num_pages)
     Hkv = weights[0].shape[1] if isinstance(weights[0], torch.Tensor) and weights[0].ndim == 3 else 0
-    shape = torch.Size((num_rows, Hkv, max_pages * 128))
+    shape = (num_rows, Hkv, max_pages * 128)
     for some in (weights, out_weights) if out_weights is not None else (weights,):
         for t in some:
             if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
@@ -757,7 +757,7 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
     if result is not None:
         _dense("result", result, _I32, shape=(1,))
     moved = weights if out_weights is None else out_weights
-    handle, context = _on(stream, "page_refs page_table seq_lens keep rows out_refs out_table out_lens result workspace" +
+    handle, context = _on(stream, lambda: "page_refs page_table seq_lens keep rows out_refs out_table out_lens result workspace" +
                           " pool" * len(pools) + " weights" * len(weights) + " out_weights" * len(moved), page_refs, page_table,
                           seq_lens, keep, rows, out_refs, out_table, out_lens, result, workspace, *pools, *weights, *moved)
     with context:
@@ -776,5 +776,5 @@ def pages_evict(pools, weights, page_refs, page_table, seq_lens, keep, *, rows=N
             result.data_ptr(), ws.data_ptr(), nbytes, handle)
     if st:
         raise SSError(st, "ss_pages_evict")
-    _written(tuple(moved))
+    _written(moved)
     return result
