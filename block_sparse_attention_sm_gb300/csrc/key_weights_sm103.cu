@@ -574,7 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (x.n > 0) break;
           }
-          if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag)) break;
+          // (A place is free when its piece is done, after millions of steps of 1-2 us on the longest caches: 60 us of limit for each.  The
+          // other warps' waits end with a tile and set the flag if they do not.)
+          const uint32_t more = k < kPieces ? 0u : 16u * static_cast<uint32_t>(min(ctl->piece[k % kPieces].n, 1 << 26));
+          if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag, kSmallTries + more)) break;
           ctl->piece[k % kPieces] = x;
           mbar_arrive(&ctl->piece_full[k % kPieces]);
           if (x.n == 0) break;

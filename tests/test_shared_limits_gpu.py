@@ -1,0 +1,56 @@
+"""The calls over shared pages and the record of attention weights at the ends of their ranges."""
+import pytest
+import torch
+
+from _serving import PAGE, offsets
+from _shared import assert_close, sequence, softmax
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import block_sparse_attention_sm_gb300 as ss
+
+    ss.build()
+    return ss
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_key_weights_of_items_that_take_seconds(ss):
+    """A CTA's first item has three million steps, and short ones stand behind it: no wait is given up.
+
+    All pages of the long sequence are the same one, so that its 384 million keys take little memory.
+    304 tokens of 128 heads on one KV head are 152 pairs of blocks, about one a CTA; the last CTA has
+    the two other sequences' as well."""
+    many, d, G = 3_000_000, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    kp, n = mk(3, 1, PAGE, d), [304, 2, 3]
+    q = mk(sum(n), G, d)
+    table = torch.zeros(3, many, dtype=torch.int32, device="cuda")
+    table[1, :1], table[2, :2] = 1, ints([2, 1])
+    lens = ints([many * PAGE, 100, 200])
+    w = torch.zeros(3, 1, many * PAGE, device="cuda")
+    ss.key_weights(q, kp, table, offsets(n).cuda(), lens, w, scale=0.05, causal=False)
+    assert ss.stream_status() is None
+    for b, (at, L) in enumerate(((0, 0), (304, 100), (306, 200))):
+        if b == 0:
+            continue
+        k = sequence(kp, table[b], L)
+        P, rel = softmax(q[at:at + n[b]], k, 0.05, torch.full((n[b],), L - 1, device="cuda"))
+        want = P.sum((1, 2))
+        # (n * G rows, 64 pairs of a block's along a thread: see the tests of the record itself)
+        assert_close(w[b, :, :L], want, (P * rel).sum((1, 2)) + want * (64 + 4 + n[b] * G / 64) * 2.0 ** -24 + 1e-37, f"sequence {b}")
+        assert not w[b, :, L:].any()
+    # The long sequence: 128 keys, each `many` times, all of a kind alike.  A row's sum adds `many` terms to one
+    # number, each rounding at 2^-24 of it (and once more where the halves and streams are joined): in all below
+    # many * 2^-24 = 0.18 of it either way.
+    P, _ = softmax(q[:304], sequence(kp, table[0], PAGE), 0.05, torch.full((304,), PAGE - 1, device="cuda"))
+    got, want = w[0].view(1, many, PAGE), P.sum((1, 2)) / many
+    for at in (0, 1, many // 2, many - 1):
+        ratio = got[:, at].double() / want
+        assert ((ratio > 1 / 1.19) & (ratio < 1 / (1 - 0.19))).all(), ratio
