@@ -453,7 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_keys(sR + st * C::kTileBytes, &ctl->r_full[st], x, page);
             } else {
               load_queries(sR + st * C::kTileBytes, &ctl->r_full[st], x, u);
-              if (!waited) wait_for_previous();  // (the rows' lse)
+              // (The rows' lse.  The waits of the other warps for tiles and results are bounded, that one
+              // is not: they make it too before the first that depends on it.)
+              if (!waited) wait_for_previous();
               waited = true;
               bulk_load(ctl->hand.keys.lse[ls], lse_of + static_cast<long>(u) * kTile, kTile * sizeof(float), &ctl->r_full[st]);
             }
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort_flag));
       };
       bool ok = true;
+      if (!ROWS) wait_for_previous();  // (see the loader: no tile comes before that)
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         if (!wwait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1)) break;
@@ -576,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // (A place is free when its piece is done, after millions of steps of 1-2 us on the longest caches: 60 us of limit for each.  The
           // other warps' waits end with a tile and set the flag if they do not.)
+          if (!ROWS && k == kPieces) wait_for_previous();
           const uint32_t more = k < kPieces ? 0u : 16u * static_cast<uint32_t>(min(ctl->piece[k % kPieces].n, 1 << 26));
           if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag, kSmallTries + more)) break;
           ctl->piece[k % kPieces] = x;
@@ -622,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sn = 0, hn = 0, cn = 0;
     int e0 = 0;  // ring entries of the pieces before
     bool ok = true;
+    if (!ROWS) wait_for_previous();  // (see the loader: no score comes before that)
 #pragma unroll 1
     for (int k = 0; ok; ++k, ++hn) {
       ok = wwait(&ctl->piece_full[k % kPieces], (k / kPieces) & 1);

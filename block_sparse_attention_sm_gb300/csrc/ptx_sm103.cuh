@@ -96,8 +96,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // The same in few instructions, for kernels whose code is read anew by every launch (cold
 // instruction caches): the limit is a number of tries.  A try that fails lasts 3.8 us on a
 // GB300 (measured with 1, 32 and 640 waiting threads; the same with a hint of 0.1, 1, 10 us and
-// without one), so the usual limit is 4 seconds.  PTX promises no least time: a wait that
-// may last for seconds has its limit raised with its work.
+// without one), so the usual limit is 4 seconds.  PTX promises no least time: a
+// wait counts on its own CTA's progress alone, never on the end of a kernel in front
+// (wait_for_previous does that, without a limit), and one that may last for seconds has
+// its limit raised with its work.
 constexpr uint32_t kSmallTries = 1u << 20;
 __device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                 uint32_t limit = kSmallTries) {
