@@ -1099,7 +1099,8 @@ __global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams
     // (a sequence without keys: zeros; NaN stays)
     p.o[to * D + tid] = __float2bfloat16(l == 0.f ? 0.f : v / l);
   }
-  if (p.lse != nullptr && tid == 0) p.lse[to] = m + log2f(l);
+  // (a row without keys, or whose scores are all -infinity, adds nothing to the weights either)
+  if (p.lse != nullptr && tid == 0) p.lse[to] = l == 0.f ? INFINITY : m + log2f(l);
 }
 
 // weights[b][kvh][key] += sum over the group's heads of exp2(s * scale * log2e - lse).

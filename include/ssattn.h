@@ -648,8 +648,9 @@ ss_status ss_prefix_plan(const int32_t* page_table, const int32_t* seq_lens, int
  *   q: bf16 [B][Hq][d], 16-byte aligned; q_token_stride: elements between
  *     sequences (0: Hq * d; a multiple of 8).  o: bf16 [B][Hq][d] contiguous.
  *   k_pages, v_pages, page_table, seq_lens: as in ss_attn_decode_paged (what a
- *     page holds behind its sequence's end is not read; a sequence without keys
- *     gives zeros; an entry that names no page reads zeros).
+ *     page holds behind its sequence's end is not read; a sequence without keys,
+ *     and a head whose scores are all -infinity in fp32, give zeros and add no weight; an
+ *     entry that names no page reads zeros).
  *   plan: what ss_prefix_plan made for this table and B; NULL, or a plan of
  *     other sizes: every sequence reads its own pages.
  *   weights: nullable fp32 [B][Hkv][max_pages * 128], 16-byte aligned: cell k of
@@ -676,7 +677,7 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
  * tokens, without the attention's output: cell k of (sequence b, KV head h) of
  * `weights` gains the sum, over the sequence's n_b new tokens i and the G query
  * heads of h, of the softmax weight of key k.  Causal: token i sees the keys up to
- * L_b - n_b + i (a row that sees none adds nothing), otherwise all L_b.  A
+ * L_b - n_b + i (a row that sees none, or whose scores are all -infinity in fp32, adds nothing), otherwise all L_b.  A
  * prompt's last tokens alone are a step of that many new tokens.
  *   q, q_token_stride, k_pages, page_table, cu_seqlens, seq_lens: as in
  *     ss_attn_chunk_paged (what a page holds behind its sequence's end, and rows

@@ -54,3 +54,31 @@ def test_key_weights_of_items_that_take_seconds(ss):
     for at in (0, 1, many // 2, many - 1):
         ratio = got[:, at].double() / want
         assert ((ratio > 1 / 1.19) & (ratio < 1 / (1 - 0.19))).all(), ratio
+
+
+def test_rows_whose_scores_are_all_minus_infinity(ss):
+    """Scores of -2^200, below what fp32 holds, in all of a row: it gives zeros and adds nothing to the record, here and there."""
+    d, L = 64, [300, 129, 128]
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kp, vp = (torch.randn(7, 2, PAGE, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    kp[..., 0] = 2.0 ** 100
+    q = torch.randn(3, 4, d, generator=g, device="cuda").to(torch.bfloat16)
+    q[..., 0] = 0
+    table, lens = ints([[0, 1, 2], [3, 4, -1], [5, -1, -1]]), ints(L)
+    clean = torch.rand(3, 2, 3 * PAGE, generator=g, device="cuda")
+    q[0, 1, 0] = q[1, 2:, 0] = q[2, :, 0] = -2.0 ** 100  # one of a group's heads, a whole group, all of a sequence
+    gone = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    gone[0, 1] = gone[1, 2:] = gone[2] = True
+    a, b = clean.clone(), clean.clone()
+    o = ss.decode_shared(q, kp, vp, table, lens, ss.prefix_plan(table, lens), scale=0.1, weights=a)
+    ss.key_weights(q, kp, table, offsets([1, 1, 1]).cuda(), lens, b, scale=0.1)
+    assert ss.stream_status() is None
+    assert (o[gone] == 0).all() and torch.isfinite(o.float()).all() and (o[~gone].abs().amax(-1) > 0).all()
+    for i, n in enumerate(L):
+        P, rel = softmax(torch.where(gone[i, :, None], torch.zeros_like(q[i]), q[i])[None], sequence(kp, table[i], n), 0.1,
+                         torch.tensor([n - 1], device="cuda"))
+        P = P * ~gone[i].view(2, 1, 2, 1)
+        want = clean[i, :, :n].double() + P.sum((1, 2))
+        for w in (a, b):
+            assert_close(w[i, :, :n], want, (P * rel).sum((1, 2)) + want * 2.0 ** -22 + 1e-37, f"sequence {i}")
+            assert torch.equal(w[i, :, n:], clean[i, :, n:])
