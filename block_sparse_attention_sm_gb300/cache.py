@@ -417,7 +417,9 @@ def prefix_plan(page_table, seq_lens, *, out=None, stream=None):
     and that are full in both (as after :func:`pages_fork`), in any grouping
     and on several levels.  The plan holds as long as these pages stay where
     they are: over steps that append keys, but not across a fork, free,
-    eviction or compaction, after which it is made anew."""
+    eviction or compaction, nor where a sequence becomes shorter than the pages
+    it shares (a rollback behind them is fine); then it is made anew.  The
+    device's time grows with the pairs of sequences that begin alike and the pages they share."""
     _dense("page_table", page_table, _I32, 2)
     B, max_pages = page_table.shape
     _dense("seq_lens", seq_lens, _I32, None, (B,))
@@ -477,7 +479,9 @@ def _pages_of(k_pages, d):
 
 
 def decode_shared_workspace(B, Hq, Hkv, max_pages, d, device, *, plan=True, weights=False):
-    """A workspace that serves every :func:`decode_shared` call of up to B sequences and max_pages pages each."""
+    """A workspace that serves every :func:`decode_shared` call of up to B sequences and max_pages pages each.
+
+    With ``weights`` it holds the scores: 512 * B * Hq * max_pages bytes, however long the sequences are."""
     n = capi.ss_attn_decode_shared_workspace_size(B, Hq, Hkv, max_pages, d, plan, weights)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -492,7 +496,9 @@ def decode_shared(q, k_pages, v_pages, page_table, seq_lens, plan=None, *, scale
     nothing is shared.  Every key counts (no skip test).  ``weights`` float32
     [B,Hkv,max_pages*128]: each key's softmax weight, summed over the query
     heads of its KV head, is added to it (:func:`pages_evict` chooses by it);
-    cells behind a sequence's end are left as they are.  A sequence without keys
+    cells behind a sequence's end are left as they are (the call's workspace then
+    takes 512 * B * Hq * max_pages bytes: make one for all layers with
+    :func:`decode_shared_workspace`).  A sequence without keys
     gives zeros.  Returns o [B,Hq,d].  A serving call: it records no gradients."""
     (B, Hq, d), stride = _tokens(q)
     _dense("page_table", page_table, _I32, 2)

@@ -632,9 +632,11 @@ ss_status ss_pages_evict(void* const* pools, int num_pools, size_t page_bytes, f
  *   plan: device int32, ss_prefix_plan_size(B) bytes (0: B not in 1 .. 8192).
  * It holds the order of the sequences and ranges of tiles, no lengths: it is
  * good as long as the shared pages stay in their places, over steps in which
- * sequences grow, but not over a fork, free, eviction or compaction (shared
- * tiles would be read for rows that no longer have them; memory beyond the given
- * arrays is not touched whatever a plan holds).  Asynchronous; SS_OK,
+ * sequences grow, but not over a fork, free, eviction or compaction, nor where a
+ * sequence has become shorter than the tiles it shares (a rollback within its own
+ * tiles is fine): shared tiles would be read for rows that no longer have them,
+ * those behind a sequence's end too.  Memory beyond the given arrays is not
+ * touched whatever a plan holds.  Asynchronous; SS_OK,
  * SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_WORKSPACE (plan too small) or SS_ERR_CUDA.
  */
 size_t ss_prefix_plan_size(int B);
@@ -658,7 +660,10 @@ ss_status ss_prefix_plan(const int32_t* page_table, const int32_t* seq_lens, int
  *     query heads; cells from L_b on are left as they are.
  *   workspace: at least ss_attn_decode_shared_workspace_size(...) bytes, 16-byte
  *     aligned (never 0; it does not shrink as B or max_pages grow: one of the
- *     largest sizes serves all).
+ *     largest sizes serves all, and all layers).  With weights it holds each
+ *     score in fp32, for the width of the table and whatever is shared:
+ *     512 * B * Hq * max_pages bytes (64 sequences of 32 heads, tables of
+ *     256 pages: 268 MB).
  * G = Hq / Hkv <= 128, d in {64, 128}, B <= 32768 (with a plan 8192), Hkv <= 65535,
  * B * max_pages * Hkv <= 2^29 (with a plan 2^26).
  * Nothing that is written (o, weights, workspace) may overlap another argument.
@@ -677,8 +682,9 @@ ss_status ss_attn_decode_shared(const void* q, int64_t q_token_stride, const voi
  * tokens, without the attention's output: cell k of (sequence b, KV head h) of
  * `weights` gains the sum, over the sequence's n_b new tokens i and the G query
  * heads of h, of the softmax weight of key k.  Causal: token i sees the keys up to
- * L_b - n_b + i (a row that sees none, or whose scores are all -infinity in fp32, adds nothing), otherwise all L_b.  A
- * prompt's last tokens alone are a step of that many new tokens.
+ * L_b - n_b + i, otherwise all L_b; a row that sees none, or whose scores are all
+ * -infinity in fp32, adds nothing.  A prompt's last tokens alone are a step of
+ * that many new tokens.
  *   q, q_token_stride, k_pages, page_table, cu_seqlens, seq_lens: as in
  *     ss_attn_chunk_paged (what a page holds behind its sequence's end, and rows
  *     behind the last sequence, may be anything).
