@@ -995,7 +995,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // every fourth or eighth piece, columns a lane; the warps' sums are added in order.
 // 256 threads as long as all blocks are resident (28 heads x 24 places: 5 us, with
 // 128 threads 6.5), 128 beyond (32 heads x 64 places: 6 us, with 256 threads 11): a chain
-// of dependent loads bounds it.
+// of dependent loads bounds it.  An SM holds 6 blocks of 256 at d = 128 (40 registers a
+// thread), 8 at d = 64 (32).  Whole steps with 256 and with 128 threads, d = 128: 900 rows 22.6 and
+// 22.6 us, 1000 rows 25.4 and 23.5, 1200 rows 28.6 and 26.2; d = 64: 1200 rows 23.3 and 23.5, 1536 rows 28.1 and 26.2.
+template <int D>
+constexpr unsigned kWideRows = (D == 128 ? 6 : 8) * kSMs;
 template <int D, int kMerge>
 __global__ void __launch_bounds__(kMerge) shared_merge_kernel(const SharedParams p) {
   constexpr int L = 1 + kPlanLevels, E = D / 32, W = kMerge / 32;
@@ -1150,8 +1154,8 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Share
   e = launch_behind(fn, p.ctas, kThreads, Cfg<D>::kSmemBytes, st, tk, tv, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
-  e = rows <= 8 * kSMs ? launch_behind(shared_merge_kernel<D, 256>, rows, 256, 0, st, p)
-                       : launch_behind(shared_merge_kernel<D, 128>, rows, 128, 0, st, p);
+  e = rows <= kWideRows<D> ? launch_behind(shared_merge_kernel<D, 256>, rows, 256, 0, st, p)
+                            : launch_behind(shared_merge_kernel<D, 128>, rows, 128, 0, st, p);
   if (e != cudaSuccess || p.weights == nullptr) return e;
   const int blocks = (p.max_pages + 7) / 8;
   return launch_behind(weigh_kernel, dim3(blocks < 64 ? blocks : 64, p.Hkv, p.B), 256, 0, st, p);

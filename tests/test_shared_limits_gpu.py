@@ -1,9 +1,11 @@
 """The calls over shared pages and the record of attention weights at the ends of their ranges."""
+import numpy as np
 import pytest
 import torch
 
 from _serving import PAGE, offsets
-from _shared import assert_close, sequence, softmax
+from _shared import assert_close, sequence, softmax, tree_batch
+from test_decode_shared_gpu import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +84,13 @@ def test_rows_whose_scores_are_all_minus_infinity(ss):
         for w in (a, b):
             assert_close(w[i, :, :n], want, (P * rel).sum((1, 2)) + want * 2.0 ** -22 + 1e-37, f"sequence {i}")
             assert torch.equal(w[i, :, n:], clean[i, :, n:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv", [(57, 16, 4), (58, 16, 4), (76, 16, 4), (77, 16, 4)])
+def test_joins_of_either_width(ss, B, Hq, Hkv, d):
+    """Rows on both sides of the numbers up to which the join of partial results has 256 threads a row."""
+    rng = np.random.default_rng(B + d)
+    lens, table, pages = tree_batch(rng, B, 3, 520, 300, [int(x) for x in rng.integers(1, 300, B)])
+    q, kp, vp, table, lens = make(rng, lens, table, pages, Hq, Hkv, d)
+    check(ss, q, kp, vp, table, lens, ss.prefix_plan(table, lens))
