@@ -8,8 +8,9 @@
 // 11 and 10 bits of the weight as an unsigned number in the same order) give
 // the smallest kept weight exactly, then one pass in the order of the keys
 // takes what is above it and the first of those equal to it, and writes their
-// places.  The weights are read from L2 after the first pass (4 bytes a key
-// next to the 4 d of keys and values that are moved).
+// places.  Up to 16384 keys the weights are read once and stay in registers (4 bytes a
+// key next to the 4 d of keys and values that are moved); of longer sequences each of the passes
+// reads them again, a block a list: 3 sequences of 64K 154 us, one of 200K 463.
 // Block 0 of the first such launch decides, as the other page calls do: it
 // checks the call, gives fresh pages to those that other sequences hold too
 // (they are read, never written), and takes note of the old and new pages.
