@@ -577,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (x.n > 0) break;
           }
-          // (A place is free when its piece is done, after millions of steps of 1-2 us on the longest caches: 60 us of limit for each.  The
-          // other warps' waits end with a tile and set the flag if they do not.)
+          // (A place is free when its piece is done, on the longest caches after millions of steps
+          // of 1-2 us: 60 us of limit for each.  The other warps' waits end with a tile and set
+          // the flag if they do not.)
           if (!ROWS && k == kPieces) wait_for_previous();
           const uint32_t more = k < kPieces ? 0u : 16u * static_cast<uint32_t>(min(ctl->piece[k % kPieces].n, 1 << 26));
           if (!mbar_wait_small(&ctl->piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort_flag, kSmallTries + more)) break;

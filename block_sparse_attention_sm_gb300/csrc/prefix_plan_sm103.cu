@@ -13,7 +13,9 @@
 // its longest common stretch with one of them (the nearest smaller row has it).
 // tree_kernel: a warp a place looks left and right for the run's ends, 32 places a
 // step, in shared memory; then a thread a place goes up the tree.  Latency bounds both
-// (48 places: 6.2 us and 3.2 us).  A batch of up to 8 has both in one launch, the blocks of
+// (48 places: 6.2 us and 3.2 us).  All pairs that begin on the same page are compared, so
+// batches of one prefix cost their square: 64 places 11 us, 256 59 us, 1024 0.69 ms, 8192
+// 42 ms (prefix of 256 pages).  A batch of up to 8 has both in one launch, the blocks of
 // a cluster (8 places: 5.1 us against 4.3, but 3 us less of the host, which bounds such calls).
 #include "launch.cuh"
 #include "ptx_pair_sm103.cuh"
